@@ -75,7 +75,9 @@ def listed():
 
 
 def _log_int(rng, lo, hi):
-    return int(min(hi, max(lo, round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+    """Spread over the logarithm; from 100 on of the form 3k + 1: even and odd ones, few on a tile's edge."""
+    n = int(min(hi, max(lo, round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+    return n if n < 100 or n - (n - 1) % 3 < lo else n - (n - 1) % 3
 
 
 def draw(rng):
