@@ -104,7 +104,9 @@ def draw(rng):
             batch = _log_int(rng, 1, 16)
             new, past = _log_int(rng, 8, (1 << 24) // (kv_heads * dim * batch)), rng.choice([0, 0, 37])
         ragged = rng.random() < 0.4
-        return dict(op="append", batch=batch, new=new * batch if ragged else new, past=past, ragged=ragged,
+        if ragged:  # tokens in all, of the form that _log_int gives
+            new = new * batch - (new * batch - 1) % 3
+        return dict(op="append", batch=batch, new=new, past=past, ragged=ragged,
                     kv_heads=kv_heads, dim=dim, block=rng.choice([16, 32, 64, 128]), fmt=rng.choice(["e4m3", "int8"]),
                     dtype=rng.choice(["bf16", "f16"]))
     if op == "route":
