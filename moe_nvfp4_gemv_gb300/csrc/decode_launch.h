@@ -1,0 +1,27 @@
+// decode_launch.h -- host-side interface between the C API of the decode
+// step's operators (decode_api.cu) and their kernel translation units, and
+// what those share with fp4gemv_api.cu.
+#pragma once
+
+#include "fp4gemv.h"
+#include "k_kv_append.cuh"
+#include "k_kv_attention.cuh"
+#include "k_logprobs.cuh"
+
+namespace fp4 {
+
+// fp4gemv_api.cu: the current device's error word and SM count, and the
+// launch counter.
+fp4gemv_status current_device_state(uint32_t** err, int* sms);
+void count_launch();
+
+cudaError_t launch_moe_route(const RouteParams& p, int dtype, int pdl, cudaStream_t stream);
+cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, int T, int sms, int pdl, cudaStream_t stream);
+cudaError_t launch_kv_append(const KvAppendParams& p, int int8, int pdl, cudaStream_t stream);
+// CTAs of the attention kernel at most (the workspace is sized for them).
+int kv_attention_max_ctas(int sms);
+// rows_per_tile: 16 or 32 (32 not with head_dim 256).
+cudaError_t launch_kv_attention(const KvAttnParams& p, int dim, int int8, int rows_per_tile, int sms, int pdl,
+                                cudaStream_t stream);
+
+}  // namespace fp4

@@ -17,6 +17,9 @@
 #include "launch.h"
 
 namespace fp4 {
+fp4gemv_status current_device_state(uint32_t** err, int* sms);  // (decode_launch.h)
+void count_launch();
+
 // Per-device error state (one copy per device context of this library image):
 // the error word, then the wait limit the kernels' bounded waits use (see
 // common.cuh; 0 = the built-in 2 s).
@@ -164,6 +167,16 @@ fp4gemv_status device_state(uint32_t** err, int* sms) {
   if (sms) *sms = n;
   return FP4GEMV_OK;
 }
+
+}  // namespace
+
+namespace fp4 {
+// For the decode step's operators (decode_api.cu).
+fp4gemv_status current_device_state(uint32_t** err, int* sms) { return device_state(err, sms); }
+void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+}  // namespace fp4
+
+namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

@@ -1,0 +1,72 @@
+// Launchers of the routing and log-probability kernels.
+#include "decode_launch.h"
+
+namespace fp4 {
+
+namespace {
+
+template <typename Params>
+cudaError_t launch_simple(void (*kernel)(Params), unsigned grid, unsigned threads, unsigned cluster, int pdl,
+                          cudaStream_t stream, const Params& p) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(grid, 1, 1);
+  lc.blockDim = dim3(threads, 1, 1);
+  lc.stream = stream;
+  cudaLaunchAttribute attrs[2];
+  unsigned na = 0;
+  if (cluster > 1) {
+    attrs[na].id = cudaLaunchAttributeClusterDimension;
+    attrs[na].val.clusterDim.x = cluster;
+    attrs[na].val.clusterDim.y = 1;
+    attrs[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  if (pdl) {
+    attrs[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+  }
+  lc.attrs = attrs;
+  lc.numAttrs = na;
+  return cudaLaunchKernelEx(&lc, kernel, p);
+}
+
+template <typename T>
+cudaError_t route_typed(const RouteParams& p, int pdl, cudaStream_t stream) {
+  const unsigned grid = (static_cast<unsigned>(p.M) + kRouteWarps - 1) / kRouteWarps;
+  const int slots = (p.E + 31) / 32;
+  auto kernel = slots <= 1   ? moe_route_kernel<T, 1>
+                : slots <= 2 ? moe_route_kernel<T, 2>
+                : slots <= 4 ? moe_route_kernel<T, 4>
+                : slots <= 8 ? moe_route_kernel<T, 8>
+                             : moe_route_kernel<T, 16>;
+  return launch_simple<RouteParams>(kernel, grid, kRouteWarps * 32, 1, pdl, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_route(const RouteParams& p, int dtype, int pdl, cudaStream_t stream) {
+  switch (dtype) {
+    case 0: return route_typed<__nv_bfloat16>(p, pdl, stream);
+    case 1: return route_typed<__half>(p, pdl, stream);
+    default: return route_typed<float>(p, pdl, stream);
+  }
+}
+
+cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, int T, int sms, int pdl, cudaStream_t stream) {
+  // a cluster per row while the rows alone leave SMs idle and a slice keeps
+  // 16 bytes for most threads
+  const int elem = dtype == 2 ? 4 : 2;
+  unsigned c = 1;
+  while (c < kLpMaxCluster && static_cast<int64_t>(T) * c * 2 <= 2 * sms &&
+         static_cast<int64_t>(p.V) * elem / (2 * c) >= kLpThreads * 16)
+    c *= 2;
+  const unsigned grid = static_cast<unsigned>(T) * c;
+  switch (dtype) {
+    case 0: return launch_simple<LogprobParams>(token_logprobs_kernel<__nv_bfloat16>, grid, kLpThreads, c, pdl, stream, p);
+    case 1: return launch_simple<LogprobParams>(token_logprobs_kernel<__half>, grid, kLpThreads, c, pdl, stream, p);
+    default: return launch_simple<LogprobParams>(token_logprobs_kernel<float>, grid, kLpThreads, c, pdl, stream, p);
+  }
+}
+
+}  // namespace fp4

@@ -1,0 +1,346 @@
+// k_logprobs.cuh -- log probabilities of given tokens, their rank, the
+// entropy and the top alternatives (fp4gemv_token_logprobs).
+//
+// One pass over the row with running statistics (m, s, u): the maximum so
+// far, s = sum 2^(c (x - m)) and u = sum 2^(c (x - m)) c (x - m), c =
+// inv_temperature log2(e); a new maximum rescales them, u to
+// f (u + s c (m - m')), f = 2^(c (m - m')).  At the end, in base-2 logs,
+//   log2 Z = log2 s,  H = ln 2 (log2 s - u / s),
+//   logprob = (x - m) inv_temperature - ln 2 log2 s.
+//
+// Top n without sorting the row: the threads form 64 groups, each with the
+// maximum of its elements (the running maximum, which the softmax needs
+// anyway); the n-th largest group maximum is a lower bound of the n-th largest
+// logit, so only threads whose own maximum reaches it look at their elements
+// again, and the elements that reach it, some n to 2 n of them, are ranked by
+// counting.  Where more reach it than the buffer holds (ties: a row of masked
+// or equal logits), the n-th largest of some that were collected is a better
+// bound, indices included, and the collection is repeated.
+//
+// A row is split over the CTAs of a cluster when there are few rows; they
+// meet in the shared memory of the cluster's first CTA.
+#pragma once
+
+#include "k_route.cuh"
+
+namespace fp4 {
+
+struct LogprobParams {
+  const void* logits;
+  int64_t ldl;
+  const int32_t* tokens;
+  float* logprob;
+  int32_t* rank;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  uint32_t* err;
+  int V, n;
+  float inv_t;
+};
+
+constexpr int kLpThreads = 512;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpGroups = 64;
+constexpr int kMaxCand = 512;
+constexpr int kRaiseFrom = 256;  // collected elements that a better bound is taken from
+constexpr int kLpMaxCluster = 8;
+// Logits at or below this are masked: probability 0.  The statistics see them
+// as this value, so that no difference of two is a NaN or overflows; a power
+// of two, so that its product with c is exact and its distance to itself 0.
+constexpr float kMasked = -0x1p100f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+struct LpStat {
+  float m, s, u;
+};
+__device__ __forceinline__ void lp_join(LpStat& a, const LpStat& b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  const float da = (a.m - m) * c, db = (b.m - m) * c;
+  const float fa = ex2(da), fb = ex2(db);
+  a.u = fa * (a.u + a.s * da) + fb * (b.u + b.s * db);
+  a.s = fa * a.s + fb * b.s;
+  a.m = m;
+}
+
+// Adds N logits to the running statistics.
+template <int N>
+__device__ __forceinline__ void lp_add(LpStat& st, const float (&x)[N], float c) {
+  float bm = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) bm = fmaxf(bm, x[i]);
+  if (bm > st.m) {
+    const float d = (st.m - bm) * c;
+    const float f = ex2(d);
+    st.u = f * (st.u + st.s * d);
+    st.s *= f;
+    st.m = bm;
+  }
+  const float mc = st.m * c;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float d = fmaf(max_nan(x[i], kMasked), c, -mc);
+    const float e = ex2(d);
+    st.s += e;
+    st.u = fmaf(e, d, st.u);
+  }
+}
+
+template <typename T>
+struct LpVec {
+  static constexpr int kN = 16 / sizeof(T);
+};
+
+template <typename T>
+__device__ __forceinline__ void lp_unpack(const uint4& v, float (&x)[LpVec<T>::kN]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      x[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+
+__device__ __forceinline__ uint64_t lp_key(float x, uint32_t i) {
+  return (static_cast<uint64_t>(order_key(x)) << 32) | (0xFFFFFFFFu - i);
+}
+
+struct LpShared {
+  LpStat stat[kLpMaxCluster][kLpWarps];
+  int count[kLpMaxCluster][kLpWarps];
+  uint32_t group[kLpGroups];
+  unsigned long long bound;
+  int n_flag, n_cand;
+  uint16_t flagged[kLpThreads];
+  uint64_t cand[kMaxCand];
+  uint64_t top[kLpMaxCluster * 32];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const LogprobParams p) {
+  __shared__ LpShared sh;
+  constexpr int kN = LpVec<T>::kN;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t C = cluster_nctarank(), rank = cluster_ctarank();
+  const int64_t t = blockIdx.x / C;
+  if (C > 1) cluster_arrive_relaxed();  // (waited for before the first store into another CTA)
+  if (tid == 0) pdl_launch_dependents();
+  if (tid < kLpGroups) sh.group[tid] = 0;
+  if (tid == 0) {
+    sh.n_flag = 0;
+    sh.n_cand = 0;
+  }
+  pdl_wait();
+  const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
+  const int token = __ldg(p.tokens + t);
+  const bool valid = token >= 0 && token < p.V;
+  const float xt = valid ? to_float(row[token]) : 0.0f;
+  const float xr = xt == xt ? xt : kNegInf;  // what ranks compare with
+  const float c = p.inv_t * 1.4426950408889634f;
+
+  // the row as single elements up to a 16-byte boundary, whole vectors, and
+  // single elements again; this CTA's vectors are [v0, v1), and every thread
+  // takes every kLpThreads-th of them
+  const int lead = static_cast<int>(
+      min(static_cast<uint64_t>(p.V), ((16u - (reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / sizeof(T)));
+  const int nvec = (p.V - lead) / kN;
+  const int v0 = static_cast<int>(static_cast<int64_t>(nvec) * rank / C);
+  const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (rank + 1) / C);
+  const uint4* vec = reinterpret_cast<const uint4*>(row + lead);
+  // (the single elements, at most 2 (kN - 1), belong to the first CTA)
+  const int singles = rank == 0 ? p.V - nvec * kN : 0;
+  auto single_index = [&](int i) { return i < lead ? i : nvec * kN + i; };
+
+  LpStat st = {kMasked, 0.0f, 0.0f};
+  int above = 0;
+  if (tid < singles) {
+    const float x[1] = {to_float(row[single_index(tid)])};
+    lp_add<1>(st, x, c);
+    above += x[0] > xr;
+  }
+  constexpr int kU = 4;  // vectors in flight per thread
+  int v = v0 + tid;
+  for (; v + (kU - 1) * kLpThreads < v1; v += kU * kLpThreads) {
+    uint4 raw[kU];
+#pragma unroll
+    for (int j = 0; j < kU; ++j) raw[j] = __ldg(vec + v + j * kLpThreads);
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      float x[kN];
+      lp_unpack<T>(raw[j], x);
+      lp_add<kN>(st, x, c);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) above += x[i] > xr;
+    }
+  }
+  for (; v < v1; v += kLpThreads) {
+    float x[kN];
+    lp_unpack<T>(__ldg(vec + v), x);
+    lp_add<kN>(st, x, c);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) above += x[i] > xr;
+  }
+
+  const float own_max = st.m;
+  const bool any = tid < singles || v0 + tid < v1;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    LpStat b;
+    b.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
+    b.s = __shfl_xor_sync(0xFFFFFFFFu, st.s, o);
+    b.u = __shfl_xor_sync(0xFFFFFFFFu, st.u, o);
+    lp_join(st, b, c);
+  }
+  above = __reduce_add_sync(0xFFFFFFFFu, above);
+  // statistics, counts and winners meet in the first CTA's shared memory
+  if (C > 1) cluster_wait();
+  if (lane == 0) {
+    const uint32_t a = mapa(smem_u32(&sh.stat[rank][warp]), 0), b = mapa(smem_u32(&sh.count[rank][warp]), 0);
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(st.m) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 4), "f"(st.s) : "memory");
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 8), "f"(st.u) : "memory");
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(b), "r"(above) : "memory");
+  }
+  const int n = p.n;
+  if (n > 0) {
+    // (a thread with masked elements only counts with the least key: bounds
+    // then lie above all masked values or below everything)
+    const uint32_t own = any ? order_key(own_max > kMasked ? own_max : kNegInf) : 0u;
+    if (own) atomicMax(&sh.group[tid & (kLpGroups - 1)], own);
+    __syncthreads();
+    if (tid < kLpGroups) {
+      const uint32_t mine = sh.group[tid];
+      int r = 0;
+#pragma unroll 16
+      for (int j = 0; j < kLpGroups; ++j) {
+        const uint32_t o = sh.group[j];
+        r += o > mine || (o == mine && j < tid);
+      }
+      if (r == n - 1) sh.bound = static_cast<unsigned long long>(mine) << 32;
+    }
+    __syncthreads();
+    uint64_t bound = sh.bound;
+    if (own && own >= static_cast<uint32_t>(bound >> 32))
+      sh.flagged[atomicAdd(&sh.n_flag, 1)] = static_cast<uint16_t>(tid);
+    __syncthreads();
+    const int nf = sh.n_flag;
+    const int steps = (v1 - v0 + kLpThreads - 1) / kLpThreads;
+    auto offer = [&](float x, int i) {
+      const uint64_t k = lp_key(x, i);
+      if (k >= bound) {
+        const int at = atomicAdd(&sh.n_cand, 1);
+        if (at < kMaxCand) sh.cand[at] = k;
+      }
+    };
+    int nc;
+    for (;;) {
+      for (int w = tid; w < nf * steps; w += kLpThreads) {
+        const int j = v0 + sh.flagged[w % nf] + (w / nf) * kLpThreads;
+        if (j < v1) {
+          float x[kN];
+          lp_unpack<T>(__ldg(vec + j), x);
+#pragma unroll
+          for (int i = 0; i < kN; ++i) offer(x[i], lead + j * kN + i);
+        }
+      }
+      if (tid < singles) offer(to_float(row[single_index(tid)]), single_index(tid));
+      __syncthreads();
+      nc = sh.n_cand;
+      if (nc <= kMaxCand) break;
+      // at least n elements reach the n-th largest of kRaiseFrom of them
+      if (tid < kRaiseFrom) {
+        const uint64_t k = sh.cand[tid];
+        int r = 0;
+        for (int j = 0; j < kRaiseFrom; ++j) r += sh.cand[j] > k;
+        if (r == n - 1) sh.bound = k;
+      }
+      __syncthreads();
+      bound = sh.bound;
+      if (tid == 0) sh.n_cand = 0;
+      __syncthreads();
+    }
+    for (int i = tid; i < nc; i += kLpThreads) {
+      const uint64_t k = sh.cand[i];
+      int r = 0;
+      for (int j = 0; j < nc; ++j) r += sh.cand[j] > k;
+      if (r < n) {
+        const uint32_t a = mapa(smem_u32(&sh.top[rank * n + r]), 0);
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(k) : "memory");
+      }
+    }
+    for (int r = nc + tid; r < n; r += kLpThreads) {  // (a slice of fewer than n elements)
+      const uint32_t a = mapa(smem_u32(&sh.top[rank * n + r]), 0);
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(0ull) : "memory");
+    }
+  }
+
+  if (C == 1) __syncthreads();
+  else cluster_sync();
+  if (rank != 0) return;
+  // one warp-wide join of all partial statistics, by every warp alike
+  LpStat all = {kMasked, 0.0f, 0.0f};
+  int total = 0;
+  for (int i = lane; i < static_cast<int>(C) * kLpWarps; i += 32) {
+    lp_join(all, (&sh.stat[0][0])[i], c);
+    total += (&sh.count[0][0])[i];
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    LpStat b;
+    b.m = __shfl_xor_sync(0xFFFFFFFFu, all.m, o);
+    b.s = __shfl_xor_sync(0xFFFFFFFFu, all.s, o);
+    b.u = __shfl_xor_sync(0xFFFFFFFFu, all.u, o);
+    lp_join(all, b, c);
+  }
+  total = __reduce_add_sync(0xFFFFFFFFu, total);
+  const bool empty = all.m <= kMasked && all.s == all.s;  // (a NaN keeps the statistics' NaN)
+  const float log_z = logf(all.s);
+  auto logprob_of = [&](float x) {
+    return empty || (x <= kMasked && log_z == log_z) ? kNegInf : fmaf(x - all.m, p.inv_t, -log_z);
+  };
+  if (tid == 0) {
+    p.entropy[t] = empty ? 0.0f : log_z - 0.6931471805599453f * (all.u / all.s);
+    if (valid) {
+      p.logprob[t] = logprob_of(xt);
+      p.rank[t] = 1 + total;
+    } else {
+      raise_error(p.err, FP4_ERR_BADIDX);
+    }
+  }
+  if (n > 0) {
+    const int have = C == 1 ? n : static_cast<int>(C) * n;
+    for (int i = tid; i < have; i += kLpThreads) {
+      const uint64_t k = sh.top[i];
+      int r = i;
+      if (C > 1) {
+        r = 0;
+        for (int j = 0; j < have; ++j) r += sh.top[j] > k;
+      }
+      if (r < n && k != 0) {
+        const int64_t o = t * n + r;
+        p.top_ids[o] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));
+        p.top_logprobs[o] = logprob_of(key_value(static_cast<uint32_t>(k >> 32)));
+      }
+    }
+  }
+}
+
+}  // namespace fp4

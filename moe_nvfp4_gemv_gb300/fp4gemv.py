@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libfp4gemv (the C ABI in include/fp4gemv.h).
+"""Thin ctypes binding of libfp4gemv (the C ABI in include/fp4gemv.h and, for
+the decode step's operators around the products, include/fp4gemv_decode.h).
 
 Argument marshalling only: every call hands device pointers, sizes and the
 current CUDA stream of the tensors' device to the library; all computation
@@ -10,11 +11,14 @@ Names follow the pages (vllm.models.flint.ops.nvfp4_gemv: nvfp4_gemv,
 bf16_gemv, dequantize_rows; vllm.models.flint.ops.moe_gemv: gate_up,
 down_combine): ``nvfp4_gemv`` / ``bf16_gemv`` / ``dequantize_rows`` allocate
 and return their output, the MoE pair writes into caller buffers.
+``moe_route`` and ``token_logprobs`` allocate their outputs unless they are
+given; the 8-bit cache's calls are methods of ``kvcache.KvCache8``.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -62,6 +66,14 @@ def _load() -> ctypes.CDLL:
         "fp4gemv_quantize_act": (i32, [vp, i64, vp, vp, vp, vp, i32, i32, vp]),
         "fp4gemv_w4a4_gemm": (i32, [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp, sz, i32, vp]),
         "fp4gemv_w4a4_linear": (i32, [vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp, vp, vp, sz, i32, vp]),
+        "fp4gemv_kv_append": (i32, [vp, vp, i64, vp, i64, i32, i32, vp, vp, i32, vp, i32, i32, vp]),
+        "fp4gemv_kv_attention_workspace_bytes": (sz, [i32]),
+        "fp4gemv_kv_attention": (i32, [vp, vp, i64, i32, i32, i32, vp, i32, vp, i32, ctypes.c_float, i32, vp, i64, vp,
+                                       vp, sz, i32, vp]),
+        "fp4gemv_moe_route": (i32, [vp, i64, i32, i32, i32, i32, i32, vp, i32, i32, i32, i32, ctypes.c_float, vp, vp,
+                                    i32, vp]),
+        "fp4gemv_token_logprobs": (i32, [vp, i64, i32, i32, i32, vp, ctypes.c_float, i32, vp, vp, vp, vp, vp, i32,
+                                         vp]),
         "fp4gemv_get_device_error": (i32, [vp]),
         "fp4gemv_status_string": (ctypes.c_char_p, [i32]),
         "fp4gemv_set_wait_limit_ns": (i32, [ctypes.c_uint64]),
@@ -360,6 +372,109 @@ def moe_down_combine(act, ids, tw, w2, w2_sf, alpha2, sact, wsd, ssd, gssd, out,
                                          _ptr(_bytes(ssd)), _ptr(gssd.reshape(1)), SI, _ptr(out), _ptr(workspace),
                                          workspace.numel() * workspace.element_size(), int(pdl),
                                          _stream(act.device)), "fp4gemv_moe_down_combine")
+
+
+# ---- the decode step's operators around the products ----
+_DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
+_moe_route = _lib.fp4gemv_moe_route
+_token_logprobs = _lib.fp4gemv_token_logprobs
+_I32 = torch.int32
+_F32 = torch.float32
+
+
+def moe_route(logits: torch.Tensor, topk: int, scores: str = "softmax", bias: torch.Tensor | None = None,
+              n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True, scale: float = 1.0,
+              ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+              pdl: bool = True) -> tuple[torch.Tensor, torch.Tensor]:
+    """Routes tokens to experts: (ids int32 [M, topk], weights fp32 [M, topk])
+    of the router's logits [M, E] (bf16, f16 or fp32, unit inner stride), as
+    ``moe_gate_up`` and ``moe_down_combine`` take them.
+
+    The experts with the largest score + ``bias`` (fp32 [E], selection only),
+    ties to the lower index, in descending order; ``scores`` "softmax" over
+    all experts or "sigmoid"; with ``n_group`` > 1 only those of the
+    ``topk_group`` groups whose ``group_top`` largest keys have the largest
+    sum.  Weights are the scores, divided by their sum with ``renormalize``,
+    times ``scale``."""
+    code = _DTYPE_CODES.get(logits.dtype)
+    if code is None or logits.dim() != 2 or logits.stride(1) != 1 or not logits.is_cuda:
+        raise ValueError("logits must be a 2-D bf16, f16 or fp32 CUDA tensor with unit inner stride")
+    M, E = logits.shape
+    kind = _ROUTE_SCORES.get(scores)
+    if kind is None:
+        raise ValueError(f"scores must be 'softmax' or 'sigmoid', not {scores!r}")
+    dev = logits.device
+    if bias is not None and (bias.dtype is not _F32 or bias.dim() != 1 or bias.shape[0] != E or
+                             not bias.is_contiguous() or bias.device != dev):
+        raise ValueError(f"bias must be a contiguous fp32 [{E}] tensor on the logits' device")
+    if ids is None:
+        ids = torch.empty(M, topk, dtype=_I32, device=dev)
+    elif ids.dtype is not _I32 or ids.shape != (M, topk) or not ids.is_contiguous() or ids.device != dev:
+        raise ValueError(f"ids must be a contiguous int32 [{M}, {topk}] tensor on the logits' device")
+    if weights is None:
+        weights = torch.empty(M, topk, dtype=_F32, device=dev)
+    elif weights.dtype is not _F32 or weights.shape != (M, topk) or not weights.is_contiguous() or \
+            weights.device != dev:
+        raise ValueError(f"weights must be a contiguous fp32 [{M}, {topk}] tensor on the logits' device")
+    if M == 0:
+        return ids, weights
+    status = _moe_route(logits.data_ptr(), logits.stride(0) if M > 1 else E, code, M, E, topk, kind,
+                        bias.data_ptr() if bias is not None else None, n_group, topk_group, group_top,
+                        1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), 1 if pdl else 0,
+                        _raw_stream(dev.index))
+    if status:
+        raise Fp4GemvError(status, "fp4gemv_moe_route")
+    return ids, weights
+
+
+class TokenLogprobs(NamedTuple):
+    """What ``token_logprobs`` returns."""
+    logprob: torch.Tensor       # fp32 [T]
+    rank: torch.Tensor          # int32 [T], 1 for the most likely token
+    entropy: torch.Tensor       # fp32 [T]
+    top_ids: torch.Tensor       # int32 [T, top_n]
+    top_logprobs: torch.Tensor  # fp32 [T, top_n]
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int = 0, temperature: float = 1.0,
+                   out: TokenLogprobs | tuple | None = None, pdl: bool = True) -> TokenLogprobs:
+    """Log probabilities of ``tokens`` (int32 [T]) under softmax(logits /
+    temperature), their ranks, the rows' entropies, and the ``top_n`` (at most
+    32) most likely tokens with their log probabilities (ties: the lower id).
+
+    ``logits`` bf16, f16 or fp32 [T, V] with unit inner stride and any row
+    stride; ``out``: tensors to write into, laid out as the result."""
+    code = _DTYPE_CODES.get(logits.dtype)
+    if code is None or logits.dim() != 2 or logits.stride(1) != 1 or not logits.is_cuda:
+        raise ValueError("logits must be a 2-D bf16, f16 or fp32 CUDA tensor with unit inner stride")
+    T, V = logits.shape
+    dev = logits.device
+    if tokens.dtype is not _I32 or tokens.dim() != 1 or tokens.shape[0] != T or not tokens.is_contiguous() or \
+            tokens.device != dev:
+        raise ValueError(f"tokens must be a contiguous int32 [{T}] tensor on the logits' device")
+    if not temperature > 0:
+        raise ValueError("temperature must be positive")
+    if out is None:
+        out = TokenLogprobs(torch.empty(T, dtype=_F32, device=dev), torch.empty(T, dtype=_I32, device=dev),
+                            torch.empty(T, dtype=_F32, device=dev), torch.empty(T, top_n, dtype=_I32, device=dev),
+                            torch.empty(T, top_n, dtype=_F32, device=dev))
+    else:
+        for o, dtype, shape in zip(out, (_F32, _I32, _F32, _I32, _F32), ((T,), (T,), (T,), (T, top_n), (T, top_n))):
+            if o.dtype is not dtype or o.shape != shape or not o.is_contiguous() or o.device != dev:
+                raise ValueError("out must hold contiguous logprob fp32 [T], rank int32 [T], entropy fp32 [T], "
+                                 "top_ids int32 [T, top_n] and top_logprobs fp32 [T, top_n] on the logits' device")
+        if not isinstance(out, TokenLogprobs):
+            out = TokenLogprobs(*out)
+    if T == 0:
+        return out
+    status = _token_logprobs(logits.data_ptr(), logits.stride(0) if T > 1 else V, code, T, V, tokens.data_ptr(),
+                             1.0 / temperature, top_n, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
+                             out[3].data_ptr() if top_n else None, out[4].data_ptr() if top_n else None,
+                             1 if pdl else 0, _raw_stream(dev.index))
+    if status:
+        raise Fp4GemvError(status, "fp4gemv_token_logprobs")
+    return out
 
 
 def get_device_error(device: torch.device | None = None) -> int:

@@ -1,0 +1,187 @@
+"""A paged key/value cache held in 8 bits, and attention over it.
+
+``KvCache8`` wraps the four tensors of a cache -- codes uint8 [num_blocks,
+kv_heads, block_size, head_dim] and fp32 scales [num_blocks, kv_heads], keys
+and values apart (the formats: include/fp4gemv_decode.h) -- with the two calls
+of a decode step:
+
+* ``append``: quantises new keys and values into the pages that the block
+  table names; a page's scale grows with what it holds;
+* ``attend``: attention of each sequence's newest tokens over its pages.
+
+The tensors stay the caller's: copy, share or reset pages as the serving
+program likes, between calls on the same stream.  Sequences are given by a
+block table (int32 [B, max_blocks], page ids) and their lengths (int32 [B],
+new tokens included), both on the device, so a step of any lengths is one
+captured graph.  Like the rest of the binding the calls only marshal
+arguments; they run on the current stream and raise ``Fp4GemvError`` on a
+refused argument.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import fp4gemv
+from .fp4gemv import Fp4GemvError, _lib, _raw_stream
+
+FORMATS = {"e4m3": 0, "int8": 1}
+_BF16, _F16, _I32, _F32 = torch.bfloat16, torch.float16, torch.int32, torch.float32
+_append = _lib.fp4gemv_kv_append
+_attend = _lib.fp4gemv_kv_attention
+
+
+class _CacheStruct(ctypes.Structure):
+    """fp4gemv_kv_cache."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("block_size", ctypes.c_int), ("head_dim", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+_workspaces: dict = {}
+
+
+def attention_workspace_bytes(head_dim: int) -> int:
+    """Bytes of ``attend``'s workspace on the current device."""
+    return int(_lib.fp4gemv_kv_attention_workspace_bytes(head_dim))
+
+
+def attention_workspace(device: torch.device, head_dim: int, stream: int | None = None) -> torch.Tensor:
+    """A zero-filled workspace for ``device`` and one CUDA stream (the current
+    one when ``stream`` is None), kept for later calls: calls on one stream
+    run one after another and may share it, calls on different streams may
+    overlap and each stream has its own."""
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    if stream is None:
+        stream = _raw_stream(index)
+    key = (index, int(stream), head_dim)
+    ws = _workspaces.get(key)
+    if ws is None:
+        ws = torch.zeros(attention_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
+        _workspaces[key] = ws
+    return ws
+
+
+class KvCache8:
+    """The cache's tensors and their calls.  ``fmt``: "e4m3" or "int8"."""
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 fmt: str = "e4m3"):
+        if fmt not in FORMATS:
+            raise ValueError(f"fmt must be 'e4m3' or 'int8', not {fmt!r}")
+        if k_codes.dim() != 4:
+            raise ValueError("codes must be [num_blocks, kv_heads, block_size, head_dim]")
+        for name, t, dtype, shape in (("k_codes", k_codes, torch.uint8, k_codes.shape),
+                                      ("v_codes", v_codes, torch.uint8, k_codes.shape),
+                                      ("k_scale", k_scale, _F32, k_codes.shape[:2]),
+                                      ("v_scale", v_scale, _F32, k_codes.shape[:2])):
+            if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != k_codes.device:
+                raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the codes' device")
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.fmt = fmt
+        self.device = k_codes.device
+        self.num_blocks, self.kv_heads, self.block_size, self.head_dim = k_codes.shape
+        self._struct = _CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                    self.num_blocks, self.kv_heads, self.block_size, self.head_dim, FORMATS[fmt])
+        self._handle = ctypes.addressof(self._struct)
+        self._sm_scale = 1.0 / math.sqrt(self.head_dim)
+
+    @classmethod
+    def allocate(cls, num_blocks: int, kv_heads: int, head_dim: int, block_size: int = 64, fmt: str = "e4m3",
+                 device: torch.device | str = "cuda") -> "KvCache8":
+        """A cache of zeroed pages."""
+        shape = (num_blocks, kv_heads, block_size, head_dim)
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.zeros(shape[:2], dtype=_F32, device=device) for _ in range(2)]
+        return cls(*codes, *scales, fmt=fmt)
+
+    def _check_sequences(self, block_table: torch.Tensor, seq_lens: torch.Tensor) -> int:
+        if block_table.dtype is not _I32 or block_table.dim() != 2 or not block_table.is_contiguous() or \
+                block_table.device != self.device:
+            raise ValueError("block_table must be a contiguous int32 [B, max_blocks] tensor on the cache's device")
+        B = block_table.shape[0]
+        if seq_lens.dtype is not _I32 or seq_lens.dim() != 1 or seq_lens.shape[0] != B or \
+                not seq_lens.is_contiguous() or seq_lens.device != self.device:
+            raise ValueError(f"seq_lens must be a contiguous int32 [{B}] tensor on the cache's device")
+        return B
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+               cu_new: torch.Tensor | None = None, pdl: bool = True) -> None:
+        """Appends k, v (bf16 or f16 [T, kv_heads, head_dim], heads contiguous,
+        any token stride that is a multiple of 8) to B sequences: T / B tokens
+        each, or tokens cu_new[b] .. cu_new[b + 1] (int32 [B + 1]) to sequence
+        b.  ``seq_lens``: the lengths with the new tokens."""
+        B = self._check_sequences(block_table, seq_lens)
+        H, D = self.kv_heads, self.head_dim
+        for name, t in (("k", k), ("v", v)):
+            if (t.dtype is not _BF16 and t.dtype is not _F16) or t.dim() != 3 or t.shape[1] != H or \
+                    t.shape[2] != D or t.stride(2) != 1 or (t.stride(1) != D and H > 1) or t.device != self.device:
+                raise ValueError(f"{name} must be a bf16 or f16 [T, {H}, {D}] tensor on the cache's device with "
+                                 "contiguous heads")
+        T = k.shape[0]
+        if v.shape[0] != T or v.dtype is not k.dtype:
+            raise ValueError("k and v must have the same tokens and type")
+        if cu_new is not None and (cu_new.dtype is not _I32 or cu_new.shape != (B + 1,) or
+                                   not cu_new.is_contiguous() or cu_new.device != self.device):
+            raise ValueError(f"cu_new must be a contiguous int32 [{B + 1}] tensor on the cache's device")
+        if T == 0 or B == 0:
+            if T:
+                raise ValueError("new tokens for no sequence")
+            return
+        status = _append(self._handle, k.data_ptr(), k.stride(0) if T > 1 else H * D, v.data_ptr(),
+                         v.stride(0) if T > 1 else H * D, 0 if k.dtype is _BF16 else 1, T,
+                         cu_new.data_ptr() if cu_new is not None else None, block_table.data_ptr(),
+                         block_table.shape[1], seq_lens.data_ptr(), B, 1 if pdl else 0,
+                         _raw_stream(self.device.index))
+        if status:
+            raise Fp4GemvError(status, "fp4gemv_kv_append")
+
+    def attend(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, sm_scale: float | None = None,
+               window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, pdl: bool = True) -> torch.Tensor:
+        """Attention of q (bf16 or f16 [B, q_len, heads, head_dim], the newest
+        q_len tokens of every sequence, already appended; tokens at one stride
+        that is a multiple of 8, heads contiguous).  Query i sees tokens up to
+        its own position, the last ``window`` of them if that is not 0; one
+        that sees none gives zeros.  ``sm_scale`` defaults to 1 /
+        sqrt(head_dim); ``lse``: fp32 [B, q_len, heads] to receive the natural
+        log of the softmax's sums.  Returns ``out``."""
+        B = self._check_sequences(block_table, seq_lens)
+        D = self.head_dim
+        if (q.dtype is not _BF16 and q.dtype is not _F16) or q.dim() != 4 or q.shape[0] != B or q.shape[3] != D or \
+                q.device != self.device:
+            raise ValueError(f"q must be a bf16 or f16 [{B}, q_len, heads, {D}] tensor on the cache's device")
+        n, heads = q.shape[1], q.shape[2]
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif out.dtype is not q.dtype or out.shape != q.shape or out.device != self.device:
+            raise ValueError("out must have q's shape, type and device")
+        ldq, ldo = self._token_stride(q, "q"), self._token_stride(out, "out")
+        if lse is not None and (lse.dtype is not _F32 or lse.shape != q.shape[:3] or not lse.is_contiguous() or
+                                lse.device != self.device):
+            raise ValueError(f"lse must be a contiguous fp32 [{B}, {n}, {heads}] tensor on the cache's device")
+        if B == 0:
+            return out
+        stream = _raw_stream(self.device.index)
+        if workspace is None:
+            workspace = attention_workspace(self.device, D, stream)
+        status = _attend(self._handle, q.data_ptr(), ldq, 0 if q.dtype is _BF16 else 1, heads, n,
+                         block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), B,
+                         self._sm_scale if sm_scale is None else sm_scale, window, out.data_ptr(), ldo,
+                         lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+                         workspace.numel() * workspace.element_size(), 1 if pdl else 0, stream)
+        if status:
+            raise Fp4GemvError(status, "fp4gemv_kv_attention")
+        return out
+
+    @staticmethod
+    def _token_stride(t: torch.Tensor, name: str) -> int:
+        """The one stride between tokens of a [B, n, heads, head_dim] tensor."""
+        B, n, heads, dim = t.shape
+        sb, sn, sh, sd = t.stride()
+        step = sn if n > 1 else sb if B > 1 else heads * dim
+        if sd != 1 or (sh != dim and heads > 1) or (n > 1 and B > 1 and sb != n * sn):
+            raise ValueError(f"{name} must have contiguous heads and one stride between all its tokens")
+        return step
