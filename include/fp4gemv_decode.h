@@ -30,7 +30,8 @@ typedef enum { FP4GEMV_BF16 = 0, FP4GEMV_F16 = 1, FP4GEMV_F32 = 2 } fp4gemv_dtyp
  *   E4M3  scale = the least power of two, not below 2^-100, with
  *         amax <= 448 * scale: joining a page moves older codes by exact
  *         powers of two;
- *   INT8  scale = max(amax / 127, 2^-100), codes -127 .. 127. */
+ *   INT8  scale = max(amax * (1 / 127), 2^-100), 1 / 127 rounded to binary32;
+ *         codes -127 .. 127. */
 typedef enum { FP4GEMV_KV_E4M3 = 0, FP4GEMV_KV_INT8 = 1 } fp4gemv_kv_format;
 
 /* Pages of block_size tokens: codes uint8 [num_blocks, kv_heads, block_size,

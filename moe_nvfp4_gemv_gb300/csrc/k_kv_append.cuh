@@ -40,7 +40,7 @@ constexpr int kAppendChunks = 8;                       // chunks of 8 values per
 // The scale of a page whose largest magnitude is amax (finite).
 template <bool kInt8>
 __device__ __forceinline__ float kv_scale(float amax) {
-  if (kInt8) return fmaxf(__fdiv_rn(amax, 127.0f), kKvMinScale);
+  if (kInt8) return fmaxf(__fmul_rn(amax, 1.0f / 127.0f), kKvMinScale);
   // the least 2^e with amax <= 1.75 * 2^(e + 8): the exponent, one more when
   // the mantissa is above 1.75
   const uint32_t b = __float_as_uint(amax);

@@ -15,7 +15,7 @@ def page_scale(amax: np.ndarray, fmt: str) -> np.ndarray:
     """fp32 scales of fp32 magnitudes."""
     amax = np.asarray(amax, np.float32)
     if fmt == "int8":
-        return np.maximum(amax / np.float32(127), MIN_SCALE).astype(np.float32)
+        return np.maximum(amax * np.float32(1 / 127), MIN_SCALE).astype(np.float32)
     e = np.full(amax.shape, -100.0)
     live = amax > 0
     m, x = np.frexp(amax[live].astype(np.float64) / 448.0)  # exact enough: a 24-bit number over 7 * 2^6
