@@ -106,11 +106,11 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   if (heads % cache->kv_heads != 0 || group > FP4GEMV_KV_MAX_GROUP || q_len > FP4GEMV_KV_MAX_QLEN ||
       B > FP4GEMV_KV_MAX_BATCH)
     return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
-  // row tiles: 16 rows per pass over the KV codes, 32 where there are more
-  // (head_dim 256 has registers for 16 only)
+  // row tiles: the 8, 16 or 32 rows that a pass over the codes serves
+  // (head_dim 256 has registers for 16)
   const int rows = q_len * group;
-  const int per_tile = rows > 16 && cache->head_dim <= 128 ? 32 : 16;
-  const int row_tiles = (rows + per_tile - 1) / per_tile;
+  const int row_units = rows <= 8 ? 1 : rows <= 16 || cache->head_dim > 128 ? 2 : 4;
+  const int row_tiles = (rows + 8 * row_units - 1) / (8 * row_units);
   const int64_t tokens = static_cast<int64_t>(max_blocks) * cache->block_size;
   if (tokens > (1ll << 30) ||
       static_cast<double>(tokens) / 16 * B * cache->kv_heads * row_tiles >= 2147480000.0)  // strips count in 32 bits
@@ -152,7 +152,7 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   p.f16 = dtype == FP4GEMV_F16;
   p.sm_scale = sm_scale;
   fp4::count_launch();
-  return from_cuda(fp4::launch_kv_attention(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, per_tile, sms, pdl,
+  return from_cuda(fp4::launch_kv_attention(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms, pdl,
                                             stream));
 }
 

@@ -20,8 +20,8 @@ cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, int T, int 
 cudaError_t launch_kv_append(const KvAppendParams& p, int int8, int pdl, cudaStream_t stream);
 // CTAs of the attention kernel at most (the workspace is sized for them).
 int kv_attention_max_ctas(int sms);
-// rows_per_tile: 16 or 32 (32 not with head_dim 256).
-cudaError_t launch_kv_attention(const KvAttnParams& p, int dim, int int8, int rows_per_tile, int sms, int pdl,
+// row_units: row tiles of 8, 16 or 32 rows: 1, 2 or 4 (4 not with head_dim 256).
+cudaError_t launch_kv_attention(const KvAttnParams& p, int dim, int int8, int row_units, int sms, int pdl,
                                 cudaStream_t stream);
 
 }  // namespace fp4

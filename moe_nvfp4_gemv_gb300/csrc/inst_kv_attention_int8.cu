@@ -3,9 +3,9 @@
 
 namespace fp4 {
 
-cudaError_t launch_kv_attention_int8(const KvAttnParams& p, int dim, int rows_per_tile, int sms, int pdl,
+cudaError_t launch_kv_attention_int8(const KvAttnParams& p, int dim, int row_units, int sms, int pdl,
                                      cudaStream_t stream) {
-  return attn_format<true>(p, dim, rows_per_tile, sms, pdl, stream);
+  return attn_format<true>(p, dim, row_units, sms, pdl, stream);
 }
 
 }  // namespace fp4

@@ -6,18 +6,26 @@
 //   s = (q . kc) ks sm_scale log2(e),
 // and instead of p = 2^(s - max s) the kernel weighs codes directly with
 //   w = 2^(s + log2 vs - m),   m the running maximum of s + log2 vs,
-// so that out = (sum w vc) / (sum w / vs) with every w <= 1 whatever the
+// so that out = (sum w vc) / (sum w / vs) with w of one size whatever the
 // scales: w is rounded to f16 for the product with vc, sums stay fp32.  The
 // codes are exact in f16.  Queries are made exact f16 operands by a power of
 // two for each row.
 //
 // The work.  KV bytes are read once, 16 tokens (a strip) of K and V of one
-// head at a time, by mma.sync m16n8k16: the rows of A are the query rows that
-// share the KV head (heads of the group x new tokens), B are the codes,
-// converted from 8 bits to f16 in registers right before use, so shared
-// memory and HBM see 8 bits only.  The contraction over head_dim is permuted
-// so that a thread's share of a K row is contiguous bytes, and V's pairs of
-// tokens are joined by byte permutes before the conversion.
+// head at a time, by mma.sync m16n8k16 in the transposed form: the codes are
+// the A operand (S^T = K Q^T with tokens as rows, out^T = V^T w^T with
+// head_dim as rows), the query rows that share the KV head (heads of the group
+// x new tokens) are the N side, in tiles of 8, so a group of up to 8 pays for
+// 8 rows and not for 16.  Codes are converted from 8 bits to f16 in registers
+// right before use: shared memory and HBM see 8 bits only.  The contraction
+// over head_dim is permuted so that a thread's share of a K row is contiguous
+// bytes, V's pairs of tokens are joined by byte permutes before the
+// conversion, and the weights turn from accumulator to operand by movmatrix.
+//
+// m follows the maximum lazily: weights may grow to 2^kAttnSlack before m
+// moves (f16 holds them, fp32 sums do), so the usual strip costs one vote and
+// no shuffles; a strip that would exceed it reduces its maxima over the warp
+// and rescales.
 //
 // Every warp streams its own strips through its own ring of cp.async stages
 // and keeps its own m, sums and accumulators: no barrier in the loop.  The
@@ -52,7 +60,7 @@ struct KvAttnParams {
   float* partial;      // [CTAs][2][rows][dim + 2]
   uint32_t* arrived;   // [CTAs], zero between calls
   int B, max_blocks, num_blocks, block_log2;
-  int kv_heads, group, q_len, row_tiles;  // row tiles of 16 R rows
+  int kv_heads, group, q_len, row_tiles;  // row tiles of 8 kN rows
   int window;
   int f16;             // element type of q and out
   float sm_scale;
@@ -60,6 +68,7 @@ struct KvAttnParams {
 
 constexpr int kAttnMaxBatch = 1024;
 constexpr float kAttnFloor = -1e30f;  // the running maximum before any token
+constexpr float kAttnSlack = 8.0f;    // log2 of the largest weight before the running maximum moves
 
 __device__ __forceinline__ float attn_ex2(float x) {
   float y;
@@ -71,12 +80,20 @@ __device__ __forceinline__ float attn_lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+// C += A B; A 16 x 16 (rows g and g + 8), B 16 x 8, f16; C fp32.
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of 16-bit values, two adjacent columns of
+// row g per thread.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -113,7 +130,8 @@ __device__ __forceinline__ uint32_t codes2_hi(uint32_t w) {
 // blocks of 64, 96 or 128 bytes.  A thread's K words of a block: kWords
 // consecutive 4-byte words of row g or g + 8, the k-steps' operands.  Its V
 // words: kWords / 2 words of each of the token rows 2t, 2t + 1, 2t + 8,
-// 2t + 9; word i, byte j is column g of the output tile 4 i + j.
+// 2t + 9; bytes 2 j and 2 j + 1 of word i are rows g and g + 8 of the output
+// tile 2 i + j.
 template <int kDim>
 struct AttnLayout {
   static constexpr int kBlk = kDim % 128 == 0 ? 128 : kDim;  // 64, 96 or 128
@@ -121,7 +139,7 @@ struct AttnLayout {
   static constexpr int kWords = kBlk / 16;   // K words per thread, row and block
   static constexpr int kVWords = kBlk / 32;  // V words per thread, token and block
   static constexpr int kSteps = kDim / 16;   // k-steps of 16
-  static constexpr int kTiles = kDim / 8;    // output tiles of 8 columns
+  static constexpr int kTiles = kDim / 16;   // output tiles of 16 dims
   static constexpr int kStripBytes = 16 * kDim;
 
   // Byte offset of 16-byte chunk c of token row r: chunks of a 128-byte line
@@ -154,10 +172,10 @@ struct AttnLayout {
                      : "r"(base + r * kDim + 32 * i + 8 * t));
     }
   }
-  // head_dim index of column n of output tile 4 i + j (block blk)
-  static __device__ __forceinline__ int v_dim(int blk, int i, int j, int n) {
-    if (kBlk == 96) return 32 * i + 4 * n + j;
-    return blk * kBlk + n * (kBlk / 8) + 4 * i + j;
+  // head_dim index of the first byte of thread row g's V word i (block blk)
+  static __device__ __forceinline__ int v_dim(int blk, int i, int g) {
+    if (kBlk == 96) return 32 * i + 4 * g;
+    return blk * kBlk + g * (kBlk / 8) + 4 * i;
   }
   static __device__ __forceinline__ void v_words(uint32_t base, int r, int blk, int g, uint32_t (&w)[kVWords]) {
     if constexpr (kBlk == 128) {
@@ -174,17 +192,20 @@ struct AttnLayout {
   }
 };
 
-template <int kDim, int kR>
+// kN: tiles of 8 query rows that a pass over the codes serves.
+template <int kDim, int kN>
 struct AttnCfg {
   using L = AttnLayout<kDim>;
   static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kRows = 16 * kR;
+  static constexpr int kRows = 8 * kN;
+  static constexpr int kResident = kDim <= 128 && kN <= 2 ? 2 : 1;  // CTAs per SM (registers, shared memory)
+  static constexpr bool kQInRegs = kN == 1 && kDim <= 128;     // queries stay in registers
   static constexpr int kStageBytes = 2 * L::kStripBytes + 16;  // K, V, the two scales
   static constexpr int kStages = kDim >= 128 ? 3 : kDim == 96 ? 4 : 5;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kQBytes = kR * L::kSteps * 32 * 16;
-  static constexpr int kSlabBytes = kWarps * 8 * 32 * 4;  // a joining pass: 8 rows, 32 columns of every warp
+  static constexpr int kQBytes = kN * L::kSteps * 32 * 8;
+  static constexpr int kSlabBytes = kWarps * 8 * 32 * 4;  // a joining pass: 8 rows, 32 dims of every warp
   // the joining passes come when the item's queries are no longer needed
   static constexpr int kQSlabBytes = kQBytes > kSlabBytes ? kQBytes : kSlabBytes;
   static constexpr int kSmem = kRingBytes + kQSlabBytes + kWarps * kRows * 8 + kRows * 8 + kRows * 4;
@@ -197,9 +218,10 @@ struct AttnCursor {
   int first;          // the sequence's first strip that any query sees (its token / 16)
 };
 
-template <int kDim, bool kInt8, int kR>
-__global__ void __launch_bounds__(256, kR == 1 && kDim <= 128 ? 2 : 1) kv_attention_kernel(const KvAttnParams p) {
-  using C = AttnCfg<kDim, kR>;
+template <int kDim, bool kInt8, int kN>
+__global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>::kResident)
+    kv_attention_kernel(const KvAttnParams p) {
+  using C = AttnCfg<kDim, kN>;
   using L = AttnLayout<kDim>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int line_of[kAttnMaxBatch + 1];  // strips of the sequences before each
@@ -365,8 +387,8 @@ __global__ void __launch_bounds__(256, kR == 1 && kDim <= 128 ? 2 : 1) kv_attent
   AttnCursor cur = seek(begin);
   int at = begin;
   int stage = 0;
-  float acc[kR][L::kTiles][4];
-  float m[kR][2], sum[kR][2];
+  float acc[kN][L::kTiles][4];  // dims by rows: thread's rows 2t, 2t + 1 of every tile of 8
+  float m[kN][2], sum[kN][2];
   while (at < end) {
     const int seg_end = min(end, at + cur.strips - cur.strip);
     const int n = length(cur.b);
@@ -419,31 +441,34 @@ __global__ void __launch_bounds__(256, kR == 1 && kDim <= 128 ? 2 : 1) kv_attent
           tt = o / (L::kBlk / 4);
           i4 = (o - tt * (L::kBlk / 4)) >> 2;
         }
-        const int st = blk * L::kWords + i4, reg = ((r >> 3) & 1) + ((o & 2) ? 2 : 0);
-        const uint32_t dst =
-            q_base + (((r >> 4) * L::kSteps + st) * 32 + (r & 7) * 4 + tt) * 16 + reg * 4;
+        const int st = blk * L::kWords + i4;
+        const uint32_t dst = q_base + ((((r >> 3) * L::kSteps + st) >> 1) * 32 + (r & 7) * 4 + tt) * 16 + (st & 1) * 8 +
+                             ((o & 2) ? 4 : 0);
         asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(pack_f16(f.x * down, f.y * down)) : "memory");
       }
     }
     __syncthreads();
-    float rs[kR][2];
-    int see_to[kR][2], see_from[kR][2];  // tokens a row sees: [from, to)
+    auto q_frag = [&](int nt, int pair) -> uint4 {  // k-steps 2 pair and 2 pair + 1
+      return lds128(q_base + ((nt * (L::kSteps / 2) + pair) * 32 + lane) * 16);
+    };
+    uint4 qr[C::kQInRegs ? L::kSteps / 2 : 1];
+    if constexpr (C::kQInRegs) {
 #pragma unroll
-    for (int r = 0; r < kR; ++r)
+      for (int i = 0; i < L::kSteps / 2; ++i) qr[i] = q_frag(0, i);
+    }
+    float rs[kN][2];
+#pragma unroll
+    for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int local = r * 16 + h * 8 + g, row = row0 + local;
-        rs[r][h] = row_scale[local];
-        const int pos = n - p.q_len + min(row, rows - 1) / p.group;
-        see_to[r][h] = pos + 1;
-        see_from[r][h] = p.window > 0 ? pos - p.window + 1 : 0;
-        m[r][h] = kAttnFloor;
-        sum[r][h] = 0.0f;
+        rs[nt][h] = row_scale[nt * 8 + 2 * t + h];
+        m[nt][h] = kAttnFloor;
+        sum[nt][h] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < L::kTiles; ++j) acc[r][j][2 * h] = acc[r][j][2 * h + 1] = 0.0f;
+        for (int j = 0; j < L::kTiles; ++j) acc[nt][j][h] = acc[nt][j][2 + h] = 0.0f;
       }
-    const int tokens_all = n - p.q_len + 1;                              // every row sees those before this one
-    const int tokens_low = p.window > 0 ? max(0, n - p.window) : 0;      // ... from this one on
+    const int tokens_all = n - p.q_len + 1;                          // every row sees those before this one
+    const int tokens_low = p.window > 0 ? max(0, n - p.window) : 0;  // ... from this one on
 
     // this warp's strips of the segment: line places begin + warp + k kWarps
     int i = at + ((begin + warp - at) % C::kWarps + C::kWarps) % C::kWarps;
@@ -456,23 +481,31 @@ __global__ void __launch_bounds__(256, kR == 1 && kDim <= 128 ? 2 : 1) kv_attent
       }
       const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + L::kStripBytes;
       const int tok = (cur.first + cur.strip + (i - at)) << 4;
-      float sc[kR][2][4];
+      float sc[kN][4];  // tokens g (0, 1) and g + 8 (2, 3) by rows 2t and 2t + 1
 #pragma unroll
-      for (int r = 0; r < kR; ++r)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) sc[r][j][0] = sc[r][j][1] = sc[r][j][2] = sc[r][j][3] = 0.0f;
+      for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
 #pragma unroll
       for (int blk = 0; blk < L::kBlocks; ++blk) {
         uint32_t w[2][L::kWords];
         L::k_words(kb, g, blk, t, w[0]);
         L::k_words(kb, g + 8, blk, t, w[1]);
 #pragma unroll
-        for (int s = 0; s < L::kWords; ++s) {
+        for (int s = 0; s < L::kWords; s += 2) {
+          uint32_t a[2][4];
 #pragma unroll
-          for (int r = 0; r < kR; ++r) {
-            const uint4 a = lds128(q_base + ((r * L::kSteps + blk * L::kWords + s) * 32 + lane) * 16);
+          for (int e = 0; e < 2; ++e) {
+            a[e][0] = codes2_lo<kInt8>(w[0][s + e]);
+            a[e][1] = codes2_lo<kInt8>(w[1][s + e]);
+            a[e][2] = codes2_hi<kInt8>(w[0][s + e]);
+            a[e][3] = codes2_hi<kInt8>(w[1][s + e]);
+          }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) mma_f16(sc[r][j], a, codes2_lo<kInt8>(w[j][s]), codes2_hi<kInt8>(w[j][s]));
+          for (int nt = 0; nt < kN; ++nt) {
+            uint4 b;
+            if constexpr (C::kQInRegs) b = qr[(blk * L::kWords + s) / 2];
+            else b = q_frag(nt, (blk * L::kWords + s) / 2);
+            mma_f16(sc[nt], a[0], b.x, b.y);
+            mma_f16(sc[nt], a[1], b.z, b.w);
           }
         }
       }
@@ -480,47 +513,51 @@ __global__ void __launch_bounds__(256, kR == 1 && kDim <= 128 ? 2 : 1) kv_attent
       const float lv = attn_lg2(fmaxf(ldsf(kb + 2 * L::kStripBytes + 4), 7.888609052210118e-31f));
       const float inv_vs = attn_ex2(-lv);
       const bool masked = tok + 16 > tokens_all || tok < tokens_low;
-      uint4 pa[kR];
+      uint32_t pb[kN][2];
 #pragma unroll
-      for (int r = 0; r < kR; ++r) {
+      for (int nt = 0; nt < kN; ++nt) {
+        const float f0 = rs[nt][0] * ks, f1 = rs[nt][1] * ks;
+        const float b0 = lv - m[nt][0], b1 = lv - m[nt][1];
+        float x[4] = {fmaf(sc[nt][0], f0, b0), fmaf(sc[nt][1], f1, b1), fmaf(sc[nt][2], f0, b0),
+                      fmaf(sc[nt][3], f1, b1)};
+        bool dead[4] = {false, false, false, false};
+        if (masked) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float f = rs[r][h] * ks;
-          float x[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = fmaf(sc[r][j >> 1][2 * h + (j & 1)], f, lv);
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int at_tok = tok + (j >> 1) * 8 + 2 * t + (j & 1);
-              if (at_tok >= see_to[r][h] || at_tok < see_from[r][h]) x[j] = -__builtin_huge_valf();
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int row = min(row0 + nt * 8 + 2 * t + (e & 1), rows - 1), at_tok = tok + (e >> 1) * 8 + g;
+            const int see_to = n - p.q_len + row / p.group + 1;
+            dead[e] = at_tok >= see_to || (p.window > 0 && at_tok < see_to - p.window);
+            if (dead[e]) x[e] = -__builtin_huge_valf();
           }
-          float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          const float mn = fmaxf(m[r][h], top);
-          if (__any_sync(0xFFFFFFFFu, mn > m[r][h])) {
-            const float fall = attn_ex2(m[r][h] - mn);
-            m[r][h] = mn;
-            sum[r][h] *= fall;
+        }
+        if (__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) > kAttnSlack)) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float f = h ? f1 : f0;
+            const float r0 = dead[h] ? -__builtin_huge_valf() : fmaf(sc[nt][h], f, lv);
+            const float r1 = dead[2 + h] ? -__builtin_huge_valf() : fmaf(sc[nt][2 + h], f, lv);
+            float top = fmaxf(r0, r1);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const float mn = fmaxf(m[nt][h], top);
+            const float fall = attn_ex2(m[nt][h] - mn);
+            m[nt][h] = mn;
+            sum[nt][h] *= fall;
 #pragma unroll
             for (int j = 0; j < L::kTiles; ++j) {
-              acc[r][j][2 * h] *= fall;
-              acc[r][j][2 * h + 1] *= fall;
+              acc[nt][j][h] *= fall;
+              acc[nt][j][2 + h] *= fall;
             }
+            x[h] = r0 - mn;
+            x[2 + h] = r1 - mn;
           }
-          float ws = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[j] = attn_ex2(x[j] - mn);
-            ws += x[j];
-          }
-          sum[r][h] = fmaf(ws, inv_vs, sum[r][h]);
-          const uint32_t lo = pack_f16(x[0], x[1]), hi = pack_f16(x[2], x[3]);
-          if (h == 0) pa[r].x = lo, pa[r].z = hi;
-          else pa[r].y = lo, pa[r].w = hi;
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = attn_ex2(x[e]);
+        sum[nt][0] = fmaf(x[0] + x[2], inv_vs, sum[nt][0]);
+        sum[nt][1] = fmaf(x[1] + x[3], inv_vs, sum[nt][1]);
+        pb[nt][0] = transpose8x8(pack_f16(x[0], x[1]));
+        pb[nt][1] = transpose8x8(pack_f16(x[2], x[3]));
       }
       const int left = n - tok;  // tokens of the sequence in this strip
 #pragma unroll
@@ -537,16 +574,16 @@ __global__ void __launch_bounds__(256, kR == 1 && kDim <= 128 ? 2 : 1) kv_attent
         }
 #pragma unroll
         for (int k = 0; k < L::kVWords; ++k) {
-          const uint32_t a01 = __byte_perm(w[0][k], w[1][k], 0x5140), a23 = __byte_perm(w[0][k], w[1][k], 0x7362);
-          const uint32_t b01 = __byte_perm(w[2][k], w[3][k], 0x5140), b23 = __byte_perm(w[2][k], w[3][k], 0x7362);
-          const uint32_t f0[4] = {codes2_lo<kInt8>(a01), codes2_hi<kInt8>(a01), codes2_lo<kInt8>(a23),
-                                  codes2_hi<kInt8>(a23)};
-          const uint32_t f1[4] = {codes2_lo<kInt8>(b01), codes2_hi<kInt8>(b01), codes2_lo<kInt8>(b23),
-                                  codes2_hi<kInt8>(b23)};
+          const uint32_t lo[2] = {__byte_perm(w[0][k], w[1][k], 0x5140), __byte_perm(w[0][k], w[1][k], 0x7362)};
+          const uint32_t hi[2] = {__byte_perm(w[2][k], w[3][k], 0x5140), __byte_perm(w[2][k], w[3][k], 0x7362)};
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t a[4] = {codes2_lo<kInt8>(lo[j]), codes2_hi<kInt8>(lo[j]), codes2_lo<kInt8>(hi[j]),
+                                   codes2_hi<kInt8>(hi[j])};
 #pragma unroll
-            for (int r = 0; r < kR; ++r) mma_f16(acc[r][(blk * L::kVWords + k) * 4 + j], pa[r], f0[j], f1[j]);
+            for (int nt = 0; nt < kN; ++nt)
+              mma_f16(acc[nt][(blk * L::kVWords + k) * 2 + j], a, pb[nt][0], pb[nt][1]);
+          }
         }
       }
       __syncwarp();
@@ -555,12 +592,12 @@ __global__ void __launch_bounds__(256, kR == 1 && kDim <= 128 ? 2 : 1) kv_attent
 
     // ---- the segment's end: join the warps ----
 #pragma unroll
-    for (int r = 0; r < kR; ++r)
+    for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        sum[r][h] += __shfl_xor_sync(0xFFFFFFFFu, sum[r][h], 1);
-        sum[r][h] += __shfl_xor_sync(0xFFFFFFFFu, sum[r][h], 2);
-        if (t == 0) ml[warp * C::kRows + r * 16 + h * 8 + g] = make_float2(m[r][h], sum[r][h]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) sum[nt][h] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][h], o);
+        if (g == 0) ml[warp * C::kRows + nt * 8 + 2 * t + h] = make_float2(m[nt][h], sum[nt][h]);
       }
     __syncthreads();
     if (tid < C::kRows) {
@@ -602,21 +639,17 @@ __global__ void __launch_bounds__(256, kR == 1 && kDim <= 128 ? 2 : 1) kv_attent
           l > 0.0f ? 0.6931471805599453f * (top + log2f(l)) : l == l ? -__builtin_huge_valf() : l;
     };
 #pragma unroll
-    for (int rh = 0; rh < 2 * kR; ++rh) {  // eight rows at a time
-      if (rh * 8 >= used) break;
+    for (int nt = 0; nt < kN; ++nt) {  // eight rows at a time
+      if (nt * 8 >= used) break;
 #pragma unroll
-      for (int k = 0; k < L::kTiles / 4; ++k) {  // and four output tiles (32 columns)
-        // (columns 2t and 2t + 1 of the four tiles are runs of four dims)
+      for (int k = 0; k < L::kTiles / 2; ++k) {  // and a V word's 32 dims
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int e = 2 * (rh & 1) + u;
-          *reinterpret_cast<float4*>(slab + ((warp * 8 + g) * 8 + 2 * t + u) * 4) =
-              make_float4(acc[rh >> 1][4 * k][e], acc[rh >> 1][4 * k + 1][e], acc[rh >> 1][4 * k + 2][e],
-                          acc[rh >> 1][4 * k + 3][e]);
-        }
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float4*>(slab + ((warp * 8 + 2 * t + h) * 8 + g) * 4) = make_float4(
+              acc[nt][2 * k][h], acc[nt][2 * k][2 + h], acc[nt][2 * k + 1][h], acc[nt][2 * k + 1][2 + h]);
         __syncthreads();
-        if (tid < 64 && rh * 8 + (tid >> 3) < used) {
-          const int r = rh * 8 + (tid >> 3), col = tid & 7;
+        if (tid < 64 && nt * 8 + (tid >> 3) < used) {
+          const int r = nt * 8 + (tid >> 3), col = tid & 7;
           const float2 tot = ml_all[r];
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -625,7 +658,7 @@ __global__ void __launch_bounds__(256, kR == 1 && kDim <= 128 ? 2 : 1) kv_attent
             const float4 a = *reinterpret_cast<const float4*>(slab + ((w * 8 + (tid >> 3)) * 8 + col) * 4);
             v.x = fmaf(a.x, f, v.x), v.y = fmaf(a.y, f, v.y), v.z = fmaf(a.z, f, v.z), v.w = fmaf(a.w, f, v.w);
           }
-          const int d = L::v_dim(k / L::kVWords, k % L::kVWords, 0, col);
+          const int d = L::v_dim(k / L::kVWords, k % L::kVWords, col);
           if (whole) {
             const float inv = tot.y != 0.0f ? 1.0f / tot.y : 0.0f;
             store(r, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
