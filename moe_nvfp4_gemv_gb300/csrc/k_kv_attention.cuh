@@ -691,25 +691,70 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
         const int64_t stride = static_cast<int64_t>(2) * C::kRows * (kDim + 2);
         // (the first CTA's part starts the item: its slot 1; the others' slot 0)
         auto part_of = [&](int c) { return p.partial + c * stride + (c == c0 ? C::kRows * (kDim + 2) : 0); };
-        for (int x = tid; x < used * (kDim / 4); x += C::kThreads) {
-          const int r = x / (kDim / 4), d = (x - r * (kDim / 4)) * 4;
+        // A thread takes four dims of a row and every `ways`-th partial, kBatch
+        // of them in flight; the ways meet in shared memory.
+        constexpr int kBatch = 8;
+        const int cells = used * (kDim / 4), parts = c1 - c0 + 1;
+        int ways = 1;
+        while (2 * ways * cells <= C::kThreads && ways * kBatch < parts) ways *= 2;
+        for (int x0 = 0; x0 < cells; x0 += C::kThreads / ways) {
+          const int way = tid / (C::kThreads / ways), x = x0 + tid - way * (C::kThreads / ways);
+          const bool live = x < cells;
+          const int r = live ? x / (kDim / 4) : 0, d = live ? (x - r * (kDim / 4)) * 4 : 0;
           float top = kAttnFloor, l = 0.0f;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int c = c0; c <= c1; ++c) {
-            const float* s = part_of(c) + r * (kDim + 2);
-            const float2 cm = __ldcg(reinterpret_cast<const float2*>(s + kDim));
-            const float2 a = __ldcg(reinterpret_cast<const float2*>(s + d));
-            const float2 b = __ldcg(reinterpret_cast<const float2*>(s + d + 2));
-            const float mn = fmaxf(top, cm.x);
-            const float fo = attn_ex2(top - mn), fn = attn_ex2(cm.x - mn);
-            v.x = v.x * fo + a.x * fn, v.y = v.y * fo + a.y * fn;
-            v.z = v.z * fo + b.x * fn, v.w = v.w * fo + b.y * fn;
-            l = l * fo + cm.y * fn;
+          for (int c = c0 + way; live && c <= c1; c += kBatch * ways) {
+            float2 cm[kBatch], a[kBatch], b[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              const int cc = c + j * ways;
+              cm[j] = make_float2(kAttnFloor, 0.0f);
+              a[j] = b[j] = make_float2(0.0f, 0.0f);
+              if (cc <= c1) {
+                const float* s = part_of(cc) + r * (kDim + 2);
+                cm[j] = __ldcg(reinterpret_cast<const float2*>(s + kDim));
+                a[j] = __ldcg(reinterpret_cast<const float2*>(s + d));
+                b[j] = __ldcg(reinterpret_cast<const float2*>(s + d + 2));
+              }
+            }
+            float mn = top;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
+            const float fall = attn_ex2(top - mn);
+            v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall, l *= fall;
             top = mn;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              const float f = attn_ex2(cm[j].x - mn);
+              v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
+              v.z = fmaf(b[j].x, f, v.z), v.w = fmaf(b[j].y, f, v.w);
+              l = fmaf(cm[j].y, f, l);
+            }
           }
-          const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-          store(r, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-          if (d == 0) store_lse(r, top, l);
+          if (ways > 1) {
+            float* const mine = slab + tid * 6;  // (6 kThreads floats: within the joining buffer)
+            *reinterpret_cast<float2*>(mine) = make_float2(v.x, v.y);
+            *reinterpret_cast<float2*>(mine + 2) = make_float2(v.z, v.w);
+            *reinterpret_cast<float2*>(mine + 4) = make_float2(top, l);
+            __syncthreads();
+            if (way == 0) {
+              for (int w = 1; w < ways; ++w) {
+                const float* o = slab + (tid + w * (C::kThreads / ways)) * 6;
+                const float mn = fmaxf(top, o[4]);
+                const float f = attn_ex2(top - mn), fo = attn_ex2(o[4] - mn);
+                v.x = v.x * f + o[0] * fo, v.y = v.y * f + o[1] * fo;
+                v.z = v.z * f + o[2] * fo, v.w = v.w * f + o[3] * fo;
+                l = l * f + o[5] * fo;
+                top = mn;
+              }
+            }
+            __syncthreads();
+          }
+          if (live && way == 0) {
+            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+            store(r, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+            if (d == 0) store_lse(r, top, l);
+          }
         }
       }
     }
