@@ -78,15 +78,15 @@ fp4gemv_status fp4gemv_kv_append(const fp4gemv_kv_cache* cache, const void* k, i
   return from_cuda(fp4::launch_kv_append(p, cache->format == FP4GEMV_KV_INT8, pdl, stream));
 }
 
-// [arrival counters | partials of at most 32 rows, two for each CTA]
-static size_t attn_counter_bytes(int ctas) { return (static_cast<size_t>(ctas) * 4 + 15) / 16 * 16; }
+// [arrival counters, three for each CTA | partials, four for each CTA]
+static size_t attn_counter_bytes(int ctas) { return (static_cast<size_t>(ctas) * 12 + 15) / 16 * 16; }
 
 size_t fp4gemv_kv_attention_workspace_bytes(int head_dim) {
   if (!dim_ok(head_dim)) return 0;
   int sms = 0;
   if (fp4::current_device_state(nullptr, &sms) != FP4GEMV_OK) return 0;
   const int ctas = fp4::kv_attention_max_ctas(sms);
-  return attn_counter_bytes(ctas) + static_cast<size_t>(ctas) * 2 * 32 * (head_dim + 2) * 4;
+  return attn_counter_bytes(ctas) + static_cast<size_t>(ctas) * 4 * fp4::kAttnMaxRows * (head_dim + 4) * 4;
 }
 
 fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype, int heads,

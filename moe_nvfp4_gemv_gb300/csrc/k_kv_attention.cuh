@@ -27,14 +27,21 @@
 // no shuffles; a strip that would exceed it reduces its maxima over the warp
 // and rescales.
 //
-// Every warp streams its own strips through its own ring of cp.async stages
-// and keeps its own m, sums and accumulators: no barrier in the loop.  The
-// strips of all (sequence, KV head, row tile) items form one line which is
-// cut into equal lengths, one for each CTA, wherever the cuts fall; at an
-// item's end the warps' results are joined through shared memory.  An item
-// that several CTAs share is joined from fp32 partials in the workspace by the
-// last of them to arrive (a counter that it leaves at zero).  Nothing waits on
-// another CTA.
+// Teams.  A team of one or two warps streams strips through its own ring of
+// cp.async stages; the warps of a team serve different query rows of the same
+// codes.  Every warp keeps its own m, sums and accumulators; nothing in the
+// loop is wider than a team.
+//
+// The line.  The strips of all (sequence, KV head, row tile) items form one
+// line.  Where items can be cut into at most one piece per CTA and still be
+// near evenly long, each CTA takes one piece; else the line itself is cut
+// into equal lengths, wherever the cuts fall.  At a segment's end (a CTA's
+// part of one item) the warps' results are joined through the ring stage that
+// happens to be free, while the other stages already fill for the next one.
+// An item that several CTAs share is joined from fp32 partials in the
+// workspace: the last of up to kAttnFan CTAs to arrive joins theirs, and with
+// more CTAs the last of those joins the joined ones (counters that are left
+// at zero).  Nothing waits on another CTA.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -57,16 +64,17 @@ struct KvAttnParams {
   const int32_t* table;
   const int32_t* lens;
   uint32_t* err;
-  float* partial;      // [CTAs][2][rows][dim + 2]
-  uint32_t* arrived;   // [CTAs], zero between calls
+  float* partial;      // [CTAs][4][kAttnMaxRows][dim + 4]
+  uint32_t* arrived;   // [CTAs][3], zero between calls
   int B, max_blocks, num_blocks, block_log2;
-  int kv_heads, group, q_len, row_tiles;  // row tiles of 8 kN rows
+  int kv_heads, group, q_len, row_tiles;  // row tiles of 8 kN kTeam rows
   int window;
   int f16;             // element type of q and out
   float sm_scale;
 };
 
-constexpr int kAttnMaxBatch = 1024;
+constexpr int kAttnMaxRows = 32;  // rows of a row tile at most
+constexpr int kAttnFan = 16;      // partials that one CTA joins
 constexpr float kAttnFloor = -1e30f;  // the running maximum before any token
 constexpr float kAttnSlack = 8.0f;    // log2 of the largest weight before the running maximum moves
 
@@ -177,6 +185,12 @@ struct AttnLayout {
     if (kBlk == 96) return 32 * i + 4 * g;
     return blk * kBlk + g * (kBlk / 8) + 4 * i;
   }
+  // the V word (of all blocks) and the row g whose first byte is dim d (a multiple of 4)
+  static __device__ __forceinline__ int2 v_place(int d) {
+    if (kBlk == 96) return make_int2(d >> 5, (d & 31) >> 2);
+    const int o = d % kBlk;
+    return make_int2((d / kBlk) * kVWords + (o % (kBlk / 8)) / 4, o / (kBlk / 8));
+  }
   static __device__ __forceinline__ void v_words(uint32_t base, int r, int blk, int g, uint32_t (&w)[kVWords]) {
     if constexpr (kBlk == 128) {
       const uint4 v = lds128(base + chunk(r, blk * 8 + g));
@@ -192,23 +206,25 @@ struct AttnLayout {
   }
 };
 
-// kN: tiles of 8 query rows that a pass over the codes serves.
-template <int kDim, int kN>
+// kN: tiles of 8 query rows per warp; kTeam: warps that share a ring.
+template <int kDim, int kN, int kTeam>
 struct AttnCfg {
   using L = AttnLayout<kDim>;
   static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kRows = 8 * kN;
-  static constexpr int kResident = kDim <= 128 && kN <= 2 ? 2 : 1;  // CTAs per SM (registers, shared memory)
-  static constexpr bool kQInRegs = kN == 1 && kDim <= 128;     // queries stay in registers
+  static constexpr int kTeams = kWarps / kTeam;
+  static constexpr int kQTiles = kN * kTeam;
+  static constexpr int kRows = 8 * kQTiles;
+  static constexpr int kResident = kDim <= 128 ? 2 : 1;        // CTAs per SM (registers, shared memory)
+  static constexpr bool kQInRegs = kN == 1;                    // a warp keeps its queries in registers
   static constexpr int kStageBytes = 2 * L::kStripBytes + 16;  // K, V, the two scales
-  static constexpr int kStages = kDim >= 128 ? 3 : kDim == 96 ? 4 : 5;
-  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kQBytes = kN * L::kSteps * 32 * 8;
-  static constexpr int kSlabBytes = kWarps * 8 * 32 * 4;  // a joining pass: 8 rows, 32 dims of every warp
-  // the joining passes come when the item's queries are no longer needed
-  static constexpr int kQSlabBytes = kQBytes > kSlabBytes ? kQBytes : kSlabBytes;
-  static constexpr int kSmem = kRingBytes + kQSlabBytes + kWarps * kRows * 8 + kRows * 8 + kRows * 4;
+  static constexpr int kStages0 = (kResident == 2 ? 102400 : 204800) / (kTeams * kStageBytes);
+  static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
+  static constexpr int kRingBytes = kTeams * kStages * kStageBytes;
+  static constexpr int kQBytes = kQInRegs ? 0 : kQTiles * L::kSteps * 32 * 8;
+  static constexpr int kSmem = kRingBytes + kQBytes + kTeams * kRows * 8 + kRows * 4;  // + the sequences
+  // dynamic shared memory for B sequences
+  static constexpr int smem(int B) { return kSmem + (B + 1) * 8; }
 };
 
 // One place on the line of all strips.
@@ -218,39 +234,100 @@ struct AttnCursor {
   int first;          // the sequence's first strip that any query sees (its token / 16)
 };
 
-template <int kDim, bool kInt8, int kN>
-__global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>::kResident)
+template <int kDim, bool kInt8, int kN, int kTeam>
+__global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kDim, kN, kTeam>::kResident)
     kv_attention_kernel(const KvAttnParams p) {
-  using C = AttnCfg<kDim, kN>;
+  using C = AttnCfg<kDim, kN, kTeam>;
   using L = AttnLayout<kDim>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int line_of[kAttnMaxBatch + 1];  // strips of the sequences before each
-  __shared__ int warp_sum[C::kWarps];
+  __shared__ int4 warp_sum[C::kWarps][2];
   __shared__ int last_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int team = warp / kTeam, sub = warp % kTeam;
+  // ring | queries (where not in registers) | (m, sum) [team][row] | row scales | sequences
+  const uint32_t sm = smem_u32(smem);
+  const uint32_t q_base = sm + C::kRingBytes;
+  float2* const ml = reinterpret_cast<float2*>(smem + C::kRingBytes + C::kQBytes);
+  float* const row_scale = reinterpret_cast<float*>(ml + C::kTeams * C::kRows);
+  int2* const seq = reinterpret_cast<int2*>(row_scale + C::kRows);  // (strips or pieces before it, length)
   if (tid == 0) pdl_launch_dependents();
   pdl_wait();
 
-  const int rows = p.q_len * p.group;      // query rows of an item's head
+  const int rows = p.q_len * p.group;  // query rows of a KV head
   const int items = p.kv_heads * p.row_tiles;
   const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.block_log2;
-  auto length = [&](int b) -> int {
-    const int n = __ldg(p.lens + b);
-    return n < 0 ? 0 : n > cap ? static_cast<int>(cap) : n;
-  };
   auto first_strip = [&](int n) -> int {
     const int at = n - p.q_len;  // the first query's position
     return p.window > 0 && at >= p.window ? (at - p.window + 1) >> 4 : 0;
   };
-  // ---- the line: an exclusive scan of the sequences' strips ----
-  int base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += C::kThreads) {
-    const int b = b0 + tid;
+  auto strips_of = [&](int n) -> int { return ((n + 15) >> 4) - first_strip(n); };
+
+  // ---- the line ----
+  // sum over the sequences of what f gives for each, by all threads (up to four sums)
+  auto block_sum = [&](int4 v) -> int4 {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+      v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+      v.z += __shfl_xor_sync(0xFFFFFFFFu, v.z, o);
+      v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, o);
+    }
+    if (C::kWarps > 1 && p.B > 32) {  // (every warp has summed the first 32 alike otherwise)
+      if (lane == 0) warp_sum[warp][0] = v;
+      __syncthreads();
+      v = make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < C::kWarps; ++i) {
+        const int4 o = warp_sum[i][0];
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+      }
+      __syncthreads();
+    }
+    return v;
+  };
+  // thread's sequences: first, first + step, ... (up to 32: one per lane, every warp alike)
+  const int first_b = p.B <= 32 ? lane : tid, step_b = p.B <= 32 ? 32 : C::kThreads;
+  int4 v4 = make_int4(0, 0, 0, 0);
+  for (int b = first_b; b < p.B; b += step_b) {
+    const int raw = __ldg(p.lens + b);
+    const int n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
+    if (n != raw && blockIdx.x == 0) raise_error(p.err, FP4_ERR_BADIDX);
+    seq[b].y = n;  // (several warps may write the same value)
+    v4.x += strips_of(n) * items;
+  }
+  const int total = block_sum(v4).x;
+  const int ctas = static_cast<int>(gridDim.x);
+  // the shortest of four lengths whose pieces fit the CTAs
+  const int even = (total + ctas - 1) / ctas;
+  int per = 0;  // strips per piece; 0: cut the line
+  {
+    auto whole_rounds = [&](int x) { return (x + C::kTeams - 1) / C::kTeams * C::kTeams; };
+    const int len[4] = {whole_rounds(even), whole_rounds(even + even / 8), whole_rounds(even + even / 4),
+                        whole_rounds(even + even / 2)};
+    v4 = make_int4(0, 0, 0, 0);
+    for (int b = first_b; b < p.B; b += step_b) {
+      const int s = strips_of(seq[b].y);
+      v4.x += (s + len[0] - 1) / max(len[0], 1) * items;
+      v4.y += (s + len[1] - 1) / max(len[1], 1) * items;
+      v4.z += (s + len[2] - 1) / max(len[2], 1) * items;
+      v4.w += (s + len[3] - 1) / max(len[3], 1) * items;
+    }
+    v4 = block_sum(v4);
+    if (v4.w <= ctas) per = len[3];
+    if (v4.z <= ctas) per = len[2];
+    if (v4.y <= ctas) per = len[1];
+    if (v4.x <= ctas) per = len[0];
+  }
+  const bool pieces = per > 0;
+  // an exclusive scan of the sequences' strips, or pieces
+  int line_end = 0;
+  for (int b0 = 0; b0 < p.B; b0 += step_b) {
+    const int b = b0 + first_b;
     int mine = 0;
     if (b < p.B) {
-      const int n = length(b);
-      if (n != __ldg(p.lens + b) && blockIdx.x == 0) raise_error(p.err, FP4_ERR_BADIDX);
-      mine = (((n + 15) >> 4) - first_strip(n)) * items;
+      mine = strips_of(seq[b].y);
+      if (pieces) mine = (mine + per - 1) / per;
+      mine *= items;
     }
     int sum = mine;
 #pragma unroll
@@ -258,25 +335,29 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
       const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
       if (lane >= o) sum += v;
     }
-    if (lane == 31) warp_sum[warp] = sum;
-    __syncthreads();
-    int before = base, whole = base;
+    int before = line_end, whole = line_end;
+    if (p.B > 32) {
+      if (lane == 31) warp_sum[warp][1].x = sum;
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < C::kWarps; ++i) {
-      before += i < warp ? warp_sum[i] : 0;
-      whole += warp_sum[i];
+      for (int i = 0; i < C::kWarps; ++i) {
+        before += i < warp ? warp_sum[i][1].x : 0;
+        whole += warp_sum[i][1].x;
+      }
+      __syncthreads();
+    } else {
+      whole += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
-    if (b < p.B) line_of[b] = before + sum - mine;
-    base = whole;
-    __syncthreads();
+    if (b < p.B) seq[b].x = before + sum - mine;
+    line_end = whole;
   }
-  const int total = base;
-  if (tid == 0) line_of[p.B] = total;
-  __syncthreads();
+  if (lane == 0) seq[p.B].x = line_end;  // (every warp the same value)
+  if (p.B > 32) __syncthreads();
+  else __syncwarp();
 
   // sequences nobody visits: zeros, lse -inf
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (line_of[b + 1] != line_of[b]) continue;
+  for (int b = blockIdx.x; b < p.B; b += ctas) {
+    if (seq[b + 1].x != seq[b].x) continue;
     const int heads = p.kv_heads * p.group;
     for (int i = tid; i < p.q_len * heads * (kDim / 8); i += C::kThreads) {
       const int64_t row = i / (kDim / 8);
@@ -285,33 +366,36 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
       if (p.lse && i % (kDim / 8) == 0) p.lse[tok * heads + row % heads] = -__builtin_huge_valf();
     }
   }
-  // this CTA's share, in whole rounds of its warps
-  const int rounds = (total + C::kWarps - 1) / C::kWarps;
-  const int per = (rounds + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x) * C::kWarps;
-  const int64_t begin64 = static_cast<int64_t>(per) * blockIdx.x;
-  if (begin64 >= total) return;
+  // this CTA's share of the line (of pieces: one)
+  if (!pieces) per = (even + C::kTeams - 1) / C::kTeams * C::kTeams;
+  const int64_t begin64 = pieces ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(per) * blockIdx.x;
+  if (begin64 >= line_end) return;
   const int begin = static_cast<int>(begin64);
-  const int end = min(total, begin + per);
 
-  auto seek = [&](int at) -> AttnCursor {  // the cursor of strip `at` of the line (at < total)
-    int lo = 0, hi = p.B - 1;
+  AttnCursor cur;  // the share's first strip
+  int count;       // its length in strips
+  int first_cta = 0, parts = 1;  // of pieces: the item's CTAs
+  {
+    int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before (never an empty one)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (line_of[mid] <= at) lo = mid;
+      if (seq[mid].x <= begin) lo = mid;
       else hi = mid - 1;
     }
-    AttnCursor c;
-    c.b = lo;  // (the last that starts at or before: never an empty one)
-    const int n = length(lo);
-    c.first = first_strip(n);
-    c.strips = ((n + 15) >> 4) - c.first;
-    const int item = (at - line_of[lo]) / c.strips;
-    c.strip = (at - line_of[lo]) - item * c.strips;
-    c.head = item / p.row_tiles;
-    c.tile = item - c.head * p.row_tiles;
-    return c;
-  };
-  auto advance = [&](AttnCursor& c, int by) {  // (towards a place before `total`)
+    const int n = seq[lo].y, off = begin - seq[lo].x;
+    cur.b = lo;
+    cur.first = first_strip(n);
+    cur.strips = strips_of(n);
+    parts = pieces ? (cur.strips + per - 1) / per : 1;
+    const int unit = pieces ? parts : cur.strips;
+    const int item = off / unit, within = off - item * unit;
+    cur.head = item / p.row_tiles;
+    cur.tile = item - cur.head * p.row_tiles;
+    first_cta = begin - within;
+    cur.strip = pieces ? within * per : within;
+    count = pieces ? min(per, cur.strips - cur.strip) : min(per, line_end - begin);
+  }
+  auto advance = [&](AttnCursor& c, int by) {  // (towards a place on the line)
     c.strip += by;
     while (c.strip >= c.strips) {
       c.strip -= c.strips;
@@ -320,148 +404,156 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
         if (++c.head == p.kv_heads) {
           c.head = 0;
           do ++c.b;
-          while (line_of[c.b + 1] == line_of[c.b]);
-          const int n = length(c.b);
+          while (seq[c.b + 1].x == seq[c.b].x);
+          const int n = seq[c.b].y;
           c.first = first_strip(n);
-          c.strips = ((n + 15) >> 4) - c.first;
+          c.strips = strips_of(n);
         }
       }
     }
   };
 
-  // ---- the warp's ring ----
-  const uint32_t sm = smem_u32(smem);
-  const uint32_t ring = sm + warp * C::kStages * C::kStageBytes;
-  const uint32_t q_base = sm + C::kRingBytes;
-  float* const slab = reinterpret_cast<float*>(smem + C::kRingBytes);
-  float2* const ml = reinterpret_cast<float2*>(smem + C::kRingBytes + C::kQSlabBytes);  // [warp][row]
-  float2* const ml_all = ml + C::kWarps * C::kRows;                                     // [row]
-  float* const row_scale = reinterpret_cast<float*>(ml_all + C::kRows);
-
-  AttnCursor ahead{};
-  int ahead_at = begin + warp;
-  if (ahead_at < end) ahead = seek(ahead_at);
+  // ---- the team's ring: strips team, team + kTeams, ... of the share ----
+  const uint32_t ring = sm + team * C::kStages * C::kStageBytes;
   const int block_mask = (1 << p.block_log2) - 1;
-  auto page_of = [&](const AttnCursor& c) -> int {
-    const int tok = (c.first + c.strip) << 4;
-    return __ldg(p.table + static_cast<int64_t>(c.b) * p.max_blocks + (tok >> p.block_log2));
+  AttnCursor ahead = cur;     // the strip whose page is read next
+  int ahead_at = team;        // its place in the share
+  int page[2], where[2];      // of the next two strips to copy: page id; KV head and place on the page
+  auto look_up = [&](int slot) {
+    page[slot] = 0;
+    where[slot] = -1;
+    if (ahead_at < count) {
+      const int tok = (ahead.first + ahead.strip) << 4;
+      page[slot] = __ldg(p.table + static_cast<int64_t>(ahead.b) * p.max_blocks + (tok >> p.block_log2));
+      where[slot] = (ahead.head << 8) | (tok & block_mask);
+      ahead_at += C::kTeams;
+      if (ahead_at < count) advance(ahead, C::kTeams);
+    }
   };
-  int page = ahead_at < end ? page_of(ahead) : 0;
+  if (ahead_at < count) advance(ahead, team);
+  look_up(0);
+  look_up(1);
   auto issue = [&](int stage) {
-    if (ahead_at < end) {
+    if (where[0] >= 0) {
       const uint32_t dst = ring + stage * C::kStageBytes;
-      int id = page;
+      int id = page[0];
       const bool good = id >= 0 && id < p.num_blocks;
       if (!good) {
         if (lane == 0) raise_error(p.err, FP4_ERR_BADIDX);
         id = 0;
       }
       const uint32_t bytes = good ? 16u : 0u;
-      const int64_t tile = static_cast<int64_t>(id) * p.kv_heads + ahead.head;
-      const int64_t at = ((tile << p.block_log2) + (((ahead.first + ahead.strip) << 4) & block_mask)) * kDim;
+      const int64_t tile = static_cast<int64_t>(id) * p.kv_heads + (where[0] >> 8);
+      const int64_t at = ((tile << p.block_log2) + (where[0] & 255)) * kDim;
 #pragma unroll
-      for (int i = 0; i < kDim / 32; ++i) {
-        const int c = i * 32 + lane;  // 16-byte chunk of the strip
+      for (int i = 0; i < kDim / 32; ++i) {  // (a team's warps share the chunks out)
+        const int c = i * 32 + lane;         // 16-byte chunk of the strip
         const int r = c / (kDim / 16), o = L::chunk(r, c - r * (kDim / 16));
-        cp_async16(dst + o, p.k_codes + at + c * 16, bytes);
-        cp_async16(dst + L::kStripBytes + o, p.v_codes + at + c * 16, bytes);
+        if (kTeam == 1 || sub == 0) cp_async16(dst + o, p.k_codes + at + c * 16, bytes);
+        if (kTeam == 1 || sub == 1) cp_async16(dst + L::kStripBytes + o, p.v_codes + at + c * 16, bytes);
       }
-      if (lane < 2) {
+      if (lane < 2 && sub == 0) {
         const float* s = (lane ? p.v_scale : p.k_scale) + tile;
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 2 * L::kStripBytes + 4 * lane), "l"(s),
                      "r"(good ? 4u : 0u)
                      : "memory");
       }
-      ahead_at += C::kWarps;
-      if (ahead_at < end) {
-        advance(ahead, C::kWarps);
-        page = page_of(ahead);
-      }
+      page[0] = page[1];
+      where[0] = where[1];
+      look_up(1);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto team_sync = [&]() {
+    if constexpr (kTeam == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kTeam * 32) : "memory");
   };
 #pragma unroll
   for (int s = 0; s < C::kStages - 1; ++s) issue(s);
 
+  // ---- queries: f16 operands, scaled by a power of two for each row ----
+  auto q_load = [&](const AttnCursor& c, int tile8, uint4 (&raw)[L::kSteps / 2]) {  // row g of the item's tile of 8
+    const int row = c.tile * C::kRows + tile8 * 8 + g;
+    const bool live = row < rows;
+    const int64_t tok = static_cast<int64_t>(c.b) * p.q_len + (live ? row / p.group : 0);
+    const uint16_t* src =
+        p.q + tok * p.ldq + (static_cast<int64_t>(c.head) * p.group + (live ? row % p.group : 0)) * kDim;
+#pragma unroll
+    for (int i = 0; i < L::kSteps / 2; ++i) {  // words 2 i and 2 i + 1: eight dims in a row
+      const int d = L::k_dim(2 * i / L::kWords, 2 * i % L::kWords, t);
+      raw[i] = live ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto two = [&](uint32_t v) -> float2 {
+    return p.f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
+                 : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  };
+  auto q_scale = [&](uint4 (&raw)[L::kSteps / 2]) -> float {  // operands in place; row g's factor of the scores
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < L::kSteps / 2; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = two(w[j]);
+        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    // 2^-e brings amax to [2^14, 2^15)
+    const int field = static_cast<int>(__float_as_uint(amax) >> 23);
+    const int e = field == 0 ? 0 : min(max(field - 127 - 14, -126), 126);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < L::kSteps / 2; ++i) {
+      uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = two(w[j]);
+        w[j] = pack_f16(f.x * down, f.y * down);
+      }
+      raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return p.sm_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  };
+  uint4 qr[L::kSteps / 2];
+  if (C::kQInRegs) q_load(cur, sub, qr);
+
   // ---- segments: the parts of items in this CTA's share ----
-  AttnCursor cur = seek(begin);
-  int at = begin;
+  int at = 0;
   int stage = 0;
   float acc[kN][L::kTiles][4];  // dims by rows: thread's rows 2t, 2t + 1 of every tile of 8
   float m[kN][2], sum[kN][2];
-  while (at < end) {
-    const int seg_end = min(end, at + cur.strips - cur.strip);
-    const int n = length(cur.b);
+  while (at < count) {
+    const int seg_end = min(count, at + cur.strips - cur.strip);
+    const int n = seq[cur.b].y;
     const int row0 = cur.tile * C::kRows;
-    // the item's queries as f16 operands, scaled by a power of two per row
-    for (int r = warp; r < C::kRows; r += C::kWarps) {
-      const int row = row0 + r;
-      float amax = 0.0f;
-      uint32_t w[(kDim + 63) / 64];
-      const bool live = row < rows;
-      const uint32_t* src = nullptr;
-      if (live) {
-        const int64_t tok = static_cast<int64_t>(cur.b) * p.q_len + row / p.group;
-        src = reinterpret_cast<const uint32_t*>(p.q + tok * p.ldq +
-                                                (static_cast<int64_t>(cur.head) * p.group + row % p.group) * kDim);
-      }
-      auto two = [&](uint32_t v) -> float2 {
-        return p.f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
-                     : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-      };
-      // (lane takes words lane, lane + 32, ...; kDim / 2 words a row)
-#pragma unroll
-      for (int i = 0; i < (kDim + 63) / 64; ++i) {
-        const int k = i * 32 + lane;
-        const uint32_t v = live && k < kDim / 2 ? __ldg(src + k) : 0u;
-        w[i] = v;
-        const float2 f = two(v);
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-      // 2^-e brings amax to [2^14, 2^15)
-      const int field = static_cast<int>(__float_as_uint(amax) >> 23);
-      const int e = field == 0 ? 0 : min(max(field - 127 - 14, -126), 126);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      if (lane == 0)
-        row_scale[r] = p.sm_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-      for (int i = 0; i < (kDim + 63) / 64; ++i) {
-        const int k = i * 32 + lane;
-        if (k >= kDim / 2) break;
-        const float2 f = two(w[i]);
-        // where the pair (2k, 2k + 1) stands: operand word `reg` of thread (r % 8, tt) in step `st`
-        const int d = 2 * k, blk = d / L::kBlk, o = d - blk * L::kBlk;
-        int tt, i4;
-        if (L::kBlk == 96) {
-          tt = (o & 31) >> 3;
-          i4 = 2 * (o >> 5) + ((o & 7) >> 2);
-        } else {
-          tt = o / (L::kBlk / 4);
-          i4 = (o - tt * (L::kBlk / 4)) >> 2;
-        }
-        const int st = blk * L::kWords + i4;
-        const uint32_t dst = q_base + ((((r >> 3) * L::kSteps + st) >> 1) * 32 + (r & 7) * 4 + tt) * 16 + (st & 1) * 8 +
-                             ((o & 2) ? 4 : 0);
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(pack_f16(f.x * down, f.y * down)) : "memory");
-      }
-    }
-    __syncthreads();
-    auto q_frag = [&](int nt, int pair) -> uint4 {  // k-steps 2 pair and 2 pair + 1
-      return lds128(q_base + ((nt * (L::kSteps / 2) + pair) * 32 + lane) * 16);
-    };
-    uint4 qr[C::kQInRegs ? L::kSteps / 2 : 1];
-    if constexpr (C::kQInRegs) {
-#pragma unroll
-      for (int i = 0; i < L::kSteps / 2; ++i) qr[i] = q_frag(0, i);
-    }
+    const int wrow0 = row0 + sub * kN * 8;  // this warp's first row
     float rs[kN][2];
+    if constexpr (C::kQInRegs) {
+      const float f = q_scale(qr);
+      rs[0][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
+      rs[0][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+    } else {
+      for (int tile8 = warp; tile8 < C::kQTiles; tile8 += C::kWarps) {
+        q_load(cur, tile8, qr);
+        const float f = q_scale(qr);
+        if (t == 0) row_scale[tile8 * 8 + g] = f;
+#pragma unroll
+        for (int i = 0; i < L::kSteps / 2; ++i)
+          sts128(q_base + ((tile8 * (L::kSteps / 2) + i) * 32 + lane) * 16, qr[i]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) rs[nt][h] = row_scale[(sub * kN + nt) * 8 + 2 * t + h];
+    }
 #pragma unroll
     for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        rs[nt][h] = row_scale[nt * 8 + 2 * t + h];
         m[nt][h] = kAttnFloor;
         sum[nt][h] = 0.0f;
 #pragma unroll
@@ -470,15 +562,12 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
     const int tokens_all = n - p.q_len + 1;                          // every row sees those before this one
     const int tokens_low = p.window > 0 ? max(0, n - p.window) : 0;  // ... from this one on
 
-    // this warp's strips of the segment: line places begin + warp + k kWarps
-    int i = at + ((begin + warp - at) % C::kWarps + C::kWarps) % C::kWarps;
-    for (; i < seg_end; i += C::kWarps) {
+    // this team's strips of the segment: places team + k kTeams of the share
+    int i = at + ((team - at) % C::kTeams + C::kTeams) % C::kTeams;
+    for (; i < seg_end; i += C::kTeams) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-      __syncwarp();
-      {  // the stage read last is free: every lane is past it
-        const int next = stage == 0 ? C::kStages - 1 : stage - 1;
-        issue(next);
-      }
+      team_sync();  // the strip is there, and every lane is past the stage read last
+      issue(stage == 0 ? C::kStages - 1 : stage - 1);
       const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + L::kStripBytes;
       const int tok = (cur.first + cur.strip + (i - at)) << 4;
       float sc[kN][4];  // tokens g (0, 1) and g + 8 (2, 3) by rows 2t and 2t + 1
@@ -501,9 +590,10 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
           }
 #pragma unroll
           for (int nt = 0; nt < kN; ++nt) {
+            const int pair = (blk * L::kWords + s) / 2;
             uint4 b;
-            if constexpr (C::kQInRegs) b = qr[(blk * L::kWords + s) / 2];
-            else b = q_frag(nt, (blk * L::kWords + s) / 2);
+            if constexpr (C::kQInRegs) b = qr[pair];
+            else b = lds128(q_base + (((sub * kN + nt) * (L::kSteps / 2) + pair) * 32 + lane) * 16);
             mma_f16(sc[nt], a[0], b.x, b.y);
             mma_f16(sc[nt], a[1], b.z, b.w);
           }
@@ -524,7 +614,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
         if (masked) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int row = min(row0 + nt * 8 + 2 * t + (e & 1), rows - 1), at_tok = tok + (e >> 1) * 8 + g;
+            const int row = min(wrow0 + nt * 8 + 2 * t + (e & 1), rows - 1), at_tok = tok + (e >> 1) * 8 + g;
             const int see_to = n - p.q_len + row / p.group + 1;
             dead[e] = at_tok >= see_to || (p.window > 0 && at_tok < see_to - p.window);
             if (dead[e]) x[e] = -__builtin_huge_valf();
@@ -586,40 +676,47 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
           }
         }
       }
-      __syncwarp();
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
 
-    // ---- the segment's end: join the warps ----
+    // ---- the segment's end: join the teams ----
+    const bool starts = cur.strip == 0, ends = cur.strip + (seg_end - at) == cur.strips;
+    const bool whole = starts && ends;
+    AttnCursor next = cur;
+    if (seg_end < count) advance(next, cur.strips - cur.strip);
+    if (C::kQInRegs && seg_end < count) q_load(next, sub, qr);  // (arrives during the joining)
 #pragma unroll
     for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) sum[nt][h] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][h], o);
-        if (g == 0) ml[warp * C::kRows + nt * 8 + 2 * t + h] = make_float2(m[nt][h], sum[nt][h]);
+        if (g == 0) ml[team * C::kRows + (sub * kN + nt) * 8 + 2 * t + h] = make_float2(m[nt][h], sum[nt][h]);
       }
-    __syncthreads();
-    if (tid < C::kRows) {
-      float top = kAttnFloor, l = 0.0f;
-#pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, ml[w * C::kRows + tid].x);
-#pragma unroll
-      for (int w = 0; w < C::kWarps; ++w) {
-        const float2 v = ml[w * C::kRows + tid];
-        l += attn_ex2(v.x - top) * v.y;
-      }
-      ml_all[tid] = make_float2(top, l);
-    }
-    __syncthreads();
-    const bool starts = cur.strip == 0, ends = at - cur.strip + cur.strips == seg_end;
-    const bool whole = starts && ends;
     const int used = min(C::kRows, rows - row0);
-    float* const part = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (starts ? 1 : 0)) * C::kRows * (kDim + 2);
-    auto store = [&](int r, int d, float4 v) {  // four outputs of local row r, dims d .. d + 3
+    // a team's stage that is neither being read nor being filled, the one before its next: 8 rows of dims, fp32
+    auto slab_of = [&](int w) -> float* {
+      const int read = max(0, (seg_end - w + C::kTeams - 1) / C::kTeams);  // strips that the team has read so far
+      return reinterpret_cast<float*>(smem + (w * C::kStages + (read + C::kStages - 1) % C::kStages) * C::kStageBytes);
+    };
+    // 16-byte cell of word k, thread row g2 and query row r: places change by row, against bank conflicts
+    auto cell = [](int r, int k, int g2) -> int { return ((r * (L::kTiles / 2) + k) * 8 + (g2 ^ (r & 6))) * 4; };
+    // with two warps in a team, both are past the stage before either writes
+    constexpr int kRowFloats = kDim + 4;  // a partial row: the sums, m, the sum of weights
+    auto part_of = [&](int cta, int slot) -> float* {
+      return p.partial + (static_cast<int64_t>(cta) * 4 + slot) * (kAttnMaxRows * kRowFloats);
+    };
+    float* const part = part_of(blockIdx.x, starts ? 1 : 0);
+    auto out_row = [&](int r, int64_t* tok_out, int* head_out) {
       const int row = row0 + r;
-      const int64_t tok_out = static_cast<int64_t>(cur.b) * p.q_len + row / p.group;
-      uint16_t* o = p.out + tok_out * p.ldo + (static_cast<int64_t>(cur.head) * p.group + row % p.group) * kDim + d;
+      *tok_out = static_cast<int64_t>(cur.b) * p.q_len + row / p.group;
+      *head_out = cur.head * p.group + row % p.group;
+    };
+    auto store = [&](int r, int d, float4 v) {  // four outputs of local row r, dims d .. d + 3
+      int64_t tok_out;
+      int head_out;
+      out_row(r, &tok_out, &head_out);
+      uint16_t* o = p.out + tok_out * p.ldo + static_cast<int64_t>(head_out) * kDim + d;
       uint2 w;
       if (p.f16) {
         w.x = pack_f16(v.x, v.y);
@@ -633,88 +730,99 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
     };
     auto store_lse = [&](int r, float top, float l) {
       if (!p.lse) return;
-      const int row = row0 + r;
-      const int64_t tok_out = static_cast<int64_t>(cur.b) * p.q_len + row / p.group;
-      p.lse[tok_out * (p.kv_heads * p.group) + cur.head * p.group + row % p.group] =
+      int64_t tok_out;
+      int head_out;
+      out_row(r, &tok_out, &head_out);
+      p.lse[tok_out * (p.kv_heads * p.group) + head_out] =
           l > 0.0f ? 0.6931471805599453f * (top + log2f(l)) : l == l ? -__builtin_huge_valf() : l;
     };
+    if (kTeam > 1) team_sync();
 #pragma unroll
-    for (int nt = 0; nt < kN; ++nt) {  // eight rows at a time
-      if (nt * 8 >= used) break;
+    for (int q8 = 0; q8 < C::kQTiles; ++q8) {  // eight rows at a time
+      if (q8 * 8 >= used) break;
+      if (sub == q8 / kN) {
 #pragma unroll
-      for (int k = 0; k < L::kTiles / 2; ++k) {  // and a V word's 32 dims
+        for (int k = 0; k < L::kTiles / 2; ++k)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float4*>(slab + ((warp * 8 + 2 * t + h) * 8 + g) * 4) = make_float4(
-              acc[nt][2 * k][h], acc[nt][2 * k][2 + h], acc[nt][2 * k + 1][h], acc[nt][2 * k + 1][2 + h]);
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float4*>(slab_of(team) + cell(2 * t + h, k, g)) =
+                make_float4(acc[q8 % kN][2 * k][h], acc[q8 % kN][2 * k][2 + h], acc[q8 % kN][2 * k + 1][h],
+                            acc[q8 % kN][2 * k + 1][2 + h]);
+      }
+      __syncthreads();
+      for (int x = tid; x < 8 * (kDim / 4); x += C::kThreads) {
+        const int r8 = x / (kDim / 4), d = (x - r8 * (kDim / 4)) * 4, r = q8 * 8 + r8;
+        if (r >= used) break;
+        float top = kAttnFloor, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < C::kTeams; ++w) top = fmaxf(top, ml[w * C::kRows + r].x);
+        const int2 place = L::v_place(d);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < C::kTeams; ++w) {
+          const float2 o = ml[w * C::kRows + r];
+          const float f = attn_ex2(o.x - top);
+          const float4 a = *reinterpret_cast<const float4*>(slab_of(w) + cell(r8, place.x, place.y));
+          v.x = fmaf(a.x, f, v.x), v.y = fmaf(a.y, f, v.y), v.z = fmaf(a.z, f, v.z), v.w = fmaf(a.w, f, v.w);
+          l = fmaf(o.y, f, l);
+        }
+        if (whole) {
+          const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+          store(r, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+          if (d == 0) store_lse(r, top, l);
+        } else {
+          float* const o = part + r * kRowFloats;
+          __stcg(reinterpret_cast<float4*>(o + d), v);
+          if (d == 0) __stcg(reinterpret_cast<float2*>(o + kDim), make_float2(top, l));
+        }
+      }
+      __syncthreads();
+    }
+    if (!whole) {
+      // the CTAs c0 .. c0 + n_parts - 1 share the item; a CTA's part is in its slot 1 if it starts the item, else 0
+      int c0 = first_cta, n_parts = parts;
+      if (!pieces) {
+        const int item0 = begin + at - cur.strip;  // the item's place on the line
+        c0 = item0 / per;
+        n_parts = (item0 + cur.strips - 1) / per - c0 + 1;
+      }
+      // true for the last of `of` CTAs to come here (all threads alike)
+      auto last_of = [&](uint32_t* counter, int of) -> bool {
+        __threadfence();
         __syncthreads();
-        if (tid < 64 && nt * 8 + (tid >> 3) < used) {
-          const int r = nt * 8 + (tid >> 3), col = tid & 7;
-          const float2 tot = ml_all[r];
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-          for (int w = 0; w < C::kWarps; ++w) {
-            const float f = attn_ex2(ml[w * C::kRows + r].x - tot.x);
-            const float4 a = *reinterpret_cast<const float4*>(slab + ((w * 8 + (tid >> 3)) * 8 + col) * 4);
-            v.x = fmaf(a.x, f, v.x), v.y = fmaf(a.y, f, v.y), v.z = fmaf(a.z, f, v.z), v.w = fmaf(a.w, f, v.w);
-          }
-          const int d = L::v_dim(k / L::kVWords, k % L::kVWords, col);
-          if (whole) {
-            const float inv = tot.y != 0.0f ? 1.0f / tot.y : 0.0f;
-            store(r, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-          } else {
-            __stcg(reinterpret_cast<float2*>(part + r * (kDim + 2) + d), make_float2(v.x, v.y));
-            __stcg(reinterpret_cast<float2*>(part + r * (kDim + 2) + d + 2), make_float2(v.z, v.w));
-          }
+        if (tid == 0) {
+          last_flag = of == 1 || atomicAdd(counter, 1u) == static_cast<uint32_t>(of - 1);
+          if (last_flag && of > 1) *counter = 0u;
         }
         __syncthreads();
-      }
-    }
-    if (whole) {
-      if (tid < used) store_lse(tid, ml_all[tid].x, ml_all[tid].y);
-    } else {
-      if (tid < used)
-        __stcg(reinterpret_cast<float2*>(part + tid * (kDim + 2) + kDim), ml_all[tid]);
-      // the CTAs that share the item; the last to arrive joins their partials
-      const int item0 = at - cur.strip;
-      const int c0 = item0 / per, c1 = (item0 + cur.strips - 1) / per;
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const uint32_t before = atomicAdd(p.arrived + c0, 1u);
-        last_flag = before == static_cast<uint32_t>(c1 - c0);
-        if (last_flag) p.arrived[c0] = 0u;
-      }
-      __syncthreads();
-      if (last_flag) {
-        __threadfence();
-        const int64_t stride = static_cast<int64_t>(2) * C::kRows * (kDim + 2);
-        // (the first CTA's part starts the item: its slot 1; the others' slot 0)
-        auto part_of = [&](int c) { return p.partial + c * stride + (c == c0 ? C::kRows * (kDim + 2) : 0); };
-        // A thread takes four dims of a row and every `ways`-th partial, kBatch
-        // of them in flight; the ways meet in shared memory.
-        constexpr int kBatch = 8;
-        const int cells = used * (kDim / 4), parts = c1 - c0 + 1;
-        int ways = 1;
-        while (2 * ways * cells <= C::kThreads && ways * kBatch < parts) ways *= 2;
+        const bool last = last_flag;
+        if (last) __threadfence();
+        return last;
+      };
+      // joins `cnt` partials, of every step-th CTA from `from` on, into the outputs or into `into`
+      auto join = [&](int from, int step, int cnt, int slot, float* into) {
+        constexpr int kBatch = 8;  // partials in flight per thread
+        const int cells = used * (kDim / 4);
+        int ways = 1;  // neighbouring lanes that share a cell's partials out
+        while (ways < 32 && 2 * ways * cells <= C::kThreads && ways * kBatch < cnt) ways *= 2;
         for (int x0 = 0; x0 < cells; x0 += C::kThreads / ways) {
-          const int way = tid / (C::kThreads / ways), x = x0 + tid - way * (C::kThreads / ways);
+          const int way = tid % ways, x = x0 + tid / ways;
           const bool live = x < cells;
           const int r = live ? x / (kDim / 4) : 0, d = live ? (x - r * (kDim / 4)) * 4 : 0;
           float top = kAttnFloor, l = 0.0f;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int c = c0 + way; live && c <= c1; c += kBatch * ways) {
-            float2 cm[kBatch], a[kBatch], b[kBatch];
+          for (int k = way; live && k < cnt; k += kBatch * ways) {
+            float2 cm[kBatch];
+            float4 a[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-              const int cc = c + j * ways;
+              const int kk = k + j * ways, c = from + kk * step;
               cm[j] = make_float2(kAttnFloor, 0.0f);
-              a[j] = b[j] = make_float2(0.0f, 0.0f);
-              if (cc <= c1) {
-                const float* s = part_of(cc) + r * (kDim + 2);
-                cm[j] = __ldcg(reinterpret_cast<const float2*>(s + kDim));
-                a[j] = __ldcg(reinterpret_cast<const float2*>(s + d));
-                b[j] = __ldcg(reinterpret_cast<const float2*>(s + d + 2));
+              a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (kk < cnt) {
+                const float* o = part_of(c, slot + (c == c0 ? 1 : 0)) + r * kRowFloats;
+                cm[j] = __ldcg(reinterpret_cast<const float2*>(o + kDim));
+                a[j] = __ldcg(reinterpret_cast<const float4*>(o + d));
               }
             }
             float mn = top;
@@ -727,40 +835,50 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
             for (int j = 0; j < kBatch; ++j) {
               const float f = attn_ex2(cm[j].x - mn);
               v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
-              v.z = fmaf(b[j].x, f, v.z), v.w = fmaf(b[j].y, f, v.w);
+              v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
               l = fmaf(cm[j].y, f, l);
             }
           }
-          if (ways > 1) {
-            float* const mine = slab + tid * 6;  // (6 kThreads floats: within the joining buffer)
-            *reinterpret_cast<float2*>(mine) = make_float2(v.x, v.y);
-            *reinterpret_cast<float2*>(mine + 2) = make_float2(v.z, v.w);
-            *reinterpret_cast<float2*>(mine + 4) = make_float2(top, l);
-            __syncthreads();
-            if (way == 0) {
-              for (int w = 1; w < ways; ++w) {
-                const float* o = slab + (tid + w * (C::kThreads / ways)) * 6;
-                const float mn = fmaxf(top, o[4]);
-                const float f = attn_ex2(top - mn), fo = attn_ex2(o[4] - mn);
-                v.x = v.x * f + o[0] * fo, v.y = v.y * f + o[1] * fo;
-                v.z = v.z * f + o[2] * fo, v.w = v.w * f + o[3] * fo;
-                l = l * f + o[5] * fo;
-                top = mn;
-              }
-            }
-            __syncthreads();
+          for (int o = 1; o < ways; o <<= 1) {
+            const float to = __shfl_xor_sync(0xFFFFFFFFu, top, o), lo = __shfl_xor_sync(0xFFFFFFFFu, l, o);
+            const float4 u = make_float4(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o),
+                                         __shfl_xor_sync(0xFFFFFFFFu, v.z, o), __shfl_xor_sync(0xFFFFFFFFu, v.w, o));
+            const float mn = fmaxf(top, to);
+            const float f = attn_ex2(top - mn), fo = attn_ex2(to - mn);
+            v.x = v.x * f + u.x * fo, v.y = v.y * f + u.y * fo;
+            v.z = v.z * f + u.z * fo, v.w = v.w * f + u.w * fo;
+            l = l * f + lo * fo;
+            top = mn;
           }
           if (live && way == 0) {
-            const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-            store(r, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-            if (d == 0) store_lse(r, top, l);
+            if (into) {
+              float* const o = into + r * kRowFloats;
+              __stcg(reinterpret_cast<float4*>(o + d), v);
+              if (d == 0) __stcg(reinterpret_cast<float2*>(o + kDim), make_float2(top, l));
+            } else {
+              const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+              store(r, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+              if (d == 0) store_lse(r, top, l);
+            }
           }
+        }
+      };
+      const int fan = n_parts <= kAttnFan ? n_parts : kAttnFan;
+      const int mine = (static_cast<int>(blockIdx.x) - c0) / fan, from = c0 + mine * fan;
+      const int members = min(fan, n_parts - mine * fan);
+      if (last_of(p.arrived + from * 3 + (from == c0 ? 1 : 0), members)) {
+        if (n_parts <= kAttnFan) {
+          join(c0, 1, n_parts, 0, nullptr);
+        } else {
+          const int groups = (n_parts + fan - 1) / fan;
+          join(from, 1, members, 0, part_of(from, 2 + (from == c0 ? 1 : 0)));
+          if (last_of(p.arrived + c0 * 3 + 2, groups)) join(c0, fan, groups, 2, nullptr);
         }
       }
     }
-    // on to the next item (the loop's end leaves it past the share)
+    // on to the next item
     at = seg_end;
-    if (at < end) advance(cur, cur.strips - cur.strip);
+    cur = next;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
