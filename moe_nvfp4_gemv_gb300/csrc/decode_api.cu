@@ -78,7 +78,7 @@ fp4gemv_status fp4gemv_kv_append(const fp4gemv_kv_cache* cache, const void* k, i
   return from_cuda(fp4::launch_kv_append(p, cache->format == FP4GEMV_KV_INT8, pdl, stream));
 }
 
-// [arrival counters, three for each CTA | partials, four for each CTA]
+// [arrival counters, three for each CTA | partials, two for each CTA]
 static size_t attn_counter_bytes(int ctas) { return (static_cast<size_t>(ctas) * 12 + 15) / 16 * 16; }
 
 size_t fp4gemv_kv_attention_workspace_bytes(int head_dim) {
@@ -86,7 +86,7 @@ size_t fp4gemv_kv_attention_workspace_bytes(int head_dim) {
   int sms = 0;
   if (fp4::current_device_state(nullptr, &sms) != FP4GEMV_OK) return 0;
   const int ctas = fp4::kv_attention_max_ctas(sms);
-  return attn_counter_bytes(ctas) + static_cast<size_t>(ctas) * 4 * fp4::kAttnMaxRows * (head_dim + 4) * 4;
+  return attn_counter_bytes(ctas) + static_cast<size_t>(ctas) * 2 * fp4::kAttnMaxRows * (head_dim + 4) * 4;
 }
 
 fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype, int heads,
@@ -112,8 +112,9 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   const int row_units = rows <= 8 ? 1 : rows <= 16 || cache->head_dim > 128 ? 2 : 4;
   const int row_tiles = (rows + 8 * row_units - 1) / (8 * row_units);
   const int64_t tokens = static_cast<int64_t>(max_blocks) * cache->block_size;
+  // (places on the line of strips, a quarter more with padding, are 32-bit)
   if (tokens > (1ll << 30) ||
-      static_cast<double>(tokens) / 16 * B * cache->kv_heads * row_tiles >= 2147480000.0)  // strips count in 32 bits
+      (static_cast<double>(tokens) / 16 + fp4::kAttnItemCost) * B * cache->kv_heads * row_tiles >= 1.2e9)
     return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
   if (crooked || !aligned(q, 16) || !aligned(out, 16) || ldq % 8 != 0 || ldo % 8 != 0 || !aligned(lse, 4) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 16))

@@ -32,16 +32,20 @@
 // codes.  Every warp keeps its own m, sums and accumulators; nothing in the
 // loop is wider than a team.
 //
-// The line.  The strips of all (sequence, KV head, row tile) items form one
-// line.  Where items can be cut into at most one piece per CTA and still be
-// near evenly long, each CTA takes one piece; else the line itself is cut
-// into equal lengths, wherever the cuts fall.  At a segment's end (a CTA's
-// part of one item) the warps' results are joined through the ring stage that
-// happens to be free, while the other stages already fill for the next one.
-// An item that several CTAs share is joined from fp32 partials in the
-// workspace: the last of up to kAttnFan CTAs to arrive joins theirs, and with
-// more CTAs the last of those joins the joined ones (counters that are left
-// at zero).  Nothing waits on another CTA.
+// The line.  The items (sequence, KV head, row tile) stand on one line, each
+// as long as its strips and kAttnItemCost more, for what an item's end costs.
+// The line is cut into equal shares wherever the cuts fall; or, where each
+// item can be cut into near equal pieces by itself with no more shares, at the
+// items' ends too, so that no share holds two items.  One CTA serves one
+// share; there are several times more shares than resident CTAs, because SMs
+// do not get equal parts of the memory's bandwidth: those that get more take
+// more shares.  At a segment's end (a share's part of one item) the teams'
+// results are joined through the ring stage that happens to be free, while
+// the other stages already fill for the next item.  An item that several
+// shares cut is joined from fp32 partials in the workspace: the last of up to
+// kAttnFan CTAs to arrive joins theirs, and with more the last of those joins
+// the joined ones (counters that are left at zero).  Nothing waits on another
+// CTA.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -64,7 +68,7 @@ struct KvAttnParams {
   const int32_t* table;
   const int32_t* lens;
   uint32_t* err;
-  float* partial;      // [CTAs][4][kAttnMaxRows][dim + 4]
+  float* partial;      // [CTAs][2][kAttnMaxRows][dim + 4]
   uint32_t* arrived;   // [CTAs][3], zero between calls
   int B, max_blocks, num_blocks, block_log2;
   int kv_heads, group, q_len, row_tiles;  // row tiles of 8 kN kTeam rows
@@ -75,6 +79,7 @@ struct KvAttnParams {
 
 constexpr int kAttnMaxRows = 32;  // rows of a row tile at most
 constexpr int kAttnFan = 16;      // partials that one CTA joins
+constexpr int kAttnItemCost = 16;  // an item's end, in strips
 constexpr float kAttnFloor = -1e30f;  // the running maximum before any token
 constexpr float kAttnSlack = 8.0f;    // log2 of the largest weight before the running maximum moves
 
@@ -224,14 +229,15 @@ struct AttnCfg {
   static constexpr int kQBytes = kQInRegs ? 0 : kQTiles * L::kSteps * 32 * 8;
   static constexpr int kSmem = kRingBytes + kQBytes + kTeams * kRows * 8 + kRows * 4;  // + the sequences
   // dynamic shared memory for B sequences
-  static constexpr int smem(int B) { return kSmem + (B + 1) * 8; }
+  static constexpr int smem(int B) { return kSmem + (B + 1) * 12; }
 };
 
-// One place on the line of all strips.
-struct AttnCursor {
+// An item and a place in it.
+struct AttnPlace {
   int b, head, tile;  // sequence, KV head, row tile
-  int strip, strips;  // within the item; the item's number of strips
+  int strip, strips;  // the place in strips; the item's number of strips
   int first;          // the sequence's first strip that any query sees (its token / 16)
+  int item;           // number of the item within the sequence
 };
 
 template <int kDim, bool kInt8, int kN, int kTeam>
@@ -240,16 +246,20 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
   using C = AttnCfg<kDim, kN, kTeam>;
   using L = AttnLayout<kDim>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int4 warp_sum[C::kWarps][2];
+  __shared__ int4 warp_sum[C::kWarps];
   __shared__ int last_flag;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (uniform, and known to be)
   const int team = warp / kTeam, sub = warp % kTeam;
   // ring | queries (where not in registers) | (m, sum) [team][row] | row scales | sequences
   const uint32_t sm = smem_u32(smem);
   const uint32_t q_base = sm + C::kRingBytes;
   float2* const ml = reinterpret_cast<float2*>(smem + C::kRingBytes + C::kQBytes);
   float* const row_scale = reinterpret_cast<float*>(ml + C::kTeams * C::kRows);
-  int2* const seq = reinterpret_cast<int2*>(row_scale + C::kRows);  // (strips or pieces before it, length)
+  // of the sequences before: strips, length on the line; then each one's tokens
+  int* const strips_before = reinterpret_cast<int*>(row_scale + C::kRows);
+  int* const line_before = strips_before + p.B + 1;
+  int* const tokens = line_before + p.B + 1;
   if (tid == 0) pdl_launch_dependents();
   pdl_wait();
 
@@ -261,9 +271,16 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
     return p.window > 0 && at >= p.window ? (at - p.window + 1) >> 4 : 0;
   };
   auto strips_of = [&](int n) -> int { return ((n + 15) >> 4) - first_strip(n); };
+  auto ceil_div = [](int x, int y) -> int {  // a division of floats, and its rounding set right
+    int q = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(y)));
+    while (q * y < x) ++q;
+    while ((q - 1) * y >= x) --q;
+    return q;
+  };
 
   // ---- the line ----
-  // sum over the sequences of what f gives for each, by all threads (up to four sums)
+  // Every warp goes over the first 32 sequences by itself, the warps share out more of them.
+  const int first_b = p.B <= 32 ? lane : tid, step_b = p.B <= 32 ? 32 : C::kThreads;
   auto block_sum = [&](int4 v) -> int4 {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -272,92 +289,95 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
       v.z += __shfl_xor_sync(0xFFFFFFFFu, v.z, o);
       v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, o);
     }
-    if (C::kWarps > 1 && p.B > 32) {  // (every warp has summed the first 32 alike otherwise)
-      if (lane == 0) warp_sum[warp][0] = v;
+    if (p.B > 32) {
+      if (lane == 0) warp_sum[warp] = v;
       __syncthreads();
       v = make_int4(0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < C::kWarps; ++i) {
-        const int4 o = warp_sum[i][0];
+        const int4 o = warp_sum[i];
         v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
       }
       __syncthreads();
     }
     return v;
   };
-  // thread's sequences: first, first + step, ... (up to 32: one per lane, every warp alike)
-  const int first_b = p.B <= 32 ? lane : tid, step_b = p.B <= 32 ? 32 : C::kThreads;
   int4 v4 = make_int4(0, 0, 0, 0);
   for (int b = first_b; b < p.B; b += step_b) {
     const int raw = __ldg(p.lens + b);
     const int n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
     if (n != raw && blockIdx.x == 0) raise_error(p.err, FP4_ERR_BADIDX);
-    seq[b].y = n;  // (several warps may write the same value)
+    tokens[b] = n;  // (with few sequences several warps write the same)
     v4.x += strips_of(n) * items;
+    v4.y += n > 0 ? items : 0;
   }
-  const int total = block_sum(v4).x;
-  const int ctas = static_cast<int>(gridDim.x);
-  // the shortest of four lengths whose pieces fit the CTAs
-  const int even = (total + ctas - 1) / ctas;
-  int per = 0;  // strips per piece; 0: cut the line
-  {
-    auto whole_rounds = [&](int x) { return (x + C::kTeams - 1) / C::kTeams * C::kTeams; };
-    const int len[4] = {whole_rounds(even), whole_rounds(even + even / 8), whole_rounds(even + even / 4),
-                        whole_rounds(even + even / 2)};
+  v4 = block_sum(v4);
+  const int total = v4.x, all_items = v4.y, ctas = static_cast<int>(gridDim.x);
+  auto rounds = [](int x) { return (x + C::kTeams - 1) / C::kTeams * C::kTeams; };  // whole rounds of the teams
+  // pieces per item, if those of the shortest of three lengths are no more than the CTAs
+  int per = 0;
+  if (all_items <= ctas) {
+    const int even = (total + ctas - 1) / ctas;
+    const int len[3] = {max(C::kTeams, rounds(even)), max(C::kTeams, rounds(even + even / 8)),
+                        max(C::kTeams, rounds(even + even / 4))};
     v4 = make_int4(0, 0, 0, 0);
     for (int b = first_b; b < p.B; b += step_b) {
-      const int s = strips_of(seq[b].y);
-      v4.x += (s + len[0] - 1) / max(len[0], 1) * items;
-      v4.y += (s + len[1] - 1) / max(len[1], 1) * items;
-      v4.z += (s + len[2] - 1) / max(len[2], 1) * items;
-      v4.w += (s + len[3] - 1) / max(len[3], 1) * items;
+      const int s = strips_of(tokens[b]);
+      v4.x += ceil_div(s, len[0]) * items;
+      v4.y += ceil_div(s, len[1]) * items;
+      v4.z += ceil_div(s, len[2]) * items;
     }
     v4 = block_sum(v4);
-    if (v4.w <= ctas) per = len[3];
-    if (v4.z <= ctas) per = len[2];
-    if (v4.y <= ctas) per = len[1];
-    if (v4.x <= ctas) per = len[0];
+    per = v4.x <= ctas ? len[0] : v4.y <= ctas ? len[1] : v4.z <= ctas ? len[2] : 0;
   }
   const bool pieces = per > 0;
-  // an exclusive scan of the sequences' strips, or pieces
+  if (!pieces) per = max(rounds((total + all_items * kAttnItemCost + ctas - 1) / ctas), C::kTeams);
+  // an item's length on the line, of which the first `lead` is its cost
+  const int lead = pieces ? 0 : kAttnItemCost;
+  auto line_of = [&](int strips) -> int { return pieces ? ceil_div(strips, per) * per : strips + (strips ? lead : 0); };
   int line_end = 0;
-  for (int b0 = 0; b0 < p.B; b0 += step_b) {
-    const int b = b0 + first_b;
-    int mine = 0;
-    if (b < p.B) {
-      mine = strips_of(seq[b].y);
-      if (pieces) mine = (mine + per - 1) / per;
-      mine *= items;
-    }
-    int sum = mine;
+  {
+    int strips_end = 0;
+    for (int b0 = 0; b0 < p.B; b0 += step_b) {
+      const int b = b0 + first_b;
+      const int s = b < p.B ? strips_of(tokens[b]) : 0, on_line = b < p.B ? line_of(s) : 0;
+      int2 sum = make_int2(s * items, on_line * items);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    int before = line_end, whole = line_end;
-    if (p.B > 32) {
-      if (lane == 31) warp_sum[warp][1].x = sum;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < C::kWarps; ++i) {
-        before += i < warp ? warp_sum[i][1].x : 0;
-        whole += warp_sum[i][1].x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, sum.x, o), v = __shfl_up_sync(0xFFFFFFFFu, sum.y, o);
+        if (lane >= o) sum.x += u, sum.y += v;
       }
-      __syncthreads();
-    } else {
-      whole += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      int2 before = make_int2(strips_end, line_end), whole = before;
+      if (p.B > 32) {
+        if (lane == 31) warp_sum[warp] = make_int4(sum.x, sum.y, 0, 0);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < C::kWarps; ++i) {
+          const int4 o = warp_sum[i];
+          if (i < warp) before.x += o.x, before.y += o.y;
+          whole.x += o.x, whole.y += o.y;
+        }
+        __syncthreads();
+      } else {
+        whole.x += __shfl_sync(0xFFFFFFFFu, sum.x, 31), whole.y += __shfl_sync(0xFFFFFFFFu, sum.y, 31);
+      }
+      if (b < p.B) {
+        strips_before[b] = before.x + sum.x - s * items;
+        line_before[b] = before.y + sum.y - on_line * items;
+      }
+      strips_end = whole.x, line_end = whole.y;
     }
-    if (b < p.B) seq[b].x = before + sum - mine;
-    line_end = whole;
+    if (lane == 0) {  // (every warp the same values)
+      strips_before[p.B] = strips_end;
+      line_before[p.B] = line_end;
+    }
   }
-  if (lane == 0) seq[p.B].x = line_end;  // (every warp the same value)
   if (p.B > 32) __syncthreads();
   else __syncwarp();
 
   // sequences nobody visits: zeros, lse -inf
   for (int b = blockIdx.x; b < p.B; b += ctas) {
-    if (seq[b + 1].x != seq[b].x) continue;
+    if (tokens[b] > 0) continue;
     const int heads = p.kv_heads * p.group;
     for (int i = tid; i < p.q_len * heads * (kDim / 8); i += C::kThreads) {
       const int64_t row = i / (kDim / 8);
@@ -366,88 +386,81 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
       if (p.lse && i % (kDim / 8) == 0) p.lse[tok * heads + row % heads] = -__builtin_huge_valf();
     }
   }
-  // this CTA's share of the line (of pieces: one)
-  if (!pieces) per = (even + C::kTeams - 1) / C::kTeams * C::kTeams;
-  const int64_t begin64 = pieces ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(per) * blockIdx.x;
-  if (begin64 >= line_end) return;
-  const int begin = static_cast<int>(begin64);
-
-  AttnCursor cur;  // the share's first strip
-  int count;       // its length in strips
-  int first_cta = 0, parts = 1;  // of pieces: the item's CTAs
-  {
-    int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before (never an empty one)
+  // ---- this CTA's share, in strips from the line's begin ----
+  if (static_cast<int64_t>(per) * blockIdx.x >= line_end) return;
+  // the last sequence whose entry is at most `at`: never an empty one
+  auto find = [&](const int* before, int at) -> int {
+    int lo = 0, hi = p.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (seq[mid].x <= begin) lo = mid;
+      if (before[mid] <= at) lo = mid;
       else hi = mid - 1;
     }
-    const int n = seq[lo].y, off = begin - seq[lo].x;
-    cur.b = lo;
-    cur.first = first_strip(n);
-    cur.strips = strips_of(n);
-    parts = pieces ? (cur.strips + per - 1) / per : 1;
-    const int unit = pieces ? parts : cur.strips;
-    const int item = off / unit, within = off - item * unit;
-    cur.head = item / p.row_tiles;
-    cur.tile = item - cur.head * p.row_tiles;
-    first_cta = begin - within;
-    cur.strip = pieces ? within * per : within;
-    count = pieces ? min(per, cur.strips - cur.strip) : min(per, line_end - begin);
-  }
-  auto advance = [&](AttnCursor& c, int by) {  // (towards a place on the line)
-    c.strip += by;
-    while (c.strip >= c.strips) {
-      c.strip -= c.strips;
-      if (++c.tile == p.row_tiles) {
-        c.tile = 0;
-        if (++c.head == p.kv_heads) {
-          c.head = 0;
-          do ++c.b;
-          while (seq[c.b + 1].x == seq[c.b].x);
-          const int n = seq[c.b].y;
-          c.first = first_strip(n);
-          c.strips = strips_of(n);
-        }
-      }
-    }
+    return lo;
+  };
+  auto cut = [&](int at) -> int {  // strips before place `at` of the line
+    if (at >= line_end) return strips_before[p.B];
+    const int b = find(line_before, at), s = strips_of(tokens[b]), len = line_of(s);
+    const int off = at - line_before[b], item = off / len;
+    return strips_before[b] + item * s + min(max(off - item * len - lead, 0), s);
+  };
+  const int begin = cut(per * static_cast<int>(blockIdx.x));
+  const int end = cut(static_cast<int>(min(static_cast<int64_t>(per) * (blockIdx.x + 1), static_cast<int64_t>(line_end))));
+  if (begin >= end) return;
+  auto locate = [&](int at) -> AttnPlace {  // strip `at`
+    AttnPlace c;
+    c.b = find(strips_before, at);
+    const int n = tokens[c.b], off = at - strips_before[c.b];
+    c.first = first_strip(n);
+    c.strips = strips_of(n);
+    c.item = off / c.strips;
+    c.strip = off - c.item * c.strips;
+    c.head = c.item / p.row_tiles;
+    c.tile = c.item - c.head * p.row_tiles;
+    return c;
   };
 
   // ---- the team's ring: strips team, team + kTeams, ... of the share ----
   const uint32_t ring = sm + team * C::kStages * C::kStageBytes;
   const int block_mask = (1 << p.block_log2) - 1;
-  AttnCursor ahead = cur;     // the strip whose page is read next
-  int ahead_at = team;        // its place in the share
-  int page[2], where[2];      // of the next two strips to copy: page id; KV head and place on the page
-  auto look_up = [&](int slot) {
-    page[slot] = 0;
-    where[slot] = -1;
-    if (ahead_at < count) {
-      const int tok = (ahead.first + ahead.strip) << 4;
-      page[slot] = __ldg(p.table + static_cast<int64_t>(ahead.b) * p.max_blocks + (tok >> p.block_log2));
-      where[slot] = (ahead.head << 8) | (tok & block_mask);
-      ahead_at += C::kTeams;
-      if (ahead_at < count) advance(ahead, C::kTeams);
+  // Lane l looks up the page of every 32nd strip of the team, from its l-th on: one batch to copy from, one ahead.
+  int looked = begin + team + lane * C::kTeams;  // the strip that the lane looks up next
+  auto look_up = [&](int* page, int* where) {    // page id; KV head and place on the page, -1 past the share
+    *page = 0;
+    *where = -1;
+    if (looked < end) {
+      const AttnPlace c = locate(looked);
+      const int tok = (c.first + c.strip) << 4;
+      *page = __ldg(p.table + static_cast<int64_t>(c.b) * p.max_blocks + (tok >> p.block_log2));
+      *where = (c.head << 8) | (tok & block_mask);
     }
+    looked += 32 * C::kTeams;
   };
-  if (ahead_at < count) advance(ahead, team);
-  look_up(0);
-  look_up(1);
+  int page, where, page_next = 0, where_next = -1, copied = 0;
+  look_up(&page, &where);
   auto issue = [&](int stage) {
-    if (where[0] >= 0) {
+    const int source = copied & 31;
+    if (source == 0 && copied > 0) {
+      page = page_next;
+      where = where_next;
+    }
+    if (source == 16) look_up(&page_next, &where_next);  // (halfway: there in time for the next batch)
+    ++copied;
+    const int spot = __shfl_sync(0xFFFFFFFFu, where, source);
+    if (spot >= 0) {
       const uint32_t dst = ring + stage * C::kStageBytes;
-      int id = page[0];
+      int id = __shfl_sync(0xFFFFFFFFu, page, source);
       const bool good = id >= 0 && id < p.num_blocks;
       if (!good) {
         if (lane == 0) raise_error(p.err, FP4_ERR_BADIDX);
         id = 0;
       }
       const uint32_t bytes = good ? 16u : 0u;
-      const int64_t tile = static_cast<int64_t>(id) * p.kv_heads + (where[0] >> 8);
-      const int64_t at = ((tile << p.block_log2) + (where[0] & 255)) * kDim;
+      const int64_t tile = static_cast<int64_t>(id) * p.kv_heads + (spot >> 8);
+      const int64_t at = ((tile << p.block_log2) + (spot & 255)) * kDim;
 #pragma unroll
-      for (int i = 0; i < kDim / 32; ++i) {  // (a team's warps share the chunks out)
-        const int c = i * 32 + lane;         // 16-byte chunk of the strip
+      for (int i = 0; i < kDim / 32; ++i) {
+        const int c = i * 32 + lane;  // 16-byte chunk of the strip
         const int r = c / (kDim / 16), o = L::chunk(r, c - r * (kDim / 16));
         if (kTeam == 1 || sub == 0) cp_async16(dst + o, p.k_codes + at + c * 16, bytes);
         if (kTeam == 1 || sub == 1) cp_async16(dst + L::kStripBytes + o, p.v_codes + at + c * 16, bytes);
@@ -458,9 +471,6 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
                      "r"(good ? 4u : 0u)
                      : "memory");
       }
-      page[0] = page[1];
-      where[0] = where[1];
-      look_up(1);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -472,7 +482,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
   for (int s = 0; s < C::kStages - 1; ++s) issue(s);
 
   // ---- queries: f16 operands, scaled by a power of two for each row ----
-  auto q_load = [&](const AttnCursor& c, int tile8, uint4 (&raw)[L::kSteps / 2]) {  // row g of the item's tile of 8
+  auto q_load = [&](const AttnPlace& c, int tile8, uint4 (&raw)[L::kSteps / 2]) {  // row g of the item's tile of 8
     const int row = c.tile * C::kRows + tile8 * 8 + g;
     const bool live = row < rows;
     const int64_t tok = static_cast<int64_t>(c.b) * p.q_len + (live ? row / p.group : 0);
@@ -518,26 +528,30 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
     return p.sm_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
   };
   uint4 qr[L::kSteps / 2];
-  if (C::kQInRegs) q_load(cur, sub, qr);
+  if (C::kQInRegs) q_load(locate(begin), sub, qr);
 
   // ---- segments: the parts of items in this CTA's share ----
-  int at = 0;
+  int at = begin;
   int stage = 0;
   float acc[kN][L::kTiles][4];  // dims by rows: thread's rows 2t, 2t + 1 of every tile of 8
   float m[kN][2], sum[kN][2];
-  while (at < count) {
-    const int seg_end = min(count, at + cur.strips - cur.strip);
-    const int n = seq[cur.b].y;
-    const int row0 = cur.tile * C::kRows;
-    const int wrow0 = row0 + sub * kN * 8;  // this warp's first row
-    float rs[kN][2];
+  while (at < end) {
+    int seg_end, n, wrow0, tok0;  // tok0: the token at strip `at`
+    {
+      const AttnPlace c = locate(at);
+      seg_end = min(end, at + c.strips - c.strip);
+      n = tokens[c.b];
+      wrow0 = c.tile * C::kRows + sub * kN * 8;  // this warp's first row
+      tok0 = (c.first + c.strip) << 4;
+    }
+    float rs[2];  // (queries in shared memory: so are the rows' factors)
     if constexpr (C::kQInRegs) {
       const float f = q_scale(qr);
-      rs[0][0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
-      rs[0][1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+      rs[0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
+      rs[1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
     } else {
       for (int tile8 = warp; tile8 < C::kQTiles; tile8 += C::kWarps) {
-        q_load(cur, tile8, qr);
+        q_load(locate(at), tile8, qr);
         const float f = q_scale(qr);
         if (t == 0) row_scale[tile8 * 8 + g] = f;
 #pragma unroll
@@ -545,10 +559,6 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
           sts128(q_base + ((tile8 * (L::kSteps / 2) + i) * 32 + lane) * 16, qr[i]);
       }
       __syncthreads();
-#pragma unroll
-      for (int nt = 0; nt < kN; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) rs[nt][h] = row_scale[(sub * kN + nt) * 8 + 2 * t + h];
     }
 #pragma unroll
     for (int nt = 0; nt < kN; ++nt)
@@ -562,14 +572,14 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
     const int tokens_all = n - p.q_len + 1;                          // every row sees those before this one
     const int tokens_low = p.window > 0 ? max(0, n - p.window) : 0;  // ... from this one on
 
-    // this team's strips of the segment: places team + k kTeams of the share
-    int i = at + ((team - at) % C::kTeams + C::kTeams) % C::kTeams;
+    // this team's strips of the segment: begin + team + k kTeams
+    int i = at + ((begin + team - at) % C::kTeams + C::kTeams) % C::kTeams;
     for (; i < seg_end; i += C::kTeams) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
       team_sync();  // the strip is there, and every lane is past the stage read last
       issue(stage == 0 ? C::kStages - 1 : stage - 1);
       const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + L::kStripBytes;
-      const int tok = (cur.first + cur.strip + (i - at)) << 4;
+      const int tok = tok0 + ((i - at) << 4);
       float sc[kN][4];  // tokens g (0, 1) and g + 8 (2, 3) by rows 2t and 2t + 1
 #pragma unroll
       for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
@@ -606,7 +616,11 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
       uint32_t pb[kN][2];
 #pragma unroll
       for (int nt = 0; nt < kN; ++nt) {
-        const float f0 = rs[nt][0] * ks, f1 = rs[nt][1] * ks;
+        if constexpr (!C::kQInRegs) {
+          const float2 f = *reinterpret_cast<const float2*>(row_scale + (sub * kN + nt) * 8 + 2 * t);
+          rs[0] = f.x, rs[1] = f.y;
+        }
+        const float f0 = rs[0] * ks, f1 = rs[1] * ks;
         const float b0 = lv - m[nt][0], b1 = lv - m[nt][1];
         float x[4] = {fmaf(sc[nt][0], f0, b0), fmaf(sc[nt][1], f1, b1), fmaf(sc[nt][2], f0, b0),
                       fmaf(sc[nt][3], f1, b1)};
@@ -680,11 +694,11 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
     }
 
     // ---- the segment's end: join the teams ----
+    if (C::kQInRegs && seg_end < end) q_load(locate(seg_end), sub, qr);  // (arrives during the joining)
+    const AttnPlace cur = locate(at);
+    const int row0 = cur.tile * C::kRows;
     const bool starts = cur.strip == 0, ends = cur.strip + (seg_end - at) == cur.strips;
     const bool whole = starts && ends;
-    AttnCursor next = cur;
-    if (seg_end < count) advance(next, cur.strips - cur.strip);
-    if (C::kQInRegs && seg_end < count) q_load(next, sub, qr);  // (arrives during the joining)
 #pragma unroll
     for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
@@ -696,7 +710,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
     const int used = min(C::kRows, rows - row0);
     // a team's stage that is neither being read nor being filled, the one before its next: 8 rows of dims, fp32
     auto slab_of = [&](int w) -> float* {
-      const int read = max(0, (seg_end - w + C::kTeams - 1) / C::kTeams);  // strips that the team has read so far
+      const int read = max(0, (seg_end - begin - w + C::kTeams - 1) / C::kTeams);  // strips that the team has read so far
       return reinterpret_cast<float*>(smem + (w * C::kStages + (read + C::kStages - 1) % C::kStages) * C::kStageBytes);
     };
     // 16-byte cell of word k, thread row g2 and query row r: places change by row, against bank conflicts
@@ -704,7 +718,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
     // with two warps in a team, both are past the stage before either writes
     constexpr int kRowFloats = kDim + 4;  // a partial row: the sums, m, the sum of weights
     auto part_of = [&](int cta, int slot) -> float* {
-      return p.partial + (static_cast<int64_t>(cta) * 4 + slot) * (kAttnMaxRows * kRowFloats);
+      return p.partial + (static_cast<int64_t>(cta) * 2 + slot) * (kAttnMaxRows * kRowFloats);
     };
     float* const part = part_of(blockIdx.x, starts ? 1 : 0);
     auto out_row = [&](int r, int64_t* tok_out, int* head_out) {
@@ -780,12 +794,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
     }
     if (!whole) {
       // the CTAs c0 .. c0 + n_parts - 1 share the item; a CTA's part is in its slot 1 if it starts the item, else 0
-      int c0 = first_cta, n_parts = parts;
-      if (!pieces) {
-        const int item0 = begin + at - cur.strip;  // the item's place on the line
-        c0 = item0 / per;
-        n_parts = (item0 + cur.strips - 1) / per - c0 + 1;
-      }
+      const int item0 = line_before[cur.b] + cur.item * line_of(cur.strips) + lead;  // the item's first strip on the line
+      const int c0 = item0 / per, n_parts = (item0 + cur.strips - 1) / per - c0 + 1;
       // true for the last of `of` CTAs to come here (all threads alike)
       auto last_of = [&](uint32_t* counter, int of) -> bool {
         __threadfence();
@@ -799,8 +809,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
         if (last) __threadfence();
         return last;
       };
-      // joins `cnt` partials, of every step-th CTA from `from` on, into the outputs or into `into`
-      auto join = [&](int from, int step, int cnt, int slot, float* into) {
+      // joins `cnt` partials, of every step-th CTA from `from` on, into the outputs or into the first of them
+      auto join = [&](int from, int step, int cnt, bool final) {
         constexpr int kBatch = 8;  // partials in flight per thread
         const int cells = used * (kDim / 4);
         int ways = 1;  // neighbouring lanes that share a cell's partials out
@@ -820,7 +830,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
               cm[j] = make_float2(kAttnFloor, 0.0f);
               a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
               if (kk < cnt) {
-                const float* o = part_of(c, slot + (c == c0 ? 1 : 0)) + r * kRowFloats;
+                const float* o = part_of(c, c == c0 ? 1 : 0) + r * kRowFloats;
                 cm[j] = __ldcg(reinterpret_cast<const float2*>(o + kDim));
                 a[j] = __ldcg(reinterpret_cast<const float4*>(o + d));
               }
@@ -851,10 +861,9 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
             top = mn;
           }
           if (live && way == 0) {
-            if (into) {
-              float* const o = into + r * kRowFloats;
-              __stcg(reinterpret_cast<float4*>(o + d), v);
-              if (d == 0) __stcg(reinterpret_cast<float2*>(o + kDim), make_float2(top, l));
+            if (!final) {  // (m and the sum of weights once all threads have read the old ones)
+              __stcg(reinterpret_cast<float4*>(part_of(from, from == c0 ? 1 : 0) + r * kRowFloats + d), v);
+              if (d == 0) ml[r] = make_float2(top, l);
             } else {
               const float inv = l != 0.0f ? 1.0f / l : 0.0f;
               store(r, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
@@ -862,23 +871,26 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
             }
           }
         }
+        if (!final) {
+          __syncthreads();
+          if (tid < used)
+            __stcg(reinterpret_cast<float2*>(part_of(from, from == c0 ? 1 : 0) + tid * kRowFloats + kDim), ml[tid]);
+        }
       };
       const int fan = n_parts <= kAttnFan ? n_parts : kAttnFan;
       const int mine = (static_cast<int>(blockIdx.x) - c0) / fan, from = c0 + mine * fan;
       const int members = min(fan, n_parts - mine * fan);
       if (last_of(p.arrived + from * 3 + (from == c0 ? 1 : 0), members)) {
         if (n_parts <= kAttnFan) {
-          join(c0, 1, n_parts, 0, nullptr);
+          join(c0, 1, n_parts, true);
         } else {
-          const int groups = (n_parts + fan - 1) / fan;
-          join(from, 1, members, 0, part_of(from, 2 + (from == c0 ? 1 : 0)));
-          if (last_of(p.arrived + c0 * 3 + 2, groups)) join(c0, fan, groups, 2, nullptr);
+          join(from, 1, members, false);
+          if (last_of(p.arrived + c0 * 3 + 2, (n_parts + fan - 1) / fan)) join(c0, fan, (n_parts + fan - 1) / fan, true);
         }
       }
     }
     // on to the next item
     at = seg_end;
-    cur = next;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
