@@ -112,9 +112,10 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   const int row_units = rows <= 8 ? 1 : rows <= 16 || cache->head_dim > 128 ? 2 : 4;
   const int row_tiles = (rows + 8 * row_units - 1) / (8 * row_units);
   const int64_t tokens = static_cast<int64_t>(max_blocks) * cache->block_size;
-  // (places on the line of strips, a quarter more with padding, are 32-bit)
+  // (32-bit: places on the line of strips, a quarter more with padding, and strips of the cache)
   if (tokens > (1ll << 30) ||
-      (static_cast<double>(tokens) / 16 + fp4::kAttnItemCost) * B * cache->kv_heads * row_tiles >= 1.2e9)
+      (static_cast<double>(tokens) / 16 + fp4::kAttnItemCost) * B * cache->kv_heads * row_tiles >= 1.2e9 ||
+      static_cast<double>(cache->num_blocks) * cache->kv_heads * (cache->block_size / 16) >= 2147483647.0)
     return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
   if (crooked || !aligned(q, 16) || !aligned(out, 16) || ldq % 8 != 0 || ldo % 8 != 0 || !aligned(lse, 4) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 16))

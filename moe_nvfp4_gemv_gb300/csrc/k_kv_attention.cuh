@@ -27,25 +27,20 @@
 // no shuffles; a strip that would exceed it reduces its maxima over the warp
 // and rescales.
 //
-// Teams.  A team of one or two warps streams strips through its own ring of
-// cp.async stages; the warps of a team serve different query rows of the same
-// codes.  Every warp keeps its own m, sums and accumulators; nothing in the
-// loop is wider than a team.
+// Every warp streams its own strips through its own ring of cp.async stages
+// and keeps its own m, sums and accumulators: no barrier in the loop.
 //
 // The line.  The items (sequence, KV head, row tile) stand on one line, each
 // as long as its strips and kAttnItemCost more, for what an item's end costs.
-// The line is cut into equal shares wherever the cuts fall; or, where each
-// item can be cut into near equal pieces by itself with no more shares, at the
-// items' ends too, so that no share holds two items.  One CTA serves one
-// share; there are several times more shares than resident CTAs, because SMs
-// do not get equal parts of the memory's bandwidth: those that get more take
-// more shares.  At a segment's end (a share's part of one item) the teams'
-// results are joined through the ring stage that happens to be free, while
-// the other stages already fill for the next item.  An item that several
-// shares cut is joined from fp32 partials in the workspace: the last of up to
-// kAttnFan CTAs to arrive joins theirs, and with more the last of those joins
-// the joined ones (counters that are left at zero).  Nothing waits on another
-// CTA.
+// The line is cut into equal shares, one per CTA, wherever the cuts fall; or,
+// where each item can be cut into near equal pieces by itself with no more
+// shares, at the items' ends too, so that no share holds two items.  At a
+// segment's end (a share's part of one item) the warps' results are joined
+// through the ring stage that happens to be free, while the other stages
+// already fill for the next item.  An item that several shares cut is joined
+// from fp32 partials in the workspace: the last of up to kAttnFan CTAs to
+// arrive joins theirs, and with more the last of those joins the joined ones
+// (counters that are left at zero).  Nothing waits on another CTA.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -71,7 +66,7 @@ struct KvAttnParams {
   float* partial;      // [CTAs][2][kAttnMaxRows][dim + 4]
   uint32_t* arrived;   // [CTAs][3], zero between calls
   int B, max_blocks, num_blocks, block_log2;
-  int kv_heads, group, q_len, row_tiles;  // row tiles of 8 kN kTeam rows
+  int kv_heads, group, q_len, row_tiles;  // row tiles of 8 kN rows
   int window;
   int f16;             // element type of q and out
   float sm_scale;
@@ -162,27 +157,38 @@ struct AttnLayout {
     if (kBlk == 64) return r * kDim + ((c ^ (r & 2)) << 4);
     return r * kDim + (c << 4);
   }
+  // Where the lane's i-th chunk of a strip goes, given that of its first: i 32
+  // chunks further, 512 / kDim rows.
+  static __device__ __forceinline__ int copy_to(int first, int i) {
+    if (kDim == 128) return (first ^ ((i & 1) << 6)) + i * 512;
+    if (kDim == 256) return (first ^ ((i & 3) << 5)) + i * 512;
+    return first + i * 512;  // (64: eight rows further; 96: chunks in order)
+  }
   // head_dim index of the first of the four values of K word i (block blk)
   static __device__ __forceinline__ int k_dim(int blk, int i, int t) {
     if (kBlk == 96) return 32 * (i >> 1) + 8 * t + 4 * (i & 1);
     return blk * kBlk + t * (kBlk / 4) + 4 * i;
   }
-  static __device__ __forceinline__ void k_words(uint32_t base, int r, int blk, int t, uint32_t (&w)[kWords]) {
+  // K words of token row g + 8 half, given the lane's place in row g
+  static __device__ __forceinline__ int k_place(int g, int t) {
+    return kBlk == 128 ? chunk(g, 2 * t) : kBlk == 64 ? chunk(g, t) : g * kDim + 8 * t;
+  }
+  static __device__ __forceinline__ void k_words(uint32_t strip, int place, int half, int blk, uint32_t (&w)[kWords]) {
     if constexpr (kBlk == 128) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint4 v = lds128(base + chunk(r, blk * 8 + 2 * t + i));
+        const uint4 v = lds128(strip + (place ^ (16 * i)) + half * 8 * kDim + blk * 128);
         w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
     } else if constexpr (kBlk == 64) {
-      const uint4 v = lds128(base + chunk(r, t));
+      const uint4 v = lds128(strip + place + half * 8 * kDim);
       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else {
 #pragma unroll
       for (int i = 0; i < 3; ++i)
         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
                      : "=r"(w[2 * i]), "=r"(w[2 * i + 1])
-                     : "r"(base + r * kDim + 32 * i + 8 * t));
+                     : "r"(strip + place + half * 8 * kDim + 32 * i));
     }
   }
   // head_dim index of the first byte of thread row g's V word i (block blk)
@@ -196,38 +202,39 @@ struct AttnLayout {
     const int o = d % kBlk;
     return make_int2((d / kBlk) * kVWords + (o % (kBlk / 8)) / 4, o / (kBlk / 8));
   }
-  static __device__ __forceinline__ void v_words(uint32_t base, int r, int blk, int g, uint32_t (&w)[kVWords]) {
+  // V words of token row 2 t + (c & 1) + 8 (c >> 1), given the lane's place in row 2 t
+  static __device__ __forceinline__ int v_row_place(int g, int t) {
+    return kBlk == 128 ? chunk(2 * t, g) : kBlk == 64 ? chunk(2 * t, g >> 1) + 8 * (g & 1) : 2 * t * kDim + 4 * g;
+  }
+  static __device__ __forceinline__ void v_words(uint32_t strip, int place, int c, int blk, uint32_t (&w)[kVWords]) {
+    const int row = (c & 1) * kDim + (c >> 1) * 8 * kDim;
     if constexpr (kBlk == 128) {
-      const uint4 v = lds128(base + chunk(r, blk * 8 + g));
+      const uint4 v = lds128(strip + (place ^ (16 * (c & 1))) + row + blk * 128);
       w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (kBlk == 64) {
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                   : "=r"(w[0]), "=r"(w[1])
-                   : "r"(base + chunk(r, g >> 1) + 8 * (g & 1)));
+    } else if constexpr (kBlk == 64) {  // (rows 2 t and 2 t + 1 change places alike)
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(strip + place + row));
     } else {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) w[i] = lds32(base + r * kDim + 32 * i + 4 * g);
+      for (int i = 0; i < 3; ++i) w[i] = lds32(strip + place + row + 32 * i);
     }
   }
 };
 
-// kN: tiles of 8 query rows per warp; kTeam: warps that share a ring.
-template <int kDim, int kN, int kTeam>
+// kN: tiles of 8 query rows that a warp serves.
+template <int kDim, int kN>
 struct AttnCfg {
   using L = AttnLayout<kDim>;
   static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kTeams = kWarps / kTeam;
-  static constexpr int kQTiles = kN * kTeam;
-  static constexpr int kRows = 8 * kQTiles;
-  static constexpr int kResident = kDim <= 128 ? 2 : 1;        // CTAs per SM (registers, shared memory)
-  static constexpr bool kQInRegs = kN == 1;                    // a warp keeps its queries in registers
-  static constexpr int kStageBytes = 2 * L::kStripBytes + 16;  // K, V, the two scales
-  static constexpr int kStages0 = (kResident == 2 ? 102400 : 204800) / (kTeams * kStageBytes);
+  static constexpr int kRows = 8 * kN;
+  static constexpr int kResident = kDim <= 128 && kN <= 2 ? 2 : 1;  // CTAs per SM (registers, shared memory)
+  static constexpr bool kQInRegs = kN == 1;                         // a warp keeps its queries in registers
+  static constexpr int kStageBytes = 2 * L::kStripBytes + 16;       // K, V, the two scales
+  static constexpr int kStages0 = (kResident == 2 ? 102400 : 204800) / (kWarps * kStageBytes);
   static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
-  static constexpr int kRingBytes = kTeams * kStages * kStageBytes;
-  static constexpr int kQBytes = kQInRegs ? 0 : kQTiles * L::kSteps * 32 * 8;
-  static constexpr int kSmem = kRingBytes + kQBytes + kTeams * kRows * 8 + kRows * 4;  // + the sequences
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr int kQBytes = kQInRegs ? 0 : kN * L::kSteps * 32 * 8;
+  static constexpr int kSmem = kRingBytes + kQBytes + kWarps * kRows * 8 + kRows * 4;  // + the sequences
   // dynamic shared memory for B sequences
   static constexpr int smem(int B) { return kSmem + (B + 1) * 12; }
 };
@@ -240,22 +247,22 @@ struct AttnPlace {
   int item;           // number of the item within the sequence
 };
 
-template <int kDim, bool kInt8, int kN, int kTeam>
-__global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kDim, kN, kTeam>::kResident)
+template <int kDim, bool kInt8, int kN>
+__global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>::kResident)
     kv_attention_kernel(const KvAttnParams p) {
-  using C = AttnCfg<kDim, kN, kTeam>;
+  using C = AttnCfg<kDim, kN>;
   using L = AttnLayout<kDim>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int4 warp_sum[C::kWarps];
+  __shared__ AttnPlace places[3];  // the item being read and the next one by turns; the share's begin
+  __shared__ int plan_words[6];
   __shared__ int last_flag;
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (uniform, and known to be)
-  const int team = warp / kTeam, sub = warp % kTeam;
-  // ring | queries (where not in registers) | (m, sum) [team][row] | row scales | sequences
+  // ring | queries (where not in registers) | (m, sum) [warp][row] | row scales | sequences
   const uint32_t sm = smem_u32(smem);
   const uint32_t q_base = sm + C::kRingBytes;
   float2* const ml = reinterpret_cast<float2*>(smem + C::kRingBytes + C::kQBytes);
-  float* const row_scale = reinterpret_cast<float*>(ml + C::kTeams * C::kRows);
+  float* const row_scale = reinterpret_cast<float*>(ml + C::kWarps * C::kRows);
   // of the sequences before: strips, length on the line; then each one's tokens
   int* const strips_before = reinterpret_cast<int*>(row_scale + C::kRows);
   int* const line_before = strips_before + p.B + 1;
@@ -265,118 +272,130 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
 
   const int rows = p.q_len * p.group;  // query rows of a KV head
   const int items = p.kv_heads * p.row_tiles;
-  const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.block_log2;
   auto first_strip = [&](int n) -> int {
     const int at = n - p.q_len;  // the first query's position
     return p.window > 0 && at >= p.window ? (at - p.window + 1) >> 4 : 0;
   };
   auto strips_of = [&](int n) -> int { return ((n + 15) >> 4) - first_strip(n); };
-  auto ceil_div = [](int x, int y) -> int {  // a division of floats, and its rounding set right
-    int q = static_cast<int>(__fdividef(static_cast<float>(x), static_cast<float>(y)));
-    while (q * y < x) ++q;
-    while ((q - 1) * y >= x) --q;
-    return q;
+  auto div_up = [](int x, int y, float inv_y) -> int {  // ceil(x / y): a product of floats, set right
+    int q = static_cast<int>(static_cast<float>(x) * inv_y);
+    q -= static_cast<int64_t>(q) * y > x;
+    q += static_cast<int64_t>(q + 1) * y <= x;
+    return q + (q * y < x);
   };
+  auto rounds = [](int x) { return (x + C::kWarps - 1) / C::kWarps * C::kWarps; };  // whole rounds of the warps
 
-  // ---- the line ----
-  // Every warp goes over the first 32 sequences by itself, the warps share out more of them.
-  const int first_b = p.B <= 32 ? lane : tid, step_b = p.B <= 32 ? 32 : C::kThreads;
-  auto block_sum = [&](int4 v) -> int4 {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
-      v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
-      v.z += __shfl_xor_sync(0xFFFFFFFFu, v.z, o);
-      v.w += __shfl_xor_sync(0xFFFFFFFFu, v.w, o);
-    }
-    if (p.B > 32) {
-      if (lane == 0) warp_sum[warp] = v;
-      __syncthreads();
-      v = make_int4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < C::kWarps; ++i) {
-        const int4 o = warp_sum[i];
-        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-      }
-      __syncthreads();
-    }
-    return v;
-  };
-  int4 v4 = make_int4(0, 0, 0, 0);
-  for (int b = first_b; b < p.B; b += step_b) {
-    const int raw = __ldg(p.lens + b);
-    const int n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
-    if (n != raw && blockIdx.x == 0) raise_error(p.err, FP4_ERR_BADIDX);
-    tokens[b] = n;  // (with few sequences several warps write the same)
-    v4.x += strips_of(n) * items;
-    v4.y += n > 0 ? items : 0;
-  }
-  v4 = block_sum(v4);
-  const int total = v4.x, all_items = v4.y, ctas = static_cast<int>(gridDim.x);
-  auto rounds = [](int x) { return (x + C::kTeams - 1) / C::kTeams * C::kTeams; };  // whole rounds of the teams
-  // pieces per item, if those of the shortest of three lengths are no more than the CTAs
-  int per = 0;
-  if (all_items <= ctas) {
-    const int even = (total + ctas - 1) / ctas;
-    const int len[3] = {max(C::kTeams, rounds(even)), max(C::kTeams, rounds(even + even / 8)),
-                        max(C::kTeams, rounds(even + even / 4))};
-    v4 = make_int4(0, 0, 0, 0);
-    for (int b = first_b; b < p.B; b += step_b) {
-      const int s = strips_of(tokens[b]);
-      v4.x += ceil_div(s, len[0]) * items;
-      v4.y += ceil_div(s, len[1]) * items;
-      v4.z += ceil_div(s, len[2]) * items;
-    }
-    v4 = block_sum(v4);
-    per = v4.x <= ctas ? len[0] : v4.y <= ctas ? len[1] : v4.z <= ctas ? len[2] : 0;
-  }
-  const bool pieces = per > 0;
-  if (!pieces) per = max(rounds((total + all_items * kAttnItemCost + ctas - 1) / ctas), C::kTeams);
-  // an item's length on the line, of which the first `lead` is its cost
-  const int lead = pieces ? 0 : kAttnItemCost;
-  auto line_of = [&](int strips) -> int { return pieces ? ceil_div(strips, per) * per : strips + (strips ? lead : 0); };
-  int line_end = 0;
+  // ---- the plan, by the first warp; lens by all threads where there are many ----
   {
-    int strips_end = 0;
-    for (int b0 = 0; b0 < p.B; b0 += step_b) {
-      const int b = b0 + first_b;
-      const int s = b < p.B ? strips_of(tokens[b]) : 0, on_line = b < p.B ? line_of(s) : 0;
-      int2 sum = make_int2(s * items, on_line * items);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xFFFFFFFFu, sum.x, o), v = __shfl_up_sync(0xFFFFFFFFu, sum.y, o);
-        if (lane >= o) sum.x += u, sum.y += v;
+    const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.block_log2;
+    const int step = p.B <= 32 ? 32 : C::kThreads;
+    if (warp == 0 || p.B > 32)
+      for (int b = tid; b < p.B; b += step) {
+        const int raw = __ldg(p.lens + b);
+        const int n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
+        if (n != raw && blockIdx.x == 0) raise_error(p.err, FP4_ERR_BADIDX);
+        tokens[b] = n;
       }
-      int2 before = make_int2(strips_end, line_end), whole = before;
-      if (p.B > 32) {
-        if (lane == 31) warp_sum[warp] = make_int4(sum.x, sum.y, 0, 0);
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < C::kWarps; ++i) {
-          const int4 o = warp_sum[i];
-          if (i < warp) before.x += o.x, before.y += o.y;
-          whole.x += o.x, whole.y += o.y;
+    if (p.B > 32) __syncthreads();
+    if (warp == 0) {
+      const int ctas = static_cast<int>(gridDim.x);
+      int total = 0, alive = 0;
+      __syncwarp();
+      for (int b = lane; b < p.B + lane; b += 32) {  // (all lanes alike: rounds of 32 sequences)
+        const int n = b < p.B ? tokens[b] : 0;
+        total += __reduce_add_sync(0xFFFFFFFFu, n > 0 ? strips_of(n) : 0);
+        alive += __popc(__ballot_sync(0xFFFFFFFFu, n > 0));
+      }
+      total *= items;
+      alive *= items;
+      // pieces per item, if those of the shortest of three lengths are no more than the CTAs
+      int per = 0;
+      float inv_per = 0.0f;
+      if (alive <= ctas) {
+        const int even = (total + ctas - 1) / ctas;
+        for (int k = 0; k < 3 && per == 0; ++k) {
+          const int len = max(C::kWarps, rounds(even + (even * k >> 3)));
+          const float inv = 1.0f / static_cast<float>(len);
+          int sum = 0;
+          for (int b = lane; b < p.B + lane; b += 32) {
+            const int n = b < p.B ? tokens[b] : 0;
+            sum += __reduce_add_sync(0xFFFFFFFFu, n > 0 ? div_up(strips_of(n), len, inv) : 0);
+          }
+          if (sum * items <= ctas) {
+            per = len;
+            inv_per = inv;
+          }
         }
-        __syncthreads();
-      } else {
-        whole.x += __shfl_sync(0xFFFFFFFFu, sum.x, 31), whole.y += __shfl_sync(0xFFFFFFFFu, sum.y, 31);
       }
-      if (b < p.B) {
-        strips_before[b] = before.x + sum.x - s * items;
-        line_before[b] = before.y + sum.y - on_line * items;
+      const bool pieces = per > 0;
+      const int lead = pieces ? 0 : kAttnItemCost;
+      if (!pieces) per = max(rounds((total + alive * kAttnItemCost + ctas - 1) / ctas), C::kWarps);
+      // the sequences' places on both lines
+      int strips_end = 0, line_end = 0;
+      for (int b = lane; b < p.B + lane; b += 32) {
+        const int n = b < p.B ? tokens[b] : 0;
+        const int s = n > 0 ? strips_of(n) : 0;
+        int len = pieces ? div_up(s, per, inv_per) * per : s + (n > 0 ? lead : 0);
+        int sum = s, line = len;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o), v = __shfl_up_sync(0xFFFFFFFFu, line, o);
+          if (lane >= o) sum += u, line += v;
+        }
+        if (b < p.B) {
+          strips_before[b] = strips_end + (sum - s) * items;
+          line_before[b] = line_end + (line - len) * items;
+        }
+        strips_end += __shfl_sync(0xFFFFFFFFu, sum, 31) * items;
+        line_end += __shfl_sync(0xFFFFFFFFu, line, 31) * items;
       }
-      strips_end = whole.x, line_end = whole.y;
+      if (lane == 0) {
+        strips_before[p.B] = strips_end;
+        line_before[p.B] = line_end;
+      }
+      __syncwarp();
+      // lane 0: the share's begin, lane 1: its end (both in strips), from the cuts of the line
+      if (lane < 2) {
+        const int64_t at64 = static_cast<int64_t>(per) * (blockIdx.x + lane);
+        int where = strips_end;
+        if (at64 < line_end) {
+          const int at = static_cast<int>(at64);
+          int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before: never an empty one
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (line_before[mid] <= at) lo = mid;
+            else hi = mid - 1;
+          }
+          AttnPlace c;
+          const int n = tokens[lo];
+          c.b = lo;
+          c.first = first_strip(n);
+          c.strips = strips_of(n);
+          const int len = pieces ? div_up(c.strips, per, inv_per) * per : c.strips + lead, off = at - line_before[lo];
+          c.item = off / len;
+          // (a cut behind an item's last strip or in its cost: the strip that follows)
+          int strip = max(off - c.item * len - lead, 0);
+          where = strips_before[lo] + c.item * c.strips + min(strip, c.strips);
+          if (lane == 0) {
+            c.strip = strip;  // (below c.strips wherever the share is not empty, or pieces end)
+            c.head = c.item / p.row_tiles;
+            c.tile = c.item - c.head * p.row_tiles;
+            places[0] = places[2] = c;
+          }
+        }
+        plan_words[lane] = where;
+      } else if (lane == 2) {
+        plan_words[2] = per;
+        plan_words[3] = lead;
+        plan_words[4] = pieces;
+      }
     }
-    if (lane == 0) {  // (every warp the same values)
-      strips_before[p.B] = strips_end;
-      line_before[p.B] = line_end;
-    }
+    __syncthreads();
   }
-  if (p.B > 32) __syncthreads();
-  else __syncwarp();
+  const int begin = plan_words[0], end = plan_words[1], per = plan_words[2], lead = plan_words[3];
 
   // sequences nobody visits: zeros, lse -inf
-  for (int b = blockIdx.x; b < p.B; b += ctas) {
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (tokens[b] > 0) continue;
     const int heads = p.kv_heads * p.group;
     for (int i = tid; i < p.q_len * heads * (kDim / 8); i += C::kThreads) {
@@ -386,163 +405,149 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
       if (p.lse && i % (kDim / 8) == 0) p.lse[tok * heads + row % heads] = -__builtin_huge_valf();
     }
   }
-  // ---- this CTA's share, in strips from the line's begin ----
-  if (static_cast<int64_t>(per) * blockIdx.x >= line_end) return;
-  // the last sequence whose entry is at most `at`: never an empty one
-  auto find = [&](const int* before, int at) -> int {
-    int lo = 0, hi = p.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (before[mid] <= at) lo = mid;
-      else hi = mid - 1;
-    }
-    return lo;
-  };
-  auto cut = [&](int at) -> int {  // strips before place `at` of the line
-    if (at >= line_end) return strips_before[p.B];
-    const int b = find(line_before, at), s = strips_of(tokens[b]), len = line_of(s);
-    const int off = at - line_before[b], item = off / len;
-    return strips_before[b] + item * s + min(max(off - item * len - lead, 0), s);
-  };
-  const int begin = cut(per * static_cast<int>(blockIdx.x));
-  const int end = cut(static_cast<int>(min(static_cast<int64_t>(per) * (blockIdx.x + 1), static_cast<int64_t>(line_end))));
   if (begin >= end) return;
-  auto locate = [&](int at) -> AttnPlace {  // strip `at`
-    AttnPlace c;
-    c.b = find(strips_before, at);
-    const int n = tokens[c.b], off = at - strips_before[c.b];
-    c.first = first_strip(n);
-    c.strips = strips_of(n);
-    c.item = off / c.strips;
-    c.strip = off - c.item * c.strips;
-    c.head = c.item / p.row_tiles;
-    c.tile = c.item - c.head * p.row_tiles;
-    return c;
-  };
 
-  // ---- the team's ring: strips team, team + kTeams, ... of the share ----
-  const uint32_t ring = sm + team * C::kStages * C::kStageBytes;
-  const int block_mask = (1 << p.block_log2) - 1;
-  // Lane l looks up the page of every 32nd strip of the team, from its l-th on: one batch to copy from, one ahead.
-  int looked = begin + team + lane * C::kTeams;  // the strip that the lane looks up next
-  auto look_up = [&](int* page, int* where) {    // page id; KV head and place on the page, -1 past the share
-    *page = 0;
-    *where = -1;
-    if (looked < end) {
-      const AttnPlace c = locate(looked);
-      const int tok = (c.first + c.strip) << 4;
-      *page = __ldg(p.table + static_cast<int64_t>(c.b) * p.max_blocks + (tok >> p.block_log2));
-      *where = (c.head << 8) | (tok & block_mask);
+  // ---- queries: f16 operands; bf16 ones scaled by a power of two for each row ----
+  auto q_load = [&](const AttnPlace& c, int tile8, uint4 (&raw)[L::kSteps / 2]) {  // row g of the item's tile of 8
+    const int row = c.tile * C::kRows + tile8 * 8 + g;
+    const bool live = row < rows;
+    const int i = live ? row / p.group : 0;
+    const uint16_t* src = p.q + (static_cast<int64_t>(c.b) * p.q_len + i) * p.ldq +
+                          (c.head * p.group + (live ? row - i * p.group : 0)) * kDim;
+#pragma unroll
+    for (int k = 0; k < L::kSteps / 2; ++k) {  // words 2 k and 2 k + 1: eight dims in a row
+      const int d = L::k_dim(2 * k / L::kWords, 2 * k % L::kWords, t);
+      raw[k] = live ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0, 0, 0, 0);
     }
-    looked += 32 * C::kTeams;
   };
-  int page, where, page_next = 0, where_next = -1, copied = 0;
-  look_up(&page, &where);
+  auto q_scale = [&](uint4 (&raw)[L::kSteps / 2]) -> float {  // operands in place; row g's factor of the scores
+    const float factor = p.sm_scale * 1.4426950408889634f;
+    if (p.f16) return factor;
+    uint32_t top = 0;  // two magnitudes of bf16: ordered like their bits
+#pragma unroll
+    for (int k = 0; k < L::kSteps / 2; ++k) {
+      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
+    }
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    // 2^-e brings the largest to [2^14, 2^15)
+    const int field = static_cast<int>(top >> 7);
+    const int e = field == 0 ? 0 : min(max(field - 127 - 14, -126), 126);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+    for (int k = 0; k < L::kSteps / 2; ++k) {
+      uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = pack_f16(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
+      raw[k] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return factor * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  };
+  uint4 qr[L::kSteps / 2];
+  if (C::kQInRegs) q_load(places[0], 0, qr);
+
+  // ---- the warp's ring: strips warp, warp + kWarps, ... of the share ----
+  const uint32_t ring = sm + warp * C::kStages * C::kStageBytes;
+  // Lane l looks up every 32nd strip of the warp, from its l-th on: one batch to copy from, one ahead.  What it
+  // keeps is the strip's number in the cache, -1 past the share, -2 for a bad page.
+  int looked = begin + warp + lane * C::kWarps;  // the strip that the lane looks up next
+  auto look_up = [&]() -> int {
+    int found = -1;
+    if (looked < end) {
+      int b = places[2].b, head = places[2].head, strip = places[2].strip + (looked - begin);
+      if (strip >= places[2].strips) {  // (not the share's first item)
+        int lo = b, hi = p.B - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (strips_before[mid] <= looked) lo = mid;
+          else hi = mid - 1;
+        }
+        b = lo;
+        const int s = strips_of(tokens[b]), off = looked - strips_before[b], item = off / s;
+        strip = off - item * s;
+        head = item / p.row_tiles;
+      }
+      strip += first_strip(tokens[b]);
+      const int per_page = p.block_log2 - 4;
+      const int id = __ldg(p.table + static_cast<int64_t>(b) * p.max_blocks + (strip >> per_page));
+      found = id >= 0 && id < p.num_blocks
+                  ? ((id * p.kv_heads + head) << per_page) + (strip & ((1 << per_page) - 1))
+                  : -2;
+    }
+    looked += 32 * C::kWarps;
+    return found;
+  };
+  int batch = look_up(), batch_next = -1, copied = 0;
+  const int copy_first = L::chunk(lane / (kDim / 16), lane % (kDim / 16));
   auto issue = [&](int stage) {
     const int source = copied & 31;
-    if (source == 0 && copied > 0) {
-      page = page_next;
-      where = where_next;
-    }
-    if (source == 16) look_up(&page_next, &where_next);  // (halfway: there in time for the next batch)
+    if (source == 0 && copied > 0) batch = batch_next;
+    if (source == 16) batch_next = look_up();  // (halfway: there in time for the next batch)
     ++copied;
-    const int spot = __shfl_sync(0xFFFFFFFFu, where, source);
-    if (spot >= 0) {
+    int strip = __shfl_sync(0xFFFFFFFFu, batch, source);
+    if (strip != -1) {
       const uint32_t dst = ring + stage * C::kStageBytes;
-      int id = __shfl_sync(0xFFFFFFFFu, page, source);
-      const bool good = id >= 0 && id < p.num_blocks;
-      if (!good) {
+      const uint32_t bytes = strip >= 0 ? 16u : 0u;
+      if (strip < 0) {
         if (lane == 0) raise_error(p.err, FP4_ERR_BADIDX);
-        id = 0;
+        strip = 0;
       }
-      const uint32_t bytes = good ? 16u : 0u;
-      const int64_t tile = static_cast<int64_t>(id) * p.kv_heads + (spot >> 8);
-      const int64_t at = ((tile << p.block_log2) + (spot & 255)) * kDim;
+      const int64_t at = static_cast<int64_t>(strip) * L::kStripBytes + lane * 16;
+      const uint8_t* ksrc = p.k_codes + at;
+      const uint8_t* vsrc = p.v_codes + at;
 #pragma unroll
       for (int i = 0; i < kDim / 32; ++i) {
-        const int c = i * 32 + lane;  // 16-byte chunk of the strip
-        const int r = c / (kDim / 16), o = L::chunk(r, c - r * (kDim / 16));
-        if (kTeam == 1 || sub == 0) cp_async16(dst + o, p.k_codes + at + c * 16, bytes);
-        if (kTeam == 1 || sub == 1) cp_async16(dst + L::kStripBytes + o, p.v_codes + at + c * 16, bytes);
+        cp_async16(dst + L::copy_to(copy_first, i), ksrc + i * 512, bytes);
+        cp_async16(dst + L::kStripBytes + L::copy_to(copy_first, i), vsrc + i * 512, bytes);
       }
-      if (lane < 2 && sub == 0) {
-        const float* s = (lane ? p.v_scale : p.k_scale) + tile;
+      if (lane < 2) {
+        const float* s = (lane ? p.v_scale : p.k_scale) + (strip >> (p.block_log2 - 4));
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 2 * L::kStripBytes + 4 * lane), "l"(s),
-                     "r"(good ? 4u : 0u)
+                     "r"(bytes >> 2)
                      : "memory");
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto team_sync = [&]() {
-    if constexpr (kTeam == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(kTeam * 32) : "memory");
-  };
 #pragma unroll
   for (int s = 0; s < C::kStages - 1; ++s) issue(s);
-
-  // ---- queries: f16 operands, scaled by a power of two for each row ----
-  auto q_load = [&](const AttnPlace& c, int tile8, uint4 (&raw)[L::kSteps / 2]) {  // row g of the item's tile of 8
-    const int row = c.tile * C::kRows + tile8 * 8 + g;
-    const bool live = row < rows;
-    const int64_t tok = static_cast<int64_t>(c.b) * p.q_len + (live ? row / p.group : 0);
-    const uint16_t* src =
-        p.q + tok * p.ldq + (static_cast<int64_t>(c.head) * p.group + (live ? row % p.group : 0)) * kDim;
-#pragma unroll
-    for (int i = 0; i < L::kSteps / 2; ++i) {  // words 2 i and 2 i + 1: eight dims in a row
-      const int d = L::k_dim(2 * i / L::kWords, 2 * i % L::kWords, t);
-      raw[i] = live ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0, 0, 0, 0);
-    }
-  };
-  auto two = [&](uint32_t v) -> float2 {
-    return p.f16 ? __half22float2(*reinterpret_cast<const __half2*>(&v))
-                 : make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-  };
-  auto q_scale = [&](uint4 (&raw)[L::kSteps / 2]) -> float {  // operands in place; row g's factor of the scores
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < L::kSteps / 2; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = two(w[j]);
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-      }
-    }
-    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-    // 2^-e brings amax to [2^14, 2^15)
-    const int field = static_cast<int>(__float_as_uint(amax) >> 23);
-    const int e = field == 0 ? 0 : min(max(field - 127 - 14, -126), 126);
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-    for (int i = 0; i < L::kSteps / 2; ++i) {
-      uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = two(w[j]);
-        w[j] = pack_f16(f.x * down, f.y * down);
-      }
-      raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    return p.sm_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-  };
-  uint4 qr[L::kSteps / 2];
-  if (C::kQInRegs) q_load(locate(begin), sub, qr);
+  const int k_place = L::k_place(g, t), v_place = L::v_row_place(g, t);
 
   // ---- segments: the parts of items in this CTA's share ----
   int at = begin;
   int stage = 0;
+  int which = 0;                // of places
   float acc[kN][L::kTiles][4];  // dims by rows: thread's rows 2t, 2t + 1 of every tile of 8
   float m[kN][2], sum[kN][2];
   while (at < end) {
-    int seg_end, n, wrow0, tok0;  // tok0: the token at strip `at`
+    int seg_end, n, row0, tok0;  // tok0: the token at strip `at`
     {
-      const AttnPlace c = locate(at);
+      const AttnPlace c = places[which];
       seg_end = min(end, at + c.strips - c.strip);
       n = tokens[c.b];
-      wrow0 = c.tile * C::kRows + sub * kN * 8;  // this warp's first row
+      row0 = c.tile * C::kRows;
       tok0 = (c.first + c.strip) << 4;
+      if (tid == 0 && seg_end < end) {  // the next item (read behind the barriers of the joining)
+        AttnPlace x = c;
+        x.strip = 0;
+        ++x.item;
+        if (++x.tile == p.row_tiles) {
+          x.tile = 0;
+          if (++x.head == p.kv_heads) {
+            x.head = x.item = 0;
+            do ++x.b;
+            while (strips_before[x.b + 1] == strips_before[x.b]);
+            const int len = tokens[x.b];
+            x.first = first_strip(len);
+            x.strips = strips_of(len);
+          }
+        }
+        places[which ^ 1] = x;
+      }
     }
     float rs[2];  // (queries in shared memory: so are the rows' factors)
     if constexpr (C::kQInRegs) {
@@ -550,13 +555,13 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
       rs[0] = __shfl_sync(0xFFFFFFFFu, f, 8 * t);
       rs[1] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
     } else {
-      for (int tile8 = warp; tile8 < C::kQTiles; tile8 += C::kWarps) {
-        q_load(locate(at), tile8, qr);
+      if (warp < kN) {
+        q_load(places[which], warp, qr);
         const float f = q_scale(qr);
-        if (t == 0) row_scale[tile8 * 8 + g] = f;
+        if (t == 0) row_scale[warp * 8 + g] = f;
 #pragma unroll
         for (int i = 0; i < L::kSteps / 2; ++i)
-          sts128(q_base + ((tile8 * (L::kSteps / 2) + i) * 32 + lane) * 16, qr[i]);
+          sts128(q_base + ((warp * (L::kSteps / 2) + i) * 32 + lane) * 16, qr[i]);
       }
       __syncthreads();
     }
@@ -572,22 +577,22 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
     const int tokens_all = n - p.q_len + 1;                          // every row sees those before this one
     const int tokens_low = p.window > 0 ? max(0, n - p.window) : 0;  // ... from this one on
 
-    // this team's strips of the segment: begin + team + k kTeams
-    int i = at + ((begin + team - at) % C::kTeams + C::kTeams) % C::kTeams;
-    for (; i < seg_end; i += C::kTeams) {
+    // this warp's strips of the segment: begin + warp + k kWarps
+    int tok = tok0 + (((begin + warp - at) & (C::kWarps - 1)) << 4);
+    const int tok_end = tok0 + ((seg_end - at) << 4);
+    for (; tok < tok_end; tok += C::kWarps * 16) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-      team_sync();  // the strip is there, and every lane is past the stage read last
+      __syncwarp();  // the strip is there, and every lane is past the stage read last
       issue(stage == 0 ? C::kStages - 1 : stage - 1);
       const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + L::kStripBytes;
-      const int tok = tok0 + ((i - at) << 4);
       float sc[kN][4];  // tokens g (0, 1) and g + 8 (2, 3) by rows 2t and 2t + 1
 #pragma unroll
       for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
 #pragma unroll
       for (int blk = 0; blk < L::kBlocks; ++blk) {
         uint32_t w[2][L::kWords];
-        L::k_words(kb, g, blk, t, w[0]);
-        L::k_words(kb, g + 8, blk, t, w[1]);
+        L::k_words(kb, k_place, 0, blk, w[0]);
+        L::k_words(kb, k_place, 1, blk, w[1]);
 #pragma unroll
         for (int s = 0; s < L::kWords; s += 2) {
           uint32_t a[2][4];
@@ -603,21 +608,22 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
             const int pair = (blk * L::kWords + s) / 2;
             uint4 b;
             if constexpr (C::kQInRegs) b = qr[pair];
-            else b = lds128(q_base + (((sub * kN + nt) * (L::kSteps / 2) + pair) * 32 + lane) * 16);
+            else b = lds128(q_base + ((nt * (L::kSteps / 2) + pair) * 32 + lane) * 16);
             mma_f16(sc[nt], a[0], b.x, b.y);
             mma_f16(sc[nt], a[1], b.z, b.w);
           }
         }
       }
-      const float ks = ldsf(kb + 2 * L::kStripBytes);
-      const float lv = attn_lg2(fmaxf(ldsf(kb + 2 * L::kStripBytes + 4), 7.888609052210118e-31f));
+      float ks, vs;
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(kb + 2 * L::kStripBytes));
+      const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
       const float inv_vs = attn_ex2(-lv);
       const bool masked = tok + 16 > tokens_all || tok < tokens_low;
       uint32_t pb[kN][2];
 #pragma unroll
       for (int nt = 0; nt < kN; ++nt) {
         if constexpr (!C::kQInRegs) {
-          const float2 f = *reinterpret_cast<const float2*>(row_scale + (sub * kN + nt) * 8 + 2 * t);
+          const float2 f = *reinterpret_cast<const float2*>(row_scale + nt * 8 + 2 * t);
           rs[0] = f.x, rs[1] = f.y;
         }
         const float f0 = rs[0] * ks, f1 = rs[1] * ks;
@@ -628,7 +634,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
         if (masked) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int row = min(wrow0 + nt * 8 + 2 * t + (e & 1), rows - 1), at_tok = tok + (e >> 1) * 8 + g;
+            const int row = min(row0 + nt * 8 + 2 * t + (e & 1), rows - 1), at_tok = tok + (e >> 1) * 8 + g;
             const int see_to = n - p.q_len + row / p.group + 1;
             dead[e] = at_tok >= see_to || (p.window > 0 && at_tok < see_to - p.window);
             if (dead[e]) x[e] = -__builtin_huge_valf();
@@ -668,13 +674,14 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
       for (int blk = 0; blk < L::kBlocks; ++blk) {
         uint32_t w[4][L::kVWords];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int r = 2 * t + (c & 1) + (c >> 1) * 8;
-          L::v_words(vb, r, blk, g, w[c]);
-          if (left < 16 && r >= left) {  // past the end: whatever lies there counts nothing
+        for (int c = 0; c < 4; ++c) L::v_words(vb, v_place, c, blk, w[c]);
+        if (left < 16) {  // past the end: whatever lies there counts nothing
 #pragma unroll
-            for (int k = 0; k < L::kVWords; ++k) w[c][k] = 0u;
-          }
+          for (int c = 0; c < 4; ++c)
+            if (2 * t + (c & 1) + (c >> 1) * 8 >= left) {
+#pragma unroll
+              for (int k = 0; k < L::kVWords; ++k) w[c][k] = 0u;
+            }
         }
 #pragma unroll
         for (int k = 0; k < L::kVWords; ++k) {
@@ -693,44 +700,41 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
 
-    // ---- the segment's end: join the teams ----
-    if (C::kQInRegs && seg_end < end) q_load(locate(seg_end), sub, qr);  // (arrives during the joining)
-    const AttnPlace cur = locate(at);
-    const int row0 = cur.tile * C::kRows;
-    const bool starts = cur.strip == 0, ends = cur.strip + (seg_end - at) == cur.strips;
-    const bool whole = starts && ends;
+    // ---- the segment's end: join the warps ----
 #pragma unroll
     for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) sum[nt][h] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][h], o);
-        if (g == 0) ml[team * C::kRows + (sub * kN + nt) * 8 + 2 * t + h] = make_float2(m[nt][h], sum[nt][h]);
+        if (g == 0) ml[warp * C::kRows + nt * 8 + 2 * t + h] = make_float2(m[nt][h], sum[nt][h]);
       }
-    const int used = min(C::kRows, rows - row0);
-    // a team's stage that is neither being read nor being filled, the one before its next: 8 rows of dims, fp32
+    // a warp's stage that is neither being read nor being filled, the one before its next: 8 rows of dims, fp32
     auto slab_of = [&](int w) -> float* {
-      const int read = max(0, (seg_end - begin - w + C::kTeams - 1) / C::kTeams);  // strips that the team has read so far
+      const int read = max(0, (seg_end - begin - w + C::kWarps - 1) / C::kWarps);  // strips that the warp has read so far
       return reinterpret_cast<float*>(smem + (w * C::kStages + (read + C::kStages - 1) % C::kStages) * C::kStageBytes);
     };
     // 16-byte cell of word k, thread row g2 and query row r: places change by row, against bank conflicts
     auto cell = [](int r, int k, int g2) -> int { return ((r * (L::kTiles / 2) + k) * 8 + (g2 ^ (r & 6))) * 4; };
-    // with two warps in a team, both are past the stage before either writes
+    const AttnPlace cur = places[which];
+    const int used = min(C::kRows, rows - row0);
+    const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
     constexpr int kRowFloats = kDim + 4;  // a partial row: the sums, m, the sum of weights
     auto part_of = [&](int cta, int slot) -> float* {
       return p.partial + (static_cast<int64_t>(cta) * 2 + slot) * (kAttnMaxRows * kRowFloats);
     };
     float* const part = part_of(blockIdx.x, starts ? 1 : 0);
     auto out_row = [&](int r, int64_t* tok_out, int* head_out) {
-      const int row = row0 + r;
-      *tok_out = static_cast<int64_t>(cur.b) * p.q_len + row / p.group;
-      *head_out = cur.head * p.group + row % p.group;
+      const int row = row0 + r, i = row / p.group;
+      *tok_out = static_cast<int64_t>(cur.b) * p.q_len + i;
+      *head_out = cur.head * p.group + row - i * p.group;
     };
-    auto store = [&](int r, int d, float4 v) {  // four outputs of local row r, dims d .. d + 3
+    auto store = [&](int r, int d, float4 v, float top, float l) {  // four outputs of local row r, dims d .. d + 3
       int64_t tok_out;
       int head_out;
       out_row(r, &tok_out, &head_out);
-      uint16_t* o = p.out + tok_out * p.ldo + static_cast<int64_t>(head_out) * kDim + d;
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+      v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
       uint2 w;
       if (p.f16) {
         w.x = pack_f16(v.x, v.y);
@@ -740,40 +744,33 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
         w.x = *reinterpret_cast<const uint32_t*>(&a);
         w.y = *reinterpret_cast<const uint32_t*>(&b);
       }
-      *reinterpret_cast<uint2*>(o) = w;
+      *reinterpret_cast<uint2*>(p.out + tok_out * p.ldo + head_out * kDim + d) = w;
+      if (d == 0 && p.lse)
+        p.lse[tok_out * (p.kv_heads * p.group) + head_out] =
+            l > 0.0f ? 0.6931471805599453f * (top + log2f(l)) : l == l ? -__builtin_huge_valf() : l;
     };
-    auto store_lse = [&](int r, float top, float l) {
-      if (!p.lse) return;
-      int64_t tok_out;
-      int head_out;
-      out_row(r, &tok_out, &head_out);
-      p.lse[tok_out * (p.kv_heads * p.group) + head_out] =
-          l > 0.0f ? 0.6931471805599453f * (top + log2f(l)) : l == l ? -__builtin_huge_valf() : l;
-    };
-    if (kTeam > 1) team_sync();
 #pragma unroll
-    for (int q8 = 0; q8 < C::kQTiles; ++q8) {  // eight rows at a time
-      if (q8 * 8 >= used) break;
-      if (sub == q8 / kN) {
+    for (int nt = 0; nt < kN; ++nt) {  // eight rows at a time
+      if (nt * 8 >= used) break;
+      float* const mine = slab_of(warp);
 #pragma unroll
-        for (int k = 0; k < L::kTiles / 2; ++k)
+      for (int k = 0; k < L::kTiles / 2; ++k)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float4*>(slab_of(team) + cell(2 * t + h, k, g)) =
-                make_float4(acc[q8 % kN][2 * k][h], acc[q8 % kN][2 * k][2 + h], acc[q8 % kN][2 * k + 1][h],
-                            acc[q8 % kN][2 * k + 1][2 + h]);
-      }
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float4*>(mine + cell(2 * t + h, k, g)) = make_float4(
+              acc[nt][2 * k][h], acc[nt][2 * k][2 + h], acc[nt][2 * k + 1][h], acc[nt][2 * k + 1][2 + h]);
       __syncthreads();
+      if (C::kQInRegs && seg_end < end) q_load(places[which ^ 1], 0, qr);  // (arrives during the joining)
       for (int x = tid; x < 8 * (kDim / 4); x += C::kThreads) {
-        const int r8 = x / (kDim / 4), d = (x - r8 * (kDim / 4)) * 4, r = q8 * 8 + r8;
+        const int r8 = x / (kDim / 4), d = (x - r8 * (kDim / 4)) * 4, r = nt * 8 + r8;
         if (r >= used) break;
         float top = kAttnFloor, l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < C::kTeams; ++w) top = fmaxf(top, ml[w * C::kRows + r].x);
+        for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, ml[w * C::kRows + r].x);
         const int2 place = L::v_place(d);
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < C::kTeams; ++w) {
+        for (int w = 0; w < C::kWarps; ++w) {
           const float2 o = ml[w * C::kRows + r];
           const float f = attn_ex2(o.x - top);
           const float4 a = *reinterpret_cast<const float4*>(slab_of(w) + cell(r8, place.x, place.y));
@@ -781,9 +778,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
           l = fmaf(o.y, f, l);
         }
         if (whole) {
-          const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-          store(r, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-          if (d == 0) store_lse(r, top, l);
+          store(r, d, v, top, l);
         } else {
           float* const o = part + r * kRowFloats;
           __stcg(reinterpret_cast<float4*>(o + d), v);
@@ -794,7 +789,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
     }
     if (!whole) {
       // the CTAs c0 .. c0 + n_parts - 1 share the item; a CTA's part is in its slot 1 if it starts the item, else 0
-      const int item0 = line_before[cur.b] + cur.item * line_of(cur.strips) + lead;  // the item's first strip on the line
+      const int len = plan_words[4] ? (cur.strips + per - 1) / per * per : cur.strips + lead;
+      const int item0 = line_before[cur.b] + cur.item * len + lead;  // the item's first strip on the line
       const int c0 = item0 / per, n_parts = (item0 + cur.strips - 1) / per - c0 + 1;
       // true for the last of `of` CTAs to come here (all threads alike)
       auto last_of = [&](uint32_t* counter, int of) -> bool {
@@ -861,13 +857,11 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
             top = mn;
           }
           if (live && way == 0) {
-            if (!final) {  // (m and the sum of weights once all threads have read the old ones)
+            if (final) {
+              store(r, d, v, top, l);
+            } else {  // (m and the sum of weights once all threads have read the old ones)
               __stcg(reinterpret_cast<float4*>(part_of(from, from == c0 ? 1 : 0) + r * kRowFloats + d), v);
               if (d == 0) ml[r] = make_float2(top, l);
-            } else {
-              const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-              store(r, d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-              if (d == 0) store_lse(r, top, l);
             }
           }
         }
@@ -891,6 +885,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kTeam>::kThreads, AttnCfg<kD
     }
     // on to the next item
     at = seg_end;
+    which ^= 1;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
