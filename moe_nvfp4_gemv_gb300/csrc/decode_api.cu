@@ -148,6 +148,7 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   p.block_log2 = block_log2(cache->block_size);
   p.kv_heads = cache->kv_heads;
   p.group = group;
+  p.group_magic = (65536 + group - 1) / group;
   p.q_len = q_len;
   p.row_tiles = row_tiles;
   p.window = window;

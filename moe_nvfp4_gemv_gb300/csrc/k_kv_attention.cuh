@@ -39,8 +39,8 @@
 // through the ring stage that happens to be free, while the other stages
 // already fill for the next item.  An item that several shares cut is joined
 // from fp32 partials in the workspace: the last of up to kAttnFan CTAs to
-// arrive joins theirs, and with more the last of those joins the joined ones
-// (counters that are left at zero).  Nothing waits on another CTA.
+// arrive joins theirs; with more, the last of every kAttnFan2, and the last of
+// those the joined ones (counters that are left at zero).  Nothing waits on another CTA.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -69,11 +69,14 @@ struct KvAttnParams {
   int kv_heads, group, q_len, row_tiles;  // row tiles of 8 kN rows
   int window;
   int f16;             // element type of q and out
+  int group_magic;     // ceil(2^16 / group): row / group = row group_magic >> 16 for the rows there are
+  float inv_ctas;      // 1 / the grid's CTAs
   float sm_scale;
 };
 
 constexpr int kAttnMaxRows = 32;  // rows of a row tile at most
-constexpr int kAttnFan = 16;      // partials that one CTA joins
+constexpr int kAttnFan = 40;      // partials that one CTA joins at once
+constexpr int kAttnFan2 = 20;     // ... where the joined ones are joined again
 constexpr int kAttnItemCost = 16;  // an item's end, in strips
 constexpr float kAttnFloor = -1e30f;  // the running maximum before any token
 constexpr float kAttnSlack = 8.0f;    // log2 of the largest weight before the running maximum moves
@@ -255,6 +258,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ AttnPlace places[3];  // the item being read and the next one by turns; the share's begin
   __shared__ int plan_words[6];
+  __shared__ int free_stage[C::kWarps];  // byte offset of the warp's idle ring stage
   __shared__ int last_flag;
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (uniform, and known to be)
@@ -272,15 +276,28 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
 
   const int rows = p.q_len * p.group;  // query rows of a KV head
   const int items = p.kv_heads * p.row_tiles;
+  // Queries and block table on their way to L2 while the first warp plans, each CTA a part.
+  if (warp > 0) {
+    const int per_row = (p.kv_heads * p.group * kDim * 2 + 127) >> 7, q_lines = p.B * p.q_len * per_row;
+    const int t_lines = static_cast<int>((static_cast<int64_t>(p.B) * p.max_blocks * 4 + 127) >> 7);
+    const int lines = q_lines + min(t_lines, 1 << 20), step = gridDim.x * (C::kThreads - 32);
+    for (int i = blockIdx.x * (C::kThreads - 32) + tid - 32, k = 0; i < lines && k < 2; i += step, ++k) {
+      const int row = i < q_lines ? i / per_row : 0;
+      const char* at = i < q_lines ? reinterpret_cast<const char*>(p.q + row * p.ldq) + (i - row * per_row) * 128
+                                   : reinterpret_cast<const char*>(p.table) + static_cast<int64_t>(i - q_lines) * 128;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    }
+  }
   auto first_strip = [&](int n) -> int {
     const int at = n - p.q_len;  // the first query's position
     return p.window > 0 && at >= p.window ? (at - p.window + 1) >> 4 : 0;
   };
   auto strips_of = [&](int n) -> int { return ((n + 15) >> 4) - first_strip(n); };
-  auto div_up = [](int x, int y, float inv_y) -> int {  // ceil(x / y): a product of floats, set right
-    int q = static_cast<int>(static_cast<float>(x) * inv_y);
-    q -= static_cast<int64_t>(q) * y > x;
-    q += static_cast<int64_t>(q + 1) * y <= x;
+  auto div_up = [](int x, int y, float inv_y) -> int {  // ceil(x / y), x + y below 2^31
+    if (x >= 1 << 24) return (x + y - 1) / y;
+    int q = static_cast<int>(static_cast<float>(x) * inv_y);  // (at most one off)
+    q -= q * y > x;
+    q += q * y + y <= x;
     return q + (q * y < x);
   };
   auto rounds = [](int x) { return (x + C::kWarps - 1) / C::kWarps * C::kWarps; };  // whole rounds of the warps
@@ -312,10 +329,10 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
       int per = 0;
       float inv_per = 0.0f;
       if (alive <= ctas) {
-        const int even = (total + ctas - 1) / ctas;
+        const int even = div_up(total, ctas, p.inv_ctas);
         for (int k = 0; k < 3 && per == 0; ++k) {
           const int len = max(C::kWarps, rounds(even + (even * k >> 3)));
-          const float inv = 1.0f / static_cast<float>(len);
+          const float inv = __fdividef(1.0f, static_cast<float>(len));
           int sum = 0;
           for (int b = lane; b < p.B + lane; b += 32) {
             const int n = b < p.B ? tokens[b] : 0;
@@ -329,7 +346,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
       }
       const bool pieces = per > 0;
       const int lead = pieces ? 0 : kAttnItemCost;
-      if (!pieces) per = max(rounds((total + alive * kAttnItemCost + ctas - 1) / ctas), C::kWarps);
+      if (!pieces) per = max(rounds(div_up(total + alive * kAttnItemCost, ctas, p.inv_ctas)), C::kWarps);
       // the sequences' places on both lines
       int strips_end = 0, line_end = 0;
       for (int b = lane; b < p.B + lane; b += 32) {
@@ -372,13 +389,13 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
           c.first = first_strip(n);
           c.strips = strips_of(n);
           const int len = pieces ? div_up(c.strips, per, inv_per) * per : c.strips + lead, off = at - line_before[lo];
-          c.item = off / len;
+          c.item = div_up(off + 1, len, __fdividef(1.0f, static_cast<float>(len))) - 1;
           // (a cut behind an item's last strip or in its cost: the strip that follows)
           int strip = max(off - c.item * len - lead, 0);
           where = strips_before[lo] + c.item * c.strips + min(strip, c.strips);
           if (lane == 0) {
             c.strip = strip;  // (below c.strips wherever the share is not empty, or pieces end)
-            c.head = c.item / p.row_tiles;
+            c.head = p.row_tiles == 1 ? c.item : c.item / p.row_tiles;
             c.tile = c.item - c.head * p.row_tiles;
             places[0] = places[2] = c;
           }
@@ -411,7 +428,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
   auto q_load = [&](const AttnPlace& c, int tile8, uint4 (&raw)[L::kSteps / 2]) {  // row g of the item's tile of 8
     const int row = c.tile * C::kRows + tile8 * 8 + g;
     const bool live = row < rows;
-    const int i = live ? row / p.group : 0;
+    const int i = live ? (row * p.group_magic) >> 16 : 0;
     const uint16_t* src = p.q + (static_cast<int64_t>(c.b) * p.q_len + i) * p.ldq +
                           (c.head * p.group + (live ? row - i * p.group : 0)) * kDim;
 #pragma unroll
@@ -635,7 +652,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int row = min(row0 + nt * 8 + 2 * t + (e & 1), rows - 1), at_tok = tok + (e >> 1) * 8 + g;
-            const int see_to = n - p.q_len + row / p.group + 1;
+            const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
             dead[e] = at_tok >= see_to || (p.window > 0 && at_tok < see_to - p.window);
             if (dead[e]) x[e] = -__builtin_huge_valf();
           }
@@ -709,11 +726,9 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
         for (int o = 4; o < 32; o <<= 1) sum[nt][h] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][h], o);
         if (g == 0) ml[warp * C::kRows + nt * 8 + 2 * t + h] = make_float2(m[nt][h], sum[nt][h]);
       }
-    // a warp's stage that is neither being read nor being filled, the one before its next: 8 rows of dims, fp32
-    auto slab_of = [&](int w) -> float* {
-      const int read = max(0, (seg_end - begin - w + C::kWarps - 1) / C::kWarps);  // strips that the warp has read so far
-      return reinterpret_cast<float*>(smem + (w * C::kStages + (read + C::kStages - 1) % C::kStages) * C::kStageBytes);
-    };
+    // the stage that is neither being read nor being filled, the one before the next: 8 rows of dims, fp32
+    const int idle = (warp * C::kStages + (stage == 0 ? C::kStages - 1 : stage - 1)) * C::kStageBytes;
+    if (lane == 0) free_stage[warp] = idle;
     // 16-byte cell of word k, thread row g2 and query row r: places change by row, against bank conflicts
     auto cell = [](int r, int k, int g2) -> int { return ((r * (L::kTiles / 2) + k) * 8 + (g2 ^ (r & 6))) * 4; };
     const AttnPlace cur = places[which];
@@ -725,7 +740,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
     };
     float* const part = part_of(blockIdx.x, starts ? 1 : 0);
     auto out_row = [&](int r, int64_t* tok_out, int* head_out) {
-      const int row = row0 + r, i = row / p.group;
+      const int row = row0 + r, i = (row * p.group_magic) >> 16;
       *tok_out = static_cast<int64_t>(cur.b) * p.q_len + i;
       *head_out = cur.head * p.group + row - i * p.group;
     };
@@ -752,7 +767,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
 #pragma unroll
     for (int nt = 0; nt < kN; ++nt) {  // eight rows at a time
       if (nt * 8 >= used) break;
-      float* const mine = slab_of(warp);
+      float* const mine = reinterpret_cast<float*>(smem + idle);
 #pragma unroll
       for (int k = 0; k < L::kTiles / 2; ++k)
 #pragma unroll
@@ -768,12 +783,13 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, ml[w * C::kRows + r].x);
         const int2 place = L::v_place(d);
+        const int from_cell = cell(r8, place.x, place.y);
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
           const float2 o = ml[w * C::kRows + r];
           const float f = attn_ex2(o.x - top);
-          const float4 a = *reinterpret_cast<const float4*>(slab_of(w) + cell(r8, place.x, place.y));
+          const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + free_stage[w]) + from_cell);
           v.x = fmaf(a.x, f, v.x), v.y = fmaf(a.y, f, v.y), v.z = fmaf(a.z, f, v.z), v.w = fmaf(a.w, f, v.w);
           l = fmaf(o.y, f, l);
         }
@@ -794,16 +810,17 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
       const int c0 = item0 / per, n_parts = (item0 + cur.strips - 1) / per - c0 + 1;
       // true for the last of `of` CTAs to come here (all threads alike)
       auto last_of = [&](uint32_t* counter, int of) -> bool {
-        __threadfence();
         __syncthreads();
         if (tid == 0) {
+          __threadfence();  // (cumulative: what the barrier showed this thread goes before the count)
           last_flag = of == 1 || atomicAdd(counter, 1u) == static_cast<uint32_t>(of - 1);
-          if (last_flag && of > 1) *counter = 0u;
+          if (last_flag) {
+            if (of > 1) *counter = 0u;
+            __threadfence();
+          }
         }
         __syncthreads();
-        const bool last = last_flag;
-        if (last) __threadfence();
-        return last;
+        return last_flag != 0;
       };
       // joins `cnt` partials, of every step-th CTA from `from` on, into the outputs or into the first of them
       auto join = [&](int from, int step, int cnt, bool final) {
@@ -871,7 +888,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
             __stcg(reinterpret_cast<float2*>(part_of(from, from == c0 ? 1 : 0) + tid * kRowFloats + kDim), ml[tid]);
         }
       };
-      const int fan = n_parts <= kAttnFan ? n_parts : kAttnFan;
+      const int fan = n_parts <= kAttnFan ? n_parts : kAttnFan2;
       const int mine = (static_cast<int>(blockIdx.x) - c0) / fan, from = c0 + mine * fan;
       const int members = min(fan, n_parts - mine * fan);
       if (last_of(p.arrived + from * 3 + (from == c0 ? 1 : 0), members)) {
