@@ -636,33 +636,37 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
       const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
       const float inv_vs = attn_ex2(-lv);
       const bool masked = tok + 16 > tokens_all || tok < tokens_low;
-      uint32_t pb[kN][2];
+      // exponents against the running maxima; where they are masked or too high, from the scores again
+      auto factor = [&](int nt, int h) -> float {
+        return (C::kQInRegs ? rs[h] : row_scale[nt * 8 + 2 * t + h]) * ks;
+      };
+      float x[kN][4];
+      bool again = masked;
+      if (!masked) {
+        float high = -1.0f;
 #pragma unroll
-      for (int nt = 0; nt < kN; ++nt) {
-        if constexpr (!C::kQInRegs) {
-          const float2 f = *reinterpret_cast<const float2*>(row_scale + nt * 8 + 2 * t);
-          rs[0] = f.x, rs[1] = f.y;
+        for (int nt = 0; nt < kN; ++nt) {
+          const float f0 = factor(nt, 0), f1 = factor(nt, 1), b0 = lv - m[nt][0], b1 = lv - m[nt][1];
+          x[nt][0] = fmaf(sc[nt][0], f0, b0), x[nt][1] = fmaf(sc[nt][1], f1, b1);
+          x[nt][2] = fmaf(sc[nt][2], f0, b0), x[nt][3] = fmaf(sc[nt][3], f1, b1);
+          high = fmaxf(high, fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3])));
         }
-        const float f0 = rs[0] * ks, f1 = rs[1] * ks;
-        const float b0 = lv - m[nt][0], b1 = lv - m[nt][1];
-        float x[4] = {fmaf(sc[nt][0], f0, b0), fmaf(sc[nt][1], f1, b1), fmaf(sc[nt][2], f0, b0),
-                      fmaf(sc[nt][3], f1, b1)};
-        bool dead[4] = {false, false, false, false};
-        if (masked) {
+        again = __any_sync(0xFFFFFFFFu, high > kAttnSlack);
+      }
+      if (again) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = min(row0 + nt * 8 + 2 * t + (e & 1), rows - 1), at_tok = tok + (e >> 1) * 8 + g;
-            const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
-            dead[e] = at_tok >= see_to || (p.window > 0 && at_tok < see_to - p.window);
-            if (dead[e]) x[e] = -__builtin_huge_valf();
-          }
-        }
-        if (__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) > kAttnSlack)) {
+        for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float f = h ? f1 : f0;
-            const float r0 = dead[h] ? -__builtin_huge_valf() : fmaf(sc[nt][h], f, lv);
-            const float r1 = dead[2 + h] ? -__builtin_huge_valf() : fmaf(sc[nt][2 + h], f, lv);
+            const float f = factor(nt, h);
+            float r0 = fmaf(sc[nt][h], f, lv), r1 = fmaf(sc[nt][2 + h], f, lv);
+            if (masked) {
+              const int row = min(row0 + nt * 8 + 2 * t + h, rows - 1);
+              const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
+              const int see_from = p.window > 0 ? see_to - p.window : 0;
+              if (tok + g >= see_to || tok + g < see_from) r0 = -__builtin_huge_valf();
+              if (tok + 8 + g >= see_to || tok + 8 + g < see_from) r1 = -__builtin_huge_valf();
+            }
             float top = fmaxf(r0, r1);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -675,16 +679,19 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
               acc[nt][j][h] *= fall;
               acc[nt][j][2 + h] *= fall;
             }
-            x[h] = r0 - mn;
-            x[2 + h] = r1 - mn;
+            x[nt][h] = r0 - mn;
+            x[nt][2 + h] = r1 - mn;
           }
-        }
+      }
+      uint32_t pb[kN][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = attn_ex2(x[e]);
-        sum[nt][0] = fmaf(x[0] + x[2], inv_vs, sum[nt][0]);
-        sum[nt][1] = fmaf(x[1] + x[3], inv_vs, sum[nt][1]);
-        pb[nt][0] = transpose8x8(pack_f16(x[0], x[1]));
-        pb[nt][1] = transpose8x8(pack_f16(x[2], x[3]));
+      for (int nt = 0; nt < kN; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][e] = attn_ex2(x[nt][e]);
+        sum[nt][0] = fmaf(x[nt][0] + x[nt][2], inv_vs, sum[nt][0]);
+        sum[nt][1] = fmaf(x[nt][1] + x[nt][3], inv_vs, sum[nt][1]);
+        pb[nt][0] = transpose8x8(pack_f16(x[nt][0], x[nt][1]));
+        pb[nt][1] = transpose8x8(pack_f16(x[nt][2], x[nt][3]));
       }
       const int left = n - tok;  // tokens of the sequence in this strip
 #pragma unroll
