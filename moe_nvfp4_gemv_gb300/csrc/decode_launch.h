@@ -18,9 +18,7 @@ void count_launch();
 cudaError_t launch_moe_route(const RouteParams& p, int dtype, int pdl, cudaStream_t stream);
 cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, int T, int sms, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_append(const KvAppendParams& p, int int8, int pdl, cudaStream_t stream);
-// Shares of the attention kernel's work per resident CTA, and its CTAs at most
-// (the workspace is sized for them).
-constexpr int kAttnWaves = 2;
+// CTAs of the attention kernel at most (the workspace is sized for them).
 int kv_attention_max_ctas(int sms);
 // row_units: row tiles of 8, 16 or 32 rows: 1, 2 or 4 (4 not with head_dim 256).
 cudaError_t launch_kv_attention(const KvAttnParams& p, int dim, int int8, int row_units, int sms, int pdl,

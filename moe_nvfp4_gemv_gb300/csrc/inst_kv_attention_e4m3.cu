@@ -6,7 +6,7 @@ namespace fp4 {
 cudaError_t launch_kv_attention_int8(const KvAttnParams& p, int dim, int row_units, int sms, int pdl,
                                      cudaStream_t stream);
 
-int kv_attention_max_ctas(int sms) { return kAttnWaves * 2 * sms; }
+int kv_attention_max_ctas(int sms) { return 2 * sms; }
 
 cudaError_t launch_kv_attention(const KvAttnParams& p, int dim, int int8, int row_units, int sms, int pdl,
                                 cudaStream_t stream) {

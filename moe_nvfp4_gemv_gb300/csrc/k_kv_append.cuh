@@ -144,7 +144,6 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     return p.f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
                  : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   };
-  float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < kAppendChunks; ++i) {
     const int c = tid + i * kThreads;
@@ -154,16 +153,31 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
       raw[i] = __ldg(reinterpret_cast<const uint4*>(src + t * p.ld[part]) + (c - t * chunks_per_token));
     }
   }
+  // magnitudes of both types are ordered like their bits; anything from `bound` on is not finite
+  const uint32_t bound = p.f16 ? 0x7C00u : 0x7F80u;
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kAppendChunks; ++i) {
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+  for (int i = 0; i < kAppendChunks; ++i)
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu),
+                                 __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu)));
+  const bool odd = max(top & 0xFFFFu, top >> 16) >= bound;  // some value of this thread is not finite
+  float amax;
+  if (odd) {
+    amax = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack(w[j]);
-      const float a0 = fabsf(f.x), a1 = fabsf(f.y);
-      if (a0 < __builtin_huge_valf()) amax = fmaxf(amax, a0);
-      if (a1 < __builtin_huge_valf()) amax = fmaxf(amax, a1);
+    for (int i = 0; i < kAppendChunks; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack(w[j]);
+        const float a0 = fabsf(f.x), a1 = fabsf(f.y);
+        if (a0 < __builtin_huge_valf()) amax = fmaxf(amax, a0);
+        if (a1 < __builtin_huge_valf()) amax = fmaxf(amax, a1);
+      }
     }
+  } else {
+    const float2 f = unpack(top);
+    amax = fmaxf(f.x, f.y);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
@@ -192,14 +206,45 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     const int c = tid + i * kThreads;
     if (c >= chunks) break;
     const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack(w[j]);
+      x[2 * j] = f.x, x[2 * j + 1] = f.y;
+    }
     uint32_t o[2];
+    if (!kInt8) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float2 a = unpack(w[2 * h]), d = unpack(w[2 * h + 1]);
-      float x[4] = {a.x, a.y, d.x, d.y};
+      for (int h = 0; h < 2; ++h) {
+        const float v[4] = {__fmul_rn(x[4 * h], inv), __fmul_rn(x[4 * h + 1], inv), __fmul_rn(x[4 * h + 2], inv),
+                            __fmul_rn(x[4 * h + 3], inv)};
+        o[h] = kv_codes4<kInt8>(v);
+      }
+    } else {
+      // round(x / scale) from y = x (1 / scale): within 127 2^-22 of the quotient, so its nearest integer is the
+      // quotient's unless y lies that near to a half; then, and for what is not finite, the division itself.  Adding
+      // 1.5 2^23 rounds to an integer and leaves it in the low bits.
+      float far = 0.0f;
+      uint32_t bits[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = kInt8 ? __fdiv_rn(x[j], scale) : __fmul_rn(x[j], inv);
-      o[h] = kv_codes4<kInt8>(x);
+      for (int j = 0; j < 8; ++j) {
+        const float y = __fmul_rn(x[j], inv);
+        const float r = __fadd_rn(y, 12582912.0f);
+        bits[j] = __float_as_uint(r);
+        far = fmaxf(far, fabsf(__fsub_rn(y, __fsub_rn(r, 12582912.0f))));
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        o[h] = __byte_perm(__byte_perm(bits[4 * h], bits[4 * h + 1], 0x0040),
+                           __byte_perm(bits[4 * h + 2], bits[4 * h + 3], 0x0040), 0x5410);
+      if (odd || far > 0.4998f) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float v[4] = {__fdiv_rn(x[4 * h], scale), __fdiv_rn(x[4 * h + 1], scale),
+                              __fdiv_rn(x[4 * h + 2], scale), __fdiv_rn(x[4 * h + 3], scale)};
+          o[h] = kv_codes4<kInt8>(v);
+        }
+      }
     }
     dst[c] = make_uint2(o[0], o[1]);
   }

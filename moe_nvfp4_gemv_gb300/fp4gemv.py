@@ -381,6 +381,7 @@ _moe_route = _lib.fp4gemv_moe_route
 _token_logprobs = _lib.fp4gemv_token_logprobs
 _I32 = torch.int32
 _F32 = torch.float32
+_LOGITS = "logits must be a 2-D bf16, f16 or fp32 CUDA tensor with unit inner stride"
 
 
 def moe_route(logits: torch.Tensor, topk: int, scores: str = "softmax", bias: torch.Tensor | None = None,
@@ -397,32 +398,35 @@ def moe_route(logits: torch.Tensor, topk: int, scores: str = "softmax", bias: to
     ``topk_group`` groups whose ``group_top`` largest keys have the largest
     sum.  Weights are the scores, divided by their sum with ``renormalize``,
     times ``scale``."""
-    code = _DTYPE_CODES.get(logits.dtype)
-    if code is None or logits.dim() != 2 or logits.stride(1) != 1 or not logits.is_cuda:
-        raise ValueError("logits must be a 2-D bf16, f16 or fp32 CUDA tensor with unit inner stride")
-    M, E = logits.shape
+    code, shape, index = _DTYPE_CODES.get(logits.dtype), logits.shape, logits.get_device()
+    if code is None or len(shape) != 2 or index < 0:
+        raise ValueError(_LOGITS)
+    M, E = shape
+    ld, inner = logits.stride()
+    if inner != 1:
+        raise ValueError(_LOGITS)
     kind = _ROUTE_SCORES.get(scores)
     if kind is None:
         raise ValueError(f"scores must be 'softmax' or 'sigmoid', not {scores!r}")
-    dev = logits.device
-    if bias is not None and (bias.dtype is not _F32 or bias.dim() != 1 or bias.shape[0] != E or
-                             not bias.is_contiguous() or bias.device != dev):
+    if bias is not None and (bias.dtype is not _F32 or bias.shape != (E,) or not bias.is_contiguous() or
+                             bias.get_device() != index):
         raise ValueError(f"bias must be a contiguous fp32 [{E}] tensor on the logits' device")
+    want = (M, topk)
     if ids is None:
-        ids = torch.empty(M, topk, dtype=_I32, device=dev)
-    elif ids.dtype is not _I32 or ids.shape != (M, topk) or not ids.is_contiguous() or ids.device != dev:
+        ids = torch.empty(want, dtype=_I32, device=logits.device)
+    elif ids.dtype is not _I32 or ids.shape != want or not ids.is_contiguous() or ids.get_device() != index:
         raise ValueError(f"ids must be a contiguous int32 [{M}, {topk}] tensor on the logits' device")
     if weights is None:
-        weights = torch.empty(M, topk, dtype=_F32, device=dev)
-    elif weights.dtype is not _F32 or weights.shape != (M, topk) or not weights.is_contiguous() or \
-            weights.device != dev:
+        weights = torch.empty(want, dtype=_F32, device=logits.device)
+    elif weights.dtype is not _F32 or weights.shape != want or not weights.is_contiguous() or \
+            weights.get_device() != index:
         raise ValueError(f"weights must be a contiguous fp32 [{M}, {topk}] tensor on the logits' device")
     if M == 0:
         return ids, weights
-    status = _moe_route(logits.data_ptr(), logits.stride(0) if M > 1 else E, code, M, E, topk, kind,
+    status = _moe_route(logits.data_ptr(), ld if M > 1 else E, code, M, E, topk, kind,
                         bias.data_ptr() if bias is not None else None, n_group, topk_group, group_top,
                         1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), 1 if pdl else 0,
-                        _raw_stream(dev.index))
+                        _raw_stream(index))
     if status:
         raise Fp4GemvError(status, "fp4gemv_moe_route")
     return ids, weights
@@ -445,33 +449,43 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int = 0, t
 
     ``logits`` bf16, f16 or fp32 [T, V] with unit inner stride and any row
     stride; ``out``: tensors to write into, laid out as the result."""
-    code = _DTYPE_CODES.get(logits.dtype)
-    if code is None or logits.dim() != 2 or logits.stride(1) != 1 or not logits.is_cuda:
-        raise ValueError("logits must be a 2-D bf16, f16 or fp32 CUDA tensor with unit inner stride")
-    T, V = logits.shape
-    dev = logits.device
-    if tokens.dtype is not _I32 or tokens.dim() != 1 or tokens.shape[0] != T or not tokens.is_contiguous() or \
-            tokens.device != dev:
+    code, shape, index = _DTYPE_CODES.get(logits.dtype), logits.shape, logits.get_device()
+    if code is None or len(shape) != 2 or index < 0:
+        raise ValueError(_LOGITS)
+    T, V = shape
+    ld, inner = logits.stride()
+    if inner != 1:
+        raise ValueError(_LOGITS)
+    if tokens.dtype is not _I32 or tokens.shape != (T,) or not tokens.is_contiguous() or \
+            tokens.get_device() != index:
         raise ValueError(f"tokens must be a contiguous int32 [{T}] tensor on the logits' device")
     if not temperature > 0:
         raise ValueError("temperature must be positive")
     if out is None:
+        dev = logits.device
         out = TokenLogprobs(torch.empty(T, dtype=_F32, device=dev), torch.empty(T, dtype=_I32, device=dev),
                             torch.empty(T, dtype=_F32, device=dev), torch.empty(T, top_n, dtype=_I32, device=dev),
                             torch.empty(T, top_n, dtype=_F32, device=dev))
     else:
-        for o, dtype, shape in zip(out, (_F32, _I32, _F32, _I32, _F32), ((T,), (T,), (T,), (T, top_n), (T, top_n))):
-            if o.dtype is not dtype or o.shape != shape or not o.is_contiguous() or o.device != dev:
-                raise ValueError("out must hold contiguous logprob fp32 [T], rank int32 [T], entropy fp32 [T], "
-                                 "top_ids int32 [T, top_n] and top_logprobs fp32 [T, top_n] on the logits' device")
-        if not isinstance(out, TokenLogprobs):
+        logprob, rank, entropy, top_ids, top_logprobs = out
+        row, top = (T,), (T, top_n)
+        if not (logprob.dtype is _F32 and rank.dtype is _I32 and entropy.dtype is _F32 and top_ids.dtype is _I32 and
+                top_logprobs.dtype is _F32 and logprob.shape == row and rank.shape == row and entropy.shape == row and
+                top_ids.shape == top and top_logprobs.shape == top and logprob.is_contiguous() and
+                rank.is_contiguous() and entropy.is_contiguous() and top_ids.is_contiguous() and
+                top_logprobs.is_contiguous() and logprob.get_device() == index and rank.get_device() == index and
+                entropy.get_device() == index and top_ids.get_device() == index and
+                top_logprobs.get_device() == index):
+            raise ValueError("out must hold contiguous logprob fp32 [T], rank int32 [T], entropy fp32 [T], "
+                             "top_ids int32 [T, top_n] and top_logprobs fp32 [T, top_n] on the logits' device")
+        if out.__class__ is not TokenLogprobs:
             out = TokenLogprobs(*out)
     if T == 0:
         return out
-    status = _token_logprobs(logits.data_ptr(), logits.stride(0) if T > 1 else V, code, T, V, tokens.data_ptr(),
-                             1.0 / temperature, top_n, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
-                             out[3].data_ptr() if top_n else None, out[4].data_ptr() if top_n else None,
-                             1 if pdl else 0, _raw_stream(dev.index))
+    status = _token_logprobs(logits.data_ptr(), ld if T > 1 else V, code, T, V, tokens.data_ptr(),
+                             1.0 / temperature, top_n, out.logprob.data_ptr(), out.rank.data_ptr(),
+                             out.entropy.data_ptr(), out.top_ids.data_ptr() if top_n else None,
+                             out.top_logprobs.data_ptr() if top_n else None, 1 if pdl else 0, _raw_stream(index))
     if status:
         raise Fp4GemvError(status, "fp4gemv_token_logprobs")
     return out

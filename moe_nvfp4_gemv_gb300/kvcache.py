@@ -56,7 +56,7 @@ def attention_workspace(device: torch.device, head_dim: int, stream: int | None 
     index = device.index if device.index is not None else torch.cuda.current_device()
     if stream is None:
         stream = _raw_stream(index)
-    key = (index, int(stream), head_dim)
+    key = (index, stream, head_dim)
     ws = _workspaces.get(key)
     if ws is None:
         ws = torch.zeros(attention_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
@@ -82,6 +82,7 @@ class KvCache8:
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.fmt = fmt
         self.device = k_codes.device
+        self._index = k_codes.get_device()
         self.num_blocks, self.kv_heads, self.block_size, self.head_dim = k_codes.shape
         self._struct = _CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                     self.num_blocks, self.kv_heads, self.block_size, self.head_dim, FORMATS[fmt])
@@ -97,15 +98,16 @@ class KvCache8:
         scales = [torch.zeros(shape[:2], dtype=_F32, device=device) for _ in range(2)]
         return cls(*codes, *scales, fmt=fmt)
 
-    def _check_sequences(self, block_table: torch.Tensor, seq_lens: torch.Tensor) -> int:
-        if block_table.dtype is not _I32 or block_table.dim() != 2 or not block_table.is_contiguous() or \
-                block_table.device != self.device:
+    def _check_sequences(self, block_table: torch.Tensor, seq_lens: torch.Tensor) -> tuple[int, int]:
+        shape, index = block_table.shape, self._index
+        if block_table.dtype is not _I32 or len(shape) != 2 or not block_table.is_contiguous() or \
+                block_table.get_device() != index:
             raise ValueError("block_table must be a contiguous int32 [B, max_blocks] tensor on the cache's device")
-        B = block_table.shape[0]
-        if seq_lens.dtype is not _I32 or seq_lens.dim() != 1 or seq_lens.shape[0] != B or \
-                not seq_lens.is_contiguous() or seq_lens.device != self.device:
+        B, max_blocks = shape
+        if seq_lens.dtype is not _I32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous() or \
+                seq_lens.get_device() != index:
             raise ValueError(f"seq_lens must be a contiguous int32 [{B}] tensor on the cache's device")
-        return B
+        return B, max_blocks
 
     def append(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                cu_new: torch.Tensor | None = None, pdl: bool = True) -> None:
@@ -113,28 +115,26 @@ class KvCache8:
         any token stride that is a multiple of 8) to B sequences: T / B tokens
         each, or tokens cu_new[b] .. cu_new[b + 1] (int32 [B + 1]) to sequence
         b.  ``seq_lens``: the lengths with the new tokens."""
-        B = self._check_sequences(block_table, seq_lens)
-        H, D = self.kv_heads, self.head_dim
-        for name, t in (("k", k), ("v", v)):
-            if (t.dtype is not _BF16 and t.dtype is not _F16) or t.dim() != 3 or t.shape[1] != H or \
-                    t.shape[2] != D or t.stride(2) != 1 or (t.stride(1) != D and H > 1) or t.device != self.device:
-                raise ValueError(f"{name} must be a bf16 or f16 [T, {H}, {D}] tensor on the cache's device with "
-                                 "contiguous heads")
-        T = k.shape[0]
-        if v.shape[0] != T or v.dtype is not k.dtype:
-            raise ValueError("k and v must have the same tokens and type")
+        B, max_blocks = self._check_sequences(block_table, seq_lens)
+        H, D, index = self.kv_heads, self.head_dim, self._index
+        shape, dtype, ks, vs = k.shape, k.dtype, k.stride(), v.stride()
+        if (dtype is not _BF16 and dtype is not _F16) or v.dtype is not dtype or len(shape) != 3 or shape[1] != H or \
+                shape[2] != D or v.shape != shape or k.get_device() != index or v.get_device() != index or \
+                ks[2] != 1 or vs[2] != 1 or (H > 1 and (ks[1] != D or vs[1] != D)):
+            raise ValueError(f"k and v must be bf16 or f16 [T, {H}, {D}] tensors of one type on the cache's device "
+                             "with contiguous heads")
+        T = shape[0]
         if cu_new is not None and (cu_new.dtype is not _I32 or cu_new.shape != (B + 1,) or
-                                   not cu_new.is_contiguous() or cu_new.device != self.device):
+                                   not cu_new.is_contiguous() or cu_new.get_device() != index):
             raise ValueError(f"cu_new must be a contiguous int32 [{B + 1}] tensor on the cache's device")
         if T == 0 or B == 0:
             if T:
                 raise ValueError("new tokens for no sequence")
             return
-        status = _append(self._handle, k.data_ptr(), k.stride(0) if T > 1 else H * D, v.data_ptr(),
-                         v.stride(0) if T > 1 else H * D, 0 if k.dtype is _BF16 else 1, T,
-                         cu_new.data_ptr() if cu_new is not None else None, block_table.data_ptr(),
-                         block_table.shape[1], seq_lens.data_ptr(), B, 1 if pdl else 0,
-                         _raw_stream(self.device.index))
+        status = _append(self._handle, k.data_ptr(), ks[0] if T > 1 else H * D, v.data_ptr(),
+                         vs[0] if T > 1 else H * D, 0 if dtype is _BF16 else 1, T,
+                         cu_new.data_ptr() if cu_new is not None else None, block_table.data_ptr(), max_blocks,
+                         seq_lens.data_ptr(), B, 1 if pdl else 0, _raw_stream(index))
         if status:
             raise Fp4GemvError(status, "fp4gemv_kv_append")
 
@@ -148,40 +148,40 @@ class KvCache8:
         that sees none gives zeros.  ``sm_scale`` defaults to 1 /
         sqrt(head_dim); ``lse``: fp32 [B, q_len, heads] to receive the natural
         log of the softmax's sums.  Returns ``out``."""
-        B = self._check_sequences(block_table, seq_lens)
-        D = self.head_dim
-        if (q.dtype is not _BF16 and q.dtype is not _F16) or q.dim() != 4 or q.shape[0] != B or q.shape[3] != D or \
-                q.device != self.device:
+        B, max_blocks = self._check_sequences(block_table, seq_lens)
+        D, index = self.head_dim, self._index
+        shape, dtype = q.shape, q.dtype
+        if (dtype is not _BF16 and dtype is not _F16) or len(shape) != 4 or shape[0] != B or shape[3] != D or \
+                q.get_device() != index:
             raise ValueError(f"q must be a bf16 or f16 [{B}, q_len, heads, {D}] tensor on the cache's device")
-        n, heads = q.shape[1], q.shape[2]
+        _, n, heads, _ = shape
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif out.dtype is not q.dtype or out.shape != q.shape or out.device != self.device:
+            out = torch.empty(shape, dtype=dtype, device=self.device)
+        elif out.dtype is not dtype or out.shape != shape or out.get_device() != index:
             raise ValueError("out must have q's shape, type and device")
-        ldq, ldo = self._token_stride(q, "q"), self._token_stride(out, "out")
-        if lse is not None and (lse.dtype is not _F32 or lse.shape != q.shape[:3] or not lse.is_contiguous() or
-                                lse.device != self.device):
+        ldq, ldo = self._token_stride(q.stride(), shape, "q"), self._token_stride(out.stride(), shape, "out")
+        if lse is not None and (lse.dtype is not _F32 or lse.shape != shape[:3] or not lse.is_contiguous() or
+                                lse.get_device() != index):
             raise ValueError(f"lse must be a contiguous fp32 [{B}, {n}, {heads}] tensor on the cache's device")
         if B == 0:
             return out
-        stream = _raw_stream(self.device.index)
+        stream = _raw_stream(index)
         if workspace is None:
             workspace = attention_workspace(self.device, D, stream)
-        status = _attend(self._handle, q.data_ptr(), ldq, 0 if q.dtype is _BF16 else 1, heads, n,
-                         block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), B,
+        status = _attend(self._handle, q.data_ptr(), ldq, 0 if dtype is _BF16 else 1, heads, n,
+                         block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), B,
                          self._sm_scale if sm_scale is None else sm_scale, window, out.data_ptr(), ldo,
-                         lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
-                         workspace.numel() * workspace.element_size(), 1 if pdl else 0, stream)
+                         lse.data_ptr() if lse is not None else None, workspace.data_ptr(), workspace.nbytes,
+                         1 if pdl else 0, stream)
         if status:
             raise Fp4GemvError(status, "fp4gemv_kv_attention")
         return out
 
     @staticmethod
-    def _token_stride(t: torch.Tensor, name: str) -> int:
+    def _token_stride(strides: tuple, shape: tuple, name: str) -> int:
         """The one stride between tokens of a [B, n, heads, head_dim] tensor."""
-        B, n, heads, dim = t.shape
-        sb, sn, sh, sd = t.stride()
-        step = sn if n > 1 else sb if B > 1 else heads * dim
+        B, n, heads, dim = shape
+        sb, sn, sh, sd = strides
         if sd != 1 or (sh != dim and heads > 1) or (n > 1 and B > 1 and sb != n * sn):
             raise ValueError(f"{name} must have contiguous heads and one stride between all its tokens")
-        return step
+        return sn if n > 1 else sb if B > 1 else heads * dim
