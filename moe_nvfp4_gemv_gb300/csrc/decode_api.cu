@@ -73,9 +73,9 @@ fp4gemv_status fp4gemv_kv_append(const fp4gemv_kv_cache* cache, const void* k, i
   p.heads = cache->kv_heads;
   p.block = cache->block_size;
   p.dim = cache->head_dim;
-  p.f16 = dtype == FP4GEMV_F16;
+  p.chunk_magic = ((1 << 20) + p.dim / 8 - 1) / (p.dim / 8);
   fp4::count_launch();
-  return from_cuda(fp4::launch_kv_append(p, cache->format == FP4GEMV_KV_INT8, pdl, stream));
+  return from_cuda(fp4::launch_kv_append(p, cache->format == FP4GEMV_KV_INT8, dtype == FP4GEMV_F16, pdl, stream));
 }
 
 // [arrival counters, three for each CTA | partials, two for each CTA]
@@ -176,7 +176,8 @@ fp4gemv_status fp4gemv_moe_route(const void* logits, int64_t ldl, int dtype, int
   if (!aligned(logits, dtype == FP4GEMV_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
     return FP4GEMV_ERR_MISALIGNED;
   if (!logits || !ids || !weights) return FP4GEMV_ERR_INVALID_ARG;
-  fp4gemv_status st = fp4::current_device_state(nullptr, nullptr);
+  int sms = 0;
+  fp4gemv_status st = fp4::current_device_state(nullptr, &sms);
   if (st != FP4GEMV_OK) return st;
   fp4::RouteParams p = {};
   p.logits = logits;
@@ -194,7 +195,7 @@ fp4gemv_status fp4gemv_moe_route(const void* logits, int64_t ldl, int dtype, int
   p.renormalize = renormalize;
   p.scale = scale;
   fp4::count_launch();
-  return from_cuda(fp4::launch_moe_route(p, dtype, pdl, stream));
+  return from_cuda(fp4::launch_moe_route(p, dtype, sms, pdl, stream));
 }
 
 fp4gemv_status fp4gemv_token_logprobs(const void* logits, int64_t ldl, int dtype, int T, int V, const int32_t* tokens,

@@ -15,9 +15,9 @@ namespace fp4 {
 fp4gemv_status current_device_state(uint32_t** err, int* sms);
 void count_launch();
 
-cudaError_t launch_moe_route(const RouteParams& p, int dtype, int pdl, cudaStream_t stream);
+cudaError_t launch_moe_route(const RouteParams& p, int dtype, int sms, int pdl, cudaStream_t stream);
 cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, int T, int sms, int pdl, cudaStream_t stream);
-cudaError_t launch_kv_append(const KvAppendParams& p, int int8, int pdl, cudaStream_t stream);
+cudaError_t launch_kv_append(const KvAppendParams& p, int int8, int f16, int pdl, cudaStream_t stream);
 // CTAs of the attention kernel at most (the workspace is sized for them).
 int kv_attention_max_ctas(int sms);
 // row_units: row tiles of 8, 16 or 32 rows: 1, 2 or 4 (4 not with head_dim 256).

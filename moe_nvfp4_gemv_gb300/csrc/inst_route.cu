@@ -31,25 +31,37 @@ cudaError_t launch_simple(void (*kernel)(Params), unsigned grid, unsigned thread
   return cudaLaunchKernelEx(&lc, kernel, p);
 }
 
+// A token on a warp (few tokens: the shortest chain), or on 8 or 16 lanes
+// (many: fewer instructions per token).
 template <typename T>
-cudaError_t route_typed(const RouteParams& p, int pdl, cudaStream_t stream) {
-  const unsigned grid = (static_cast<unsigned>(p.M) + kRouteWarps - 1) / kRouteWarps;
-  const int slots = (p.E + 31) / 32;
-  auto kernel = slots <= 1   ? moe_route_kernel<T, 1>
-                : slots <= 2 ? moe_route_kernel<T, 2>
-                : slots <= 4 ? moe_route_kernel<T, 4>
-                : slots <= 8 ? moe_route_kernel<T, 8>
-                             : moe_route_kernel<T, 16>;
-  return launch_simple<RouteParams>(kernel, grid, kRouteWarps * 32, 1, pdl, stream, p);
+cudaError_t route_typed(const RouteParams& p, int sms, int pdl, cudaStream_t stream) {
+  const bool many = p.M >= 16 * sms;
+  int lanes = 32;
+  void (*kernel)(RouteParams);
+  if (many && p.E <= 64) {
+    kernel = moe_route_kernel<T, 8, 8>;
+    lanes = 8;
+  } else if (many && p.E <= 128) {
+    kernel = moe_route_kernel<T, 16, 8>;
+    lanes = 16;
+  } else {
+    kernel = p.E <= 32    ? moe_route_kernel<T, 32, 1>
+             : p.E <= 64  ? moe_route_kernel<T, 32, 2>
+             : p.E <= 128 ? moe_route_kernel<T, 32, 4>
+             : p.E <= 256 ? moe_route_kernel<T, 32, 8>
+                          : moe_route_kernel<T, 32, 16>;
+  }
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.M) * lanes + kRouteThreads - 1) / kRouteThreads);
+  return launch_simple<RouteParams>(kernel, grid, kRouteThreads, 1, pdl, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_moe_route(const RouteParams& p, int dtype, int pdl, cudaStream_t stream) {
+cudaError_t launch_moe_route(const RouteParams& p, int dtype, int sms, int pdl, cudaStream_t stream) {
   switch (dtype) {
-    case 0: return route_typed<__nv_bfloat16>(p, pdl, stream);
-    case 1: return route_typed<__half>(p, pdl, stream);
-    default: return route_typed<float>(p, pdl, stream);
+    case 0: return route_typed<__nv_bfloat16>(p, sms, pdl, stream);
+    case 1: return route_typed<__half>(p, sms, pdl, stream);
+    default: return route_typed<float>(p, sms, pdl, stream);
   }
 }
 

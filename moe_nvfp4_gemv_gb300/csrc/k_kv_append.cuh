@@ -31,7 +31,7 @@ struct KvAppendParams {
   uint32_t* err;
   int uniform, B, T;
   int max_blocks, num_blocks, heads, block, dim;
-  int f16;                 // element type of k, v
+  int chunk_magic;         // ceil(2^20 / (dim / 8)): chunk / (dim / 8) = chunk chunk_magic >> 20 for a page's chunks
 };
 
 constexpr float kKvMinScale = 7.888609052210118e-31f;  // 2^-100
@@ -85,7 +85,7 @@ __device__ __forceinline__ void kv_values4(uint32_t w, float (&x)[4]) {
   }
 }
 
-template <bool kInt8, int kThreads>
+template <bool kInt8, bool kF16, int kThreads>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParams p) {
   __shared__ float warp_max[kThreads / 32];
   const int tid = threadIdx.x;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
 
   uint4 raw[kAppendChunks];
   auto unpack = [&](uint32_t w) -> float2 {
-    return p.f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
+    return kF16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
                  : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   };
 #pragma unroll
@@ -149,12 +149,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     const int c = tid + i * kThreads;
     raw[i] = make_uint4(0, 0, 0, 0);
     if (c < chunks) {
-      const int t = c / chunks_per_token;
+      const int t = (c * p.chunk_magic) >> 20;
       raw[i] = __ldg(reinterpret_cast<const uint4*>(src + t * p.ld[part]) + (c - t * chunks_per_token));
     }
   }
   // magnitudes of both types are ordered like their bits; anything from `bound` on is not finite
-  const uint32_t bound = p.f16 ? 0x7C00u : 0x7F80u;
+  const uint32_t bound = kF16 ? 0x7C00u : 0x7F80u;
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < kAppendChunks; ++i)
@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
         o[h] = kv_codes4<kInt8>(v);
       }
     } else {
-      // round(x / scale) from y = x (1 / scale): within 127 2^-22 of the quotient, so its nearest integer is the
-      // quotient's unless y lies that near to a half; then, and for what is not finite, the division itself.  Adding
+      // round(x / scale) from y = x (1 / scale): within 128 2^-22 of the rounded quotient, so its nearest integer is
+      // the quotient's unless y lies that near to a half; then, and for what is not finite, the division itself.  Adding
       // 1.5 2^23 rounds to an integer and leaves it in the low bits.
       float far = 0.0f;
       uint32_t bits[8];
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
       for (int h = 0; h < 2; ++h)
         o[h] = __byte_perm(__byte_perm(bits[4 * h], bits[4 * h + 1], 0x0040),
                            __byte_perm(bits[4 * h + 2], bits[4 * h + 3], 0x0040), 0x5410);
-      if (odd || far > 0.4998f) {
+      if (odd || far > 0.49995f) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float v[4] = {__fdiv_rn(x[4 * h], scale), __fdiv_rn(x[4 * h + 1], scale),

@@ -73,27 +73,53 @@ __device__ __forceinline__ void lp_join(LpStat& a, const LpStat& b, float c) {
   a.m = m;
 }
 
-// Adds N logits to the running statistics.
-template <int N>
-__device__ __forceinline__ void lp_add(LpStat& st, const float (&x)[N], float c) {
-  float bm = x[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) bm = fmaxf(bm, x[i]);
+// Pairs of floats in one register pair, with one instruction for both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// What a thread gathers: the statistics with s and u in two halves, and the
+// number of logits above the given token's.
+struct LpThread {
+  float m;
+  uint64_t s, u;
+  int above;
+};
+
+// A new running maximum, if bm is one.
+__device__ __forceinline__ void lp_raise(LpThread& st, float bm, float c) {
   if (bm > st.m) {
     const float d = (st.m - bm) * c;
-    const float f = ex2(d);
-    st.u = f * (st.u + st.s * d);
-    st.s *= f;
+    const uint64_t f = pair(ex2(d), ex2(d)), d2 = pair(d, d);
+    st.u = fma2(f, fma2(st.s, d2, st.u), 0ull);
+    st.s = fma2(f, st.s, 0ull);
     st.m = bm;
   }
-  const float mc = st.m * c;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float d = fmaf(max_nan(x[i], kMasked), c, -mc);
-    const float e = ex2(d);
-    st.s += e;
-    st.u = fmaf(e, d, st.u);
-  }
+}
+// Two logits (masked ones already at kMasked) into the sums; c2 = (c, c), mc2 = (-m c, -m c).
+__device__ __forceinline__ void lp_sum(LpThread& st, uint64_t x, uint64_t c2, uint64_t mc2) {
+  const uint64_t d = fma2(x, c2, mc2);
+  const float2 df = unpair(d);
+  const uint64_t e = pair(ex2(df.x), ex2(df.y));
+  st.s = add2(st.s, e);
+  st.u = fma2(e, d, st.u);
 }
 
 template <typename T>
@@ -116,6 +142,59 @@ __device__ __forceinline__ void lp_unpack(const uint4& v, float (&x)[LpVec<T>::k
       x[2 * i] = f.x;
       x[2 * i + 1] = f.y;
     }
+  }
+}
+
+// Adds kW words of logits (each one fp32 or two 16-bit ones).  Rows' given
+// tokens are mostly likely ones, so a batch none of whose logits is above
+// the token's is the usual case and is not counted through.
+template <typename T, int kW>
+__device__ __forceinline__ void lp_add(LpThread& st, const uint32_t (&w)[kW], float xr, float c) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    auto two = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); };
+    __nv_bfloat162 top = two(w[0]);
+#pragma unroll
+    for (int i = 1; i < kW; ++i) top = __hmax2(top, two(w[i]));
+    const float bm = fmaxf(__low2float(top), __high2float(top));
+    lp_raise(st, bm, c);
+    if (bm > xr) {
+      const __nv_bfloat162 limit = __float2bfloat162_rn(xr);  // (a logit of the row: exact)
+      __nv_bfloat162 n = __float2bfloat162_rn(0.0f);
+#pragma unroll
+      for (int i = 0; i < kW; ++i) n = __hadd2(n, __hgt2(two(w[i]), limit));  // (at most kW: exact)
+      st.above += static_cast<int>(__low2float(n) + __high2float(n));
+    }
+    const uint64_t c2 = pair(c, c), mc2 = pair(-st.m * c, -st.m * c);
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      const __nv_bfloat162 x = __hmax2_nan(two(w[i]), __float2bfloat162_rn(kMasked));
+      const uint32_t b = *reinterpret_cast<const uint32_t*>(&x);
+      lp_sum(st, pair(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u)), c2, mc2);
+    }
+  } else {
+    constexpr int kX = std::is_same<T, float>::value ? kW : 2 * kW;
+    float x[kX];
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      if constexpr (std::is_same<T, float>::value) {
+        x[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+      }
+    }
+    float bm = x[0];
+#pragma unroll
+    for (int i = 1; i < kX; ++i) bm = fmaxf(bm, x[i]);
+    lp_raise(st, bm, c);
+    if (bm > xr) {
+#pragma unroll
+      for (int i = 0; i < kX; ++i) st.above += x[i] > xr;
+    }
+    const uint64_t c2 = pair(c, c), mc2 = pair(-st.m * c, -st.m * c);
+#pragma unroll
+    for (int i = 0; i < kX; i += 2)
+      lp_sum(st, pair(max_nan(x[i], kMasked), max_nan(x[i + 1], kMasked)), c2, mc2);
   }
 }
 
@@ -169,35 +248,41 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
   const int singles = rank == 0 ? p.V - nvec * kN : 0;
   auto single_index = [&](int i) { return i < lead ? i : nvec * kN + i; };
 
-  LpStat st = {kMasked, 0.0f, 0.0f};
-  int above = 0;
+  LpThread mine = {kMasked, 0ull, 0ull, 0};
   if (tid < singles) {
-    const float x[1] = {to_float(row[single_index(tid)])};
-    lp_add<1>(st, x, c);
-    above += x[0] > xr;
+    const float x = to_float(row[single_index(tid)]);
+    lp_raise(mine, x, c);
+    mine.above += x > xr;
+    const float d = fmaf(max_nan(x, kMasked), c, -mine.m * c), e = ex2(d);
+    mine.s = add2(mine.s, pair(e, 0.0f));
+    mine.u = add2(mine.u, pair(e * d, 0.0f));
   }
   constexpr int kU = 4;  // vectors in flight per thread
   int v = v0 + tid;
   for (; v + (kU - 1) * kLpThreads < v1; v += kU * kLpThreads) {
-    uint4 raw[kU];
-#pragma unroll
-    for (int j = 0; j < kU; ++j) raw[j] = __ldg(vec + v + j * kLpThreads);
+    uint32_t w[4 * kU];
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
-      float x[kN];
-      lp_unpack<T>(raw[j], x);
-      lp_add<kN>(st, x, c);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) above += x[i] > xr;
+      const uint4 raw = __ldg(vec + v + j * kLpThreads);
+      w[4 * j] = raw.x, w[4 * j + 1] = raw.y, w[4 * j + 2] = raw.z, w[4 * j + 3] = raw.w;
     }
+    lp_add<T, 4 * kU>(mine, w, xr, c);
   }
-  for (; v < v1; v += kLpThreads) {
-    float x[kN];
-    lp_unpack<T>(__ldg(vec + v), x);
-    lp_add<kN>(st, x, c);
+  {
+    uint32_t w[kU - 1][4];  // the last few, loaded together
 #pragma unroll
-    for (int i = 0; i < kN; ++i) above += x[i] > xr;
+    for (int j = 0; j < kU - 1; ++j)
+      if (v + j * kLpThreads < v1) {
+        const uint4 raw = __ldg(vec + v + j * kLpThreads);
+        w[j][0] = raw.x, w[j][1] = raw.y, w[j][2] = raw.z, w[j][3] = raw.w;
+      }
+#pragma unroll
+    for (int j = 0; j < kU - 1; ++j)
+      if (v + j * kLpThreads < v1) lp_add<T, 4>(mine, w[j], xr, c);
   }
+  const float2 s2 = unpair(mine.s), u2 = unpair(mine.u);
+  LpStat st = {mine.m, s2.x + s2.y, u2.x + u2.y};
+  int above = mine.above;
 
   const float own_max = st.m;
   const bool any = tid < singles || v0 + tid < v1;

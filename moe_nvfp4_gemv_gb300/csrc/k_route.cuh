@@ -5,15 +5,16 @@
 // keys within the topk_group strongest groups; weights = scores of those,
 // renormalised on request.
 //
-// One warp per token, element e on lane e % 32, slot e / 32, so each slot is
-// one contiguous load.  Keys are compared as unsigned integers that order
-// like the floats (0: taken or absent), so a round of the selection is one
-// redux.sync over each lane's best plus a vote; the lower index wins because
-// a lane's slots are scanned upwards and equal lanes compare their indices.
+// kL lanes per token (a warp, or a part of one where there are many tokens),
+// expert e on lane e / S of the token's, slot e % S: a lane's experts are
+// neighbours, so of equal keys the lowest lane's lowest slot is the lower
+// index, and an expert group is a run of lanes.  Keys are compared as unsigned
+// integers that order like the floats (0: taken or absent).  A round of the
+// selection is a maximum over the lanes' best keys and a vote for the lane.
 //
 // Keys have to come out the same for every order of summation, or experts
 // whose keys nearly tie would change places: exp and the division are the
-// IEEE-rounded or library ones, and the softmax's sum is carried as an
+// library's and the IEEE-rounded one, and the softmax's sum is carried as an
 // unevaluated sum of two floats (Knuth's two-sum), ~48 bits.
 #pragma once
 
@@ -39,7 +40,7 @@ struct RouteParams {
   float scale;
 };
 
-constexpr int kRouteWarps = 4;  // tokens per CTA
+constexpr int kRouteThreads = 128;
 
 template <typename T>
 __device__ __forceinline__ float to_float(T v);
@@ -72,36 +73,51 @@ __device__ __forceinline__ void two_sum(float& hi, float& lo, float b, float c) 
   hi = s;
 }
 
-// Warp-wide: the lane and slot of the largest key (ties: the lowest index).
-template <int S>
-__device__ __forceinline__ uint32_t warp_best(const uint32_t (&key)[S], uint32_t lane, uint32_t* index) {
-  uint32_t best = key[0], slot = 0;
+// The largest of the token's lanes' values.
+template <int kL>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (kL == 32) {
+    return __reduce_max_sync(0xFFFFFFFFu, v);
+  } else {
 #pragma unroll
-  for (int i = 1; i < S; ++i)
-    if (key[i] > best) {
-      best = key[i];
-      slot = i;
-    }
-  const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-  *index = __reduce_min_sync(0xFFFFFFFFu, best == top ? slot * 32 + lane : 0xFFFFFFFFu);
-  return top;
+    for (int o = kL / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+  }
+}
+// The first of the token's lanes for which `is` holds (one does).
+template <int kL>
+__device__ __forceinline__ int first_lane(bool is, int lane) {
+  const uint32_t vote = __ballot_sync(0xFFFFFFFFu, is);
+  if constexpr (kL == 32) return __ffs(vote) - 1;
+  else return __ffs((vote >> (lane & ~(kL - 1))) & ((1u << kL) - 1u)) - 1;
 }
 
-template <typename T, int S>
-__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteParams p) {
-  const uint32_t lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+template <typename T, int kL, int S>
+__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteParams p) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31, sub = lane & (kL - 1);
+  const int64_t t = (static_cast<int64_t>(blockIdx.x) * kRouteThreads + threadIdx.x) / kL;
   if (threadIdx.x == 0) pdl_launch_dependents();
   pdl_wait();
-  if (t >= p.M) return;
-  const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
+  const bool live = t < p.M;  // (the lanes of no token go along)
+  const T* row = static_cast<const T*>(p.logits) + (live ? t : 0) * p.ldl;
+  const int e0 = sub * S;
   float x[S];
+  if (S * sizeof(T) >= 16 && e0 + S <= p.E && (reinterpret_cast<uintptr_t>(row + e0) & 15u) == 0) {
+    constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
-  for (int i = 0; i < S; ++i) {
-    const int e = i * 32 + lane;
-    x[i] = e < p.E ? to_float(row[e]) : kNegInf;
-    if (x[i] != x[i]) x[i] = kNegInf;
+    for (int i = 0; i < S / kPer; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + i);
+      const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) x[i * kPer + j] = to_float(e[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < S; ++i) x[i] = e0 + i < p.E ? to_float(row[e0 + i]) : kNegInf;
   }
+#pragma unroll
+  for (int i = 0; i < S; ++i) x[i] = x[i] == x[i] ? x[i] : kNegInf;
   // scores where the keys or an unnormalised softmax need all of them
   const bool by_logit = p.bias == nullptr && p.group_top == 1;
   float top = 0.0f, sum = 1.0f;
@@ -110,7 +126,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
 #pragma unroll
     for (int i = 1; i < S; ++i) m = fmaxf(m, x[i]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    for (int o = kL / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
     top = m;
   }
   auto raw_score = [&](float v) -> float {  // softmax: before the division by the sum
@@ -118,104 +134,163 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     return v == kNegInf ? 0.0f : v == top ? 1.0f : expf(__fsub_rn(v, top));
   };
   uint32_t key[S];
-  if (by_logit && (p.sigmoid || p.renormalize)) {
+  if (by_logit) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) key[i] = i * 32 + lane < p.E ? order_key(x[i]) : 0u;
-  } else {
+    for (int i = 0; i < S; ++i) key[i] = e0 + i < p.E ? order_key(x[i]) : 0u;
+  }
+  if (!by_logit || !(p.sigmoid || p.renormalize)) {
     float score[S];
 #pragma unroll
-    for (int i = 0; i < S; ++i) score[i] = raw_score(x[i]);  // (past E: x = -inf, sigmoid 0)
+    for (int i = 0; i < S; ++i) score[i] = raw_score(x[i]);  // (past E: x = -inf, score 0)
     if (!p.sigmoid) {
-      float hi = 0.0f, lo = 0.0f;
+      float hi = score[0], lo = 0.0f;
 #pragma unroll
-      for (int i = 0; i < S; ++i) two_sum(hi, lo, score[i], 0.0f);
+      for (int i = 1; i < S; ++i) two_sum(hi, lo, score[i], 0.0f);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float h2 = __shfl_xor_sync(0xFFFFFFFFu, hi, o), l2 = __shfl_xor_sync(0xFFFFFFFFu, lo, o);
+      for (int o = kL / 2; o; o >>= 1) {
+        const float h2 = __shfl_xor_sync(kAll, hi, o), l2 = __shfl_xor_sync(kAll, lo, o);
         two_sum(hi, lo, h2, l2);
       }
       sum = __fadd_rn(hi, lo);
     }
+    if (!by_logit) {
+      const bool divide = !p.sigmoid && sum > 0.0f;
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int e = i * 32 + lane;
-      if (by_logit) {
-        key[i] = e < p.E ? order_key(x[i]) : 0u;
-      } else {
-        float s = p.sigmoid ? score[i] : sum > 0.0f ? __fdiv_rn(score[i], sum) : 0.0f;
+      for (int i = 0; i < S; ++i) {
+        const int e = e0 + i;
+        float s = divide ? __fdiv_rn(score[i], sum) : score[i];  // (no sum: every score is 0)
         if (p.bias && e < p.E) s = __fadd_rn(s, __ldg(p.bias + e));
         key[i] = e < p.E ? order_key(s) : 0u;
       }
     }
   }
   if (p.n_group > 1) {
-    // strengths: lane g ends with group g's
-    const int size = p.E / p.n_group;
-    uint32_t strength = 0;
-    for (int g = 0; g < p.n_group; ++g) {
-      uint32_t a = 0, b = 0;  // this lane's two best of the group
+    const int size = p.E / p.n_group, width = size / S;
+    uint32_t chosen = 0;  // the groups that take part
+    if (width * S == size && (width & (width - 1)) == 0) {
+      // a group is a run of 2^k lanes: its two best keys by exchange within the run
+      uint32_t a = 0, b = 0;
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        const int e = i * 32 + lane;
-        const uint32_t k = e >= g * size && e < (g + 1) * size ? key[i] : 0u;
-        b = max(b, min(a, k));
-        a = max(a, k);
+        b = max(b, min(a, key[i]));
+        a = max(a, key[i]);
       }
-      const uint32_t first = __reduce_max_sync(0xFFFFFFFFu, a);
-      uint32_t s = first;
-      if (p.group_top == 2) {
-        const uint32_t who = __ballot_sync(0xFFFFFFFFu, a == first);
-        const uint32_t rest = lane == __ffs(who) - 1 ? b : a;
-        const uint32_t second = __reduce_max_sync(0xFFFFFFFFu, rest);
-        s = order_key(__fadd_rn(key_value(first), key_value(second)));
+      for (int o = 1; o < width; o <<= 1) {
+        const uint32_t a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+        b = max(min(a, a2), max(b, b2));
+        a = max(a, a2);
       }
-      if (lane == g) strength = s;
-    }
-    uint32_t chosen = 0;
-    for (int j = 0; j < p.topk_group; ++j) {
-      const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, strength);
-      const uint32_t g = __ffs(__ballot_sync(0xFFFFFFFFu, strength == best)) - 1;
-      chosen |= 1u << g;
-      if (lane == g) strength = 0;
-    }
+      const uint32_t strength =
+          e0 >= p.E ? 0u : p.group_top == 2 ? order_key(__fadd_rn(key_value(a), key_value(b))) : a;
+      // its place among the groups: those that are stronger, or as strong and earlier
+      const int mine = e0 / size;
+      int before = 0;
+      for (int g = 0; g < p.n_group; ++g) {
+        const uint32_t other = __shfl_sync(kAll, strength, (lane & ~(kL - 1)) + g * width);
+        before += other > strength || (other == strength && g < mine);
+      }
+      if (before >= p.topk_group) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int e = i * 32 + lane;
-      if (e < p.E && !((chosen >> (e / size)) & 1u)) key[i] = 0;
+        for (int i = 0; i < S; ++i) key[i] = 0;
+      }
+    } else {
+      uint32_t strength[32 / kL];  // group g: lane g % kL's entry g / kL
+#pragma unroll
+      for (int i = 0; i < 32 / kL; ++i) strength[i] = 0;
+      for (int g = 0; g < p.n_group; ++g) {
+        uint32_t a = 0, b = 0;  // this lane's two best of the group
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const uint32_t k = e0 + i >= g * size && e0 + i < (g + 1) * size ? key[i] : 0u;
+          b = max(b, min(a, k));
+          a = max(a, k);
+        }
+        uint32_t s = lanes_max<kL>(a);
+        if (p.group_top == 2) {
+          const int who = first_lane<kL>(a == s, lane);
+          const uint32_t second = lanes_max<kL>(sub == who ? b : a);
+          s = order_key(__fadd_rn(key_value(s), key_value(second)));
+        }
+#pragma unroll
+        for (int i = 0; i < 32 / kL; ++i)
+          if (g == i * kL + sub) strength[i] = s;
+      }
+      for (int j = 0; j < p.topk_group; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < 32 / kL; ++i) best = max(best, strength[i]);
+        best = lanes_max<kL>(best);
+        int g = 32;  // the lowest group that has it: the lowest entry's lowest lane
+#pragma unroll
+        for (int i = 0; i < 32 / kL; ++i) {
+          const uint32_t vote = __ballot_sync(kAll, strength[i] == best) >> (lane & ~(kL - 1));
+          const uint32_t here = kL == 32 ? vote : vote & ((1u << (kL & 31)) - 1u);
+          if (g == 32 && here != 0) g = i * kL + __ffs(here) - 1;
+        }
+        chosen |= 1u << g;
+#pragma unroll
+        for (int i = 0; i < 32 / kL; ++i)
+          if (g == i * kL + sub) strength[i] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+        if (e0 + i < p.E && !((chosen >> ((e0 + i) / size)) & 1u)) key[i] = 0;
     }
   }
-  // the selection: lane j keeps the j-th
-  uint32_t mine = 0;
-  float logit = kNegInf;
+  // the selection: the token's lane j keeps the j-th (and lane j % kL the later ones)
+  constexpr int kKeep = 32 / kL;
+  int mine[kKeep];
+  float logit[kKeep];
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    mine[i] = 0;
+    logit[i] = kNegInf;
+  }
   for (int j = 0; j < p.topk; ++j) {
-    uint32_t e;
-    warp_best<S>(key, lane, &e);
-    float v = 0.0f;
+    uint32_t best = key[0], best_x = __float_as_uint(x[0]);
+    int slot = 0;
+#pragma unroll
+    for (int i = 1; i < S; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        best_x = __float_as_uint(x[i]);
+        slot = i;
+      }
+    const uint32_t most = lanes_max<kL>(best);
+    const int who = first_lane<kL>(best == most, lane);
+    // (the winner's slot, and its logit where that is not the key itself)
+    const int e = who * S + __shfl_sync(kAll, slot, (lane & ~(kL - 1)) + who);
+    const float v = by_logit ? key_value(most)
+                             : __uint_as_float(__shfl_sync(kAll, best_x, (lane & ~(kL - 1)) + who));
 #pragma unroll
     for (int i = 0; i < S; ++i)
-      if (static_cast<uint32_t>(i) == e >> 5) {
-        v = x[i];
-        if (lane == (e & 31)) key[i] = 0;
-      }
-    v = __shfl_sync(0xFFFFFFFFu, v, e & 31);
-    if (lane == static_cast<uint32_t>(j)) {
-      mine = e;
-      logit = v;
-    }
-  }
-  const bool live = lane < static_cast<uint32_t>(p.topk);
-  float w = live ? raw_score(logit) : 0.0f;
-  if (p.renormalize) {
-    float total = w;
+      if (e0 + i == e) key[i] = 0;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
-  } else if (!p.sigmoid) {
-    w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;
+    for (int i = 0; i < kKeep; ++i)
+      if (j == i * kL + sub) {
+        mine[i] = e;
+        logit[i] = v;
+      }
   }
-  if (live) {
-    p.ids[t * p.topk + lane] = static_cast<int32_t>(mine);
-    p.weights[t * p.topk + lane] = w * p.scale;
+  float w[kKeep], total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    w[i] = i * kL + sub < p.topk ? raw_score(logit[i]) : 0.0f;
+    total += w[i];
+  }
+  if (p.renormalize) {
+#pragma unroll
+    for (int o = kL / 2; o; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  } else {
+    total = p.sigmoid ? 1.0f : sum;
+  }
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int j = i * kL + sub;
+    if (live && j < p.topk) {
+      p.ids[t * p.topk + j] = mine[i];
+      p.weights[t * p.topk + j] = (total > 0.0f ? __fdiv_rn(w[i], total) : 0.0f) * p.scale;
+    }
   }
 }
 
