@@ -73,7 +73,6 @@ fp4gemv_status fp4gemv_kv_append(const fp4gemv_kv_cache* cache, const void* k, i
   p.heads = cache->kv_heads;
   p.block = cache->block_size;
   p.dim = cache->head_dim;
-  p.chunk_magic = ((1 << 20) + p.dim / 8 - 1) / (p.dim / 8);
   fp4::count_launch();
   return from_cuda(fp4::launch_kv_append(p, cache->format == FP4GEMV_KV_INT8, dtype == FP4GEMV_F16, pdl, stream));
 }

@@ -65,19 +65,22 @@ cudaError_t launch_moe_route(const RouteParams& p, int dtype, int sms, int pdl, 
   }
 }
 
-cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, int T, int sms, int pdl, cudaStream_t stream) {
-  // a cluster per row while the rows alone leave SMs idle and a slice keeps
-  // 16 bytes for most threads
-  const int elem = dtype == 2 ? 4 : 2;
+template <typename T>
+static cudaError_t logprobs_typed(const LogprobParams& p, int rows, int sms, int pdl, cudaStream_t stream) {
+  auto kernel = token_logprobs_kernel<T>;
+  // a cluster per row while the rows alone leave CTAs idle and a slice keeps 16 bytes for every thread
   unsigned c = 1;
-  while (c < kLpMaxCluster && static_cast<int64_t>(T) * c * 2 <= 2 * sms &&
-         static_cast<int64_t>(p.V) * elem / (2 * c) >= kLpThreads * 16)
+  while (c < kLpMaxCluster && static_cast<int64_t>(rows) * c * 2 <= 4 * sms &&
+         static_cast<int64_t>(p.V) * static_cast<int>(sizeof(T)) / (2 * c) >= kLpThreads * 16)
     c *= 2;
-  const unsigned grid = static_cast<unsigned>(T) * c;
+  return launch_simple<LogprobParams>(kernel, static_cast<unsigned>(rows) * c, kLpThreads, c, pdl, stream, p);
+}
+
+cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, int T, int sms, int pdl, cudaStream_t stream) {
   switch (dtype) {
-    case 0: return launch_simple<LogprobParams>(token_logprobs_kernel<__nv_bfloat16>, grid, kLpThreads, c, pdl, stream, p);
-    case 1: return launch_simple<LogprobParams>(token_logprobs_kernel<__half>, grid, kLpThreads, c, pdl, stream, p);
-    default: return launch_simple<LogprobParams>(token_logprobs_kernel<float>, grid, kLpThreads, c, pdl, stream, p);
+    case 0: return logprobs_typed<__nv_bfloat16>(p, T, sms, pdl, stream);
+    case 1: return logprobs_typed<__half>(p, T, sms, pdl, stream);
+    default: return logprobs_typed<float>(p, T, sms, pdl, stream);
   }
 }
 

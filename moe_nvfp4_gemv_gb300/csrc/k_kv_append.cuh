@@ -2,7 +2,7 @@
 // (fp4gemv_kv_append; the formats are in include/fp4gemv_decode.h).
 //
 // One CTA per (touched page, KV head, K or V): it holds the page's new values
-// in registers (8 chunks of 8 per thread at most), takes their largest
+// in registers (a chunk of 8 in each of at most 8 tokens per thread), takes their largest
 // finite magnitude, settles the page's scale, rounds the older codes again
 // where the scale grew, and stores codes and scale.  Every value is read
 // once and every code written once; no two CTAs write the same page and head.
@@ -31,7 +31,6 @@ struct KvAppendParams {
   uint32_t* err;
   int uniform, B, T;
   int max_blocks, num_blocks, heads, block, dim;
-  int chunk_magic;         // ceil(2^20 / (dim / 8)): chunk / (dim / 8) = chunk chunk_magic >> 20 for a page's chunks
 };
 
 constexpr float kKvMinScale = 7.888609052210118e-31f;  // 2^-100
@@ -131,13 +130,17 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     return;
   }
   const int slot = static_cast<int>(begin - page * p.block);  // the first new token's place on the page
-  const int chunks_per_token = p.dim / 8;
-  const int chunks = static_cast<int>(end - begin) * chunks_per_token;
+  // A thread takes chunk `col` of tokens first, first + step, ...
+  const int chunks = p.dim / 8, step = kThreads / chunks, first = tid / chunks, col = tid - first * chunks;
+  const int count_here = static_cast<int>(end - begin);
+  const int left = first < step ? count_here - first : 0;  // (threads past the last whole row of chunks do nothing)
   const int64_t token0 = first_new + (begin - start);
-  const uint16_t* src = p.src[part] + token0 * p.ld[part] + static_cast<int64_t>(head) * p.dim;
+  const int64_t ld = part ? p.ld[1] : p.ld[0];
+  const uint16_t* src = (part ? p.src[1] : p.src[0]) + (token0 + first) * ld + static_cast<int64_t>(head) * p.dim + col * 8;
+  const int64_t src_step = step * ld;
   const int64_t tile = static_cast<int64_t>(id) * p.heads + head;
-  uint8_t* codes = p.codes[part] + tile * p.block * p.dim;
-  float* scale_at = p.scale[part] + tile;
+  uint8_t* codes = (part ? p.codes[1] : p.codes[0]) + tile * p.block * p.dim;
+  float* scale_at = (part ? p.scale[1] : p.scale[0]) + tile;
 
   uint4 raw[kAppendChunks];
   auto unpack = [&](uint32_t w) -> float2 {
@@ -146,12 +149,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
   };
 #pragma unroll
   for (int i = 0; i < kAppendChunks; ++i) {
-    const int c = tid + i * kThreads;
     raw[i] = make_uint4(0, 0, 0, 0);
-    if (c < chunks) {
-      const int t = (c * p.chunk_magic) >> 20;
-      raw[i] = __ldg(reinterpret_cast<const uint4*>(src + t * p.ld[part]) + (c - t * chunks_per_token));
-    }
+    if (i * step < left) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + i * src_step));
   }
   // magnitudes of both types are ordered like their bits; anything from `bound` on is not finite
   const uint32_t bound = kF16 ? 0x7C00u : 0x7F80u;
@@ -200,53 +199,63 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     }
   }
   const float inv = __fdiv_rn(1.0f, scale);  // (E4M3: an exact power of two)
-  uint2* dst = reinterpret_cast<uint2*>(codes + static_cast<int64_t>(slot) * p.dim);
+  uint2* dst = reinterpret_cast<uint2*>(codes + static_cast<int64_t>(slot + first) * p.dim) + col;
+  const int dst_step = step * chunks;
+  uint32_t again = kInt8 && odd ? 0xFFu : 0u;  // chunks that need the division itself
 #pragma unroll
   for (int i = 0; i < kAppendChunks; ++i) {
-    const int c = tid + i * kThreads;
-    if (c >= chunks) break;
+    if (i * step >= left) continue;
     const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
     float x[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = unpack(w[j]);
-      x[2 * j] = f.x, x[2 * j + 1] = f.y;
+      x[2 * j] = __fmul_rn(f.x, inv), x[2 * j + 1] = __fmul_rn(f.y, inv);
     }
     uint32_t o[2];
     if (!kInt8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float v[4] = {__fmul_rn(x[4 * h], inv), __fmul_rn(x[4 * h + 1], inv), __fmul_rn(x[4 * h + 2], inv),
-                            __fmul_rn(x[4 * h + 3], inv)};
+        const float v[4] = {x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
         o[h] = kv_codes4<kInt8>(v);
       }
     } else {
       // round(x / scale) from y = x (1 / scale): within 128 2^-22 of the rounded quotient, so its nearest integer is
-      // the quotient's unless y lies that near to a half; then, and for what is not finite, the division itself.  Adding
-      // 1.5 2^23 rounds to an integer and leaves it in the low bits.
+      // the quotient's unless y lies that near to a half; then, and for what is not finite, the division itself,
+      // below.  Adding 1.5 2^23 rounds to an integer and leaves it in the low bits.
       float far = 0.0f;
       uint32_t bits[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float y = __fmul_rn(x[j], inv);
-        const float r = __fadd_rn(y, 12582912.0f);
-        bits[j] = __float_as_uint(r);
-        far = fmaxf(far, fabsf(__fsub_rn(y, __fsub_rn(r, 12582912.0f))));
+        const float n = __fadd_rn(x[j], 12582912.0f);
+        bits[j] = __float_as_uint(n);
+        far = fmaxf(far, fabsf(__fsub_rn(x[j], __fsub_rn(n, 12582912.0f))));
       }
+      if (far > 0.49995f) again |= 1u << i;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         o[h] = __byte_perm(__byte_perm(bits[4 * h], bits[4 * h + 1], 0x0040),
                            __byte_perm(bits[4 * h + 2], bits[4 * h + 3], 0x0040), 0x5410);
-      if (odd || far > 0.49995f) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float v[4] = {__fdiv_rn(x[4 * h], scale), __fdiv_rn(x[4 * h + 1], scale),
-                              __fdiv_rn(x[4 * h + 2], scale), __fdiv_rn(x[4 * h + 3], scale)};
-          o[h] = kv_codes4<kInt8>(v);
-        }
-      }
     }
-    dst[c] = make_uint2(o[0], o[1]);
+    dst[i * dst_step] = make_uint2(o[0], o[1]);
+  }
+  if (kInt8) {
+#pragma unroll 1
+    for (int i = 0; i * step < left; ++i) {
+      if (!((again >> i) & 1u)) continue;
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + i * src_step));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t o[2];
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const float2 a = unpack(h ? w[2] : w[0]), d = unpack(h ? w[3] : w[1]);
+        const float q[4] = {__fdiv_rn(a.x, scale), __fdiv_rn(a.y, scale), __fdiv_rn(d.x, scale), __fdiv_rn(d.y, scale)};
+        const uint32_t c = kv_codes4<kInt8>(q);
+        if (h) o[1] = c;
+        else o[0] = c;
+      }
+      dst[i * dst_step] = make_uint2(o[0], o[1]);
+    }
   }
 }
 

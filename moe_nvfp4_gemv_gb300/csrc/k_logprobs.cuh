@@ -39,7 +39,8 @@ struct LogprobParams {
   float inv_t;
 };
 
-constexpr int kLpThreads = 512;
+constexpr int kLpThreads = 256;
+constexpr int kLpResident = 5;  // CTAs per SM
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpGroups = 64;
 constexpr int kMaxCand = 512;
@@ -64,13 +65,21 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 struct LpStat {
   float m, s, u;
 };
-__device__ __forceinline__ void lp_join(LpStat& a, const LpStat& b, float c) {
-  const float m = fmaxf(a.m, b.m);
-  const float da = (a.m - m) * c, db = (b.m - m) * c;
-  const float fa = ex2(da), fb = ex2(db);
-  a.u = fa * (a.u + a.s * da) + fb * (b.u + b.s * db);
-  a.s = fa * a.s + fb * b.s;
+// The warp's statistics as one, in every lane: the maximum first, then sums
+// of what each lane has against it (a shorter chain than joining pairs).
+__device__ __forceinline__ void lp_join_warp(LpStat& a, float c) {
+  float m = a.m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const float d = (a.m - m) * c, f = ex2(d);
+  a.u = f * fmaf(a.s, d, a.u);
+  a.s *= f;
   a.m = m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, o);
+    a.u += __shfl_xor_sync(0xFFFFFFFFu, a.u, o);
+  }
 }
 
 // Pairs of floats in one register pair, with one instruction for both.
@@ -202,6 +211,21 @@ __device__ __forceinline__ uint64_t lp_key(float x, uint32_t i) {
   return (static_cast<uint64_t>(order_key(x)) << 32) | (0xFFFFFFFFu - i);
 }
 
+// How many of the keys are above k: the list is followed by zeros up to a
+// multiple of 8 keys (two per load, eight in flight).
+__device__ __forceinline__ int count_above(const uint64_t* list, int n, uint64_t k) {
+  int r = 0;
+#pragma unroll 1
+  for (int j = 0; j < n; j += 8) {
+    ulonglong2 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const ulonglong2*>(list + j)[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r += (v[i].x > k) + (v[i].y > k);
+  }
+  return r;
+}
+
 struct LpShared {
   LpStat stat[kLpMaxCluster][kLpWarps];
   int count[kLpMaxCluster][kLpWarps];
@@ -209,24 +233,28 @@ struct LpShared {
   unsigned long long bound;
   int n_flag, n_cand;
   uint16_t flagged[kLpThreads];
-  uint64_t cand[kMaxCand];
-  uint64_t top[kLpMaxCluster * 32];
+  alignas(16) uint64_t cand[kMaxCand];
+  alignas(16) uint64_t top[kLpMaxCluster * 32];
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, kLpResident) token_logprobs_kernel(const LogprobParams p) {
   __shared__ LpShared sh;
   constexpr int kN = LpVec<T>::kN;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t C = cluster_nctarank(), rank = cluster_ctarank();
   const int64_t t = blockIdx.x / C;
-  if (C > 1) cluster_arrive_relaxed();  // (waited for before the first store into another CTA)
   if (tid == 0) pdl_launch_dependents();
   if (tid < kLpGroups) sh.group[tid] = 0;
   if (tid == 0) {
     sh.n_flag = 0;
     sh.n_cand = 0;
   }
+  if (p.n > 0) {
+    for (int i = tid; i < kMaxCand; i += kLpThreads) sh.cand[i] = 0;
+    for (int i = tid; i < kLpMaxCluster * 32; i += kLpThreads) sh.top[i] = 0;
+  }
+  if (C > 1) cluster_arrive();  // (waited for before the first store into another CTA)
   pdl_wait();
   const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
   const int token = __ldg(p.tokens + t);
@@ -286,14 +314,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
 
   const float own_max = st.m;
   const bool any = tid < singles || v0 + tid < v1;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    LpStat b;
-    b.m = __shfl_xor_sync(0xFFFFFFFFu, st.m, o);
-    b.s = __shfl_xor_sync(0xFFFFFFFFu, st.s, o);
-    b.u = __shfl_xor_sync(0xFFFFFFFFu, st.u, o);
-    lp_join(st, b, c);
-  }
+  lp_join_warp(st, c);
   above = __reduce_add_sync(0xFFFFFFFFu, above);
   // statistics, counts and winners meet in the first CTA's shared memory
   if (C > 1) cluster_wait();
@@ -311,15 +332,20 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
     const uint32_t own = any ? order_key(own_max > kMasked ? own_max : kNegInf) : 0u;
     if (own) atomicMax(&sh.group[tid & (kLpGroups - 1)], own);
     __syncthreads();
-    if (tid < kLpGroups) {
-      const uint32_t mine = sh.group[tid];
+    {  // four threads rank a group among the others
+      static_assert(kLpThreads == 4 * kLpGroups, "");
+      const int mine_at = tid >> 2;
+      const uint32_t group_max = sh.group[mine_at];
       int r = 0;
-#pragma unroll 16
-      for (int j = 0; j < kLpGroups; ++j) {
+#pragma unroll 4
+      for (int k = 0; k < kLpGroups / 4; ++k) {
+        const int j = 4 * k + (tid & 3);
         const uint32_t o = sh.group[j];
-        r += o > mine || (o == mine && j < tid);
+        r += o > group_max || (o == group_max && j < mine_at);
       }
-      if (r == n - 1) sh.bound = static_cast<unsigned long long>(mine) << 32;
+      r += __shfl_xor_sync(0xFFFFFFFFu, r, 1);
+      r += __shfl_xor_sync(0xFFFFFFFFu, r, 2);
+      if (r == n - 1 && (tid & 3) == 0) sh.bound = static_cast<unsigned long long>(group_max) << 32;
     }
     __syncthreads();
     uint64_t bound = sh.bound;
@@ -328,6 +354,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
     __syncthreads();
     const int nf = sh.n_flag;
     const int steps = (v1 - v0 + kLpThreads - 1) / kLpThreads;
+    float bound_value = key_value(static_cast<uint32_t>(bound >> 32));
     auto offer = [&](float x, int i) {
       const uint64_t k = lp_key(x, i);
       if (k >= bound) {
@@ -335,15 +362,22 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
         if (at < kMaxCand) sh.cand[at] = k;
       }
     };
+    const int flag_bits = nf > 1 ? 32 - __clz(nf - 1) : 0;  // their number rounded up to a power of two
     int nc;
     for (;;) {
-      for (int w = tid; w < nf * steps; w += kLpThreads) {
-        const int j = v0 + sh.flagged[w % nf] + (w / nf) * kLpThreads;
+      for (int w = tid; w < steps << flag_bits; w += kLpThreads) {
+        const int f = w & ((1 << flag_bits) - 1);
+        const int j = f < nf ? v0 + sh.flagged[f] + (w >> flag_bits) * kLpThreads : v1;
         if (j < v1) {
           float x[kN];
           lp_unpack<T>(__ldg(vec + j), x);
+          uint32_t hits = 0;  // (a NaN goes on to its key)
 #pragma unroll
-          for (int i = 0; i < kN; ++i) offer(x[i], lead + j * kN + i);
+          for (int i = 0; i < kN; ++i) hits |= x[i] < bound_value ? 0u : 1u << i;
+          for (; hits; hits &= hits - 1) {
+            const int i = lead + j * kN + __ffs(hits) - 1;
+            offer(to_float(row[i]), i);
+          }
         }
       }
       if (tid < singles) offer(to_float(row[single_index(tid)]), single_index(tid));
@@ -359,22 +393,20 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
       }
       __syncthreads();
       bound = sh.bound;
+      bound_value = key_value(static_cast<uint32_t>(bound >> 32));
       if (tid == 0) sh.n_cand = 0;
+      for (int i = tid; i < kMaxCand; i += kLpThreads) sh.cand[i] = 0;
       __syncthreads();
     }
     for (int i = tid; i < nc; i += kLpThreads) {
       const uint64_t k = sh.cand[i];
-      int r = 0;
-      for (int j = 0; j < nc; ++j) r += sh.cand[j] > k;
+      const int r = count_above(sh.cand, nc, k);
       if (r < n) {
         const uint32_t a = mapa(smem_u32(&sh.top[rank * n + r]), 0);
         asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(k) : "memory");
       }
     }
-    for (int r = nc + tid; r < n; r += kLpThreads) {  // (a slice of fewer than n elements)
-      const uint32_t a = mapa(smem_u32(&sh.top[rank * n + r]), 0);
-      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(0ull) : "memory");
-    }
+    // (a slice of fewer than n elements leaves zeros)
   }
 
   if (C == 1) __syncthreads();
@@ -383,18 +415,20 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
   // one warp-wide join of all partial statistics, by every warp alike
   LpStat all = {kMasked, 0.0f, 0.0f};
   int total = 0;
-  for (int i = lane; i < static_cast<int>(C) * kLpWarps; i += 32) {
-    lp_join(all, (&sh.stat[0][0])[i], c);
-    total += (&sh.count[0][0])[i];
+  static_assert(kLpMaxCluster * kLpWarps <= 64, "");
+  if (lane < static_cast<int>(C) * kLpWarps) {
+    all = (&sh.stat[0][0])[lane];
+    total = (&sh.count[0][0])[lane];
+    if (lane + 32 < static_cast<int>(C) * kLpWarps) {
+      const LpStat b = (&sh.stat[0][0])[lane + 32];
+      total += (&sh.count[0][0])[lane + 32];
+      const float m = fmaxf(all.m, b.m), da = (all.m - m) * c, db = (b.m - m) * c, fa = ex2(da), fb = ex2(db);
+      all.u = fa * fmaf(all.s, da, all.u) + fb * fmaf(b.s, db, b.u);
+      all.s = fa * all.s + fb * b.s;
+      all.m = m;
+    }
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    LpStat b;
-    b.m = __shfl_xor_sync(0xFFFFFFFFu, all.m, o);
-    b.s = __shfl_xor_sync(0xFFFFFFFFu, all.s, o);
-    b.u = __shfl_xor_sync(0xFFFFFFFFu, all.u, o);
-    lp_join(all, b, c);
-  }
+  lp_join_warp(all, c);
   total = __reduce_add_sync(0xFFFFFFFFu, total);
   const bool empty = all.m <= kMasked && all.s == all.s;  // (a NaN keeps the statistics' NaN)
   const float log_z = logf(all.s);
@@ -411,14 +445,11 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const Logpro
     }
   }
   if (n > 0) {
-    const int have = C == 1 ? n : static_cast<int>(C) * n;
+    // the CTAs' winners, each ranked among all (one CTA's are in order already)
+    const int have = static_cast<int>(C) * n;
     for (int i = tid; i < have; i += kLpThreads) {
       const uint64_t k = sh.top[i];
-      int r = i;
-      if (C > 1) {
-        r = 0;
-        for (int j = 0; j < have; ++j) r += sh.top[j] > k;
-      }
+      const int r = C > 1 ? count_above(sh.top, have, k) : i;
       if (r < n && k != 0) {
         const int64_t o = t * n + r;
         p.top_ids[o] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));

@@ -73,6 +73,15 @@ __device__ __forceinline__ void two_sum(float& hi, float& lo, float b, float c) 
   hi = s;
 }
 
+// a / b from r = 1 / b rounded to nearest: the quotient a r, its remainder by
+// a fused operation and one correction give the correctly rounded quotient as
+// long as nothing leaves the normal range (P. Markstein, IBM J. Res. Dev. 34,
+// 1990); b in [1, 512] here, so a from 2^-100 on (0 is exact too).
+__device__ __forceinline__ float divide_by(float a, float b, float r) {
+  const float q = __fmul_rn(a, r);
+  return __fmaf_rn(__fmaf_rn(-q, b, a), r, q);
+}
+
 // The largest of the token's lanes' values.
 template <int kL>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
@@ -154,11 +163,28 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
       sum = __fadd_rn(hi, lo);
     }
     if (!by_logit) {
-      const bool divide = !p.sigmoid && sum > 0.0f;
+      if (!p.sigmoid && sum > 0.0f) {  // (no sum: every score is 0)
+        const float inv = __fdiv_rn(1.0f, sum);
+        float least = 1.0f;
+#pragma unroll
+        for (int i = 0; i < S; ++i) least = fminf(least, score[i] > 0.0f ? score[i] : 1.0f);
+        if (least >= 0x1p-100f) {
+#pragma unroll
+          for (int i = 0; i < S; ++i) score[i] = divide_by(score[i], sum, inv);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < S; ++i) {  // (registers are not indexed: the first moves to the end)
+            const float q = __fdiv_rn(score[0], sum);
+#pragma unroll
+            for (int j = 0; j + 1 < S; ++j) score[j] = score[j + 1];
+            score[S - 1] = q;
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         const int e = e0 + i;
-        float s = divide ? __fdiv_rn(score[i], sum) : score[i];  // (no sum: every score is 0)
+        float s = score[i];
         if (p.bias && e < p.E) s = __fadd_rn(s, __ldg(p.bias + e));
         key[i] = e < p.E ? order_key(s) : 0u;
       }
