@@ -223,17 +223,19 @@ struct AttnLayout {
   }
 };
 
-// kN: tiles of 8 query rows that a warp serves.
-template <int kDim, int kN>
+// kN: tiles of 8 query rows that a warp serves; kRes: CTAs per SM (registers, shared memory).
+template <int kDim, int kN, int kRes>
 struct AttnCfg {
   using L = AttnLayout<kDim>;
   static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = 8 * kN;
-  static constexpr int kResident = kDim <= 128 && kN <= 2 ? 2 : 1;  // CTAs per SM (registers, shared memory)
   static constexpr bool kQInRegs = kN == 1;                         // a warp keeps its queries in registers
+  // with 8 warps per SM a strip is scored while the one before is weighed: twice the independent work (32 rows leave
+  // no registers for it)
+  static constexpr bool kAhead = kRes == 1 && kN < 4;
   static constexpr int kStageBytes = 2 * L::kStripBytes + 16;       // K, V, the two scales
-  static constexpr int kStages0 = (kResident == 2 ? 102400 : 204800) / (kWarps * kStageBytes);
+  static constexpr int kStages0 = (kRes == 2 ? 102400 : 204800) / (kWarps * kStageBytes);
   static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kQBytes = kQInRegs ? 0 : kN * L::kSteps * 32 * 8;
@@ -250,10 +252,9 @@ struct AttnPlace {
   int item;           // number of the item within the sequence
 };
 
-template <int kDim, bool kInt8, int kN>
-__global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>::kResident)
-    kv_attention_kernel(const KvAttnParams p) {
-  using C = AttnCfg<kDim, kN>;
+template <int kDim, bool kInt8, int kN, int kRes>
+__global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_attention_kernel(const KvAttnParams p) {
+  using C = AttnCfg<kDim, kN, kRes>;
   using L = AttnLayout<kDim>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ AttnPlace places[3];  // the item being read and the next one by turns; the share's begin
@@ -594,41 +595,88 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
     const int tokens_all = n - p.q_len + 1;                          // every row sees those before this one
     const int tokens_low = p.window > 0 ? max(0, n - p.window) : 0;  // ... from this one on
 
+    auto after = [](int stage) { return stage + 1 == C::kStages ? 0 : stage + 1; };
+    auto before = [](int stage) { return stage == 0 ? C::kStages - 1 : stage - 1; };
+    // S^T += K Q^T of two k-steps of a strip; w: its K words of a block, of rows g and g + 8
+    auto score = [&](const uint32_t (&w)[2][L::kWords], int blk, int s, float (&sc)[kN][4]) {
+      uint32_t a[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        a[e][0] = codes2_lo<kInt8>(w[0][s + e]);
+        a[e][1] = codes2_lo<kInt8>(w[1][s + e]);
+        a[e][2] = codes2_hi<kInt8>(w[0][s + e]);
+        a[e][3] = codes2_hi<kInt8>(w[1][s + e]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < kN; ++nt) {
+        const int pair = (blk * L::kWords + s) / 2;
+        uint4 b;
+        if constexpr (C::kQInRegs) b = qr[pair];
+        else b = lds128(q_base + ((nt * (L::kSteps / 2) + pair) * 32 + lane) * 16);
+        mma_f16(sc[nt], a[0], b.x, b.y);
+        mma_f16(sc[nt], a[1], b.z, b.w);
+      }
+    };
+    auto k_load = [&](uint32_t kb, int blk, uint32_t (&w)[2][L::kWords]) {
+      L::k_words(kb, k_place, 0, blk, w[0]);
+      L::k_words(kb, k_place, 1, blk, w[1]);
+    };
+    // out^T += V^T w^T of one V word's dims
+    auto weigh = [&](const uint32_t (&w)[4][L::kVWords], int blk, int k, const uint32_t (&pb)[kN][2]) {
+      const uint32_t lo[2] = {__byte_perm(w[0][k], w[1][k], 0x5140), __byte_perm(w[0][k], w[1][k], 0x7362)};
+      const uint32_t hi[2] = {__byte_perm(w[2][k], w[3][k], 0x5140), __byte_perm(w[2][k], w[3][k], 0x7362)};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t a[4] = {codes2_lo<kInt8>(lo[j]), codes2_hi<kInt8>(lo[j]), codes2_lo<kInt8>(hi[j]),
+                               codes2_hi<kInt8>(hi[j])};
+#pragma unroll
+        for (int nt = 0; nt < kN; ++nt) mma_f16(acc[nt][(blk * L::kVWords + k) * 2 + j], a, pb[nt][0], pb[nt][1]);
+      }
+    };
+    auto v_load = [&](uint32_t vb, int blk, int left, uint32_t (&w)[4][L::kVWords]) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) L::v_words(vb, v_place, c, blk, w[c]);
+      if (left < 16) {  // past the end: whatever lies there counts nothing
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (2 * t + (c & 1) + (c >> 1) * 8 >= left) {
+#pragma unroll
+            for (int k = 0; k < L::kVWords; ++k) w[c][k] = 0u;
+          }
+      }
+    };
     // this warp's strips of the segment: begin + warp + k kWarps
     int tok = tok0 + (((begin + warp - at) & (C::kWarps - 1)) << 4);
     const int tok_end = tok0 + ((seg_end - at) << 4);
-    for (; tok < tok_end; tok += C::kWarps * 16) {
+    bool fresh = true;
+    float sc[kN][4];  // tokens g (0, 1) and g + 8 (2, 3) by rows 2t and 2t + 1
+    if (C::kAhead && tok < tok_end) {
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-      __syncwarp();  // the strip is there, and every lane is past the stage read last
-      issue(stage == 0 ? C::kStages - 1 : stage - 1);
-      const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + L::kStripBytes;
-      float sc[kN][4];  // tokens g (0, 1) and g + 8 (2, 3) by rows 2t and 2t + 1
+      __syncwarp();
 #pragma unroll
       for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
 #pragma unroll
       for (int blk = 0; blk < L::kBlocks; ++blk) {
         uint32_t w[2][L::kWords];
-        L::k_words(kb, k_place, 0, blk, w[0]);
-        L::k_words(kb, k_place, 1, blk, w[1]);
+        k_load(ring + stage * C::kStageBytes, blk, w);
 #pragma unroll
-        for (int s = 0; s < L::kWords; s += 2) {
-          uint32_t a[2][4];
+        for (int s = 0; s < L::kWords; s += 2) score(w, blk, s, sc);
+      }
+    }
+    for (; tok < tok_end; tok += C::kWarps * 16) {
+      const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + L::kStripBytes;
+      if (!C::kAhead) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+        __syncwarp();  // the strip is there, and every lane is past the stage read last
+        issue(before(stage));
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            a[e][0] = codes2_lo<kInt8>(w[0][s + e]);
-            a[e][1] = codes2_lo<kInt8>(w[1][s + e]);
-            a[e][2] = codes2_hi<kInt8>(w[0][s + e]);
-            a[e][3] = codes2_hi<kInt8>(w[1][s + e]);
-          }
+        for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
 #pragma unroll
-          for (int nt = 0; nt < kN; ++nt) {
-            const int pair = (blk * L::kWords + s) / 2;
-            uint4 b;
-            if constexpr (C::kQInRegs) b = qr[pair];
-            else b = lds128(q_base + ((nt * (L::kSteps / 2) + pair) * 32 + lane) * 16);
-            mma_f16(sc[nt], a[0], b.x, b.y);
-            mma_f16(sc[nt], a[1], b.z, b.w);
-          }
+        for (int blk = 0; blk < L::kBlocks; ++blk) {
+          uint32_t w[2][L::kWords];
+          k_load(kb, blk, w);
+#pragma unroll
+          for (int s = 0; s < L::kWords; s += 2) score(w, blk, s, sc);
         }
       }
       float ks, vs;
@@ -636,30 +684,27 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
       const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
       const float inv_vs = attn_ex2(-lv);
       const bool masked = tok + 16 > tokens_all || tok < tokens_low;
-      // exponents against the running maxima; where they are masked or too high, from the scores again
-      auto factor = [&](int nt, int h) -> float {
-        return (C::kQInRegs ? rs[h] : row_scale[nt * 8 + 2 * t + h]) * ks;
-      };
-      float x[kN][4];
-      bool again = masked;
-      if (!masked) {
-        float high = -1.0f;
+      // Exponents against the running maxima, in the scores' place; against 0 while the warp has seen no strip that
+      // every row sees some of (`fresh`: a row's first maximum is only known then).  Where they are masked, too high
+      // or fresh, the maxima are taken and the exponents made again.
+      float high = -1.0f;
 #pragma unroll
-        for (int nt = 0; nt < kN; ++nt) {
-          const float f0 = factor(nt, 0), f1 = factor(nt, 1), b0 = lv - m[nt][0], b1 = lv - m[nt][1];
-          x[nt][0] = fmaf(sc[nt][0], f0, b0), x[nt][1] = fmaf(sc[nt][1], f1, b1);
-          x[nt][2] = fmaf(sc[nt][2], f0, b0), x[nt][3] = fmaf(sc[nt][3], f1, b1);
-          high = fmaxf(high, fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3])));
+      for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float f = (C::kQInRegs ? rs[h] : row_scale[nt * 8 + 2 * t + h]) * ks;
+          const float base = fresh ? lv : lv - m[nt][h];
+          sc[nt][h] = fmaf(sc[nt][h], f, base);
+          sc[nt][2 + h] = fmaf(sc[nt][2 + h], f, base);
+          high = fmaxf(high, fmaxf(sc[nt][h], sc[nt][2 + h]));
         }
-        again = __any_sync(0xFFFFFFFFu, high > kAttnSlack);
-      }
-      if (again) {
+      if (masked || fresh || __any_sync(0xFFFFFFFFu, high > kAttnSlack)) {
 #pragma unroll
         for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float f = factor(nt, h);
-            float r0 = fmaf(sc[nt][h], f, lv), r1 = fmaf(sc[nt][2 + h], f, lv);
+            const float base = fresh ? 0.0f : m[nt][h];
+            float r0 = sc[nt][h] + base, r1 = sc[nt][2 + h] + base;
             if (masked) {
               const int row = min(row0 + nt * 8 + 2 * t + h, rows - 1);
               const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
@@ -679,49 +724,51 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
               acc[nt][j][h] *= fall;
               acc[nt][j][2 + h] *= fall;
             }
-            x[nt][h] = r0 - mn;
-            x[nt][2 + h] = r1 - mn;
+            sc[nt][h] = r0 - mn;
+            sc[nt][2 + h] = r1 - mn;
           }
+        fresh = fresh && tok < tokens_low;
       }
       uint32_t pb[kN][2];
 #pragma unroll
       for (int nt = 0; nt < kN; ++nt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = attn_ex2(x[nt][e]);
-        sum[nt][0] = fmaf(x[nt][0] + x[nt][2], inv_vs, sum[nt][0]);
-        sum[nt][1] = fmaf(x[nt][1] + x[nt][3], inv_vs, sum[nt][1]);
-        pb[nt][0] = transpose8x8(pack_f16(x[nt][0], x[nt][1]));
-        pb[nt][1] = transpose8x8(pack_f16(x[nt][2], x[nt][3]));
+        for (int e = 0; e < 4; ++e) sc[nt][e] = attn_ex2(sc[nt][e]);
+        sum[nt][0] = fmaf(sc[nt][0] + sc[nt][2], inv_vs, sum[nt][0]);
+        sum[nt][1] = fmaf(sc[nt][1] + sc[nt][3], inv_vs, sum[nt][1]);
+        pb[nt][0] = transpose8x8(pack_f16(sc[nt][0], sc[nt][1]));
+        pb[nt][1] = transpose8x8(pack_f16(sc[nt][2], sc[nt][3]));
       }
-      const int left = n - tok;  // tokens of the sequence in this strip
+      if constexpr (C::kAhead) {
+        // the next strip's scores along with this one's sums (past the last strip: of no use, and none is made)
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 3) : "memory");
+        __syncwarp();  // the next strip is there, and every lane is past the stage read last
+        issue(before(stage));
+        const uint32_t next_kb = ring + after(stage) * C::kStageBytes;
 #pragma unroll
-      for (int blk = 0; blk < L::kBlocks; ++blk) {
-        uint32_t w[4][L::kVWords];
+        for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+        static_assert(L::kWords == 2 * L::kVWords, "a V word for every two K words");
 #pragma unroll
-        for (int c = 0; c < 4; ++c) L::v_words(vb, v_place, c, blk, w[c]);
-        if (left < 16) {  // past the end: whatever lies there counts nothing
+        for (int blk = 0; blk < L::kBlocks; ++blk) {
+          uint32_t wk[2][L::kWords], wv[4][L::kVWords];
+          k_load(next_kb, blk, wk);
+          v_load(vb, blk, n - tok, wv);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (2 * t + (c & 1) + (c >> 1) * 8 >= left) {
-#pragma unroll
-              for (int k = 0; k < L::kVWords; ++k) w[c][k] = 0u;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < L::kVWords; ++k) {
-          const uint32_t lo[2] = {__byte_perm(w[0][k], w[1][k], 0x5140), __byte_perm(w[0][k], w[1][k], 0x7362)};
-          const uint32_t hi[2] = {__byte_perm(w[2][k], w[3][k], 0x5140), __byte_perm(w[2][k], w[3][k], 0x7362)};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t a[4] = {codes2_lo<kInt8>(lo[j]), codes2_hi<kInt8>(lo[j]), codes2_lo<kInt8>(hi[j]),
-                                   codes2_hi<kInt8>(hi[j])};
-#pragma unroll
-            for (int nt = 0; nt < kN; ++nt)
-              mma_f16(acc[nt][(blk * L::kVWords + k) * 2 + j], a, pb[nt][0], pb[nt][1]);
+          for (int k = 0; k < L::kVWords; ++k) {
+            score(wk, blk, 2 * k, sc);
+            weigh(wv, blk, k, pb);
           }
         }
+      } else {
+#pragma unroll
+        for (int blk = 0; blk < L::kBlocks; ++blk) {
+          uint32_t w[4][L::kVWords];
+          v_load(vb, blk, n - tok, w);
+#pragma unroll
+          for (int k = 0; k < L::kVWords; ++k) weigh(w, blk, k, pb);
+        }
       }
-      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+      stage = after(stage);
     }
 
     // ---- the segment's end: join the warps ----
@@ -734,7 +781,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN>::kThreads, AttnCfg<kDim, kN>
         if (g == 0) ml[warp * C::kRows + nt * 8 + 2 * t + h] = make_float2(m[nt][h], sum[nt][h]);
       }
     // the stage that is neither being read nor being filled, the one before the next: 8 rows of dims, fp32
-    const int idle = (warp * C::kStages + (stage == 0 ? C::kStages - 1 : stage - 1)) * C::kStageBytes;
+    const int idle = (warp * C::kStages + before(stage)) * C::kStageBytes;
     if (lane == 0) free_stage[warp] = idle;
     // 16-byte cell of word k, thread row g2 and query row r: places change by row, against bank conflicts
     auto cell = [](int r, int k, int g2) -> int { return ((r * (L::kTiles / 2) + k) * 8 + (g2 ^ (r & 6))) * 4; };

@@ -98,25 +98,21 @@ class KvCache8:
         scales = [torch.zeros(shape[:2], dtype=_F32, device=device) for _ in range(2)]
         return cls(*codes, *scales, fmt=fmt)
 
-    def _check_sequences(self, block_table: torch.Tensor, seq_lens: torch.Tensor) -> tuple[int, int]:
-        shape, index = block_table.shape, self._index
-        if block_table.dtype is not _I32 or len(shape) != 2 or not block_table.is_contiguous() or \
-                block_table.get_device() != index:
-            raise ValueError("block_table must be a contiguous int32 [B, max_blocks] tensor on the cache's device")
-        B, max_blocks = shape
-        if seq_lens.dtype is not _I32 or seq_lens.shape != (B,) or not seq_lens.is_contiguous() or \
-                seq_lens.get_device() != index:
-            raise ValueError(f"seq_lens must be a contiguous int32 [{B}] tensor on the cache's device")
-        return B, max_blocks
-
     def append(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                cu_new: torch.Tensor | None = None, pdl: bool = True) -> None:
         """Appends k, v (bf16 or f16 [T, kv_heads, head_dim], heads contiguous,
         any token stride that is a multiple of 8) to B sequences: T / B tokens
         each, or tokens cu_new[b] .. cu_new[b + 1] (int32 [B + 1]) to sequence
         b.  ``seq_lens``: the lengths with the new tokens."""
-        B, max_blocks = self._check_sequences(block_table, seq_lens)
-        H, D, index = self.kv_heads, self.head_dim, self._index
+        index, shape = self._index, block_table.shape
+        if block_table.dtype is not _I32 or len(shape) != 2 or not block_table.is_contiguous() or \
+                block_table.get_device() != index:
+            raise ValueError("block_table must be a contiguous int32 [B, max_blocks] tensor on the cache's device")
+        B, max_blocks = shape
+        if seq_lens.dtype is not _I32 or seq_lens.numel() != B or not seq_lens.is_contiguous() or \
+                seq_lens.get_device() != index:
+            raise ValueError(f"seq_lens must be a contiguous int32 [{B}] tensor on the cache's device")
+        H, D = self.kv_heads, self.head_dim
         shape, dtype, ks, vs = k.shape, k.dtype, k.stride(), v.stride()
         if (dtype is not _BF16 and dtype is not _F16) or v.dtype is not dtype or len(shape) != 3 or shape[1] != H or \
                 shape[2] != D or v.shape != shape or k.get_device() != index or v.get_device() != index or \
@@ -124,7 +120,7 @@ class KvCache8:
             raise ValueError(f"k and v must be bf16 or f16 [T, {H}, {D}] tensors of one type on the cache's device "
                              "with contiguous heads")
         T = shape[0]
-        if cu_new is not None and (cu_new.dtype is not _I32 or cu_new.shape != (B + 1,) or
+        if cu_new is not None and (cu_new.dtype is not _I32 or cu_new.numel() != B + 1 or
                                    not cu_new.is_contiguous() or cu_new.get_device() != index):
             raise ValueError(f"cu_new must be a contiguous int32 [{B + 1}] tensor on the cache's device")
         if T == 0 or B == 0:
@@ -148,8 +144,15 @@ class KvCache8:
         that sees none gives zeros.  ``sm_scale`` defaults to 1 /
         sqrt(head_dim); ``lse``: fp32 [B, q_len, heads] to receive the natural
         log of the softmax's sums.  Returns ``out``."""
-        B, max_blocks = self._check_sequences(block_table, seq_lens)
-        D, index = self.head_dim, self._index
+        index, shape = self._index, block_table.shape
+        if block_table.dtype is not _I32 or len(shape) != 2 or not block_table.is_contiguous() or \
+                block_table.get_device() != index:
+            raise ValueError("block_table must be a contiguous int32 [B, max_blocks] tensor on the cache's device")
+        B, max_blocks = shape
+        if seq_lens.dtype is not _I32 or seq_lens.numel() != B or not seq_lens.is_contiguous() or \
+                seq_lens.get_device() != index:
+            raise ValueError(f"seq_lens must be a contiguous int32 [{B}] tensor on the cache's device")
+        D = self.head_dim
         shape, dtype = q.shape, q.dtype
         if (dtype is not _BF16 and dtype is not _F16) or len(shape) != 4 or shape[0] != B or shape[3] != D or \
                 q.get_device() != index:
@@ -159,15 +162,18 @@ class KvCache8:
             out = torch.empty(shape, dtype=dtype, device=self.device)
         elif out.dtype is not dtype or out.shape != shape or out.get_device() != index:
             raise ValueError("out must have q's shape, type and device")
-        ldq, ldo = self._token_stride(q.stride(), shape, "q"), self._token_stride(out.stride(), shape, "out")
-        if lse is not None and (lse.dtype is not _F32 or lse.shape != shape[:3] or not lse.is_contiguous() or
+        ldq = heads * D if q.is_contiguous() else self._token_stride(q.stride(), shape, "q")
+        ldo = heads * D if out.is_contiguous() else self._token_stride(out.stride(), shape, "out")
+        if lse is not None and (lse.dtype is not _F32 or lse.numel() != B * n * heads or not lse.is_contiguous() or
                                 lse.get_device() != index):
             raise ValueError(f"lse must be a contiguous fp32 [{B}, {n}, {heads}] tensor on the cache's device")
         if B == 0:
             return out
         stream = _raw_stream(index)
         if workspace is None:
-            workspace = attention_workspace(self.device, D, stream)
+            workspace = _workspaces.get((index, stream, D))
+            if workspace is None:
+                workspace = attention_workspace(self.device, D, stream)
         status = _attend(self._handle, q.data_ptr(), ldq, 0 if dtype is _BF16 else 1, heads, n,
                          block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), B,
                          self._sm_scale if sm_scale is None else sm_scale, window, out.data_ptr(), ldo,
