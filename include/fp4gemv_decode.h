@@ -72,7 +72,8 @@ typedef struct {
  * at positions outside the table's row, or on a page id outside [0,
  * num_blocks), are not stored and raise FP4GEMV_ERR_BAD_INDEX.
  * Shapes: 1 <= B <= FP4GEMV_KV_MAX_BATCH, T >= 0 (with cu_new = NULL a
- *   multiple of B), max_blocks >= 1. */
+ *   multiple of B), max_blocks >= 1, max_blocks * block_size and T at most
+ *   2^30. */
 fp4gemv_status fp4gemv_kv_append(const fp4gemv_kv_cache* cache, const void* k, int64_t ldk, const void* v, int64_t ldv,
                                  int dtype, int T, const int32_t* cu_new, const int32_t* block_table, int max_blocks,
                                  const int32_t* seq_lens, int B, int pdl, cudaStream_t stream);

@@ -42,7 +42,8 @@ fp4gemv_status fp4gemv_kv_append(const fp4gemv_kv_cache* cache, const void* k, i
   const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
   if (T < 0 || B < 1 || max_blocks < 1 || ldk < width || ldv < width) return FP4GEMV_ERR_INVALID_ARG;
   if (!cu_new && T % B != 0) return FP4GEMV_ERR_INVALID_ARG;
-  if (B > FP4GEMV_KV_MAX_BATCH) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+  if (B > FP4GEMV_KV_MAX_BATCH || static_cast<int64_t>(max_blocks) * cache->block_size > (1ll << 30) || T > (1 << 30))
+    return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
   if (crooked || !aligned(k, 16) || !aligned(v, 16) || ldk % 8 != 0 || ldv % 8 != 0 || !aligned(cu_new, 4) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4))
     return FP4GEMV_ERR_MISALIGNED;
@@ -71,7 +72,7 @@ fp4gemv_status fp4gemv_kv_append(const fp4gemv_kv_cache* cache, const void* k, i
   p.max_blocks = max_blocks;
   p.num_blocks = cache->num_blocks;
   p.heads = cache->kv_heads;
-  p.block = cache->block_size;
+  p.block_log2 = block_log2(cache->block_size);
   p.dim = cache->head_dim;
   fp4::count_launch();
   return from_cuda(fp4::launch_kv_append(p, cache->format == FP4GEMV_KV_INT8, dtype == FP4GEMV_F16, pdl, stream));
