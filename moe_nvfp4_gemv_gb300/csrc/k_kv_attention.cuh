@@ -303,106 +303,117 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
   };
   auto rounds = [](int x) { return (x + C::kWarps - 1) / C::kWarps * C::kWarps; };  // whole rounds of the warps
 
-  // ---- the plan, by the first warp; lens by all threads where there are many ----
+  // ---- the plan, by the first warp (a lane per sequence, in rounds of 32); lens by all threads where there are many ----
   {
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
     const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.block_log2;
-    const int step = p.B <= 32 ? 32 : C::kThreads;
-    if (warp == 0 || p.B > 32)
-      for (int b = tid; b < p.B; b += step) {
-        const int raw = __ldg(p.lens + b);
-        const int n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
-        if (n != raw && blockIdx.x == 0) raise_error(p.err, FP4_ERR_BADIDX);
-        tokens[b] = n;
-      }
-    if (p.B > 32) __syncthreads();
+    auto length = [&](int b) -> int {
+      const int raw = __ldg(p.lens + b);
+      const int n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
+      if (n != raw && blockIdx.x == 0) raise_error(p.err, FP4_ERR_BADIDX);
+      return n;
+    };
+    const bool few = p.B <= 32;
+    if (!few) {
+      for (int b = tid; b < p.B; b += C::kThreads) tokens[b] = length(b);
+      __syncthreads();
+    }
     if (warp == 0) {
       const int ctas = static_cast<int>(gridDim.x);
+      int n0 = 0;  // the lane's sequence, where there are few
+      if (few && lane < p.B) {
+        n0 = length(lane);
+        tokens[lane] = n0;
+      }
+      auto tokens_of = [&](int b) -> int { return few ? n0 : b < p.B ? tokens[b] : 0; };
+      auto strips_at = [&](int b) -> int {
+        const int n = tokens_of(b);
+        return n > 0 ? strips_of(n) : 0;
+      };
       int total = 0, alive = 0;
-      __syncwarp();
-      for (int b = lane; b < p.B + lane; b += 32) {  // (all lanes alike: rounds of 32 sequences)
-        const int n = b < p.B ? tokens[b] : 0;
-        total += __reduce_add_sync(0xFFFFFFFFu, n > 0 ? strips_of(n) : 0);
-        alive += __popc(__ballot_sync(0xFFFFFFFFu, n > 0));
+      for (int b = lane; b < p.B + lane; b += 32) {  // (all lanes alike)
+        const int s = strips_at(b);
+        total += __reduce_add_sync(kAll, s);
+        alive += __popc(__ballot_sync(kAll, s > 0));
       }
       total *= items;
       alive *= items;
       // pieces per item, if those of the shortest of three lengths are no more than the CTAs
       int per = 0;
-      float inv_per = 0.0f;
       if (alive <= ctas) {
         const int even = div_up(total, ctas, p.inv_ctas);
-        for (int k = 0; k < 3 && per == 0; ++k) {
-          const int len = max(C::kWarps, rounds(even + (even * k >> 3)));
-          const float inv = __fdividef(1.0f, static_cast<float>(len));
-          int sum = 0;
-          for (int b = lane; b < p.B + lane; b += 32) {
-            const int n = b < p.B ? tokens[b] : 0;
-            sum += __reduce_add_sync(0xFFFFFFFFu, n > 0 ? div_up(strips_of(n), len, inv) : 0);
-          }
-          if (sum * items <= ctas) {
-            per = len;
-            inv_per = inv;
-          }
+        int len[3], sum[3] = {0, 0, 0};
+        float inv[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          len[k] = max(C::kWarps, rounds(even + (even * k >> 3)));
+          inv[k] = __fdividef(1.0f, static_cast<float>(len[k]));
         }
+        for (int b = lane; b < p.B + lane; b += 32) {
+          const int s = strips_at(b);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) sum[k] += __reduce_add_sync(kAll, div_up(s, len[k], inv[k]));
+        }
+#pragma unroll
+        for (int k = 2; k >= 0; --k)
+          if (sum[k] * items <= ctas) per = len[k];
       }
       const bool pieces = per > 0;
       const int lead = pieces ? 0 : kAttnItemCost;
       if (!pieces) per = max(rounds(div_up(total + alive * kAttnItemCost, ctas, p.inv_ctas)), C::kWarps);
-      // the sequences' places on both lines
-      int strips_end = 0, line_end = 0;
+      const float inv_per = __fdividef(1.0f, static_cast<float>(per));
+      auto on_line = [&](int s) -> int { return pieces ? div_up(s, per, inv_per) * per : s > 0 ? s + lead : 0; };
+      // the sequences' places on both lines; and the share's begin and end in strips, where the cuts fall
+      int strips_end = 0, line_end = 0, share[2] = {-1, -1};
+      AttnPlace place = {};
       for (int b = lane; b < p.B + lane; b += 32) {
-        const int n = b < p.B ? tokens[b] : 0;
-        const int s = n > 0 ? strips_of(n) : 0;
-        int len = pieces ? div_up(s, per, inv_per) * per : s + (n > 0 ? lead : 0);
+        const int s = strips_at(b), len = on_line(s);
         int sum = s, line = len;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o), v = __shfl_up_sync(0xFFFFFFFFu, line, o);
+          const int u = __shfl_up_sync(kAll, sum, o), v = __shfl_up_sync(kAll, line, o);
           if (lane >= o) sum += u, line += v;
         }
+        const int strips_here = strips_end + (sum - s) * items, line_here = line_end + (line - len) * items;
         if (b < p.B) {
-          strips_before[b] = strips_end + (sum - s) * items;
-          line_before[b] = line_end + (line - len) * items;
+          strips_before[b] = strips_here;
+          line_before[b] = line_here;
         }
-        strips_end += __shfl_sync(0xFFFFFFFFu, sum, 31) * items;
-        line_end += __shfl_sync(0xFFFFFFFFu, line, 31) * items;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int64_t at64 = static_cast<int64_t>(per) * (blockIdx.x + k);
+          if (len > 0 && at64 >= line_here && at64 < line_here + static_cast<int64_t>(len) * items) {
+            const int off = static_cast<int>(at64) - line_here;
+            const int item = div_up(off + 1, len, __fdividef(1.0f, static_cast<float>(len))) - 1;
+            // (a cut behind an item's last strip or in its cost: the strip that follows)
+            const int strip = max(off - item * len - lead, 0);
+            share[k] = strips_here + item * s + min(strip, s);
+            if (k == 0) {
+              place.b = b;
+              place.first = first_strip(tokens_of(b));
+              place.strips = s;
+              place.item = item;
+              place.strip = strip;  // (below s wherever the share is not empty, or pieces end)
+              place.head = p.row_tiles == 1 ? item : item / p.row_tiles;
+              place.tile = item - place.head * p.row_tiles;
+            }
+          }
+        }
+        strips_end += __shfl_sync(kAll, sum, 31) * items;
+        line_end += __shfl_sync(kAll, line, 31) * items;
       }
+      // (the one lane that met a cut writes it; cuts past the line's end: no strip follows)
+      if (share[0] >= 0) {
+        plan_words[0] = share[0];
+        places[0] = places[2] = place;
+      }
+      if (share[1] >= 0) plan_words[1] = share[1];
+      const bool met0 = __any_sync(kAll, share[0] >= 0), met1 = __any_sync(kAll, share[1] >= 0);
       if (lane == 0) {
         strips_before[p.B] = strips_end;
         line_before[p.B] = line_end;
-      }
-      __syncwarp();
-      // lane 0: the share's begin, lane 1: its end (both in strips), from the cuts of the line
-      if (lane < 2) {
-        const int64_t at64 = static_cast<int64_t>(per) * (blockIdx.x + lane);
-        int where = strips_end;
-        if (at64 < line_end) {
-          const int at = static_cast<int>(at64);
-          int lo = 0, hi = p.B - 1;  // the last sequence that starts at or before: never an empty one
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (line_before[mid] <= at) lo = mid;
-            else hi = mid - 1;
-          }
-          AttnPlace c;
-          const int n = tokens[lo];
-          c.b = lo;
-          c.first = first_strip(n);
-          c.strips = strips_of(n);
-          const int len = pieces ? div_up(c.strips, per, inv_per) * per : c.strips + lead, off = at - line_before[lo];
-          c.item = div_up(off + 1, len, __fdividef(1.0f, static_cast<float>(len))) - 1;
-          // (a cut behind an item's last strip or in its cost: the strip that follows)
-          int strip = max(off - c.item * len - lead, 0);
-          where = strips_before[lo] + c.item * c.strips + min(strip, c.strips);
-          if (lane == 0) {
-            c.strip = strip;  // (below c.strips wherever the share is not empty, or pieces end)
-            c.head = p.row_tiles == 1 ? c.item : c.item / p.row_tiles;
-            c.tile = c.item - c.head * p.row_tiles;
-            places[0] = places[2] = c;
-          }
-        }
-        plan_words[lane] = where;
-      } else if (lane == 2) {
+        if (!met0) plan_words[0] = strips_end;
+        if (!met1) plan_words[1] = strips_end;
         plan_words[2] = per;
         plan_words[3] = lead;
         plan_words[4] = pieces;

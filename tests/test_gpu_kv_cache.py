@@ -436,3 +436,35 @@ def test_refusals(kv, fp4):
     # nothing to do is no error
     cache.append(k[:0], k[:0], t, n)
     assert cache.attend(q[:0], t[:0], n[:0]).shape == (0, 1, 4, 128)
+
+
+@pytest.mark.parametrize("heads", [8, 32])
+@pytest.mark.parametrize("lens", [[1 + 17 * i % 90 for i in range(70)], [600 - 8 * i for i in range(45)] + [0] * 5])
+def test_attention_more_items_than_sms(kv, heads, lens):
+    """head_dim 128 on its two-CTA form (more items than SMs), 2 and 8 rows per KV head; few rounds of 32 sequences."""
+    g = gen(len(lens))
+    table, pages = make_table(lens, 16, g)
+    c = scaled(random_cache(pages, 4, 16, 128, g, 1.0), "int8")
+    q = torch.randn(len(lens), 1, heads, 128, generator=g).to(torch.float16).to(DEV)
+    check_attention(kv, q, c, table, lens, "int8", "f16")
+    q = torch.randn(len(lens), 3, heads, 128, generator=g).to(torch.float16).to(DEV)  # 6 and 24 rows
+    check_attention(kv, q, c, table, lens, "int8", "f16")
+
+
+@pytest.mark.parametrize("B", [31, 32, 33, 64, 65, 200, 1024])
+def test_attention_batch_sizes(kv, B):
+    lens = [(7 * i) % 50 for i in range(B)]
+    g = gen(B)
+    table, pages = make_table(lens, 16, g)
+    c = scaled(random_cache(pages, 1, 16, 64, g, 1.0), "e4m3")
+    q = torch.randn(B, 1, 2, 64, generator=g).to(torch.bfloat16).to(DEV)
+    check_attention(kv, q, c, table, lens, "e4m3", "bf16")
+
+
+@pytest.mark.parametrize("heads", [1, 5, 8, 11])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_append_heads(kv, heads, fmt):
+    """Several heads per CTA, and a rest of them; the last of 300 sequences (a search of two rounds)."""
+    run_append(kv, fmt, "bf16", 16, heads, 128, [3, 16, 29], [1] * 3, heads, False)
+    run_append(kv, fmt, "bf16", 32, heads, 64, [0, 31, 64], [70, 1, 5], heads + 1, True)
+    run_append(kv, fmt, "f16", 16, heads, 64, [i % 20 for i in range(300)], [i % 4 for i in range(300)], heads + 2, True)
