@@ -126,7 +126,7 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   st = fp4::current_device_state(&err, &sms);
   if (st != FP4GEMV_OK) return st;
   if (workspace_bytes < fp4gemv_kv_attention_workspace_bytes(cache->head_dim)) return FP4GEMV_ERR_INVALID_ARG;
-  fp4::KvAttnParams p = {};
+  fp4::KvAttnTcParams p = {};
   p.k_codes = cache->k_codes;
   p.v_codes = cache->v_codes;
   p.k_scale = cache->k_scale;
@@ -152,9 +152,18 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   p.q_len = q_len;
   p.row_tiles = row_tiles;
   p.window = window;
+  p.unit = 1;
   p.f16 = dtype == FP4GEMV_F16;
   p.sm_scale = sm_scale;
   fp4::count_launch();
+  if (row_units == 4 && cache->head_dim == 128 && cache->format == FP4GEMV_KV_E4M3) {
+    const int64_t pages = static_cast<int64_t>(cache->num_blocks) * cache->kv_heads;
+    if (!fp4::encode_pages_128(&p.k_map, cache->k_codes, cache->block_size, pages) ||
+        !fp4::encode_pages_128(&p.v_map, cache->v_codes, cache->block_size, pages))
+      return FP4GEMV_ERR_CUDA;
+    p.unit = 8;  // tiles of 128 tokens are of whole pages
+    return from_cuda(fp4::launch_kv_attention_tc(p, sms, pdl, stream));
+  }
   return from_cuda(fp4::launch_kv_attention(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms, pdl,
                                             stream));
 }

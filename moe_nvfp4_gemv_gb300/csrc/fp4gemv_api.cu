@@ -19,6 +19,7 @@
 namespace fp4 {
 fp4gemv_status current_device_state(uint32_t** err, int* sms);  // (decode_launch.h)
 void count_launch();
+bool encode_pages_128(CUtensorMap* m, const void* base, int block_size, int64_t pages);
 
 // Per-device error state (one copy per device context of this library image):
 // the error word, then the wait limit the kernels' bounded waits use (see
@@ -174,6 +175,22 @@ namespace fp4 {
 // For the decode step's operators (decode_api.cu).
 fp4gemv_status current_device_state(uint32_t** err, int* sms) { return device_state(err, sms); }
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+bool encode_pages_128(CUtensorMap* m, const void* base, int block_size, int64_t pages) {
+  MapKey k;
+  std::memset(&k, 0, sizeof(k));
+  k.base = base;
+  k.dims[0] = 128;
+  k.dims[1] = static_cast<uint64_t>(block_size);
+  k.dims[2] = static_cast<uint64_t>(pages);
+  k.strides[0] = 128;
+  k.strides[1] = static_cast<uint64_t>(block_size) * 128;
+  k.box[0] = 128;
+  k.box[1] = static_cast<uint32_t>(block_size);
+  k.box[2] = 1;
+  k.rank = 3;
+  k.dtype = static_cast<int>(CU_TENSOR_MAP_DATA_TYPE_UINT8);
+  return encode_cached(m, k);
+}
 }  // namespace fp4
 
 namespace {

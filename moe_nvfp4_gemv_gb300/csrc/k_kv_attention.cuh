@@ -43,6 +43,7 @@
 // those the joined ones (counters that are left at zero).  Nothing waits on another CTA.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -69,12 +70,20 @@ struct KvAttnParams {
   int kv_heads, group, q_len, row_tiles;  // row tiles of 8 kN rows
   int window;
   int f16;             // element type of q and out
+  int unit;            // strips (a power of two): items start and are cut at its multiples
   int group_magic;     // ceil(2^16 / group): row / group = row group_magic >> 16 for the rows there are
   float inv_ctas;      // 1 / the grid's CTAs
   float sm_scale;
 };
 
+// ... of the kernel on the 5th-generation tensor core
+struct KvAttnTcParams : KvAttnParams {
+  CUtensorMap k_map;  // [num_blocks kv_heads][block_size][128] bytes, boxes of a page, 128-byte swizzle
+  CUtensorMap v_map;
+};
+
 constexpr int kAttnMaxRows = 32;  // rows of a row tile at most
+constexpr int kAttnRound = 8;     // strips of a round, one for each warp: shares are whole rounds
 constexpr int kAttnFan = 40;      // partials that one CTA joins at once
 constexpr int kAttnFan2 = 20;     // ... where the joined ones are joined again
 constexpr int kAttnItemCost = 16;  // an item's end, in strips
@@ -135,6 +144,334 @@ __device__ __forceinline__ uint32_t codes2_hi(uint32_t w) {
   }
   return h;
 }
+
+// An item and a place in it.
+struct AttnPlace {
+  int b, head, tile;  // sequence, KV head, row tile
+  int strip, strips;  // the place in strips; the item's number of strips
+  int first;          // the sequence's first strip that any query sees (its token / 16)
+  int item;           // number of the item within the sequence
+};
+
+// ceil(x / y), x + y below 2^31
+__device__ __forceinline__ int attn_div_up(int x, int y, float inv_y) {
+  if (x >= 1 << 24) return (x + y - 1) / y;
+  int q = static_cast<int>(static_cast<float>(x) * inv_y);  // (at most one off)
+  q -= q * y > x;
+  q += q * y + y <= x;
+  return q + (q * y < x);
+}
+// Of a sequence of n tokens: the first strip that any query sees (or the unit that holds it), and the strips from there
+// on; what strips take on the line.
+__device__ __forceinline__ int attn_first_strip(const KvAttnParams& p, int n) {
+  const int at = n - p.q_len;  // the first query's position
+  return p.window > 0 && at >= p.window ? ((at - p.window + 1) >> 4) & -p.unit : 0;
+}
+__device__ __forceinline__ int attn_strips_of(const KvAttnParams& p, int n) {
+  return ((n + 15) >> 4) - attn_first_strip(p, n);
+}
+
+__device__ __forceinline__ int attn_units(const KvAttnParams& p, int strips) { return (strips + p.unit - 1) & -p.unit; }
+
+// The plan, by the first warp (a lane per sequence, in rounds of 32; lens by
+// all threads where there are many).  For every sequence: its tokens, and what
+// the sequences before hold in strips and in length on the line.  The share:
+// begin, end (strips), strips per share, an item's cost, and whether items are
+// cut into pieces by themselves.  places[0] and [2]: the share's begin.
+template <int kThreads>
+__device__ __forceinline__ void attn_plan(const KvAttnParams& p, int* strips_before, int* line_before, int* tokens,
+                                          int* plan_words, AttnPlace* places) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int items = p.kv_heads * p.row_tiles;
+  auto whole = [](int x) { return (x + kAttnRound - 1) / kAttnRound * kAttnRound; };  // whole rounds
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.block_log2;
+  auto length = [&](int b) -> int {
+    const int raw = __ldg(p.lens + b);
+    const int n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
+    if (n != raw && blockIdx.x == 0) raise_error(p.err, FP4_ERR_BADIDX);
+    return n;
+  };
+  const bool few = p.B <= 32;
+  if (!few) {
+    for (int b = tid; b < p.B; b += kThreads) tokens[b] = length(b);
+    __syncthreads();
+  }
+  if (warp == 0) {
+    const int ctas = static_cast<int>(gridDim.x);
+    int n0 = 0;  // the lane's sequence, where there are few
+    if (few && lane < p.B) {
+      n0 = length(lane);
+      tokens[lane] = n0;
+    }
+    auto tokens_of = [&](int b) -> int { return few ? n0 : b < p.B ? tokens[b] : 0; };
+    auto strips_at = [&](int b) -> int {
+      const int n = tokens_of(b);
+      return n > 0 ? attn_strips_of(p, n) : 0;
+    };
+    int total = 0, alive = 0;
+    for (int b = lane; b < p.B + lane; b += 32) {  // (all lanes alike)
+      const int s = strips_at(b);
+      total += __reduce_add_sync(kAll, attn_units(p, s));
+      alive += __popc(__ballot_sync(kAll, s > 0));
+    }
+    total *= items;
+    alive *= items;
+    // pieces per item, if those of the shortest of three lengths are no more than the CTAs
+    int per = 0;
+    if (alive <= ctas) {
+      const int even = attn_div_up(total, ctas, p.inv_ctas);
+      int len[3], sum[3] = {0, 0, 0};
+      float inv[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        len[k] = max(kAttnRound, whole(even + (even * k >> 3)));
+        inv[k] = __fdividef(1.0f, static_cast<float>(len[k]));
+      }
+      for (int b = lane; b < p.B + lane; b += 32) {
+        const int s = strips_at(b);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sum[k] += __reduce_add_sync(kAll, attn_div_up(s, len[k], inv[k]));
+      }
+#pragma unroll
+      for (int k = 2; k >= 0; --k)
+        if (sum[k] * items <= ctas) per = len[k];
+    }
+    const bool pieces = per > 0;
+    const int lead = pieces ? 0 : kAttnItemCost;
+    if (!pieces) per = max(whole(attn_div_up(total + alive * kAttnItemCost, ctas, p.inv_ctas)), kAttnRound);
+    const float inv_per = __fdividef(1.0f, static_cast<float>(per));
+    auto on_line = [&](int s) -> int { return pieces ? attn_div_up(s, per, inv_per) * per : s > 0 ? attn_units(p, s) + lead : 0; };
+    // the sequences' places on both lines; and the share's begin and end in strips, where the cuts fall
+    int strips_end = 0, line_end = 0, share[2] = {-1, -1};
+    AttnPlace place = {};
+    for (int b = lane; b < p.B + lane; b += 32) {
+      const int s = strips_at(b), len = on_line(s);
+      int sum = s, line = len;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kAll, sum, o), v = __shfl_up_sync(kAll, line, o);
+        if (lane >= o) sum += u, line += v;
+      }
+      const int strips_here = strips_end + (sum - s) * items, line_here = line_end + (line - len) * items;
+      if (b < p.B) {
+        strips_before[b] = strips_here;
+        line_before[b] = line_here;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t at64 = static_cast<int64_t>(per) * (blockIdx.x + k);
+        if (len > 0 && at64 >= line_here && at64 < line_here + static_cast<int64_t>(len) * items) {
+          const int off = static_cast<int>(at64) - line_here;
+          const int item = attn_div_up(off + 1, len, __fdividef(1.0f, static_cast<float>(len))) - 1;
+          // (a cut behind an item's last strip or in its cost: the strip that follows)
+          const int strip = max(off - item * len - lead, 0);
+          share[k] = strips_here + item * s + min(strip, s);
+          if (k == 0) {
+            place.b = b;
+            place.first = attn_first_strip(p, tokens_of(b));
+            place.strips = s;
+            place.item = item;
+            place.strip = strip;  // (below s wherever the share is not empty, or pieces end)
+            place.head = p.row_tiles == 1 ? item : item / p.row_tiles;
+            place.tile = item - place.head * p.row_tiles;
+          }
+        }
+      }
+      strips_end += __shfl_sync(kAll, sum, 31) * items;
+      line_end += __shfl_sync(kAll, line, 31) * items;
+    }
+    // (the one lane that met a cut writes it; cuts past the line's end: no strip follows)
+    if (share[0] >= 0) {
+      plan_words[0] = share[0];
+      places[0] = places[2] = place;
+    }
+    if (share[1] >= 0) plan_words[1] = share[1];
+    const bool met0 = __any_sync(kAll, share[0] >= 0), met1 = __any_sync(kAll, share[1] >= 0);
+    if (lane == 0) {
+      strips_before[p.B] = strips_end;
+      line_before[p.B] = line_end;
+      if (!met0) plan_words[0] = strips_end;
+      if (!met1) plan_words[1] = strips_end;
+      plan_words[2] = per;
+      plan_words[3] = lead;
+      plan_words[4] = pieces;
+    }
+  }
+  __syncthreads();
+}
+
+// Sequences nobody visits: zeros, lse -inf.
+template <int kDim, int kThreads>
+__device__ __forceinline__ void attn_empty(const KvAttnParams& p, const int* tokens) {
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (tokens[b] > 0) continue;
+    const int heads = p.kv_heads * p.group;
+    for (int i = threadIdx.x; i < p.q_len * heads * (kDim / 8); i += kThreads) {
+      const int64_t row = i / (kDim / 8);
+      const int64_t tok = static_cast<int64_t>(b) * p.q_len + row / heads;
+      reinterpret_cast<uint4*>(p.out + tok * p.ldo + (row % heads) * kDim)[i % (kDim / 8)] = make_uint4(0, 0, 0, 0);
+      if (p.lse && i % (kDim / 8) == 0) p.lse[tok * heads + row % heads] = -__builtin_huge_valf();
+    }
+  }
+}
+
+// The place after an item: the next item's begin (there is one).
+__device__ __forceinline__ AttnPlace attn_next(const KvAttnParams& p, AttnPlace x, const int* strips_before,
+                                               const int* tokens) {
+  x.strip = 0;
+  ++x.item;
+  if (++x.tile == p.row_tiles) {
+    x.tile = 0;
+    if (++x.head == p.kv_heads) {
+      x.head = x.item = 0;
+      do ++x.b;
+      while (strips_before[x.b + 1] == strips_before[x.b]);
+      const int len = tokens[x.b];
+      x.first = attn_first_strip(p, len);
+      x.strips = attn_strips_of(p, len);
+    }
+  }
+  return x;
+}
+
+// What follows an item's sums: row r's outputs, or its partials and their
+// joining.  A partial row holds the sums, m and the sum of weights.
+template <int kDim, int kThreads>
+struct AttnItemEnd {
+  static constexpr int kRowFloats = kDim + 4;
+  const KvAttnParams& p;
+  const AttnPlace& cur;
+  int row0, used;  // the item's first row, its rows
+
+  __device__ __forceinline__ float* part_of(int cta, int slot) const {
+    return p.partial + (static_cast<int64_t>(cta) * 2 + slot) * (kAttnMaxRows * kRowFloats);
+  }
+  // four outputs of local row r, dims d .. d + 3
+  __device__ __forceinline__ void store(int r, int d, float4 v, float top, float l) const {
+    const int row = row0 + r, i = (row * p.group_magic) >> 16;
+    const int64_t tok_out = static_cast<int64_t>(cur.b) * p.q_len + i;
+    const int head_out = cur.head * p.group + row - i * p.group;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+    uint2 w;
+    if (p.f16) {
+      w.x = pack_f16(v.x, v.y);
+      w.y = pack_f16(v.z, v.w);
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+      w.x = *reinterpret_cast<const uint32_t*>(&a);
+      w.y = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint2*>(p.out + tok_out * p.ldo + head_out * kDim + d) = w;
+    if (d == 0 && p.lse)
+      p.lse[tok_out * (p.kv_heads * p.group) + head_out] =
+          l > 0.0f ? 0.6931471805599453f * (top + log2f(l)) : l == l ? -__builtin_huge_valf() : l;
+  }
+  // Behind the CTA's partial: the last CTA of those that share the item joins
+  // them.  Called by kThreads threads, tid 0 on; sync() is their barrier; ml
+  // holds a float2 for each row.
+  template <class Sync>
+  __device__ __forceinline__ void share(const int* plan_words, const int* line_before, float2* ml, int* last_flag,
+                                        Sync sync) const {
+    const int tid = threadIdx.x, per = plan_words[2], lead = plan_words[3];
+    // the CTAs c0 .. c0 + n_parts - 1 share the item; a CTA's part is in its slot 1 if it starts the item, else 0
+    const int len = plan_words[4] ? (cur.strips + per - 1) / per * per : attn_units(p, cur.strips) + lead;
+    const int item0 = line_before[cur.b] + cur.item * len + lead;  // the item's first strip on the line
+    const int c0 = item0 / per, n_parts = (item0 + cur.strips - 1) / per - c0 + 1;
+    // true for the last of `of` CTAs to come here (all threads alike)
+    auto last_of = [&](uint32_t* counter, int of) -> bool {
+      sync();
+      if (tid == 0) {
+        __threadfence();  // (cumulative: what the barrier showed this thread goes before the count)
+        *last_flag = of == 1 || atomicAdd(counter, 1u) == static_cast<uint32_t>(of - 1);
+        if (*last_flag) {
+          if (of > 1) *counter = 0u;
+          __threadfence();
+        }
+      }
+      sync();
+      return *last_flag != 0;
+    };
+    // joins `cnt` partials, of every step-th CTA from `from` on, into the outputs or into the first of them
+    auto join = [&](int from, int step, int cnt, bool final) {
+      constexpr int kBatch = 8;  // partials in flight per thread
+      const int cells = used * (kDim / 4);
+      int ways = 1;  // neighbouring lanes that share a cell's partials out
+      while (ways < 32 && 2 * ways * cells <= kThreads && ways * kBatch < cnt) ways *= 2;
+      for (int x0 = 0; x0 < cells; x0 += kThreads / ways) {
+        const int way = tid % ways, x = x0 + tid / ways;
+        const bool live = x < cells;
+        const int r = live ? x / (kDim / 4) : 0, d = live ? (x - r * (kDim / 4)) * 4 : 0;
+        float top = kAttnFloor, l = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k = way; live && k < cnt; k += kBatch * ways) {
+          float2 cm[kBatch];
+          float4 a[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int kk = k + j * ways, c = from + kk * step;
+            cm[j] = make_float2(kAttnFloor, 0.0f);
+            a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (kk < cnt) {
+              const float* o = part_of(c, c == c0 ? 1 : 0) + r * kRowFloats;
+              cm[j] = __ldcg(reinterpret_cast<const float2*>(o + kDim));
+              a[j] = __ldcg(reinterpret_cast<const float4*>(o + d));
+            }
+          }
+          float mn = top;
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
+          const float fall = attn_ex2(top - mn);
+          v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall, l *= fall;
+          top = mn;
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const float f = attn_ex2(cm[j].x - mn);
+            v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
+            v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
+            l = fmaf(cm[j].y, f, l);
+          }
+        }
+        for (int o = 1; o < ways; o <<= 1) {
+          const float to = __shfl_xor_sync(0xFFFFFFFFu, top, o), lo = __shfl_xor_sync(0xFFFFFFFFu, l, o);
+          const float4 u = make_float4(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o),
+                                       __shfl_xor_sync(0xFFFFFFFFu, v.z, o), __shfl_xor_sync(0xFFFFFFFFu, v.w, o));
+          const float mn = fmaxf(top, to);
+          const float f = attn_ex2(top - mn), fo = attn_ex2(to - mn);
+          v.x = v.x * f + u.x * fo, v.y = v.y * f + u.y * fo;
+          v.z = v.z * f + u.z * fo, v.w = v.w * f + u.w * fo;
+          l = l * f + lo * fo;
+          top = mn;
+        }
+        if (live && way == 0) {
+          if (final) {
+            store(r, d, v, top, l);
+          } else {  // (m and the sum of weights once all threads have read the old ones)
+            __stcg(reinterpret_cast<float4*>(part_of(from, from == c0 ? 1 : 0) + r * kRowFloats + d), v);
+            if (d == 0) ml[r] = make_float2(top, l);
+          }
+        }
+      }
+      if (!final) {
+        sync();
+        if (tid < used)
+          __stcg(reinterpret_cast<float2*>(part_of(from, from == c0 ? 1 : 0) + tid * kRowFloats + kDim), ml[tid]);
+      }
+    };
+    const int fan = n_parts <= kAttnFan ? n_parts : kAttnFan2;
+    const int mine = (static_cast<int>(blockIdx.x) - c0) / fan, from = c0 + mine * fan;
+    const int members = min(fan, n_parts - mine * fan);
+    if (last_of(p.arrived + from * 3 + (from == c0 ? 1 : 0), members)) {
+      if (n_parts <= kAttnFan) {
+        join(c0, 1, n_parts, true);
+      } else {
+        join(from, 1, members, false);
+        if (last_of(p.arrived + c0 * 3 + 2, (n_parts + fan - 1) / fan)) join(c0, fan, (n_parts + fan - 1) / fan, true);
+      }
+    }
+  }
+};
 
 // How a strip of 16 rows of kDim code bytes lies in shared memory and which
 // bytes a thread (g = lane / 4, t = lane % 4) takes.  Rows are cut into
@@ -227,7 +564,7 @@ struct AttnLayout {
 template <int kDim, int kN, int kRes>
 struct AttnCfg {
   using L = AttnLayout<kDim>;
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = kAttnRound;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = 8 * kN;
   static constexpr bool kQInRegs = kN == 1;                         // a warp keeps its queries in registers
@@ -242,14 +579,6 @@ struct AttnCfg {
   static constexpr int kSmem = kRingBytes + kQBytes + kWarps * kRows * 8 + kRows * 4;  // + the sequences
   // dynamic shared memory for B sequences
   static constexpr int smem(int B) { return kSmem + (B + 1) * 12; }
-};
-
-// An item and a place in it.
-struct AttnPlace {
-  int b, head, tile;  // sequence, KV head, row tile
-  int strip, strips;  // the place in strips; the item's number of strips
-  int first;          // the sequence's first strip that any query sees (its token / 16)
-  int item;           // number of the item within the sequence
 };
 
 template <int kDim, bool kInt8, int kN, int kRes>
@@ -276,7 +605,6 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
   pdl_wait();
 
   const int rows = p.q_len * p.group;  // query rows of a KV head
-  const int items = p.kv_heads * p.row_tiles;
   // Queries and block table on their way to L2 while the first warp plans, each CTA a part.
   if (warp > 0) {
     const int per_row = (p.kv_heads * p.group * kDim * 2 + 127) >> 7, q_lines = p.B * p.q_len * per_row;
@@ -289,151 +617,12 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
       asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
     }
   }
-  auto first_strip = [&](int n) -> int {
-    const int at = n - p.q_len;  // the first query's position
-    return p.window > 0 && at >= p.window ? (at - p.window + 1) >> 4 : 0;
-  };
-  auto strips_of = [&](int n) -> int { return ((n + 15) >> 4) - first_strip(n); };
-  auto div_up = [](int x, int y, float inv_y) -> int {  // ceil(x / y), x + y below 2^31
-    if (x >= 1 << 24) return (x + y - 1) / y;
-    int q = static_cast<int>(static_cast<float>(x) * inv_y);  // (at most one off)
-    q -= q * y > x;
-    q += q * y + y <= x;
-    return q + (q * y < x);
-  };
-  auto rounds = [](int x) { return (x + C::kWarps - 1) / C::kWarps * C::kWarps; };  // whole rounds of the warps
+  auto first_strip = [&](int n) -> int { return attn_first_strip(p, n); };
+  auto strips_of = [&](int n) -> int { return attn_strips_of(p, n); };
+  attn_plan<C::kThreads>(p, strips_before, line_before, tokens, plan_words, places);
+  const int begin = plan_words[0], end = plan_words[1];
 
-  // ---- the plan, by the first warp (a lane per sequence, in rounds of 32); lens by all threads where there are many ----
-  {
-    constexpr uint32_t kAll = 0xFFFFFFFFu;
-    const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.block_log2;
-    auto length = [&](int b) -> int {
-      const int raw = __ldg(p.lens + b);
-      const int n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
-      if (n != raw && blockIdx.x == 0) raise_error(p.err, FP4_ERR_BADIDX);
-      return n;
-    };
-    const bool few = p.B <= 32;
-    if (!few) {
-      for (int b = tid; b < p.B; b += C::kThreads) tokens[b] = length(b);
-      __syncthreads();
-    }
-    if (warp == 0) {
-      const int ctas = static_cast<int>(gridDim.x);
-      int n0 = 0;  // the lane's sequence, where there are few
-      if (few && lane < p.B) {
-        n0 = length(lane);
-        tokens[lane] = n0;
-      }
-      auto tokens_of = [&](int b) -> int { return few ? n0 : b < p.B ? tokens[b] : 0; };
-      auto strips_at = [&](int b) -> int {
-        const int n = tokens_of(b);
-        return n > 0 ? strips_of(n) : 0;
-      };
-      int total = 0, alive = 0;
-      for (int b = lane; b < p.B + lane; b += 32) {  // (all lanes alike)
-        const int s = strips_at(b);
-        total += __reduce_add_sync(kAll, s);
-        alive += __popc(__ballot_sync(kAll, s > 0));
-      }
-      total *= items;
-      alive *= items;
-      // pieces per item, if those of the shortest of three lengths are no more than the CTAs
-      int per = 0;
-      if (alive <= ctas) {
-        const int even = div_up(total, ctas, p.inv_ctas);
-        int len[3], sum[3] = {0, 0, 0};
-        float inv[3];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          len[k] = max(C::kWarps, rounds(even + (even * k >> 3)));
-          inv[k] = __fdividef(1.0f, static_cast<float>(len[k]));
-        }
-        for (int b = lane; b < p.B + lane; b += 32) {
-          const int s = strips_at(b);
-#pragma unroll
-          for (int k = 0; k < 3; ++k) sum[k] += __reduce_add_sync(kAll, div_up(s, len[k], inv[k]));
-        }
-#pragma unroll
-        for (int k = 2; k >= 0; --k)
-          if (sum[k] * items <= ctas) per = len[k];
-      }
-      const bool pieces = per > 0;
-      const int lead = pieces ? 0 : kAttnItemCost;
-      if (!pieces) per = max(rounds(div_up(total + alive * kAttnItemCost, ctas, p.inv_ctas)), C::kWarps);
-      const float inv_per = __fdividef(1.0f, static_cast<float>(per));
-      auto on_line = [&](int s) -> int { return pieces ? div_up(s, per, inv_per) * per : s > 0 ? s + lead : 0; };
-      // the sequences' places on both lines; and the share's begin and end in strips, where the cuts fall
-      int strips_end = 0, line_end = 0, share[2] = {-1, -1};
-      AttnPlace place = {};
-      for (int b = lane; b < p.B + lane; b += 32) {
-        const int s = strips_at(b), len = on_line(s);
-        int sum = s, line = len;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(kAll, sum, o), v = __shfl_up_sync(kAll, line, o);
-          if (lane >= o) sum += u, line += v;
-        }
-        const int strips_here = strips_end + (sum - s) * items, line_here = line_end + (line - len) * items;
-        if (b < p.B) {
-          strips_before[b] = strips_here;
-          line_before[b] = line_here;
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int64_t at64 = static_cast<int64_t>(per) * (blockIdx.x + k);
-          if (len > 0 && at64 >= line_here && at64 < line_here + static_cast<int64_t>(len) * items) {
-            const int off = static_cast<int>(at64) - line_here;
-            const int item = div_up(off + 1, len, __fdividef(1.0f, static_cast<float>(len))) - 1;
-            // (a cut behind an item's last strip or in its cost: the strip that follows)
-            const int strip = max(off - item * len - lead, 0);
-            share[k] = strips_here + item * s + min(strip, s);
-            if (k == 0) {
-              place.b = b;
-              place.first = first_strip(tokens_of(b));
-              place.strips = s;
-              place.item = item;
-              place.strip = strip;  // (below s wherever the share is not empty, or pieces end)
-              place.head = p.row_tiles == 1 ? item : item / p.row_tiles;
-              place.tile = item - place.head * p.row_tiles;
-            }
-          }
-        }
-        strips_end += __shfl_sync(kAll, sum, 31) * items;
-        line_end += __shfl_sync(kAll, line, 31) * items;
-      }
-      // (the one lane that met a cut writes it; cuts past the line's end: no strip follows)
-      if (share[0] >= 0) {
-        plan_words[0] = share[0];
-        places[0] = places[2] = place;
-      }
-      if (share[1] >= 0) plan_words[1] = share[1];
-      const bool met0 = __any_sync(kAll, share[0] >= 0), met1 = __any_sync(kAll, share[1] >= 0);
-      if (lane == 0) {
-        strips_before[p.B] = strips_end;
-        line_before[p.B] = line_end;
-        if (!met0) plan_words[0] = strips_end;
-        if (!met1) plan_words[1] = strips_end;
-        plan_words[2] = per;
-        plan_words[3] = lead;
-        plan_words[4] = pieces;
-      }
-    }
-    __syncthreads();
-  }
-  const int begin = plan_words[0], end = plan_words[1], per = plan_words[2], lead = plan_words[3];
-
-  // sequences nobody visits: zeros, lse -inf
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (tokens[b] > 0) continue;
-    const int heads = p.kv_heads * p.group;
-    for (int i = tid; i < p.q_len * heads * (kDim / 8); i += C::kThreads) {
-      const int64_t row = i / (kDim / 8);
-      const int64_t tok = static_cast<int64_t>(b) * p.q_len + row / heads;
-      reinterpret_cast<uint4*>(p.out + tok * p.ldo + (row % heads) * kDim)[i % (kDim / 8)] = make_uint4(0, 0, 0, 0);
-      if (p.lse && i % (kDim / 8) == 0) p.lse[tok * heads + row % heads] = -__builtin_huge_valf();
-    }
-  }
+  attn_empty<kDim, C::kThreads>(p, tokens);
   if (begin >= end) return;
 
   // ---- queries: f16 operands; bf16 ones scaled by a power of two for each row ----
@@ -561,21 +750,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
       row0 = c.tile * C::kRows;
       tok0 = (c.first + c.strip) << 4;
       if (tid == 0 && seg_end < end) {  // the next item (read behind the barriers of the joining)
-        AttnPlace x = c;
-        x.strip = 0;
-        ++x.item;
-        if (++x.tile == p.row_tiles) {
-          x.tile = 0;
-          if (++x.head == p.kv_heads) {
-            x.head = x.item = 0;
-            do ++x.b;
-            while (strips_before[x.b + 1] == strips_before[x.b]);
-            const int len = tokens[x.b];
-            x.first = first_strip(len);
-            x.strips = strips_of(len);
-          }
-        }
-        places[which ^ 1] = x;
+        places[which ^ 1] = attn_next(p, c, strips_before, tokens);
       }
     }
     float rs[2];  // (queries in shared memory: so are the rows' factors)
@@ -799,36 +974,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
     const AttnPlace cur = places[which];
     const int used = min(C::kRows, rows - row0);
     const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
-    constexpr int kRowFloats = kDim + 4;  // a partial row: the sums, m, the sum of weights
-    auto part_of = [&](int cta, int slot) -> float* {
-      return p.partial + (static_cast<int64_t>(cta) * 2 + slot) * (kAttnMaxRows * kRowFloats);
-    };
-    float* const part = part_of(blockIdx.x, starts ? 1 : 0);
-    auto out_row = [&](int r, int64_t* tok_out, int* head_out) {
-      const int row = row0 + r, i = (row * p.group_magic) >> 16;
-      *tok_out = static_cast<int64_t>(cur.b) * p.q_len + i;
-      *head_out = cur.head * p.group + row - i * p.group;
-    };
-    auto store = [&](int r, int d, float4 v, float top, float l) {  // four outputs of local row r, dims d .. d + 3
-      int64_t tok_out;
-      int head_out;
-      out_row(r, &tok_out, &head_out);
-      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-      v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-      uint2 w;
-      if (p.f16) {
-        w.x = pack_f16(v.x, v.y);
-        w.y = pack_f16(v.z, v.w);
-      } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-        w.x = *reinterpret_cast<const uint32_t*>(&a);
-        w.y = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      *reinterpret_cast<uint2*>(p.out + tok_out * p.ldo + head_out * kDim + d) = w;
-      if (d == 0 && p.lse)
-        p.lse[tok_out * (p.kv_heads * p.group) + head_out] =
-            l > 0.0f ? 0.6931471805599453f * (top + log2f(l)) : l == l ? -__builtin_huge_valf() : l;
-    };
+    const AttnItemEnd<kDim, C::kThreads> item_end = {p, cur, row0, used};
+    float* const part = item_end.part_of(blockIdx.x, starts ? 1 : 0);
 #pragma unroll
     for (int nt = 0; nt < kN; ++nt) {  // eight rows at a time
       if (nt * 8 >= used) break;
@@ -859,112 +1006,17 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
           l = fmaf(o.y, f, l);
         }
         if (whole) {
-          store(r, d, v, top, l);
+          item_end.store(r, d, v, top, l);
         } else {
-          float* const o = part + r * kRowFloats;
+          float* const o = part + r * (kDim + 4);
           __stcg(reinterpret_cast<float4*>(o + d), v);
           if (d == 0) __stcg(reinterpret_cast<float2*>(o + kDim), make_float2(top, l));
         }
       }
       __syncthreads();
     }
-    if (!whole) {
-      // the CTAs c0 .. c0 + n_parts - 1 share the item; a CTA's part is in its slot 1 if it starts the item, else 0
-      const int len = plan_words[4] ? (cur.strips + per - 1) / per * per : cur.strips + lead;
-      const int item0 = line_before[cur.b] + cur.item * len + lead;  // the item's first strip on the line
-      const int c0 = item0 / per, n_parts = (item0 + cur.strips - 1) / per - c0 + 1;
-      // true for the last of `of` CTAs to come here (all threads alike)
-      auto last_of = [&](uint32_t* counter, int of) -> bool {
-        __syncthreads();
-        if (tid == 0) {
-          __threadfence();  // (cumulative: what the barrier showed this thread goes before the count)
-          last_flag = of == 1 || atomicAdd(counter, 1u) == static_cast<uint32_t>(of - 1);
-          if (last_flag) {
-            if (of > 1) *counter = 0u;
-            __threadfence();
-          }
-        }
-        __syncthreads();
-        return last_flag != 0;
-      };
-      // joins `cnt` partials, of every step-th CTA from `from` on, into the outputs or into the first of them
-      auto join = [&](int from, int step, int cnt, bool final) {
-        constexpr int kBatch = 8;  // partials in flight per thread
-        const int cells = used * (kDim / 4);
-        int ways = 1;  // neighbouring lanes that share a cell's partials out
-        while (ways < 32 && 2 * ways * cells <= C::kThreads && ways * kBatch < cnt) ways *= 2;
-        for (int x0 = 0; x0 < cells; x0 += C::kThreads / ways) {
-          const int way = tid % ways, x = x0 + tid / ways;
-          const bool live = x < cells;
-          const int r = live ? x / (kDim / 4) : 0, d = live ? (x - r * (kDim / 4)) * 4 : 0;
-          float top = kAttnFloor, l = 0.0f;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int k = way; live && k < cnt; k += kBatch * ways) {
-            float2 cm[kBatch];
-            float4 a[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-              const int kk = k + j * ways, c = from + kk * step;
-              cm[j] = make_float2(kAttnFloor, 0.0f);
-              a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (kk < cnt) {
-                const float* o = part_of(c, c == c0 ? 1 : 0) + r * kRowFloats;
-                cm[j] = __ldcg(reinterpret_cast<const float2*>(o + kDim));
-                a[j] = __ldcg(reinterpret_cast<const float4*>(o + d));
-              }
-            }
-            float mn = top;
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
-            const float fall = attn_ex2(top - mn);
-            v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall, l *= fall;
-            top = mn;
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-              const float f = attn_ex2(cm[j].x - mn);
-              v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
-              v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
-              l = fmaf(cm[j].y, f, l);
-            }
-          }
-          for (int o = 1; o < ways; o <<= 1) {
-            const float to = __shfl_xor_sync(0xFFFFFFFFu, top, o), lo = __shfl_xor_sync(0xFFFFFFFFu, l, o);
-            const float4 u = make_float4(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o),
-                                         __shfl_xor_sync(0xFFFFFFFFu, v.z, o), __shfl_xor_sync(0xFFFFFFFFu, v.w, o));
-            const float mn = fmaxf(top, to);
-            const float f = attn_ex2(top - mn), fo = attn_ex2(to - mn);
-            v.x = v.x * f + u.x * fo, v.y = v.y * f + u.y * fo;
-            v.z = v.z * f + u.z * fo, v.w = v.w * f + u.w * fo;
-            l = l * f + lo * fo;
-            top = mn;
-          }
-          if (live && way == 0) {
-            if (final) {
-              store(r, d, v, top, l);
-            } else {  // (m and the sum of weights once all threads have read the old ones)
-              __stcg(reinterpret_cast<float4*>(part_of(from, from == c0 ? 1 : 0) + r * kRowFloats + d), v);
-              if (d == 0) ml[r] = make_float2(top, l);
-            }
-          }
-        }
-        if (!final) {
-          __syncthreads();
-          if (tid < used)
-            __stcg(reinterpret_cast<float2*>(part_of(from, from == c0 ? 1 : 0) + tid * kRowFloats + kDim), ml[tid]);
-        }
-      };
-      const int fan = n_parts <= kAttnFan ? n_parts : kAttnFan2;
-      const int mine = (static_cast<int>(blockIdx.x) - c0) / fan, from = c0 + mine * fan;
-      const int members = min(fan, n_parts - mine * fan);
-      if (last_of(p.arrived + from * 3 + (from == c0 ? 1 : 0), members)) {
-        if (n_parts <= kAttnFan) {
-          join(c0, 1, n_parts, true);
-        } else {
-          join(from, 1, members, false);
-          if (last_of(p.arrived + c0 * 3 + 2, (n_parts + fan - 1) / fan)) join(c0, fan, (n_parts + fan - 1) / fan, true);
-        }
-      }
-    }
+    if (!whole)
+      item_end.share(plan_words, line_before, ml, &last_flag, [] { __syncthreads(); });
     // on to the next item
     at = seg_end;
     which ^= 1;
