@@ -114,7 +114,7 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   const int64_t tokens = static_cast<int64_t>(max_blocks) * cache->block_size;
   // (32-bit: places on the line of strips, a quarter more with padding, and strips of the cache)
   if (tokens > (1ll << 30) ||
-      (static_cast<double>(tokens) / 16 + fp4::kAttnItemCost) * B * cache->kv_heads * row_tiles >= 1.2e9 ||
+      (static_cast<double>(tokens) / 16 + fp4::kAttnTcItemCost + 8) * B * cache->kv_heads * row_tiles >= 1.2e9 ||
       static_cast<double>(cache->num_blocks) * cache->kv_heads * (cache->block_size / 16) >= 2147483647.0)
     return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
   if (crooked || !aligned(q, 16) || !aligned(out, 16) || ldq % 8 != 0 || ldo % 8 != 0 || !aligned(lse, 4) ||
@@ -153,6 +153,7 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   p.row_tiles = row_tiles;
   p.window = window;
   p.unit = 1;
+  p.item_cost = fp4::kAttnItemCost;
   p.f16 = dtype == FP4GEMV_F16;
   p.sm_scale = sm_scale;
   fp4::count_launch();
@@ -162,6 +163,7 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
         !fp4::encode_pages_128(&p.v_map, cache->v_codes, cache->block_size, pages))
       return FP4GEMV_ERR_CUDA;
     p.unit = 8;  // tiles of 128 tokens are of whole pages
+    p.item_cost = fp4::kAttnTcItemCost;
     return from_cuda(fp4::launch_kv_attention_tc(p, sms, pdl, stream));
   }
   return from_cuda(fp4::launch_kv_attention(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms, pdl,

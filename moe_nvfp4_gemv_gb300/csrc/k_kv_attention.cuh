@@ -71,6 +71,7 @@ struct KvAttnParams {
   int window;
   int f16;             // element type of q and out
   int unit;            // strips (a power of two): items start and are cut at its multiples
+  int item_cost;       // what an item's end costs, in strips
   int group_magic;     // ceil(2^16 / group): row / group = row group_magic >> 16 for the rows there are
   float inv_ctas;      // 1 / the grid's CTAs
   float sm_scale;
@@ -87,6 +88,7 @@ constexpr int kAttnRound = 8;     // strips of a round, one for each warp: share
 constexpr int kAttnFan = 40;      // partials that one CTA joins at once
 constexpr int kAttnFan2 = 20;     // ... where the joined ones are joined again
 constexpr int kAttnItemCost = 16;  // an item's end, in strips
+constexpr int kAttnTcItemCost = 64;  // ... of the kernel on the 5th-generation tensor core
 constexpr float kAttnFloor = -1e30f;  // the running maximum before any token
 constexpr float kAttnSlack = 8.0f;    // log2 of the largest weight before the running maximum moves
 
@@ -238,8 +240,8 @@ __device__ __forceinline__ void attn_plan(const KvAttnParams& p, int* strips_bef
         if (sum[k] * items <= ctas) per = len[k];
     }
     const bool pieces = per > 0;
-    const int lead = pieces ? 0 : kAttnItemCost;
-    if (!pieces) per = max(whole(attn_div_up(total + alive * kAttnItemCost, ctas, p.inv_ctas)), kAttnRound);
+    const int lead = pieces ? 0 : p.item_cost;
+    if (!pieces) per = max(whole(attn_div_up(total + alive * p.item_cost, ctas, p.inv_ctas)), kAttnRound);
     const float inv_per = __fdividef(1.0f, static_cast<float>(per));
     auto on_line = [&](int s) -> int { return pieces ? attn_div_up(s, per, inv_per) * per : s > 0 ? attn_units(p, s) + lead : 0; };
     // the sequences' places on both lines; and the share's begin and end in strips, where the cuts fall

@@ -8,13 +8,14 @@
 // as sums of E4M3 values of 4 significant bits each:
 //
 // * a query row, scaled by a power of two to a largest magnitude in
-//   [128, 256), is q1 + (q2 + q3) / 16.  Two parts hold bf16's 8 bits and three
-//   f16's 11; values below 2^-14 of the row's largest lose bits below 2^-22 of
-//   it.  S^T [128 tokens x 64] = K [128 x 128] [q1 | q2 + q3]^T, the parts side
+//   [128, 256), is q1 + (q2 + q3) / 32.  Two parts hold bf16's 8 bits and three
+//   f16's 11; values below 2^-14 of the row's largest (f16: 2^-11) lose bits
+//   below 2^-22 of it.  S^T [128 tokens x 64] = K [128 x 128] [q1 | q2 + q3]^T, the parts side
 //   by side on N, q3 added by an MMA of its own (f16 only).
 // * a weight w = 2^(s + log2 vs - m), rounded to f16 as it is there, is
-//   (w1 + w2 / 16 + w3 / 256) / 16, which holds its 11 bits; below 2^-11 the
-//   low ones go at 2^-22.  out^T [128 dims x 96] = V^T [128 dims x 128 tokens]
+//   (w1 + w2 / 32 + w3 / 1024) / 16, which holds its 11 bits; of weights below
+//   2^-12 what lies below 2^-24 goes.  (What a part leaves is at most half the
+//   last place of its 4 bits, 8 of 256, so 32 times it fits the next.)  out^T [128 dims x 96] = V^T [128 dims x 128 tokens]
 //   [w1 | w2 | w3]: V^T is read from the V tile as it lies (M-major), the
 //   weights' tile has a token's 96 bytes in a row (N-major).
 //
@@ -23,13 +24,23 @@
 // clears where the token is of no sequence, are plain registers; and a
 // dimension while it moves sums (TMEM lane = dim).
 //
-// The work: a CTA per SM; a producer warp brings tiles of 128 tokens by TMA, in
-// boxes of 16 tokens of a page, into a ring of kStages; two groups of four
-// warps take the tiles by turns, each with sums and running maxima of its own,
-// an MMA warp for each.  While a group makes weights the other's products run
-// and its own next scores are made, so a tile costs the SM about 600 issue
-// slots of each scheduler, where the loads of a tile take twice that.  Shares,
-// segments, partials and their joining are those of k_kv_attention.cuh.
+// The work: a CTA per SM, twelve warps.  A producer warp for K and one for V
+// bring tiles of 128 tokens, whole pages by TMA, into rings of their own (K is
+// free as soon as its scores are made); two groups of four warps take the tiles
+// by turns, each with sums and running maxima of its own, and an MMA warp for
+// each.  While a group makes weights the other's products run and its own next
+// scores are made.  Shares, segments, partials and their joining are those of
+// k_kv_attention.cuh; shares are cut at tiles, so that tiles hold whole pages.
+//
+// What bounds it.  32 sequences of 16384 tokens, 4 new ones each, 64 heads over
+// 8: 173 us, 0.93 of the measured bandwidth (mma.sync with the codes converted
+// in registers: 263, bound by issue: 447 instructions a strip of 16 tokens,
+// where this kernel needs 350).  Steps to it: both rings as one, a V tile held
+// as long as its K and 16 TMA boxes a tile from one warp 228; rings apart, boxes
+// of a page 175.  Short calls pay for the set-up and the first tile's chain
+// (14 us for one sequence of 1000 tokens; mma.sync 16), several items in a share
+// for the drains between them (kAttnTcItemCost: 24 ragged sequences of up to
+// 8191 tokens 68 us with 16, 58 with 32, 53 with 64; mma.sync 90).
 //
 // Every wait is bounded.  After a failed one (the error word holds
 // FP4_ERR_TIMEOUT) the waits that follow are skipped, so that all roles come to
@@ -60,8 +71,8 @@ struct AttnTc {
   static constexpr int smem(int B) { return 1024 + kSeqOff + (B + 1) * 12; }
   static constexpr uint32_t kCols = 512;     // TMEM: S 64 for each group, then out 96 for each
   static constexpr int kSCols = 64, kOCols = 96;
-  static constexpr float kSlack = 4.0f;      // log2 of the largest weight before m moves: w1 up to 2^8
-  static constexpr float kWScale = 4.0f;     // log2 of w1's scale
+  static constexpr float kSlack = 4.0f;      // log2 of the largest weight before m moves
+  static constexpr float kWScale = 4.0f;     // log2 of w1's scale: w1 up to 2^8, of E4M3's 448
 };
 
 // D[tmem] (+)= A[smem] B[smem], E4M3
@@ -117,9 +128,9 @@ __device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t f16x2_mul16(uint32_t a) {
+__device__ __forceinline__ uint32_t f16x2_mul32(uint32_t a) {
   uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x4C004C00u));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x50005000u));
   return r;
 }
 template <int kId>
@@ -378,19 +389,22 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
     const uint32_t s_cols = group_s[g] + lanes, o_cols = group_o[g] + lanes;
     const uint32_t w_row = sm + C::kWOff + g * C::kTileBytes + who * 128;  // the token's weights
     int first_tile = 0, count = 0;
+    // queries: eight threads a row, 16 dims each
+    const int q_row = tid >> 3, q_part = tid & 7;
+    auto q_source = [&](const AttnPlace& x, int row) -> const uint4* {
+      const int i = (row * p.group_magic) >> 16;
+      return reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(x.b) * p.q_len + i) * p.ldq +
+                                            (x.head * p.group + row - i * p.group) * C::kDim + q_part * 16);
+    };
     while (at < end) {
       const int seg_end = min(end, at + cur.strips - cur.strip);
       const int tiles = (seg_end - at + 7) >> 3;
       const int n = tokens[cur.b], row0 = cur.tile * C::kRows, tok0 = (cur.first + cur.strip) << 4;
       const int used = min(C::kRows, rows - row0);
       {
-        // ---- queries: eight threads a row, 16 dims each ----
-        const int r = tid >> 3, c = tid & 7, row = row0 + r;
         uint32_t raw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (r < used) {
-          const int i = (row * p.group_magic) >> 16;
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(cur.b) * p.q_len + i) * p.ldq +
-                                                            (cur.head * p.group + row - i * p.group) * C::kDim + c * 16);
+        if (q_row < used) {
+          const uint4* src = q_source(cur, row0 + q_row);
           const uint4 a = __ldg(src), b = __ldg(src + 1);
           raw[0] = a.x, raw[1] = a.y, raw[2] = a.z, raw[3] = a.w, raw[4] = b.x, raw[5] = b.y, raw[6] = b.z, raw[7] = b.w;
         }
@@ -423,25 +437,31 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
           // (v down has at most 11 bits: f16 holds it, but for bits below 2^-24)
           const uint32_t h = pack_f16(v[2 * k] * down, v[2 * k + 1] * down);
           const uint16_t p1 = e4m3x2_of_f16x2(h);
-          const uint32_t rest = f16x2_mul16(f16x2_sub(h, f16x2_of_e4m3x2(p1)));
+          const uint32_t rest = f16x2_mul32(f16x2_sub(h, f16x2_of_e4m3x2(p1)));
           const uint16_t p2 = e4m3x2_of_f16x2(rest);
           const uint16_t p3 = e4m3x2_of_f16x2(f16x2_sub(rest, f16x2_of_e4m3x2(p2)));  // (of the second part's scale)
           part[0][k >> 1] |= static_cast<uint32_t>(finite ? p1 : 0x7F7Fu) << (16 * (k & 1));  // (else: NaN)
           part[1][k >> 1] |= static_cast<uint32_t>(p2) << (16 * (k & 1));
           part[2][k >> 1] |= static_cast<uint32_t>(p3) << (16 * (k & 1));
         }
-        const uint32_t q_row = sm + C::kQOff + (r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4);
+        const uint32_t q_at = sm + C::kQOff + (q_row >> 3) * 1024 + (q_row & 7) * 128 + ((q_part ^ (q_row & 7)) << 4);
 #pragma unroll
         for (int u = 0; u < 3; ++u)
-          sts128(q_row + u * 32 * C::kDim, make_uint4(part[u][0], part[u][1], part[u][2], part[u][3]));
-        if (c == 0) row_factor[r] = p.sm_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        if (c < C::kGroups) {
-          row_base[c][r] = 0.0f;
-          row_m[c][r] = kAttnFloor;
+          sts128(q_at + u * 32 * C::kDim, make_uint4(part[u][0], part[u][1], part[u][2], part[u][3]));
+        if (q_part == 0)
+          row_factor[q_row] = p.sm_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        if (q_part < C::kGroups) {
+          row_base[q_part][q_row] = 0.0f;
+          row_m[q_part][q_row] = kAttnFloor;
         }
         fence_proxy_async_smem();
       }
       named_sync<4>(C::kWeighers + 32 * C::kGroups);  // the queries and the rows' factors are there
+      if (seg_end < end) {  // the next item's on their way to L2
+        const AttnPlace x = attn_next(p, cur, strips_before, tokens);
+        const int row = x.tile * C::kRows + q_row;
+        if (row < rows) asm volatile("prefetch.global.L2 [%0];" ::"l"(q_source(x, row)));
+      }
       const int tokens_all = n - p.q_len + 1;                          // every row sees those before this one
       const int tokens_low = p.window > 0 ? max(0, n - p.window) : 0;  // ... from this one on
       const int tok_end = min(n, tok0 + ((seg_end - at) << 4));
@@ -466,7 +486,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
           mbar_arrive(taken(g));
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            x[i] = fma2(pair(low[2 * i], low[2 * i + 1]), pair(0.0625f, 0.0625f), pair(high[2 * i], high[2 * i + 1]));
+            x[i] = fma2(pair(low[2 * i], low[2 * i + 1]), pair(0.03125f, 0.03125f), pair(high[2 * i], high[2 * i + 1]));
         }
         const uint32_t scales = sm + C::kScaleOff + stage * 64 + (who >> p.block_log2) * 4;
         const float ks = ldsf(scales), vs = ldsf(scales + 32);
@@ -548,7 +568,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
             tmem_wait_st();
           }
         }
-        // weights, their sums, their parts: x = p1 + p2 / 16 + p3 / 256
+        // weights, their sums, their parts
         const uint64_t inv2 = pair(inv_vs, inv_vs);
 #pragma unroll
         for (int r0 = 0; r0 < C::kRows; r0 += 16) {
@@ -564,9 +584,9 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
               sum[i] = fma2(pair(a, b), inv2, sum[i]);
               const uint32_t w = pack_f16(a, b);
               code[0][h] = e4m3x2_of_f16x2(w);
-              const uint32_t rest = f16x2_mul16(f16x2_sub(w, f16x2_of_e4m3x2(code[0][h])));  // (exact)
+              const uint32_t rest = f16x2_mul32(f16x2_sub(w, f16x2_of_e4m3x2(code[0][h])));  // (exact)
               code[1][h] = e4m3x2_of_f16x2(rest);
-              code[2][h] = e4m3x2_of_f16x2(f16x2_mul16(f16x2_sub(rest, f16x2_of_e4m3x2(code[1][h]))));
+              code[2][h] = e4m3x2_of_f16x2(f16x2_mul32(f16x2_sub(rest, f16x2_of_e4m3x2(code[1][h]))));
             }
 #pragma unroll
             for (int u = 0; u < 3; ++u) part[u][k] = join16(code[u][0], code[u][1]);
@@ -600,19 +620,21 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         tmem_get32(o_cols, o);
         tmem_get32(o_cols + 32, low);
 #pragma unroll
-        for (int r = 0; r < 32; ++r) o[r] = fmaf(low[r], 0.0625f, o[r]);
+        for (int r = 0; r < 32; ++r) o[r] = fmaf(low[r], 0.03125f, o[r]);
         tmem_get32(o_cols + 64, low);
         tc_fence_before();
         float* const mine = reinterpret_cast<float*>(smem + C::kWOff + g * C::kTileBytes);
 #pragma unroll
-        for (int r = 0; r < 32; ++r) mine[r * C::kDim + who] = any ? fmaf(low[r], 0.00390625f, o[r]) : 0.0f;
+        for (int r = 0; r < 32; ++r) mine[r * C::kDim + who] = any ? fmaf(low[r], 0.0009765625f, o[r]) : 0.0f;
       }
       named_sync<3>(C::kWeighers);
       const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
       const AttnItemEnd<C::kDim, C::kWeighers> item_end = {p, cur, row0, used};
       float* const part = item_end.part_of(blockIdx.x, starts ? 1 : 0);
-      for (int x = tid; x < used * (C::kDim / 4); x += C::kWeighers) {
-        const int r = x / (C::kDim / 4), d = (x - r * (C::kDim / 4)) * 4;
+#pragma unroll
+      for (int k = 0; k < C::kRows / (C::kWeighers / 32); ++k) {
+        const int r = k * (C::kWeighers / 32) + warp, d = lane * 4;
+        if (r >= used) break;
         const float m0 = row_m[0][r], m1 = row_m[1][r], top = fmaxf(m0, m1);
         const float f0 = attn_ex2(m0 - top), f1 = attn_ex2(m1 - top);
         const float l0 = (row_tmp[0][r] + row_tmp[1][r]) + (row_tmp[2][r] + row_tmp[3][r]);
