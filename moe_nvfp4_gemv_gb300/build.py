@@ -2,8 +2,9 @@
 
 Each translation unit compiles in its own nvcc process (in parallel); the
 objects are linked into ``moe_nvfp4_gemv_gb300/libfp4gemv.so`` against the
-shared CUDA runtime.  Rebuilds only when a source or header is newer than the
-library.  Usage: ``python -m moe_nvfp4_gemv_gb300.build [--force]``.
+shared CUDA runtime.  csrc/marshal.cpp becomes ``_marshal.so`` beside it, an
+extension module on this interpreter's torch (g++, at the same time).  Rebuilds
+only when a source or header is newer than what it makes.  Usage: ``python -m moe_nvfp4_gemv_gb300.build [--force]``.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp4gemv.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -47,11 +50,60 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def _marshal_stale() -> bool:
+    if not os.path.exists(MARSHAL):
+        return True
+    t = os.path.getmtime(MARSHAL)
+    deps = [os.path.join(CSRC, "marshal.cpp"), os.path.abspath(__file__), os.path.join(_torch_dir(), "version.py")] + \
+        glob.glob(os.path.join(INCLUDE, "*.h"))
+    return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _start_marshal(nvcc: str) -> tuple[str, subprocess.Popen]:
+    """Starts the compiler of _marshal.so; the path it writes to, and the process."""
+    import torch
+    tdir, cuda = _torch_dir(), os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-isystem", os.path.join(tdir, "include"),
+           "-isystem", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+           os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L", os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + os.path.join(tdir, "lib")]
+    return tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish_marshal(tmp: str, proc: subprocess.Popen) -> None:
+    out, _ = proc.communicate()
+    if proc.returncode != 0:
+        sys.stderr.write(out.decode(errors="replace"))
+        raise RuntimeError("the C++ compiler failed for marshal.cpp")
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if needed) and return the path of libfp4gemv.so."""
-    if not force and not _stale():
+    library, marshal = force or _stale(), force or _marshal_stale()
+    if not library and not marshal:
         return LIB
     nvcc = _nvcc()
+    started = _start_marshal(nvcc) if marshal else None
+    try:
+        if library:
+            _build_library(nvcc, verbose)
+    finally:
+        if started:
+            _finish_marshal(*started)
+    return LIB
+
+
+def _build_library(nvcc: str, verbose: bool) -> None:
     os.makedirs(BUILD_DIR, exist_ok=True)
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
     if verbose:
@@ -76,7 +128,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "shared",
                            "-Xlinker", "-rpath," + _cuda_lib_dir(nvcc)])
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -12,7 +12,9 @@ bf16_gemv, dequantize_rows; vllm.models.flint.ops.moe_gemv: gate_up,
 down_combine): ``nvfp4_gemv`` / ``bf16_gemv`` / ``dequantize_rows`` allocate
 and return their output, the MoE pair writes into caller buffers.
 ``moe_route`` and ``token_logprobs`` allocate their outputs unless they are
-given; the 8-bit cache's calls are methods of ``kvcache.KvCache8``.
+given; the 8-bit cache's calls are methods of ``kvcache.KvCache8``.  These
+short calls are marshalled by ``_marshal`` (csrc/marshal.cpp), which reads the
+tensors without ctypes.
 """
 from __future__ import annotations
 
@@ -45,7 +47,7 @@ class Fp4GemvError(RuntimeError):
 
 def _load() -> ctypes.CDLL:
     path = _build.LIB
-    if not os.path.exists(path) or _build._stale():
+    if not os.path.exists(path) or _build._stale() or _build._marshal_stale():
         path = _build.build()
     lib = ctypes.CDLL(path)
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -89,6 +91,11 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 LIB_PATH = _build.LIB
+
+from . import _marshal  # noqa: E402  (built by _load where it has to be)
+
+_marshal.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+    _lib.fp4gemv_kv_append, _lib.fp4gemv_kv_attention, _lib.fp4gemv_moe_route, _lib.fp4gemv_token_logprobs)))
 _nvfp4_gemv = _lib.fp4gemv_nvfp4_gemv
 
 
@@ -375,13 +382,10 @@ def moe_down_combine(act, ids, tw, w2, w2_sf, alpha2, sact, wsd, ssd, gssd, out,
 
 
 # ---- the decode step's operators around the products ----
-_DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
-_moe_route = _lib.fp4gemv_moe_route
-_token_logprobs = _lib.fp4gemv_token_logprobs
+_moe_route = _marshal.moe_route
+_token_logprobs = _marshal.token_logprobs
 _I32 = torch.int32
 _F32 = torch.float32
-_LOGITS = "logits must be a 2-D bf16, f16 or fp32 CUDA tensor with unit inner stride"
 
 
 def moe_route(logits: torch.Tensor, topk: int, scores: str = "softmax", bias: torch.Tensor | None = None,
@@ -398,35 +402,12 @@ def moe_route(logits: torch.Tensor, topk: int, scores: str = "softmax", bias: to
     ``topk_group`` groups whose ``group_top`` largest keys have the largest
     sum.  Weights are the scores, divided by their sum with ``renormalize``,
     times ``scale``."""
-    code, shape, index = _DTYPE_CODES.get(logits.dtype), logits.shape, logits.get_device()
-    if code is None or len(shape) != 2 or index < 0:
-        raise ValueError(_LOGITS)
-    M, E = shape
-    ld, inner = logits.stride()
-    if inner != 1:
-        raise ValueError(_LOGITS)
-    kind = _ROUTE_SCORES.get(scores)
-    if kind is None:
-        raise ValueError(f"scores must be 'softmax' or 'sigmoid', not {scores!r}")
-    if bias is not None and (bias.dtype is not _F32 or bias.shape != (E,) or not bias.is_contiguous() or
-                             bias.get_device() != index):
-        raise ValueError(f"bias must be a contiguous fp32 [{E}] tensor on the logits' device")
-    want = (M, topk)
     if ids is None:
-        ids = torch.empty(want, dtype=_I32, device=logits.device)
-    elif ids.dtype is not _I32 or ids.shape != want or not ids.is_contiguous() or ids.get_device() != index:
-        raise ValueError(f"ids must be a contiguous int32 [{M}, {topk}] tensor on the logits' device")
+        ids = torch.empty((*logits.shape[:1], topk), dtype=_I32, device=logits.device)
     if weights is None:
-        weights = torch.empty(want, dtype=_F32, device=logits.device)
-    elif weights.dtype is not _F32 or weights.shape != want or not weights.is_contiguous() or \
-            weights.get_device() != index:
-        raise ValueError(f"weights must be a contiguous fp32 [{M}, {topk}] tensor on the logits' device")
-    if M == 0:
-        return ids, weights
-    status = _moe_route(logits.data_ptr(), ld if M > 1 else E, code, M, E, topk, kind,
-                        bias.data_ptr() if bias is not None else None, n_group, topk_group, group_top,
-                        1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), 1 if pdl else 0,
-                        _raw_stream(index))
+        weights = torch.empty((*logits.shape[:1], topk), dtype=_F32, device=logits.device)
+    status = _moe_route(logits, topk, scores, bias, n_group, topk_group, group_top, renormalize, scale, ids, weights,
+                        pdl)
     if status:
         raise Fp4GemvError(status, "fp4gemv_moe_route")
     return ids, weights
@@ -449,43 +430,14 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top_n: int = 0, t
 
     ``logits`` bf16, f16 or fp32 [T, V] with unit inner stride and any row
     stride; ``out``: tensors to write into, laid out as the result."""
-    code, shape, index = _DTYPE_CODES.get(logits.dtype), logits.shape, logits.get_device()
-    if code is None or len(shape) != 2 or index < 0:
-        raise ValueError(_LOGITS)
-    T, V = shape
-    ld, inner = logits.stride()
-    if inner != 1:
-        raise ValueError(_LOGITS)
-    if tokens.dtype is not _I32 or tokens.shape != (T,) or not tokens.is_contiguous() or \
-            tokens.get_device() != index:
-        raise ValueError(f"tokens must be a contiguous int32 [{T}] tensor on the logits' device")
-    if not temperature > 0:
-        raise ValueError("temperature must be positive")
     if out is None:
-        dev = logits.device
+        T, dev = logits.shape[0] if logits.dim() else 0, logits.device
         out = TokenLogprobs(torch.empty(T, dtype=_F32, device=dev), torch.empty(T, dtype=_I32, device=dev),
                             torch.empty(T, dtype=_F32, device=dev), torch.empty(T, top_n, dtype=_I32, device=dev),
                             torch.empty(T, top_n, dtype=_F32, device=dev))
-    else:
-        logprob, rank, entropy, top_ids, top_logprobs = out
-        row, top = (T,), (T, top_n)
-        if not (logprob.dtype is _F32 and rank.dtype is _I32 and entropy.dtype is _F32 and top_ids.dtype is _I32 and
-                top_logprobs.dtype is _F32 and logprob.shape == row and rank.shape == row and entropy.shape == row and
-                top_ids.shape == top and top_logprobs.shape == top and logprob.is_contiguous() and
-                rank.is_contiguous() and entropy.is_contiguous() and top_ids.is_contiguous() and
-                top_logprobs.is_contiguous() and logprob.get_device() == index and rank.get_device() == index and
-                entropy.get_device() == index and top_ids.get_device() == index and
-                top_logprobs.get_device() == index):
-            raise ValueError("out must hold contiguous logprob fp32 [T], rank int32 [T], entropy fp32 [T], "
-                             "top_ids int32 [T, top_n] and top_logprobs fp32 [T, top_n] on the logits' device")
-        if out.__class__ is not TokenLogprobs:
-            out = TokenLogprobs(*out)
-    if T == 0:
-        return out
-    status = _token_logprobs(logits.data_ptr(), ld if T > 1 else V, code, T, V, tokens.data_ptr(),
-                             1.0 / temperature, top_n, out.logprob.data_ptr(), out.rank.data_ptr(),
-                             out.entropy.data_ptr(), out.top_ids.data_ptr() if top_n else None,
-                             out.top_logprobs.data_ptr() if top_n else None, 1 if pdl else 0, _raw_stream(index))
+    elif out.__class__ is not TokenLogprobs:
+        out = TokenLogprobs(*out)
+    status = _token_logprobs(logits, tokens, top_n, temperature, *out, pdl)
     if status:
         raise Fp4GemvError(status, "fp4gemv_token_logprobs")
     return out

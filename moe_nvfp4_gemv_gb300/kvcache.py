@@ -24,13 +24,12 @@ import math
 
 import torch
 
-from . import fp4gemv
-from .fp4gemv import Fp4GemvError, _lib, _raw_stream
+from .fp4gemv import Fp4GemvError, _lib, _marshal, _raw_stream
 
 FORMATS = {"e4m3": 0, "int8": 1}
-_BF16, _F16, _I32, _F32 = torch.bfloat16, torch.float16, torch.int32, torch.float32
-_append = _lib.fp4gemv_kv_append
-_attend = _lib.fp4gemv_kv_attention
+_F32 = torch.float32
+_append = _marshal.kv_append
+_attend = _marshal.kv_attention
 
 
 class _CacheStruct(ctypes.Structure):
@@ -104,33 +103,8 @@ class KvCache8:
         any token stride that is a multiple of 8) to B sequences: T / B tokens
         each, or tokens cu_new[b] .. cu_new[b + 1] (int32 [B + 1]) to sequence
         b.  ``seq_lens``: the lengths with the new tokens."""
-        index, shape = self._index, block_table.shape
-        if block_table.dtype is not _I32 or len(shape) != 2 or not block_table.is_contiguous() or \
-                block_table.get_device() != index:
-            raise ValueError("block_table must be a contiguous int32 [B, max_blocks] tensor on the cache's device")
-        B, max_blocks = shape
-        if seq_lens.dtype is not _I32 or seq_lens.numel() != B or not seq_lens.is_contiguous() or \
-                seq_lens.get_device() != index:
-            raise ValueError(f"seq_lens must be a contiguous int32 [{B}] tensor on the cache's device")
-        H, D = self.kv_heads, self.head_dim
-        shape, dtype, ks, vs = k.shape, k.dtype, k.stride(), v.stride()
-        if (dtype is not _BF16 and dtype is not _F16) or v.dtype is not dtype or len(shape) != 3 or shape[1] != H or \
-                shape[2] != D or v.shape != shape or k.get_device() != index or v.get_device() != index or \
-                ks[2] != 1 or vs[2] != 1 or (H > 1 and (ks[1] != D or vs[1] != D)):
-            raise ValueError(f"k and v must be bf16 or f16 [T, {H}, {D}] tensors of one type on the cache's device "
-                             "with contiguous heads")
-        T = shape[0]
-        if cu_new is not None and (cu_new.dtype is not _I32 or cu_new.numel() != B + 1 or
-                                   not cu_new.is_contiguous() or cu_new.get_device() != index):
-            raise ValueError(f"cu_new must be a contiguous int32 [{B + 1}] tensor on the cache's device")
-        if T == 0 or B == 0:
-            if T:
-                raise ValueError("new tokens for no sequence")
-            return
-        status = _append(self._handle, k.data_ptr(), ks[0] if T > 1 else H * D, v.data_ptr(),
-                         vs[0] if T > 1 else H * D, 0 if dtype is _BF16 else 1, T,
-                         cu_new.data_ptr() if cu_new is not None else None, block_table.data_ptr(), max_blocks,
-                         seq_lens.data_ptr(), B, 1 if pdl else 0, _raw_stream(index))
+        status = _append(self._handle, self._index, self.kv_heads, self.head_dim, k, v, block_table, seq_lens, cu_new,
+                         pdl)
         if status:
             raise Fp4GemvError(status, "fp4gemv_kv_append")
 
@@ -144,50 +118,15 @@ class KvCache8:
         that sees none gives zeros.  ``sm_scale`` defaults to 1 /
         sqrt(head_dim); ``lse``: fp32 [B, q_len, heads] to receive the natural
         log of the softmax's sums.  Returns ``out``."""
-        index, shape = self._index, block_table.shape
-        if block_table.dtype is not _I32 or len(shape) != 2 or not block_table.is_contiguous() or \
-                block_table.get_device() != index:
-            raise ValueError("block_table must be a contiguous int32 [B, max_blocks] tensor on the cache's device")
-        B, max_blocks = shape
-        if seq_lens.dtype is not _I32 or seq_lens.numel() != B or not seq_lens.is_contiguous() or \
-                seq_lens.get_device() != index:
-            raise ValueError(f"seq_lens must be a contiguous int32 [{B}] tensor on the cache's device")
-        D = self.head_dim
-        shape, dtype = q.shape, q.dtype
-        if (dtype is not _BF16 and dtype is not _F16) or len(shape) != 4 or shape[0] != B or shape[3] != D or \
-                q.get_device() != index:
-            raise ValueError(f"q must be a bf16 or f16 [{B}, q_len, heads, {D}] tensor on the cache's device")
-        _, n, heads, _ = shape
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=self.device)
-        elif out.dtype is not dtype or out.shape != shape or out.get_device() != index:
-            raise ValueError("out must have q's shape, type and device")
-        ldq = heads * D if q.is_contiguous() else self._token_stride(q.stride(), shape, "q")
-        ldo = heads * D if out.is_contiguous() else self._token_stride(out.stride(), shape, "out")
-        if lse is not None and (lse.dtype is not _F32 or lse.numel() != B * n * heads or not lse.is_contiguous() or
-                                lse.get_device() != index):
-            raise ValueError(f"lse must be a contiguous fp32 [{B}, {n}, {heads}] tensor on the cache's device")
-        if B == 0:
-            return out
-        stream = _raw_stream(index)
+            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
         if workspace is None:
-            workspace = _workspaces.get((index, stream, D))
+            stream = _raw_stream(self._index)
+            workspace = _workspaces.get((self._index, stream, self.head_dim))
             if workspace is None:
-                workspace = attention_workspace(self.device, D, stream)
-        status = _attend(self._handle, q.data_ptr(), ldq, 0 if dtype is _BF16 else 1, heads, n,
-                         block_table.data_ptr(), max_blocks, seq_lens.data_ptr(), B,
-                         self._sm_scale if sm_scale is None else sm_scale, window, out.data_ptr(), ldo,
-                         lse.data_ptr() if lse is not None else None, workspace.data_ptr(), workspace.nbytes,
-                         1 if pdl else 0, stream)
+                workspace = attention_workspace(self.device, self.head_dim, stream)
+        status = _attend(self._handle, self._index, self.head_dim, q, block_table, seq_lens,
+                         self._sm_scale if sm_scale is None else sm_scale, window, out, lse, workspace, pdl)
         if status:
             raise Fp4GemvError(status, "fp4gemv_kv_attention")
         return out
-
-    @staticmethod
-    def _token_stride(strides: tuple, shape: tuple, name: str) -> int:
-        """The one stride between tokens of a [B, n, heads, head_dim] tensor."""
-        B, n, heads, dim = shape
-        sb, sn, sh, sd = strides
-        if sd != 1 or (sh != dim and heads > 1) or (n > 1 and B > 1 and sb != n * sn):
-            raise ValueError(f"{name} must have contiguous heads and one stride between all its tokens")
-        return sn if n > 1 else sb if B > 1 else heads * dim

@@ -125,3 +125,48 @@ def test_reference_route_groups():
     assert ref.route(x, 2, "softmax", n_group=3, topk_group=1)[0].tolist() == [[4, 5]]
     ids, w, _ = ref.route(np.zeros((1, 4)), 2, "sigmoid")
     assert ids.tolist() == [[0, 1]] and w.tolist() == [[0.5, 0.5]]
+
+
+# ---- the Python calls' own checks (no GPU is touched) ----
+def test_python_calls_refuse_what_is_no_cuda_tensor():
+    torch = pytest.importorskip("torch")
+    from moe_nvfp4_gemv_gb300 import fp4gemv, kvcache
+    logits = torch.zeros(2, 8)
+    ids, weights = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2)
+    with pytest.raises(ValueError, match="logits"):
+        fp4gemv.moe_route(logits, 2, ids=ids, weights=weights)
+    with pytest.raises(ValueError, match="logits"):
+        fp4gemv.token_logprobs(logits, torch.zeros(2, dtype=torch.int32))
+    for bad in (None, 3, [1.0], "x"):
+        with pytest.raises(TypeError, match="logits must be a tensor"):
+            fp4gemv.moe_route(bad, 2, ids=ids, weights=weights)
+    cache = kvcache.KvCache8.allocate(2, 1, 64, 16, device="cpu")
+    k, table, lens = torch.zeros(1, 1, 64, dtype=torch.bfloat16), torch.zeros(1, 2, dtype=torch.int32), \
+        torch.ones(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="block_table"):
+        cache.append(k, k, table, lens)
+    with pytest.raises(TypeError, match="k must be a tensor"):
+        cache.append(None, k, table, lens)
+    with pytest.raises(ValueError, match="block_table"):
+        cache.attend(k[None], table, lens, out=k[None], workspace=torch.zeros(4))
+
+
+def test_marshalling_refuses_a_wrong_number_or_kind_of_arguments():
+    from moe_nvfp4_gemv_gb300.fp4gemv import _marshal
+    for fn, count in ((_marshal.kv_append, 10), (_marshal.kv_attention, 12), (_marshal.moe_route, 12),
+                      (_marshal.token_logprobs, 10), (_marshal.bind, 4)):
+        with pytest.raises(TypeError):
+            fn()
+        with pytest.raises(TypeError):
+            fn(*[None] * (count + 1))
+        with pytest.raises(TypeError):
+            fn(*["x"] * count)
+
+
+def test_lengths_past_thirty_bits_are_refused(fp4):
+    """Places in a sequence, and new tokens, are 32-bit numbers on the device."""
+    assert attend(fp4, max_blocks=(1 << 26) + 1) == 2  # 16-token pages: past 2^30 tokens
+    c = struct()
+    for T, max_blocks, B in ((1, (1 << 26) + 1, 1), ((1 << 30) + 1, 4, 1)):
+        assert fp4.lib().fp4gemv_kv_append(ctypes.addressof(c), None, 256, None, 256, 0, T, None, None, max_blocks, None,
+                                           B, 1, None) == 2
