@@ -238,10 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) kv_append_kernel(co
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 f = unpack(w[j]);
-          const float n0 = __fmaf_rn(f.x, inv, 12582912.0f), n1 = __fmaf_rn(f.y, inv, 12582912.0f);
-          bits[2 * j] = __float_as_uint(n0), bits[2 * j + 1] = __float_as_uint(n1);
-          far = fmaxf(far, fmaxf(fabsf(__fmaf_rn(f.x, inv, __fsub_rn(12582912.0f, n0))),
-                                 fabsf(__fmaf_rn(f.y, inv, __fsub_rn(12582912.0f, n1)))));
+          const uint64_t x = pair(f.x, f.y), round = pair(12582912.0f, 12582912.0f), inv2 = pair(inv, inv);
+          const uint64_t near = fma2(x, inv2, round);
+          const float2 n = unpair(near), rest = unpair(fma2(x, inv2, fma2(near, pair(-1.0f, -1.0f), round)));
+          bits[2 * j] = __float_as_uint(n.x), bits[2 * j + 1] = __float_as_uint(n.y);
+          far = fmaxf(far, fmaxf(fabsf(rest.x), fabsf(rest.y)));
         }
         if (far > 0.49995f) again |= 1u << i;
 #pragma unroll

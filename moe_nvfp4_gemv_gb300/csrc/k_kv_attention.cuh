@@ -199,8 +199,40 @@ __device__ __forceinline__ void attn_plan(const KvAttnParams& p, int* strips_bef
     for (int b = tid; b < p.B; b += kThreads) tokens[b] = length(b);
     __syncthreads();
   }
-  if (warp == 0) {
-    const int ctas = static_cast<int>(gridDim.x);
+  const int ctas = static_cast<int>(gridDim.x);
+  if (p.B == 1 && items <= ctas) {
+    // one sequence: as many pieces of each item as there are CTAs for, without the sums over sequences below (777 tokens:
+    // 7.4 us, with them 8.6)
+    if (warp == 0) {
+      const int n = length(0), s = n > 0 ? attn_strips_of(p, n) : 0;
+      const int most = attn_div_up(ctas + 1, items, __fdividef(1.0f, static_cast<float>(items))) - 1;
+      const int per = max(whole(attn_div_up(s, most, __fdividef(1.0f, static_cast<float>(most)))), kAttnRound);
+      const int pieces = max(attn_div_up(s, per, __fdividef(1.0f, static_cast<float>(per))), 1);
+      const int cta = static_cast<int>(blockIdx.x);
+      const int item = attn_div_up(cta + 1, pieces, __fdividef(1.0f, static_cast<float>(pieces))) - 1;
+      const int strip = (cta - item * pieces) * per;
+      if (lane == 0) {
+        AttnPlace place;
+        place.b = 0;
+        place.first = attn_first_strip(p, n);
+        place.strips = s;
+        place.item = item;
+        place.strip = strip;
+        place.head = p.row_tiles == 1 ? item : item / p.row_tiles;
+        place.tile = item - place.head * p.row_tiles;
+        places[0] = places[2] = place;
+        tokens[0] = n;
+        strips_before[0] = line_before[0] = 0;
+        strips_before[1] = s * items;
+        line_before[1] = per * pieces * items;
+        plan_words[0] = item < items ? item * s + strip : s * items;
+        plan_words[1] = item < items ? item * s + min(strip + per, s) : s * items;
+        plan_words[2] = per;
+        plan_words[3] = 0;
+        plan_words[4] = 1;
+      }
+    }
+  } else if (warp == 0) {
     int n0 = 0;  // the lane's sequence, where there are few
     if (few && lane < p.B) {
       n0 = length(lane);
