@@ -164,6 +164,7 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
       return FP4GEMV_ERR_CUDA;
     p.unit = 8;  // tiles of 128 tokens are of whole pages
     p.item_cost = fp4::kAttnTcItemCost;
+    p.skip_tile = fp4::skipped_stage();
     return from_cuda(fp4::launch_kv_attention_tc(p, sms, pdl, stream));
   }
   return from_cuda(fp4::launch_kv_attention(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms, pdl,

@@ -14,6 +14,8 @@ namespace fp4 {
 // launch counter.
 fp4gemv_status current_device_state(uint32_t** err, int* sms);
 void count_launch();
+// The test hook's stage (fp4gemv_debug_skip_stage), -1: none.
+int skipped_stage();
 // A tensor map of [pages][block_size][128] bytes in boxes of a page.
 bool encode_pages_128(CUtensorMap* m, const void* base, int block_size, int64_t pages);
 

@@ -19,6 +19,7 @@
 namespace fp4 {
 fp4gemv_status current_device_state(uint32_t** err, int* sms);  // (decode_launch.h)
 void count_launch();
+int skipped_stage();
 bool encode_pages_128(CUtensorMap* m, const void* base, int block_size, int64_t pages);
 
 // Per-device error state (one copy per device context of this library image):
@@ -175,6 +176,7 @@ namespace fp4 {
 // For the decode step's operators (decode_api.cu).
 fp4gemv_status current_device_state(uint32_t** err, int* sms) { return device_state(err, sms); }
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+int skipped_stage() { return g_skip_stage.load(std::memory_order_relaxed); }
 bool encode_pages_128(CUtensorMap* m, const void* base, int block_size, int64_t pages) {
   MapKey k;
   std::memset(&k, 0, sizeof(k));

@@ -81,6 +81,7 @@ struct KvAttnParams {
 struct KvAttnTcParams : KvAttnParams {
   CUtensorMap k_map;  // [num_blocks kv_heads][block_size][128] bytes, boxes of a page, 128-byte swizzle
   CUtensorMap v_map;
+  int skip_tile;      // test hook: V of this tile of every CTA is not brought (-1: of none)
 };
 
 constexpr int kAttnMaxRows = 32;  // rows of a row tile at most

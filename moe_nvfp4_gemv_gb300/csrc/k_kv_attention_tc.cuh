@@ -44,7 +44,8 @@
 //
 // Every wait is bounded.  After a failed one (the error word holds
 // FP4_ERR_TIMEOUT) the waits that follow are skipped, so that all roles come to
-// their ends, named barriers included.
+// their ends, named barriers included, and the outputs of the items concerned
+// are NaN.
 #pragma once
 
 #include "k_kv_attention.cuh"
@@ -140,12 +141,13 @@ __device__ __forceinline__ void named_sync(int threads) {
 __device__ __forceinline__ void group_sync(int group) {
   asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + group) : "memory");
 }
-__device__ __forceinline__ bool group_any(int group, bool v) {
+// Barrier `id` of `threads` threads: whether v holds for any.
+__device__ __forceinline__ bool named_any(int id, int threads, bool v) {
   uint32_t r;
   asm volatile(
-      "{ .reg .pred p, q; setp.ne.u32 p, %2, 0; barrier.cta.red.or.pred.aligned q, %1, 128, p; selp.u32 %0, 1, 0, q; }"
+      "{ .reg .pred p, q; setp.ne.u32 p, %3, 0; barrier.cta.red.or.pred.aligned q, %1, %2, p; selp.u32 %0, 1, 0, q; }"
       : "=r"(r)
-      : "r"(1 + group), "r"(static_cast<uint32_t>(v))
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(v))
       : "memory");
   return r != 0;
 }
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
   __shared__ int plan_words[6];
   __shared__ int last_flag;
   __shared__ uint32_t tmem_slot;
-  __shared__ __align__(8) uint64_t bars[2 * (C::kKStages + C::kVStages) + 4 * C::kGroups];
+  __shared__ __align__(8) uint64_t bars[2 * (C::kKStages + C::kVStages) + 5 * C::kGroups];
   __shared__ __align__(16) float row_factor[C::kRows];             // of the scores
   __shared__ __align__(16) float row_m[C::kGroups][C::kRows];
   __shared__ __align__(16) float row_base[C::kGroups][C::kRows];   // kWScale - m; 0 while there is no m to go by
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
   auto taken = [&](int g) -> uint32_t { return bar0 + 8 * (kBars + 2 + g); };    // S has been read
   auto weighed = [&](int g) -> uint32_t { return bar0 + 8 * (kBars + 4 + g); };  // the weights are there
   auto added = [&](int g) -> uint32_t { return bar0 + 8 * (kBars + 6 + g); };    // the sums are
+  auto idle = [&](int g) -> uint32_t { return bar0 + 8 * (kBars + 8 + g); };     // no MMA is in flight any more
   int* const strips_before = reinterpret_cast<int*>(smem + C::kSeqOff);
   int* const line_before = strips_before + p.B + 1;
   int* const tokens = line_before + p.B + 1;
@@ -211,6 +214,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
       mbar_init(taken(g), 128);
       mbar_init(weighed(g), 128);
       mbar_init(added(g), 1);
+      mbar_init(idle(g), 1);
     }
     mbar_fence_init();
     prefetch_tensormap(&p.k_map);
@@ -292,9 +296,10 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
       const uint32_t pages = __popc(__ballot_sync(0xFFFFFFFFu, want) & 0xFFu);
       const bool good = id >= 0 && id < p.num_blocks;
       const int page = good ? id * p.kv_heads + head : p.num_blocks * p.kv_heads;  // (past the map: zeros)
-      if (lane == 0) mbar_arrive_expect_tx(bar, pages * page_bytes);
+      const bool skip = v && tile == p.skip_tile;
+      if (lane == 0 && !skip) mbar_arrive_expect_tx(bar, pages * page_bytes);
       __syncwarp();
-      if (lane < 8 && want) {
+      if (lane < 8 && want && !skip) {
         if (!good) raise_error(p.err, FP4_ERR_BADIDX);
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
                        "l"(scale), "r"(good ? 4u : 0u)
                        : "memory");
         }
-        cp_async_arrive_noinc(bar);
+        if (!skip) cp_async_arrive_noinc(bar);
       }
       filled = min(filled + 1, stages);
       if (++stage == stages) {
@@ -381,6 +386,9 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
       at = seg_end;
       if (at < end) cur = attn_next(p, cur, strips_before, tokens);
     }
+    if (elect_one()) mma_commit(idle(g));
+    __syncwarp();
+    mbar_wait(idle(g), 0, p.err);
   } else {
     // ---- weights and sums ----
     const int g = warp >> 2, who = tid & 127;  // token of the tile, dim of the sums
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
           }
         }
         if (j > j0) wait(added(g), (count - 1) & 1);  // the sums so far; the weights' tile is free
-        if (group_any(g, masked || fresh || top > C::kSlack + C::kWScale)) {
+        if (named_any(1 + g, 128, masked || fresh || top > C::kSlack + C::kWScale)) {
           // ---- masks; the running maxima move ----
           float v[32];
 #pragma unroll
@@ -627,7 +635,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
 #pragma unroll
         for (int r = 0; r < 32; ++r) mine[r * C::kDim + who] = any ? fmaf(low[r], 0.0009765625f, o[r]) : 0.0f;
       }
-      named_sync<3>(C::kWeighers);
+      const bool failed = named_any(3, C::kWeighers, !ok);  // (some wait ran out: NaN)
       const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
       const AttnItemEnd<C::kDim, C::kWeighers> item_end = {p, cur, row0, used};
       float* const part = item_end.part_of(blockIdx.x, starts ? 1 : 0);
@@ -643,7 +651,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         const float4 u = *reinterpret_cast<const float4*>(a);
         const float4 w = *reinterpret_cast<const float4*>(a + C::kTileBytes / 4);
         const float4 v = make_float4(u.x * f0 + w.x * f1, u.y * f0 + w.y * f1, u.z * f0 + w.z * f1, u.w * f0 + w.w * f1);
-        const float l = l0 * f0 + l1 * f1;
+        const float l = failed ? __int_as_float(0x7FC00000) : l0 * f0 + l1 * f1;
         // (weights are 2^kWScale of what m says)
         if (whole) {
           item_end.store(r, d, v, top - C::kWScale, l);

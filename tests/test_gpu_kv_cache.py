@@ -624,3 +624,32 @@ def test_attention_wide_bad_pages_non_finite_and_streams(kv, fp4):
                 got.append(cache.attend(q, tab, n))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in got)
+
+
+@pytest.mark.parametrize("lens,skip,met", [([700, 64], 0, True), ([4000, 300, 2000], 0, True), ([20000], 2, True),
+                                           ([4000, 300, 2000], 1, False)])
+def test_attention_wide_timeout_then_recovery(kv, fp4, lens, skip, met):
+    """A tile's values that never come (a host-side hook; nothing is in flight): the call comes back, the error word
+    reads a timeout, outputs are NaN where the tile was missing; the next calls on the same workspace are right.  (The
+    last case's 100 tiles are a CTA's first ones each: the hook's second is nobody's.)"""
+    g = gen(30)
+    table, pages = make_table(lens, 64, g)
+    c = scaled(random_cache(pages, 2, 64, 128, g, 1.0), "e4m3")
+    cache = on_gpu(kv, c, "e4m3")
+    q = torch.randn(len(lens), 3, 16, 128, generator=g).to(torch.bfloat16).to(DEV)
+    tab, n = table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    good = cache.attend(q, tab, n)
+    assert fp4.get_device_error() == 0
+    try:
+        fp4.set_wait_limit_ns(5_000_000)
+        fp4.debug_skip_stage(skip)
+        lost = cache.attend(q, tab, n)
+        assert fp4.get_device_error() == (5 if met else 0)
+    finally:
+        fp4.debug_skip_stage(-1)
+        fp4.set_wait_limit_ns(0)
+    whole = ~lost.isnan().any(-1)
+    assert whole.all() != met and torch.equal(lost[whole], good[whole])
+    for _ in range(2):
+        assert torch.equal(cache.attend(q, tab, n), good)
+    assert fp4.get_device_error() == 0
