@@ -107,7 +107,8 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
       B > FP4GEMV_KV_MAX_BATCH)
     return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
   // row tiles: the 8, 16 or 32 rows that a pass over the codes serves
-  // (head_dim 256 has registers for 16)
+  // (head_dim 256 has registers for 16).  One pass of 16 rows or two of 8, 32
+  // sequences of 16384 tokens, 8 KV heads: 185 us against 350.
   const int rows = q_len * group;
   const int row_units = rows <= 8 ? 1 : rows <= 16 || cache->head_dim > 128 ? 2 : 4;
   const int row_tiles = (rows + 8 * row_units - 1) / (8 * row_units);

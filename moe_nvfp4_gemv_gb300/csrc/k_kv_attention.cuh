@@ -41,6 +41,18 @@
 // from fp32 partials in the workspace: the last of up to kAttnFan CTAs to
 // arrive joins theirs; with more, the last of every kAttnFan2, and the last of
 // those the joined ones (counters that are left at zero).  Nothing waits on another CTA.
+//
+// What bounds it (fractions of the measured copy bandwidth on the codes and
+// scales read).  Long caches: HBM; 32 sequences of 16384 tokens, 8 KV heads of
+// 128, us: E4M3 182 (0.88), INT8 186 (0.87), 16 rows 184 (0.88); heads of 64 97
+// (0.83), of 96 141 (0.86), of 256 (16 sequences) 167 (0.96); pages of 16 tokens
+// 186.  Fewer bytes: the launch, the plan, the first strips' latency and the
+// joining, 8 us together: 24 ragged ones of up to 8191 tokens 45.6 us (0.69), one
+// of 131071 (INT8) 50.9 (0.79), one of 777 7.4, one of 16 4.9.  32 rows: issue
+// (INT8 279 us, 0.58; E4M3 of 128 is k_kv_attention_tc.cuh's).  Measured and not
+// taken: more shares than resident CTAs (24 ragged 46 to 51 .. 73 us: every CTA
+// pays for its plan and first strips), two warps on one ring that part the rows
+// or the dims of 32 rows between them (260 to 344 and 334 us).
 #pragma once
 
 #include <cuda.h>
@@ -86,12 +98,16 @@ struct KvAttnTcParams : KvAttnParams {
 
 constexpr int kAttnMaxRows = 32;  // rows of a row tile at most
 constexpr int kAttnRound = 8;     // strips of a round, one for each warp: shares are whole rounds
-constexpr int kAttnFan = 40;      // partials that one CTA joins at once
-constexpr int kAttnFan2 = 20;     // ... where the joined ones are joined again
-constexpr int kAttnItemCost = 16;  // an item's end, in strips
-constexpr int kAttnTcItemCost = 64;  // ... of the kernel on the 5th-generation tensor core
+// Partials that one CTA joins at once, and where the joined ones are joined again.  One sequence of 131072 tokens on one
+// KV head, 8 rows: 16.3 us; all 152 partials at once 23.0.
+constexpr int kAttnFan = 40;
+constexpr int kAttnFan2 = 20;
+// An item's end, in strips.  256 sequences of 500 tokens, 8 KV heads: 66 us with 8 or 16, 63 with 32.
+constexpr int kAttnItemCost = 32;
+constexpr int kAttnTcItemCost = 64;  // ... of the kernel on the 5th-generation tensor core (its figures there)
 constexpr float kAttnFloor = -1e30f;  // the running maximum before any token
-constexpr float kAttnSlack = 8.0f;    // log2 of the largest weight before the running maximum moves
+// log2 of the largest weight before the running maximum moves.  256 sequences of 500 tokens: 66 us; with 0 68.8.
+constexpr float kAttnSlack = 8.0f;
 
 __device__ __forceinline__ float attn_ex2(float x) {
   float y;

@@ -90,6 +90,34 @@ def test_route_bias_large_batch(fp4):
     check_route(fp4, x[:, :100], 8, "sigmoid", bias[:100])  # a strided view of the rows
 
 
+def many_tokens():
+    """So many that up to 64 experts are routed on 8 lanes per token; not a whole number of CTAs."""
+    return 64 * torch.cuda.get_device_properties(0).multi_processor_count + 5
+
+
+@pytest.mark.parametrize("E,topk,kind,renorm,dtype", [
+    (1, 1, "softmax", True, "bf16"), (7, 7, "sigmoid", True, "f16"), (8, 3, "softmax", False, "f32"),
+    (33, 32, "softmax", False, "bf16"), (60, 4, "softmax", True, "f32"), (64, 8, "sigmoid", False, "bf16"),
+    (64, 32, "softmax", True, "f16")])
+def test_route_many_tokens(fp4, E, topk, kind, renorm, dtype):
+    x = (torch.randn(many_tokens(), E, generator=gen(E)) * 2).to(TYPES[dtype])
+    x[3::7, E // 2] = -math.inf
+    x[5::11, 0] = math.nan
+    check_route(fp4, x, topk, kind, exact=True, renormalize=renorm, scale=0.6)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group,topk_group,group_top,topk", [(60, 4, 2, 2, 6), (64, 32, 31, 2, 20), (64, 8, 3, 1, 8),
+                                                                 (30, 10, 4, 2, 9), (32, 4, 1, 2, 8)])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_route_many_tokens_groups(fp4, kind, E, n_group, topk_group, group_top, topk, with_bias):
+    g = gen(E * n_group)
+    x = torch.randn(many_tokens(), E, generator=g)
+    bias = torch.randn(E, generator=g) * 0.1 if with_bias else None
+    check_route(fp4, x, topk, kind, bias, n_group=n_group, topk_group=topk_group, group_top=group_top,
+                exact=not with_bias and group_top == 1)
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_route_ties_and_special_values(fp4, kind):
     E = 96
