@@ -157,7 +157,6 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   p.item_cost = fp4::kAttnItemCost;
   p.f16 = dtype == FP4GEMV_F16;
   p.sm_scale = sm_scale;
-  fp4::count_launch();
   if (row_units == 4 && cache->head_dim == 128 && cache->format == FP4GEMV_KV_E4M3) {
     const int64_t pages = static_cast<int64_t>(cache->num_blocks) * cache->kv_heads;
     if (!fp4::encode_pages_128(&p.k_map, cache->k_codes, cache->block_size, pages) ||
@@ -166,8 +165,10 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
     p.unit = 8;  // tiles of 128 tokens are of whole pages
     p.item_cost = fp4::kAttnTcItemCost;
     p.skip_tile = fp4::skipped_stage();
+    fp4::count_launch();
     return from_cuda(fp4::launch_kv_attention_tc(p, sms, pdl, stream));
   }
+  fp4::count_launch();
   return from_cuda(fp4::launch_kv_attention(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms, pdl,
                                             stream));
 }

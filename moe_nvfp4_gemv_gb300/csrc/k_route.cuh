@@ -19,7 +19,7 @@
 //
 // What bounds it.  Few tokens: the launch (one token of 128 experts, top 8:
 // 1.9 us; 96 tokens of 256 with 8 groups 3.5).  Many: the selection's
-// instructions, issue slots 64 % taken (20011 tokens of 60 experts, top 6, fp32:
+// instructions, issue slots 64 % taken (20011 tokens of 60 experts, top 4, fp32:
 // 7.1 us, where reading and writing would take 0.8; one warp per token 12.4).
 #pragma once
 

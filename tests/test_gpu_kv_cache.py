@@ -653,3 +653,14 @@ def test_attention_wide_timeout_then_recovery(kv, fp4, lens, skip, met):
     for _ in range(2):
         assert torch.equal(cache.attend(q, tab, n), good)
     assert fp4.get_device_error() == 0
+
+
+@pytest.mark.parametrize("B", [33, 300, 1024])
+def test_attention_wide_batch_sizes(kv, B):
+    """Up to the largest batch (the plan's tables fill shared memory to its end), idle sequences among them."""
+    lens = [(11 * i) % 150 for i in range(B)]
+    g = gen(B)
+    table, pages = make_table(lens, 32, g)
+    c = scaled(random_cache(pages, 1, 32, 128, g, 1.0), "e4m3")
+    q = torch.randn(B, 2, 9, 128, generator=g).to(torch.bfloat16).to(DEV)
+    check_attention(kv, q, c, table, lens, "e4m3", "bf16")
