@@ -96,6 +96,10 @@ size_t fp4gemv_kv_attention_workspace_bytes(int head_dim);
  * Numerics: codes and queries are exact f16 operands (queries scaled by a
  * power of two for each row), sums, maxima and statistics fp32,
  * probabilities rounded to f16 for the product with V, one final rounding.
+ * With E4M3, head_dim 128 and more than 16 rows (q_len heads / kv_heads) both
+ * become sums of E4M3 parts: entries of a query below 2^-14 (f16: 2^-11) of
+ * its largest are rounded at 2^-22 of that, probabilities below 2^-12 of the
+ * largest at 2^-24; an infinite entry counts as NaN.
  * Page memory past seq_lens is never used, whatever it holds.  Lengths
  * outside [0, max_blocks * block_size] are clamped, and tokens on a page id
  * outside [0, num_blocks) read as zeros; both raise FP4GEMV_ERR_BAD_INDEX.
@@ -103,7 +107,10 @@ size_t fp4gemv_kv_attention_workspace_bytes(int head_dim);
  * 16-byte aligned.
  * Shapes: 1 <= B <= FP4GEMV_KV_MAX_BATCH, 1 <= q_len <= FP4GEMV_KV_MAX_QLEN,
  *   heads a multiple of kv_heads, at most FP4GEMV_KV_MAX_GROUP times it,
- *   window >= 0, sm_scale finite. */
+ *   window >= 0, sm_scale finite.  FP4GEMV_ERR_UNSUPPORTED_SHAPE also where
+ *   max_blocks * block_size is above 2^30, or, with the passes over 8, 16 or
+ *   32 rows that a KV head takes, kv_heads * passes is 2^20 or more or
+ *   (max_blocks * block_size / 16 + 72) * B * kv_heads * passes 1.2e9. */
 fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype, int heads,
                                     int q_len, const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
                                     int B, float sm_scale, int window, void* out, int64_t ldo, float* lse,

@@ -114,7 +114,7 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   const int row_tiles = (rows + 8 * row_units - 1) / (8 * row_units);
   const int64_t tokens = static_cast<int64_t>(max_blocks) * cache->block_size;
   // (32-bit: places on the line of strips, a quarter more with padding, and strips of the cache)
-  if (tokens > (1ll << 30) ||
+  if (tokens > (1ll << 30) || static_cast<int64_t>(cache->kv_heads) * row_tiles >= (1 << 20) ||
       (static_cast<double>(tokens) / 16 + fp4::kAttnTcItemCost + 8) * B * cache->kv_heads * row_tiles >= 1.2e9 ||
       static_cast<double>(cache->num_blocks) * cache->kv_heads * (cache->block_size / 16) >= 2147483647.0)
     return FP4GEMV_ERR_UNSUPPORTED_SHAPE;

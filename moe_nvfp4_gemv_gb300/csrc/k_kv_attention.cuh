@@ -55,6 +55,8 @@
 // or the dims of 32 rows between them (260 to 344 and 334 us).
 #pragma once
 
+#include <type_traits>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -180,6 +182,13 @@ __device__ __forceinline__ int attn_div_up(int x, int y, float inv_y) {
   q += q * y + y <= x;
   return q + (q * y < x);
 }
+// The same for quotients below 2^20: no other path.
+__device__ __forceinline__ int attn_div_up_small(int x, int y, float inv_y) {
+  int q = static_cast<int>(static_cast<float>(x) * inv_y);  // (at most one off)
+  q -= q * y > x;
+  q += q * y + y <= x;
+  return q + (q * y < x);
+}
 // Of a sequence of n tokens: the first strip that any query sees (or the unit that holds it), and the strips from there
 // on; what strips take on the line.
 __device__ __forceinline__ int attn_first_strip(const KvAttnParams& p, int n) {
@@ -218,8 +227,8 @@ __device__ __forceinline__ void attn_plan(const KvAttnParams& p, int* strips_bef
   }
   const int ctas = static_cast<int>(gridDim.x);
   if (p.B == 1 && items <= ctas) {
-    // one sequence: as many pieces of each item as there are CTAs for, without the sums over sequences below (777 tokens:
-    // 7.4 us, with them 8.6)
+    // one sequence: as many pieces of each item as there are CTAs for, without the sums over sequences below (a call of
+    // 777 tokens 7.4 us, with them 8.6)
     if (warp == 0) {
       const int n = length(0), s = n > 0 ? attn_strips_of(p, n) : 0;
       const int most = attn_div_up(ctas + 1, items, __fdividef(1.0f, static_cast<float>(items))) - 1;
@@ -250,104 +259,113 @@ __device__ __forceinline__ void attn_plan(const KvAttnParams& p, int* strips_bef
       }
     }
   } else if (warp == 0) {
-    int n0 = 0;  // the lane's sequence, where there are few
-    if (few && lane < p.B) {
-      n0 = length(lane);
-      tokens[lane] = n0;
-    }
-    auto tokens_of = [&](int b) -> int { return few ? n0 : b < p.B ? tokens[b] : 0; };
-    auto strips_at = [&](int b) -> int {
-      const int n = tokens_of(b);
-      return n > 0 ? attn_strips_of(p, n) : 0;
-    };
-    int total = 0, alive = 0;
-    for (int b = lane; b < p.B + lane; b += 32) {  // (all lanes alike)
-      const int s = strips_at(b);
-      total += __reduce_add_sync(kAll, attn_units(p, s));
-      alive += __popc(__ballot_sync(kAll, s > 0));
-    }
-    total *= items;
-    alive *= items;
-    // pieces per item, if those of the shortest of three lengths are no more than the CTAs
-    int per = 0;
-    if (alive <= ctas) {
-      const int even = attn_div_up(total, ctas, p.inv_ctas);
-      int len[3], sum[3] = {0, 0, 0};
-      float inv[3];
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        len[k] = max(kAttnRound, whole(even + (even * k >> 3)));
-        inv[k] = __fdividef(1.0f, static_cast<float>(len[k]));
+    auto plan = [&](auto is_few) {
+      constexpr bool kFew = decltype(is_few)::value;  // no more than a sequence for each lane: the loops run once
+      auto again = [&](int b) -> bool { return kFew ? b == lane : b < p.B + lane; };  // (all lanes alike)
+      int n0 = 0;
+      if (kFew && lane < p.B) {
+        n0 = length(lane);
+        tokens[lane] = n0;
       }
-      for (int b = lane; b < p.B + lane; b += 32) {
+      auto tokens_of = [&](int b) -> int { return kFew ? n0 : b < p.B ? tokens[b] : 0; };
+      auto strips_at = [&](int b) -> int {
+        const int n = tokens_of(b);
+        return n > 0 ? attn_strips_of(p, n) : 0;
+      };
+      int total = 0, alive = 0;
+      for (int b = lane; again(b); b += 32) {
         const int s = strips_at(b);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) sum[k] += __reduce_add_sync(kAll, attn_div_up(s, len[k], inv[k]));
+        total += __reduce_add_sync(kAll, attn_units(p, s));
+        alive += __popc(__ballot_sync(kAll, s > 0));
       }
+      total *= items;
+      alive *= items;
+      // pieces per item, if those of the shortest of three lengths are no more than the CTAs
+      int per = 0;
+      if (alive <= ctas) {
+        const int even = attn_div_up(total, ctas, p.inv_ctas);
+        int len[3], sum[3] = {0, 0, 0};
+        float inv[3];
 #pragma unroll
-      for (int k = 2; k >= 0; --k)
-        if (sum[k] * items <= ctas) per = len[k];
-    }
-    const bool pieces = per > 0;
-    const int lead = pieces ? 0 : p.item_cost;
-    if (!pieces) per = max(whole(attn_div_up(total + alive * p.item_cost, ctas, p.inv_ctas)), kAttnRound);
-    const float inv_per = __fdividef(1.0f, static_cast<float>(per));
-    auto on_line = [&](int s) -> int { return pieces ? attn_div_up(s, per, inv_per) * per : s > 0 ? attn_units(p, s) + lead : 0; };
-    // the sequences' places on both lines; and the share's begin and end in strips, where the cuts fall
-    int strips_end = 0, line_end = 0, share[2] = {-1, -1};
-    AttnPlace place = {};
-    for (int b = lane; b < p.B + lane; b += 32) {
-      const int s = strips_at(b), len = on_line(s);
-      int sum = s, line = len;
+        for (int k = 0; k < 3; ++k) {
+          len[k] = max(kAttnRound, whole(even + (even * k >> 3)));
+          inv[k] = __fdividef(1.0f, static_cast<float>(len[k]));
+        }
+        for (int b = lane; again(b); b += 32) {
+          const int s = strips_at(b);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kAll, sum, o), v = __shfl_up_sync(kAll, line, o);
-        if (lane >= o) sum += u, line += v;
+          for (int k = 0; k < 3; ++k) sum[k] += __reduce_add_sync(kAll, attn_div_up_small(s, len[k], inv[k]));
+        }
+#pragma unroll
+        for (int k = 2; k >= 0; --k)
+          if (sum[k] * items <= ctas) per = len[k];
       }
-      const int strips_here = strips_end + (sum - s) * items, line_here = line_end + (line - len) * items;
-      if (b < p.B) {
-        strips_before[b] = strips_here;
-        line_before[b] = line_here;
-      }
+      const bool pieces = per > 0;
+      const int lead = pieces ? 0 : p.item_cost;
+      if (!pieces) per = max(whole(attn_div_up(total + alive * p.item_cost, ctas, p.inv_ctas)), kAttnRound);
+      const float inv_per = __fdividef(1.0f, static_cast<float>(per));
+      auto on_line = [&](int s) -> int {
+        return pieces ? attn_div_up_small(s, per, inv_per) * per : s > 0 ? attn_units(p, s) + lead : 0;
+      };
+      // the sequences' places on both lines; and the share's begin and end in strips, where the cuts fall
+      int strips_end = 0, line_end = 0, share[2] = {-1, -1};
+      AttnPlace place = {};
+      for (int b = lane; again(b); b += 32) {
+        const int s = strips_at(b), len = on_line(s);
+        int sum = s, line = len;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int64_t at64 = static_cast<int64_t>(per) * (blockIdx.x + k);
-        if (len > 0 && at64 >= line_here && at64 < line_here + static_cast<int64_t>(len) * items) {
-          const int off = static_cast<int>(at64) - line_here;
-          const int item = attn_div_up(off + 1, len, __fdividef(1.0f, static_cast<float>(len))) - 1;
-          // (a cut behind an item's last strip or in its cost: the strip that follows)
-          const int strip = max(off - item * len - lead, 0);
-          share[k] = strips_here + item * s + min(strip, s);
-          if (k == 0) {
-            place.b = b;
-            place.first = attn_first_strip(p, tokens_of(b));
-            place.strips = s;
-            place.item = item;
-            place.strip = strip;  // (below s wherever the share is not empty, or pieces end)
-            place.head = p.row_tiles == 1 ? item : item / p.row_tiles;
-            place.tile = item - place.head * p.row_tiles;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(kAll, sum, o), v = __shfl_up_sync(kAll, line, o);
+          if (lane >= o) sum += u, line += v;
+        }
+        const float inv_len = __fdividef(1.0f, static_cast<float>(len));
+        const int strips_here = strips_end + (sum - s) * items, line_here = line_end + (line - len) * items;
+        if (b < p.B) {
+          strips_before[b] = strips_here;
+          line_before[b] = line_here;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int64_t at64 = static_cast<int64_t>(per) * (blockIdx.x + k);
+          if (len > 0 && at64 >= line_here && at64 < line_here + static_cast<int64_t>(len) * items) {
+            const int off = static_cast<int>(at64) - line_here;
+            const int item = attn_div_up_small(off + 1, len, inv_len) - 1;
+            // (a cut behind an item's last strip or in its cost: the strip that follows)
+            const int strip = max(off - item * len - lead, 0);
+            share[k] = strips_here + item * s + min(strip, s);
+            if (k == 0) {
+              place.b = b;
+              place.first = attn_first_strip(p, tokens_of(b));
+              place.strips = s;
+              place.item = item;
+              place.strip = strip;  // (below s wherever the share is not empty, or pieces end)
+              place.head = p.row_tiles == 1 ? item : item / p.row_tiles;
+              place.tile = item - place.head * p.row_tiles;
+            }
           }
         }
+        strips_end += __shfl_sync(kAll, sum, 31) * items;
+        line_end += __shfl_sync(kAll, line, 31) * items;
       }
-      strips_end += __shfl_sync(kAll, sum, 31) * items;
-      line_end += __shfl_sync(kAll, line, 31) * items;
-    }
-    // (the one lane that met a cut writes it; cuts past the line's end: no strip follows)
-    if (share[0] >= 0) {
-      plan_words[0] = share[0];
-      places[0] = places[2] = place;
-    }
-    if (share[1] >= 0) plan_words[1] = share[1];
-    const bool met0 = __any_sync(kAll, share[0] >= 0), met1 = __any_sync(kAll, share[1] >= 0);
-    if (lane == 0) {
-      strips_before[p.B] = strips_end;
-      line_before[p.B] = line_end;
-      if (!met0) plan_words[0] = strips_end;
-      if (!met1) plan_words[1] = strips_end;
-      plan_words[2] = per;
-      plan_words[3] = lead;
-      plan_words[4] = pieces;
-    }
+      // (the one lane that met a cut writes it; cuts past the line's end: no strip follows)
+      if (share[0] >= 0) {
+        plan_words[0] = share[0];
+        places[0] = places[2] = place;
+      }
+      if (share[1] >= 0) plan_words[1] = share[1];
+      const bool met0 = __any_sync(kAll, share[0] >= 0), met1 = __any_sync(kAll, share[1] >= 0);
+      if (lane == 0) {
+        strips_before[p.B] = strips_end;
+        line_before[p.B] = line_end;
+        if (!met0) plan_words[0] = strips_end;
+        if (!met1) plan_words[1] = strips_end;
+        plan_words[2] = per;
+        plan_words[3] = lead;
+        plan_words[4] = pieces;
+      }
+    };
+    if (few) plan(std::true_type{});
+    else plan(std::false_type{});
   }
   __syncthreads();
 }
@@ -1052,7 +1070,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
         for (int w = 0; w < C::kWarps; ++w) {
           const float2 o = ml[w * C::kRows + r];
           const float f = attn_ex2(o.x - top);
-          const float4 a = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + free_stage[w]) + from_cell);
+          const float* const cells = reinterpret_cast<const float*>(smem + free_stage[w]);
+          const float4 a = *reinterpret_cast<const float4*>(cells + from_cell);
           v.x = fmaf(a.x, f, v.x), v.y = fmaf(a.y, f, v.y), v.z = fmaf(a.z, f, v.z), v.w = fmaf(a.w, f, v.w);
           l = fmaf(o.y, f, l);
         }

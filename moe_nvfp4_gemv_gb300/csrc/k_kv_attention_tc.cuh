@@ -15,9 +15,10 @@
 // * a weight w = 2^(s + log2 vs - m), rounded to f16 as it is there, is
 //   (w1 + w2 / 32 + w3 / 1024) / 16, which holds its 11 bits; of weights below
 //   2^-12 what lies below 2^-24 goes.  (What a part leaves is at most half the
-//   last place of its 4 bits, 8 of 256, so 32 times it fits the next.)  out^T [128 dims x 96] = V^T [128 dims x 128 tokens]
-//   [w1 | w2 | w3]: V^T is read from the V tile as it lies (M-major), the
-//   weights' tile has a token's 96 bytes in a row (N-major).
+//   last place of its 4 bits, 8 of 256, so 32 times it fits the next.)
+//   out^T [128 dims x 96] = V^T [128 dims x 128 tokens] [w1 | w2 | w3]: V^T is
+//   read from the V tile as it lies (M-major), the weights' tile has a token's
+//   96 bytes in a row (N-major).
 //
 // A thread owns a token of the tile while it makes weights (TMEM lane = token),
 // so a token's scales, its place among the masks and its own V row, which it

@@ -234,8 +234,9 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Logits l = logits_of(logits);
     const int topk = int32(a[1]);
     int scores;
-    if (PyUnicode_Check(a[2]) && PyUnicode_CompareWithASCIIString(a[2], "softmax") == 0) scores = FP4GEMV_ROUTE_SOFTMAX;
-    else if (PyUnicode_Check(a[2]) && PyUnicode_CompareWithASCIIString(a[2], "sigmoid") == 0) scores = FP4GEMV_ROUTE_SIGMOID;
+    auto is = [&](const char* name) { return PyUnicode_Check(a[2]) && PyUnicode_CompareWithASCIIString(a[2], name) == 0; };
+    if (is("softmax")) scores = FP4GEMV_ROUTE_SOFTMAX;
+    else if (is("sigmoid")) scores = FP4GEMV_ROUTE_SIGMOID;
     else refuse("scores must be 'softmax' or 'sigmoid', not %R", a[2]);
     const float* bias = nullptr;
     if (a[3] != Py_None) {
@@ -274,11 +275,12 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int top_n = int32(a[2]);
     const double temperature = real(a[3]);
     if (!(temperature > 0)) refuse("temperature must be positive");
-    const at::Tensor &logprob = tensor(a[4], "logprob"), &rank = tensor(a[5], "rank"), &entropy = tensor(a[6], "entropy"),
-                     &top_ids = tensor(a[7], "top_ids"), &top_logprobs = tensor(a[8], "top_logprobs");
+    const at::Tensor &logprob = tensor(a[4], "logprob"), &rank = tensor(a[5], "rank"),
+                     &entropy = tensor(a[6], "entropy"), &top_ids = tensor(a[7], "top_ids"),
+                     &top_logprobs = tensor(a[8], "top_logprobs");
     if (!shaped(logprob, l.rows) || !shaped(rank, l.rows) || !shaped(entropy, l.rows) ||
-        !shaped(top_ids, l.rows, top_n) || !shaped(top_logprobs, l.rows, top_n) || !plain(logprob, at::kFloat, l.index) ||
-        !plain(rank, at::kInt, l.index) || !plain(entropy, at::kFloat, l.index) || !plain(top_ids, at::kInt, l.index) ||
+        !shaped(top_ids, l.rows, top_n) || !shaped(top_logprobs, l.rows, top_n) ||
+        !plain(logprob, at::kFloat, l.index) || !plain(rank, at::kInt, l.index) || !plain(entropy, at::kFloat, l.index) || !plain(top_ids, at::kInt, l.index) ||
         !plain(top_logprobs, at::kFloat, l.index))
       refuse("out must hold contiguous logprob fp32 [T], rank int32 [T], entropy fp32 [T], top_ids int32 [T, top_n] and "
              "top_logprobs fp32 [T, top_n] on the logits' device");

@@ -166,6 +166,9 @@ def test_marshalling_refuses_a_wrong_number_or_kind_of_arguments():
 def test_lengths_past_thirty_bits_are_refused(fp4):
     """Places in a sequence, and new tokens, are 32-bit numbers on the device."""
     assert attend(fp4, max_blocks=(1 << 26) + 1) == 2  # 16-token pages: past 2^30 tokens
+    assert attend(fp4, max_blocks=1 << 24, B=100) == 2  # too many strips in all
+    many = struct(kv_heads=1 << 20)
+    assert attend(fp4, cache=many, heads=1 << 20, ldq=1 << 30, ldo=1 << 30) == 2
     c = struct()
     for T, max_blocks, B in ((1, (1 << 26) + 1, 1), ((1 << 30) + 1, 4, 1)):
         assert fp4.lib().fp4gemv_kv_append(ctypes.addressof(c), None, 256, None, 256, 0, T, None, None, max_blocks, None,
