@@ -47,7 +47,7 @@
 // 128, us: E4M3 182 (0.88), INT8 186 (0.87), 16 rows 184 (0.88); heads of 64 97
 // (0.83), of 96 141 (0.86), of 256 (16 sequences) 167 (0.96); pages of 16 tokens
 // 186.  Fewer bytes: the launch, the plan, the first strips' latency and the
-// joining, 8 us together: 24 ragged ones of up to 8191 tokens 45.6 us (0.69), one
+// joining, 8 us together: 24 ragged ones of up to 8191 tokens 44.8 us (0.70), one
 // of 131071 (INT8) 50.9 (0.79), one of 777 7.4, one of 16 4.9.  32 rows: issue
 // (INT8 279 us, 0.58; E4M3 of 128 is k_kv_attention_tc.cuh's).  Measured and not
 // taken: more shares than resident CTAs (24 ragged 46 to 51 .. 73 us: every CTA

@@ -23,7 +23,7 @@
 // What bounds it.  Many rows: HBM (2048 rows of 131072 bf16: 92 us, 0.87 of the
 // measured copy bandwidth), with the exponentials close behind (issue slots 57 %
 // taken; one scalar chain per element 114 us, paired fp32 sums 101, loads of a
-// slot ahead 92).  Few: latency; one row of 128003 6.7 us (2.6 of it the top
+// slot ahead 92).  Few: latency; one row of 128003 6.1 us (2.1 of it the top
 // alternatives), 64 rows of 100001 fp32 9.5.  Measured and not taken: 512 or 1024
 // threads (fewer CTAs to fill the phases without loads), double-buffered loads
 // (104 us for the 2048 rows).
@@ -431,11 +431,32 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) token_logprobs_kernel
     }
   }
   if (n > 0) {
-    // the CTAs' winners, each ranked among all (one CTA's are in order already)
+    // The CTAs' winners, each ranked among all (one CTA's are in order already): by counting, or, where they are many, by
+    // its place in its own CTA's list and a binary search in the others'.  Counting / searching, us: top 20 of a row of
+    // 128003 6.6 / 6.1, top 5 of 64 rows of 100001 9.5 / 9.9.
     const int have = static_cast<int>(C) * n;
     for (int i = tid; i < have; i += kLpThreads) {
       const uint64_t k = sh.top[i];
-      const int r = C > 1 ? count_above(sh.top, have, k) : i;
+      int r = i;
+      if (have <= 64) {
+        if (C > 1) r = count_above(sh.top, have, k);
+      } else {
+        const int own_list = i / n;
+        int above[kLpMaxCluster];
+#pragma unroll
+        for (int l = 0; l < kLpMaxCluster; ++l) above[l] = 0;
+#pragma unroll
+        for (int step = 32; step > 0; step >>= 1)
+#pragma unroll
+          for (int l = 0; l < kLpMaxCluster; ++l) {
+            const int at = above[l] + step;
+            const uint64_t o = sh.top[l * n + min(at, n) - 1];  // (lists past the cluster's: zeros)
+            above[l] += at <= n && o > k ? step : 0;
+          }
+        r -= own_list * n;
+#pragma unroll
+        for (int l = 0; l < kLpMaxCluster; ++l) r += l == own_list ? 0 : above[l];
+      }
       if (r < n && k != 0) {
         const int64_t o = t * n + r;
         p.top_ids[o] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));
