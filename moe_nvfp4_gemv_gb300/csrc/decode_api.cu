@@ -155,6 +155,7 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   p.window = window;
   p.unit = 1;
   p.item_cost = fp4::kAttnItemCost;
+  p.uncut = cache->head_dim > 128 ? fp4::kAttnUncut256 : fp4::kAttnUncut;
   p.f16 = dtype == FP4GEMV_F16;
   p.sm_scale = sm_scale;
   if (row_units == 4 && cache->head_dim == 128 && cache->format == FP4GEMV_KV_E4M3) {

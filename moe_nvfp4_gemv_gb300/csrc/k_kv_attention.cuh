@@ -86,6 +86,7 @@ struct KvAttnParams {
   int f16;             // element type of q and out
   int unit;            // strips (a power of two): items start and are cut at its multiples
   int item_cost;       // what an item's end costs, in strips
+  int uncut;           // items of up to this many strips stay whole where there are CTAs for all
   int group_magic;     // ceil(2^16 / group): row / group = row group_magic >> 16 for the rows there are
   float inv_ctas;      // 1 / the grid's CTAs
   float sm_scale;
@@ -108,6 +109,10 @@ constexpr int kAttnFan2 = 20;
 constexpr int kAttnItemCost = 32;
 constexpr int kAttnTcItemCost = 64;  // ... of the kernel on the 5th-generation tensor core (its figures there)
 constexpr float kAttnFloor = -1e30f;  // the running maximum before any token
+// Items of up to this many strips stay whole where there are CTAs for all: joining pieces costs 1.2 us, eight strips 0.15.
+// Cut / whole, one sequence on 8 KV heads of 128, us: 130 tokens 7.2 / 5.5, 300 7.5 / 6.3, 500 7.5 / 7.4, 777 7.7 / 9.1;
+// heads of 256: 300 9.0 / 8.3, 500 9.0 / 10.2; 32 rows, E4M3: 130 12.2 / 9.0, 500 12.5 / 10.3, 777 13.3 / 14.1.
+constexpr int kAttnUncut = 40, kAttnUncut256 = 20;
 // log2 of the largest weight before the running maximum moves.  256 sequences of 500 tokens: 66 us; with 0 68.8.
 constexpr float kAttnSlack = 8.0f;
 
@@ -232,7 +237,8 @@ __device__ __forceinline__ void attn_plan(const KvAttnParams& p, int* strips_bef
     if (warp == 0) {
       const int n = length(0), s = n > 0 ? attn_strips_of(p, n) : 0;
       const int most = attn_div_up(ctas + 1, items, __fdividef(1.0f, static_cast<float>(items))) - 1;
-      const int per = max(whole(attn_div_up(s, most, __fdividef(1.0f, static_cast<float>(most)))), kAttnRound);
+      const int even = attn_div_up(s, most, __fdividef(1.0f, static_cast<float>(most)));
+      const int per = max(whole(s <= p.uncut ? s : even), kAttnRound);
       const int pieces = max(attn_div_up(s, per, __fdividef(1.0f, static_cast<float>(per))), 1);
       const int cta = static_cast<int>(blockIdx.x);
       const int item = attn_div_up(cta + 1, pieces, __fdividef(1.0f, static_cast<float>(pieces))) - 1;
@@ -272,15 +278,16 @@ __device__ __forceinline__ void attn_plan(const KvAttnParams& p, int* strips_bef
         const int n = tokens_of(b);
         return n > 0 ? attn_strips_of(p, n) : 0;
       };
-      int total = 0, alive = 0;
+      int total = 0, alive = 0, longest = 0;
       for (int b = lane; again(b); b += 32) {
         const int s = strips_at(b);
         total += __reduce_add_sync(kAll, attn_units(p, s));
         alive += __popc(__ballot_sync(kAll, s > 0));
+        longest = max(longest, static_cast<int>(__reduce_max_sync(kAll, static_cast<unsigned>(s))));
       }
       total *= items;
       alive *= items;
-      // pieces per item, if those of the shortest of three lengths are no more than the CTAs
+      // pieces per item, if those of the shortest of three lengths are no more than the CTAs; one, where items are short
       int per = 0;
       if (alive <= ctas) {
         const int even = attn_div_up(total, ctas, p.inv_ctas);
@@ -299,6 +306,7 @@ __device__ __forceinline__ void attn_plan(const KvAttnParams& p, int* strips_bef
 #pragma unroll
         for (int k = 2; k >= 0; --k)
           if (sum[k] * items <= ctas) per = len[k];
+        if (longest <= p.uncut) per = max(whole(longest), kAttnRound);
       }
       const bool pieces = per > 0;
       const int lead = pieces ? 0 : p.item_cost;
