@@ -39,7 +39,7 @@
 // where this kernel needs 350).  Steps to it: both rings as one, a V tile held
 // as long as its K and 16 TMA boxes a tile from one warp 228; rings apart, boxes
 // of a page 175.  Short calls pay for the set-up and the first tile's chain
-// (14 us for one sequence of 1000 tokens; mma.sync 16), several items in a share
+// (13.3 us for one sequence of 1000 tokens; mma.sync 16), several items in a share
 // for the drains between them (kAttnTcItemCost: 24 ragged sequences of up to
 // 8191 tokens 68 us with 16, 58 with 32, 53 with 64; mma.sync 90).
 //
