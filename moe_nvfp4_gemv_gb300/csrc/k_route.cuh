@@ -8,7 +8,8 @@
 // kL lanes per token (a warp, or a part of one where there are many tokens),
 // expert e on lane e / S of the token's, slot e % S: a lane's experts are
 // neighbours, so of equal keys the lowest lane's lowest slot is the lower
-// index, and an expert group is a run of lanes.  Keys are compared as unsigned
+// index.  Expert groups of any size begin at lanes of their own, a power of two
+// of lanes each (group_lanes), unless that takes more than 16 slots.  Keys are compared as unsigned
 // integers that order like the floats (0: taken or absent).  A round of the
 // selection is a maximum over the lanes' best keys and a vote for the lane.
 //
@@ -41,6 +42,7 @@ struct RouteParams {
   float* weights;
   int M, E, topk;
   int n_group, topk_group, group_top;
+  int group_lanes, lane_experts;  // lanes of a group and experts on each; 0: groups lie across lanes
   int sigmoid, renormalize;
   float scale;
 };
@@ -115,9 +117,18 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
   pdl_wait();
   const bool live = t < p.M;  // (the lanes of no token go along)
   const T* row = static_cast<const T*>(p.logits) + (live ? t : 0) * p.ldl;
-  const int e0 = sub * S;
+  // the lane's experts: e0, e0 + 1, ... (cnt of them)
+  int e0 = sub * S, cnt = min(max(p.E - e0, 0), S), group = 0;
+  if (kL < 32) {  // (groups, if any, are whole lanes of S)
+    if (p.n_group > 1) group = sub / p.group_lanes;
+  } else if (p.group_lanes > 0) {
+    const int size = p.E / p.n_group, within = (sub & (p.group_lanes - 1)) * p.lane_experts;
+    group = sub / p.group_lanes;
+    e0 = group * size + within;
+    cnt = group < p.n_group ? min(max(size - within, 0), p.lane_experts) : 0;
+  }
   float x[S];
-  if (S * sizeof(T) >= 16 && e0 + S <= p.E && (reinterpret_cast<uintptr_t>(row + e0) & 15u) == 0) {
+  if (S * sizeof(T) >= 16 && cnt == S && (reinterpret_cast<uintptr_t>(row + e0) & 15u) == 0) {
     constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
     for (int i = 0; i < S / kPer; ++i) {
@@ -128,7 +139,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < S; ++i) x[i] = e0 + i < p.E ? to_float(row[e0 + i]) : kNegInf;
+    for (int i = 0; i < S; ++i) x[i] = i < cnt ? to_float(row[e0 + i]) : kNegInf;
   }
 #pragma unroll
   for (int i = 0; i < S; ++i) x[i] = x[i] == x[i] ? x[i] : kNegInf;
@@ -144,13 +155,13 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     top = m;
   }
   auto raw_score = [&](float v) -> float {  // softmax: before the division by the sum
-    if (p.sigmoid) return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-v)));
+    if (p.sigmoid) return __frcp_rn(__fadd_rn(1.0f, expf(-v)));
     return v == kNegInf ? 0.0f : v == top ? 1.0f : expf(__fsub_rn(v, top));
   };
   uint32_t key[S];
   if (by_logit) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) key[i] = e0 + i < p.E ? order_key(x[i]) : 0u;
+    for (int i = 0; i < S; ++i) key[i] = i < cnt ? order_key(x[i]) : 0u;
   }
   if (!by_logit || !(p.sigmoid || p.renormalize)) {
     float score[S];
@@ -188,18 +199,17 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
       }
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        const int e = e0 + i;
         float s = score[i];
-        if (p.bias && e < p.E) s = __fadd_rn(s, __ldg(p.bias + e));
-        key[i] = e < p.E ? order_key(s) : 0u;
+        if (p.bias && i < cnt) s = __fadd_rn(s, __ldg(p.bias + e0 + i));
+        key[i] = i < cnt ? order_key(s) : 0u;
       }
     }
   }
   if (p.n_group > 1) {
-    const int size = p.E / p.n_group, width = size / S;
+    const int size = p.E / p.n_group, width = p.group_lanes;
     uint32_t chosen = 0;  // the groups that take part
-    if (width * S == size && (width & (width - 1)) == 0) {
-      // a group is a run of 2^k lanes: its two best keys by exchange within the run
+    if (kL < 32 || width > 0) {
+      // a group's two best keys by exchange within its lanes
       uint32_t a = 0, b = 0;
 #pragma unroll
       for (int i = 0; i < S; ++i) {
@@ -212,13 +222,12 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
         a = max(a, a2);
       }
       const uint32_t strength =
-          e0 >= p.E ? 0u : p.group_top == 2 ? order_key(__fadd_rn(key_value(a), key_value(b))) : a;
+          group >= p.n_group ? 0u : p.group_top == 2 ? order_key(__fadd_rn(key_value(a), key_value(b))) : a;
       // its place among the groups: those that are stronger, or as strong and earlier
-      const int mine = e0 / size;
       int before = 0;
       for (int g = 0; g < p.n_group; ++g) {
         const uint32_t other = __shfl_sync(kAll, strength, (lane & ~(kL - 1)) + g * width);
-        before += other > strength || (other == strength && g < mine);
+        before += other > strength || (other == strength && g < group);
       }
       if (before >= p.topk_group) {
 #pragma unroll
@@ -289,13 +298,13 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
       }
     const uint32_t most = lanes_max<kL>(best);
     const int who = first_lane<kL>(best == most, lane);
-    // (the winner's slot, and its logit where that is not the key itself)
-    const int e = who * S + __shfl_sync(kAll, slot, (lane & ~(kL - 1)) + who);
+    // (the winner, and its logit where that is not the key itself)
+    const int e = __shfl_sync(kAll, e0 + slot, (lane & ~(kL - 1)) + who);
     const float v = by_logit ? key_value(most)
                              : __uint_as_float(__shfl_sync(kAll, best_x, (lane & ~(kL - 1)) + who));
 #pragma unroll
     for (int i = 0; i < S; ++i)
-      if (e0 + i == e) key[i] = 0;
+      if (kL < 32 ? e0 + i == e : sub == who && slot == i) key[i] = 0;
 #pragma unroll
     for (int i = 0; i < kKeep; ++i)
       if (j == i * kL + sub) {

@@ -108,7 +108,8 @@ def test_route_many_tokens(fp4, E, topk, kind, renorm, dtype):
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,n_group,topk_group,group_top,topk", [(60, 4, 2, 2, 6), (64, 32, 31, 2, 20), (64, 8, 3, 1, 8),
-                                                                 (30, 10, 4, 2, 9), (32, 4, 1, 2, 8)])
+                                                                 (30, 10, 4, 2, 9), (32, 4, 1, 2, 8), (64, 4, 2, 2, 8),
+                                                                 (64, 2, 1, 1, 12)])
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_route_many_tokens_groups(fp4, kind, E, n_group, topk_group, group_top, topk, with_bias):
     g = gen(E * n_group)
@@ -304,3 +305,19 @@ def test_logprobs_refusals(fp4):
     with pytest.raises(ValueError):
         fp4.token_logprobs(x, t, temperature=0.0)
     assert fp4.token_logprobs(x[:0], t[:0], 3).top_ids.shape == (0, 3)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group,topk_group,group_top,topk", [
+    (72, 8, 7, 2, 14), (240, 8, 4, 1, 6), (510, 17, 5, 2, 8), (102, 17, 6, 2, 9), (33, 11, 3, 2, 7), (448, 28, 9, 2, 20),
+    (300, 2, 1, 1, 32), (62, 31, 20, 1, 16), (291, 3, 2, 2, 7)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_route_uneven_groups(fp4, kind, E, n_group, topk_group, group_top, topk, dtype):
+    """Groups that fill their lanes in part, and (17 of 30) groups across lanes."""
+    g = gen(E + topk)
+    x = torch.randn(200, E, generator=g).to(TYPES[dtype])
+    x[::9, 1] = -math.inf
+    check_route(fp4, x, topk, kind, n_group=n_group, topk_group=topk_group, group_top=group_top, renormalize=False,
+                exact=group_top == 1)
+    bias = torch.randn(E, generator=g) * 0.1
+    check_route(fp4, x, topk, kind, bias, n_group=n_group, topk_group=topk_group, group_top=group_top)
