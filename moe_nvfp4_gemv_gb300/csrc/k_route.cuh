@@ -9,9 +9,10 @@
 // expert e on lane e / S of the token's, slot e % S: a lane's experts are
 // neighbours, so of equal keys the lowest lane's lowest slot is the lower
 // index.  Expert groups of any size begin at lanes of their own, a power of two
-// of lanes each (group_lanes), unless that takes more than 16 slots.  Keys are compared as unsigned
-// integers that order like the floats (0: taken or absent).  A round of the
-// selection is a maximum over the lanes' best keys and a vote for the lane.
+// of lanes each (group_lanes), unless that takes more than 16 slots.  Keys are
+// compared as unsigned integers that order like the floats (0: taken or
+// absent).  A round of the selection is a maximum over the lanes' best keys and
+// a vote for the lane.
 //
 // Keys have to come out the same for every order of summation, or experts
 // whose keys nearly tie would change places: exp and the division are the
@@ -21,7 +22,7 @@
 // What bounds it.  Few tokens: the launch (one token of 128 experts, top 8:
 // 1.9 us; 96 tokens of 256 with 8 groups 3.5).  Many: the selection's
 // instructions, issue slots 64 % taken (20011 tokens of 60 experts, top 4, fp32:
-// 7.1 us, where reading and writing would take 0.8; one warp per token 12.4).
+// 7.2 us, where reading and writing would take 0.8; one warp per token 12.4).
 #pragma once
 
 #include <cstdint>
