@@ -55,8 +55,7 @@ constexpr int kMaxCand = 512;
 constexpr int kRaiseFrom = 256;  // collected elements that a better bound is taken from
 constexpr int kLpMaxCluster = 8;
 // Logits at or below this are masked: probability 0.  The statistics see them
-// as this value, so that no difference of two is a NaN or overflows; a power
-// of two, so that its product with c is exact and its distance to itself 0.
+// as this value, so that no difference of two is a NaN or overflows.
 constexpr float kMasked = -0x1p100f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -108,9 +107,11 @@ __device__ __forceinline__ void lp_raise(LpThread& st, float bm, float c) {
     st.m = bm;
   }
 }
-// Two logits (masked ones already at kMasked) into the sums; c2 = (c, c), mc2 = (-m c, -m c).
-__device__ __forceinline__ void lp_sum(LpThread& st, uint64_t x, uint64_t c2, uint64_t mc2) {
-  const uint64_t d = fma2(x, c2, mc2);
+// Two logits (masked ones already at kMasked) into the sums; c2 = (c, c), m2 = (-m, -m).  The difference comes first: it is
+// 0 for the maximum itself and rounds to its own size, where x c - RN(m c) would carry the rounding of m c, which grows
+// with |m| / temperature, into every term and into log Z.
+__device__ __forceinline__ void lp_sum(LpThread& st, uint64_t x, uint64_t c2, uint64_t m2) {
+  const uint64_t d = mul2(add2(x, m2), c2);
   const float2 df = unpair(d);
   const uint64_t e = pair(ex2(df.x), ex2(df.y));
   st.s = add2(st.s, e);
@@ -159,12 +160,12 @@ __device__ __forceinline__ void lp_add(LpThread& st, const uint32_t (&w)[kW], fl
       for (int i = 0; i < kW; ++i) n = __hadd2(n, __hgt2(two(w[i]), limit));  // (at most kW: exact)
       st.above += static_cast<int>(__low2float(n) + __high2float(n));
     }
-    const uint64_t c2 = pair(c, c), mc2 = pair(-st.m * c, -st.m * c);
+    const uint64_t c2 = pair(c, c), m2 = pair(-st.m, -st.m);
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
       const __nv_bfloat162 x = __hmax2_nan(two(w[i]), __float2bfloat162_rn(kMasked));
       const uint32_t b = *reinterpret_cast<const uint32_t*>(&x);
-      lp_sum(st, pair(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u)), c2, mc2);
+      lp_sum(st, pair(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u)), c2, m2);
     }
   } else {
     constexpr int kX = std::is_same<T, float>::value ? kW : 2 * kW;
@@ -186,10 +187,10 @@ __device__ __forceinline__ void lp_add(LpThread& st, const uint32_t (&w)[kW], fl
 #pragma unroll
       for (int i = 0; i < kX; ++i) st.above += x[i] > xr;
     }
-    const uint64_t c2 = pair(c, c), mc2 = pair(-st.m * c, -st.m * c);
+    const uint64_t c2 = pair(c, c), m2 = pair(-st.m, -st.m);
 #pragma unroll
     for (int i = 0; i < kX; i += 2)
-      lp_sum(st, pair(max_nan(x[i], kMasked), max_nan(x[i + 1], kMasked)), c2, mc2);
+      lp_sum(st, pair(max_nan(x[i], kMasked), max_nan(x[i + 1], kMasked)), c2, m2);
   }
 }
 
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) token_logprobs_kernel
     const float x = to_float(row[single_index(tid)]);
     lp_raise(mine, x, c);
     mine.above += x > xr;
-    const float d = fmaf(max_nan(x, kMasked), c, -mine.m * c), e = ex2(d);
+    const float d = (max_nan(x, kMasked) - mine.m) * c, e = ex2(d);
     mine.s = add2(mine.s, pair(e, 0.0f));
     mine.u = add2(mine.u, pair(e * d, 0.0f));
   }
