@@ -4,7 +4,8 @@
 // One pass over the row with running statistics (m, s, u): the maximum so
 // far, s = sum 2^(c (x - m)) and u = sum 2^(c (x - m)) c (x - m), c =
 // inv_temperature log2(e); a new maximum rescales them, u to
-// f (u + s c (m - m')), f = 2^(c (m - m')).  At the end, in base-2 logs,
+// f u + (f s) c (m - m'), f = 2^(c (m - m')): f s before the product, since where
+// f is 0 (masked logits alone so far) s c (m - m') need not be finite.  At the end, in base-2 logs,
 //   log2 Z = log2 s,  H = ln 2 (log2 s - u / s),
 //   logprob = (x - m) inv_temperature - ln 2 log2 s.
 //
@@ -79,8 +80,8 @@ __device__ __forceinline__ void lp_join_warp(LpStat& a, float c) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   const float d = (a.m - m) * c, f = ex2(d);
-  a.u = f * fmaf(a.s, d, a.u);
   a.s *= f;
+  a.u = fmaf(a.s, d, f * a.u);
   a.m = m;
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -102,8 +103,8 @@ __device__ __forceinline__ void lp_raise(LpThread& st, float bm, float c) {
   if (bm > st.m) {
     const float d = (st.m - bm) * c;
     const uint64_t f = pair(ex2(d), ex2(d)), d2 = pair(d, d);
-    st.u = fma2(f, fma2(st.s, d2, st.u), 0ull);
-    st.s = fma2(f, st.s, 0ull);
+    st.s = mul2(f, st.s);
+    st.u = fma2(st.s, d2, mul2(f, st.u));
     st.m = bm;
   }
 }
@@ -410,8 +411,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) token_logprobs_kernel
       const LpStat b = (&sh.stat[0][0])[lane + 32];
       total += (&sh.count[0][0])[lane + 32];
       const float m = fmaxf(all.m, b.m), da = (all.m - m) * c, db = (b.m - m) * c, fa = ex2(da), fb = ex2(db);
-      all.u = fa * fmaf(all.s, da, all.u) + fb * fmaf(b.s, db, b.u);
-      all.s = fa * all.s + fb * b.s;
+      const float sa = fa * all.s, sb = fb * b.s;
+      all.u = fmaf(sa, da, fa * all.u) + fmaf(sb, db, fb * b.u);
+      all.s = sa + sb;
       all.m = m;
     }
   }

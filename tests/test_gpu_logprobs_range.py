@@ -69,3 +69,23 @@ def test_logprobs_at_every_temperature(fp4, dtype, temperature, times):
     x = x.to(TYPES[dtype])
     tokens = torch.stack([x[0].argmax(), torch.tensor(77), torch.tensor(V - 1)]).to(torch.int32)
     check(fp4, x, tokens, 5, temperature, times)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("temperature", [1.0, 1e-3, 1e-5, 1e-6])
+@pytest.mark.parametrize("V,times", [(128003, 1), (20011, 100)])
+def test_masked_rows_at_low_temperatures(fp4, dtype, temperature, V, times):
+    """A few live logits among thousands of masked ones: a thread, a warp or a CTA that has summed masked ones only meets
+    a live one later, or never."""
+    low = -math.inf if dtype == "f16" else torch.finfo(TYPES[dtype]).min
+    g = gen(V)
+    few = torch.full((V,), -math.inf)
+    few[[5, V // 2, V - 3]] = torch.tensor([1.0, 2.0, 1.5])
+    last = torch.full((V,), low)
+    last[V - 1] = -30.0
+    half = torch.randn(V, generator=g) * 3
+    half[torch.rand(V, generator=g) < 0.5] = low
+    tail = torch.randn(V, generator=g)
+    tail[: V - 700] = -math.inf
+    rows = torch.stack([few, last, half, tail]).to(TYPES[dtype])
+    check(fp4, rows, torch.tensor([5, V - 1, 17, V - 8], dtype=torch.int32), 3, temperature, times)
