@@ -2,12 +2,13 @@
 // entropy and the top alternatives (fp4gemv_token_logprobs).
 //
 // One pass over the row with running statistics (m, s, u): the maximum so
-// far, s = sum 2^(c (x - m)) and u = sum 2^(c (x - m)) c (x - m), c =
+// far, s = sum 2^(c (x - m)) and u = sum 2^(c (x - m)) (x - m), c =
 // inv_temperature log2(e); a new maximum rescales them, u to
-// f u + (f s) c (m - m'), f = 2^(c (m - m')): f s before the product, since where
-// f is 0 (masked logits alone so far) s c (m - m') need not be finite.  At the end, in base-2 logs,
-//   log2 Z = log2 s,  H = ln 2 (log2 s - u / s),
-//   logprob = (x - m) inv_temperature - ln 2 log2 s.
+// f u + (f s) (m - m'), f = 2^(c (m - m')).  u is in the logits' units, and f s
+// comes before its product: differences of logits are finite, c times them or s
+// times them need not be, and a weight or f of 0 has to leave 0.  At the end
+//   log Z = ln s,  H = log Z - inv_temperature u / s,
+//   logprob = (x - m) inv_temperature - log Z.
 //
 // Top n without sorting the row: the threads form 64 groups, each with the
 // maximum of its elements (the running maximum, which the softmax needs
@@ -56,7 +57,7 @@ constexpr int kMaxCand = 512;
 constexpr int kRaiseFrom = 256;  // collected elements that a better bound is taken from
 constexpr int kLpMaxCluster = 8;
 // Logits at or below this are masked: probability 0.  The statistics see them
-// as this value, so that no difference of two is a NaN or overflows.
+// as this value, so that no difference of two finite ones is a NaN or overflows.
 constexpr float kMasked = -0x1p100f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -79,7 +80,7 @@ __device__ __forceinline__ void lp_join_warp(LpStat& a, float c) {
   float m = a.m;
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  const float d = (a.m - m) * c, f = ex2(d);
+  const float d = a.m - m, f = ex2(d * c);
   a.s *= f;
   a.u = fmaf(a.s, d, f * a.u);
   a.m = m;
@@ -101,8 +102,8 @@ struct LpThread {
 // A new running maximum, if bm is one.
 __device__ __forceinline__ void lp_raise(LpThread& st, float bm, float c) {
   if (bm > st.m) {
-    const float d = (st.m - bm) * c;
-    const uint64_t f = pair(ex2(d), ex2(d)), d2 = pair(d, d);
+    const float d = st.m - bm, e = ex2(d * c);
+    const uint64_t f = pair(e, e), d2 = pair(d, d);
     st.s = mul2(f, st.s);
     st.u = fma2(st.s, d2, mul2(f, st.u));
     st.m = bm;
@@ -112,8 +113,8 @@ __device__ __forceinline__ void lp_raise(LpThread& st, float bm, float c) {
 // 0 for the maximum itself and rounds to its own size, where x c - RN(m c) would carry the rounding of m c, which grows
 // with |m| / temperature, into every term and into log Z.
 __device__ __forceinline__ void lp_sum(LpThread& st, uint64_t x, uint64_t c2, uint64_t m2) {
-  const uint64_t d = mul2(add2(x, m2), c2);
-  const float2 df = unpair(d);
+  const uint64_t d = add2(x, m2);
+  const float2 df = unpair(mul2(d, c2));
   const uint64_t e = pair(ex2(df.x), ex2(df.y));
   st.s = add2(st.s, e);
   st.u = fma2(e, d, st.u);
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) token_logprobs_kernel
     const float x = to_float(row[single_index(tid)]);
     lp_raise(mine, x, c);
     mine.above += x > xr;
-    const float d = (max_nan(x, kMasked) - mine.m) * c, e = ex2(d);
+    const float d = max_nan(x, kMasked) - mine.m, e = ex2(d * c);
     mine.s = add2(mine.s, pair(e, 0.0f));
     mine.u = add2(mine.u, pair(e * d, 0.0f));
   }
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) token_logprobs_kernel
     if (lane + 32 < static_cast<int>(C) * kLpWarps) {
       const LpStat b = (&sh.stat[0][0])[lane + 32];
       total += (&sh.count[0][0])[lane + 32];
-      const float m = fmaxf(all.m, b.m), da = (all.m - m) * c, db = (b.m - m) * c, fa = ex2(da), fb = ex2(db);
+      const float m = fmaxf(all.m, b.m), da = all.m - m, db = b.m - m, fa = ex2(da * c), fb = ex2(db * c);
       const float sa = fa * all.s, sb = fb * b.s;
       all.u = fmaf(sa, da, fa * all.u) + fmaf(sb, db, fb * b.u);
       all.s = sa + sb;
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) token_logprobs_kernel
     return empty || (x <= kMasked && log_z == log_z) ? kNegInf : fmaf(x - all.m, p.inv_t, -log_z);
   };
   if (tid == 0) {
-    p.entropy[t] = empty ? 0.0f : log_z - 0.6931471805599453f * (all.u / all.s);
+    p.entropy[t] = empty ? 0.0f : log_z - p.inv_t * (all.u / all.s);
     if (valid) {
       p.logprob[t] = logprob_of(xt);
       p.rank[t] = 1 + total;

@@ -89,3 +89,15 @@ def test_masked_rows_at_low_temperatures(fp4, dtype, temperature, V, times):
     tail[: V - 700] = -math.inf
     rows = torch.stack([few, last, half, tail]).to(TYPES[dtype])
     check(fp4, rows, torch.tensor([5, V - 1, 17, V - 8], dtype=torch.int32), 3, temperature, times)
+
+
+@pytest.mark.parametrize("temperature", [1.0, 1e-6])
+@pytest.mark.parametrize("times", [1, 200])
+def test_logprobs_of_the_largest_numbers(fp4, temperature, times):
+    """Differences that overflow once they are divided by T: probability 0, and nothing is NaN."""
+    V = 20011
+    x = torch.randn(2, V, generator=gen(8))
+    x[0, [9, 15000]] = torch.tensor([3.0e38, 3.0e38])
+    x[0, [70, 800]] = torch.tensor([1.0e38, -3.0e38])
+    x[1, 5] = 3.0e32
+    check(fp4, x, torch.tensor([15000, 6], dtype=torch.int32), 4, temperature, times)
