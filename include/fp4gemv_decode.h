@@ -160,13 +160,14 @@ fp4gemv_status fp4gemv_moe_route(const void* logits, int64_t ldl, int dtype, int
  * tokens int32 [T]; logprob, entropy fp32 [T]; rank int32 [T]; top_* [T,
  * top_n] (may be NULL with top_n = 0).  A token id outside [0, V) raises
  * FP4GEMV_ERR_BAD_INDEX and leaves that row's logprob and rank unwritten.
- * Logits at or below -2^100 (-inf, a type's lowest value) are masked: their
+ * Logits at or below -2^100 (-inf, bf16's and fp32's lowest value; f16's,
+ * -65504, is a logit like others) are masked: their
  * probability is 0 and their log probability -inf; a row of nothing else has
  * entropy 0.  +inf or NaN logits make the row's logprobs and entropy NaN; NaN
  * is ordered like -inf.
  * The logits are read once, and again near the top_n largest.  One launch.
  * Shapes: T >= 1, V >= 1, 0 <= top_n <= min(V, FP4GEMV_MAX_TOP_N),
- *   0 < inv_temperature <= 1e6. */
+ *   1e-20 <= inv_temperature <= 1e6. */
 fp4gemv_status fp4gemv_token_logprobs(const void* logits, int64_t ldl, int dtype, int T, int V, const int32_t* tokens,
                                       float inv_temperature, int top_n, float* logprob, int32_t* rank, float* entropy,
                                       int32_t* top_ids, float* top_logprobs, int pdl, cudaStream_t stream);

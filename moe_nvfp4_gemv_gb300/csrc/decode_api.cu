@@ -219,7 +219,8 @@ fp4gemv_status fp4gemv_token_logprobs(const void* logits, int64_t ldl, int dtype
   if (pdl != 0 && pdl != 1) return FP4GEMV_ERR_INVALID_ARG;
   if (dtype < FP4GEMV_BF16 || dtype > FP4GEMV_F32) return FP4GEMV_ERR_INVALID_ARG;
   if (T < 1 || V < 1 || top_n < 0 || top_n > V || ldl < V) return FP4GEMV_ERR_INVALID_ARG;
-  if (!(inv_temperature > 0.0f) || inv_temperature > 1e6f) return FP4GEMV_ERR_INVALID_ARG;
+  // (below: a masked logit, 2^100 away from the others, would come to weigh something)
+  if (!(inv_temperature >= 1e-20f) || inv_temperature > 1e6f) return FP4GEMV_ERR_INVALID_ARG;
   if (top_n > FP4GEMV_MAX_TOP_N || T > (1 << 28)) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(logits, dtype == FP4GEMV_F32 ? 4 : 2) || !aligned(tokens, 4) || !aligned(logprob, 4) ||
       !aligned(rank, 4) || !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4))

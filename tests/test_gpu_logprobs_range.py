@@ -101,3 +101,14 @@ def test_logprobs_of_the_largest_numbers(fp4, temperature, times):
     x[0, [70, 800]] = torch.tensor([1.0e38, -3.0e38])
     x[1, 5] = 3.0e32
     check(fp4, x, torch.tensor([15000, 6], dtype=torch.int32), 4, temperature, times)
+
+
+@pytest.mark.parametrize("temperature", [1e4, 1e12, 1e20])
+def test_masked_rows_at_high_temperatures(fp4, temperature):
+    """Up to the highest temperature masked logits (of bf16 and fp32; f16's lowest value is a logit) have no weight."""
+    x = torch.randn(2, 5003, generator=gen(9))
+    x[0, 100:3000] = -math.inf
+    x[1, ::2] = torch.finfo(torch.float32).min
+    check(fp4, x, torch.tensor([0, 4], dtype=torch.int32), 2, temperature, 1)
+    with pytest.raises(fp4.Fp4GemvError):
+        fp4.token_logprobs(x.to(DEV), torch.zeros(2, dtype=torch.int32, device=DEV), temperature=2e20)
