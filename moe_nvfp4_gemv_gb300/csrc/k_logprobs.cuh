@@ -243,7 +243,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) token_logprobs_kernel
     for (int i = tid; i < kMaxCand; i += kLpThreads) sh.cand[i] = 0;
     for (int i = tid; i < kLpMaxCluster * 32; i += kLpThreads) sh.top[i] = 0;
   }
-  if (C > 1) cluster_arrive();  // (waited for before the first store into another CTA)
+  // (what was cleared, before any thread adds to it: the first store into another CTA waits for all of the cluster)
+  if (C > 1) cluster_arrive();
+  else __syncthreads();
   pdl_wait();
   const T* row = static_cast<const T*>(p.logits) + t * p.ldl;
   const int token = __ldg(p.tokens + t);
