@@ -152,7 +152,8 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
   p.group_magic = (65536 + group - 1) / group;
   p.q_len = q_len;
   p.row_tiles = row_tiles;
-  p.window = window;
+  // (a window that no sequence is longer than is none: on the device differences of it and a position fit 32 bits)
+  p.window = window >= tokens ? 0 : window;
   p.unit = 1;
   p.item_cost = fp4::kAttnItemCost;
   p.uncut = cache->head_dim > 128 ? fp4::kAttnUncut256 : fp4::kAttnUncut;
