@@ -108,7 +108,8 @@ constexpr int kAttnFan2 = 20;
 // An item's end, in strips.  256 sequences of 500 tokens, 8 KV heads: 66 us with 8 or 16, 63 with 32.
 constexpr int kAttnItemCost = 32;
 constexpr int kAttnTcItemCost = 64;  // ... of the kernel on the 5th-generation tensor core (its figures there)
-constexpr float kAttnFloor = -1e30f;  // the running maximum before any token
+// The running maximum before any token: finite, so that no difference of two is a NaN, and below every finite score.
+constexpr float kAttnFloor = -0x1.fffffep127f;
 // Items of up to this many strips stay whole where there are CTAs for all: joining pieces costs 1.2 us, eight strips 0.15.
 // Cut / whole, one sequence on 8 KV heads of 128, us: 130 tokens 7.2 / 5.5, 300 7.5 / 6.3, 500 7.5 / 7.4, 777 7.7 / 9.1;
 // heads of 256: 300 9.0 / 8.3, 500 9.0 / 10.2; 32 rows, E4M3: 130 12.2 / 9.0, 500 12.5 / 10.3, 777 13.3 / 14.1.

@@ -23,3 +23,17 @@ def test_attention_largest_windows(kv, group, fmt, window):
     c = scaled(random_cache(pages, 2, 16, 128, g, 1.0), fmt)
     q = torch.randn(len(lens), 4, 2 * group, 128, generator=g).to(torch.bfloat16).to(DEV)
     check_attention(kv, q, c, table, lens, fmt, "bf16", window=window)
+
+
+@pytest.mark.parametrize("group,dim,fmt", [(2, 128, "e4m3"), (2, 64, "int8"), (8, 96, "e4m3"), (8, 128, "e4m3")])
+def test_attention_of_far_negative_scores(kv, group, dim, fmt):
+    """Scores of -1e32 and below are scores: their rows are not taken for empty ones.  (Scales and codes of K are alike, and
+    no warp has a second strip: next to such a score nothing else has bits left, its own rounding is 2^80.)"""
+    lens = [1, 3, 16, 17, 128]
+    g = gen(dim + group)
+    table, pages = make_table(lens, 32, g)
+    c = random_cache(pages, 1, 32, dim, g, 0.0)
+    c["k_codes"][:] = int(ref.encode(torch.tensor([1.0]), fmt)[0])
+    c["v_scale"][:] = 2.0 ** -6
+    q = -torch.ones(len(lens), 4, group, dim, dtype=torch.bfloat16, device=DEV)
+    check_attention(kv, q, c, table, lens, fmt, "bf16", sm_scale=1e30)
