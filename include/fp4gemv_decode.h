@@ -95,7 +95,8 @@ size_t fp4gemv_kv_attention_workspace_bytes(int head_dim);
  * elements (multiples of 8); lse fp32 [B * q_len, heads] or NULL.
  * Numerics: codes and queries are exact f16 operands (queries scaled by a
  * power of two for each row), sums, maxima and statistics fp32,
- * probabilities rounded to f16 for the product with V, one final rounding.
+ * probabilities rounded to f16 for the product with V (below 2^-21 of the
+ * largest, at 2^-32 of it), one final rounding.
  * With E4M3, head_dim 128 and more than 16 rows (q_len heads / kv_heads) both
  * become sums of E4M3 parts: entries of a query below 2^-14 (f16: 2^-11) of
  * its largest are rounded at 2^-22 of that, probabilities below 2^-12 of the

@@ -5,11 +5,14 @@
 // V = vs vc (codes kc, vc) the score in base 2 is
 //   s = (q . kc) ks sm_scale log2(e),
 // and instead of p = 2^(s - max s) the kernel weighs codes directly with
-//   w = 2^(s + log2 vs - m),   m the running maximum of s + log2 vs,
+//   w = 2^(s + log2 vs - m),   m + kAttnLift the running maximum of s + log2 vs,
 // so that out = (sum w vc) / (sum w / vs) with w of one size whatever the
 // scales: w is rounded to f16 for the product with vc, sums stay fp32.  The
-// codes are exact in f16.  Queries are made exact f16 operands by a power of
-// two for each row.
+// maximum's weight is 2^kAttnLift and not 1, so that f16 holds 11 bits of
+// weights down to 2^-21 of it and loses only what is below 2^-32: with weights
+// up to 1 the edge was 2^-25, and a long tail of tokens below it was missing
+// from the output that its sum is counted in.  The codes are exact in f16.
+// Queries are made exact f16 operands by a power of two for each row.
 //
 // The work.  KV bytes are read once, 16 tokens (a strip) of K and V of one
 // head at a time, by mma.sync m16n8k16 in the transposed form: the codes are
@@ -22,9 +25,9 @@
 // bytes, V's pairs of tokens are joined by byte permutes before the
 // conversion, and the weights turn from accumulator to operand by movmatrix.
 //
-// m follows the maximum lazily: weights may grow to 2^kAttnSlack before m
-// moves (f16 holds them, fp32 sums do), so the usual strip costs one vote and
-// no shuffles; a strip that would exceed it reduces its maxima over the warp
+// m follows the maximum lazily: weights may grow to 2^(kAttnLift + kAttnSlack)
+// before m moves (f16 holds them, fp32 sums do), so the usual strip costs one
+// vote and no shuffles; a strip that would exceed it reduces its maxima over the warp
 // and rescales.
 //
 // Every warp streams its own strips through its own ring of cp.async stages
@@ -114,8 +117,10 @@ constexpr float kAttnFloor = -0x1.fffffep127f;
 // Cut / whole, one sequence on 8 KV heads of 128, us: 130 tokens 7.2 / 5.5, 300 7.5 / 6.3, 500 7.5 / 7.4, 777 7.7 / 9.1;
 // heads of 256: 300 9.0 / 8.3, 500 9.0 / 10.2; 32 rows, E4M3: 130 12.2 / 9.0, 500 12.5 / 10.3, 777 13.3 / 14.1.
 constexpr int kAttnUncut = 40, kAttnUncut256 = 20;
-// log2 of the largest weight before the running maximum moves.  256 sequences of 500 tokens: 66 us; with 0 68.8.
-constexpr float kAttnSlack = 8.0f;
+// log2 of the weight of the running maximum; and of how much larger a weight may be before the running maximum moves: 256
+// sequences of 500 tokens 66 us; with 0 68.8.  (2^15 in all: f16 holds 65504.)
+constexpr float kAttnLift = 7.0f, kAttnSlack = 8.0f;
+constexpr float kAttnUnlift = 0x1p-7f;  // 2^-kAttnLift
 
 __device__ __forceinline__ float attn_ex2(float x) {
   float y;
@@ -946,7 +951,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
       float ks, vs;
       asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(kb + 2 * L::kStripBytes));
       const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
-      const float inv_vs = attn_ex2(-lv);
+      const float inv_vs = attn_ex2(-lv) * kAttnUnlift;  // (sums stay those of weights up to 1)
       const bool masked = tok + 16 > tokens_all || tok < tokens_low;
       // Exponents against the running maxima, in the scores' place; against 0 while the warp has seen no strip that
       // every row sees some of (`fresh`: a row's first maximum is only known then).  Where they are masked, too high
@@ -962,7 +967,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
           sc[nt][2 + h] = fmaf(sc[nt][2 + h], f, base);
           high = fmaxf(high, fmaxf(sc[nt][h], sc[nt][2 + h]));
         }
-      if (masked || fresh || __any_sync(0xFFFFFFFFu, high > kAttnSlack)) {
+      if (masked || fresh || __any_sync(0xFFFFFFFFu, high > kAttnLift + kAttnSlack)) {
 #pragma unroll
         for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
@@ -979,7 +984,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
             float top = fmaxf(r0, r1);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const float mn = fmaxf(m[nt][h], top);
+            const float mn = fmaxf(m[nt][h], top - kAttnLift);
             const float fall = attn_ex2(m[nt][h] - mn);
             m[nt][h] = mn;
             sum[nt][h] *= fall;
@@ -1042,7 +1047,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) sum[nt][h] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][h], o);
-        if (g == 0) ml[warp * C::kRows + nt * 8 + 2 * t + h] = make_float2(m[nt][h], sum[nt][h]);
+        if (g == 0) ml[warp * C::kRows + nt * 8 + 2 * t + h] = make_float2(m[nt][h] + kAttnLift, sum[nt][h]);
       }
     // the stage that is neither being read nor being filled, the one before the next: 8 rows of dims, fp32
     const int idle = (warp * C::kStages + before(stage)) * C::kStageBytes;
@@ -1078,10 +1083,10 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
           const float2 o = ml[w * C::kRows + r];
-          const float f = attn_ex2(o.x - top);
+          const float f = attn_ex2(o.x - top), fv = f * kAttnUnlift;  // (sums of weights up to 1, as those of weights are)
           const float* const cells = reinterpret_cast<const float*>(smem + free_stage[w]);
           const float4 a = *reinterpret_cast<const float4*>(cells + from_cell);
-          v.x = fmaf(a.x, f, v.x), v.y = fmaf(a.y, f, v.y), v.z = fmaf(a.z, f, v.z), v.w = fmaf(a.w, f, v.w);
+          v.x = fmaf(a.x, fv, v.x), v.y = fmaf(a.y, fv, v.y), v.z = fmaf(a.z, fv, v.z), v.w = fmaf(a.w, fv, v.w);
           l = fmaf(o.y, f, l);
         }
         if (whole) {

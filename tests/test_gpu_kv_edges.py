@@ -37,3 +37,34 @@ def test_attention_of_far_negative_scores(kv, group, dim, fmt):
     c["v_scale"][:] = 2.0 ** -6
     q = -torch.ones(len(lens), 4, group, dim, dtype=torch.bfloat16, device=DEV)
     check_attention(kv, q, c, table, lens, fmt, "bf16", sm_scale=1e30)
+
+
+def tail_output(kv, fmt, heads, q_len, dim, bits, n=32768, B=320):
+    """B sequences over the same n tokens: the first scores `bits` (base 2) above all others and holds zeros, the others
+    ones.  Returns (out, the exact value)."""
+    block = 128
+    one, top = (int(ref.encode(torch.tensor([x]), fmt)[0]) for x in (1.0, float(bits)))
+    cache = kv.KvCache8.allocate(n // block, 1, dim, block, fmt)
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(1.0)
+    cache.v_codes.fill_(one)
+    table = torch.arange(n // block, dtype=torch.int32, device=DEV).repeat(B, 1)
+    cache.k_codes[0, 0, 0, 0] = top
+    cache.v_codes[0, 0, 0] = 0
+    q = torch.zeros(B, q_len, heads, dim, dtype=torch.float16, device=DEV)
+    q[..., 0] = 1.0
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    out = cache.attend(q, table, lens, sm_scale=math.log(2.0))
+    seen = torch.arange(n - q_len, n, dtype=torch.float64, device=DEV).view(1, q_len, 1, 1)  # others, for each query
+    return out.double(), (seen * 2.0 ** -bits / (1 + seen * 2.0 ** -bits)).expand_as(out)
+
+
+@pytest.mark.parametrize("heads,q_len,dim,fmt", [(8, 1, 128, "e4m3"), (8, 1, 64, "int8"), (4, 3, 256, "e4m3"),
+                                                 (6, 4, 96, "e4m3"), (32, 1, 128, "int8")])
+@pytest.mark.parametrize("bits", [24, 26, 28])
+def test_attention_small_weights_count(kv, heads, q_len, dim, fmt, bits):
+    """Weights of 2^-24 to 2^-28 of the largest, 32767 of them: f16 rounds the weights (2^-11 relative, from 2^-21 of the
+    largest down 2^-32 of it), so what is lost is at most 2^-32 for each; f16 outputs."""
+    out, want = tail_output(kv, fmt, heads, q_len, dim, bits)
+    d = 2.0 ** -10 * want + 32768 * 2.0 ** -32
+    assert ((out - want).abs() <= d).all(), float((out / want).min())
