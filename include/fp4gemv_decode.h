@@ -98,9 +98,9 @@ size_t fp4gemv_kv_attention_workspace_bytes(int head_dim);
  * probabilities rounded to f16 for the product with V (below 2^-21 of the
  * largest, at 2^-32 of it), one final rounding.
  * With E4M3, head_dim 128 and more than 16 rows (q_len heads / kv_heads) both
- * become sums of E4M3 parts: entries of a query below 2^-14 (f16: 2^-11) of
- * its largest are rounded at 2^-22 of that, probabilities below 2^-12 of the
- * largest at 2^-24; an infinite entry counts as NaN.
+ * become sums of 8-bit parts, which hold f16's probabilities exactly; entries
+ * of a query below 2^-14 (f16: 2^-11) of its largest are rounded at 2^-22 of
+ * that, and an infinite entry counts as NaN.
  * Page memory past seq_lens is never used, whatever it holds.  Lengths
  * outside [0, max_blocks * block_size] are clamped, and tokens on a page id
  * outside [0, num_blocks) read as zeros; both raise FP4GEMV_ERR_BAD_INDEX.

@@ -4,18 +4,22 @@
 //
 // The mathematics of k_kv_attention.cuh, with both products on the codes as
 // they lie in the cache: tcgen05.mma of kind f8f6f4 takes E4M3 from shared
-// memory, so no code is converted.  What meets the codes is made E4M3 as well,
-// as sums of E4M3 values of 4 significant bits each:
+// memory, so no code is converted.  What meets the codes is made 8 bits wide as
+// well, as sums of such values:
 //
 // * a query row, scaled by a power of two to a largest magnitude in
-//   [128, 256), is q1 + (q2 + q3) / 32.  Two parts hold bf16's 8 bits and three
-//   f16's 11; values below 2^-14 of the row's largest (f16: 2^-11) lose bits
-//   below 2^-22 of it.  S^T [128 tokens x 64] = K [128 x 128] [q1 | q2 + q3]^T, the parts side
-//   by side on N, q3 added by an MMA of its own (f16 only).
-// * a weight w = 2^(s + log2 vs - m), rounded to f16 as it is there, is
-//   (w1 + w2 / 32 + w3 / 1024) / 16, which holds its 11 bits; of weights below
-//   2^-12 what lies below 2^-24 goes.  (What a part leaves is at most half the
-//   last place of its 4 bits, 8 of 256, so 32 times it fits the next.)
+//   [128, 256), is q1 + (q2 + q3) / 32 in E4M3 of 4 bits each.  Two parts hold
+//   bf16's 8 bits and three f16's 11; values below 2^-14 of the row's largest
+//   (f16: 2^-11) lose bits below 2^-22 of it.  S^T [128 tokens x 64] = K
+//   [128 x 128] [q1 | q2 + q3]^T, the parts side by side on N, q3 added by an MMA
+//   of its own (f16 only).
+// * a weight w = 2^(s + log2 vs - m + kWScale), rounded to f16 as it is there, is
+//   w1 + w2 / 16 + w3 / 256 in E5M2, of 3 bits each and f16's exponents: exactly,
+//   for every f16 up to 2^15.  (What a part leaves is at most half the last place
+//   of its 3 bits, 2^11 of 2^15, so 16 times it fits the next; with the parts'
+//   signs that is 11 bits.)  The maximum's weight is 2^kWScale, so that a long tail
+//   of small ones is not lost: f16 has 11 bits of them down to 2^-25 of the maximum
+//   and loses what is below 2^-36.  (E4M3 parts of weights up to 1 end at 2^-24.)
 //   out^T [128 dims x 96] = V^T [128 dims x 128 tokens] [w1 | w2 | w3]: V^T is
 //   read from the V tile as it lies (M-major), the weights' tile has a token's
 //   96 bytes in a row (N-major).
@@ -73,12 +77,13 @@ struct AttnTc {
   static constexpr int smem(int B) { return 1024 + kSeqOff + (B + 1) * 12; }
   static constexpr uint32_t kCols = 512;     // TMEM: S 64 for each group, then out 96 for each
   static constexpr int kSCols = 64, kOCols = 96;
-  static constexpr float kSlack = 4.0f;      // log2 of the largest weight before m moves
-  static constexpr float kWScale = 4.0f;     // log2 of w1's scale: w1 up to 2^8, of E4M3's 448
+  static constexpr float kWScale = 11.0f;    // log2 of the maximum's weight
+  static constexpr float kWUnscale = 0x1p-11f;
+  static constexpr float kSlack = 4.0f;      // ... and of how much larger one may be before m moves: 2^15 in all
 };
 
-// D[tmem] (+)= A[smem] B[smem], E4M3
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// D[tmem] (+)= A[smem] B[smem], of the 8-bit types that the instruction descriptor names
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
       "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(
@@ -86,9 +91,12 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// kind::f8f6f4, E4M3 A and B, fp32 D; `mn`: both operands M- and N-major
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, bool mn) {
-  return (1u << 4) | (mn ? (1u << 15) | (1u << 16) : 0u) | ((N >> 3) << 17) | ((M >> 4) << 24);
+// kind::f8f6f4, fp32 D: E4M3 A and B, both K-major; E4M3 A and E5M2 B, M- and N-major
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32_mn(uint32_t M, uint32_t N) {
+  return (1u << 4) | (1u << 10) | (1u << 15) | (1u << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 // Shared-memory matrix descriptor of an M- or N-major tile of up to 128 one-byte
 // rows: 128-byte lines, one for each k, swizzled in atoms of 8.
@@ -120,6 +128,16 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint16_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
+__device__ __forceinline__ uint16_t e5m2x2_of_f16x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of_e5m2x2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t join16(uint16_t lo, uint16_t hi) {
   uint32_t r;
   asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(lo), "h"(hi));
@@ -133,6 +151,11 @@ __device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t f16x2_mul32(uint32_t a) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x50005000u));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_mul16(uint32_t a) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x4C004C00u));
   return r;
 }
 template <int kId>
@@ -335,8 +358,8 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
   } else if (warp >= C::kWeighers / 32) {
     // ---- MMA warp of group g: the tiles of the CTA whose number is g mod 2 ----
     const int g = warp - C::kWeighers / 32;
-    constexpr uint32_t id_s = idesc_e4m3_f32(128, 64, false), id_s3 = idesc_e4m3_f32(128, 32, false);
-    constexpr uint32_t id_o = idesc_e4m3_f32(128, 96, true);
+    constexpr uint32_t id_s = idesc_e4m3_f32(128, 64), id_s3 = idesc_e4m3_f32(128, 32);
+    constexpr uint32_t id_o = idesc_e4m3_e5m2_f32_mn(128, 96);
     const uint64_t q_desc = sdesc_sw128(sm + C::kQOff), w_desc = sdesc_mn_sw128(sm + C::kWOff + g * C::kTileBytes);
     int first_tile = 0, count = 0;  // tiles before the segment; the group's tiles
     while (at < end) {
@@ -353,11 +376,11 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         if (ok && elect_one()) {
           const uint64_t k_desc = sdesc_sw128(sm + stage * C::kTileBytes);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_e4m3(group_s[g], k_desc + 2 * k, q_desc + 2 * k, id_s, k > 0);
+          for (int k = 0; k < 4; ++k) mma_f8(group_s[g], k_desc + 2 * k, q_desc + 2 * k, id_s, k > 0);
           if (p.f16) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_e4m3(group_s[g] + 32, k_desc + 2 * k, q_desc + (64 * C::kDim >> 4) + 2 * k, id_s3, 1u);
+              mma_f8(group_s[g] + 32, k_desc + 2 * k, q_desc + (64 * C::kDim >> 4) + 2 * k, id_s3, 1u);
           }
           mma_commit(scored(g));
           mma_commit(k_empty(stage));
@@ -377,7 +400,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
           const uint64_t v_desc = sdesc_mn_sw128(sm + C::kVOff + stage * C::kTileBytes);
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 tokens each, 4096 bytes
-            mma_e4m3(group_o[g], v_desc + 256 * k, w_desc + 256 * k, id_o, j > j0 || k > 0);
+            mma_f8(group_o[g], v_desc + 256 * k, w_desc + 256 * k, id_o, j > j0 || k > 0);
           mma_commit(added(g));
           mma_commit(v_empty(stage));
         }
@@ -578,7 +601,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
           }
         }
         // weights, their sums, their parts
-        const uint64_t inv2 = pair(inv_vs, inv_vs);
+        const uint64_t inv2 = pair(inv_vs * C::kWUnscale, inv_vs * C::kWUnscale);  // (sums are those of weights up to 1)
 #pragma unroll
         for (int r0 = 0; r0 < C::kRows; r0 += 16) {
           uint32_t part[3][4];
@@ -592,10 +615,10 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
               const float a = attn_ex2(e.x), b = attn_ex2(e.y);
               sum[i] = fma2(pair(a, b), inv2, sum[i]);
               const uint32_t w = pack_f16(a, b);
-              code[0][h] = e4m3x2_of_f16x2(w);
-              const uint32_t rest = f16x2_mul32(f16x2_sub(w, f16x2_of_e4m3x2(code[0][h])));  // (exact)
-              code[1][h] = e4m3x2_of_f16x2(rest);
-              code[2][h] = e4m3x2_of_f16x2(f16x2_mul32(f16x2_sub(rest, f16x2_of_e4m3x2(code[1][h]))));
+              code[0][h] = e5m2x2_of_f16x2(w);
+              const uint32_t rest = f16x2_mul16(f16x2_sub(w, f16x2_of_e5m2x2(code[0][h])));  // (exact)
+              code[1][h] = e5m2x2_of_f16x2(rest);
+              code[2][h] = e5m2x2_of_f16x2(f16x2_mul16(f16x2_sub(rest, f16x2_of_e5m2x2(code[1][h]))));
             }
 #pragma unroll
             for (int u = 0; u < 3; ++u) part[u][k] = join16(code[u][0], code[u][1]);
@@ -629,12 +652,12 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         tmem_get32(o_cols, o);
         tmem_get32(o_cols + 32, low);
 #pragma unroll
-        for (int r = 0; r < 32; ++r) o[r] = fmaf(low[r], 0.03125f, o[r]);
+        for (int r = 0; r < 32; ++r) o[r] = fmaf(low[r], 0.0625f, o[r]);
         tmem_get32(o_cols + 64, low);
         tc_fence_before();
         float* const mine = reinterpret_cast<float*>(smem + C::kWOff + g * C::kTileBytes);
 #pragma unroll
-        for (int r = 0; r < 32; ++r) mine[r * C::kDim + who] = any ? fmaf(low[r], 0.0009765625f, o[r]) : 0.0f;
+        for (int r = 0; r < 32; ++r) mine[r * C::kDim + who] = any ? fmaf(low[r], 0.00390625f, o[r]) * C::kWUnscale : 0.0f;
       }
       const bool failed = named_any(3, C::kWeighers, !ok);  // (some wait ran out: NaN)
       const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
@@ -653,13 +676,12 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         const float4 w = *reinterpret_cast<const float4*>(a + C::kTileBytes / 4);
         const float4 v = make_float4(u.x * f0 + w.x * f1, u.y * f0 + w.y * f1, u.z * f0 + w.z * f1, u.w * f0 + w.w * f1);
         const float l = failed ? __int_as_float(0x7FC00000) : l0 * f0 + l1 * f1;
-        // (weights are 2^kWScale of what m says)
         if (whole) {
-          item_end.store(r, d, v, top - C::kWScale, l);
+          item_end.store(r, d, v, top, l);
         } else {
           float* const o = part + r * (C::kDim + 4);
           __stcg(reinterpret_cast<float4*>(o + d), v);
-          if (d == 0) __stcg(reinterpret_cast<float2*>(o + C::kDim), make_float2(top - C::kWScale, l));
+          if (d == 0) __stcg(reinterpret_cast<float2*>(o + C::kDim), make_float2(top, l));
         }
       }
       if (!whole) item_end.share(plan_words, line_before, ml, &last_flag, [] { named_sync<3>(C::kWeighers); });

@@ -68,3 +68,12 @@ def test_attention_small_weights_count(kv, heads, q_len, dim, fmt, bits):
     out, want = tail_output(kv, fmt, heads, q_len, dim, bits)
     d = 2.0 ** -10 * want + 32768 * 2.0 ** -32
     assert ((out - want).abs() <= d).all(), float((out / want).min())
+
+
+@pytest.mark.parametrize("heads,q_len", [(32, 1), (6, 4), (24, 2)])
+@pytest.mark.parametrize("bits", [22, 24, 26, 28])
+def test_attention_wide_small_weights_count(kv, heads, q_len, bits):
+    """The same on the tensor core: three parts of a weight hold what f16 does."""
+    out, want = tail_output(kv, "e4m3", heads, q_len, 128, bits)
+    d = 2.0 ** -10 * want + 32768 * 2.0 ** -32
+    assert ((out - want).abs() <= d).all(), float((out / want).min())
