@@ -101,9 +101,11 @@ size_t fp4gemv_kv_attention_workspace_bytes(int head_dim);
  * become sums of 8-bit parts, which hold f16's probabilities exactly; entries
  * of a query below 2^-14 (f16: 2^-11) of its largest are rounded at 2^-22 of
  * that, and an infinite entry counts as NaN.
- * Page memory past seq_lens is never used, whatever it holds.  Lengths
- * outside [0, max_blocks * block_size] are clamped, and tokens on a page id
- * outside [0, num_blocks) read as zeros; both raise FP4GEMV_ERR_BAD_INDEX.
+ * What a query does not see has no part in its row, whatever it holds: NaN
+ * codes of later tokens or of tokens before the window, page memory past
+ * seq_lens.  Lengths outside [0, max_blocks * block_size] are clamped, and
+ * tokens on a page id outside [0, num_blocks) read as zeros; both raise
+ * FP4GEMV_ERR_BAD_INDEX.
  * workspace: at least fp4gemv_kv_attention_workspace_bytes(head_dim) bytes,
  * 16-byte aligned.
  * Shapes: 1 <= B <= FP4GEMV_KV_MAX_BATCH, 1 <= q_len <= FP4GEMV_KV_MAX_QLEN,

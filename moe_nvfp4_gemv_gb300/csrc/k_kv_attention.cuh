@@ -672,6 +672,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
   __shared__ AttnPlace places[3];  // the item being read and the next one by turns; the share's begin
   __shared__ int plan_words[6];
   __shared__ int free_stage[C::kWarps];  // byte offset of the warp's idle ring stage
+  __shared__ uint32_t nan_dims[C::kRows][kDim / 32];  // of the segment's rows: dims where a token that the row sees is NaN
+  __shared__ int nan_any;
   __shared__ int last_flag;
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (uniform, and known to be)
@@ -685,6 +687,10 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
   int* const line_before = strips_before + p.B + 1;
   int* const tokens = line_before + p.B + 1;
   if (tid == 0) pdl_launch_dependents();
+  if (!kInt8) {
+    for (int i = tid; i < C::kRows * (kDim / 32); i += C::kThreads) (&nan_dims[0][0])[i] = 0u;
+    if (tid == 0) nan_any = 0;
+  }
   pdl_wait();
 
   const int rows = p.q_len * p.group;  // query rows of a KV head
@@ -902,7 +908,36 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
         for (int nt = 0; nt < kN; ++nt) mma_f16(acc[nt][(blk * L::kVWords + k) * 2 + j], a, pb[nt][0], pb[nt][1]);
       }
     };
-    auto v_load = [&](uint32_t vb, int blk, int left, uint32_t (&w)[4][L::kVWords]) {
+    // A strip that some row sees only in part: a weight of 0 does not silence a NaN code (E4M3; INT8 has none), so NaNs
+    // give way to zeros, and the rows that do see the token are noted for the segment's end.
+    auto quiet = [&](int tok, int blk, uint32_t (&w)[4][L::kVWords]) {
+      uint32_t found = 0u;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int k = 0; k < L::kVWords; ++k) found |= (w[c][k] & 0x7F7F7F7Fu) + 0x01010101u;
+      if ((found & 0x80808080u) == 0u) return;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int k = 0; k < L::kVWords; ++k) {
+          const uint32_t nan = ((w[c][k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // the NaN codes' high bits
+          if (nan == 0u) continue;
+          w[c][k] &= ~((nan >> 7) * 0xFFu);
+          const int at = tok + 2 * t + (c & 1) + (c >> 1) * 8, d = L::v_dim(blk, k, g);
+          const uint32_t dims = ((nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u)) << (d & 31);
+#pragma unroll 1
+          for (int r = 0; r < min(C::kRows, rows - row0); ++r) {
+            const int see_to = n - p.q_len + (((row0 + r) * p.group_magic) >> 16) + 1;
+            if (at < see_to && (p.window == 0 || at >= see_to - p.window)) {
+              atomicOr(&nan_dims[r][d >> 5], dims);
+              nan_any = 1;
+            }
+          }
+        }
+    };
+    auto v_load = [&](uint32_t vb, int blk, int tok, bool masked, uint32_t (&w)[4][L::kVWords]) {
+      const int left = n - tok;
 #pragma unroll
       for (int c = 0; c < 4; ++c) L::v_words(vb, v_place, c, blk, w[c]);
       if (left < 16) {  // past the end: whatever lies there counts nothing
@@ -913,6 +948,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
             for (int k = 0; k < L::kVWords; ++k) w[c][k] = 0u;
           }
       }
+      if (!kInt8 && masked) quiet(tok, blk, w);
     };
     // this warp's strips of the segment: begin + warp + k kWarps
     int tok = tok0 + (((begin + warp - at) & (C::kWarps - 1)) << 4);
@@ -1021,7 +1057,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
         for (int blk = 0; blk < L::kBlocks; ++blk) {
           uint32_t wk[2][L::kWords], wv[4][L::kVWords];
           k_load(next_kb, blk, wk);
-          v_load(vb, blk, n - tok, wv);
+          v_load(vb, blk, tok, masked, wv);
 #pragma unroll
           for (int k = 0; k < L::kVWords; ++k) {
             score(wk, blk, 2 * k, sc);
@@ -1032,7 +1068,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
 #pragma unroll
         for (int blk = 0; blk < L::kBlocks; ++blk) {
           uint32_t w[4][L::kVWords];
-          v_load(vb, blk, n - tok, w);
+          v_load(vb, blk, tok, masked, w);
 #pragma unroll
           for (int k = 0; k < L::kVWords; ++k) weigh(w, blk, k, pb);
         }
@@ -1059,6 +1095,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
     const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
     const AttnItemEnd<kDim, C::kThreads> item_end = {p, cur, row0, used};
     float* const part = item_end.part_of(blockIdx.x, starts ? 1 : 0);
+    bool nans = false;
 #pragma unroll
     for (int nt = 0; nt < kN; ++nt) {  // eight rows at a time
       if (nt * 8 >= used) break;
@@ -1070,6 +1107,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
           *reinterpret_cast<float4*>(mine + cell(2 * t + h, k, g)) = make_float4(
               acc[nt][2 * k][h], acc[nt][2 * k][2 + h], acc[nt][2 * k + 1][h], acc[nt][2 * k + 1][2 + h]);
       __syncthreads();
+      if (!kInt8) nans = nan_any != 0;  // (read between two barriers: all threads alike)
       if (C::kQInRegs && seg_end < end) q_load(places[which ^ 1], 0, qr);  // (arrives during the joining)
       for (int x = tid; x < 8 * (kDim / 4); x += C::kThreads) {
         const int r8 = x / (kDim / 4), d = (x - r8 * (kDim / 4)) * 4, r = nt * 8 + r8;
@@ -1089,6 +1127,14 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
           v.x = fmaf(a.x, fv, v.x), v.y = fmaf(a.y, fv, v.y), v.z = fmaf(a.z, fv, v.z), v.w = fmaf(a.w, fv, v.w);
           l = fmaf(o.y, f, l);
         }
+        if (nans) {
+          const uint32_t nan = nan_dims[r][d >> 5] >> (d & 31);
+          const float none = __int_as_float(0x7FC00000);
+          if (nan & 1u) v.x = none;
+          if (nan & 2u) v.y = none;
+          if (nan & 4u) v.z = none;
+          if (nan & 8u) v.w = none;
+        }
         if (whole) {
           item_end.store(r, d, v, top, l);
         } else {
@@ -1097,6 +1143,11 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
           if (d == 0) __stcg(reinterpret_cast<float2*>(o + kDim), make_float2(top, l));
         }
       }
+      __syncthreads();
+    }
+    if (nans) {
+      for (int i = tid; i < C::kRows * (kDim / 32); i += C::kThreads) (&nan_dims[0][0])[i] = 0u;
+      if (tid == 0) nan_any = 0;
       __syncthreads();
     }
     if (!whole)

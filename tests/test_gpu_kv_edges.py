@@ -77,3 +77,37 @@ def test_attention_wide_small_weights_count(kv, heads, q_len, bits):
     out, want = tail_output(kv, "e4m3", heads, q_len, 128, bits)
     d = 2.0 ** -10 * want + 32768 * 2.0 ** -32
     assert ((out - want).abs() <= d).all(), float((out / want).min())
+
+
+def check_nan_values(kv, q_len, group, dim, block, window):
+    """NaN values of tokens that some queries see, some do not, and (before the window) none does: NaN where the formula
+    says, the other outputs as if they were not there."""
+    lens = [1, 5, 16, 17, 40, 129, 133, 300, 1000]
+    g = gen(dim + q_len + block)
+    table, pages = make_table(lens, block, g)
+    c = scaled(random_cache(pages, 2, block, dim, g, 1.0), "e4m3")
+    for b, n in enumerate(lens):
+        first = n - q_len + 1 - window if window else n  # the first query's first token
+        for i, t in enumerate((n - 1, n - 2, n - q_len, first, first - 1, first - 2)):
+            if 0 <= t < n and (i < 3 or window):
+                code = c["v_codes"][int(table[b, t // block])]
+                code[b % 2, t % block, 3 + 8 * i] = 0x7F
+                code[b % 2, t % block, dim - 1 - i] = 0xFF
+    q = torch.randn(len(lens), q_len, 2 * group, dim, generator=g).to(torch.float16).to(DEV)
+    n_len = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out = on_gpu(kv, c, "e4m3").attend(q, table.to(DEV), n_len, window=window)
+    want, _, mass, _ = ref.attention(q, {k: v.to(DEV) for k, v in c.items()}, table, lens, "e4m3", 1 / math.sqrt(dim),
+                                     window)
+    assert torch.equal(out.isnan(), want.isnan())
+    assert 0 < int(want.isnan().sum()) < want.numel() // 8
+    vmax = float(ref.decode(c["v_codes"], "e4m3").abs().nan_to_num(0).amax() * c["v_scale"].amax())
+    d = 2.0 ** -10 * mass + max(lens) * 2.0 ** -25 * vmax
+    low, high = (want - d).to(q.dtype), (want + d).to(q.dtype)
+    assert (((out >= low) & (out <= high)) | want.isnan()).all()
+
+
+@pytest.mark.parametrize("q_len,group,dim,block", [(4, 2, 128, 16), (3, 5, 64, 32), (2, 7, 256, 16), (4, 8, 96, 64),
+                                                   (8, 1, 128, 128), (16, 1, 128, 16)])
+@pytest.mark.parametrize("window", [0, 1, 20, 130])
+def test_attention_nan_values_of_unseen_tokens(kv, q_len, group, dim, block, window):
+    check_nan_values(kv, q_len, group, dim, block, window)
