@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
   __shared__ float row_tmp[C::kWeighers / 32][C::kRows];          // maxima, sums of the warps
   __shared__ __align__(16) float row_fall[C::kGroups][C::kRows];
   __shared__ float2 ml[C::kRows];
+  __shared__ uint32_t nan_dims[C::kRows][C::kDim / 32];  // of the segment's rows: dims where a token that the row sees is NaN
+  __shared__ int nan_any;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   uint8_t* const smem = smem_tc + (-smem_u32(smem_tc) & 1023u);  // (swizzle atoms of 1024 bytes)
@@ -244,6 +246,8 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
     prefetch_tensormap(&p.k_map);
     prefetch_tensormap(&p.v_map);
   }
+  if (tid < C::kRows * (C::kDim / 32)) (&nan_dims[0][0])[tid] = 0u;
+  if (tid == 0) nan_any = 0;
   pdl_wait();
   if (warp == C::kWeighers / 32) {
     tmem_alloc(smem_u32(&tmem_slot), C::kCols);
@@ -525,10 +529,38 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f)), inv_vs = attn_ex2(-lv);
         const bool live = tok < tok_end && tok >= tok_low;
         const bool masked = tile0 + C::kTile > min(tokens_all, tok_end) || tile0 < tokens_low;
+        const uint32_t v_row = sm + C::kVOff + stage * C::kTileBytes + who * 128;
         if (!live) {  // whatever lies there counts nothing
-          const uint32_t v_row = sm + C::kVOff + stage * C::kTileBytes + who * 128;
 #pragma unroll
           for (int k = 0; k < 8; ++k) sts128(v_row + k * 16, make_uint4(0, 0, 0, 0));
+        } else if (masked) {
+          // A tile that some row sees only in part: a weight of 0 does not silence a NaN code, so NaNs give way to zeros, and
+          // the rows that do see the token are noted for the segment's end.  (Chunk k of the row lies at k ^ its row mod 8.)
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            const uint4 chunk = lds128(v_row + k * 16);
+            uint32_t w[4] = {chunk.x, chunk.y, chunk.z, chunk.w};
+            uint32_t found = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) found |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;
+            if ((found & 0x80808080u) == 0u) continue;
+            uint32_t dims = 0u;  // of the chunk's 16
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t nan = ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // the NaN codes' high bits
+              w[i] &= ~((nan >> 7) * 0xFFu);
+              dims |= ((nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u)) << (4 * i);
+            }
+            sts128(v_row + k * 16, make_uint4(w[0], w[1], w[2], w[3]));
+            const int chunk_no = k ^ (who & 7);
+            for (int r = 0; r < used; ++r) {
+              const int see_to = n - p.q_len + (((row0 + r) * p.group_magic) >> 16) + 1;
+              if (tok < see_to && (p.window == 0 || tok >= see_to - p.window)) {
+                atomicOr(&nan_dims[r][chunk_no >> 1], dims << (16 * (chunk_no & 1)));
+                nan_any = 1;
+              }
+            }
+          }
         }
         // the weights' exponents against the running maxima
         float top = 0.0f;
@@ -660,6 +692,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         for (int r = 0; r < 32; ++r) mine[r * C::kDim + who] = any ? fmaf(low[r], 0.00390625f, o[r]) * C::kWUnscale : 0.0f;
       }
       const bool failed = named_any(3, C::kWeighers, !ok);  // (some wait ran out: NaN)
+      const bool nans = nan_any != 0;                        // (read between two barriers: all threads alike)
       const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
       const AttnItemEnd<C::kDim, C::kWeighers> item_end = {p, cur, row0, used};
       float* const part = item_end.part_of(blockIdx.x, starts ? 1 : 0);
@@ -674,8 +707,16 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         const float* a = reinterpret_cast<const float*>(smem + C::kWOff) + r * C::kDim + d;
         const float4 u = *reinterpret_cast<const float4*>(a);
         const float4 w = *reinterpret_cast<const float4*>(a + C::kTileBytes / 4);
-        const float4 v = make_float4(u.x * f0 + w.x * f1, u.y * f0 + w.y * f1, u.z * f0 + w.z * f1, u.w * f0 + w.w * f1);
+        float4 v = make_float4(u.x * f0 + w.x * f1, u.y * f0 + w.y * f1, u.z * f0 + w.z * f1, u.w * f0 + w.w * f1);
         const float l = failed ? __int_as_float(0x7FC00000) : l0 * f0 + l1 * f1;
+        if (nans) {
+          const uint32_t nan = nan_dims[r][d >> 5] >> (d & 31);
+          const float none = __int_as_float(0x7FC00000);
+          if (nan & 1u) v.x = none;
+          if (nan & 2u) v.y = none;
+          if (nan & 4u) v.z = none;
+          if (nan & 8u) v.w = none;
+        }
         if (whole) {
           item_end.store(r, d, v, top, l);
         } else {
@@ -686,6 +727,11 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
       }
       if (!whole) item_end.share(plan_words, line_before, ml, &last_flag, [] { named_sync<3>(C::kWeighers); });
       named_sync<3>(C::kWeighers);  // (before the tables and tiles are written again)
+      if (nans) {
+        if (tid < C::kRows * (C::kDim / 32)) (&nan_dims[0][0])[tid] = 0u;
+        if (tid == 0) nan_any = 0;
+        named_sync<3>(C::kWeighers);
+      }
       first_tile += tiles;
       at = seg_end;
       if (at < end) cur = attn_next(p, cur, strips_before, tokens);

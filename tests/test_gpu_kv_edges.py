@@ -111,3 +111,9 @@ def check_nan_values(kv, q_len, group, dim, block, window):
 @pytest.mark.parametrize("window", [0, 1, 20, 130])
 def test_attention_nan_values_of_unseen_tokens(kv, q_len, group, dim, block, window):
     check_nan_values(kv, q_len, group, dim, block, window)
+
+
+@pytest.mark.parametrize("q_len,group,block", [(4, 8, 16), (3, 11, 64), (16, 4, 128), (2, 12, 32)])
+@pytest.mark.parametrize("window", [0, 1, 20, 130, 300])
+def test_attention_wide_nan_values_of_unseen_tokens(kv, q_len, group, block, window):
+    check_nan_values(kv, q_len, group, 128, block, window)
