@@ -84,6 +84,12 @@ fp4gemv_status fp4gemv_kv_append(const fp4gemv_kv_cache* cache, const void* k, i
  * calls that may run concurrently on the GPU must not share one. */
 size_t fp4gemv_kv_attention_workspace_bytes(int head_dim);
 
+/* The number of the capture that `stream` is being recorded into, 0 where it
+ * is not (no two captures of a process have the same).  A workspace that is
+ * zero-filled during a capture is so in that graph alone: calls captured into
+ * another graph, and calls outside captures, must not use it. */
+uint64_t fp4gemv_stream_capture_id(cudaStream_t stream);
+
 /* Attention of the newest q_len tokens of every sequence over the cache:
  * query i of sequence b stands at position p = seq_lens[b] - q_len + i and
  * sees the tokens max(0, p - window + 1) .. p (window = 0: 0 .. p):

@@ -89,6 +89,16 @@ size_t fp4gemv_kv_attention_workspace_bytes(int head_dim) {
   return attn_counter_bytes(ctas) + static_cast<size_t>(ctas) * 2 * fp4::kAttnMaxRows * (head_dim + 4) * 4;
 }
 
+uint64_t fp4gemv_stream_capture_id(cudaStream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess) {
+    cudaGetLastError();  // (the legacy stream beside a capture: it takes no part)
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype, int heads,
                                     int q_len, const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
                                     int B, float sm_scale, int window, void* out, int64_t ldo, float* lse,

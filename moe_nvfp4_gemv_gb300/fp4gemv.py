@@ -70,6 +70,7 @@ def _load() -> ctypes.CDLL:
         "fp4gemv_w4a4_linear": (i32, [vp, i64, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp, vp, vp, sz, i32, vp]),
         "fp4gemv_kv_append": (i32, [vp, vp, i64, vp, i64, i32, i32, vp, vp, i32, vp, i32, i32, vp]),
         "fp4gemv_kv_attention_workspace_bytes": (sz, [i32]),
+        "fp4gemv_stream_capture_id": (ctypes.c_uint64, [vp]),
         "fp4gemv_kv_attention": (i32, [vp, vp, i64, i32, i32, i32, vp, i32, vp, i32, ctypes.c_float, i32, vp, i64, vp,
                                        vp, sz, i32, vp]),
         "fp4gemv_moe_route": (i32, [vp, i64, i32, i32, i32, i32, i32, vp, i32, i32, i32, i32, ctypes.c_float, vp, vp,

@@ -19,6 +19,7 @@ refused argument.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -39,7 +40,8 @@ class _CacheStruct(ctypes.Structure):
                 ("block_size", ctypes.c_int), ("head_dim", ctypes.c_int), ("format", ctypes.c_int)]
 
 
-_workspaces: dict = {}
+_workspaces: dict = {}  # (device, stream, head_dim): the workspace
+_captured: dict = {}    # the same: (capture, its workspace) of the last capture without one of the above
 
 
 def attention_workspace_bytes(head_dim: int) -> int:
@@ -51,14 +53,32 @@ def attention_workspace(device: torch.device, head_dim: int, stream: int | None 
     """A zero-filled workspace for ``device`` and one CUDA stream (the current
     one when ``stream`` is None), kept for later calls: calls on one stream
     run one after another and may share it, calls on different streams may
-    overlap and each stream has its own."""
+    overlap and each stream has its own.
+
+    While the stream is being captured and has none yet, the capture gets one
+    of its own, which its graph clears whenever it runs.  A graph captured on a
+    stream that has one uses that one: such graphs may not run at the same time
+    as each other or as that stream's calls (give them a ``workspace`` each)."""
     index = device.index if device.index is not None else torch.cuda.current_device()
+    current = _raw_stream(index)
     if stream is None:
-        stream = _raw_stream(index)
+        stream = current
     key = (index, stream, head_dim)
     ws = _workspaces.get(key)
-    if ws is None:
+    if ws is not None:
+        return ws
+    capture = _lib.fp4gemv_stream_capture_id(stream)
+    last = _captured.get(key)
+    if capture and last is not None and last[0] == capture:
+        return last[1]
+    on = contextlib.nullcontext()
+    if stream != current:  # (cleared on the stream that it is for)
+        on = torch.cuda.stream(torch.cuda.ExternalStream(stream, index) if stream else torch.cuda.default_stream(index))
+    with on:
         ws = torch.zeros(attention_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
+    if capture:
+        _captured[key] = (capture, ws)
+    else:
         _workspaces[key] = ws
     return ws
 
@@ -117,7 +137,9 @@ class KvCache8:
         its own position, the last ``window`` of them if that is not 0; one
         that sees none gives zeros.  ``sm_scale`` defaults to 1 /
         sqrt(head_dim); ``lse``: fp32 [B, q_len, heads] to receive the natural
-        log of the softmax's sums.  Returns ``out``."""
+        log of the softmax's sums; ``workspace``: uint8, zero-filled once, of
+        attention_workspace_bytes(head_dim), the stream's own by default
+        (``attention_workspace``; captured calls too).  Returns ``out``."""
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
         if workspace is None:

@@ -117,3 +117,63 @@ def test_attention_nan_values_of_unseen_tokens(kv, q_len, group, dim, block, win
 @pytest.mark.parametrize("window", [0, 1, 20, 130, 300])
 def test_attention_wide_nan_values_of_unseen_tokens(kv, q_len, group, block, window):
     check_nan_values(kv, q_len, group, 128, block, window)
+
+
+@pytest.mark.parametrize("heads", [8, 24])
+def test_first_calls_inside_captures(kv, monkeypatch, heads):
+    """Two graphs captured on a stream that attend has never run on, in memory full of ones: each counts on counters that
+    it cleared itself, so the second may run before the first; and an eager call there does not meet the graphs'."""
+    monkeypatch.setattr(kv, "_workspaces", {})
+    lens = [5000, 700]
+    g = gen(heads)
+    table, pages = make_table(lens, 64, g)
+    c = scaled(random_cache(pages, 1, 64, 128, g, 1.0), "e4m3")
+    cache, tab = on_gpu(kv, c, "e4m3"), table.to(DEV)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    q = torch.randn(2, 1, heads, 128, generator=g).to(torch.bfloat16).to(DEV)
+    want = cache.attend(q, tab, n)
+    side, pool = torch.cuda.Stream(), torch.cuda.graph_pool_handle()
+    side.wait_stream(torch.cuda.current_stream())
+    size = kv.attention_workspace_bytes(128)
+    dirty, graphs, outs = torch.cuda.CUDAGraph(), [], []
+    with torch.cuda.graph(dirty, pool=pool, stream=side):
+        junk = [torch.full((size,), 1, dtype=torch.uint8, device=DEV) for _ in range(3)]
+    dirty.replay()
+    torch.cuda.synchronize()
+    del junk
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        out = torch.full_like(q, 9.0)
+        with torch.cuda.graph(graphs[-1], pool=pool, stream=side):
+            cache.attend(q, tab, n, out=out)
+            cache.attend(q, tab, n, out=out)
+        outs.append(out)
+    for i in (1, 0, 1):
+        outs[i].fill_(9.0)
+        torch.cuda.synchronize()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], want)
+    with torch.cuda.stream(side):
+        eager = cache.attend(q, tab, n)
+    torch.cuda.synchronize()
+    assert torch.equal(eager, want)
+
+
+def test_workspace_of_another_stream_is_cleared_there(kv, monkeypatch):
+    """The workspace of a stream that is not the current one is cleared on that stream, whatever the current one does."""
+    monkeypatch.setattr(kv, "_workspaces", {})
+    side, dev = torch.cuda.Stream(), torch.device(DEV, torch.cuda.current_device())
+    size = kv.attention_workspace_bytes(64)
+    torch.cuda.empty_cache()
+    for s in (side, torch.cuda.current_stream()):  # both streams' next block of that size holds ones
+        with torch.cuda.stream(s):
+            junk = torch.full((size,), 1, dtype=torch.uint8, device=dev)
+        torch.cuda.synchronize()
+        del junk
+    torch.cuda._sleep(400_000_000)  # (some 200 ms of the current stream)
+    ws = kv.attention_workspace(dev, 64, side.cuda_stream)
+    with torch.cuda.stream(side):
+        left = torch.count_nonzero(ws).cpu()
+    assert int(left) == 0
+    assert kv.attention_workspace(dev, 64, side.cuda_stream) is ws
