@@ -14,7 +14,8 @@ and return their output, the MoE pair writes into caller buffers.
 ``moe_route`` and ``token_logprobs`` allocate their outputs unless they are
 given; the 8-bit cache's calls are methods of ``kvcache.KvCache8``.  These
 short calls are marshalled by ``_marshal`` (csrc/marshal.cpp), which reads the
-tensors without ctypes.
+tensors without ctypes; where it can be neither built nor loaded they raise and
+the products' calls work all the same.
 """
 from __future__ import annotations
 
@@ -45,10 +46,18 @@ class Fp4GemvError(RuntimeError):
         super().__init__(f"{what}: {STATUS_NAMES.get(status, status)}")
 
 
+_unbuilt: list = []  # why the extension module could not be built
+
+
 def _load() -> ctypes.CDLL:
     path = _build.LIB
     if not os.path.exists(path) or _build._stale() or _build._marshal_stale():
-        path = _build.build()
+        try:
+            _build.build()
+        except Exception as e:
+            if not os.path.exists(path) or _build._stale():
+                raise
+            _unbuilt.append(e)  # (the extension module alone: the products do without it)
     lib = ctypes.CDLL(path)
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     sigs = {
@@ -93,10 +102,28 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 LIB_PATH = _build.LIB
 
-from . import _marshal  # noqa: E402  (built by _load where it has to be)
 
-_marshal.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
-    _lib.fp4gemv_kv_append, _lib.fp4gemv_kv_attention, _lib.fp4gemv_moe_route, _lib.fp4gemv_token_logprobs)))
+
+class _NoMarshal:
+    """In the extension module's place where it cannot be built or loaded: its calls say why."""
+
+    def __init__(self, why: Exception):
+        self._why = why
+
+    def __getattr__(self, name: str):
+        def call(*args):
+            raise RuntimeError(f"{name} needs the extension module _marshal, which is missing: {self._why}") from self._why
+        return call
+
+
+try:
+    if _unbuilt:
+        raise _unbuilt[0]
+    from . import _marshal  # noqa: E402  (built by _load where it has to be)
+    _marshal.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+        _lib.fp4gemv_kv_append, _lib.fp4gemv_kv_attention, _lib.fp4gemv_moe_route, _lib.fp4gemv_token_logprobs)))
+except Exception as e:
+    _marshal = _NoMarshal(e)
 _nvfp4_gemv = _lib.fp4gemv_nvfp4_gemv
 
 

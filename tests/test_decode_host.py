@@ -17,3 +17,39 @@ def test_logprobs_range_of_temperatures(fp4, inv_t, status):
     """Outside the range: refused for it (1), before the misaligned logits are (3)."""
     assert fp4.lib().fp4gemv_token_logprobs(vp((1 << 20) + 1), 100, 0, 1, 100, None, inv_t, 4, None, None, None, None, None,
                                             1, None) == status
+
+
+RUN = """
+import sys
+sys.path.insert(0, {root!r})
+{setup}
+from moe_nvfp4_gemv_gb300 import fp4gemv, kvcache, linear
+import torch
+assert fp4gemv.scale_bytes(128, 64) == 512 and fp4gemv.launch_count() == 0
+x, i = torch.zeros(2, 8), torch.zeros(2, 2, dtype=torch.int32)
+cache = kvcache.KvCache8.allocate(2, 1, 64, 16, device="cpu")
+for call in (lambda: fp4gemv.moe_route(x, 2, ids=i, weights=x[:, :2]), lambda: fp4gemv.token_logprobs(x, i[:, 0]),
+             lambda: cache.append(x, x, i, i), lambda: cache.attend(x, i, i, out=x, workspace=x)):
+    try:
+        call()
+    except RuntimeError as e:
+        assert "no module" in str(e) and not isinstance(e, fp4gemv.Fp4GemvError), e
+    else:
+        raise AssertionError("a call without its module went through")
+print("fine")
+"""
+
+
+@pytest.mark.parametrize("setup", [
+    "class No:\n    def find_spec(self, name, *a):\n        if name.endswith('_marshal'): raise ImportError('no module')\n"
+    "sys.meta_path.insert(0, No())",
+    "from moe_nvfp4_gemv_gb300 import build\nbuild._marshal_stale = lambda: True\n"
+    "def failing(*a, **k): raise RuntimeError('no module: no compiler')\nbuild.build = failing"])
+def test_the_package_without_its_extension_module(setup):
+    """The products' calls need libfp4gemv.so alone; those of the decode operators say what is missing."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", RUN.format(root=root, setup=setup)], capture_output=True, text=True)
+    assert out.returncode == 0 and "fine" in out.stdout, out.stderr
