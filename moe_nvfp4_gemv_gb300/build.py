@@ -4,12 +4,15 @@ Each translation unit compiles in its own nvcc process (in parallel); the
 objects are linked into ``moe_nvfp4_gemv_gb300/libfp4gemv.so`` against the
 shared CUDA runtime.  csrc/marshal.cpp becomes ``_marshal.so`` beside it, an
 extension module on this interpreter's torch (g++, at the same time).  Rebuilds
-only when a source or header is newer than what it makes.  Usage: ``python -m moe_nvfp4_gemv_gb300.build [--force]``.
+only when a source or header is newer than what it makes, and the extension
+module also for another interpreter or torch than it was built for.  Usage:
+``python -m moe_nvfp4_gemv_gb300.build [--force]``.
 """
 from __future__ import annotations
 
 import glob
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -22,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp4gemv.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_FOR = os.path.join(BUILD_DIR, "marshal_for.txt")  # what it was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -55,12 +59,21 @@ def _torch_dir() -> str:
     return os.path.dirname(os.path.abspath(torch.__file__))
 
 
+def _marshal_for() -> str:
+    """What the extension module depends on besides its sources: its binary interfaces, and where torch's are."""
+    import torch
+    return "\n".join((torch.__version__, _torch_dir(), str(torch.compiled_with_cxx11_abi()), sys.version,
+                      platform.machine()))
+
+
 def _marshal_stale() -> bool:
-    if not os.path.exists(MARSHAL):
+    if not os.path.exists(MARSHAL) or not os.path.exists(MARSHAL_FOR):
         return True
+    with open(MARSHAL_FOR) as f:
+        if f.read() != _marshal_for():
+            return True
     t = os.path.getmtime(MARSHAL)
-    deps = [os.path.join(CSRC, "marshal.cpp"), os.path.abspath(__file__), os.path.join(_torch_dir(), "version.py")] + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
+    deps = [os.path.join(CSRC, "marshal.cpp"), os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -84,7 +97,12 @@ def _finish_marshal(tmp: str, proc: subprocess.Popen) -> None:
     if proc.returncode != 0:
         sys.stderr.write(out.decode(errors="replace"))
         raise RuntimeError("the C++ compiler failed for marshal.cpp")
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    if os.path.exists(MARSHAL_FOR):
+        os.remove(MARSHAL_FOR)
     os.replace(tmp, MARSHAL)
+    with open(MARSHAL_FOR, "w") as f:
+        f.write(_marshal_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -53,3 +53,15 @@ def test_the_package_without_its_extension_module(setup):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     out = subprocess.run([sys.executable, "-c", RUN.format(root=root, setup=setup)], capture_output=True, text=True)
     assert out.returncode == 0 and "fine" in out.stdout, out.stderr
+
+
+@pytest.mark.parametrize("name,other", [("__version__", "2.0.0+other"), ("__file__", "/elsewhere/torch/__init__.py")])
+def test_the_extension_module_is_rebuilt_for_another_torch(monkeypatch, name, other):
+    """Whatever the files' times are."""
+    import torch
+
+    from moe_nvfp4_gemv_gb300 import build
+    build.build()
+    assert not build._marshal_stale()
+    monkeypatch.setattr(torch, name, other)
+    assert build._marshal_stale()
