@@ -84,7 +84,15 @@ def attention_workspace(device: torch.device, head_dim: int, stream: int | None 
 
 
 class KvCache8:
-    """The cache's tensors and their calls.  ``fmt``: "e4m3" or "int8"."""
+    """The cache's tensors and their calls.  ``fmt``: "e4m3" or "int8".
+
+    The calls use the tensors' memory as it was given: write into them in
+    place; other tensors make another cache."""
+
+    k_codes = property(lambda self: self._tensors[0])
+    v_codes = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                  fmt: str = "e4m3"):
@@ -98,7 +106,7 @@ class KvCache8:
                                       ("v_scale", v_scale, _F32, k_codes.shape[:2])):
             if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != k_codes.device:
                 raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the codes' device")
-        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self._tensors = k_codes, v_codes, k_scale, v_scale
         self.fmt = fmt
         self.device = k_codes.device
         self._index = k_codes.get_device()

@@ -65,3 +65,20 @@ def test_the_extension_module_is_rebuilt_for_another_torch(monkeypatch, name, ot
     assert not build._marshal_stale()
     monkeypatch.setattr(torch, name, other)
     assert build._marshal_stale()
+
+
+def test_a_cache_keeps_its_tensors():
+    """The calls use the memory that the cache was made with: its tensors cannot be exchanged behind their back."""
+    import torch
+
+    from moe_nvfp4_gemv_gb300.kvcache import KvCache8
+    cache = KvCache8.allocate(2, 1, 64, 16, device="cpu")
+    for name in ("k_codes", "v_codes", "k_scale", "v_scale"):
+        was = getattr(cache, name)
+        with pytest.raises(AttributeError):
+            setattr(cache, name, torch.ones_like(was))
+        was.fill_(3)  # (in place: the same memory)
+        assert getattr(cache, name) is was
+    s = cache._struct
+    assert [s.k_codes, s.v_codes, s.k_scale, s.v_scale] == [t.data_ptr() for t in (cache.k_codes, cache.v_codes,
+                                                                                 cache.k_scale, cache.v_scale)]
