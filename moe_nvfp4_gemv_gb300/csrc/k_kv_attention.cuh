@@ -177,6 +177,12 @@ __device__ __forceinline__ uint32_t codes2_hi(uint32_t w) {
   return h;
 }
 
+// Four E4M3 codes: the high bits of those that are NaN; and these as bits 0 to 3.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t nan_lanes(uint32_t nan) {
+  return (nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u);
+}
+
 // An item and a place in it.
 struct AttnPlace {
   int b, head, tile;  // sequence, KV head, row tile
@@ -915,17 +921,17 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int k = 0; k < L::kVWords; ++k) found |= (w[c][k] & 0x7F7F7F7Fu) + 0x01010101u;
-      if ((found & 0x80808080u) == 0u) return;
+        for (int k = 0; k < L::kVWords; ++k) found |= nan_codes(w[c][k]);
+      if (found == 0u) return;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int k = 0; k < L::kVWords; ++k) {
-          const uint32_t nan = ((w[c][k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // the NaN codes' high bits
+          const uint32_t nan = nan_codes(w[c][k]);
           if (nan == 0u) continue;
           w[c][k] &= ~((nan >> 7) * 0xFFu);
           const int at = tok + 2 * t + (c & 1) + (c >> 1) * 8, d = L::v_dim(blk, k, g);
-          const uint32_t dims = ((nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u)) << (d & 31);
+          const uint32_t dims = nan_lanes(nan) << (d & 31);
 #pragma unroll 1
           for (int r = 0; r < min(C::kRows, rows - row0); ++r) {
             const int see_to = n - p.q_len + (((row0 + r) * p.group_magic) >> 16) + 1;

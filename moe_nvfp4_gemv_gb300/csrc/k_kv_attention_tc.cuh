@@ -529,38 +529,10 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f)), inv_vs = attn_ex2(-lv);
         const bool live = tok < tok_end && tok >= tok_low;
         const bool masked = tile0 + C::kTile > min(tokens_all, tok_end) || tile0 < tokens_low;
-        const uint32_t v_row = sm + C::kVOff + stage * C::kTileBytes + who * 128;
         if (!live) {  // whatever lies there counts nothing
+          const uint32_t v_row = sm + C::kVOff + stage * C::kTileBytes + who * 128;
 #pragma unroll
           for (int k = 0; k < 8; ++k) sts128(v_row + k * 16, make_uint4(0, 0, 0, 0));
-        } else if (masked) {
-          // A tile that some row sees only in part: a weight of 0 does not silence a NaN code, so NaNs give way to zeros, and
-          // the rows that do see the token are noted for the segment's end.  (Chunk k of the row lies at k ^ its row mod 8.)
-#pragma unroll 1
-          for (int k = 0; k < 8; ++k) {
-            const uint4 chunk = lds128(v_row + k * 16);
-            uint32_t w[4] = {chunk.x, chunk.y, chunk.z, chunk.w};
-            uint32_t found = 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) found |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;
-            if ((found & 0x80808080u) == 0u) continue;
-            uint32_t dims = 0u;  // of the chunk's 16
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t nan = ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // the NaN codes' high bits
-              w[i] &= ~((nan >> 7) * 0xFFu);
-              dims |= ((nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u)) << (4 * i);
-            }
-            sts128(v_row + k * 16, make_uint4(w[0], w[1], w[2], w[3]));
-            const int chunk_no = k ^ (who & 7);
-            for (int r = 0; r < used; ++r) {
-              const int see_to = n - p.q_len + (((row0 + r) * p.group_magic) >> 16) + 1;
-              if (tok < see_to && (p.window == 0 || tok >= see_to - p.window)) {
-                atomicOr(&nan_dims[r][chunk_no >> 1], dims << (16 * (chunk_no & 1)));
-                nan_any = 1;
-              }
-            }
-          }
         }
         // the weights' exponents against the running maxima
         float top = 0.0f;
@@ -592,6 +564,37 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
               const int row = min(row0 + r, rows - 1);
               const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
               if (!live || tok >= see_to || (p.window > 0 && tok < see_to - p.window)) v[r] = -__builtin_huge_valf();
+            }
+            // A tile that some row sees only in part: a weight of 0 does not silence a NaN code, so NaNs give way to zeros, and
+            // the rows that do see the token are noted for the segment's end.  (Chunk k of the row lies at k ^ its row mod 8.)
+            const uint32_t v_row = sm + C::kVOff + stage * C::kTileBytes + who * 128;
+            uint32_t found = 0u;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint4 u = lds128(v_row + k * 16);
+              found |= nan_codes(u.x) | nan_codes(u.y) | nan_codes(u.z) | nan_codes(u.w);
+            }
+#pragma unroll 1
+            for (int k = 0; found != 0u && k < 8; ++k) {
+              const uint4 chunk = lds128(v_row + k * 16);
+              uint32_t u[4] = {chunk.x, chunk.y, chunk.z, chunk.w};
+              uint32_t dims = 0u;  // of the chunk's 16
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t nan = nan_codes(u[i]);
+                u[i] &= ~((nan >> 7) * 0xFFu);
+                dims |= nan_lanes(nan) << (4 * i);
+              }
+              if (dims == 0u) continue;
+              sts128(v_row + k * 16, make_uint4(u[0], u[1], u[2], u[3]));
+              const int chunk_no = k ^ (who & 7);
+              for (int r = 0; r < used; ++r) {
+                const int see_to = n - p.q_len + (((row0 + r) * p.group_magic) >> 16) + 1;
+                if (tok < see_to && (p.window == 0 || tok >= see_to - p.window)) {
+                  atomicOr(&nan_dims[r][chunk_no >> 1], dims << (16 * (chunk_no & 1)));
+                  nan_any = 1;
+                }
+              }
             }
           }
           float w[32];
