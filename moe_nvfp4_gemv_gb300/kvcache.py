@@ -89,10 +89,10 @@ class KvCache8:
     The calls use the tensors' memory as it was given: write into them in
     place; other tensors make another cache."""
 
-    k_codes = property(lambda self: self._tensors[0])
-    v_codes = property(lambda self: self._tensors[1])
-    k_scale = property(lambda self: self._tensors[2])
-    v_scale = property(lambda self: self._tensors[3])
+    def __setattr__(self, name, value):
+        if name in ("k_codes", "v_codes", "k_scale", "v_scale") and name in self.__dict__:
+            raise AttributeError(f"{name} is the memory that the calls use: write into it, or make another cache")
+        super().__setattr__(name, value)
 
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                  fmt: str = "e4m3"):
@@ -106,7 +106,7 @@ class KvCache8:
                                       ("v_scale", v_scale, _F32, k_codes.shape[:2])):
             if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != k_codes.device:
                 raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the codes' device")
-        self._tensors = k_codes, v_codes, k_scale, v_scale
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.fmt = fmt
         self.device = k_codes.device
         self._index = k_codes.get_device()
