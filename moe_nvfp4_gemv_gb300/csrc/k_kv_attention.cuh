@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
             for (int k = 0; k < L::kVWords; ++k) w[c][k] = 0u;
           }
       }
-      if (!kInt8 && masked) quiet(tok, blk, w);
+      if (!kInt8 && masked && (p.q_len > 1 || p.window > 0)) quiet(tok, blk, w);  // (else: no token is seen in part)
     };
     // this warp's strips of the segment: begin + warp + k kWarps
     int tok = tok0 + (((begin + warp - at) & (C::kWarps - 1)) << 4);

@@ -191,6 +191,45 @@ __device__ __forceinline__ float warp_columns(float (&v)[32], Op op) {
   return v[0];
 }
 
+// NaN codes of tokens that some of an item's rows see and some do not (`part` of the warp's 32 tokens, their V rows from
+// shared address v_rows on; the first of them is seen by queries from `since` on): a weight of 0 does not silence them, so
+// they give way to zeros, and the rows that do see their token are noted in nan_dims for the segment's end.  The warp takes
+// four tokens at a time, a lane for each 16 bytes (chunk k of a row lies at k ^ its number mod 8).  A function of its own,
+// since the masks' path is short of instruction cache: 128 sequences of 500 tokens, 4 new ones, 64 heads on 8, 67.4 us,
+// 68.2 where it stands.
+__device__ __noinline__ void attn_tc_quiet(uint32_t part, uint32_t v_rows, int since, int window, int q_len, int group,
+                                           int row0, int used, uint32_t (*nan_dims)[AttnTc::kDim / 32], int* nan_any) {
+  const int lane = threadIdx.x & 31, k = lane & 7;
+  while (part != 0u) {
+    uint32_t mine = part;
+    for (int i = lane >> 3; i > 0; --i) mine &= mine - 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part &= part - 1;
+    const int token = __ffs(mine) - 1;
+    const uint32_t at = v_rows + token * 128 + ((k ^ (token & 7)) << 4);
+    uint32_t u[4] = {0u, 0u, 0u, 0u};
+    if (mine != 0u) {
+      const uint4 chunk = lds128(at);
+      u[0] = chunk.x, u[1] = chunk.y, u[2] = chunk.z, u[3] = chunk.w;
+    }
+    if ((nan_codes(u[0]) | nan_codes(u[1]) | nan_codes(u[2]) | nan_codes(u[3])) == 0u) continue;
+    uint32_t dims = 0u;  // of the chunk's 16
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t nan = nan_codes(u[i]);
+      u[i] &= ~((nan >> 7) * 0xFFu);
+      dims |= nan_lanes(nan) << (4 * i);
+    }
+    sts128(at, make_uint4(u[0], u[1], u[2], u[3]));
+    const int first = max(since + token, 0), last = window > 0 ? min(since + token + window, q_len) : q_len;  // its queries
+    for (int r = max(first * group - row0, 0); r < min(last * group - row0, used); ++r) {
+      atomicOr(&nan_dims[r][k >> 1], dims << (16 * (k & 1)));
+      *nan_any = 1;
+    }
+  }
+  __syncwarp();
+}
+
 __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(const __grid_constant__ KvAttnTcParams p) {
   using C = AttnTc;
   extern __shared__ __align__(128) uint8_t smem_tc[];
@@ -532,7 +571,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         if (!live) {  // whatever lies there counts nothing
           const uint32_t v_row = sm + C::kVOff + stage * C::kTileBytes + who * 128;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sts128(v_row + k * 16, make_uint4(0, 0, 0, 0));
+          for (int k = 0; k < 8; ++k) sts128(v_row + ((k ^ (who & 7)) << 4), make_uint4(0, 0, 0, 0));
         }
         // the weights' exponents against the running maxima
         float top = 0.0f;
@@ -559,43 +598,19 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
             v[2 * i + 1] = a.y - row_base[g][2 * i + 1];
           }
           if (masked) {
+            // The rows [from, to) see the token: those of the queries from `since` on, and with a window of fewer than all.
+            // (Rows that are no rows go with the last one, so that their maxima are not the floor.)
+            const int since = tok - (n - p.q_len);
+            const int from = max(since, 0) * p.group - row0;
+            const int to = !live ? from
+                           : p.window > 0 && since + p.window < p.q_len ? max(since + p.window, 0) * p.group - row0 : C::kRows;
 #pragma unroll
-            for (int r = 0; r < C::kRows; ++r) {
-              const int row = min(row0 + r, rows - 1);
-              const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
-              if (!live || tok >= see_to || (p.window > 0 && tok < see_to - p.window)) v[r] = -__builtin_huge_valf();
-            }
-            // A tile that some row sees only in part: a weight of 0 does not silence a NaN code, so NaNs give way to zeros, and
-            // the rows that do see the token are noted for the segment's end.  (Chunk k of the row lies at k ^ its row mod 8.)
-            const uint32_t v_row = sm + C::kVOff + stage * C::kTileBytes + who * 128;
-            uint32_t found = 0u;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint4 u = lds128(v_row + k * 16);
-              found |= nan_codes(u.x) | nan_codes(u.y) | nan_codes(u.z) | nan_codes(u.w);
-            }
-#pragma unroll 1
-            for (int k = 0; found != 0u && k < 8; ++k) {
-              const uint4 chunk = lds128(v_row + k * 16);
-              uint32_t u[4] = {chunk.x, chunk.y, chunk.z, chunk.w};
-              uint32_t dims = 0u;  // of the chunk's 16
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t nan = nan_codes(u[i]);
-                u[i] &= ~((nan >> 7) * 0xFFu);
-                dims |= nan_lanes(nan) << (4 * i);
-              }
-              if (dims == 0u) continue;
-              sts128(v_row + k * 16, make_uint4(u[0], u[1], u[2], u[3]));
-              const int chunk_no = k ^ (who & 7);
-              for (int r = 0; r < used; ++r) {
-                const int see_to = n - p.q_len + (((row0 + r) * p.group_magic) >> 16) + 1;
-                if (tok < see_to && (p.window == 0 || tok >= see_to - p.window)) {
-                  atomicOr(&nan_dims[r][chunk_no >> 1], dims << (16 * (chunk_no & 1)));
-                  nan_any = 1;
-                }
-              }
-            }
+            for (int r = 0; r < C::kRows; ++r)
+              if (r < from || r >= to) v[r] = -__builtin_huge_valf();
+            const uint32_t part = __ballot_sync(0xFFFFFFFFu, live && (tok >= tokens_all || tok < tokens_low));
+            if (part != 0u)
+              attn_tc_quiet(part, sm + C::kVOff + stage * C::kTileBytes + (who - lane) * 128, tok - lane - (n - p.q_len),
+                            p.window, p.q_len, p.group, row0, used, nan_dims, &nan_any);
           }
           float w[32];
 #pragma unroll
@@ -695,7 +710,15 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         for (int r = 0; r < 32; ++r) mine[r * C::kDim + who] = any ? fmaf(low[r], 0.00390625f, o[r]) * C::kWUnscale : 0.0f;
       }
       const bool failed = named_any(3, C::kWeighers, !ok);  // (some wait ran out: NaN)
-      const bool nans = nan_any != 0;                        // (read between two barriers: all threads alike)
+      if (nan_any != 0) {  // (written before that barrier, cleared behind the next: all threads alike)
+        float* const sums = reinterpret_cast<float*>(smem + C::kWOff);
+#pragma unroll 1
+        for (int i = tid; i < C::kRows * C::kDim; i += C::kWeighers)
+          if (nan_dims[i / C::kDim][i % C::kDim / 32] >> (i & 31) & 1u) sums[i] = __int_as_float(0x7FC00000);
+        named_sync<3>(C::kWeighers);
+        if (tid < C::kRows * (C::kDim / 32)) (&nan_dims[0][0])[tid] = 0u;
+        if (tid == 0) nan_any = 0;
+      }
       const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
       const AttnItemEnd<C::kDim, C::kWeighers> item_end = {p, cur, row0, used};
       float* const part = item_end.part_of(blockIdx.x, starts ? 1 : 0);
@@ -710,16 +733,8 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         const float* a = reinterpret_cast<const float*>(smem + C::kWOff) + r * C::kDim + d;
         const float4 u = *reinterpret_cast<const float4*>(a);
         const float4 w = *reinterpret_cast<const float4*>(a + C::kTileBytes / 4);
-        float4 v = make_float4(u.x * f0 + w.x * f1, u.y * f0 + w.y * f1, u.z * f0 + w.z * f1, u.w * f0 + w.w * f1);
+        const float4 v = make_float4(u.x * f0 + w.x * f1, u.y * f0 + w.y * f1, u.z * f0 + w.z * f1, u.w * f0 + w.w * f1);
         const float l = failed ? __int_as_float(0x7FC00000) : l0 * f0 + l1 * f1;
-        if (nans) {
-          const uint32_t nan = nan_dims[r][d >> 5] >> (d & 31);
-          const float none = __int_as_float(0x7FC00000);
-          if (nan & 1u) v.x = none;
-          if (nan & 2u) v.y = none;
-          if (nan & 4u) v.z = none;
-          if (nan & 8u) v.w = none;
-        }
         if (whole) {
           item_end.store(r, d, v, top, l);
         } else {
@@ -730,11 +745,6 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
       }
       if (!whole) item_end.share(plan_words, line_before, ml, &last_flag, [] { named_sync<3>(C::kWeighers); });
       named_sync<3>(C::kWeighers);  // (before the tables and tiles are written again)
-      if (nans) {
-        if (tid < C::kRows * (C::kDim / 32)) (&nan_dims[0][0])[tid] = 0u;
-        if (tid == 0) nan_any = 0;
-        named_sync<3>(C::kWeighers);
-      }
       first_tile += tiles;
       at = seg_end;
       if (at < end) cur = attn_next(p, cur, strips_before, tokens);
