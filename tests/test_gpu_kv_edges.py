@@ -177,3 +177,36 @@ def test_workspace_of_another_stream_is_cleared_there(kv, monkeypatch):
         left = ws.cpu()  # (a copy: a kernel's first launch may wait for all streams)
     assert not left.any()
     assert kv.attention_workspace(dev, 64, side.cuda_stream) is ws
+
+
+@pytest.mark.parametrize("heads,dim,fmt", [(8, 128, "e4m3"), (24, 128, "e4m3"), (8, 64, "int8"), (4, 256, "e4m3")])
+def test_pages_past_four_gibibytes(kv, heads, dim, fmt):
+    """Pages at the end of caches whose codes take more than 2^32 bytes: append and attention as on the same pages of a
+    small cache."""
+    block, n = 128, 700
+    g = gen(dim + heads)
+    pages = (1 << 32) // (block * dim) + 9
+    big = kv.KvCache8.allocate(pages, 1, dim, block, fmt)
+    small = kv.KvCache8.allocate(9, 1, dim, block, fmt)
+    x = torch.randn(n, 2, 1, dim, generator=g).to(torch.bfloat16).to(DEV)
+    q = torch.randn(1, 3, heads, dim, generator=g).to(torch.bfloat16).to(DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    far = torch.tensor([[8, 3, 5, 0, 7, 1]], dtype=torch.int32, device=DEV)
+    outs = []
+    for cache, table in ((big, far + (pages - 9)), (small, far)):
+        cache.append(x[:, 0], x[:, 1], table, lens)
+        outs.append(cache.attend(q, table, lens))
+    assert torch.equal(big.k_codes[-9:], small.k_codes) and torch.equal(big.v_scale[-9:], small.v_scale)
+    assert torch.equal(outs[0], outs[1]) and outs[0].abs().max() > 0
+    assert int(big.k_codes[:-9].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("heads,q_len,dim,fmt", [(8, 1, 128, "e4m3"), (32, 1, 128, "e4m3"), (8, 2, 64, "int8")])
+def test_attention_of_a_very_long_sequence(kv, heads, q_len, dim, fmt):
+    """500001 tokens on one KV head: every CTA has a part, joined in two levels."""
+    lens = [500001, 3]
+    g = gen(dim + heads)
+    table, pages = make_table(lens, 128, g)
+    c = scaled(random_cache(pages, 1, 128, dim, g, 1.0), fmt)
+    q = torch.randn(2, q_len, heads, dim, generator=g).to(torch.float16).to(DEV)
+    check_attention(kv, q, c, table, lens, fmt, "f16")
