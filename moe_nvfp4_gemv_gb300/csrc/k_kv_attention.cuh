@@ -649,6 +649,39 @@ struct AttnLayout {
   }
 };
 
+// NaN codes of tokens that some of an item's rows do not see, in a strip of V (`count` tokens, the first of them seen by
+// queries from `since` on): a weight of 0 does not silence them, so they give way to zeros, and the rows that do see their
+// token are noted in nan_dims for the segment's end.  By a warp, a lane for each 16 bytes.
+template <int kDim>
+__device__ __noinline__ void attn_quiet(uint32_t strip, int count, int since, int window, int q_len, int group, int row0,
+                                        int used, uint32_t (*nan_dims)[kDim / 32], int* nan_any) {
+  using L = AttnLayout<kDim>;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int i = lane; i < count * (kDim / 16); i += 32) {
+    const int token = i / (kDim / 16), k = i - token * (kDim / 16), from = since + token;
+    if (from <= 0 && (window == 0 || from + window >= q_len)) continue;  // (all rows see it)
+    const uint32_t at = strip + L::chunk(token, k);
+    const uint4 chunk = lds128(at);
+    uint32_t u[4] = {chunk.x, chunk.y, chunk.z, chunk.w};
+    if ((nan_codes(u[0]) | nan_codes(u[1]) | nan_codes(u[2]) | nan_codes(u[3])) == 0u) continue;
+    uint32_t dims = 0u;  // of the chunk's 16
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t nan = nan_codes(u[j]);
+      u[j] &= ~((nan >> 7) * 0xFFu);
+      dims |= nan_lanes(nan) << (4 * j);
+    }
+    sts128(at, make_uint4(u[0], u[1], u[2], u[3]));
+    const int first = max(from, 0), last = window > 0 ? min(from + window, q_len) : q_len;  // its queries
+    for (int r = max(first * group - row0, 0); r < min(last * group - row0, used); ++r) {
+      atomicOr(&nan_dims[r][k >> 1], dims << (16 * (k & 1)));
+      *nan_any = 1;
+    }
+  }
+  __syncwarp();
+}
+
 // kN: tiles of 8 query rows that a warp serves; kRes: CTAs per SM (registers, shared memory).
 template <int kDim, int kN, int kRes>
 struct AttnCfg {
@@ -914,36 +947,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
         for (int nt = 0; nt < kN; ++nt) mma_f16(acc[nt][(blk * L::kVWords + k) * 2 + j], a, pb[nt][0], pb[nt][1]);
       }
     };
-    // A strip that some row sees only in part: a weight of 0 does not silence a NaN code (E4M3; INT8 has none), so NaNs
-    // give way to zeros, and the rows that do see the token are noted for the segment's end.
-    auto quiet = [&](int tok, int blk, uint32_t (&w)[4][L::kVWords]) {
-      uint32_t found = 0u;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int k = 0; k < L::kVWords; ++k) found |= nan_codes(w[c][k]);
-      if (found == 0u) return;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int k = 0; k < L::kVWords; ++k) {
-          const uint32_t nan = nan_codes(w[c][k]);
-          if (nan == 0u) continue;
-          w[c][k] &= ~((nan >> 7) * 0xFFu);
-          const int at = tok + 2 * t + (c & 1) + (c >> 1) * 8, d = L::v_dim(blk, k, g);
-          const uint32_t dims = nan_lanes(nan) << (d & 31);
-#pragma unroll 1
-          for (int r = 0; r < min(C::kRows, rows - row0); ++r) {
-            const int see_to = n - p.q_len + (((row0 + r) * p.group_magic) >> 16) + 1;
-            if (at < see_to && (p.window == 0 || at >= see_to - p.window)) {
-              atomicOr(&nan_dims[r][d >> 5], dims);
-              nan_any = 1;
-            }
-          }
-        }
-    };
-    auto v_load = [&](uint32_t vb, int blk, int tok, bool masked, uint32_t (&w)[4][L::kVWords]) {
-      const int left = n - tok;
+    auto v_load = [&](uint32_t vb, int blk, int left, uint32_t (&w)[4][L::kVWords]) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) L::v_words(vb, v_place, c, blk, w[c]);
       if (left < 16) {  // past the end: whatever lies there counts nothing
@@ -954,7 +958,6 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
             for (int k = 0; k < L::kVWords; ++k) w[c][k] = 0u;
           }
       }
-      if (!kInt8 && masked && (p.q_len > 1 || p.window > 0)) quiet(tok, blk, w);  // (else: no token is seen in part)
     };
     // this warp's strips of the segment: begin + warp + k kWarps
     int tok = tok0 + (((begin + warp - at) & (C::kWarps - 1)) << 4);
@@ -974,112 +977,129 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
         for (int s = 0; s < L::kWords; s += 2) score(w, blk, s, sc);
       }
     }
-    for (; tok < tok_end; tok += C::kWarps * 16) {
-      const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + L::kStripBytes;
-      if (!C::kAhead) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-        __syncwarp();  // the strip is there, and every lane is past the stage read last
-        issue(before(stage));
-#pragma unroll
-        for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
-#pragma unroll
-        for (int blk = 0; blk < L::kBlocks; ++blk) {
-          uint32_t w[2][L::kWords];
-          k_load(kb, blk, w);
-#pragma unroll
-          for (int s = 0; s < L::kWords; s += 2) score(w, blk, s, sc);
+    // Strips that some row sees in part are gone through one by one, quieted first: outside the loop over the others, where
+    // even a call costs registers.  32 rows, heads of 64, 32 sequences of 16384: 169 us, with the call inside 182.
+    const bool parts = !kInt8 && (p.q_len > 1 || p.window > 0);
+    for (int stop = tok_end; tok < tok_end;) {
+      if (parts) {
+        stop = min(tok_end, tokens_all - 15);
+        if (tok < tokens_low || tok >= stop) {
+          if (!C::kAhead) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+            __syncwarp();
+          }
+          attn_quiet<kDim>(ring + stage * C::kStageBytes + L::kStripBytes, min(16, n - tok), tok - (n - p.q_len), p.window,
+                           p.q_len, p.group, row0, min(C::kRows, rows - row0), nan_dims, &nan_any);
+          stop = tok + 1;
         }
       }
-      float ks, vs;
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(kb + 2 * L::kStripBytes));
-      const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
-      const float inv_vs = attn_ex2(-lv) * kAttnUnlift;  // (sums stay those of weights up to 1)
-      const bool masked = tok + 16 > tokens_all || tok < tokens_low;
-      // Exponents against the running maxima, in the scores' place; against 0 while the warp has seen no strip that
-      // every row sees some of (`fresh`: a row's first maximum is only known then).  Where they are masked, too high
-      // or fresh, the maxima are taken and the exponents made again.
-      float high = -1.0f;
+      for (; tok < stop; tok += C::kWarps * 16) {
+        const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + L::kStripBytes;
+        if (!C::kAhead) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+          __syncwarp();  // the strip is there, and every lane is past the stage read last
+          issue(before(stage));
 #pragma unroll
-      for (int nt = 0; nt < kN; ++nt)
+          for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float f = (C::kQInRegs ? rs[h] : row_scale[nt * 8 + 2 * t + h]) * ks;
-          const float base = fresh ? lv : lv - m[nt][h];
-          sc[nt][h] = fmaf(sc[nt][h], f, base);
-          sc[nt][2 + h] = fmaf(sc[nt][2 + h], f, base);
-          high = fmaxf(high, fmaxf(sc[nt][h], sc[nt][2 + h]));
+          for (int blk = 0; blk < L::kBlocks; ++blk) {
+            uint32_t w[2][L::kWords];
+            k_load(kb, blk, w);
+#pragma unroll
+            for (int s = 0; s < L::kWords; s += 2) score(w, blk, s, sc);
+          }
         }
-      if (masked || fresh || __any_sync(0xFFFFFFFFu, high > kAttnLift + kAttnSlack)) {
+        float ks, vs;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(kb + 2 * L::kStripBytes));
+        const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
+        const float inv_vs = attn_ex2(-lv) * kAttnUnlift;  // (sums stay those of weights up to 1)
+        const bool masked = tok + 16 > tokens_all || tok < tokens_low;
+        // Exponents against the running maxima, in the scores' place; against 0 while the warp has seen no strip that
+        // every row sees some of (`fresh`: a row's first maximum is only known then).  Where they are masked, too high
+        // or fresh, the maxima are taken and the exponents made again.
+        float high = -1.0f;
 #pragma unroll
         for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float base = fresh ? 0.0f : m[nt][h];
-            float r0 = sc[nt][h] + base, r1 = sc[nt][2 + h] + base;
-            if (masked) {
-              const int row = min(row0 + nt * 8 + 2 * t + h, rows - 1);
-              const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
-              const int see_from = p.window > 0 ? see_to - p.window : 0;
-              if (tok + g >= see_to || tok + g < see_from) r0 = -__builtin_huge_valf();
-              if (tok + 8 + g >= see_to || tok + 8 + g < see_from) r1 = -__builtin_huge_valf();
-            }
-            float top = fmaxf(r0, r1);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const float mn = fmaxf(m[nt][h], top - kAttnLift);
-            const float fall = attn_ex2(m[nt][h] - mn);
-            m[nt][h] = mn;
-            sum[nt][h] *= fall;
-#pragma unroll
-            for (int j = 0; j < L::kTiles; ++j) {
-              acc[nt][j][h] *= fall;
-              acc[nt][j][2 + h] *= fall;
-            }
-            sc[nt][h] = r0 - mn;
-            sc[nt][2 + h] = r1 - mn;
+            const float f = (C::kQInRegs ? rs[h] : row_scale[nt * 8 + 2 * t + h]) * ks;
+            const float base = fresh ? lv : lv - m[nt][h];
+            sc[nt][h] = fmaf(sc[nt][h], f, base);
+            sc[nt][2 + h] = fmaf(sc[nt][2 + h], f, base);
+            high = fmaxf(high, fmaxf(sc[nt][h], sc[nt][2 + h]));
           }
-        fresh = fresh && tok < tokens_low;
-      }
-      uint32_t pb[kN][2];
+        if (masked || fresh || __any_sync(0xFFFFFFFFu, high > kAttnLift + kAttnSlack)) {
 #pragma unroll
-      for (int nt = 0; nt < kN; ++nt) {
+          for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] = attn_ex2(sc[nt][e]);
-        sum[nt][0] = fmaf(sc[nt][0] + sc[nt][2], inv_vs, sum[nt][0]);
-        sum[nt][1] = fmaf(sc[nt][1] + sc[nt][3], inv_vs, sum[nt][1]);
-        pb[nt][0] = transpose8x8(pack_f16(sc[nt][0], sc[nt][1]));
-        pb[nt][1] = transpose8x8(pack_f16(sc[nt][2], sc[nt][3]));
-      }
-      if constexpr (C::kAhead) {
-        // the next strip's scores along with this one's sums (past the last strip: of no use, and none is made)
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 3) : "memory");
-        __syncwarp();  // the next strip is there, and every lane is past the stage read last
-        issue(before(stage));
-        const uint32_t next_kb = ring + after(stage) * C::kStageBytes;
+            for (int h = 0; h < 2; ++h) {
+              const float base = fresh ? 0.0f : m[nt][h];
+              float r0 = sc[nt][h] + base, r1 = sc[nt][2 + h] + base;
+              if (masked) {
+                const int row = min(row0 + nt * 8 + 2 * t + h, rows - 1);
+                const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
+                const int see_from = p.window > 0 ? see_to - p.window : 0;
+                if (tok + g >= see_to || tok + g < see_from) r0 = -__builtin_huge_valf();
+                if (tok + 8 + g >= see_to || tok + 8 + g < see_from) r1 = -__builtin_huge_valf();
+              }
+              float top = fmaxf(r0, r1);
 #pragma unroll
-        for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
-        static_assert(L::kWords == 2 * L::kVWords, "a V word for every two K words");
+              for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+              const float mn = fmaxf(m[nt][h], top - kAttnLift);
+              const float fall = attn_ex2(m[nt][h] - mn);
+              m[nt][h] = mn;
+              sum[nt][h] *= fall;
 #pragma unroll
-        for (int blk = 0; blk < L::kBlocks; ++blk) {
-          uint32_t wk[2][L::kWords], wv[4][L::kVWords];
-          k_load(next_kb, blk, wk);
-          v_load(vb, blk, tok, masked, wv);
+              for (int j = 0; j < L::kTiles; ++j) {
+                acc[nt][j][h] *= fall;
+                acc[nt][j][2 + h] *= fall;
+              }
+              sc[nt][h] = r0 - mn;
+              sc[nt][2 + h] = r1 - mn;
+            }
+          fresh = fresh && tok < tokens_low;
+        }
+        uint32_t pb[kN][2];
 #pragma unroll
-          for (int k = 0; k < L::kVWords; ++k) {
-            score(wk, blk, 2 * k, sc);
-            weigh(wv, blk, k, pb);
+        for (int nt = 0; nt < kN; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[nt][e] = attn_ex2(sc[nt][e]);
+          sum[nt][0] = fmaf(sc[nt][0] + sc[nt][2], inv_vs, sum[nt][0]);
+          sum[nt][1] = fmaf(sc[nt][1] + sc[nt][3], inv_vs, sum[nt][1]);
+          pb[nt][0] = transpose8x8(pack_f16(sc[nt][0], sc[nt][1]));
+          pb[nt][1] = transpose8x8(pack_f16(sc[nt][2], sc[nt][3]));
+        }
+        if constexpr (C::kAhead) {
+          // the next strip's scores along with this one's sums (past the last strip: of no use, and none is made)
+          asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 3) : "memory");
+          __syncwarp();  // the next strip is there, and every lane is past the stage read last
+          issue(before(stage));
+          const uint32_t next_kb = ring + after(stage) * C::kStageBytes;
+#pragma unroll
+          for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+          static_assert(L::kWords == 2 * L::kVWords, "a V word for every two K words");
+#pragma unroll
+          for (int blk = 0; blk < L::kBlocks; ++blk) {
+            uint32_t wk[2][L::kWords], wv[4][L::kVWords];
+            k_load(next_kb, blk, wk);
+            v_load(vb, blk, n - tok, wv);
+#pragma unroll
+            for (int k = 0; k < L::kVWords; ++k) {
+              score(wk, blk, 2 * k, sc);
+              weigh(wv, blk, k, pb);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int blk = 0; blk < L::kBlocks; ++blk) {
+            uint32_t w[4][L::kVWords];
+            v_load(vb, blk, n - tok, w);
+#pragma unroll
+            for (int k = 0; k < L::kVWords; ++k) weigh(w, blk, k, pb);
           }
         }
-      } else {
-#pragma unroll
-        for (int blk = 0; blk < L::kBlocks; ++blk) {
-          uint32_t w[4][L::kVWords];
-          v_load(vb, blk, tok, masked, w);
-#pragma unroll
-          for (int k = 0; k < L::kVWords; ++k) weigh(w, blk, k, pb);
-        }
+        stage = after(stage);
       }
-      stage = after(stage);
     }
 
     // ---- the segment's end: join the warps ----
@@ -1113,7 +1133,19 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
           *reinterpret_cast<float4*>(mine + cell(2 * t + h, k, g)) = make_float4(
               acc[nt][2 * k][h], acc[nt][2 * k][2 + h], acc[nt][2 * k + 1][h], acc[nt][2 * k + 1][2 + h]);
       __syncthreads();
-      if (!kInt8) nans = nan_any != 0;  // (read between two barriers: all threads alike)
+      if (!kInt8 && nan_any != 0) {  // (set before that barrier, cleared behind the last: all threads alike)
+        nans = true;
+#pragma unroll 1
+        for (int i = tid; i < 8 * kDim; i += C::kThreads) {
+          const int r8 = i / kDim, d = i - r8 * kDim;
+          if (nan_dims[nt * 8 + r8][d >> 5] >> (d & 31) & 1u) {
+            const int2 place = L::v_place(d & ~3);
+            reinterpret_cast<float*>(smem + free_stage[0])[cell(r8, place.x, place.y) + (d & 3)] =
+                __int_as_float(0x7FC00000);
+          }
+        }
+        __syncthreads();
+      }
       if (C::kQInRegs && seg_end < end) q_load(places[which ^ 1], 0, qr);  // (arrives during the joining)
       for (int x = tid; x < 8 * (kDim / 4); x += C::kThreads) {
         const int r8 = x / (kDim / 4), d = (x - r8 * (kDim / 4)) * 4, r = nt * 8 + r8;
@@ -1132,14 +1164,6 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
           const float4 a = *reinterpret_cast<const float4*>(cells + from_cell);
           v.x = fmaf(a.x, fv, v.x), v.y = fmaf(a.y, fv, v.y), v.z = fmaf(a.z, fv, v.z), v.w = fmaf(a.w, fv, v.w);
           l = fmaf(o.y, f, l);
-        }
-        if (nans) {
-          const uint32_t nan = nan_dims[r][d >> 5] >> (d & 31);
-          const float none = __int_as_float(0x7FC00000);
-          if (nan & 1u) v.x = none;
-          if (nan & 2u) v.y = none;
-          if (nan & 4u) v.z = none;
-          if (nan & 8u) v.w = none;
         }
         if (whole) {
           item_end.store(r, d, v, top, l);
