@@ -47,12 +47,12 @@
 //
 // What bounds it (fractions of the measured copy bandwidth on the codes and
 // scales read).  Long caches: HBM; 32 sequences of 16384 tokens, 8 KV heads of
-// 128, us: E4M3 182 (0.88), INT8 186 (0.87), 16 rows 184 (0.88); heads of 64 97
-// (0.83), of 96 141 (0.86), of 256 (16 sequences) 167 (0.96); pages of 16 tokens
-// 186.  Fewer bytes: the launch, the plan, the first strips' latency and the
-// joining, 8 us together: 24 ragged ones of up to 8191 tokens 44.8 us (0.70), one
-// of 131071 (INT8) 50.9 (0.79), one of 777 7.4, one of 16 4.9.  32 rows: issue
-// (INT8 279 us, 0.58; E4M3 of 128 is k_kv_attention_tc.cuh's).  Measured and not
+// 128, us: E4M3 186 (0.86), INT8 187 (0.86), 16 rows 186 (0.87); heads of 64 98
+// (0.82), of 96 143 (0.84), of 256 (16 sequences) 168 (0.96); pages of 16 tokens
+// 188.  Fewer bytes: the launch, the plan, the first strips' latency and the
+// joining, 8 us together: 24 ragged ones of up to 8191 tokens 45.0 us (0.70), one
+// of 131071 (INT8) 51.3 (0.78), one of 777 7.5, one of 16 5.2.  32 rows: issue
+// (INT8 282 us, 0.57; heads of 64 and 96, E4M3, 169 and 228, 0.48 and 0.53; E4M3 of 128 is k_kv_attention_tc.cuh's).  Measured and not
 // taken: more shares than resident CTAs (24 ragged 46 to 51 .. 73 us: every CTA
 // pays for its plan and first strips), two warps on one ring that part the rows
 // or the dims of 32 rows between them (260 to 344 and 334 us).

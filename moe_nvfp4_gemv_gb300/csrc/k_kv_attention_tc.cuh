@@ -38,14 +38,14 @@
 // k_kv_attention.cuh; shares are cut at tiles, so that tiles hold whole pages.
 //
 // What bounds it.  32 sequences of 16384 tokens, 4 new ones each, 64 heads over
-// 8: 173 us, 0.93 of the measured bandwidth (mma.sync with the codes converted
+// 8: 174 us, 0.93 of the measured bandwidth (mma.sync with the codes converted
 // in registers: 263, bound by issue: 447 instructions a strip of 16 tokens,
-// where this kernel needs 350).  Steps to it: both rings as one, a V tile held
+// where this kernel needs 342).  Steps to it: both rings as one, a V tile held
 // as long as its K and 16 TMA boxes a tile from one warp 228; rings apart, boxes
 // of a page 175.  Short calls pay for the set-up and the first tile's chain
-// (13.3 us for one sequence of 1000 tokens; mma.sync 16), several items in a share
+// (13.4 us for one sequence of 1000 tokens; mma.sync 16), several items in a share
 // for the drains between them (kAttnTcItemCost: 24 ragged sequences of up to
-// 8191 tokens 68 us with 16, 58 with 32, 53 with 64; mma.sync 90).
+// 8191 tokens 68 us with 16, 58 with 32, 54 with 64; mma.sync 90).
 //
 // Every wait is bounded.  After a failed one (the error word holds
 // FP4_ERR_TIMEOUT) the waits that follow are skipped, so that all roles come to

@@ -22,11 +22,12 @@
 // A row is split over the CTAs of a cluster when there are few rows; they
 // meet in the shared memory of the cluster's first CTA.
 //
-// What bounds it.  Many rows: HBM (2048 rows of 131072 bf16: 92 us, 0.87 of the
-// measured copy bandwidth), with the exponentials close behind (issue slots 57 %
+// What bounds it.  Many rows: HBM (2048 rows of 131072 bf16: 92.6 us, 0.87 of the
+// measured copy bandwidth), with the exponentials close behind (issue slots 60 %
 // taken; one scalar chain per element 114 us, paired fp32 sums 101, loads of a
-// slot ahead 92).  Few: latency; one row of 128003 6.1 us (2.1 of it the top
-// alternatives), 64 rows of 100001 fp32 9.5.  Measured and not taken: 512 or 1024
+// slot ahead 92; the difference to the maximum as an operation of its own 92.6).
+// Few: latency; one row of 128003 6.2 us (2.1 of it the top
+// alternatives), 64 rows of 100001 fp32 9.8.  Measured and not taken: 512 or 1024
 // threads (fewer CTAs to fill the phases without loads), double-buffered loads
 // (104 us for the 2048 rows).
 #pragma once
