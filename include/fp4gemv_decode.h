@@ -1,7 +1,7 @@
 /*
  * fp4gemv_decode.h -- the decode step's operators around the products of
- * fp4gemv.h: a paged key/value cache held in 8 bits (append, attention),
- * routing of tokens to experts (what fp4gemv_moe_gate_up takes as ids and
+ * fp4gemv.h: a paged key/value cache held in 8 bits (append, attention,
+ * reading it back), the residual stream with its norms, routing of tokens to experts (what fp4gemv_moe_gate_up takes as ids and
  * fp4gemv_moe_down_combine as tw), and the log probabilities of the answer.
  *
  * The conventions of fp4gemv.h hold: device pointers owned by the caller,
@@ -124,6 +124,51 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
                                     int q_len, const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
                                     int B, float sm_scale, int window, void* out, int64_t ldo, float* lse,
                                     void* workspace, size_t workspace_bytes, int pdl, cudaStream_t stream);
+
+/* The last tokens of B sequences out of the cache: rows cu[b] .. cu[b + 1] of
+ * k and v (cu int32 [B + 1] device, not decreasing, within 0 .. T), or T / B
+ * rows each with cu = NULL, receive the tokens that end at position
+ * seq_lens[b], value = code * scale in binary32 rounded to `dtype` (bf16, f16
+ * or f32).  k, v [T, kv_heads, head_dim], token strides ldk, ldv in elements
+ * (multiples of 8; f32: of 4).  The other way of fp4gemv_kv_append.
+ * Rows of positions below 0, outside the table's row, or on a page id outside
+ * [0, num_blocks) become zeros and raise FP4GEMV_ERR_BAD_INDEX; rows that cu
+ * does not name stay as they were.
+ * Shapes as fp4gemv_kv_append. */
+fp4gemv_status fp4gemv_kv_read(const fp4gemv_kv_cache* cache, void* k, int64_t ldk, void* v, int64_t ldv, int dtype,
+                               int T, const int32_t* cu, const int32_t* block_table, int max_blocks,
+                               const int32_t* seq_lens, int B, int pdl, cudaStream_t stream);
+
+/* ---- the residual stream and its norms ---------------------------------- */
+
+/* Largest H. */
+#define FP4GEMV_NORM_MAX_WIDTH 32768
+
+typedef enum { FP4GEMV_GATE_CHANNEL = 0, FP4GEMV_GATE_TOKEN = 1 } fp4gemv_gate_kind;
+
+/* Per token t, in binary32 (sums of squares as well):
+ *   u = y[t], or with post_weight y[t] / sqrt(mean(y[t]^2) + eps) *
+ *       (weight_offset + post_weight)
+ *   r = x[t] + scale * g * u     g: 1 with gate = NULL, else the gate, or
+ *       1 / (1 + exp(-gate)) with gate_sigmoid
+ *   residual[t] = r
+ *   out[t] = r / sqrt(mean(r^2) + eps) * (weight_offset + weight)
+ * each rounded once (out from r before its rounding).  y = NULL: out is the
+ * norm of x; post_weight and gate have to be NULL, and residual is not used.
+ * x, residual [M, H] of x_dtype (dtype or f32); y, out [M, H] of dtype (bf16
+ * or f16); weight, post_weight [H] of weight_dtype, gate of gate_dtype (dtype
+ * or f32).  gate_kind CHANNEL: gate [M, H] with row stride ldg, 0 for one row
+ * that all tokens take; TOKEN: gate[t * ldg] for all of a token's values.
+ * Row strides in elements, at least H; nothing needs more alignment than its
+ * element's, and 16-byte aligned rows of H a multiple of 8 are faster.
+ * residual may be x, and out may be y, with the same stride.  One launch.
+ * Shapes: M >= 1, 1 <= H <= FP4GEMV_NORM_MAX_WIDTH; scale, weight_offset
+ *   finite, eps finite and not negative. */
+fp4gemv_status fp4gemv_add_norm(const void* x, int64_t ldx, int x_dtype, const void* y, int64_t ldy, int dtype,
+                                const void* weight, const void* post_weight, int weight_dtype, const void* gate,
+                                int64_t ldg, int gate_dtype, int gate_kind, int gate_sigmoid, float scale, float eps,
+                                float weight_offset, void* residual, int64_t ldr, void* out, int64_t ldo, int M, int H,
+                                int pdl, cudaStream_t stream);
 
 /* ---- routing to experts ------------------------------------------------ */
 

@@ -78,6 +78,112 @@ fp4gemv_status fp4gemv_kv_append(const fp4gemv_kv_cache* cache, const void* k, i
   return from_cuda(fp4::launch_kv_append(p, cache->format == FP4GEMV_KV_INT8, dtype == FP4GEMV_F16, pdl, stream));
 }
 
+fp4gemv_status fp4gemv_kv_read(const fp4gemv_kv_cache* cache, void* k, int64_t ldk, void* v, int64_t ldv, int dtype,
+                               int T, const int32_t* cu, const int32_t* block_table, int max_blocks,
+                               const int32_t* seq_lens, int B, int pdl, cudaStream_t stream) {
+  bool nulls, crooked;
+  fp4gemv_status st = check_cache(cache, &nulls, &crooked);
+  if (st != FP4GEMV_OK) return st;
+  if (pdl != 0 && pdl != 1) return FP4GEMV_ERR_INVALID_ARG;
+  if (dtype < FP4GEMV_BF16 || dtype > FP4GEMV_F32) return FP4GEMV_ERR_INVALID_ARG;
+  const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
+  if (T < 0 || B < 1 || max_blocks < 1 || ldk < width || ldv < width) return FP4GEMV_ERR_INVALID_ARG;
+  if (!cu && T % B != 0) return FP4GEMV_ERR_INVALID_ARG;
+  if (B > FP4GEMV_KV_MAX_BATCH || static_cast<int64_t>(max_blocks) * cache->block_size > (1ll << 30) || T > (1 << 30))
+    return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+  const int unit = dtype == FP4GEMV_F32 ? 4 : 8;  // elements of 16 bytes
+  if (crooked || !aligned(k, 16) || !aligned(v, 16) || ldk % unit != 0 || ldv % unit != 0 || !aligned(cu, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return FP4GEMV_ERR_MISALIGNED;
+  if (nulls || !block_table || !seq_lens) return FP4GEMV_ERR_INVALID_ARG;
+  if (T == 0) return FP4GEMV_OK;
+  if (!k || !v) return FP4GEMV_ERR_INVALID_ARG;
+  uint32_t* err = nullptr;
+  int sms = 0;
+  st = fp4::current_device_state(&err, &sms);
+  if (st != FP4GEMV_OK) return st;
+  fp4::KvReadParams p = {};
+  p.codes[0] = cache->k_codes;
+  p.codes[1] = cache->v_codes;
+  p.scale[0] = cache->k_scale;
+  p.scale[1] = cache->v_scale;
+  p.dst[0] = k;
+  p.dst[1] = v;
+  p.ld[0] = ldk;
+  p.ld[1] = ldv;
+  p.cu = cu;
+  p.table = block_table;
+  p.lens = seq_lens;
+  p.err = err;
+  p.uniform = T / B;
+  p.B = B;
+  p.T = T;
+  p.max_blocks = max_blocks;
+  p.num_blocks = cache->num_blocks;
+  p.heads = cache->kv_heads;
+  p.block_log2 = block_log2(cache->block_size);
+  p.dim = cache->head_dim;
+  fp4::count_launch();
+  return from_cuda(fp4::launch_kv_read(p, cache->format == FP4GEMV_KV_INT8, dtype, sms, pdl, stream));
+}
+
+fp4gemv_status fp4gemv_add_norm(const void* x, int64_t ldx, int x_dtype, const void* y, int64_t ldy, int dtype,
+                                const void* weight, const void* post_weight, int weight_dtype, const void* gate,
+                                int64_t ldg, int gate_dtype, int gate_kind, int gate_sigmoid, float scale, float eps,
+                                float weight_offset, void* residual, int64_t ldr, void* out, int64_t ldo, int M, int H,
+                                int pdl, cudaStream_t stream) {
+  if (pdl != 0 && pdl != 1) return FP4GEMV_ERR_INVALID_ARG;
+  if (dtype != FP4GEMV_BF16 && dtype != FP4GEMV_F16) return FP4GEMV_ERR_INVALID_ARG;
+  auto kind = [&](int t) { return t == dtype || t == FP4GEMV_F32; };
+  if (!kind(x_dtype) || !kind(weight_dtype) || (gate && !kind(gate_dtype))) return FP4GEMV_ERR_INVALID_ARG;
+  if (gate && gate_kind != FP4GEMV_GATE_CHANNEL && gate_kind != FP4GEMV_GATE_TOKEN) return FP4GEMV_ERR_INVALID_ARG;
+  if (gate_sigmoid != 0 && gate_sigmoid != 1) return FP4GEMV_ERR_INVALID_ARG;
+  if (M < 1 || H < 1 || ldx < H || ldo < H || (y && (ldy < H || ldr < H))) return FP4GEMV_ERR_INVALID_ARG;
+  const bool channel = gate && gate_kind == FP4GEMV_GATE_CHANNEL;
+  if (gate && (channel ? ldg != 0 && ldg < H : ldg < 0)) return FP4GEMV_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(weight_offset) || !std::isfinite(eps) || eps < 0.0f)
+    return FP4GEMV_ERR_INVALID_ARG;
+  if (!y && (post_weight || gate)) return FP4GEMV_ERR_INVALID_ARG;
+  if (H > FP4GEMV_NORM_MAX_WIDTH) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+  auto size = [](int t) -> uintptr_t { return t == FP4GEMV_F32 ? 4 : 2; };
+  if (!aligned(x, size(x_dtype)) || !aligned(residual, size(x_dtype)) || !aligned(y, 2) || !aligned(out, 2) ||
+      !aligned(weight, size(weight_dtype)) || !aligned(post_weight, size(weight_dtype)) ||
+      (gate && !aligned(gate, size(gate_dtype))))
+    return FP4GEMV_ERR_MISALIGNED;
+  if (!x || !weight || !out || (y && !residual)) return FP4GEMV_ERR_INVALID_ARG;
+  fp4gemv_status st = fp4::current_device_state(nullptr, nullptr);
+  if (st != FP4GEMV_OK) return st;
+  fp4::AddNormParams p = {};
+  p.x = x;
+  p.y = y;
+  p.weight = weight;
+  p.post = post_weight;
+  p.gate = gate;
+  p.residual = residual;
+  p.out = out;
+  p.ldx = ldx;
+  p.ldy = ldy;
+  p.ldg = ldg;
+  p.ldr = ldr;
+  p.ldo = ldo;
+  p.M = M;
+  p.H = H;
+  p.x_type = x_dtype;
+  p.w_type = weight_dtype;
+  p.g_type = gate_dtype;
+  p.gate_scalar = gate && !channel;
+  p.sigmoid = gate_sigmoid;
+  p.scale = scale;
+  p.eps = eps;
+  p.offset = weight_offset;
+  // whole chunks of 8 values on 16-byte boundaries (an f32 chunk is two of them)
+  auto rows16 = [](const void* q, int64_t ld) { return aligned(q, 16) && ld % 8 == 0; };
+  const bool vec = H % 8 == 0 && rows16(x, ldx) && rows16(out, ldo) && aligned(weight, 16) && aligned(post_weight, 16) &&
+                   (!y || (rows16(y, ldy) && rows16(residual, ldr))) && (!channel || rows16(gate, ldg));
+  fp4::count_launch();
+  return from_cuda(fp4::launch_add_norm(p, dtype == FP4GEMV_F16, vec, pdl, stream));
+}
+
 // [arrival counters, three for each CTA | partials, two for each CTA]
 static size_t attn_counter_bytes(int ctas) { return (static_cast<size_t>(ctas) * 12 + 15) / 16 * 16; }
 

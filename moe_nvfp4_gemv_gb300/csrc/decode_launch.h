@@ -4,8 +4,10 @@
 #pragma once
 
 #include "fp4gemv.h"
+#include "k_add_norm.cuh"
 #include "k_kv_append.cuh"
 #include "k_kv_attention.cuh"
+#include "k_kv_read.cuh"
 #include "k_logprobs.cuh"
 
 namespace fp4 {
@@ -22,6 +24,9 @@ bool encode_pages_128(CUtensorMap* m, const void* base, int block_size, int64_t 
 cudaError_t launch_moe_route(const RouteParams& p, int dtype, int sms, int pdl, cudaStream_t stream);
 cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, int T, int sms, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_append(const KvAppendParams& p, int int8, int f16, int pdl, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvReadParams& p, int int8, int dtype, int sms, int pdl, cudaStream_t stream);
+// vec: rows of 16-byte aligned chunks of 8 values.
+cudaError_t launch_add_norm(const AddNormParams& p, int f16, int vec, int pdl, cudaStream_t stream);
 // CTAs of the attention kernel at most (the workspace is sized for them).
 int kv_attention_max_ctas(int sms);
 // row_units: row tiles of 8, 16 or 32 rows: 1, 2 or 4 (4 not with head_dim 256).

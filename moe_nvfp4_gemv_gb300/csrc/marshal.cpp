@@ -15,6 +15,7 @@
 // nothing to do).  No C++ exception leaves a function.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -27,6 +28,8 @@ namespace {
 
 decltype(&fp4gemv_kv_append) g_append;
 decltype(&fp4gemv_kv_attention) g_attention;
+decltype(&fp4gemv_kv_read) g_read;
+decltype(&fp4gemv_add_norm) g_add_norm;
 decltype(&fp4gemv_moe_route) g_route;
 decltype(&fp4gemv_token_logprobs) g_logprobs;
 
@@ -76,6 +79,13 @@ bool plain(const at::Tensor& t, at::ScalarType type, int64_t index) {
 }
 int half_code(const at::Tensor& t) {  // -1: neither bf16 nor f16
   return t.scalar_type() == at::kBFloat16 ? FP4GEMV_BF16 : t.scalar_type() == at::kHalf ? FP4GEMV_F16 : -1;
+}
+int type_code(const at::Tensor& t) {  // -1: none of bf16, f16, f32
+  return t.scalar_type() == at::kFloat ? static_cast<int>(FP4GEMV_F32) : half_code(t);
+}
+bool shaped(const at::Tensor& t, int64_t rows) { return t.dim() == 1 && t.size(0) == rows; }
+bool shaped(const at::Tensor& t, int64_t rows, int64_t columns) {
+  return t.dim() == 2 && t.size(0) == rows && t.size(1) == columns;
 }
 cudaStream_t stream_of(int64_t index) {
   return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream();
@@ -155,6 +165,113 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// kv_read(cache, device, kv_heads, head_dim, block_table, seq_lens, cu, k, v, pdl)
+PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&]() -> int {
+    const auto* cache = reinterpret_cast<const fp4gemv_kv_cache*>(integer(a[0]));
+    const int64_t index = integer(a[1]), H = integer(a[2]), D = integer(a[3]);
+    const at::Tensor &table = tensor(a[4], "block_table"), &lens = tensor(a[5], "seq_lens"), &k = tensor(a[7], "k"),
+                     &v = tensor(a[8], "v");
+    int B, max_blocks;
+    sequences(table, lens, index, &B, &max_blocks);
+    const int dtype = type_code(k);
+    auto fits = [&](const at::Tensor& t) {
+      return t.scalar_type() == k.scalar_type() && t.dim() == 3 && t.size(1) == H && t.size(2) == D && t.is_cuda() &&
+             t.get_device() == index && t.stride(2) == 1 && (H == 1 || t.stride(1) == D);
+    };
+    if (dtype < 0 || !fits(k) || !fits(v) || v.size(0) != k.size(0))
+      refuse("k and v must be bf16, f16 or fp32 [T, %d, %d] tensors of one type on the cache's device with contiguous heads",
+             static_cast<int>(H), static_cast<int>(D));
+    const int64_t T = k.size(0);
+    const int32_t* cu = nullptr;
+    if (a[6] != Py_None) {
+      const at::Tensor& t = tensor(a[6], "cu");
+      if (t.numel() != static_cast<int64_t>(B) + 1 || !plain(t, at::kInt, index))
+        refuse("cu must be a contiguous int32 [%d] tensor on the cache's device", B + 1);
+      cu = address_as<int32_t>(t);
+    }
+    const int pdl = flag(a[9]);
+    if (T == 0) return FP4GEMV_OK;
+    if (B == 0) refuse("tokens of no sequence");
+    if (T > INT_MAX) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+    const int64_t ldk = T > 1 ? k.stride(0) : H * D, ldv = T > 1 ? v.stride(0) : H * D;
+    void *pk = address_as<void>(k), *pv = address_as<void>(v);
+    const int32_t *pt = address_as<int32_t>(table), *pl = address_as<int32_t>(lens);
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(index));
+    const cudaStream_t stream = stream_of(index);
+    return unlocked([&] {
+      return g_read(cache, pk, ldk, pv, ldv, dtype, static_cast<int>(T), cu, pt, max_blocks, pl, B, pdl, stream);
+    });
+  });
+}
+
+// add_norm(x, y, weight, post_weight, gate, gate_sigmoid, scale, eps, weight_offset, residual, out, pdl)
+PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> int {
+    const at::Tensor &x = tensor(a[0], "x"), &weight = tensor(a[2], "weight"), &out = tensor(a[10], "out");
+    const bool block = a[1] != Py_None;
+    if (x.dim() != 2 || !x.is_cuda() || x.stride(1) != 1) refuse("x must be a 2-D CUDA tensor with unit inner stride");
+    const int64_t M = x.size(0), H = x.size(1), index = x.get_device();
+    const at::ScalarType half = out.scalar_type();
+    const int dtype = half_code(out), x_type = type_code(x);
+    auto rows = [&](const at::Tensor& t) {
+      return t.dim() == 2 && t.size(0) == M && t.size(1) == H && t.stride(1) == 1 && t.is_cuda() && t.get_device() == index;
+    };
+    auto stride = [&](const at::Tensor& t) { return M > 1 ? t.stride(0) : H; };
+    if (dtype < 0 || !rows(out)) refuse("out must be a bf16 or f16 tensor of x's shape and device with unit inner stride");
+    auto kind = [&](const at::Tensor& t) { return t.scalar_type() == half || t.scalar_type() == at::kFloat; };
+    if (!kind(x)) refuse("x must be of out's type or fp32");
+    auto is_weight = [&](const at::Tensor& t) { return shaped(t, H) && kind(t) && plain(t, t.scalar_type(), index); };
+    if (!is_weight(weight)) refuse("weight must be a contiguous [%lld] tensor of out's type or fp32 on x's device", static_cast<long long>(H));
+    const void *py = nullptr, *post = nullptr, *gate = nullptr;
+    int64_t ldy = H, ldg = 0, ldr = H;
+    int gate_type = dtype, gate_kind = FP4GEMV_GATE_CHANNEL;
+    void* pr = nullptr;
+    if (block) {
+      const at::Tensor &y = tensor(a[1], "y"), &residual = tensor(a[9], "residual");
+      if (y.scalar_type() != half || !rows(y)) refuse("y must be a tensor of out's type and x's shape with unit inner stride");
+      if (residual.scalar_type() != x.scalar_type() || !rows(residual))
+        refuse("residual must be a tensor of x's type and shape with unit inner stride");
+      py = address(y);
+      ldy = stride(y);
+      pr = address_as<void>(residual);
+      ldr = stride(residual);
+    }
+    if (a[3] != Py_None) {
+      const at::Tensor& t = tensor(a[3], "post_weight");
+      if (!is_weight(t) || t.scalar_type() != weight.scalar_type()) refuse("post_weight must be a tensor like weight");
+      post = address(t);
+    }
+    if (a[4] != Py_None) {
+      const at::Tensor& t = tensor(a[4], "gate");
+      const bool channel = t.dim() == 1 && t.size(0) == H && (H == 1 || t.stride(0) == 1);
+      const bool token = t.dim() == 2 && t.size(0) == M && t.size(1) == 1 && H != 1;
+      if (!kind(t) || !t.is_cuda() || t.get_device() != index || !(channel || token || rows(t)))
+        refuse("gate must be an [H], [M, H] or [M, 1] tensor of out's type or fp32 on x's device with unit inner stride");
+      gate = address(t);
+      gate_type = type_code(t);
+      gate_kind = token ? FP4GEMV_GATE_TOKEN : FP4GEMV_GATE_CHANNEL;
+      ldg = channel ? 0 : token ? (M > 1 ? t.stride(0) : 0) : stride(t);
+    }
+    if (!block && (post || gate)) refuse("post_weight and gate need y");
+    const int sigmoid = flag(a[5]), pdl = flag(a[11]);
+    const float scale = static_cast<float>(real(a[6])), eps = static_cast<float>(real(a[7])),
+                offset = static_cast<float>(real(a[8]));
+    if (M == 0) return FP4GEMV_OK;
+    if (M > INT_MAX || H > INT_MAX) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+    const void *px = address(x), *pw = address(weight);
+    const int w_type = type_code(weight);
+    const int64_t ldx = stride(x), ldo = stride(out);
+    void* po = address_as<void>(out);
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(index));
+    const cudaStream_t stream = stream_of(index);
+    return unlocked([&] {
+      return g_add_norm(px, ldx, x_type, py, ldy, dtype, pw, post, w_type, gate, ldg, gate_type, gate_kind, sigmoid, scale,
+                        eps, offset, pr, ldr, po, ldo, static_cast<int>(M), static_cast<int>(H), pdl, stream);
+    });
+  });
+}
+
 // The one stride between tokens of a [B, n, heads, dim] tensor.
 int64_t token_stride(const at::Tensor& t, const char* name) {
   const int64_t B = t.size(0), n = t.size(1), heads = t.size(2), dim = t.size(3);
@@ -212,7 +329,7 @@ struct Logits {
 };
 Logits logits_of(const at::Tensor& t) {
   Logits l;
-  l.dtype = t.scalar_type() == at::kFloat ? static_cast<int>(FP4GEMV_F32) : half_code(t);
+  l.dtype = type_code(t);
   if (l.dtype < 0 || t.dim() != 2 || !t.is_cuda() || t.stride(1) != 1)
     refuse("logits must be a 2-D bf16, f16 or fp32 CUDA tensor with unit inner stride");
   l.rows = t.size(0);
@@ -221,10 +338,6 @@ Logits logits_of(const at::Tensor& t) {
   l.index = t.get_device();
   if (l.rows > INT_MAX || l.width > INT_MAX) refuse("logits are too large");
   return l;
-}
-bool shaped(const at::Tensor& t, int64_t rows) { return t.dim() == 1 && t.size(0) == rows; }
-bool shaped(const at::Tensor& t, int64_t rows, int64_t columns) {
-  return t.dim() == 2 && t.size(0) == rows && t.size(1) == columns;
 }
 
 // moe_route(logits, topk, scores, bias, n_group, topk_group, group_top, renormalize, scale, ids, weights, pdl)
@@ -311,13 +424,23 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// bind_more(kv_read, add_norm): the others'
+PyObject* bind_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 2, [&]() -> int {
+    g_read = reinterpret_cast<decltype(g_read)>(integer(a[0]));
+    g_add_norm = reinterpret_cast<decltype(g_add_norm)>(integer(a[1]));
+    return 0;
+  });
+}
+
 template <PyObject* (*kFunction)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kFunction)), METH_FASTCALL, nullptr};
 }
 PyMethodDef g_methods[] = {method<bind>("bind"),           method<kv_append>("kv_append"),
                            method<kv_attention>("kv_attention"), method<moe_route>("moe_route"),
-                           method<token_logprobs>("token_logprobs"), {nullptr, nullptr, 0, nullptr}};
+                           method<token_logprobs>("token_logprobs"), method<bind_more>("bind_more"),
+                           method<kv_read>("kv_read"),     method<add_norm>("add_norm"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

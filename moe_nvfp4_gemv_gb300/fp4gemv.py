@@ -82,6 +82,9 @@ def _load() -> ctypes.CDLL:
         "fp4gemv_stream_capture_id": (ctypes.c_uint64, [vp]),
         "fp4gemv_kv_attention": (i32, [vp, vp, i64, i32, i32, i32, vp, i32, vp, i32, ctypes.c_float, i32, vp, i64, vp,
                                        vp, sz, i32, vp]),
+        "fp4gemv_kv_read": (i32, [vp, vp, i64, vp, i64, i32, i32, vp, vp, i32, vp, i32, i32, vp]),
+        "fp4gemv_add_norm": (i32, [vp, i64, i32, vp, i64, i32, vp, vp, i32, vp, i64, i32, i32, i32, ctypes.c_float,
+                                   ctypes.c_float, ctypes.c_float, vp, i64, vp, i64, i32, i32, i32, vp]),
         "fp4gemv_moe_route": (i32, [vp, i64, i32, i32, i32, i32, i32, vp, i32, i32, i32, i32, ctypes.c_float, vp, vp,
                                     i32, vp]),
         "fp4gemv_token_logprobs": (i32, [vp, i64, i32, i32, i32, vp, ctypes.c_float, i32, vp, vp, vp, vp, vp, i32,
@@ -122,6 +125,7 @@ try:
     from . import _marshal  # noqa: E402  (built by _load where it has to be)
     _marshal.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
         _lib.fp4gemv_kv_append, _lib.fp4gemv_kv_attention, _lib.fp4gemv_moe_route, _lib.fp4gemv_token_logprobs)))
+    _marshal.bind_more(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (_lib.fp4gemv_kv_read, _lib.fp4gemv_add_norm)))
 except Exception as e:
     _marshal = _NoMarshal(e)
 _nvfp4_gemv = _lib.fp4gemv_nvfp4_gemv
@@ -412,6 +416,7 @@ def moe_down_combine(act, ids, tw, w2, w2_sf, alpha2, sact, wsd, ssd, gssd, out,
 # ---- the decode step's operators around the products ----
 _moe_route = _marshal.moe_route
 _token_logprobs = _marshal.token_logprobs
+_add_norm = _marshal.add_norm
 _I32 = torch.int32
 _F32 = torch.float32
 
@@ -439,6 +444,37 @@ def moe_route(logits: torch.Tensor, topk: int, scores: str = "softmax", bias: to
     if status:
         raise Fp4GemvError(status, "fp4gemv_moe_route")
     return ids, weights
+
+
+def add_norm(x: torch.Tensor, y: torch.Tensor | None, weight: torch.Tensor, post_weight: torch.Tensor | None = None,
+             gate: torch.Tensor | None = None, gate_sigmoid: bool = False, scale: float = 1.0, eps: float = 1e-6,
+             weight_offset: float = 0.0, out: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+             pdl: bool = True) -> tuple[torch.Tensor, torch.Tensor]:
+    """A block's output ``y`` into the residual stream ``x`` (both [M, H]) and the
+    next block's RMS norm: (out, residual) with
+
+        u = y, or with ``post_weight`` rms_norm(y) * (weight_offset + post_weight)
+        residual = x + scale * g * u;  g: 1, ``gate``, or sigmoid(gate) with ``gate_sigmoid``
+        out = rms_norm(x + scale * g * u) * (weight_offset + weight)
+
+    in fp32, each rounded once.  y and out bf16 or f16; x and residual of that
+    type or fp32; weights [H] and the gate ([H], [M, H] or [M, 1]) likewise.
+    Unit inner strides, any row strides.  ``residual`` may be x and ``out`` may
+    be y.  With y = None: (rms_norm(x) * (weight_offset + weight), x), out in
+    x's type, bf16 for fp32, unless ``out`` is given."""
+    if out is None:
+        if y is not None:
+            out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        else:
+            out = torch.empty(x.shape, dtype=_BF16 if x.dtype is _F32 else x.dtype, device=x.device)
+    if y is None:
+        residual = x
+    elif residual is None:
+        residual = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    status = _add_norm(x, y, weight, post_weight, gate, gate_sigmoid, scale, eps, weight_offset, residual, out, pdl)
+    if status:
+        raise Fp4GemvError(status, "fp4gemv_add_norm")
+    return out, residual
 
 
 class TokenLogprobs(NamedTuple):

@@ -2,12 +2,13 @@
 
 ``KvCache8`` wraps the four tensors of a cache -- codes uint8 [num_blocks,
 kv_heads, block_size, head_dim] and fp32 scales [num_blocks, kv_heads], keys
-and values apart (the formats: include/fp4gemv_decode.h) -- with the two calls
+and values apart (the formats: include/fp4gemv_decode.h) -- with the calls
 of a decode step:
 
 * ``append``: quantises new keys and values into the pages that the block
   table names; a page's scale grows with what it holds;
-* ``attend``: attention of each sequence's newest tokens over its pages.
+* ``attend``: attention of each sequence's newest tokens over its pages;
+* ``read``: tokens out of the pages again.
 
 The tensors stay the caller's: copy, share or reset pages as the serving
 program likes, between calls on the same stream.  Sequences are given by a
@@ -31,6 +32,7 @@ FORMATS = {"e4m3": 0, "int8": 1}
 _F32 = torch.float32
 _append = _marshal.kv_append
 _attend = _marshal.kv_attention
+_read = _marshal.kv_read
 
 
 class _CacheStruct(ctypes.Structure):
@@ -135,6 +137,25 @@ class KvCache8:
                          pdl)
         if status:
             raise Fp4GemvError(status, "fp4gemv_kv_append")
+
+    def read(self, block_table: torch.Tensor, seq_lens: torch.Tensor, tokens: int | None = None,
+             cu: torch.Tensor | None = None, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
+             dtype: torch.dtype = torch.bfloat16, pdl: bool = True) -> tuple[torch.Tensor, torch.Tensor]:
+        """The last tokens of B sequences out of the cache: (k, v) [T, kv_heads,
+        head_dim], code * scale rounded to ``dtype`` (bf16, f16 or fp32).  T / B
+        tokens of each, or rows cu[b] .. cu[b + 1] (int32 [B + 1]) of sequence
+        b, that end at position seq_lens[b]; rows that ``cu`` does not name stay
+        as they are.  ``tokens`` is T; or ``k`` and ``v`` (any token stride that
+        is a multiple of 16 bytes, heads contiguous) receive them."""
+        if (k is None) != (v is None) or (k is None) == (tokens is None):
+            raise ValueError("either tokens, or both k and v")
+        if k is None:
+            shape = (tokens, self.kv_heads, self.head_dim)
+            k, v = (torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
+        status = _read(self._handle, self._index, self.kv_heads, self.head_dim, block_table, seq_lens, cu, k, v, pdl)
+        if status:
+            raise Fp4GemvError(status, "fp4gemv_kv_read")
+        return k, v
 
     def attend(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, sm_scale: float | None = None,
                window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
