@@ -1,7 +1,8 @@
 /*
  * fp4gemv_decode.h -- the decode step's operators around the products of
  * fp4gemv.h: a paged key/value cache held in 8 bits (append, attention,
- * reading it back), the residual stream with its norms, routing of tokens to experts (what fp4gemv_moe_gate_up takes as ids and
+ * also with first tokens that stay visible in a window, reading it back), the
+ * residual stream with its norms, routing of tokens to experts (what fp4gemv_moe_gate_up takes as ids and
  * fp4gemv_moe_down_combine as tw), and the log probabilities of the answer.
  *
  * The conventions of fp4gemv.h hold: device pointers owned by the caller,
@@ -124,6 +125,17 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
                                     int q_len, const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
                                     int B, float sm_scale, int window, void* out, int64_t ldo, float* lse,
                                     void* workspace, size_t workspace_bytes, int pdl, cudaStream_t stream);
+
+/* fp4gemv_kv_attention with first tokens that stay visible: the query at
+ * position p sees the tokens t <= p with t > p - window or t < sinks.  Pages
+ * of tokens that no query of a sequence sees are not looked at.  window = 0:
+ * all of 0 .. p.  sinks >= 0, at most 2^30; the rest as fp4gemv_kv_attention
+ * (E4M3, more than 16 rows: exact f16 operands like all others). */
+fp4gemv_status fp4gemv_kv_attention_sinks(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype,
+                                          int heads, int q_len, const int32_t* block_table, int max_blocks,
+                                          const int32_t* seq_lens, int B, float sm_scale, int window, int sinks,
+                                          void* out, int64_t ldo, float* lse, void* workspace, size_t workspace_bytes,
+                                          int pdl, cudaStream_t stream);
 
 /* The last tokens of B sequences out of the cache: rows cu[b] .. cu[b + 1] of
  * k and v (cu int32 [B + 1] device, not decreasing, within 0 .. T), or T / B

@@ -205,77 +205,107 @@ uint64_t fp4gemv_stream_capture_id(cudaStream_t stream) {
   return status == cudaStreamCaptureStatusActive ? id : 0;
 }
 
-fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype, int heads,
-                                    int q_len, const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
-                                    int B, float sm_scale, int window, void* out, int64_t ldo, float* lse,
-                                    void* workspace, size_t workspace_bytes, int pdl, cudaStream_t stream) {
+// What the attention calls share: every check, and the kernels' parameters.
+struct AttentionCall {
+  const fp4gemv_kv_cache* cache;
+  const void* q;
+  int64_t ldq;
+  int dtype, heads, q_len;
+  const int32_t* block_table;
+  int max_blocks;
+  const int32_t* seq_lens;
+  int B;
+  float sm_scale;
+  int window;
+  void* out;
+  int64_t ldo;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int pdl;
+};
+
+// Fills p, *row_units and *sms.
+static fp4gemv_status attention_params(const AttentionCall& a, fp4::KvAttnParams* out_p, int* out_row_units, int* out_sms) {
+  const fp4gemv_kv_cache* const cache = a.cache;
   bool nulls, crooked;
   fp4gemv_status st = check_cache(cache, &nulls, &crooked);
   if (st != FP4GEMV_OK) return st;
-  if (pdl != 0 && pdl != 1) return FP4GEMV_ERR_INVALID_ARG;
-  if (dtype != FP4GEMV_BF16 && dtype != FP4GEMV_F16) return FP4GEMV_ERR_INVALID_ARG;
-  if (heads < 1 || q_len < 1 || B < 1 || max_blocks < 1 || window < 0 || !std::isfinite(sm_scale))
+  if (a.pdl != 0 && a.pdl != 1) return FP4GEMV_ERR_INVALID_ARG;
+  if (a.dtype != FP4GEMV_BF16 && a.dtype != FP4GEMV_F16) return FP4GEMV_ERR_INVALID_ARG;
+  if (a.heads < 1 || a.q_len < 1 || a.B < 1 || a.max_blocks < 1 || a.window < 0 || !std::isfinite(a.sm_scale))
     return FP4GEMV_ERR_INVALID_ARG;
-  const int64_t width = static_cast<int64_t>(heads) * cache->head_dim;
-  if (ldq < width || ldo < width) return FP4GEMV_ERR_INVALID_ARG;
-  const int group = heads / cache->kv_heads;
-  if (heads % cache->kv_heads != 0 || group > FP4GEMV_KV_MAX_GROUP || q_len > FP4GEMV_KV_MAX_QLEN ||
-      B > FP4GEMV_KV_MAX_BATCH)
+  const int64_t width = static_cast<int64_t>(a.heads) * cache->head_dim;
+  if (a.ldq < width || a.ldo < width) return FP4GEMV_ERR_INVALID_ARG;
+  const int group = a.heads / cache->kv_heads;
+  if (a.heads % cache->kv_heads != 0 || group > FP4GEMV_KV_MAX_GROUP || a.q_len > FP4GEMV_KV_MAX_QLEN ||
+      a.B > FP4GEMV_KV_MAX_BATCH)
     return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
   // row tiles: the 8, 16 or 32 rows that a pass over the codes serves
   // (head_dim 256 has registers for 16).  One pass of 16 rows or two of 8, 32
   // sequences of 16384 tokens, 8 KV heads: 185 us against 350.
-  const int rows = q_len * group;
+  const int rows = a.q_len * group;
   const int row_units = rows <= 8 ? 1 : rows <= 16 || cache->head_dim > 128 ? 2 : 4;
   const int row_tiles = (rows + 8 * row_units - 1) / (8 * row_units);
-  const int64_t tokens = static_cast<int64_t>(max_blocks) * cache->block_size;
+  const int64_t tokens = static_cast<int64_t>(a.max_blocks) * cache->block_size;
   // (32-bit: places on the line of strips, a quarter more with padding, and strips of the cache)
   if (tokens > (1ll << 30) || static_cast<int64_t>(cache->kv_heads) * row_tiles >= (1 << 20) ||
-      (static_cast<double>(tokens) / 16 + fp4::kAttnTcItemCost + 8) * B * cache->kv_heads * row_tiles >= 1.2e9 ||
+      (static_cast<double>(tokens) / 16 + fp4::kAttnTcItemCost + 8) * a.B * cache->kv_heads * row_tiles >= 1.2e9 ||
       static_cast<double>(cache->num_blocks) * cache->kv_heads * (cache->block_size / 16) >= 2147483647.0)
     return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
-  if (crooked || !aligned(q, 16) || !aligned(out, 16) || ldq % 8 != 0 || ldo % 8 != 0 || !aligned(lse, 4) ||
-      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 16))
+  if (crooked || !aligned(a.q, 16) || !aligned(a.out, 16) || a.ldq % 8 != 0 || a.ldo % 8 != 0 || !aligned(a.lse, 4) ||
+      !aligned(a.block_table, 4) || !aligned(a.seq_lens, 4) || !aligned(a.workspace, 16))
     return FP4GEMV_ERR_MISALIGNED;
-  if (nulls || !q || !out || !block_table || !seq_lens || !workspace) return FP4GEMV_ERR_INVALID_ARG;
+  if (nulls || !a.q || !a.out || !a.block_table || !a.seq_lens || !a.workspace) return FP4GEMV_ERR_INVALID_ARG;
   uint32_t* err = nullptr;
   int sms = 0;
   st = fp4::current_device_state(&err, &sms);
   if (st != FP4GEMV_OK) return st;
-  if (workspace_bytes < fp4gemv_kv_attention_workspace_bytes(cache->head_dim)) return FP4GEMV_ERR_INVALID_ARG;
-  fp4::KvAttnTcParams p = {};
+  if (a.workspace_bytes < fp4gemv_kv_attention_workspace_bytes(cache->head_dim)) return FP4GEMV_ERR_INVALID_ARG;
+  fp4::KvAttnParams& p = *out_p;
   p.k_codes = cache->k_codes;
   p.v_codes = cache->v_codes;
   p.k_scale = cache->k_scale;
   p.v_scale = cache->v_scale;
-  p.q = static_cast<const uint16_t*>(q);
-  p.ldq = ldq;
-  p.out = static_cast<uint16_t*>(out);
-  p.ldo = ldo;
-  p.lse = lse;
-  p.table = block_table;
-  p.lens = seq_lens;
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.ldq = a.ldq;
+  p.out = static_cast<uint16_t*>(a.out);
+  p.ldo = a.ldo;
+  p.lse = a.lse;
+  p.table = a.block_table;
+  p.lens = a.seq_lens;
   p.err = err;
-  p.arrived = static_cast<uint32_t*>(workspace);
-  p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+  p.arrived = static_cast<uint32_t*>(a.workspace);
+  p.partial = reinterpret_cast<float*>(static_cast<char*>(a.workspace) +
                                        attn_counter_bytes(fp4::kv_attention_max_ctas(sms)));
-  p.B = B;
-  p.max_blocks = max_blocks;
+  p.B = a.B;
+  p.max_blocks = a.max_blocks;
   p.num_blocks = cache->num_blocks;
   p.block_log2 = block_log2(cache->block_size);
   p.kv_heads = cache->kv_heads;
   p.group = group;
   p.group_magic = (65536 + group - 1) / group;
-  p.q_len = q_len;
+  p.q_len = a.q_len;
   p.row_tiles = row_tiles;
   // (a window that no sequence is longer than is none: on the device differences of it and a position fit 32 bits)
-  p.window = window >= tokens ? 0 : window;
+  p.window = a.window >= tokens ? 0 : a.window;
   p.unit = 1;
   p.item_cost = fp4::kAttnItemCost;
   p.uncut = cache->head_dim > 128 ? fp4::kAttnUncut256 : fp4::kAttnUncut;
-  p.f16 = dtype == FP4GEMV_F16;
-  p.sm_scale = sm_scale;
+  p.f16 = a.dtype == FP4GEMV_F16;
+  p.sm_scale = a.sm_scale;
+  *out_row_units = row_units;
+  *out_sms = sms;
+  return FP4GEMV_OK;
+}
+
+// (the checks are done)
+static fp4gemv_status plain_attention(const AttentionCall& a, const fp4::KvAttnParams& base, int row_units, int sms,
+                                      cudaStream_t stream) {
+  const fp4gemv_kv_cache* const cache = a.cache;
   if (row_units == 4 && cache->head_dim == 128 && cache->format == FP4GEMV_KV_E4M3) {
+    fp4::KvAttnTcParams p = {};
+    static_cast<fp4::KvAttnParams&>(p) = base;
     const int64_t pages = static_cast<int64_t>(cache->num_blocks) * cache->kv_heads;
     if (!fp4::encode_pages_128(&p.k_map, cache->k_codes, cache->block_size, pages) ||
         !fp4::encode_pages_128(&p.v_map, cache->v_codes, cache->block_size, pages))
@@ -284,11 +314,44 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
     p.item_cost = fp4::kAttnTcItemCost;
     p.skip_tile = fp4::skipped_stage();
     fp4::count_launch();
-    return from_cuda(fp4::launch_kv_attention_tc(p, sms, pdl, stream));
+    return from_cuda(fp4::launch_kv_attention_tc(p, sms, a.pdl, stream));
   }
   fp4::count_launch();
-  return from_cuda(fp4::launch_kv_attention(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms, pdl,
-                                            stream));
+  return from_cuda(fp4::launch_kv_attention(base, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms,
+                                            a.pdl, stream));
+}
+
+fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype, int heads,
+                                    int q_len, const int32_t* block_table, int max_blocks, const int32_t* seq_lens,
+                                    int B, float sm_scale, int window, void* out, int64_t ldo, float* lse,
+                                    void* workspace, size_t workspace_bytes, int pdl, cudaStream_t stream) {
+  const AttentionCall a = {cache, q, ldq, dtype, heads, q_len, block_table, max_blocks, seq_lens, B, sm_scale, window,
+                           out, ldo, lse, workspace, workspace_bytes, pdl};
+  fp4::KvAttnParams p = {};
+  int row_units, sms;
+  const fp4gemv_status st = attention_params(a, &p, &row_units, &sms);
+  return st != FP4GEMV_OK ? st : plain_attention(a, p, row_units, sms, stream);
+}
+
+fp4gemv_status fp4gemv_kv_attention_sinks(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype,
+                                          int heads, int q_len, const int32_t* block_table, int max_blocks,
+                                          const int32_t* seq_lens, int B, float sm_scale, int window, int sinks,
+                                          void* out, int64_t ldo, float* lse, void* workspace, size_t workspace_bytes,
+                                          int pdl, cudaStream_t stream) {
+  if (sinks < 0) return FP4GEMV_ERR_INVALID_ARG;
+  if (sinks > (1 << 30)) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+  const AttentionCall a = {cache, q, ldq, dtype, heads, q_len, block_table, max_blocks, seq_lens, B, sm_scale, window,
+                           out, ldo, lse, workspace, workspace_bytes, pdl};
+  fp4::KvAttnMoreParams p = {};
+  int row_units, sms;
+  const fp4gemv_status st = attention_params(a, &p, &row_units, &sms);
+  if (st != FP4GEMV_OK) return st;
+  if (sinks == 0 || p.window == 0) return plain_attention(a, p, row_units, sms, stream);
+  p.sinks = sinks;
+  p.lead = (sinks + 15) / 16;
+  fp4::count_launch();
+  return from_cuda(fp4::launch_kv_attention_more(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms,
+                                                 pdl, stream));
 }
 
 fp4gemv_status fp4gemv_moe_route(const void* logits, int64_t ldl, int dtype, int M, int E, int topk, int scores,

@@ -33,6 +33,10 @@ int kv_attention_max_ctas(int sms);
 cudaError_t launch_kv_attention(const KvAttnParams& p, int dim, int int8, int row_units, int sms, int pdl,
                                 cudaStream_t stream);
 
+// ... with leading strips; row tiles of 32 for every head_dim but 256.
+cudaError_t launch_kv_attention_more(const KvAttnMoreParams& p, int dim, int int8, int row_units, int sms, int pdl,
+                                     cudaStream_t stream);
+
 // E4M3, head_dim 128, row tiles of 32.
 cudaError_t launch_kv_attention_tc(const KvAttnTcParams& p, int sms, int pdl, cudaStream_t stream);
 

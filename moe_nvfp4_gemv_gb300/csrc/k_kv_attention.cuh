@@ -95,6 +95,13 @@ struct KvAttnParams {
   float sm_scale;
 };
 
+// ... with first tokens that stay visible in a window: a sequence's items hold `lead` strips of its beginning, then those
+// of its window, with a gap between them that counts as no strips.
+struct KvAttnMoreParams : KvAttnParams {
+  int sinks;  // the first tokens that stay visible (0: none)
+  int lead;   // their strips
+};
+
 // ... of the kernel on the 5th-generation tensor core
 struct KvAttnTcParams : KvAttnParams {
   CUtensorMap k_map;  // [num_blocks kv_heads][block_size][128] bytes, boxes of a page, 128-byte swizzle
@@ -187,7 +194,7 @@ __device__ __forceinline__ uint32_t nan_lanes(uint32_t nan) {
 struct AttnPlace {
   int b, head, tile;  // sequence, KV head, row tile
   int strip, strips;  // the place in strips; the item's number of strips
-  int first;          // the sequence's first strip that any query sees (its token / 16)
+  int first;          // the sequence's first strip that any query sees (its token / 16); with leading strips, the gap
   int item;           // number of the item within the sequence
 };
 
@@ -212,7 +219,12 @@ __device__ __forceinline__ int attn_first_strip(const KvAttnParams& p, int n) {
   const int at = n - p.q_len;  // the first query's position
   return p.window > 0 && at >= p.window ? ((at - p.window + 1) >> 4) & -p.unit : 0;
 }
-__device__ __forceinline__ int attn_strips_of(const KvAttnParams& p, int n) {
+// ... with leading strips: the strips between them and the window
+__device__ __forceinline__ int attn_first_strip(const KvAttnMoreParams& p, int n) {
+  return max(attn_first_strip(static_cast<const KvAttnParams&>(p), n) - p.lead, 0);
+}
+template <class P>
+__device__ __forceinline__ int attn_strips_of(const P& p, int n) {
   return ((n + 15) >> 4) - attn_first_strip(p, n);
 }
 
@@ -223,8 +235,8 @@ __device__ __forceinline__ int attn_units(const KvAttnParams& p, int strips) { r
 // the sequences before hold in strips and in length on the line.  The share:
 // begin, end (strips), strips per share, an item's cost, and whether items are
 // cut into pieces by themselves.  places[0] and [2]: the share's begin.
-template <int kThreads>
-__device__ __forceinline__ void attn_plan(const KvAttnParams& p, int* strips_before, int* line_before, int* tokens,
+template <int kThreads, class P>
+__device__ __forceinline__ void attn_plan(const P& p, int* strips_before, int* line_before, int* tokens,
                                           int* plan_words, AttnPlace* places) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = p.kv_heads * p.row_tiles;
@@ -406,7 +418,8 @@ __device__ __forceinline__ void attn_empty(const KvAttnParams& p, const int* tok
 }
 
 // The place after an item: the next item's begin (there is one).
-__device__ __forceinline__ AttnPlace attn_next(const KvAttnParams& p, AttnPlace x, const int* strips_before,
+template <class P>
+__device__ __forceinline__ AttnPlace attn_next(const P& p, AttnPlace x, const int* strips_before,
                                                const int* tokens) {
   x.strip = 0;
   ++x.item;
@@ -651,16 +664,18 @@ struct AttnLayout {
 
 // NaN codes of tokens that some of an item's rows do not see, in a strip of V (`count` tokens, the first of them seen by
 // queries from `since` on): a weight of 0 does not silence them, so they give way to zeros, and the rows that do see their
-// token are noted in nan_dims for the segment's end.  By a warp, a lane for each 16 bytes.
-template <int kDim>
+// token are noted in nan_dims for the segment's end.  By a warp, a lane for each 16 bytes.  kMore: the strip's tokens
+// before `sinks` are outside no window.
+template <int kDim, bool kMore>
 __device__ __noinline__ void attn_quiet(uint32_t strip, int count, int since, int window, int q_len, int group, int row0,
-                                        int used, uint32_t (*nan_dims)[kDim / 32], int* nan_any) {
+                                        int used, uint32_t (*nan_dims)[kDim / 32], int* nan_any, int sinks) {
   using L = AttnLayout<kDim>;
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int i = lane; i < count * (kDim / 16); i += 32) {
     const int token = i / (kDim / 16), k = i - token * (kDim / 16), from = since + token;
-    if (from <= 0 && (window == 0 || from + window >= q_len)) continue;  // (all rows see it)
+    const bool stays = window == 0 || (kMore && token < sinks);
+    if (from <= 0 && (stays || from + window >= q_len)) continue;  // (all rows see it)
     const uint32_t at = strip + L::chunk(token, k);
     const uint4 chunk = lds128(at);
     uint32_t u[4] = {chunk.x, chunk.y, chunk.z, chunk.w};
@@ -673,7 +688,7 @@ __device__ __noinline__ void attn_quiet(uint32_t strip, int count, int since, in
       dims |= nan_lanes(nan) << (4 * j);
     }
     sts128(at, make_uint4(u[0], u[1], u[2], u[3]));
-    const int first = max(from, 0), last = window > 0 ? min(from + window, q_len) : q_len;  // its queries
+    const int first = max(from, 0), last = stays ? q_len : min(from + window, q_len);  // its queries
     for (int r = max(first * group - row0, 0); r < min(last * group - row0, used); ++r) {
       atomicOr(&nan_dims[r][k >> 1], dims << (16 * (k & 1)));
       *nan_any = 1;
@@ -703,8 +718,10 @@ struct AttnCfg {
   static constexpr int smem(int B) { return kSmem + (B + 1) * 12; }
 };
 
-template <int kDim, bool kInt8, int kN, int kRes>
-__global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_attention_kernel(const KvAttnParams p) {
+// kMore: with leading strips (KvAttnMoreParams).
+template <int kDim, bool kInt8, int kN, int kRes, bool kMore = false>
+__global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
+    kv_attention_kernel(const std::conditional_t<kMore, KvAttnMoreParams, KvAttnParams> p) {
   using C = AttnCfg<kDim, kN, kRes>;
   using L = AttnLayout<kDim>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -817,7 +834,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
         strip = off - item * s;
         head = item / p.row_tiles;
       }
-      strip += first_strip(tokens[b]);
+      if constexpr (kMore) strip += strip >= p.lead ? first_strip(tokens[b]) : 0;
+      else strip += first_strip(tokens[b]);
       const int per_page = p.block_log2 - 4;
       const int id = __ldg(p.table + static_cast<int64_t>(b) * p.max_blocks + (strip >> per_page));
       found = id >= 0 && id < p.num_blocks
@@ -870,13 +888,19 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
   float acc[kN][L::kTiles][4];  // dims by rows: thread's rows 2t, 2t + 1 of every tile of 8
   float m[kN][2], sum[kN][2];
   while (at < end) {
-    int seg_end, n, row0, tok0;  // tok0: the token at strip `at`
+    int seg_end, n, row0, tok0;  // tok0: the token at strip `at`; kMore: as if there were no gap,
+    int gap = 0;                 // ... which is that many tokens long
     {
       const AttnPlace c = places[which];
       seg_end = min(end, at + c.strips - c.strip);
       n = tokens[c.b];
       row0 = c.tile * C::kRows;
-      tok0 = (c.first + c.strip) << 4;
+      if constexpr (kMore) {
+        tok0 = c.strip << 4;
+        gap = c.first << 4;
+      } else {
+        tok0 = (c.first + c.strip) << 4;
+      }
       if (tid == 0 && seg_end < end) {  // the next item (read behind the barriers of the joining)
         places[which ^ 1] = attn_next(p, c, strips_before, tokens);
       }
@@ -909,6 +933,11 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
     const int tokens_all = n - p.q_len + 1;                          // every row sees those before this one
     const int tokens_low = p.window > 0 ? max(0, n - p.window) : 0;  // ... from this one on
 
+    // the token at place `tok` of the strips that there are
+    auto real = [&](int tok) -> int {
+      if constexpr (kMore) return tok >= p.lead << 4 ? tok + gap : tok;
+      else return tok;
+    };
     auto after = [](int stage) { return stage + 1 == C::kStages ? 0 : stage + 1; };
     auto before = [](int stage) { return stage == 0 ? C::kStages - 1 : stage - 1; };
     // S^T += K Q^T of two k-steps of a strip; w: its K words of a block, of rows g and g + 8
@@ -982,18 +1011,22 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
     const bool parts = !kInt8 && (p.q_len > 1 || p.window > 0);
     for (int stop = tok_end; tok < tok_end;) {
       if (parts) {
-        stop = min(tok_end, tokens_all - 15);
-        if (tok < tokens_low || tok >= stop) {
+        stop = min(tok_end, tokens_all - gap - 15);  // (a gap ends before the first query's position)
+        if (real(tok) < tokens_low || tok >= stop) {
           if (!C::kAhead) {
             asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
             __syncwarp();
           }
-          attn_quiet<kDim>(ring + stage * C::kStageBytes + L::kStripBytes, min(16, n - tok), tok - (n - p.q_len), p.window,
-                           p.q_len, p.group, row0, min(C::kRows, rows - row0), nan_dims, &nan_any);
+          int sinks = 0;
+          if constexpr (kMore) sinks = p.sinks - real(tok);
+          attn_quiet<kDim, kMore>(ring + stage * C::kStageBytes + L::kStripBytes, min(16, n - real(tok)),
+                                  real(tok) - (n - p.q_len), p.window, p.q_len, p.group, row0,
+                                  min(C::kRows, rows - row0), nan_dims, &nan_any, sinks);
           stop = tok + 1;
         }
       }
       for (; tok < stop; tok += C::kWarps * 16) {
+        const int here = real(tok);
         const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + L::kStripBytes;
         if (!C::kAhead) {
           asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
@@ -1013,7 +1046,12 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(kb + 2 * L::kStripBytes));
         const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
         const float inv_vs = attn_ex2(-lv) * kAttnUnlift;  // (sums stay those of weights up to 1)
-        const bool masked = tok + 16 > tokens_all || tok < tokens_low;
+        bool masked = here + 16 > tokens_all || here < tokens_low;
+        bool some = here >= tokens_low;  // every row sees some of the strip
+        if constexpr (kMore) {
+          masked = here + 16 > tokens_all || (here < tokens_low && here + 16 > p.sinks);
+          some = some || here < min(p.sinks, tokens_all);
+        }
         // Exponents against the running maxima, in the scores' place; against 0 while the warp has seen no strip that
         // every row sees some of (`fresh`: a row's first maximum is only known then).  Where they are masked, too high
         // or fresh, the maxima are taken and the exponents made again.
@@ -1039,8 +1077,13 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
                 const int row = min(row0 + nt * 8 + 2 * t + h, rows - 1);
                 const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
                 const int see_from = p.window > 0 ? see_to - p.window : 0;
-                if (tok + g >= see_to || tok + g < see_from) r0 = -__builtin_huge_valf();
-                if (tok + 8 + g >= see_to || tok + 8 + g < see_from) r1 = -__builtin_huge_valf();
+                bool out0 = here + g < see_from, out1 = here + 8 + g < see_from;
+                if constexpr (kMore) {
+                  out0 = out0 && here + g >= p.sinks;
+                  out1 = out1 && here + 8 + g >= p.sinks;
+                }
+                if (here + g >= see_to || out0) r0 = -__builtin_huge_valf();
+                if (here + 8 + g >= see_to || out1) r1 = -__builtin_huge_valf();
               }
               float top = fmaxf(r0, r1);
 #pragma unroll
@@ -1057,7 +1100,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
               sc[nt][h] = r0 - mn;
               sc[nt][2 + h] = r1 - mn;
             }
-          fresh = fresh && tok < tokens_low;
+          fresh = fresh && !some;
         }
         uint32_t pb[kN][2];
 #pragma unroll
@@ -1082,7 +1125,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
           for (int blk = 0; blk < L::kBlocks; ++blk) {
             uint32_t wk[2][L::kWords], wv[4][L::kVWords];
             k_load(next_kb, blk, wk);
-            v_load(vb, blk, n - tok, wv);
+            v_load(vb, blk, n - here, wv);
 #pragma unroll
             for (int k = 0; k < L::kVWords; ++k) {
               score(wk, blk, 2 * k, sc);
@@ -1093,7 +1136,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes) kv_at
 #pragma unroll
           for (int blk = 0; blk < L::kBlocks; ++blk) {
             uint32_t w[4][L::kVWords];
-            v_load(vb, blk, n - tok, w);
+            v_load(vb, blk, n - here, w);
 #pragma unroll
             for (int k = 0; k < L::kVWords; ++k) weigh(w, blk, k, pb);
           }

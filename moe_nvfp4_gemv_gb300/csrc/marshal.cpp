@@ -28,6 +28,7 @@ namespace {
 
 decltype(&fp4gemv_kv_append) g_append;
 decltype(&fp4gemv_kv_attention) g_attention;
+decltype(&fp4gemv_kv_attention_sinks) g_attention_sinks;
 decltype(&fp4gemv_kv_read) g_read;
 decltype(&fp4gemv_add_norm) g_add_norm;
 decltype(&fp4gemv_moe_route) g_route;
@@ -281,43 +282,79 @@ int64_t token_stride(const at::Tensor& t, const char* name) {
   return n > 1 ? t.stride(1) : B > 1 ? t.stride(0) : heads * dim;
 }
 
+// The arguments of an attention call as the C calls take them; empty: there is nothing to do.
+struct Attention {
+  const fp4gemv_kv_cache* cache;
+  const void* q;
+  int64_t ldq, ldo, index;
+  int dtype, heads, q_len, B, max_blocks, window, pdl;
+  const int32_t *table, *lens;
+  float sm_scale;
+  void *out, *workspace;
+  float* lse;
+  size_t bytes;
+  bool empty, large;
+};
+// a: cache, device, head_dim, q, block_table, seq_lens, sm_scale, window, out, lse, workspace, pdl
+Attention attention_of(PyObject* const* a) {
+  const auto* cache = reinterpret_cast<const fp4gemv_kv_cache*>(integer(a[0]));
+  const int64_t index = integer(a[1]), D = integer(a[2]);
+  const at::Tensor &q = tensor(a[3], "q"), &table = tensor(a[4], "block_table"), &lens = tensor(a[5], "seq_lens"),
+                   &out = tensor(a[8], "out"), &workspace = tensor(a[10], "workspace");
+  int B, max_blocks;
+  sequences(table, lens, index, &B, &max_blocks);
+  const int dtype = half_code(q);
+  if (dtype < 0 || q.dim() != 4 || q.size(0) != B || q.size(3) != D || !q.is_cuda() || q.get_device() != index)
+    refuse("q must be a bf16 or f16 [%d, q_len, heads, %d] tensor on the cache's device", B, static_cast<int>(D));
+  if (out.scalar_type() != q.scalar_type() || out.sizes() != q.sizes() || !out.is_cuda() || out.get_device() != index)
+    refuse("out must have q's shape, type and device");
+  const int64_t ldq = token_stride(q, "q"), ldo = token_stride(out, "out"), q_len = q.size(1), heads = q.size(2);
+  float* lse = nullptr;
+  if (a[9] != Py_None) {
+    const at::Tensor& t = tensor(a[9], "lse");
+    if (t.numel() != B * q_len * heads || !plain(t, at::kFloat, index))
+      refuse("lse must be a contiguous fp32 [%d, %d, %d] tensor on the cache's device", B, static_cast<int>(q_len),
+             static_cast<int>(heads));
+    lse = address_as<float>(t);
+  }
+  if (!workspace.is_cuda() || workspace.get_device() != index || !workspace.is_contiguous())
+    refuse("workspace must be a contiguous tensor on the cache's device");
+  const float sm_scale = static_cast<float>(real(a[6]));
+  const int window = int32(a[7]), pdl = flag(a[11]);
+  const void* pq = address(q);
+  void *po = address_as<void>(out), *pw = address_as<void>(workspace);
+  const int32_t *pt = address_as<int32_t>(table), *pl = address_as<int32_t>(lens);
+  const size_t bytes = workspace.nbytes();
+  return {cache, pq, ldq, ldo, index, dtype, static_cast<int>(heads), static_cast<int>(q_len), B, max_blocks, window, pdl,
+          pt, pl, sm_scale, po, pw, lse, bytes, B == 0, q_len > INT_MAX || heads > INT_MAX};
+}
+
 // kv_attention(cache, device, head_dim, q, block_table, seq_lens, sm_scale, window, out, lse, workspace, pdl)
 PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> int {
-    const auto* cache = reinterpret_cast<const fp4gemv_kv_cache*>(integer(a[0]));
-    const int64_t index = integer(a[1]), D = integer(a[2]);
-    const at::Tensor &q = tensor(a[3], "q"), &table = tensor(a[4], "block_table"), &lens = tensor(a[5], "seq_lens"),
-                     &out = tensor(a[8], "out"), &workspace = tensor(a[10], "workspace");
-    int B, max_blocks;
-    sequences(table, lens, index, &B, &max_blocks);
-    const int dtype = half_code(q);
-    if (dtype < 0 || q.dim() != 4 || q.size(0) != B || q.size(3) != D || !q.is_cuda() || q.get_device() != index)
-      refuse("q must be a bf16 or f16 [%d, q_len, heads, %d] tensor on the cache's device", B, static_cast<int>(D));
-    if (out.scalar_type() != q.scalar_type() || out.sizes() != q.sizes() || !out.is_cuda() || out.get_device() != index)
-      refuse("out must have q's shape, type and device");
-    const int64_t ldq = token_stride(q, "q"), ldo = token_stride(out, "out"), q_len = q.size(1), heads = q.size(2);
-    float* lse = nullptr;
-    if (a[9] != Py_None) {
-      const at::Tensor& t = tensor(a[9], "lse");
-      if (t.numel() != B * q_len * heads || !plain(t, at::kFloat, index))
-        refuse("lse must be a contiguous fp32 [%d, %d, %d] tensor on the cache's device", B, static_cast<int>(q_len),
-               static_cast<int>(heads));
-      lse = address_as<float>(t);
-    }
-    if (!workspace.is_cuda() || workspace.get_device() != index || !workspace.is_contiguous())
-      refuse("workspace must be a contiguous tensor on the cache's device");
-    const float sm_scale = static_cast<float>(real(a[6]));
-    const int window = int32(a[7]), pdl = flag(a[11]);
-    if (B == 0) return FP4GEMV_OK;
-    if (q_len > INT_MAX || heads > INT_MAX) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
-    const void* pq = address(q);
-    void *po = address_as<void>(out), *pw = address_as<void>(workspace);
-    const int32_t *pt = address_as<int32_t>(table), *pl = address_as<int32_t>(lens);
-    const size_t bytes = workspace.nbytes();
-    const cudaStream_t stream = stream_of(index);
+    const Attention c = attention_of(a);
+    if (c.empty) return FP4GEMV_OK;
+    if (c.large) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+    const cudaStream_t stream = stream_of(c.index);
     return unlocked([&] {
-      return g_attention(cache, pq, ldq, dtype, static_cast<int>(heads), static_cast<int>(q_len), pt, max_blocks, pl, B,
-                         sm_scale, window, po, ldo, lse, pw, bytes, pdl, stream);
+      return g_attention(c.cache, c.q, c.ldq, c.dtype, c.heads, c.q_len, c.table, c.max_blocks, c.lens, c.B, c.sm_scale,
+                         c.window, c.out, c.ldo, c.lse, c.workspace, c.bytes, c.pdl, stream);
+    });
+  });
+}
+
+// kv_attention_sinks(kv_attention's, sinks)
+PyObject* kv_attention_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> int {
+    const Attention c = attention_of(a);
+    const int sinks = int32(a[12]);
+    if (c.empty) return FP4GEMV_OK;
+    if (c.large) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.index));
+    const cudaStream_t stream = stream_of(c.index);
+    return unlocked([&] {
+      return g_attention_sinks(c.cache, c.q, c.ldq, c.dtype, c.heads, c.q_len, c.table, c.max_blocks, c.lens, c.B,
+                               c.sm_scale, c.window, sinks, c.out, c.ldo, c.lse, c.workspace, c.bytes, c.pdl, stream);
     });
   });
 }
@@ -424,11 +461,12 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind_more(kv_read, add_norm): the others'
+// bind_more(kv_read, add_norm, kv_attention_sinks): the others'
 PyObject* bind_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 2, [&]() -> int {
+  return guarded(n, 3, [&]() -> int {
     g_read = reinterpret_cast<decltype(g_read)>(integer(a[0]));
     g_add_norm = reinterpret_cast<decltype(g_add_norm)>(integer(a[1]));
+    g_attention_sinks = reinterpret_cast<decltype(g_attention_sinks)>(integer(a[2]));
     return 0;
   });
 }
@@ -440,7 +478,8 @@ PyMethodDef method(const char* name) {
 PyMethodDef g_methods[] = {method<bind>("bind"),           method<kv_append>("kv_append"),
                            method<kv_attention>("kv_attention"), method<moe_route>("moe_route"),
                            method<token_logprobs>("token_logprobs"), method<bind_more>("bind_more"),
-                           method<kv_read>("kv_read"),     method<add_norm>("add_norm"), {nullptr, nullptr, 0, nullptr}};
+                           method<kv_read>("kv_read"),     method<add_norm>("add_norm"),
+                           method<kv_attention_sinks>("kv_attention_sinks"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

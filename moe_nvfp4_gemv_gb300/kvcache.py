@@ -32,6 +32,7 @@ FORMATS = {"e4m3": 0, "int8": 1}
 _F32 = torch.float32
 _append = _marshal.kv_append
 _attend = _marshal.kv_attention
+_attend_sinks = _marshal.kv_attention_sinks
 _read = _marshal.kv_read
 
 
@@ -159,12 +160,12 @@ class KvCache8:
 
     def attend(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, sm_scale: float | None = None,
                window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-               workspace: torch.Tensor | None = None, pdl: bool = True) -> torch.Tensor:
+               workspace: torch.Tensor | None = None, pdl: bool = True, sinks: int = 0) -> torch.Tensor:
         """Attention of q (bf16 or f16 [B, q_len, heads, head_dim], the newest
         q_len tokens of every sequence, already appended; tokens at one stride
         that is a multiple of 8, heads contiguous).  Query i sees tokens up to
-        its own position, the last ``window`` of them if that is not 0; one
-        that sees none gives zeros.  ``sm_scale`` defaults to 1 /
+        its own position, the last ``window`` of them if that is not 0 and the
+        sequence's first ``sinks`` as well; one that sees none gives zeros.  ``sm_scale`` defaults to 1 /
         sqrt(head_dim); ``lse``: fp32 [B, q_len, heads] to receive the natural
         log of the softmax's sums; ``workspace``: uint8, zero-filled once, of
         attention_workspace_bytes(head_dim), the stream's own by default
@@ -176,8 +177,16 @@ class KvCache8:
             workspace = _workspaces.get((self._index, stream, self.head_dim))
             if workspace is None:
                 workspace = attention_workspace(self.device, self.head_dim, stream)
-        status = _attend(self._handle, self._index, self.head_dim, q, block_table, seq_lens,
-                         self._sm_scale if sm_scale is None else sm_scale, window, out, lse, workspace, pdl)
+        if sm_scale is None:
+            sm_scale = self._sm_scale
+        if sinks:
+            status = _attend_sinks(self._handle, self._index, self.head_dim, q, block_table, seq_lens, sm_scale, window,
+                                   out, lse, workspace, pdl, sinks)
+            if status:
+                raise Fp4GemvError(status, "fp4gemv_kv_attention_sinks")
+            return out
+        status = _attend(self._handle, self._index, self.head_dim, q, block_table, seq_lens, sm_scale, window, out, lse,
+                         workspace, pdl)
         if status:
             raise Fp4GemvError(status, "fp4gemv_kv_attention")
         return out

@@ -1,0 +1,174 @@
+"""Attention with a sliding window and first tokens that stay visible
+(KvCache8.attend with ``sinks``) on the GPU, against 64 bits.
+
+Tolerances are those of test_gpu_kv_cache.py (its docstring); the mass that the
+rounding of weights acts on is that of the tokens seen."""
+import math
+
+import pytest
+import torch
+
+import decode_ref as ref
+from test_gpu_kv_cache import DEV, TYPES, fp4, gen, kv, make_table, on_gpu, random_cache, scaled  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def attention64(q, c, table, lens, fmt, sm_scale, window, sinks):
+    """(out, lse, mass, largest score) in 64 bits, as decode_ref.attention, of the tokens that the masks leave."""
+    B, n, H, D = q.shape
+    kv_heads, block = c["k_codes"].shape[1:3]
+    g = H // kv_heads
+    out = torch.zeros(B, n, H, D, dtype=torch.float64, device=DEV)
+    mass, lse, peak = torch.zeros_like(out), torch.full((B, n, H), -math.inf, dtype=torch.float64, device=DEV), 0.0
+    c = {name: t.to(DEV) for name, t in c.items()}
+    for b, length in enumerate(lens):
+        for i in range(n):
+            p = length - n + i
+            t = torch.arange(max(0, p + 1))
+            if window:
+                t = t[(t > p - window) | (t < sinks)]
+            if not len(t):
+                continue
+            page, slot = table[b][t // block].long().to(DEV), (t % block).to(DEV)
+            k, v = (ref.decode(c[x + "_codes"][page, :, slot], fmt).double() * c[x + "_scale"][page].double()[..., None]
+                    for x in ("k", "v"))
+            x = torch.einsum("hgd,thd->hgt", q[b, i].double().view(kv_heads, g, D), k) * sm_scale
+            peak = max(peak, float(x.abs().nan_to_num(0).max()))
+            w = torch.softmax(x, -1)
+            out[b, i] = torch.einsum("hgt,thd->hgd", w, v).reshape(H, D)
+            mass[b, i] = torch.einsum("hgt,thd->hgd", w, v.abs()).reshape(H, D)
+            lse[b, i] = torch.logsumexp(x, -1).reshape(H)
+    return out, lse, mass, peak
+
+
+def check(kv, q, c, table, lens, fmt, window, sinks, sm_scale=None, nans=False):
+    cache = on_gpu(kv, c, fmt)
+    tab, n_len = table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    lse = torch.full(q.shape[:3], 7.0, dtype=torch.float32, device=DEV)
+    out = cache.attend(q, tab, n_len, window=window, sinks=sinks, lse=lse, sm_scale=sm_scale)
+    again = cache.attend(q, tab, n_len, window=window, sinks=sinks, sm_scale=sm_scale)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16)), "two calls differ"
+    want, want_lse, mass, peak = attention64(q, c, table, lens, fmt, sm_scale or 1 / math.sqrt(q.shape[-1]), window, sinks)
+    assert torch.equal(out.isnan(), want.isnan())
+    assert bool(want.isnan().any()) == nans
+    n = max(max(lens), 1)
+    vmax = float(ref.decode(c["v_codes"], fmt).abs().nan_to_num(0).amax() * c["v_scale"].nan_to_num(0, 0, 0).amax())
+    d = 2.0 ** -10 * mass + n * 2.0 ** -25 * vmax
+    low, high = (want - d).to(q.dtype), (want + d).to(q.dtype)
+    outside = ~((out >= low) & (out <= high)) & ~want.isnan()
+    assert not outside.any(), f"{int(outside.sum())} values outside"
+    empty = torch.isinf(want_lse)
+    assert torch.equal(torch.isinf(lse) & (lse < 0), empty) and (out[empty] == 0).all()
+    tol = 2.0 ** -19 * (1 + peak) + (16 + n / 128) * 2.0 ** -23
+    assert ((lse.double() - want_lse)[~empty].abs().nan_to_num(0) <= tol).all()
+
+
+@pytest.mark.parametrize("dim,block,group,fmt,dtype", [
+    (64, 16, 1, "e4m3", "bf16"), (96, 32, 3, "int8", "f16"), (128, 64, 4, "e4m3", "f16"), (128, 16, 8, "int8", "bf16"),
+    (256, 128, 2, "e4m3", "bf16"), (128, 128, 24, "e4m3", "bf16"), (64, 64, 31, "int8", "bf16")])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (1, 16), (16, 4), (20, 17), (100, 4), (64, 130), (300, 33), (2000, 5)])
+def test_sinks(kv, dim, block, group, fmt, dtype, window, sinks):
+    lens = [0, 1, 2, 5, 16, 17, 33, 100, 129, 333, 700, 1500]
+    g = gen(dim + window + sinks)
+    table, pages = make_table(lens, block, g)
+    c = scaled(random_cache(pages, 2, block, dim, g, 1.0), fmt)
+    for q_len in (1, 5) if group < 24 else (1,):
+        q = torch.randn(len(lens), q_len, 2 * group, dim, generator=g).to(TYPES[dtype]).to(DEV)
+        check(kv, q, c, table, lens, fmt, window, sinks)
+
+
+@pytest.mark.parametrize("lens,heads,kv_heads,q_len,window,sinks", [
+    ([9000], 8, 8, 1, 1024, 4), ([70000], 4, 1, 1, 30000, 700), ([5000, 4000, 3000], 16, 2, 2, 2500, 64),
+    ([3000] * 40, 8, 4, 1, 500, 4), ([257] * 130, 4, 2, 3, 60, 20)])
+def test_sinks_of_items_in_pieces(kv, lens, heads, kv_heads, q_len, window, sinks):
+    """Items cut by many CTAs, the gap within a share and at its ends."""
+    g = gen(len(lens) + heads)
+    table, pages = make_table(lens, 64, g)
+    c = scaled(random_cache(pages, kv_heads, 64, 128, g, 1.0), "e4m3")
+    q = torch.randn(len(lens), q_len, heads, 128, generator=g).to(torch.bfloat16).to(DEV)
+    check(kv, q, c, table, lens, "e4m3", window, sinks)
+
+
+@pytest.mark.parametrize("group,dim,q_len", [(2, 128, 4), (5, 64, 3), (3, 256, 5), (7, 96, 4), (1, 128, 16)])
+@pytest.mark.parametrize("window,sinks", [(1, 3), (20, 18), (130, 5)])
+def test_sinks_nan_values(kv, group, dim, q_len, window, sinks):
+    """NaN values among the first tokens, behind them, at the window's begin and at the newest tokens: in the rows that see
+    them alone.  Short sequences' first tokens are newer than some queries."""
+    lens = [1, 3, 5, 17, 40, 133, 300, 1000]
+    g = gen(dim + q_len + sinks)
+    table, pages = make_table(lens, 16, g)
+    c = scaled(random_cache(pages, 2, 16, dim, g, 1.0), "e4m3")
+    for b, n in enumerate(lens):
+        first = n - q_len + 1 - window
+        for i, t in enumerate((n - 1, n - 2, first, first - 1, sinks, sinks + 1, sinks - 1)):
+            if 0 <= t < n and (t != sinks - 1 or b % 2):
+                code = c["v_codes"][int(table[b, t // 16])]
+                code[b % 2, t % 16, 3 + 7 * i] = 0x7F
+    q = torch.randn(len(lens), q_len, 2 * group, dim, generator=g).to(torch.float16).to(DEV)
+    check(kv, q, c, table, lens, "e4m3", window, sinks, nans=True)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_sinks_pages_between_are_not_read(kv, fp4, fmt):
+    """Pages of tokens that no query sees may be anyone's: other ids, no ids at all, NaN scales."""
+    block, window, sinks, lens = 16, 50, 20, [400, 161, 90]
+    g = gen(4)
+    table, pages = make_table(lens, block, g)
+    c = scaled(random_cache(pages, 2, block, 64, g, 1.0), fmt)
+    q = torch.randn(3, 2, 4, 64, generator=g).to(torch.bfloat16).to(DEV)
+    cache, n_len = on_gpu(kv, c, fmt), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    want = cache.attend(q, table.to(DEV), n_len, window=window, sinks=sinks)
+    for b, n in enumerate(lens):
+        for j in range(-(-sinks // block), max(0, n - 2 - window + 1) // block):
+            cache.v_scale[int(table[b, j])] = math.nan
+            table[b, j] = (-1, 1 << 30)[j % 2]
+    got = cache.attend(q, table.to(DEV), n_len, window=window, sinks=sinks)
+    assert torch.equal(got, want) and fp4.get_device_error() == 0
+
+
+def test_sinks_leave_other_calls_alone(kv):
+    """No window, a window past every length, no sinks: the results of the calls without."""
+    lens = [300, 20, 0]
+    g = gen(6)
+    table, pages = make_table(lens, 32, g)
+    c = scaled(random_cache(pages, 1, 32, 128, g, 1.0), "e4m3")
+    cache, tab, n = on_gpu(kv, c, "e4m3"), table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for heads in (4, 20):
+        q = torch.randn(3, 1, heads, 128, generator=g).to(torch.bfloat16).to(DEV)
+        want = cache.attend(q, tab, n)
+        for kw in (dict(sinks=5), dict(window=1 << 30, sinks=5), dict(window=400, sinks=3), dict(window=100, sinks=400),
+                   dict(window=10, sinks=1 << 30)):
+            got = cache.attend(q, tab, n, **kw)
+            if kw.get("window", 0) in (0, 400, 1 << 30):
+                assert torch.equal(got, want)
+            else:  # every token is seen all the same; another kernel's order of sums
+                assert (got.float() - want.float()).abs().max() <= 2.0 ** -6
+    with pytest.raises(RuntimeError):
+        cache.attend(q, tab, n, window=5, sinks=-1)
+    with pytest.raises(RuntimeError):
+        cache.attend(q, tab, n, window=5, sinks=(1 << 30) + 1)
+    with pytest.raises(RuntimeError):
+        cache.attend(q, tab, n, window=-1, sinks=2)
+
+
+def test_sinks_captured(kv):
+    """A captured call follows lengths that grow past the window."""
+    B, window, sinks = 4, 64, 8
+    g = gen(12)
+    table, pages = make_table([600] * B, 16, g)
+    c = scaled(random_cache(pages, 2, 16, 128, g, 1.0), "int8")
+    q = torch.randn(B, 1, 8, 128, generator=g).to(torch.bfloat16).to(DEV)
+    cache, tab, n = on_gpu(kv, c, "int8"), table.to(DEV), torch.tensor([1, 60, 72, 100], dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = cache.attend(q, tab, n, window=window, sinks=sinks)
+    for lens in ([1, 60, 72, 100], [65, 80, 0, 599], [600, 73, 81, 15]):
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, cache.attend(q, tab, n, window=window, sinks=sinks))
+        check(kv, q, c, table, lens, "int8", window, sinks)
