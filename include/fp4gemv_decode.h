@@ -1,8 +1,9 @@
 /*
  * fp4gemv_decode.h -- the decode step's operators around the products of
  * fp4gemv.h: a paged key/value cache held in 8 bits (append, attention,
- * also with first tokens that stay visible in a window, reading it back), the
- * residual stream with its norms, routing of tokens to experts (what fp4gemv_moe_gate_up takes as ids and
+ * also with first tokens that stay visible in a window or with a beginning that
+ * the sequences share, and reading it back), the residual stream with its
+ * norms, routing of tokens to experts (what fp4gemv_moe_gate_up takes as ids and
  * fp4gemv_moe_down_combine as tw), and the log probabilities of the answer.
  *
  * The conventions of fp4gemv.h hold: device pointers owned by the caller,
@@ -136,6 +137,33 @@ fp4gemv_status fp4gemv_kv_attention_sinks(const fp4gemv_kv_cache* cache, const v
                                           const int32_t* seq_lens, int B, float sm_scale, int window, int sinks,
                                           void* out, int64_t ldo, float* lse, void* workspace, size_t workspace_bytes,
                                           int pdl, cudaStream_t stream);
+
+/* Bytes of fp4gemv_kv_attention_shared's scratch on the current device, 0 for
+ * sizes that the call refuses.  It needs no initialisation and holds nothing
+ * between calls; calls that may run concurrently must not share it. */
+size_t fp4gemv_kv_attention_shared_scratch_bytes(int kv_heads, int head_dim, int heads, int q_len, int B);
+
+/* fp4gemv_kv_attention (window = 0) of sequences that begin with the same
+ * tokens, that beginning read and multiplied once for all of them.
+ * prefix_len int32 [1], device: how many first tokens are the same.  Their
+ * whole pages hold the same for every sequence of the call that is not empty
+ * (usually they are the same pages); what is on them is read through the first
+ * such sequence's row of block_table alone, the rest through each one's own.
+ * How many tokens are taken together is prefix_len rounded down to a multiple
+ * of 128, less where a sequence's first query stands before that; none is not an
+ * error, nor is a negative prefix_len.  Two launches.
+ * scratch: 16-byte aligned, fp4gemv_kv_attention_shared_scratch_bytes; the
+ * workspace is fp4gemv_kv_attention's.
+ * Numerics as fp4gemv_kv_attention's of up to 16 rows: exact f16 operands,
+ * probabilities rounded to f16, sums fp32.
+ * Shapes as fp4gemv_kv_attention; kv_heads * (B * q_len * heads / kv_heads
+ *   rows in blocks of 128) * (max_blocks * block_size / 64) at most 2^30. */
+fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype,
+                                           int heads, int q_len, const int32_t* block_table, int max_blocks,
+                                           const int32_t* seq_lens, int B, const int32_t* prefix_len, float sm_scale,
+                                           void* out, int64_t ldo, float* lse, void* workspace,
+                                           size_t workspace_bytes, void* scratch, size_t scratch_bytes, int pdl,
+                                           cudaStream_t stream);
 
 /* The last tokens of B sequences out of the cache: rows cu[b] .. cu[b + 1] of
  * k and v (cu int32 [B + 1] device, not decreasing, within 0 .. T), or T / B

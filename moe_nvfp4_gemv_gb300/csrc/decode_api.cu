@@ -6,6 +6,7 @@
 
 #include "decode_launch.h"
 #include "fp4gemv_decode.h"
+#include "k_kv_prefix.cuh"
 
 namespace {
 
@@ -223,7 +224,27 @@ struct AttentionCall {
   void* workspace;
   size_t workspace_bytes;
   int pdl;
+  // of sequences that share a beginning
+  bool shared;
+  const int32_t* prefix_len;
+  void* scratch;
+  size_t scratch_bytes;
 };
+
+// Blocks of 128 rows of a KV head, items of the beginning's line of a KV head, and the pieces that they come to at most.
+static int64_t shared_blocks(int64_t rows) { return (rows + 127) / 128; }
+static int64_t shared_items(int64_t rows, int dim) {
+  const int slots = fp4::kv_prefix_slots(dim);
+  return (shared_blocks(rows) + slots - 1) / slots;
+}
+// [tokens taken together | (m, sum of weights) of every row | sums]
+static size_t shared_ml_bytes(int64_t pieces, int dim) {
+  return static_cast<size_t>(pieces) * fp4::kv_prefix_slots(dim) * 128 * 8;
+}
+static size_t shared_scratch_bytes(int kv_heads, int dim, int64_t rows, int sms) {
+  const int64_t pieces = sms + kv_heads * shared_items(rows, dim);
+  return 16 + shared_ml_bytes(pieces, dim) * (1 + dim / 2);
+}
 
 // Fills p, *row_units and *sms.
 static fp4gemv_status attention_params(const AttentionCall& a, fp4::KvAttnParams* out_p, int* out_row_units, int* out_sms) {
@@ -253,15 +274,22 @@ static fp4gemv_status attention_params(const AttentionCall& a, fp4::KvAttnParams
       (static_cast<double>(tokens) / 16 + fp4::kAttnTcItemCost + 8) * a.B * cache->kv_heads * row_tiles >= 1.2e9 ||
       static_cast<double>(cache->num_blocks) * cache->kv_heads * (cache->block_size / 16) >= 2147483647.0)
     return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+  const int64_t all_rows = static_cast<int64_t>(a.B) * rows;
+  if (a.shared && static_cast<double>(cache->kv_heads) * shared_blocks(all_rows) * (tokens / 64 + 1) > (1 << 30))
+    return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
   if (crooked || !aligned(a.q, 16) || !aligned(a.out, 16) || a.ldq % 8 != 0 || a.ldo % 8 != 0 || !aligned(a.lse, 4) ||
-      !aligned(a.block_table, 4) || !aligned(a.seq_lens, 4) || !aligned(a.workspace, 16))
+      !aligned(a.block_table, 4) || !aligned(a.seq_lens, 4) || !aligned(a.workspace, 16) || !aligned(a.prefix_len, 4) ||
+      !aligned(a.scratch, 16))
     return FP4GEMV_ERR_MISALIGNED;
   if (nulls || !a.q || !a.out || !a.block_table || !a.seq_lens || !a.workspace) return FP4GEMV_ERR_INVALID_ARG;
+  if (a.shared && (!a.prefix_len || !a.scratch)) return FP4GEMV_ERR_INVALID_ARG;
   uint32_t* err = nullptr;
   int sms = 0;
   st = fp4::current_device_state(&err, &sms);
   if (st != FP4GEMV_OK) return st;
   if (a.workspace_bytes < fp4gemv_kv_attention_workspace_bytes(cache->head_dim)) return FP4GEMV_ERR_INVALID_ARG;
+  if (a.shared && a.scratch_bytes < shared_scratch_bytes(cache->kv_heads, cache->head_dim, all_rows, sms))
+    return FP4GEMV_ERR_INVALID_ARG;
   fp4::KvAttnParams& p = *out_p;
   p.k_codes = cache->k_codes;
   p.v_codes = cache->v_codes;
@@ -326,7 +354,7 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
                                     int B, float sm_scale, int window, void* out, int64_t ldo, float* lse,
                                     void* workspace, size_t workspace_bytes, int pdl, cudaStream_t stream) {
   const AttentionCall a = {cache, q, ldq, dtype, heads, q_len, block_table, max_blocks, seq_lens, B, sm_scale, window,
-                           out, ldo, lse, workspace, workspace_bytes, pdl};
+                           out, ldo, lse, workspace, workspace_bytes, pdl, false, nullptr, nullptr, 0};
   fp4::KvAttnParams p = {};
   int row_units, sms;
   const fp4gemv_status st = attention_params(a, &p, &row_units, &sms);
@@ -341,7 +369,7 @@ fp4gemv_status fp4gemv_kv_attention_sinks(const fp4gemv_kv_cache* cache, const v
   if (sinks < 0) return FP4GEMV_ERR_INVALID_ARG;
   if (sinks > (1 << 30)) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
   const AttentionCall a = {cache, q, ldq, dtype, heads, q_len, block_table, max_blocks, seq_lens, B, sm_scale, window,
-                           out, ldo, lse, workspace, workspace_bytes, pdl};
+                           out, ldo, lse, workspace, workspace_bytes, pdl, false, nullptr, nullptr, 0};
   fp4::KvAttnMoreParams p = {};
   int row_units, sms;
   const fp4gemv_status st = attention_params(a, &p, &row_units, &sms);
@@ -352,6 +380,70 @@ fp4gemv_status fp4gemv_kv_attention_sinks(const fp4gemv_kv_cache* cache, const v
   fp4::count_launch();
   return from_cuda(fp4::launch_kv_attention_more(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms,
                                                  pdl, stream));
+}
+
+size_t fp4gemv_kv_attention_shared_scratch_bytes(int kv_heads, int head_dim, int heads, int q_len, int B) {
+  if (!dim_ok(head_dim) || kv_heads < 1 || kv_heads > 65535 || heads < 1 || heads % kv_heads != 0 ||
+      heads / kv_heads > FP4GEMV_KV_MAX_GROUP || q_len < 1 || q_len > FP4GEMV_KV_MAX_QLEN || B < 1 ||
+      B > FP4GEMV_KV_MAX_BATCH)
+    return 0;
+  int sms = 0;
+  if (fp4::current_device_state(nullptr, &sms) != FP4GEMV_OK) return 0;
+  return shared_scratch_bytes(kv_heads, head_dim, static_cast<int64_t>(B) * q_len * (heads / kv_heads), sms);
+}
+
+fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype,
+                                           int heads, int q_len, const int32_t* block_table, int max_blocks,
+                                           const int32_t* seq_lens, int B, const int32_t* prefix_len, float sm_scale,
+                                           void* out, int64_t ldo, float* lse, void* workspace,
+                                           size_t workspace_bytes, void* scratch, size_t scratch_bytes, int pdl,
+                                           cudaStream_t stream) {
+  const AttentionCall a = {cache, q, ldq, dtype, heads, q_len, block_table, max_blocks, seq_lens, B, sm_scale, 0, out, ldo,
+                           lse, workspace, workspace_bytes, pdl, true, prefix_len, scratch, scratch_bytes};
+  fp4::KvAttnMoreParams p = {};
+  int row_units, sms;
+  const fp4gemv_status st = attention_params(a, &p, &row_units, &sms);
+  if (st != FP4GEMV_OK) return st;
+  const int dim = cache->head_dim, int8 = cache->format == FP4GEMV_KV_INT8;
+  const int64_t all_rows = static_cast<int64_t>(B) * q_len * p.group, items = shared_items(all_rows, dim);
+  fp4::KvPrefixParams x = {};
+  x.line.tokens = static_cast<const int32_t*>(scratch);
+  x.line.ml = reinterpret_cast<float2*>(static_cast<char*>(scratch) + 16);
+  x.line.sums = reinterpret_cast<float*>(reinterpret_cast<char*>(x.line.ml) +
+                                         shared_ml_bytes(sms + cache->kv_heads * items, dim));
+  x.line.slots = fp4::kv_prefix_slots(dim);
+  x.line.tile = fp4::kv_prefix_tile(dim);
+  x.line.blocks = static_cast<int>(shared_blocks(all_rows));
+  x.line.items = static_cast<int>(items);
+  // no more CTAs than tiles that the table's width could hold
+  const int64_t tiles = (static_cast<int64_t>(max_blocks) << p.block_log2) / x.line.tile * cache->kv_heads * items;
+  x.line.ctas = tiles < 1 ? 1 : tiles < sms ? static_cast<int>(tiles) : sms;
+  x.k_codes = cache->k_codes;
+  x.v_codes = cache->v_codes;
+  x.k_scale = cache->k_scale;
+  x.v_scale = cache->v_scale;
+  x.q = p.q;
+  x.ldq = ldq;
+  x.table = block_table;
+  x.lens = seq_lens;
+  x.prefix_len = prefix_len;
+  x.err = p.err;
+  x.tokens = static_cast<int32_t*>(scratch);
+  x.B = B;
+  x.max_blocks = max_blocks;
+  x.num_blocks = cache->num_blocks;
+  x.block_log2 = p.block_log2;
+  x.kv_heads = cache->kv_heads;
+  x.group = p.group;
+  x.q_len = q_len;
+  x.f16 = p.f16;
+  x.sm_scale = sm_scale;
+  p.line = x.line;
+  fp4::count_launch();
+  const cudaError_t e = fp4::launch_kv_prefix(x, dim, int8, pdl, stream);
+  if (e != cudaSuccess) return from_cuda(e);
+  fp4::count_launch();
+  return from_cuda(fp4::launch_kv_attention_more(p, dim, int8, row_units, sms, pdl, stream));
 }
 
 fp4gemv_status fp4gemv_moe_route(const void* logits, int64_t ldl, int dtype, int M, int E, int topk, int scores,

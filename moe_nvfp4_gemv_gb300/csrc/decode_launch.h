@@ -37,6 +37,13 @@ cudaError_t launch_kv_attention(const KvAttnParams& p, int dim, int int8, int ro
 cudaError_t launch_kv_attention_more(const KvAttnMoreParams& p, int dim, int int8, int row_units, int sms, int pdl,
                                      cudaStream_t stream);
 
+// The common beginning of shared attention (k_kv_prefix.cuh).  The line's slots and tile by head_dim; its ctas and the
+// scratch's pieces by the SMs.
+struct KvPrefixParams;
+int kv_prefix_slots(int dim);
+int kv_prefix_tile(int dim);
+cudaError_t launch_kv_prefix(const KvPrefixParams& p, int dim, int int8, int pdl, cudaStream_t stream);
+
 // E4M3, head_dim 128, row tiles of 32.
 cudaError_t launch_kv_attention_tc(const KvAttnTcParams& p, int sms, int pdl, cudaStream_t stream);
 

@@ -1,0 +1,40 @@
+// Launcher of the kernel for a beginning that sequences share.
+#include "decode_launch.h"
+#include "k_kv_prefix.cuh"
+#include "launch.h"
+
+namespace fp4 {
+
+int kv_prefix_slots(int dim) { return dim == 256 ? PrefixCfg<256>::kSlots : PrefixCfg<128>::kSlots; }
+int kv_prefix_tile(int dim) { return dim == 256 ? PrefixCfg<256>::kTile : PrefixCfg<128>::kTile; }
+
+template <int kDim, bool kInt8>
+static cudaError_t prefix_typed(const KvPrefixParams& p, int pdl, cudaStream_t stream) {
+  using C = PrefixCfg<kDim>;
+  auto kernel = kv_prefix_kernel<kDim, kInt8>;
+  static int configured[64];
+  cudaError_t e = configure_kernel(kernel, configured, C::kSmem, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(static_cast<unsigned>(p.line.ctas), 1, 1);
+  lc.blockDim = dim3(C::kThreads, 1, 1);
+  lc.dynamicSmemBytes = C::kSmem;
+  lc.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &attr;
+  lc.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&lc, kernel, p);
+}
+
+cudaError_t launch_kv_prefix(const KvPrefixParams& p, int dim, int int8, int pdl, cudaStream_t stream) {
+  switch (dim) {
+    case 64: return int8 ? prefix_typed<64, true>(p, pdl, stream) : prefix_typed<64, false>(p, pdl, stream);
+    case 96: return int8 ? prefix_typed<96, true>(p, pdl, stream) : prefix_typed<96, false>(p, pdl, stream);
+    case 128: return int8 ? prefix_typed<128, true>(p, pdl, stream) : prefix_typed<128, false>(p, pdl, stream);
+    default: return int8 ? prefix_typed<256, true>(p, pdl, stream) : prefix_typed<256, false>(p, pdl, stream);
+  }
+}
+
+}  // namespace fp4

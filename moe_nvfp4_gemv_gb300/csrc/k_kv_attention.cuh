@@ -95,12 +95,34 @@ struct KvAttnParams {
   float sm_scale;
 };
 
-// ... with first tokens that stay visible in a window: a sequence's items hold `lead` strips of its beginning, then those
-// of its window, with a gap between them that counts as no strips.
-struct KvAttnMoreParams : KvAttnParams {
-  int sinks;  // the first tokens that stay visible (0: none)
-  int lead;   // their strips
+// The tiles of a beginning that the sequences share (k_kv_prefix.cuh) on their line, and what their sums are.
+struct KvPrefixLine {
+  const int32_t* tokens;  // [1], device: how many tokens were taken together
+  float* sums;            // [piece][slot][128 rows][dim]
+  float2* ml;             // [piece][slot][128 rows]: m, the sum of weights
+  int ctas;
+  int blocks;             // of 128 rows
+  int items;              // of a KV head
+  int slots;
+  int tile;               // tokens
 };
+
+// A share of the line: pieces are numbered by CTA + item, which never repeats.
+__host__ __device__ inline int prefix_share(int tiles, int ctas) { return (tiles + ctas - 1) / ctas; }
+
+// ... with first tokens that stay visible in a window: a sequence's items hold `lead` strips of its beginning, then those
+// of its window, with a gap between them that counts as no strips.  Or with a beginning that another kernel has taken: the
+// gap is that, and its sums are joined with an item's.
+struct KvAttnMoreParams : KvAttnParams {
+  int sinks;          // the first tokens that stay visible (0: none)
+  int lead;           // their strips
+  KvPrefixLine line;  // .tokens NULL: none
+};
+// The tokens of the beginning that were taken (in shared memory, for the kernel's life).
+__device__ __forceinline__ int& attn_taken() {
+  __shared__ int taken;
+  return taken;
+}
 
 // ... of the kernel on the 5th-generation tensor core
 struct KvAttnTcParams : KvAttnParams {
@@ -138,6 +160,14 @@ __device__ __forceinline__ float attn_lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// l 2^d, d <= 0.  kMore: in two steps, for sums of weights / vs.  Beside a page of V that is zero these reach 2^100 and
+// the factors to other pages' maxima 2^-130, which is no binary32 number; few tokens to a warp make that usual here.
+template <bool kMore>
+__device__ __forceinline__ float attn_lower(float l, float d) {
+  if (!kMore) return l * attn_ex2(d);
+  const float half = attn_ex2(0.5f * d);
+  return l * half * half;
 }
 // C += A B; A 16 x 16 (rows g and g + 8), B 16 x 8, f16; C fp32.
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -219,8 +249,9 @@ __device__ __forceinline__ int attn_first_strip(const KvAttnParams& p, int n) {
   const int at = n - p.q_len;  // the first query's position
   return p.window > 0 && at >= p.window ? ((at - p.window + 1) >> 4) & -p.unit : 0;
 }
-// ... with leading strips: the strips between them and the window
+// ... with leading strips: the strips between them and the window; those of a beginning that is taken
 __device__ __forceinline__ int attn_first_strip(const KvAttnMoreParams& p, int n) {
+  if (p.line.tokens) return attn_taken() >> 4;
   return max(attn_first_strip(static_cast<const KvAttnParams&>(p), n) - p.lead, 0);
 }
 template <class P>
@@ -437,12 +468,58 @@ __device__ __forceinline__ AttnPlace attn_next(const P& p, AttnPlace x, const in
   return x;
 }
 
+// The sums of the taken beginning's pieces to four of row `row`'s (of sequence b), dims d .. d + 3.
+template <int kDim>
+__device__ __forceinline__ void attn_join_taken(const KvAttnMoreParams& p, int b, int head, int row, int d, float4& v,
+                                                float& top, float& l) {
+  constexpr int kBatch = 8;  // pieces in flight
+  const KvPrefixLine& line = p.line;
+  const int tiles = attn_taken() / line.tile;
+  if (tiles == 0) return;
+  const int per = prefix_share(tiles * p.kv_heads * line.items, line.ctas);
+  const int all = b * p.q_len * p.group + row, block = all >> 7;
+  const int number = line.slots == 1 ? block : block >> 1;
+  const bool pair = line.slots == 2 && 2 * number + 1 < line.blocks;
+  const int ways = line.slots == 1 || pair ? 1 : 2;  // slots that took the row's tiles by turns
+  const int item = head * line.items + number, c0 = item * tiles / per, c1 = ((item + 1) * tiles - 1) / per;
+  const int64_t first = (static_cast<int64_t>(c0) + item) * line.slots + (pair ? block & 1 : 0);
+  const int step = pair ? 2 : 1, cnt = (c1 - c0 + 1) * ways;
+  for (int k = 0; k < cnt; k += kBatch) {
+    float2 cm[kBatch];
+    float4 a[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      cm[j] = make_float2(kAttnFloor, 0.0f);
+      if (k + j < cnt) {
+        const int64_t at = (first + (k + j) * step) * 128 + (all & 127);
+        cm[j] = __ldcg(line.ml + at);
+        a[j] = __ldcg(reinterpret_cast<const float4*>(line.sums + at * kDim + d));
+      }
+      if (cm[j].y == 0.0f) a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // (a slot that had no tile wrote none)
+    }
+    float mn = top;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
+    const float fall = attn_ex2(top - mn);
+    v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall, l = attn_lower<true>(l, top - mn);
+    top = mn;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float f = attn_ex2(cm[j].x - mn);
+      v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
+      v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
+      l += attn_lower<true>(cm[j].y, cm[j].x - mn);
+    }
+  }
+}
+
 // What follows an item's sums: row r's outputs, or its partials and their
 // joining.  A partial row holds the sums, m and the sum of weights.
-template <int kDim, int kThreads>
+template <int kDim, int kThreads, class P = KvAttnParams>
 struct AttnItemEnd {
   static constexpr int kRowFloats = kDim + 4;
-  const KvAttnParams& p;
+  static constexpr bool kMore = std::is_same_v<P, KvAttnMoreParams>;
+  const P& p;
   const AttnPlace& cur;
   int row0, used;  // the item's first row, its rows
 
@@ -454,6 +531,8 @@ struct AttnItemEnd {
     const int row = row0 + r, i = (row * p.group_magic) >> 16;
     const int64_t tok_out = static_cast<int64_t>(cur.b) * p.q_len + i;
     const int head_out = cur.head * p.group + row - i * p.group;
+    if constexpr (kMore)
+      if (p.line.tokens) attn_join_taken<kDim>(p, cur.b, cur.head, row, d, v, top, l);
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
     uint2 w;
@@ -525,14 +604,15 @@ struct AttnItemEnd {
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
           const float fall = attn_ex2(top - mn);
-          v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall, l *= fall;
+          v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall;
+          l = kMore ? attn_lower<kMore>(l, top - mn) : l * fall;
           top = mn;
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
             const float f = attn_ex2(cm[j].x - mn);
             v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
             v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
-            l = fmaf(cm[j].y, f, l);
+            l = kMore ? l + attn_lower<kMore>(cm[j].y, cm[j].x - mn) : fmaf(cm[j].y, f, l);
           }
         }
         for (int o = 1; o < ways; o <<= 1) {
@@ -543,7 +623,7 @@ struct AttnItemEnd {
           const float f = attn_ex2(top - mn), fo = attn_ex2(to - mn);
           v.x = v.x * f + u.x * fo, v.y = v.y * f + u.y * fo;
           v.z = v.z * f + u.z * fo, v.w = v.w * f + u.w * fo;
-          l = l * f + lo * fo;
+          l = kMore ? attn_lower<kMore>(l, top - mn) + attn_lower<kMore>(lo, to - mn) : l * f + lo * fo;
           top = mn;
         }
         if (live && way == 0) {
@@ -760,6 +840,12 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
       const char* at = i < q_lines ? reinterpret_cast<const char*>(p.q + row * p.ldq) + (i - row * per_row) * 128
                                    : reinterpret_cast<const char*>(p.table) + static_cast<int64_t>(i - q_lines) * 128;
       asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    }
+  }
+  if constexpr (kMore) {
+    if (p.line.tokens && warp == 0) {  // (the plan is the first warp's, and ends with a barrier)
+      if (lane == 0) attn_taken() = __ldcg(p.line.tokens);
+      __syncwarp();
     }
   }
   auto first_strip = [&](int n) -> int { return attn_first_strip(p, n); };
@@ -1090,8 +1176,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
               const float mn = fmaxf(m[nt][h], top - kAttnLift);
               const float fall = attn_ex2(m[nt][h] - mn);
+              sum[nt][h] = kMore ? attn_lower<kMore>(sum[nt][h], m[nt][h] - mn) : sum[nt][h] * fall;
               m[nt][h] = mn;
-              sum[nt][h] *= fall;
 #pragma unroll
               for (int j = 0; j < L::kTiles; ++j) {
                 acc[nt][j][h] *= fall;
@@ -1162,7 +1248,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
     const AttnPlace cur = places[which];
     const int used = min(C::kRows, rows - row0);
     const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
-    const AttnItemEnd<kDim, C::kThreads> item_end = {p, cur, row0, used};
+    const AttnItemEnd<kDim, C::kThreads, std::conditional_t<kMore, KvAttnMoreParams, KvAttnParams>> item_end = {p, cur, row0,
+                                                                                                               used};
     float* const part = item_end.part_of(blockIdx.x, starts ? 1 : 0);
     bool nans = false;
 #pragma unroll
@@ -1206,7 +1293,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
           const float* const cells = reinterpret_cast<const float*>(smem + free_stage[w]);
           const float4 a = *reinterpret_cast<const float4*>(cells + from_cell);
           v.x = fmaf(a.x, fv, v.x), v.y = fmaf(a.y, fv, v.y), v.z = fmaf(a.z, fv, v.z), v.w = fmaf(a.w, fv, v.w);
-          l = fmaf(o.y, f, l);
+          l = kMore ? l + attn_lower<kMore>(o.y, o.x - top) : fmaf(o.y, f, l);
         }
         if (whole) {
           item_end.store(r, d, v, top, l);

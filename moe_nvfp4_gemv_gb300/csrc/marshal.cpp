@@ -29,6 +29,7 @@ namespace {
 decltype(&fp4gemv_kv_append) g_append;
 decltype(&fp4gemv_kv_attention) g_attention;
 decltype(&fp4gemv_kv_attention_sinks) g_attention_sinks;
+decltype(&fp4gemv_kv_attention_shared) g_attention_shared;
 decltype(&fp4gemv_kv_read) g_read;
 decltype(&fp4gemv_add_norm) g_add_norm;
 decltype(&fp4gemv_moe_route) g_route;
@@ -359,6 +360,30 @@ PyObject* kv_attention_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// kv_attention_shared(kv_attention's, prefix_len, scratch); the window is none
+PyObject* kv_attention_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> int {
+    const Attention c = attention_of(a);
+    const at::Tensor &prefix = tensor(a[12], "prefix_len"), &scratch = tensor(a[13], "scratch");
+    if (prefix.numel() != 1 || !plain(prefix, at::kInt, c.index))
+      refuse("prefix_len must be an int32 [1] tensor on the cache's device");
+    if (!scratch.is_cuda() || scratch.get_device() != c.index || !scratch.is_contiguous())
+      refuse("scratch must be a contiguous tensor on the cache's device");
+    if (c.window != 0) refuse("no window together with a shared beginning");
+    if (c.empty) return FP4GEMV_OK;
+    if (c.large) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+    const int32_t* pp = address_as<int32_t>(prefix);
+    void* ps = address_as<void>(scratch);
+    const size_t scratch_bytes = scratch.nbytes();
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.index));
+    const cudaStream_t stream = stream_of(c.index);
+    return unlocked([&] {
+      return g_attention_shared(c.cache, c.q, c.ldq, c.dtype, c.heads, c.q_len, c.table, c.max_blocks, c.lens, c.B, pp,
+                                c.sm_scale, c.out, c.ldo, c.lse, c.workspace, c.bytes, ps, scratch_bytes, c.pdl, stream);
+    });
+  });
+}
+
 // The logits' type, rows, row length and row stride.
 struct Logits {
   int dtype;
@@ -461,12 +486,13 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind_more(kv_read, add_norm, kv_attention_sinks): the others'
+// bind_more(kv_read, add_norm, kv_attention_sinks, kv_attention_shared): the others'
 PyObject* bind_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 3, [&]() -> int {
+  return guarded(n, 4, [&]() -> int {
     g_read = reinterpret_cast<decltype(g_read)>(integer(a[0]));
     g_add_norm = reinterpret_cast<decltype(g_add_norm)>(integer(a[1]));
     g_attention_sinks = reinterpret_cast<decltype(g_attention_sinks)>(integer(a[2]));
+    g_attention_shared = reinterpret_cast<decltype(g_attention_shared)>(integer(a[3]));
     return 0;
   });
 }
@@ -479,7 +505,8 @@ PyMethodDef g_methods[] = {method<bind>("bind"),           method<kv_append>("kv
                            method<kv_attention>("kv_attention"), method<moe_route>("moe_route"),
                            method<token_logprobs>("token_logprobs"), method<bind_more>("bind_more"),
                            method<kv_read>("kv_read"),     method<add_norm>("add_norm"),
-                           method<kv_attention_sinks>("kv_attention_sinks"), {nullptr, nullptr, 0, nullptr}};
+                           method<kv_attention_sinks>("kv_attention_sinks"),
+                           method<kv_attention_shared>("kv_attention_shared"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -84,6 +84,9 @@ def _load() -> ctypes.CDLL:
                                        vp, sz, i32, vp]),
         "fp4gemv_kv_attention_sinks": (i32, [vp, vp, i64, i32, i32, i32, vp, i32, vp, i32, ctypes.c_float, i32, i32, vp,
                                              i64, vp, vp, sz, i32, vp]),
+        "fp4gemv_kv_attention_shared_scratch_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "fp4gemv_kv_attention_shared": (i32, [vp, vp, i64, i32, i32, i32, vp, i32, vp, i32, vp, ctypes.c_float, vp, i64,
+                                              vp, vp, sz, vp, sz, i32, vp]),
         "fp4gemv_kv_read": (i32, [vp, vp, i64, vp, i64, i32, i32, vp, vp, i32, vp, i32, i32, vp]),
         "fp4gemv_add_norm": (i32, [vp, i64, i32, vp, i64, i32, vp, vp, i32, vp, i64, i32, i32, i32, ctypes.c_float,
                                    ctypes.c_float, ctypes.c_float, vp, i64, vp, i64, i32, i32, i32, vp]),
@@ -128,7 +131,8 @@ try:
     _marshal.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
         _lib.fp4gemv_kv_append, _lib.fp4gemv_kv_attention, _lib.fp4gemv_moe_route, _lib.fp4gemv_token_logprobs)))
     _marshal.bind_more(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
-        _lib.fp4gemv_kv_read, _lib.fp4gemv_add_norm, _lib.fp4gemv_kv_attention_sinks)))
+        _lib.fp4gemv_kv_read, _lib.fp4gemv_add_norm, _lib.fp4gemv_kv_attention_sinks,
+        _lib.fp4gemv_kv_attention_shared)))
 except Exception as e:
     _marshal = _NoMarshal(e)
 _nvfp4_gemv = _lib.fp4gemv_nvfp4_gemv

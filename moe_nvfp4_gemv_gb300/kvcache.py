@@ -8,6 +8,8 @@ of a decode step:
 * ``append``: quantises new keys and values into the pages that the block
   table names; a page's scale grows with what it holds;
 * ``attend``: attention of each sequence's newest tokens over its pages;
+* ``attend_shared``: the same for sequences that begin alike, their beginning
+  read and multiplied once;
 * ``read``: tokens out of the pages again.
 
 The tensors stay the caller's: copy, share or reset pages as the serving
@@ -33,6 +35,7 @@ _F32 = torch.float32
 _append = _marshal.kv_append
 _attend = _marshal.kv_attention
 _attend_sinks = _marshal.kv_attention_sinks
+_attend_shared = _marshal.kv_attention_shared
 _read = _marshal.kv_read
 
 
@@ -190,3 +193,32 @@ class KvCache8:
         if status:
             raise Fp4GemvError(status, "fp4gemv_kv_attention")
         return out
+
+    def attend_shared(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                      prefix_len: torch.Tensor, sm_scale: float | None = None, out: torch.Tensor | None = None,
+                      lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      scratch: torch.Tensor | None = None, pdl: bool = True) -> torch.Tensor:
+        """``attend`` of sequences whose first ``prefix_len`` tokens (int32 [1],
+        device) are the same: every sequence's row of the block table names
+        pages with that beginning, usually the same ones, and what fills whole
+        pages of it is read and multiplied once for all.  (In multiples of 128
+        tokens, and no further than the first query of the shortest sequence;
+        empty sequences do not count.)  ``scratch``: uint8, of
+        ``shared_scratch_bytes``, allocated for the call by default."""
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        if workspace is None:
+            workspace = attention_workspace(self.device, self.head_dim)
+        if scratch is None:
+            nbytes = self.shared_scratch_bytes(*q.shape[:3]) if q.dim() == 4 else 0
+            scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        status = _attend_shared(self._handle, self._index, self.head_dim, q, block_table, seq_lens,
+                                self._sm_scale if sm_scale is None else sm_scale, 0, out, lse, workspace, pdl,
+                                prefix_len, scratch)
+        if status:
+            raise Fp4GemvError(status, "fp4gemv_kv_attention_shared")
+        return out
+
+    def shared_scratch_bytes(self, batch: int, q_len: int, heads: int) -> int:
+        """Bytes of ``attend_shared``'s scratch (0 for sizes that it refuses)."""
+        return int(_lib.fp4gemv_kv_attention_shared_scratch_bytes(self.kv_heads, self.head_dim, heads, q_len, batch))
