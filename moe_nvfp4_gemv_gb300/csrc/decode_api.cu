@@ -370,7 +370,7 @@ fp4gemv_status fp4gemv_kv_attention_sinks(const fp4gemv_kv_cache* cache, const v
   if (sinks > (1 << 30)) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
   const AttentionCall a = {cache, q, ldq, dtype, heads, q_len, block_table, max_blocks, seq_lens, B, sm_scale, window,
                            out, ldo, lse, workspace, workspace_bytes, pdl, false, nullptr, nullptr, 0};
-  fp4::KvAttnMoreParams p = {};
+  fp4::KvAttnSinksParams p = {};
   int row_units, sms;
   const fp4gemv_status st = attention_params(a, &p, &row_units, &sms);
   if (st != FP4GEMV_OK) return st;
@@ -378,7 +378,7 @@ fp4gemv_status fp4gemv_kv_attention_sinks(const fp4gemv_kv_cache* cache, const v
   p.sinks = sinks;
   p.lead = (sinks + 15) / 16;
   fp4::count_launch();
-  return from_cuda(fp4::launch_kv_attention_more(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms,
+  return from_cuda(fp4::launch_kv_attention_sinks(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms,
                                                  pdl, stream));
 }
 
@@ -400,7 +400,7 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
                                            cudaStream_t stream) {
   const AttentionCall a = {cache, q, ldq, dtype, heads, q_len, block_table, max_blocks, seq_lens, B, sm_scale, 0, out, ldo,
                            lse, workspace, workspace_bytes, pdl, true, prefix_len, scratch, scratch_bytes};
-  fp4::KvAttnMoreParams p = {};
+  fp4::KvAttnRestParams p = {};
   int row_units, sms;
   const fp4gemv_status st = attention_params(a, &p, &row_units, &sms);
   if (st != FP4GEMV_OK) return st;
@@ -443,7 +443,7 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
   const cudaError_t e = fp4::launch_kv_prefix(x, dim, int8, pdl, stream);
   if (e != cudaSuccess) return from_cuda(e);
   fp4::count_launch();
-  return from_cuda(fp4::launch_kv_attention_more(p, dim, int8, row_units, sms, pdl, stream));
+  return from_cuda(fp4::launch_kv_attention_rest(p, dim, int8, row_units, sms, pdl, stream));
 }
 
 fp4gemv_status fp4gemv_moe_route(const void* logits, int64_t ldl, int dtype, int M, int E, int topk, int scores,

@@ -33,8 +33,11 @@ int kv_attention_max_ctas(int sms);
 cudaError_t launch_kv_attention(const KvAttnParams& p, int dim, int int8, int row_units, int sms, int pdl,
                                 cudaStream_t stream);
 
-// ... with leading strips; row tiles of 32 for every head_dim but 256.
-cudaError_t launch_kv_attention_more(const KvAttnMoreParams& p, int dim, int int8, int row_units, int sms, int pdl,
+// ... with first tokens that stay visible, and behind a beginning that is taken; row tiles of 32 for every head_dim but
+// 256.
+cudaError_t launch_kv_attention_sinks(const KvAttnSinksParams& p, int dim, int int8, int row_units, int sms, int pdl,
+                                      cudaStream_t stream);
+cudaError_t launch_kv_attention_rest(const KvAttnRestParams& p, int dim, int int8, int row_units, int sms, int pdl,
                                      cudaStream_t stream);
 
 // The common beginning of shared attention (k_kv_prefix.cuh).  The line's slots and tile by head_dim; its ctas and the

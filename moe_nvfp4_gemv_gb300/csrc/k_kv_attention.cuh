@@ -110,14 +110,22 @@ struct KvPrefixLine {
 // A share of the line: pieces are numbered by CTA + item, which never repeats.
 __host__ __device__ inline int prefix_share(int tiles, int ctas) { return (tiles + ctas - 1) / ctas; }
 
-// ... with first tokens that stay visible in a window: a sequence's items hold `lead` strips of its beginning, then those
-// of its window, with a gap between them that counts as no strips.  Or with a beginning that another kernel has taken: the
-// gap is that, and its sums are joined with an item's.
-struct KvAttnMoreParams : KvAttnParams {
-  int sinks;          // the first tokens that stay visible (0: none)
-  int lead;           // their strips
-  KvPrefixLine line;  // .tokens NULL: none
+// What a kernel does beyond a window: first tokens that stay visible in it; or the rest of sequences whose beginning
+// another kernel has taken.
+enum AttnMode { kAttnPlain, kAttnSinks, kAttnRest };
+// A sequence's items hold `lead` strips of its beginning, then those of its window, with a gap between them that counts as
+// no strips.
+struct KvAttnSinksParams : KvAttnParams {
+  int sinks;  // the first tokens that stay visible
+  int lead;   // their strips
 };
+// The beginning's strips count as none, and its sums are joined with an item's.
+struct KvAttnRestParams : KvAttnParams {
+  KvPrefixLine line;
+};
+template <int kMode>
+using AttnModeParams = std::conditional_t<kMode == kAttnSinks, KvAttnSinksParams,
+                                          std::conditional_t<kMode == kAttnRest, KvAttnRestParams, KvAttnParams>>;
 // The tokens of the beginning that were taken (in shared memory, for the kernel's life).
 __device__ __forceinline__ int& attn_taken() {
   __shared__ int taken;
@@ -161,11 +169,12 @@ __device__ __forceinline__ float attn_lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// l 2^d, d <= 0.  kMore: in two steps, for sums of weights / vs.  Beside a page of V that is zero these reach 2^100 and
-// the factors to other pages' maxima 2^-130, which is no binary32 number; few tokens to a warp make that usual here.
-template <bool kMore>
+// l 2^d, d <= 0, in two steps: for sums of weights / vs.  Beside a page of V that is zero these reach 2^100 and the
+// factors to other pages' maxima 2^-130, which is no binary32 number; few tokens to a warp make that usual in the modes
+// beyond the plain one.
+template <int kMode>
 __device__ __forceinline__ float attn_lower(float l, float d) {
-  if (!kMore) return l * attn_ex2(d);
+  if (kMode == kAttnPlain) return l * attn_ex2(d);
   const float half = attn_ex2(0.5f * d);
   return l * half * half;
 }
@@ -249,9 +258,10 @@ __device__ __forceinline__ int attn_first_strip(const KvAttnParams& p, int n) {
   const int at = n - p.q_len;  // the first query's position
   return p.window > 0 && at >= p.window ? ((at - p.window + 1) >> 4) & -p.unit : 0;
 }
-// ... with leading strips: the strips between them and the window; those of a beginning that is taken
-__device__ __forceinline__ int attn_first_strip(const KvAttnMoreParams& p, int n) {
-  if (p.line.tokens) return attn_taken() >> 4;
+// ... behind a beginning that is taken
+__device__ __forceinline__ int attn_first_strip(const KvAttnRestParams& p, int n) { return attn_taken() >> 4; }
+// ... with leading strips: the strips between them and the window
+__device__ __forceinline__ int attn_first_strip(const KvAttnSinksParams& p, int n) {
   return max(attn_first_strip(static_cast<const KvAttnParams&>(p), n) - p.lead, 0);
 }
 template <class P>
@@ -468,49 +478,60 @@ __device__ __forceinline__ AttnPlace attn_next(const P& p, AttnPlace x, const in
   return x;
 }
 
-// The sums of the taken beginning's pieces to four of row `row`'s (of sequence b), dims d .. d + 3.
+// Four outputs of a row, and (lse not NULL) its log of the sums.
+__device__ __forceinline__ void attn_put(float4 v, float top, float l, uint16_t* out, float* lse, int f16) {
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+  uint2 w;
+  if (f16) {
+    w.x = pack_f16(v.x, v.y);
+    w.y = pack_f16(v.z, v.w);
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    w.x = *reinterpret_cast<const uint32_t*>(&a);
+    w.y = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint2*>(out) = w;
+  if (lse) *lse = l > 0.0f ? 0.6931471805599453f * (top + log2f(l)) : l == l ? -__builtin_huge_valf() : l;
+}
+
+// The same with the sums of `cnt` pieces of the taken beginning: the row's (m, sum of weights) from ml on, the dims' sums
+// from `sums` on, `step` pieces' slots apart.  A function of its own: its loads in flight would cost the loops over
+// tokens their registers (128 a thread: 61 us for 64 sequences of up to 701 own tokens, as a function 31).
 template <int kDim>
-__device__ __forceinline__ void attn_join_taken(const KvAttnMoreParams& p, int b, int head, int row, int d, float4& v,
-                                                float& top, float& l) {
+__device__ __noinline__ void attn_join_taken(float4 v, float top, float l, const float2* ml, const float* sums, int step,
+                                             int cnt, uint16_t* out, float* lse, int f16) {
   constexpr int kBatch = 8;  // pieces in flight
-  const KvPrefixLine& line = p.line;
-  const int tiles = attn_taken() / line.tile;
-  if (tiles == 0) return;
-  const int per = prefix_share(tiles * p.kv_heads * line.items, line.ctas);
-  const int all = b * p.q_len * p.group + row, block = all >> 7;
-  const int number = line.slots == 1 ? block : block >> 1;
-  const bool pair = line.slots == 2 && 2 * number + 1 < line.blocks;
-  const int ways = line.slots == 1 || pair ? 1 : 2;  // slots that took the row's tiles by turns
-  const int item = head * line.items + number, c0 = item * tiles / per, c1 = ((item + 1) * tiles - 1) / per;
-  const int64_t first = (static_cast<int64_t>(c0) + item) * line.slots + (pair ? block & 1 : 0);
-  const int step = pair ? 2 : 1, cnt = (c1 - c0 + 1) * ways;
+#pragma unroll 1
   for (int k = 0; k < cnt; k += kBatch) {
     float2 cm[kBatch];
     float4 a[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       cm[j] = make_float2(kAttnFloor, 0.0f);
+      a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (k + j < cnt) {
-        const int64_t at = (first + (k + j) * step) * 128 + (all & 127);
-        cm[j] = __ldcg(line.ml + at);
-        a[j] = __ldcg(reinterpret_cast<const float4*>(line.sums + at * kDim + d));
+        cm[j] = __ldcg(ml + static_cast<int64_t>(k + j) * step * 128);
+        a[j] = __ldcg(reinterpret_cast<const float4*>(sums + static_cast<int64_t>(k + j) * step * (128 * kDim)));
       }
-      if (cm[j].y == 0.0f) a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // (a slot that had no tile wrote none)
     }
     float mn = top;
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
     const float fall = attn_ex2(top - mn);
-    v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall, l = attn_lower<true>(l, top - mn);
+    v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall;
+    l = attn_lower<kAttnRest>(l, top - mn);
     top = mn;
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
+      if (cm[j].y == 0.0f) a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // (a slot that had no tile wrote no sums)
       const float f = attn_ex2(cm[j].x - mn);
       v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
       v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
-      l += attn_lower<true>(cm[j].y, cm[j].x - mn);
+      l += attn_lower<kAttnRest>(cm[j].y, cm[j].x - mn);
     }
   }
+  attn_put(v, top, l, out, lse, f16);
 }
 
 // What follows an item's sums: row r's outputs, or its partials and their
@@ -518,7 +539,9 @@ __device__ __forceinline__ void attn_join_taken(const KvAttnMoreParams& p, int b
 template <int kDim, int kThreads, class P = KvAttnParams>
 struct AttnItemEnd {
   static constexpr int kRowFloats = kDim + 4;
-  static constexpr bool kMore = std::is_same_v<P, KvAttnMoreParams>;
+  static constexpr int kMode = std::is_same_v<P, KvAttnSinksParams>  ? kAttnSinks
+                               : std::is_same_v<P, KvAttnRestParams> ? kAttnRest
+                                                                     : kAttnPlain;
   const P& p;
   const AttnPlace& cur;
   int row0, used;  // the item's first row, its rows
@@ -531,23 +554,24 @@ struct AttnItemEnd {
     const int row = row0 + r, i = (row * p.group_magic) >> 16;
     const int64_t tok_out = static_cast<int64_t>(cur.b) * p.q_len + i;
     const int head_out = cur.head * p.group + row - i * p.group;
-    if constexpr (kMore)
-      if (p.line.tokens) attn_join_taken<kDim>(p, cur.b, cur.head, row, d, v, top, l);
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-    uint2 w;
-    if (p.f16) {
-      w.x = pack_f16(v.x, v.y);
-      w.y = pack_f16(v.z, v.w);
-    } else {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-      w.x = *reinterpret_cast<const uint32_t*>(&a);
-      w.y = *reinterpret_cast<const uint32_t*>(&b);
+    uint16_t* const out = p.out + tok_out * p.ldo + head_out * kDim + d;
+    float* const lse = d == 0 && p.lse ? p.lse + tok_out * (p.kv_heads * p.group) + head_out : nullptr;
+    if constexpr (kMode == kAttnRest) {
+      const KvPrefixLine& line = p.line;
+      const int tiles = attn_taken() / line.tile;
+      if (tiles > 0) {
+        const int per = prefix_share(tiles * p.kv_heads * line.items, line.ctas);
+        const int all = cur.b * p.q_len * p.group + row, block = all >> 7;
+        const int number = line.slots == 1 ? block : block >> 1;
+        const bool pair = line.slots == 2 && 2 * number + 1 < line.blocks;  // (else: slots that took the tiles by turns)
+        const int item = cur.head * line.items + number, c0 = item * tiles / per, c1 = ((item + 1) * tiles - 1) / per;
+        const int64_t at = ((static_cast<int64_t>(c0) + item) * line.slots + (pair ? block & 1 : 0)) * 128 + (all & 127);
+        attn_join_taken<kDim>(v, top, l, line.ml + at, line.sums + at * kDim + d, pair ? 2 : 1,
+                              (c1 - c0 + 1) * (line.slots == 1 || pair ? 1 : 2), out, lse, p.f16);
+        return;
+      }
     }
-    *reinterpret_cast<uint2*>(p.out + tok_out * p.ldo + head_out * kDim + d) = w;
-    if (d == 0 && p.lse)
-      p.lse[tok_out * (p.kv_heads * p.group) + head_out] =
-          l > 0.0f ? 0.6931471805599453f * (top + log2f(l)) : l == l ? -__builtin_huge_valf() : l;
+    attn_put(v, top, l, out, lse, p.f16);
   }
   // Behind the CTA's partial: the last CTA of those that share the item joins
   // them.  Called by kThreads threads, tid 0 on; sync() is their barrier; ml
@@ -605,14 +629,14 @@ struct AttnItemEnd {
           for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
           const float fall = attn_ex2(top - mn);
           v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall;
-          l = kMore ? attn_lower<kMore>(l, top - mn) : l * fall;
+          l = kMode != kAttnPlain ? attn_lower<kMode>(l, top - mn) : l * fall;
           top = mn;
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
             const float f = attn_ex2(cm[j].x - mn);
             v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
             v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
-            l = kMore ? l + attn_lower<kMore>(cm[j].y, cm[j].x - mn) : fmaf(cm[j].y, f, l);
+            l = kMode != kAttnPlain ? l + attn_lower<kMode>(cm[j].y, cm[j].x - mn) : fmaf(cm[j].y, f, l);
           }
         }
         for (int o = 1; o < ways; o <<= 1) {
@@ -623,7 +647,7 @@ struct AttnItemEnd {
           const float f = attn_ex2(top - mn), fo = attn_ex2(to - mn);
           v.x = v.x * f + u.x * fo, v.y = v.y * f + u.y * fo;
           v.z = v.z * f + u.z * fo, v.w = v.w * f + u.w * fo;
-          l = kMore ? attn_lower<kMore>(l, top - mn) + attn_lower<kMore>(lo, to - mn) : l * f + lo * fo;
+          l = kMode != kAttnPlain ? attn_lower<kMode>(l, top - mn) + attn_lower<kMode>(lo, to - mn) : l * f + lo * fo;
           top = mn;
         }
         if (live && way == 0) {
@@ -744,9 +768,9 @@ struct AttnLayout {
 
 // NaN codes of tokens that some of an item's rows do not see, in a strip of V (`count` tokens, the first of them seen by
 // queries from `since` on): a weight of 0 does not silence them, so they give way to zeros, and the rows that do see their
-// token are noted in nan_dims for the segment's end.  By a warp, a lane for each 16 bytes.  kMore: the strip's tokens
+// token are noted in nan_dims for the segment's end.  By a warp, a lane for each 16 bytes.  kSinks: the strip's tokens
 // before `sinks` are outside no window.
-template <int kDim, bool kMore>
+template <int kDim, bool kSinks>
 __device__ __noinline__ void attn_quiet(uint32_t strip, int count, int since, int window, int q_len, int group, int row0,
                                         int used, uint32_t (*nan_dims)[kDim / 32], int* nan_any, int sinks) {
   using L = AttnLayout<kDim>;
@@ -754,7 +778,7 @@ __device__ __noinline__ void attn_quiet(uint32_t strip, int count, int since, in
 #pragma unroll 1
   for (int i = lane; i < count * (kDim / 16); i += 32) {
     const int token = i / (kDim / 16), k = i - token * (kDim / 16), from = since + token;
-    const bool stays = window == 0 || (kMore && token < sinks);
+    const bool stays = window == 0 || (kSinks && token < sinks);
     if (from <= 0 && (stays || from + window >= q_len)) continue;  // (all rows see it)
     const uint32_t at = strip + L::chunk(token, k);
     const uint4 chunk = lds128(at);
@@ -798,10 +822,9 @@ struct AttnCfg {
   static constexpr int smem(int B) { return kSmem + (B + 1) * 12; }
 };
 
-// kMore: with leading strips (KvAttnMoreParams).
-template <int kDim, bool kInt8, int kN, int kRes, bool kMore = false>
+template <int kDim, bool kInt8, int kN, int kRes, int kMode = kAttnPlain>
 __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
-    kv_attention_kernel(const std::conditional_t<kMore, KvAttnMoreParams, KvAttnParams> p) {
+    kv_attention_kernel(const AttnModeParams<kMode> p) {
   using C = AttnCfg<kDim, kN, kRes>;
   using L = AttnLayout<kDim>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -842,8 +865,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
     }
   }
-  if constexpr (kMore) {
-    if (p.line.tokens && warp == 0) {  // (the plan is the first warp's, and ends with a barrier)
+  if constexpr (kMode == kAttnRest) {
+    if (warp == 0) {  // (the plan is the first warp's, and ends with a barrier)
       if (lane == 0) attn_taken() = __ldcg(p.line.tokens);
       __syncwarp();
     }
@@ -920,7 +943,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
         strip = off - item * s;
         head = item / p.row_tiles;
       }
-      if constexpr (kMore) strip += strip >= p.lead ? first_strip(tokens[b]) : 0;
+      if constexpr (kMode == kAttnSinks) strip += strip >= p.lead ? first_strip(tokens[b]) : 0;
       else strip += first_strip(tokens[b]);
       const int per_page = p.block_log2 - 4;
       const int id = __ldg(p.table + static_cast<int64_t>(b) * p.max_blocks + (strip >> per_page));
@@ -974,14 +997,14 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
   float acc[kN][L::kTiles][4];  // dims by rows: thread's rows 2t, 2t + 1 of every tile of 8
   float m[kN][2], sum[kN][2];
   while (at < end) {
-    int seg_end, n, row0, tok0;  // tok0: the token at strip `at`; kMore: as if there were no gap,
+    int seg_end, n, row0, tok0;  // tok0: the token at strip `at`; with sinks: as if there were no gap,
     int gap = 0;                 // ... which is that many tokens long
     {
       const AttnPlace c = places[which];
       seg_end = min(end, at + c.strips - c.strip);
       n = tokens[c.b];
       row0 = c.tile * C::kRows;
-      if constexpr (kMore) {
+      if constexpr (kMode == kAttnSinks) {
         tok0 = c.strip << 4;
         gap = c.first << 4;
       } else {
@@ -1021,7 +1044,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
 
     // the token at place `tok` of the strips that there are
     auto real = [&](int tok) -> int {
-      if constexpr (kMore) return tok >= p.lead << 4 ? tok + gap : tok;
+      if constexpr (kMode == kAttnSinks) return tok >= p.lead << 4 ? tok + gap : tok;
       else return tok;
     };
     auto after = [](int stage) { return stage + 1 == C::kStages ? 0 : stage + 1; };
@@ -1104,8 +1127,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
             __syncwarp();
           }
           int sinks = 0;
-          if constexpr (kMore) sinks = p.sinks - real(tok);
-          attn_quiet<kDim, kMore>(ring + stage * C::kStageBytes + L::kStripBytes, min(16, n - real(tok)),
+          if constexpr (kMode == kAttnSinks) sinks = p.sinks - real(tok);
+          attn_quiet<kDim, kMode == kAttnSinks>(ring + stage * C::kStageBytes + L::kStripBytes, min(16, n - real(tok)),
                                   real(tok) - (n - p.q_len), p.window, p.q_len, p.group, row0,
                                   min(C::kRows, rows - row0), nan_dims, &nan_any, sinks);
           stop = tok + 1;
@@ -1134,7 +1157,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
         const float inv_vs = attn_ex2(-lv) * kAttnUnlift;  // (sums stay those of weights up to 1)
         bool masked = here + 16 > tokens_all || here < tokens_low;
         bool some = here >= tokens_low;  // every row sees some of the strip
-        if constexpr (kMore) {
+        if constexpr (kMode == kAttnSinks) {
           masked = here + 16 > tokens_all || (here < tokens_low && here + 16 > p.sinks);
           some = some || here < min(p.sinks, tokens_all);
         }
@@ -1164,7 +1187,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
                 const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
                 const int see_from = p.window > 0 ? see_to - p.window : 0;
                 bool out0 = here + g < see_from, out1 = here + 8 + g < see_from;
-                if constexpr (kMore) {
+                if constexpr (kMode == kAttnSinks) {
                   out0 = out0 && here + g >= p.sinks;
                   out1 = out1 && here + 8 + g >= p.sinks;
                 }
@@ -1176,7 +1199,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
               const float mn = fmaxf(m[nt][h], top - kAttnLift);
               const float fall = attn_ex2(m[nt][h] - mn);
-              sum[nt][h] = kMore ? attn_lower<kMore>(sum[nt][h], m[nt][h] - mn) : sum[nt][h] * fall;
+              sum[nt][h] = kMode != kAttnPlain ? attn_lower<kMode>(sum[nt][h], m[nt][h] - mn) : sum[nt][h] * fall;
               m[nt][h] = mn;
 #pragma unroll
               for (int j = 0; j < L::kTiles; ++j) {
@@ -1248,8 +1271,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
     const AttnPlace cur = places[which];
     const int used = min(C::kRows, rows - row0);
     const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
-    const AttnItemEnd<kDim, C::kThreads, std::conditional_t<kMore, KvAttnMoreParams, KvAttnParams>> item_end = {p, cur, row0,
-                                                                                                               used};
+    const AttnItemEnd<kDim, C::kThreads, AttnModeParams<kMode>> item_end = {p, cur, row0, used};
     float* const part = item_end.part_of(blockIdx.x, starts ? 1 : 0);
     bool nans = false;
 #pragma unroll
@@ -1293,7 +1315,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
           const float* const cells = reinterpret_cast<const float*>(smem + free_stage[w]);
           const float4 a = *reinterpret_cast<const float4*>(cells + from_cell);
           v.x = fmaf(a.x, fv, v.x), v.y = fmaf(a.y, fv, v.y), v.z = fmaf(a.z, fv, v.z), v.w = fmaf(a.w, fv, v.w);
-          l = kMore ? l + attn_lower<kMore>(o.y, o.x - top) : fmaf(o.y, f, l);
+          l = kMode != kAttnPlain ? l + attn_lower<kMode>(o.y, o.x - top) : fmaf(o.y, f, l);
         }
         if (whole) {
           item_end.store(r, d, v, top, l);
