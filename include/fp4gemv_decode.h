@@ -151,7 +151,7 @@ size_t fp4gemv_kv_attention_shared_scratch_bytes(int kv_heads, int head_dim, int
  * such sequence's row of block_table alone, the rest through each one's own.
  * How many tokens are taken together is prefix_len rounded down to a multiple
  * of 128, less where a sequence's first query stands before that; none is not an
- * error, nor is a negative prefix_len.  Two launches.
+ * error, nor is a negative prefix_len.  Three launches.
  * scratch: 16-byte aligned, fp4gemv_kv_attention_shared_scratch_bytes; the
  * workspace is fp4gemv_kv_attention's.
  * Numerics as fp4gemv_kv_attention's of up to 16 rows: exact f16 operands,

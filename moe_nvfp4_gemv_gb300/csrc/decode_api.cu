@@ -237,13 +237,13 @@ static int64_t shared_items(int64_t rows, int dim) {
   const int slots = fp4::kv_prefix_slots(dim);
   return (shared_blocks(rows) + slots - 1) / slots;
 }
-// [tokens taken together | (m, sum of weights) of every row | sums]
+// [tokens taken together | (m, sum of weights) of the pieces' rows | their sums | those of the rows' own tokens | sums]
 static size_t shared_ml_bytes(int64_t pieces, int dim) {
   return static_cast<size_t>(pieces) * fp4::kv_prefix_slots(dim) * 128 * 8;
 }
 static size_t shared_scratch_bytes(int kv_heads, int dim, int64_t rows, int sms) {
   const int64_t pieces = sms + kv_heads * shared_items(rows, dim);
-  return 16 + shared_ml_bytes(pieces, dim) * (1 + dim / 2);
+  return 16 + shared_ml_bytes(pieces, dim) * (1 + dim / 2) + static_cast<size_t>(kv_heads) * ((rows + 1) / 2 * 2) * (8 + 4 * dim);
 }
 
 // Fills p, *row_units and *sms.
@@ -406,11 +406,16 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
   if (st != FP4GEMV_OK) return st;
   const int dim = cache->head_dim, int8 = cache->format == FP4GEMV_KV_INT8;
   const int64_t all_rows = static_cast<int64_t>(B) * q_len * p.group, items = shared_items(all_rows, dim);
+  const int64_t piece_ml = shared_ml_bytes(sms + cache->kv_heads * items, dim);
+  const int64_t own_ml = static_cast<int64_t>(cache->kv_heads) * ((all_rows + 1) / 2 * 2) * 8;  // (16-byte places)
+  char* at = static_cast<char*>(scratch);
   fp4::KvPrefixParams x = {};
-  x.line.tokens = static_cast<const int32_t*>(scratch);
-  x.line.ml = reinterpret_cast<float2*>(static_cast<char*>(scratch) + 16);
-  x.line.sums = reinterpret_cast<float*>(reinterpret_cast<char*>(x.line.ml) +
-                                         shared_ml_bytes(sms + cache->kv_heads * items, dim));
+  x.line.tokens = reinterpret_cast<int32_t*>(at);
+  x.line.ml = reinterpret_cast<float2*>(at += 16);
+  x.line.sums = reinterpret_cast<float*>(at += piece_ml);
+  p.ml = reinterpret_cast<float2*>(at += piece_ml * (dim / 2));
+  p.sums = reinterpret_cast<float*>(at += own_ml);
+  p.prefix_len = prefix_len;
   x.line.slots = fp4::kv_prefix_slots(dim);
   x.line.tile = fp4::kv_prefix_tile(dim);
   x.line.blocks = static_cast<int>(shared_blocks(all_rows));
@@ -428,7 +433,6 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
   x.lens = seq_lens;
   x.prefix_len = prefix_len;
   x.err = p.err;
-  x.tokens = static_cast<int32_t*>(scratch);
   x.B = B;
   x.max_blocks = max_blocks;
   x.num_blocks = cache->num_blocks;
@@ -438,12 +442,28 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
   x.q_len = q_len;
   x.f16 = p.f16;
   x.sm_scale = sm_scale;
-  p.line = x.line;
+  fp4::KvJoinParams y = {};
+  y.line = x.line;
+  y.sums = p.sums;
+  y.ml = p.ml;
+  y.lens = seq_lens;
+  y.out = p.out;
+  y.ldo = ldo;
+  y.lse = lse;
+  y.B = B;
+  y.kv_heads = cache->kv_heads;
+  y.group = p.group;
+  y.q_len = q_len;
+  y.f16 = p.f16;
+  // the own tokens first: the beginning's kernel, which needs whole SMs, starts where its CTAs end
   fp4::count_launch();
-  const cudaError_t e = fp4::launch_kv_prefix(x, dim, int8, pdl, stream);
+  cudaError_t e = fp4::launch_kv_attention_rest(p, dim, int8, row_units, sms, pdl, stream);
   if (e != cudaSuccess) return from_cuda(e);
   fp4::count_launch();
-  return from_cuda(fp4::launch_kv_attention_rest(p, dim, int8, row_units, sms, pdl, stream));
+  e = fp4::launch_kv_prefix(x, dim, int8, pdl, stream);
+  if (e != cudaSuccess) return from_cuda(e);
+  fp4::count_launch();
+  return from_cuda(fp4::launch_kv_join(y, dim, pdl, stream));
 }
 
 fp4gemv_status fp4gemv_moe_route(const void* logits, int64_t ldl, int dtype, int M, int E, int topk, int scores,

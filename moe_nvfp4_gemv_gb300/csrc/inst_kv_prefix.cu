@@ -37,4 +37,26 @@ cudaError_t launch_kv_prefix(const KvPrefixParams& p, int dim, int int8, int pdl
   }
 }
 
+template <int kDim>
+static cudaError_t join_typed(const KvJoinParams& p, int pdl, cudaStream_t stream) {
+  const int64_t cells = static_cast<int64_t>(p.B) * p.q_len * p.group * p.kv_heads * (kDim / 4);
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(static_cast<unsigned>((cells + kJoinThreads - 1) / kJoinThreads), 1, 1);
+  lc.blockDim = dim3(kJoinThreads, 1, 1);
+  lc.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &attr;
+  lc.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&lc, kv_join_kernel<kDim>, p);
+}
+
+cudaError_t launch_kv_join(const KvJoinParams& p, int dim, int pdl, cudaStream_t stream) {
+  return dim == 64    ? join_typed<64>(p, pdl, stream)
+         : dim == 96  ? join_typed<96>(p, pdl, stream)
+         : dim == 128 ? join_typed<128>(p, pdl, stream)
+                      : join_typed<256>(p, pdl, stream);
+}
+
 }  // namespace fp4

@@ -95,23 +95,8 @@ struct KvAttnParams {
   float sm_scale;
 };
 
-// The tiles of a beginning that the sequences share (k_kv_prefix.cuh) on their line, and what their sums are.
-struct KvPrefixLine {
-  const int32_t* tokens;  // [1], device: how many tokens were taken together
-  float* sums;            // [piece][slot][128 rows][dim]
-  float2* ml;             // [piece][slot][128 rows]: m, the sum of weights
-  int ctas;
-  int blocks;             // of 128 rows
-  int items;              // of a KV head
-  int slots;
-  int tile;               // tokens
-};
-
-// A share of the line: pieces are numbered by CTA + item, which never repeats.
-__host__ __device__ inline int prefix_share(int tiles, int ctas) { return (tiles + ctas - 1) / ctas; }
-
 // What a kernel does beyond a window: first tokens that stay visible in it; or the rest of sequences whose beginning
-// another kernel has taken.
+// another kernel takes.
 enum AttnMode { kAttnPlain, kAttnSinks, kAttnRest };
 // A sequence's items hold `lead` strips of its beginning, then those of its window, with a gap between them that counts as
 // no strips.
@@ -119,14 +104,31 @@ struct KvAttnSinksParams : KvAttnParams {
   int sinks;  // the first tokens that stay visible
   int lead;   // their strips
 };
-// The beginning's strips count as none, and its sums are joined with an item's.
+// The beginning's strips count as none; a row's sums are left as they are for k_kv_prefix.cuh's join.
 struct KvAttnRestParams : KvAttnParams {
-  KvPrefixLine line;
+  const int32_t* prefix_len;
+  float* sums;  // [kv_heads][B q_len group rows][dim]
+  float2* ml;   // [kv_heads][rows]: m, the sum of weights
 };
 template <int kMode>
 using AttnModeParams = std::conditional_t<kMode == kAttnSinks, KvAttnSinksParams,
                                           std::conditional_t<kMode == kAttnRest, KvAttnRestParams, KvAttnParams>>;
-// The tokens of the beginning that were taken (in shared memory, for the kernel's life).
+// How many tokens of a beginning of `said` tokens are taken together: a multiple of 128 before every sequence's first query.
+// By a warp; *owner: the first sequence that is not empty.
+__device__ __forceinline__ int attn_together(int said, const int32_t* lens, int B, int q_len, int64_t cap, int* owner) {
+  int low = 0x7FFFFFFF, who = 0x7FFFFFFF;
+  for (int b = threadIdx.x & 31; b < B; b += 32) {
+    const int raw = __ldcg(lens + b), n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
+    if (n > 0) {
+      low = min(low, n - q_len);  // (every row sees them, and some token is left)
+      who = min(who, b);
+    }
+  }
+  low = __reduce_min_sync(0xFFFFFFFFu, low);
+  *owner = __reduce_min_sync(0xFFFFFFFFu, who);
+  return *owner == 0x7FFFFFFF ? 0 : max(min(low, said), 0) & ~127;
+}
+// The same in shared memory, for the kernel's life.
 __device__ __forceinline__ int& attn_taken() {
   __shared__ int taken;
   return taken;
@@ -495,45 +497,6 @@ __device__ __forceinline__ void attn_put(float4 v, float top, float l, uint16_t*
   if (lse) *lse = l > 0.0f ? 0.6931471805599453f * (top + log2f(l)) : l == l ? -__builtin_huge_valf() : l;
 }
 
-// The same with the sums of `cnt` pieces of the taken beginning: the row's (m, sum of weights) from ml on, the dims' sums
-// from `sums` on, `step` pieces' slots apart.  A function of its own: its loads in flight would cost the loops over
-// tokens their registers (128 a thread: 61 us for 64 sequences of up to 701 own tokens, as a function 31).
-template <int kDim>
-__device__ __noinline__ void attn_join_taken(float4 v, float top, float l, const float2* ml, const float* sums, int step,
-                                             int cnt, uint16_t* out, float* lse, int f16) {
-  constexpr int kBatch = 8;  // pieces in flight
-#pragma unroll 1
-  for (int k = 0; k < cnt; k += kBatch) {
-    float2 cm[kBatch];
-    float4 a[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      cm[j] = make_float2(kAttnFloor, 0.0f);
-      a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (k + j < cnt) {
-        cm[j] = __ldcg(ml + static_cast<int64_t>(k + j) * step * 128);
-        a[j] = __ldcg(reinterpret_cast<const float4*>(sums + static_cast<int64_t>(k + j) * step * (128 * kDim)));
-      }
-    }
-    float mn = top;
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
-    const float fall = attn_ex2(top - mn);
-    v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall;
-    l = attn_lower<kAttnRest>(l, top - mn);
-    top = mn;
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (cm[j].y == 0.0f) a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // (a slot that had no tile wrote no sums)
-      const float f = attn_ex2(cm[j].x - mn);
-      v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
-      v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
-      l += attn_lower<kAttnRest>(cm[j].y, cm[j].x - mn);
-    }
-  }
-  attn_put(v, top, l, out, lse, f16);
-}
-
 // What follows an item's sums: row r's outputs, or its partials and their
 // joining.  A partial row holds the sums, m and the sum of weights.
 template <int kDim, int kThreads, class P = KvAttnParams>
@@ -551,26 +514,18 @@ struct AttnItemEnd {
   }
   // four outputs of local row r, dims d .. d + 3
   __device__ __forceinline__ void store(int r, int d, float4 v, float top, float l) const {
+    if constexpr (kMode == kAttnRest) {
+      const int rows = p.q_len * p.group;
+      const int64_t at = static_cast<int64_t>(cur.head) * p.B * rows + cur.b * rows + row0 + r;
+      *reinterpret_cast<float4*>(p.sums + at * kDim + d) = v;
+      if (d == 0) p.ml[at] = make_float2(top, l);
+      return;
+    }
     const int row = row0 + r, i = (row * p.group_magic) >> 16;
     const int64_t tok_out = static_cast<int64_t>(cur.b) * p.q_len + i;
     const int head_out = cur.head * p.group + row - i * p.group;
     uint16_t* const out = p.out + tok_out * p.ldo + head_out * kDim + d;
     float* const lse = d == 0 && p.lse ? p.lse + tok_out * (p.kv_heads * p.group) + head_out : nullptr;
-    if constexpr (kMode == kAttnRest) {
-      const KvPrefixLine& line = p.line;
-      const int tiles = attn_taken() / line.tile;
-      if (tiles > 0) {
-        const int per = prefix_share(tiles * p.kv_heads * line.items, line.ctas);
-        const int all = cur.b * p.q_len * p.group + row, block = all >> 7;
-        const int number = line.slots == 1 ? block : block >> 1;
-        const bool pair = line.slots == 2 && 2 * number + 1 < line.blocks;  // (else: slots that took the tiles by turns)
-        const int item = cur.head * line.items + number, c0 = item * tiles / per, c1 = ((item + 1) * tiles - 1) / per;
-        const int64_t at = ((static_cast<int64_t>(c0) + item) * line.slots + (pair ? block & 1 : 0)) * 128 + (all & 127);
-        attn_join_taken<kDim>(v, top, l, line.ml + at, line.sums + at * kDim + d, pair ? 2 : 1,
-                              (c1 - c0 + 1) * (line.slots == 1 || pair ? 1 : 2), out, lse, p.f16);
-        return;
-      }
-    }
     attn_put(v, top, l, out, lse, p.f16);
   }
   // Behind the CTA's partial: the last CTA of those that share the item joins
@@ -845,7 +800,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
   int* const strips_before = reinterpret_cast<int*>(row_scale + C::kRows);
   int* const line_before = strips_before + p.B + 1;
   int* const tokens = line_before + p.B + 1;
-  if (tid == 0) pdl_launch_dependents();
+  if (kMode != kAttnRest && tid == 0) pdl_launch_dependents();
   if (!kInt8) {
     for (int i = tid; i < C::kRows * (kDim / 32); i += C::kThreads) (&nan_dims[0][0])[i] = 0u;
     if (tid == 0) nan_any = 0;
@@ -866,8 +821,13 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
     }
   }
   if constexpr (kMode == kAttnRest) {
+    // (the kernel that takes the beginning may start now: what this one waited for is there)
+    if (tid == 0) pdl_launch_dependents();
     if (warp == 0) {  // (the plan is the first warp's, and ends with a barrier)
-      if (lane == 0) attn_taken() = __ldcg(p.line.tokens);
+      int owner;
+      const int taken = attn_together(__ldcg(p.prefix_len), p.lens, p.B, p.q_len,
+                                      static_cast<int64_t>(p.max_blocks) << p.block_log2, &owner);
+      if (lane == 0) attn_taken() = taken;
       __syncwarp();
     }
   }
@@ -876,7 +836,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
   attn_plan<C::kThreads>(p, strips_before, line_before, tokens, plan_words, places);
   const int begin = plan_words[0], end = plan_words[1];
 
-  attn_empty<kDim, C::kThreads>(p, tokens);
+  if (kMode != kAttnRest) attn_empty<kDim, C::kThreads>(p, tokens);  // (the join sees to them)
   if (begin >= end) return;
 
   // ---- queries: f16 operands; bf16 ones scaled by a power of two for each row ----

@@ -36,6 +36,21 @@
 
 namespace fp4 {
 
+// The tiles of a beginning that the sequences share (k_kv_prefix.cuh) on their line, and what their sums are.
+struct KvPrefixLine {
+  int32_t* tokens;        // [1]: how many tokens were taken together
+  float* sums;            // [piece][slot][128 rows][dim]
+  float2* ml;             // [piece][slot][128 rows]: m, the sum of weights
+  int ctas;
+  int blocks;             // of 128 rows
+  int items;              // of a KV head
+  int slots;
+  int tile;               // tokens
+};
+
+// A share of the line: pieces are numbered by CTA + item, which never repeats.
+__host__ __device__ inline int prefix_share(int tiles, int ctas) { return (tiles + ctas - 1) / ctas; }
+
 struct KvPrefixParams {
   const uint8_t* k_codes;
   const uint8_t* v_codes;
@@ -47,7 +62,6 @@ struct KvPrefixParams {
   const int32_t* lens;
   const int32_t* prefix_len;
   uint32_t* err;
-  int32_t* tokens;  // KvPrefixLine's
   KvPrefixLine line;
   int B, max_blocks, num_blocks, block_log2;
   int kv_heads, group, q_len;
@@ -60,22 +74,25 @@ struct PrefixCfg {
   static constexpr int kTile = kDim == 256 ? 64 : 128;  // tokens
   static constexpr int kSlots = kDim == 256 ? 1 : 2;    // accumulators
   static constexpr int kWeighers = kSlots * 128;
-  static constexpr int kMovers = 256;                   // 128 threads for K, 128 for V
-  static constexpr int kThreads = kWeighers + kMovers + 32;
+  static constexpr int kMovers = 7;                     // warps
+  static constexpr int kThreads = kWeighers + kMovers * 32 + 32;
   static constexpr int kDimBlocks = (kDim + 63) / 64;
   static constexpr int kBlockBytes = kTile * 128;       // a tile's 64 dims
   static constexpr int kTileBytes = kDimBlocks * kBlockBytes;
   static constexpr int kQBytes = kDimBlocks * 128 * 128;
   static constexpr int kStages = 2;
   static constexpr int kGroups = kTile / 16;            // of 16 tokens: no page is smaller
-  // Q | K ring | V ring | scales [stage][K factor, log2 vs, 1 / vs][group of 16] | row factors
+  // Q | K ring | V ring | scales [stage][group of 16](K factor, log2 vs, 1 / vs, -) | row factors
   static constexpr int kKOff = kSlots * kQBytes;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
   static constexpr int kScaleOff = kVOff + kStages * kTileBytes;
-  static constexpr int kRowOff = kScaleOff + kStages * 3 * 8 * 4;
+  static constexpr int kRowOff = kScaleOff + kStages * kGroups * 16;
   static constexpr int kSmem = 1024 + kRowOff + kSlots * 128 * 4;
   static constexpr uint32_t kCols = 512;                // TMEM: S of 128 columns twice, accumulators from 256 on
-  static constexpr int kChunks = kTile * (kDim / 16) / 128;  // of 16 codes, per mover
+  static constexpr int kParts = kTile / 32;             // of 32 tokens: what a weigher holds in registers
+  // Movers' jobs: 16 tokens of K or of V, K's of a tile first.
+  static constexpr int kJobs = 2 * kGroups;
+  static constexpr int kChunks = kDim / 32;             // of 16 codes, per lane and job
 };
 
 // kind::f16, f16 A and B, fp32 D; B K-major, or N-major
@@ -88,13 +105,71 @@ __device__ __forceinline__ uint64_t sdesc_n_major_f16(uint32_t saddr, uint32_t b
   return (sdesc_sw128(saddr) & ~(static_cast<uint64_t>(0x3FFF) << 16)) | (static_cast<uint64_t>(block_bytes >> 4) << 16);
 }
 
+// 32 consecutive columns of the lane, on their way until tmem_here.
+__device__ __forceinline__ void tmem_fetch32(uint32_t taddr, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// (the values pass through the wait, so that nothing that uses them moves before it)
+__device__ __forceinline__ void tmem_here(float (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+                 "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]),
+                 "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                 "+f"(r[30]), "+f"(r[31])
+               :
+               : "memory");
+}
+// `columns` (a multiple of 32) sums of the lane times f.
+inline __device__ __noinline__ void prefix_rescale(uint32_t cols, int columns, float f) {
+#pragma unroll 1
+  for (int c = 0; c < columns; c += 32) {
+    float o[32];
+    uint32_t w[16];
+    tmem_get32(cols + c, o);
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[h + i] * f);
+      tmem_st16(cols + c + h, w);
+    }
+  }
+  tmem_wait_st();
+}
+// 32 weights (two to a column) of the lane times f, a power of two.
+inline __device__ __noinline__ void prefix_rescale_weights(uint32_t cols, float f) {
+  uint32_t a[8], b[8], w[16];
+  tmem_wait_st();  // (they may be on their way)
+  tmem_ld8(cols, a);
+  tmem_ld8(cols + 8, b);
+  tmem_wait_ld();
+  const __half2 f2 = __float2half2_rn(f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&a[i]), f2);
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&b[i]), f2);
+    w[i] = *reinterpret_cast<const uint32_t*>(&x);
+    w[8 + i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  tmem_st16(cols, w);
+  tmem_wait_st();
+}
+
 template <int kDim, bool kInt8>
 __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel(const KvPrefixParams p) {
   using C = PrefixCfg<kDim>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[4 * C::kStages + 2 * 3 + 2];
+  __shared__ __align__(8) uint64_t bars[4 * C::kStages + 2 * 5 + 2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int least, first_alive;
+  __shared__ int together_s, owner_s;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (swizzle atoms of 1024 bytes)
@@ -104,59 +179,53 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
   auto v_full = [&](int s) -> uint32_t { return bar0 + 8 * (2 * C::kStages + s); };
   auto v_empty = [&](int s) -> uint32_t { return bar0 + 8 * (3 * C::kStages + s); };
   auto scored = [&](int b) -> uint32_t { return bar0 + 8 * (4 * C::kStages + b); };       // S is there
-  auto weighed = [&](int b) -> uint32_t { return bar0 + 8 * (4 * C::kStages + 2 + b); };  // P is there, S is read
-  auto added = [&](int b) -> uint32_t { return bar0 + 8 * (4 * C::kStages + 4 + b); };    // the sums are
-  const uint32_t q_there = bar0 + 8 * (4 * C::kStages + 6), idle = bar0 + 8 * (4 * C::kStages + 7);
+  // half h of P is there (and of S read); its products are done; so are the second half's, the unit's sums
+  auto weighed = [&](int b, int h) -> uint32_t { return bar0 + 8 * (4 * C::kStages + 2 + 2 * b + h); };
+  auto halved = [&](int b) -> uint32_t { return bar0 + 8 * (4 * C::kStages + 6 + b); };
+  auto added = [&](int b) -> uint32_t { return bar0 + 8 * (4 * C::kStages + 8 + b); };
+  const uint32_t q_there = bar0 + 8 * (4 * C::kStages + 10), idle = bar0 + 8 * (4 * C::kStages + 11);
 
   if (tid == 0) {
     pdl_launch_dependents();
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(k_full(s), 128);
+      mbar_init(k_full(s), C::kGroups);
       mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), 128);
+      mbar_init(v_full(s), C::kGroups);
       mbar_init(v_empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(scored(b), 1);
-      mbar_init(weighed(b), 128);
+      mbar_init(weighed(b, 0), 128);
+      mbar_init(weighed(b, 1), 128);
+      mbar_init(halved(b), 1);
       mbar_init(added(b), 1);
     }
     mbar_init(q_there, C::kWeighers);
     mbar_init(idle, 1);
     mbar_fence_init();
-    least = 0x7FFFFFFF;
-    first_alive = 0x7FFFFFFF;
   }
-  pdl_wait();
-  __syncthreads();
-  // ---- how many tokens are taken together, and whose pages hold them ----
-  {
-    const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.block_log2;
-    int low = 0x7FFFFFFF, who = 0x7FFFFFFF;
-    for (int b = tid; b < p.B; b += C::kThreads) {
-      const int raw = __ldg(p.lens + b);
-      const int n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
-      if (n > 0) {
-        low = min(low, n - p.q_len);  // (before the first query: every row sees them, and some token is left)
-        who = min(who, b);
-      }
-    }
-    low = __reduce_min_sync(0xFFFFFFFFu, low);
-    who = __reduce_min_sync(0xFFFFFFFFu, who);
-    if (lane == 0 && who != 0x7FFFFFFF) {
-      atomicMin(&least, low);
-      atomicMin(&first_alive, who);
+  // What this kernel reads was there before the one in front of it (the rest of the sequences) let it start; it is waited
+  // for at the end, for those who follow.  Reads go to L2, since no wait has made the first-level cache's lines new.
+  if (warp == 0) {
+    int owner;
+    const int n = attn_together(__ldcg(p.prefix_len), p.lens, p.B, p.q_len, static_cast<int64_t>(p.max_blocks) << p.block_log2,
+                                &owner);
+    if (lane == 0) {
+      together_s = n;
+      owner_s = owner;
+      if (blockIdx.x == 0) *p.line.tokens = n;
     }
   }
   __syncthreads();
-  const int owner = first_alive;
-  const int together = owner == 0x7FFFFFFF ? 0 : max(min(least, __ldg(p.prefix_len)), 0) & ~127;
-  if (blockIdx.x == 0 && tid == 0) *p.tokens = together;
+  const int together = together_s, owner = owner_s;
   const int tiles_each = together / C::kTile, total = tiles_each * p.kv_heads * p.line.items;
   const int per = prefix_share(total, static_cast<int>(gridDim.x));
   const int begin = static_cast<int>(min(static_cast<int64_t>(per) * blockIdx.x, static_cast<int64_t>(total)));
   const int end = min(begin + per, total);
-  if (begin >= end) return;
+  if (begin >= end) {
+    pdl_wait();
+    return;
+  }
   if (warp == C::kThreads / 32 - 1) {
     tmem_alloc(smem_u32(&tmem_slot), C::kCols);
     tc_fence_before();
@@ -188,33 +257,41 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
     int tile_no = 0;        // tiles before the segment
     for (int at = begin; at < end;) {
       const int item = at / tiles_each, seg_end = min(end, (item + 1) * tiles_each), tiles = seg_end - at;
-      const bool pair = paired(item);
-      const int units = pair ? 2 * tiles : tiles;
+      const bool both = paired(item);
+      const int units = both ? 2 * tiles : tiles;
       const int head = item / p.line.items, number = item - head * p.line.items;
-      const int block = C::kSlots == 1 ? number : 2 * number + (pair ? slot : 0);
+      const int block = C::kSlots == 1 ? number : 2 * number + (both ? slot : 0);
       const bool works = C::kSlots == 1 || units > slot;
       // (no slot without work runs ahead to arrive twice in a segment's count)
       asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::kWeighers) : "memory");
       // ---- queries: eight lanes to a row, four rows of the warp at a time ----
       if (works) {
-        const float sign = p.sm_scale < 0.0f ? -1.0f : 1.0f;
-        constexpr int kQChunks = kDim / 8;              // of 16 bytes
-        constexpr int kPer = (kQChunks + 7) / 8;        // of a lane
-#pragma unroll 2
-        for (int r0 = 0; r0 < 32; r0 += 4) {
-          const int r = (warp & 3) * 32 + r0 + (lane >> 3), part = lane & 7;
-          const int gr = block * 128 + r;
-          uint4 raw[kPer];
+        const uint32_t flip = p.sm_scale < 0.0f ? 0x80008000u : 0u;  // (scores' factors are not negative)
+        constexpr int kQChunks = kDim / 8;                           // of 16 bytes
+        constexpr int kPer = (kQChunks + 7) / 8;                     // of a lane
+        constexpr int kTurns = kDim == 256 ? 4 : 8;                  // four rows each, all their loads under way at once
+        const int part = lane & 7;
+#pragma unroll 1
+        for (int t0 = 0; t0 < 8; t0 += kTurns) {
+        uint4 raws[kTurns][kPer];
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) raw[k] = make_uint4(0, 0, 0, 0);
+        for (int t = 0; t < kTurns; ++t) {
+          const int gr = block * 128 + (warp & 3) * 32 + (t0 + t) * 4 + (lane >> 3);
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) raws[t][k] = make_uint4(0, 0, 0, 0);
           if (gr < all_rows) {
             const int b = gr / rows, in = gr - b * rows, i = in / p.group;
             const uint16_t* src = p.q + (static_cast<int64_t>(b) * p.q_len + i) * p.ldq +
                                   (head * p.group + in - i * p.group) * kDim;
 #pragma unroll
             for (int k = 0; k < kPer; ++k)
-              if (part + 8 * k < kQChunks) raw[k] = __ldg(reinterpret_cast<const uint4*>(src) + part + 8 * k);
+              if (part + 8 * k < kQChunks) raws[t][k] = __ldcg(reinterpret_cast<const uint4*>(src) + part + 8 * k);
           }
+        }
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+          const int r = (warp & 3) * 32 + (t0 + t) * 4 + (lane >> 3);
+          uint4(&raw)[kPer] = raws[t];
           float factor = fabsf(p.sm_scale) * 1.4426950408889634f;
           if (!p.f16) {  // 2^-e brings the largest to [2^14, 2^15): exact f16 values
             uint32_t top = 0;
@@ -238,7 +315,6 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
             }
             factor *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
           }
-          const uint32_t flip = sign < 0.0f ? 0x80008000u : 0u;  // (scores' factors are not negative)
 #pragma unroll
           for (int k = 0; k < kPer; ++k) {
             const int c = part + 8 * k;
@@ -248,6 +324,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
           }
           if (part == 0) row_factor[r] = factor;
         }
+        }
         fence_proxy_async_smem();
       }
       __syncwarp();
@@ -255,82 +332,96 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
       mbar_arrive(q_there);
       // (the warp has a row that is one)
       const bool live = block * 128 + (row & ~31) < all_rows;
-      float m = kAttnFloor, l = 0.0f;
-      int last = -1;  // the slot's last unit's S
+      // weights are 2^(x - m), x = s + log2 vs; m moves by whole numbers, so that weights already made move exactly
+      float m = 0.0f, l = 0.0f;
+      bool fresh = true;  // no m yet
+      int last = -1;      // the slot's last unit's S
       for (int u = C::kSlots == 1 ? 0 : slot, k = 0; u < units; u += C::kSlots, ++k) {
         const int b = u & 1;
-        const int tile = tile_no + (pair ? u >> 1 : u), stage = tile % C::kStages;
+        const int tile = tile_no + (both ? u >> 1 : u), stage = tile % C::kStages;
         const int turn = turns[b] + (u >> 1);
         const uint32_t s_cols = tmem + b * 128 + lanes;
+        const uint32_t scales = sm + C::kScaleOff + stage * (C::kGroups * 16);
         wait(scored(b), turn & 1);
         wait(v_full(stage), (tile / C::kStages) & 1);  // the scales
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
-        if (live && ok) {
-          const float* const scales = reinterpret_cast<const float*>(smem + C::kScaleOff) + stage * 24;
-          float top = kAttnFloor;
+        const bool go = live && ok;
+        float x[2][32];
+        if (go) tmem_fetch32(s_cols, x[0]);
 #pragma unroll
-          for (int c = 0; c < C::kTile / 32; ++c) {
-            float x[32];
-            tmem_get32(s_cols + 32 * c, x);
+        for (int c = 0; c < C::kParts; ++c) {
+          if (go) {
+            float(&v)[32] = x[c & 1];
+            tmem_here(v);
+            if (c + 1 < C::kParts) tmem_fetch32(s_cols + 32 * (c + 1), x[(c + 1) & 1]);
+            float sum[2];
+            auto weigh = [&]() {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float most = x[16 * h];
+              for (int h = 0; h < 2; ++h) {
+                const uint4 g = lds128(scales + (2 * c + h) * 16);
+                const float f = factor * __uint_as_float(g.x), base = __uint_as_float(g.y) - m;
+                const uint64_t f2 = pair(f, f), base2 = pair(base, base);
+                uint64_t total = 0ull;
 #pragma unroll
-              for (int i = 1; i < 16; ++i) most = fmaxf(most, x[16 * h + i]);
-              top = fmaxf(top, fmaf(most, factor * scales[2 * c + h], scales[8 + 2 * c + h]));
-            }
-          }
-          if (__any_sync(0xFFFFFFFFu, top - m > kAttnLift + kAttnSlack)) {
-            const float now = fmaxf(m, top - kAttnLift), fall = attn_ex2(m - now);
-            l = attn_lower<true>(l, m - now);
-            m = now;
-            if (k > 0) {
-              // (one accumulator for both S: the other's sums may be under way)
-              if (C::kSlots == 1) {
-                wait(added(b ^ 1), (turns[b ^ 1] + ((u - 1) >> 1)) & 1);
-                tc_fence_after();
-              }
-#pragma unroll 1
-              for (int c = 0; c < kDim; c += 32) {
-                float o[32];
-                uint32_t w[16];
-                tmem_get32(o_cols + c, o);
-#pragma unroll
-                for (int h = 0; h < 32; h += 16) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[h + i] * fall);
-                  tmem_st16(o_cols + c + h, w);
+                for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+                  const float2 e = unpair(fma2(pair(v[i], v[i + 1]), f2, base2));
+                  v[i] = attn_ex2(e.x), v[i + 1] = attn_ex2(e.y);
+                  total = add2(total, pair(v[i], v[i + 1]));
                 }
+                const float2 t = unpair(total);
+                sum[h] = t.x + t.y;
               }
-              tmem_wait_st();
-            }
-          }
+            };
+            if (!fresh) weigh();
+            // (a sum below f16's largest value has no weight above it)
+            if (fresh || __any_sync(0xFFFFFFFFu, fmaxf(sum[0], sum[1]) > 65000.0f)) {
+              // (no values are held across the calls: the scores are fetched again behind them)
+              if (c + 1 < C::kParts) tmem_here(x[(c + 1) & 1]);
+              tmem_get32(s_cols + 32 * c, v);
+              float top = kAttnFloor;
 #pragma unroll
-          for (int c = 0; c < C::kTile / 32; ++c) {
-            float x[32];
-            tmem_get32(s_cols + 32 * c, x);
+              for (int h = 0; h < 2; ++h) {
+                const uint4 g = lds128(scales + (2 * c + h) * 16);
+                float most = v[16 * h];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) most = fmaxf(most, v[16 * h + i]);
+                top = fmaxf(top, fmaf(most, factor * __uint_as_float(g.x), __uint_as_float(g.y)));
+              }
+              const float want = fmaxf(ceilf(top - kAttnLift), kAttnFloor), now = fresh ? want : fmaxf(m, want);
+              if (!fresh) {
+                const float fall = attn_ex2(m - now);
+                l = attn_lower<kAttnRest>(l, m - now);
+                // the sums so far; of this unit's weights the first half's are on their way into them, later ones wait
+                if (c >= C::kParts / 2) wait(halved(b), turn & 1);
+                else if (C::kSlots == 1 && k > 0) wait(added(b ^ 1), (turns[b ^ 1] + ((u - 1) >> 1)) & 1);
+                tc_fence_after();
+                if (k > 0 || c >= C::kParts / 2) prefix_rescale(o_cols, kDim, fall);
+                for (int e = c >= C::kParts / 2 ? C::kParts / 2 : 0; e < c; ++e)
+                  prefix_rescale_weights(s_cols + 16 * e, fall);
+              }
+              m = now;
+              fresh = false;
+              tmem_get32(s_cols + 32 * c, v);
+              if (c + 1 < C::kParts) tmem_fetch32(s_cols + 32 * (c + 1), x[(c + 1) & 1]);
+              weigh();
+            }
             uint32_t w[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float f = factor * scales[2 * c + h], base = scales[8 + 2 * c + h] - m;
-              float part = 0.0f;
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const float a = attn_ex2(fmaf(x[16 * h + i], f, base)), d = attn_ex2(fmaf(x[16 * h + i + 1], f, base));
-                part += a + d;
-                w[8 * h + i / 2] = pack_f16(a, d);
-              }
-              l = fmaf(part, scales[16 + 2 * c + h], l);
-            }
+            for (int i = 0; i < 16; ++i) w[i] = pack_f16(v[2 * i], v[2 * i + 1]);
             tmem_st16(s_cols + 16 * c, w);  // (over columns that are read)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) l = fmaf(sum[h], ldsf(scales + (2 * c + h) * 16 + 8), l);
           }
-          tmem_wait_st();
+          if ((c + 1) % (C::kParts / 2) == 0) {
+            if (go) tmem_wait_st();
+            tc_fence_before();
+            if (ok) mbar_arrive(weighed(b, (c + 1) / (C::kParts / 2) - 1));
+          }
         }
-        tc_fence_before();
-        if (ok) mbar_arrive(weighed(b));
         last = b;
       }
+      m = fresh ? kAttnFloor : m;
       // ---- the segment's end: the piece's sums ----
       const int64_t piece = (static_cast<int64_t>(blockIdx.x) + item) * C::kSlots + slot;
       if (last >= 0) {
@@ -370,90 +461,106 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
       tile_no += tiles;
       at = seg_end;
     }
-  } else if (warp < (C::kWeighers + C::kMovers) / 32) {
-    // ---- movers: 128 threads for K, 128 for V: codes to f16 ----
-    const bool v = warp >= (C::kWeighers + 128) / 32;
-    const int t = (tid - C::kWeighers) & 127;
-    const uint8_t* const codes = v ? p.v_codes : p.k_codes;
-    const uint32_t ring = sm + (v ? C::kVOff : C::kKOff);
+  } else if (warp < C::kWeighers / 32 + C::kMovers) {
+    // ---- movers: codes to f16, a job of 16 tokens at a time, the next one's loads on their way ----
+    const int first = warp - C::kWeighers / 32, jobs = (end - begin) * C::kJobs;
     const int32_t* const table = p.table + static_cast<int64_t>(owner) * p.max_blocks;
-    const int64_t head_bytes = static_cast<int64_t>(kDim) << p.block_log2;
-    constexpr int kCols = kDim / 16;
-    // lane l looks up the page of the tile's tokens 16 (l mod 8): -1 past the share, -2 where there is none
-    auto look_up = [&](int at) -> int {
-      if (at >= end) return -1;
-      const int token = (at % tiles_each) * C::kTile + 16 * (lane & (C::kGroups - 1));
-      const int id = __ldg(table + (token >> p.block_log2));
-      return id >= 0 && id < p.num_blocks ? id : -2;
+    // Lane l looks up the warp's l-th next job: its strip of 16 tokens in the cache, -1 past the share, -2 for a bad page.
+    int looked = first + lane * C::kMovers;
+    auto look_up = [&]() -> int {
+      int found = -1;
+      if (looked < jobs) {
+        const int at = begin + looked / C::kJobs, item = at / tiles_each, head = item / p.line.items;
+        const int strip = (at - item * tiles_each) * C::kGroups + looked % C::kGroups, per_page = p.block_log2 - 4;
+        const int id = __ldcg(table + (strip >> per_page));
+        found = id >= 0 && id < p.num_blocks
+                    ? ((id * p.kv_heads + head) << per_page) + (strip & ((1 << per_page) - 1))
+                    : -2;
+      }
+      looked += 32 * C::kMovers;
+      return found;
     };
-    // the page and head of a tile's group of 16 tokens, and where it begins there
-    auto place_of = [&](int at, int id, int group16) -> const uint8_t* {
-      const int token = (at % tiles_each) * C::kTile + 16 * group16, head = at / tiles_each / p.line.items;
-      return codes + (static_cast<int64_t>(id) * p.kv_heads + head) * head_bytes +
-             (token & ((1 << p.block_log2) - 1)) * kDim;
+    int batch = look_up(), batch_next = look_up();
+    struct Job {
+      uint4 raw[C::kChunks];
+      float scale;  // lane 0: of K, lane 1: of V
+      int strip;
     };
-    uint4 raw[C::kChunks];
-    auto load = [&](int at, int ids) {
+    // the strip of the warp's n-th job, n within this batch or the next
+    auto strip_of = [&](int n, int now) -> int {
+      const int a = __shfl_sync(0xFFFFFFFFu, batch, n & 31), c = __shfl_sync(0xFFFFFFFFu, batch_next, n & 31);
+      return (n >> 5) == (now >> 5) ? a : c;
+    };
+    auto source = [&](int n, int strip) -> const uint8_t* {
+      const bool v = (first + n * C::kMovers) % C::kJobs >= C::kGroups;
+      return (v ? p.v_codes : p.k_codes) + static_cast<int64_t>(strip) * (16 * kDim);
+    };
+    auto load = [&](Job& job, int n, int now) {
+      job.strip = strip_of(n, now);
+      job.scale = 0.0f;
+      const uint8_t* const src = source(n, max(job.strip, 0)) + lane * 16;
 #pragma unroll
       for (int i = 0; i < C::kChunks; ++i) {
-        const int chunk = t + 128 * i, r = chunk / kCols, c = chunk - r * kCols;
-        const int id = __shfl_sync(0xFFFFFFFFu, ids, r >> 4);
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (id >= 0) raw[i] = __ldg(reinterpret_cast<const uint4*>(place_of(at, id, r >> 4) + (r & 15) * kDim) + c);
+        job.raw[i] = make_uint4(0, 0, 0, 0);
+        if (job.strip >= 0) job.raw[i] = __ldcg(reinterpret_cast<const uint4*>(src + i * 512));
       }
+      if (job.strip >= 0 && lane < 2) job.scale = __ldcg((lane ? p.v_scale : p.k_scale) + (job.strip >> (p.block_log2 - 4)));
+      // further on, to L2: the job after three more
+      const int far = strip_of(n + 3, now);
+      if (far >= 0 && lane < kDim / 8) asm volatile("prefetch.global.L2 [%0];" ::"l"(source(n + 3, far) + lane * 128));
     };
-    auto prefetch = [&](int at, int ids) {  // 128 bytes for each thread, as far as the tile has them
-      const int line = t, r = line * 128 / kDim;
-      const int id = __shfl_sync(0xFFFFFFFFu, ids, (r >> 4) & 7);
-      if (id >= 0 && r < C::kTile)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(place_of(at, id, r >> 4) + (r & 15) * kDim + line * 128 % kDim));
-    };
-    int ids[4] = {look_up(begin), look_up(begin + 1), look_up(begin + 2), look_up(begin + 3)};
-    load(begin, ids[0]);
-    prefetch(begin + 1, ids[1]);
-    prefetch(begin + 2, ids[2]);
-    for (int at = begin, tile = 0; at < end; ++at, ++tile) {
-      const int stage = tile % C::kStages;
-      const int far = look_up(at + 4);
+    auto convert = [&](const Job& job, int n) {
+      const int j = first + n * C::kMovers, tile = j / C::kJobs, kind = j % C::kJobs, stage = tile % C::kStages;
+      const bool v = kind >= C::kGroups;
+      const int group = kind % C::kGroups;
       if (tile >= C::kStages) wait(v ? v_empty(stage) : k_empty(stage), (tile / C::kStages - 1) & 1);
       ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      const uint32_t dst = ring + stage * C::kTileBytes;
+      if (!ok) return;
+      const uint32_t dst = sm + (v ? C::kVOff : C::kKOff) + stage * C::kTileBytes;
+      constexpr int kCols = kDim / 16;
 #pragma unroll
       for (int i = 0; i < C::kChunks; ++i) {
-        const int chunk = t + 128 * i, r = chunk / kCols, c = chunk - r * kCols;
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint4 h[2];
-        h[0] = make_uint4(codes2_lo<kInt8>(w[0]), codes2_hi<kInt8>(w[0]), codes2_lo<kInt8>(w[1]), codes2_hi<kInt8>(w[1]));
-        h[1] = make_uint4(codes2_lo<kInt8>(w[2]), codes2_hi<kInt8>(w[2]), codes2_lo<kInt8>(w[3]), codes2_hi<kInt8>(w[3]));
+        const int chunk = lane + 32 * i, r = chunk / kCols, c = chunk - r * kCols, row = group * 16 + r;
+        const uint32_t w[4] = {job.raw[i].x, job.raw[i].y, job.raw[i].z, job.raw[i].w};
+        const uint4 lo = make_uint4(codes2_lo<kInt8>(w[0]), codes2_hi<kInt8>(w[0]), codes2_lo<kInt8>(w[1]),
+                                    codes2_hi<kInt8>(w[1]));
+        const uint4 hi = make_uint4(codes2_lo<kInt8>(w[2]), codes2_hi<kInt8>(w[2]), codes2_lo<kInt8>(w[3]),
+                                    codes2_hi<kInt8>(w[3]));
         // (neighbours whose chunks lie in different blocks of 64 dims store their halves in the other order: no two of
         // eight lanes meet a bank)
-        const int swap = (c >> 2) & 1;
-        const uint32_t row_at = dst + (c >> 2) * C::kBlockBytes + r * 128;
-        const int pos = 2 * (c & 3);
-        sts128(row_at + (((pos + swap) ^ (r & 7)) << 4), swap ? h[1] : h[0]);
-        sts128(row_at + (((pos + 1 - swap) ^ (r & 7)) << 4), swap ? h[0] : h[1]);
+        const bool swap = (c >> 2) & 1;
+        const uint32_t to = dst + (c >> 2) * C::kBlockBytes + row * 128 + (((2 * (c & 3)) ^ (r & 7)) << 4);
+        sts128(swap ? to ^ 16 : to, swap ? hi : lo);
+        sts128(swap ? to : to ^ 16, swap ? lo : hi);
       }
-      if (v && t < C::kGroups) {
-        const int id = ids[0], head = at / tiles_each / p.line.items;
-        float ks = 0.0f, vs = 0.0f;
-        if (id >= 0) {
-          ks = __ldg(p.k_scale + static_cast<int64_t>(id) * p.kv_heads + head);
-          vs = __ldg(p.v_scale + static_cast<int64_t>(id) * p.kv_heads + head);
-        } else {
-          raise_error(p.err, FP4_ERR_BADIDX);
+      if (v) {
+        const uint32_t at = sm + C::kScaleOff + stage * (C::kGroups * 16) + group * 16;
+        if (lane == 0) {
+          stsf(at, job.scale);
+          if (job.strip < 0) raise_error(p.err, FP4_ERR_BADIDX);
+        } else if (lane == 1) {
+          const float lv = attn_lg2(fmaxf(job.scale, 7.888609052210118e-31f));
+          stsf(at + 4, lv);
+          stsf(at + 8, attn_ex2(-lv));
         }
-        const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
-        float* const scales = reinterpret_cast<float*>(smem + C::kScaleOff) + stage * 24;
-        scales[t] = ks;
-        scales[8 + t] = lv;
-        scales[16 + t] = attn_ex2(-lv);
       }
       fence_proxy_async_smem();
-      mbar_arrive(v ? v_full(stage) : k_full(stage));
-      ids[0] = ids[1], ids[1] = ids[2], ids[2] = ids[3], ids[3] = far;
-      if (at + 1 < end) load(at + 1, ids[0]);
-      prefetch(at + 3, ids[2]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v ? v_full(stage) : k_full(stage));
+    };
+    const int count = first < jobs ? (jobs - first + C::kMovers - 1) / C::kMovers : 0;  // of the warp
+    Job job[2];
+    if (count > 0) load(job[0], 0, 0);
+    for (int n = 0; n < count; n += 2) {
+      if (n > 0 && (n & 31) == 0) {
+        batch = batch_next;
+        batch_next = look_up();
+      }
+      load(job[1], n + 1, n);
+      convert(job[0], n);
+      load(job[0], n + 2, n);
+      if (n + 1 < count) convert(job[1], n + 1);
+      if (!ok) break;
     }
   } else {
     // ---- MMA warp ----
@@ -461,12 +568,12 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
     int turns[2] = {0, 0}, tile_no = 0, segment = 0;
     for (int at = begin; at < end; ++segment) {
       const int item = at / tiles_each, seg_end = min(end, (item + 1) * tiles_each), tiles = seg_end - at;
-      const bool pair = paired(item);
-      const int units = pair ? 2 * tiles : tiles;
+      const bool both = paired(item);
+      const int units = both ? 2 * tiles : tiles;
       wait(q_there, segment & 1);
       tc_fence_after();
       auto score = [&](int u) {
-        const int b = u & 1, tile = tile_no + (pair ? u >> 1 : u), stage = tile % C::kStages;
+        const int b = u & 1, tile = tile_no + (both ? u >> 1 : u), stage = tile % C::kStages;
         wait(k_full(stage), (tile / C::kStages) & 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
@@ -478,28 +585,34 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
             mma_ss(tmem + b * 128, q_desc + (k >> 2) * (128 * 128 >> 4) + 2 * (k & 3),
                    k_desc + (k >> 2) * (C::kBlockBytes >> 4) + 2 * (k & 3), id_s, k > 0);
           mma_commit(scored(b));
-          if (!pair || b == 1) mma_commit(k_empty(stage));
+          if (!both || b == 1) mma_commit(k_empty(stage));
         }
         __syncwarp();
       };
       score(0);
       if (units > 1) score(1);
       for (int u = 0; u < units; ++u) {
-        const int b = u & 1, tile = tile_no + (pair ? u >> 1 : u), stage = tile % C::kStages;
-        wait(weighed(b), (turns[b] + (u >> 1)) & 1);
+        const int b = u & 1, tile = tile_no + (both ? u >> 1 : u), stage = tile % C::kStages;
+        const uint64_t v_desc = sdesc_n_major_f16(sm + C::kVOff + stage * C::kTileBytes, C::kBlockBytes);
+        const uint32_t o = tmem + 256 + (C::kSlots == 2 ? b : 0) * 128;
+        const bool more = C::kSlots == 2 ? u > 1 : u > 0;  // (there are sums to add to)
         wait(v_full(stage), (tile / C::kStages) & 1);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        tc_fence_after();
-        if (ok && elect_one()) {
-          const uint64_t v_desc = sdesc_n_major_f16(sm + C::kVOff + stage * C::kTileBytes, C::kBlockBytes);
-          const uint32_t o = tmem + 256 + (C::kSlots == 2 ? b : 0) * 128;
 #pragma unroll
-          for (int k = 0; k < C::kTile / 16; ++k)  // 16 tokens each, 2048 bytes
-            mma_ts(o, tmem + b * 128 + 8 * k, v_desc + 128 * k, id_o, (C::kSlots == 2 ? u > 1 : u > 0) || k > 0);
-          mma_commit(added(b));
-          if (!pair || b == 1) mma_commit(v_empty(stage));
+        for (int h = 0; h < 2; ++h) {
+          wait(weighed(b, h), (turns[b] + (u >> 1)) & 1);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          tc_fence_after();
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int k = 0; k < C::kTile / 32; ++k) {  // 16 tokens each, 2048 bytes
+              const int step = h * (C::kTile / 32) + k;
+              mma_ts(o, tmem + b * 128 + 8 * step, v_desc + 128 * step, id_o, more || step > 0);
+            }
+            mma_commit(h == 0 ? halved(b) : added(b));
+            if (h == 1 && (!both || b == 1)) mma_commit(v_empty(stage));
+          }
+          __syncwarp();
         }
-        __syncwarp();
         if (u + 2 < units) score(u + 2);
       }
       turns[0] += (units + 1) / 2;
@@ -516,6 +629,87 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
+  pdl_wait();
+}
+
+struct KvJoinParams {
+  KvPrefixLine line;
+  const float* sums;  // of the sequences' own tokens (KvAttnRestParams)
+  const float2* ml;
+  const int32_t* lens;
+  uint16_t* out;
+  int64_t ldo;
+  float* lse;
+  int B, kv_heads, group, q_len, f16;
+};
+constexpr int kJoinThreads = 256;
+
+// Own sums and the pieces of the beginning's to outputs: a thread for four dims of a row, kBatch pieces' loads under way.
+template <int kDim>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvJoinParams p) {
+  constexpr int kBatch = 8, kCells = kDim / 4;
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  pdl_wait();
+  const KvPrefixLine& line = p.line;
+  const int rows = p.q_len * p.group, all_rows = p.B * rows;
+  const int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
+  const int64_t at = x / kCells;
+  const int d = static_cast<int>(x - at * kCells) * 4;
+  if (at >= static_cast<int64_t>(all_rows) * p.kv_heads) return;
+  const int head = static_cast<int>(at / all_rows), all = static_cast<int>(at - static_cast<int64_t>(head) * all_rows);
+  const int b = all / rows, in = all - b * rows, i = in / p.group;
+  const int64_t token = static_cast<int64_t>(b) * p.q_len + i;
+  const int head_out = head * p.group + in - i * p.group;
+  uint16_t* const out = p.out + token * p.ldo + head_out * kDim + d;
+  float* const lse = d == 0 && p.lse ? p.lse + token * (p.kv_heads * p.group) + head_out : nullptr;
+  if (__ldg(p.lens + b) <= 0) {
+    attn_put(make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f, out, lse, p.f16);
+    return;
+  }
+  const float2 own = __ldcg(p.ml + at);
+  float4 v = __ldcg(reinterpret_cast<const float4*>(p.sums + at * kDim + d));
+  float top = own.x, l = own.y;
+  const int tiles = __ldcg(line.tokens) / line.tile;
+  if (tiles > 0) {
+    const int per = prefix_share(tiles * p.kv_heads * line.items, line.ctas), block = all >> 7;
+    const int number = line.slots == 1 ? block : block >> 1;
+    const bool both = line.slots == 2 && 2 * number + 1 < line.blocks;  // (else: slots that took the tiles by turns)
+    const int item = head * line.items + number, c0 = item * tiles / per, c1 = ((item + 1) * tiles - 1) / per;
+    const int64_t piece = ((static_cast<int64_t>(c0) + item) * line.slots + (both ? block & 1 : 0)) * 128 + (all & 127);
+    const int step = both ? 2 : 1, cnt = (c1 - c0 + 1) * (line.slots == 1 || both ? 1 : 2);
+    const float2* const ml = line.ml + piece;
+    const float* const sums = line.sums + piece * kDim + d;
+#pragma unroll 1
+    for (int k = 0; k < cnt; k += kBatch) {
+      float2 cm[kBatch];
+      float4 a[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        cm[j] = make_float2(kAttnFloor, 0.0f);
+        a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k + j < cnt) {
+          cm[j] = __ldcg(ml + (k + j) * step * 128);
+          a[j] = __ldcg(reinterpret_cast<const float4*>(sums + static_cast<int64_t>(k + j) * step * (128 * kDim)));
+        }
+      }
+      float mn = top;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
+      const float fall = attn_ex2(top - mn);
+      v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall;
+      l = attn_lower<kAttnRest>(l, top - mn);
+      top = mn;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (cm[j].y == 0.0f) a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // (a slot that had no tile wrote no sums)
+        const float f = attn_ex2(cm[j].x - mn);
+        v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
+        v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
+        l += attn_lower<kAttnRest>(cm[j].y, cm[j].x - mn);
+      }
+    }
+  }
+  attn_put(v, top, l, out, lse, p.f16);
 }
 
 }  // namespace fp4
