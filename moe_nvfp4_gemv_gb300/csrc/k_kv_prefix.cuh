@@ -73,7 +73,7 @@ template <int kDim>
 struct PrefixCfg {
   static constexpr int kTile = kDim == 256 ? 64 : 128;  // tokens
   static constexpr int kSlots = kDim == 256 ? 1 : 2;    // accumulators
-  static constexpr int kWeighers = kSlots * 128;
+  static constexpr int kWeighers = kSlots * 256;        // two to a row, half a tile's tokens each
   static constexpr int kMovers = 7;                     // warps
   static constexpr int kThreads = kWeighers + kMovers * 32 + 32;
   static constexpr int kDimBlocks = (kDim + 63) / 64;
@@ -82,14 +82,17 @@ struct PrefixCfg {
   static constexpr int kQBytes = kDimBlocks * 128 * 128;
   static constexpr int kStages = 2;
   static constexpr int kGroups = kTile / 16;            // of 16 tokens: no page is smaller
-  // Q | K ring | V ring | scales [stage][group of 16](K factor, log2 vs, 1 / vs, -) | row factors
+  // Q | K ring | V ring | scales [stage][group of 16](K factor, log2 vs, 1 / vs, -) | of the slots' rows: factors; what a
+  // row's two weighers tell each other
   static constexpr int kKOff = kSlots * kQBytes;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
   static constexpr int kScaleOff = kVOff + kStages * kTileBytes;
   static constexpr int kRowOff = kScaleOff + kStages * kGroups * 16;
-  static constexpr int kSmem = 1024 + kRowOff + kSlots * 128 * 4;
+  static constexpr int kSmem = 1024 + kRowOff + kSlots * 128 * 12;
   static constexpr uint32_t kCols = 512;                // TMEM: S of 128 columns twice, accumulators from 256 on
-  static constexpr int kParts = kTile / 32;             // of 32 tokens: what a weigher holds in registers
+  static constexpr int kHalf = kTile / 2;               // a weigher's tokens of a tile
+  static constexpr int kParts = kHalf / 16;             // of 16 tokens, which share a page
+  static constexpr int kSplit = (kDim / 32 + 1) / 2 * 32;  // a row's sums up to here are its first weigher's to move
   // Movers' jobs: 16 tokens of K or of V, K's of a tile first.
   static constexpr int kJobs = 2 * kGroups;
   static constexpr int kChunks = kDim / 32;             // of 16 codes, per lane and job
@@ -105,61 +108,69 @@ __device__ __forceinline__ uint64_t sdesc_n_major_f16(uint32_t saddr, uint32_t b
   return (sdesc_sw128(saddr) & ~(static_cast<uint64_t>(0x3FFF) << 16)) | (static_cast<uint64_t>(block_bytes >> 4) << 16);
 }
 
-// 32 consecutive columns of the lane, on their way until tmem_here.
-__device__ __forceinline__ void tmem_fetch32(uint32_t taddr, float (&r)[32]) {
+// 16 consecutive columns of the lane, on their way until tmem_here.
+__device__ __forceinline__ void tmem_fetch16(uint32_t taddr, float (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
       : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
-        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
-        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
-        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(taddr)
       : "memory");
 }
 // (the values pass through the wait, so that nothing that uses them moves before it)
-__device__ __forceinline__ void tmem_here(float (&r)[32]) {
+__device__ __forceinline__ void tmem_here(float (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
-                 "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]),
-                 "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
-                 "+f"(r[30]), "+f"(r[31])
+                 "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
                :
                : "memory");
 }
-// `columns` (a multiple of 32) sums of the lane times f.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// Barrier `id` of two warps: whether v holds for any of their threads.
+__device__ __forceinline__ bool named_any_of(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %2, 0; barrier.cta.red.or.pred.aligned q, %1, 64, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"(id), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+// `columns` (a multiple of 16) sums of the lane times f.
 inline __device__ __noinline__ void prefix_rescale(uint32_t cols, int columns, float f) {
 #pragma unroll 1
-  for (int c = 0; c < columns; c += 32) {
-    float o[32];
+  for (int c = 0; c < columns; c += 16) {
+    float o[16];
     uint32_t w[16];
-    tmem_get32(cols + c, o);
+    tmem_fetch16(cols + c, o);
+    tmem_here(o);
 #pragma unroll
-    for (int h = 0; h < 32; h += 16) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[h + i] * f);
-      tmem_st16(cols + c + h, w);
-    }
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+    tmem_st16(cols + c, w);
   }
   tmem_wait_st();
 }
-// 32 weights (two to a column) of the lane times f, a power of two.
-inline __device__ __noinline__ void prefix_rescale_weights(uint32_t cols, float f) {
-  uint32_t a[8], b[8], w[16];
+// `parts` times 16 weights (two to a column) of the lane times f, a power of two.
+inline __device__ __noinline__ void prefix_rescale_weights(uint32_t cols, int parts, float f) {
   tmem_wait_st();  // (they may be on their way)
-  tmem_ld8(cols, a);
-  tmem_ld8(cols + 8, b);
-  tmem_wait_ld();
   const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+  for (int c = 0; c < parts; ++c) {
+    uint32_t w[8];
+    tmem_ld8(cols + 8 * c, w);
+    tmem_wait_ld();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&a[i]), f2);
-    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&b[i]), f2);
-    w[i] = *reinterpret_cast<const uint32_t*>(&x);
-    w[8 + i] = *reinterpret_cast<const uint32_t*>(&y);
+    for (int i = 0; i < 8; ++i) {
+      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w[i]), f2);
+      w[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    tmem_st8(cols + 8 * c, w);
   }
-  tmem_st16(cols, w);
   tmem_wait_st();
 }
 
@@ -167,7 +178,7 @@ template <int kDim, bool kInt8>
 __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel(const KvPrefixParams p) {
   using C = PrefixCfg<kDim>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[4 * C::kStages + 2 * 5 + 2];
+  __shared__ __align__(8) uint64_t bars[4 * C::kStages + 2 * 3 + 2];
   __shared__ uint32_t tmem_slot;
   __shared__ int together_s, owner_s;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -179,11 +190,9 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
   auto v_full = [&](int s) -> uint32_t { return bar0 + 8 * (2 * C::kStages + s); };
   auto v_empty = [&](int s) -> uint32_t { return bar0 + 8 * (3 * C::kStages + s); };
   auto scored = [&](int b) -> uint32_t { return bar0 + 8 * (4 * C::kStages + b); };       // S is there
-  // half h of P is there (and of S read); its products are done; so are the second half's, the unit's sums
-  auto weighed = [&](int b, int h) -> uint32_t { return bar0 + 8 * (4 * C::kStages + 2 + 2 * b + h); };
-  auto halved = [&](int b) -> uint32_t { return bar0 + 8 * (4 * C::kStages + 6 + b); };
-  auto added = [&](int b) -> uint32_t { return bar0 + 8 * (4 * C::kStages + 8 + b); };
-  const uint32_t q_there = bar0 + 8 * (4 * C::kStages + 10), idle = bar0 + 8 * (4 * C::kStages + 11);
+  auto weighed = [&](int b) -> uint32_t { return bar0 + 8 * (4 * C::kStages + 2 + b); };  // P is there, S is read
+  auto added = [&](int b) -> uint32_t { return bar0 + 8 * (4 * C::kStages + 4 + b); };    // the sums are
+  const uint32_t q_there = bar0 + 8 * (4 * C::kStages + 6), idle = bar0 + 8 * (4 * C::kStages + 7);
 
   if (tid == 0) {
     pdl_launch_dependents();
@@ -195,9 +204,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(scored(b), 1);
-      mbar_init(weighed(b, 0), 128);
-      mbar_init(weighed(b, 1), 128);
-      mbar_init(halved(b), 1);
+      mbar_init(weighed(b), 256);
       mbar_init(added(b), 1);
     }
     mbar_init(q_there, C::kWeighers);
@@ -247,12 +254,15 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
   };
 
   if (warp < C::kWeighers / 32) {
-    // ---- weights and sums: thread = row of the slot's block ----
-    const int slot = warp >> 2, row = tid & 127;
-    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    // ---- weights and sums: two threads to a row of the slot's block, half a tile's tokens each ----
+    const int slot = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
     const uint32_t o_cols = tmem + 256 + slot * 128 + lanes;
-    float* const row_factor = reinterpret_cast<float*>(smem + C::kRowOff) + slot * 128;
+    float* const row_factor = reinterpret_cast<float*>(smem + C::kRowOff) + slot * 384;
+    float* const row_said = row_factor + 128;  // [half][row]
     const uint32_t q_base = sm + slot * C::kQBytes;
+    // the two warps of the same rows; whether `v` holds for any of them
+    auto both_any = [&](bool v) -> bool { return named_any_of(2 + slot * 4 + quarter, v); };
     int turns[2] = {0, 0};  // units of each S before the segment
     int tile_no = 0;        // tiles before the segment
     for (int at = begin; at < end;) {
@@ -261,22 +271,18 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
       const int units = both ? 2 * tiles : tiles;
       const int head = item / p.line.items, number = item - head * p.line.items;
       const int block = C::kSlots == 1 ? number : 2 * number + (both ? slot : 0);
-      const bool works = C::kSlots == 1 || units > slot;
       // (no slot without work runs ahead to arrive twice in a segment's count)
       asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::kWeighers) : "memory");
-      // ---- queries: eight lanes to a row, four rows of the warp at a time ----
-      if (works) {
+      // ---- queries: eight lanes to a row, four rows of the warp at a time, all loads under way at once ----
+      if (C::kSlots == 1 || units > slot) {
         const uint32_t flip = p.sm_scale < 0.0f ? 0x80008000u : 0u;  // (scores' factors are not negative)
         constexpr int kQChunks = kDim / 8;                           // of 16 bytes
         constexpr int kPer = (kQChunks + 7) / 8;                     // of a lane
-        constexpr int kTurns = kDim == 256 ? 4 : 8;                  // four rows each, all their loads under way at once
         const int part = lane & 7;
-#pragma unroll 1
-        for (int t0 = 0; t0 < 8; t0 += kTurns) {
-        uint4 raws[kTurns][kPer];
+        uint4 raws[4][kPer];
 #pragma unroll
-        for (int t = 0; t < kTurns; ++t) {
-          const int gr = block * 128 + (warp & 3) * 32 + (t0 + t) * 4 + (lane >> 3);
+        for (int t = 0; t < 4; ++t) {
+          const int gr = block * 128 + (warp & 7) * 16 + t * 4 + (lane >> 3);
 #pragma unroll
           for (int k = 0; k < kPer; ++k) raws[t][k] = make_uint4(0, 0, 0, 0);
           if (gr < all_rows) {
@@ -289,8 +295,8 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
           }
         }
 #pragma unroll
-        for (int t = 0; t < kTurns; ++t) {
-          const int r = (warp & 3) * 32 + (t0 + t) * 4 + (lane >> 3);
+        for (int t = 0; t < 4; ++t) {
+          const int r = (warp & 7) * 16 + t * 4 + (lane >> 3);
           uint4(&raw)[kPer] = raws[t];
           float factor = fabsf(p.sm_scale) * 1.4426950408889634f;
           if (!p.f16) {  // 2^-e brings the largest to [2^14, 2^15): exact f16 values
@@ -324,15 +330,15 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
           }
           if (part == 0) row_factor[r] = factor;
         }
-        }
         fence_proxy_async_smem();
       }
-      __syncwarp();
-      const float factor = row_factor[row];
       mbar_arrive(q_there);
+      asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::kWeighers) : "memory");  // (the rows' factors are there)
+      const float factor = row_factor[row];
       // (the warp has a row that is one)
-      const bool live = block * 128 + (row & ~31) < all_rows;
-      // weights are 2^(x - m), x = s + log2 vs; m moves by whole numbers, so that weights already made move exactly
+      const bool live = block * 128 + quarter * 32 < all_rows;
+      // weights are 2^(x - m), x = s + log2 vs; m moves by whole numbers, so that weights already made move exactly; at a
+      // unit's end a row's two weighers have the same
       float m = 0.0f, l = 0.0f;
       bool fresh = true;  // no m yet
       int last = -1;      // the slot's last unit's S
@@ -340,88 +346,94 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
         const int b = u & 1;
         const int tile = tile_no + (both ? u >> 1 : u), stage = tile % C::kStages;
         const int turn = turns[b] + (u >> 1);
-        const uint32_t s_cols = tmem + b * 128 + lanes;
-        const uint32_t scales = sm + C::kScaleOff + stage * (C::kGroups * 16);
+        const uint32_t s_cols = tmem + b * 128 + half * C::kHalf + lanes;
+        const uint32_t scales = sm + C::kScaleOff + stage * (C::kGroups * 16) + half * (C::kParts * 16);
         wait(scored(b), turn & 1);
         wait(v_full(stage), (tile / C::kStages) & 1);  // the scales
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         const bool go = live && ok;
-        float x[2][32];
-        if (go) tmem_fetch32(s_cols, x[0]);
+        const float m_before = m;
+        const bool first = fresh;
+        bool moved = false;
+        if (go) {
+          float x[2][16];
+          tmem_fetch16(s_cols, x[0]);
 #pragma unroll
-        for (int c = 0; c < C::kParts; ++c) {
-          if (go) {
-            float(&v)[32] = x[c & 1];
+          for (int c = 0; c < C::kParts; ++c) {
+            float(&v)[16] = x[c & 1];
             tmem_here(v);
-            if (c + 1 < C::kParts) tmem_fetch32(s_cols + 32 * (c + 1), x[(c + 1) & 1]);
-            float sum[2];
+            if (c + 1 < C::kParts) tmem_fetch16(s_cols + 16 * (c + 1), x[(c + 1) & 1]);
+            const uint4 g = lds128(scales + c * 16);
+            const float f = factor * __uint_as_float(g.x);
+            float sum;
             auto weigh = [&]() {
+              const float base = __uint_as_float(g.y) - m;
+              const uint64_t f2 = pair(f, f), base2 = pair(base, base);
+              uint64_t total[2] = {0ull, 0ull};
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint4 g = lds128(scales + (2 * c + h) * 16);
-                const float f = factor * __uint_as_float(g.x), base = __uint_as_float(g.y) - m;
-                const uint64_t f2 = pair(f, f), base2 = pair(base, base);
-                uint64_t total = 0ull;
-#pragma unroll
-                for (int i = 16 * h; i < 16 * h + 16; i += 2) {
-                  const float2 e = unpair(fma2(pair(v[i], v[i + 1]), f2, base2));
-                  v[i] = attn_ex2(e.x), v[i + 1] = attn_ex2(e.y);
-                  total = add2(total, pair(v[i], v[i + 1]));
-                }
-                const float2 t = unpair(total);
-                sum[h] = t.x + t.y;
+              for (int i = 0; i < 16; i += 2) {
+                const float2 e = unpair(fma2(pair(v[i], v[i + 1]), f2, base2));
+                v[i] = attn_ex2(e.x), v[i + 1] = attn_ex2(e.y);
+                total[(i >> 1) & 1] = add2(total[(i >> 1) & 1], pair(v[i], v[i + 1]));
               }
+              const float2 t = unpair(add2(total[0], total[1]));
+              sum = t.x + t.y;
             };
             if (!fresh) weigh();
             // (a sum below f16's largest value has no weight above it)
-            if (fresh || __any_sync(0xFFFFFFFFu, fmaxf(sum[0], sum[1]) > 65000.0f)) {
-              // (no values are held across the calls: the scores are fetched again behind them)
+            if (fresh || __any_sync(0xFFFFFFFFu, sum > 65000.0f)) {
+              // (no values are held across the call: the scores are fetched again behind it)
               if (c + 1 < C::kParts) tmem_here(x[(c + 1) & 1]);
-              tmem_get32(s_cols + 32 * c, v);
-              float top = kAttnFloor;
+              tmem_fetch16(s_cols + 16 * c, v);
+              tmem_here(v);
+              float most = v[0];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint4 g = lds128(scales + (2 * c + h) * 16);
-                float most = v[16 * h];
-#pragma unroll
-                for (int i = 1; i < 16; ++i) most = fmaxf(most, v[16 * h + i]);
-                top = fmaxf(top, fmaf(most, factor * __uint_as_float(g.x), __uint_as_float(g.y)));
-              }
-              const float want = fmaxf(ceilf(top - kAttnLift), kAttnFloor), now = fresh ? want : fmaxf(m, want);
+              for (int i = 1; i < 16; ++i) most = fmaxf(most, v[i]);
+              const float want = fmaxf(ceilf(fmaf(most, f, __uint_as_float(g.y)) - kAttnLift), kAttnFloor);
+              const float now = fresh ? want : fmaxf(m, want);
               if (!fresh) {
-                const float fall = attn_ex2(m - now);
                 l = attn_lower<kAttnRest>(l, m - now);
-                // the sums so far; of this unit's weights the first half's are on their way into them, later ones wait
-                if (c >= C::kParts / 2) wait(halved(b), turn & 1);
-                else if (C::kSlots == 1 && k > 0) wait(added(b ^ 1), (turns[b ^ 1] + ((u - 1) >> 1)) & 1);
-                tc_fence_after();
-                if (k > 0 || c >= C::kParts / 2) prefix_rescale(o_cols, kDim, fall);
-                for (int e = c >= C::kParts / 2 ? C::kParts / 2 : 0; e < c; ++e)
-                  prefix_rescale_weights(s_cols + 16 * e, fall);
+                prefix_rescale_weights(s_cols, c, attn_ex2(m - now));
               }
               m = now;
               fresh = false;
-              tmem_get32(s_cols + 32 * c, v);
-              if (c + 1 < C::kParts) tmem_fetch32(s_cols + 32 * (c + 1), x[(c + 1) & 1]);
+              moved = true;
+              tmem_fetch16(s_cols + 16 * c, v);
+              tmem_here(v);
+              if (c + 1 < C::kParts) tmem_fetch16(s_cols + 16 * (c + 1), x[(c + 1) & 1]);
               weigh();
             }
-            uint32_t w[16];
+            l = fmaf(sum, __uint_as_float(g.z), l);
+            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = pack_f16(v[2 * i], v[2 * i + 1]);
-            tmem_st16(s_cols + 16 * c, w);  // (over columns that are read)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) l = fmaf(sum[h], ldsf(scales + (2 * c + h) * 16 + 8), l);
+            for (int i = 0; i < 8; ++i) w[i] = pack_f16(v[2 * i], v[2 * i + 1]);
+            tmem_st8(s_cols + 8 * c, w);  // (over columns that are read)
           }
-          if ((c + 1) % (C::kParts / 2) == 0) {
-            if (go) tmem_wait_st();
-            tc_fence_before();
-            if (ok) mbar_arrive(weighed(b, (c + 1) / (C::kParts / 2) - 1));
-          }
+          tmem_wait_st();
         }
+        if (both_any(moved)) {
+          // one of the row's weighers has another m: the larger one for both
+          row_said[half * 128 + row] = m;
+          both_any(false);
+          const float now = fmaxf(m, row_said[(half ^ 1) * 128 + row]);
+          if (go) {
+            l = attn_lower<kAttnRest>(l, m - now);
+            prefix_rescale_weights(s_cols, C::kParts, attn_ex2(m - now));
+            if (!first) {
+              if (C::kSlots == 1) {  // (one accumulator for both S: the other's sums may be under way)
+                wait(added(b ^ 1), (turns[b ^ 1] + ((u - 1) >> 1)) & 1);
+                tc_fence_after();
+              }
+              prefix_rescale(o_cols + half * C::kSplit, half ? kDim - C::kSplit : C::kSplit, attn_ex2(m_before - now));
+            }
+          }
+          m = now;
+        }
+        tc_fence_before();
+        if (ok) mbar_arrive(weighed(b));
         last = b;
       }
-      m = fresh ? kAttnFloor : m;
       // ---- the segment's end: the piece's sums ----
       const int64_t piece = (static_cast<int64_t>(blockIdx.x) + item) * C::kSlots + slot;
       if (last >= 0) {
@@ -430,30 +442,35 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
       tc_fence_after();
+      if (half == 1) row_said[128 + row] = ok ? l : __int_as_float(0x7FC00000);
+      both_any(false);
       if (live) {
-        float* const sums = p.line.sums + (piece * 128 + (warp & 3) * 32) * kDim;
-        const uint32_t spare = q_base + (warp & 3) * 4096;  // (the queries are of no use any more) 32 rows of 32 floats
+        float* const sums = p.line.sums + (piece * 128 + quarter * 32) * kDim;
+        const uint32_t spare = q_base + (warp & 7) * 2048;  // (the queries are of no use any more) 32 rows of 16 floats
         if (last >= 0) {
 #pragma unroll 1
-          for (int c = 0; c < kDim; c += 32) {
-            float o[32];
-            tmem_get32(o_cols + c, o);
+          for (int c = half ? C::kSplit : 0; c < (half ? kDim : C::kSplit); c += 16) {
+            float o[16];
+            tmem_fetch16(o_cols + c, o);
+            tmem_here(o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              sts128(spare + lane * 128 + ((i ^ (lane & 7)) << 4),
+            for (int i = 0; i < 4; ++i)
+              sts128(spare + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4),
                      make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
                                 __float_as_uint(o[4 * i + 3])));
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = i * 4 + (lane >> 3);
-              const uint4 v = lds128(spare + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-              __stcg(reinterpret_cast<uint4*>(sums + r * kDim + c) + (lane & 7), v);
+            for (int i = 0; i < 4; ++i) {
+              const int r = i * 8 + (lane >> 2);
+              const uint4 v = lds128(spare + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+              __stcg(reinterpret_cast<uint4*>(sums + r * kDim + c) + (lane & 3), v);
             }
             __syncwarp();
           }
         }
-        __stcg(p.line.ml + piece * 128 + row, make_float2(m, ok ? l : __int_as_float(0x7FC00000)));
+        if (half == 0)
+          __stcg(p.line.ml + piece * 128 + row,
+                 make_float2(fresh ? kAttnFloor : m, ok ? l + row_said[128 + row] : __int_as_float(0x7FC00000)));
       }
       tc_fence_before();
       turns[0] += (units + 1) / 2;
@@ -597,22 +614,17 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
         const uint32_t o = tmem + 256 + (C::kSlots == 2 ? b : 0) * 128;
         const bool more = C::kSlots == 2 ? u > 1 : u > 0;  // (there are sums to add to)
         wait(v_full(stage), (tile / C::kStages) & 1);
+        wait(weighed(b), (turns[b] + (u >> 1)) & 1);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+        if (ok && elect_one()) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          wait(weighed(b, h), (turns[b] + (u >> 1)) & 1);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          tc_fence_after();
-          if (ok && elect_one()) {
-#pragma unroll
-            for (int k = 0; k < C::kTile / 32; ++k) {  // 16 tokens each, 2048 bytes
-              const int step = h * (C::kTile / 32) + k;
-              mma_ts(o, tmem + b * 128 + 8 * step, v_desc + 128 * step, id_o, more || step > 0);
-            }
-            mma_commit(h == 0 ? halved(b) : added(b));
-            if (h == 1 && (!both || b == 1)) mma_commit(v_empty(stage));
-          }
-          __syncwarp();
+          for (int k = 0; k < C::kTile / 16; ++k)  // 16 tokens each, 2048 bytes; P of a half lies where its S did
+            mma_ts(o, tmem + b * 128 + k / C::kParts * C::kHalf + 8 * (k % C::kParts), v_desc + 128 * k, id_o, more || k > 0);
+          mma_commit(added(b));
+          if (!both || b == 1) mma_commit(v_empty(stage));
         }
+        __syncwarp();
         if (u + 2 < units) score(u + 2);
       }
       turns[0] += (units + 1) / 2;
