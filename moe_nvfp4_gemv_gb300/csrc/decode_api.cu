@@ -396,8 +396,9 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
                                            int heads, int q_len, const int32_t* block_table, int max_blocks,
                                            const int32_t* seq_lens, int B, const int32_t* prefix_len, float sm_scale,
                                            void* out, int64_t ldo, float* lse, void* workspace,
-                                           size_t workspace_bytes, void* scratch, size_t scratch_bytes, int pdl,
-                                           cudaStream_t stream) {
+                                           size_t workspace_bytes, void* scratch, size_t scratch_bytes, int always,
+                                           int pdl, cudaStream_t stream) {
+  if (always != 0 && always != 1) return FP4GEMV_ERR_INVALID_ARG;
   const AttentionCall a = {cache, q, ldq, dtype, heads, q_len, block_table, max_blocks, seq_lens, B, sm_scale, 0, out, ldo,
                            lse, workspace, workspace_bytes, pdl, true, prefix_len, scratch, scratch_bytes};
   fp4::KvAttnRestParams p = {};
@@ -405,6 +406,11 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
   const fp4gemv_status st = attention_params(a, &p, &row_units, &sms);
   if (st != FP4GEMV_OK) return st;
   const int dim = cache->head_dim, int8 = cache->format == FP4GEMV_KV_INT8;
+  // Where reading a common beginning again and again, out of L2, costs less than two more launches and a beginning cut over
+  // all SMs.  Apart / together, us, heads of 128, E4M3: 4 sequences of 1077 tokens, 8 KV heads (9 MB) 8.9 / 15.1; 16 of 2112
+  // (69 MB) 17 / 26; 8 of 8256 (135 MB) 30 / 29; 16 of 8256 (271 MB) 46 / 31; heads of 256, 32 of 576 (75 MB) 23 / 21.
+  const double apart = static_cast<double>(max_blocks) * cache->block_size * B * cache->kv_heads * dim * 2;
+  if (!always && apart <= FP4GEMV_KV_SHARE_FROM) return plain_attention(a, p, row_units, sms, stream);
   const int64_t all_rows = static_cast<int64_t>(B) * q_len * p.group, items = shared_items(all_rows, dim);
   const int64_t piece_ml = shared_ml_bytes(sms + cache->kv_heads * items, dim);
   const int64_t own_ml = static_cast<int64_t>(cache->kv_heads) * ((all_rows + 1) / 2 * 2) * 8;  // (16-byte places)

@@ -72,6 +72,10 @@ struct KvPrefixParams {
 template <int kDim>
 struct PrefixCfg {
   static constexpr int kTile = kDim == 256 ? 64 : 128;  // tokens
+  // Queries lie in tensor memory where there is room: the products then read K alone from shared memory, whose bandwidth
+  // they share with the movers.  (128 dims with room made by tiles of 64 tokens: 86 us instead of 72.5, 64 sequences on
+  // 32768 tokens; 256 dims 41 instead of 43, 7 sequences on 65536.)
+  static constexpr bool kQInTmem = kDim == 64 || kDim == 256;
   static constexpr int kSlots = kDim == 256 ? 1 : 2;    // accumulators
   static constexpr int kWeighers = kSlots * 256;        // two to a row, half a tile's tokens each
   static constexpr int kMovers = 7;                     // warps
@@ -79,23 +83,26 @@ struct PrefixCfg {
   static constexpr int kDimBlocks = (kDim + 63) / 64;
   static constexpr int kBlockBytes = kTile * 128;       // a tile's 64 dims
   static constexpr int kTileBytes = kDimBlocks * kBlockBytes;
-  static constexpr int kQBytes = kDimBlocks * 128 * 128;
-  static constexpr int kStages = 2;
+  static constexpr int kStages = kDim == 256 ? 3 : kDim == 64 ? 4 : 2;
+  static constexpr int kQBytes = kQInTmem ? 0 : kDimBlocks * 128 * 128;  // of a slot
   static constexpr int kGroups = kTile / 16;            // of 16 tokens: no page is smaller
-  // Q | K ring | V ring | scales [stage][group of 16](K factor, log2 vs, 1 / vs, -) | of the slots' rows: factors; what a
-  // row's two weighers tell each other
-  static constexpr int kKOff = kSlots * kQBytes;
-  static constexpr int kVOff = kKOff + kStages * kTileBytes;
-  static constexpr int kScaleOff = kVOff + kStages * kTileBytes;
-  static constexpr int kRowOff = kScaleOff + kStages * kGroups * 16;
-  static constexpr int kSmem = 1024 + kRowOff + kSlots * 128 * 12;
-  static constexpr uint32_t kCols = 512;                // TMEM: S of 128 columns twice, accumulators from 256 on
   static constexpr int kHalf = kTile / 2;               // a weigher's tokens of a tile
   static constexpr int kParts = kHalf / 16;             // of 16 tokens, which share a page
-  static constexpr int kSplit = (kDim / 32 + 1) / 2 * 32;  // a row's sums up to here are its first weigher's to move
+  static constexpr int kSplit = (kDim / 32 + 1) / 2 * 32;  // a row's dims up to here are its first weigher's to move
   // Movers' jobs: 16 tokens of K or of V, K's of a tile first.
   static constexpr int kJobs = 2 * kGroups;
   static constexpr int kChunks = kDim / 32;             // of 16 codes, per lane and job
+  // Q | K ring | V ring | 2 KB for each weighing warp (of Q, where it is here) | scales [stage][group of 16](K factor, log2 vs, 1 / vs, -) | what a row's
+  // two weighers tell each other [slot][half][row]
+  static constexpr int kKOff = kSlots * kQBytes;
+  static constexpr int kVOff = kKOff + kStages * kTileBytes;
+  static constexpr int kSpareOff = kVOff + kStages * kTileBytes;
+  static constexpr int kScaleOff = kSpareOff + (kQInTmem ? kWeighers / 32 * 2048 : 0);
+  static constexpr int kRowOff = kScaleOff + kStages * kGroups * 16;
+  static constexpr int kSmem = 1024 + kRowOff + kSlots * 256 * 4;
+  // TMEM columns: two S, the slots' queries, their sums
+  static constexpr uint32_t kCols = 512, kQCol = 2 * kTile, kOCol = 512 - kSlots * kDim;
+  static_assert(kQCol + (kQInTmem ? kSlots * kDim / 2 : 0) <= kOCol, "room for all");
 };
 
 // kind::f16, f16 A and B, fp32 D; B K-major, or N-major
@@ -257,10 +264,10 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
     // ---- weights and sums: two threads to a row of the slot's block, half a tile's tokens each ----
     const int slot = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
-    const uint32_t o_cols = tmem + 256 + slot * 128 + lanes;
-    float* const row_factor = reinterpret_cast<float*>(smem + C::kRowOff) + slot * 384;
-    float* const row_said = row_factor + 128;  // [half][row]
+    const uint32_t o_cols = tmem + C::kOCol + slot * kDim + lanes, q_cols = tmem + C::kQCol + slot * (kDim / 2) + lanes;
+    float* const row_said = reinterpret_cast<float*>(smem + C::kRowOff) + slot * 256;  // [half][row]
     const uint32_t q_base = sm + slot * C::kQBytes;
+    const uint32_t spare = C::kQInTmem ? sm + C::kSpareOff + warp * 2048 : q_base + (warp & 7) * 2048;  // 32 rows of 64 bytes
     // the two warps of the same rows; whether `v` holds for any of them
     auto both_any = [&](bool v) -> bool { return named_any_of(2 + slot * 4 + quarter, v); };
     int turns[2] = {0, 0};  // units of each S before the segment
@@ -273,68 +280,91 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
       const int block = C::kSlots == 1 ? number : 2 * number + (both ? slot : 0);
       // (no slot without work runs ahead to arrive twice in a segment's count)
       asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::kWeighers) : "memory");
-      // ---- queries: eight lanes to a row, four rows of the warp at a time, all loads under way at once ----
+      // ---- queries: four lanes to a row and 32 dims, all loads under way at once; to tensor memory through shared memory,
+      // since a lane there is a row ----
+      float factor = fabsf(p.sm_scale) * 1.4426950408889634f;
       if (C::kSlots == 1 || units > slot) {
         const uint32_t flip = p.sm_scale < 0.0f ? 0x80008000u : 0u;  // (scores' factors are not negative)
-        constexpr int kQChunks = kDim / 8;                           // of 16 bytes
-        constexpr int kPer = (kQChunks + 7) / 8;                     // of a lane
-        const int part = lane & 7;
-        uint4 raws[4][kPer];
+        constexpr int kRuns = C::kSplit / 32;                        // of 32 dims, at most
+        const int runs = half ? (kDim - C::kSplit) / 32 : kRuns, part = lane & 3;
+        uint4 raw[kRuns][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int gr = block * 128 + (warp & 7) * 16 + t * 4 + (lane >> 3);
+          const int gr = block * 128 + quarter * 32 + t * 8 + (lane >> 2);
+          const int b = gr / rows, in = gr - b * rows, i = in / p.group;
+          const uint16_t* const src = p.q + (static_cast<int64_t>(b) * p.q_len + i) * p.ldq +
+                                      (head * p.group + in - i * p.group) * kDim + half * C::kSplit + part * 8;
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) raws[t][k] = make_uint4(0, 0, 0, 0);
-          if (gr < all_rows) {
-            const int b = gr / rows, in = gr - b * rows, i = in / p.group;
-            const uint16_t* src = p.q + (static_cast<int64_t>(b) * p.q_len + i) * p.ldq +
-                                  (head * p.group + in - i * p.group) * kDim;
-#pragma unroll
-            for (int k = 0; k < kPer; ++k)
-              if (part + 8 * k < kQChunks) raws[t][k] = __ldcg(reinterpret_cast<const uint4*>(src) + part + 8 * k);
+          for (int k = 0; k < kRuns; ++k) {
+            raw[k][t] = make_uint4(0, 0, 0, 0);
+            if (gr < all_rows && k < runs) raw[k][t] = __ldcg(reinterpret_cast<const uint4*>(src + k * 32));
           }
         }
+        float down[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+        if (!p.f16) {  // 2^-e brings a row's largest to [2^14, 2^15): exact f16 values
+          uint32_t* const tops = reinterpret_cast<uint32_t*>(row_said);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int r = (warp & 7) * 16 + t * 4 + (lane >> 3);
-          uint4(&raw)[kPer] = raws[t];
-          float factor = fabsf(p.sm_scale) * 1.4426950408889634f;
-          if (!p.f16) {  // 2^-e brings the largest to [2^14, 2^15): exact f16 values
+          for (int t = 0; t < 4; ++t) {
             uint32_t top = 0;
 #pragma unroll
-            for (int k = 0; k < kPer; ++k)
-              top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[k].x & 0x7FFF7FFFu, raw[k].y & 0x7FFF7FFFu),
-                                           __vmaxu2(raw[k].z & 0x7FFF7FFFu, raw[k].w & 0x7FFF7FFFu)));
+            for (int k = 0; k < kRuns; ++k)
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[k][t].x & 0x7FFF7FFFu, raw[k][t].y & 0x7FFF7FFFu),
+                                           __vmaxu2(raw[k][t].z & 0x7FFF7FFFu, raw[k][t].w & 0x7FFF7FFFu)));
             top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const int field = static_cast<int>(top >> 7);
-            const int e = field == 0 ? 0 : min(max(field - 127 - 14, -126), 126);
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-              uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = pack_f16(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
-              raw[k] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            factor *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            if (part == 0) tops[half * 128 + quarter * 32 + t * 8 + (lane >> 2)] = top;
           }
+          both_any(false);
+          auto exponent = [&](int r) -> int {
+            const int field = static_cast<int>(max(tops[quarter * 32 + r], tops[128 + quarter * 32 + r]) >> 7);
+            return field == 0 ? 0 : min(max(field - 127 - 14, -126), 126);
+          };
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int c = part + 8 * k;
-            if (c < kQChunks)
-              sts128(q_base + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                     make_uint4(raw[k].x ^ flip, raw[k].y ^ flip, raw[k].z ^ flip, raw[k].w ^ flip));
-          }
-          if (part == 0) row_factor[r] = factor;
+          for (int t = 0; t < 4; ++t)
+            down[t] = __uint_as_float(static_cast<uint32_t>(127 - exponent(t * 8 + (lane >> 2))) << 23);
+          factor *= __uint_as_float(static_cast<uint32_t>(127 + exponent(lane)) << 23);
         }
-        fence_proxy_async_smem();
+#pragma unroll
+        for (int k = 0; k < kRuns; ++k) {
+          if (k >= runs) break;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            uint32_t w[4] = {raw[k][t].x, raw[k][t].y, raw[k][t].z, raw[k][t].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (!p.f16)
+                w[j] = pack_f16(__uint_as_float(w[j] << 16) * down[t], __uint_as_float(w[j] & 0xFFFF0000u) * down[t]);
+              w[j] ^= flip;
+            }
+            const int r = t * 8 + (lane >> 2);
+            if (C::kQInTmem) {
+              sts128(spare + r * 64 + ((part ^ ((r >> 1) & 3)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+            } else {
+              const int c = (half * C::kSplit + k * 32) / 8 + part;  // of 16 bytes
+              sts128(q_base + (c >> 3) * (128 * 128) + (quarter * 32 + r) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                     make_uint4(w[0], w[1], w[2], w[3]));
+            }
+          }
+          if (!C::kQInTmem) continue;
+          __syncwarp();
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = lds128(spare + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+          }
+          tmem_st16(q_cols + (half * C::kSplit + k * 32) / 2, w);
+          __syncwarp();
+        }
+        if (C::kQInTmem) {
+          tmem_wait_st();
+          tc_fence_before();
+        } else {
+          fence_proxy_async_smem();
+        }
       }
       mbar_arrive(q_there);
-      asm volatile("barrier.cta.sync 1, %0;" ::"n"(C::kWeighers) : "memory");  // (the rows' factors are there)
-      const float factor = row_factor[row];
       // (the warp has a row that is one)
       const bool live = block * 128 + quarter * 32 < all_rows;
       // weights are 2^(x - m), x = s + log2 vs; m moves by whole numbers, so that weights already made move exactly; at a
@@ -346,7 +376,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
         const int b = u & 1;
         const int tile = tile_no + (both ? u >> 1 : u), stage = tile % C::kStages;
         const int turn = turns[b] + (u >> 1);
-        const uint32_t s_cols = tmem + b * 128 + half * C::kHalf + lanes;
+        const uint32_t s_cols = tmem + b * C::kTile + half * C::kHalf + lanes;
         const uint32_t scales = sm + C::kScaleOff + stage * (C::kGroups * 16) + half * (C::kParts * 16);
         wait(scored(b), turn & 1);
         wait(v_full(stage), (tile / C::kStages) & 1);  // the scales
@@ -446,7 +476,6 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
       both_any(false);
       if (live) {
         float* const sums = p.line.sums + (piece * 128 + quarter * 32) * kDim;
-        const uint32_t spare = q_base + (warp & 7) * 2048;  // (the queries are of no use any more) 32 rows of 16 floats
         if (last >= 0) {
 #pragma unroll 1
           for (int c = half ? C::kSplit : 0; c < (half ? kDim : C::kSplit); c += 16) {
@@ -595,12 +624,16 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
         ok = __all_sync(0xFFFFFFFFu, ok);
         tc_fence_after();
         if (ok && elect_one()) {
-          const uint64_t q_desc = sdesc_sw128(sm + (C::kSlots == 2 ? b : 0) * C::kQBytes);
+          const int q_slot = C::kSlots == 2 ? b : 0;
           const uint64_t k_desc = sdesc_sw128(sm + C::kKOff + stage * C::kTileBytes);
+          const uint64_t q_desc = sdesc_sw128(sm + q_slot * C::kQBytes);
+          const uint32_t q = tmem + C::kQCol + q_slot * (kDim / 2);
 #pragma unroll
-          for (int k = 0; k < kDim / 16; ++k)
-            mma_ss(tmem + b * 128, q_desc + (k >> 2) * (128 * 128 >> 4) + 2 * (k & 3),
-                   k_desc + (k >> 2) * (C::kBlockBytes >> 4) + 2 * (k & 3), id_s, k > 0);
+          for (int k = 0; k < kDim / 16; ++k) {
+            const uint64_t from = k_desc + (k >> 2) * (C::kBlockBytes >> 4) + 2 * (k & 3);
+            if (C::kQInTmem) mma_ts(tmem + b * C::kTile, q + 8 * k, from, id_s, k > 0);
+            else mma_ss(tmem + b * C::kTile, q_desc + (k >> 2) * (128 * 128 >> 4) + 2 * (k & 3), from, id_s, k > 0);
+          }
           mma_commit(scored(b));
           if (!both || b == 1) mma_commit(k_empty(stage));
         }
@@ -611,7 +644,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
       for (int u = 0; u < units; ++u) {
         const int b = u & 1, tile = tile_no + (both ? u >> 1 : u), stage = tile % C::kStages;
         const uint64_t v_desc = sdesc_n_major_f16(sm + C::kVOff + stage * C::kTileBytes, C::kBlockBytes);
-        const uint32_t o = tmem + 256 + (C::kSlots == 2 ? b : 0) * 128;
+        const uint32_t o = tmem + C::kOCol + (C::kSlots == 2 ? b : 0) * kDim;
         const bool more = C::kSlots == 2 ? u > 1 : u > 0;  // (there are sums to add to)
         wait(v_full(stage), (tile / C::kStages) & 1);
         wait(weighed(b), (turns[b] + (u >> 1)) & 1);
@@ -620,7 +653,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
         if (ok && elect_one()) {
 #pragma unroll
           for (int k = 0; k < C::kTile / 16; ++k)  // 16 tokens each, 2048 bytes; P of a half lies where its S did
-            mma_ts(o, tmem + b * 128 + k / C::kParts * C::kHalf + 8 * (k % C::kParts), v_desc + 128 * k, id_o, more || k > 0);
+            mma_ts(o, tmem + b * C::kTile + k / C::kParts * C::kHalf + 8 * (k % C::kParts), v_desc + 128 * k, id_o, more || k > 0);
           mma_commit(added(b));
           if (!both || b == 1) mma_commit(v_empty(stage));
         }

@@ -360,15 +360,16 @@ PyObject* kv_attention_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// kv_attention_shared(kv_attention's, prefix_len, scratch); the window is none
+// kv_attention_shared(kv_attention's, prefix_len, scratch, always); the window is none
 PyObject* kv_attention_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 14, [&]() -> int {
+  return guarded(n, 15, [&]() -> int {
     const Attention c = attention_of(a);
     const at::Tensor &prefix = tensor(a[12], "prefix_len"), &scratch = tensor(a[13], "scratch");
     if (prefix.numel() != 1 || !plain(prefix, at::kInt, c.index))
       refuse("prefix_len must be an int32 [1] tensor on the cache's device");
     if (!scratch.is_cuda() || scratch.get_device() != c.index || !scratch.is_contiguous())
       refuse("scratch must be a contiguous tensor on the cache's device");
+    const int always = flag(a[14]);
     if (c.window != 0) refuse("no window together with a shared beginning");
     if (c.empty) return FP4GEMV_OK;
     if (c.large) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
@@ -379,7 +380,8 @@ PyObject* kv_attention_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const cudaStream_t stream = stream_of(c.index);
     return unlocked([&] {
       return g_attention_shared(c.cache, c.q, c.ldq, c.dtype, c.heads, c.q_len, c.table, c.max_blocks, c.lens, c.B, pp,
-                                c.sm_scale, c.out, c.ldo, c.lse, c.workspace, c.bytes, ps, scratch_bytes, c.pdl, stream);
+                                c.sm_scale, c.out, c.ldo, c.lse, c.workspace, c.bytes, ps, scratch_bytes, always, c.pdl,
+                                stream);
     });
   });
 }

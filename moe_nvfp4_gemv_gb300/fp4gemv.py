@@ -86,7 +86,7 @@ def _load() -> ctypes.CDLL:
                                              i64, vp, vp, sz, i32, vp]),
         "fp4gemv_kv_attention_shared_scratch_bytes": (sz, [i32, i32, i32, i32, i32]),
         "fp4gemv_kv_attention_shared": (i32, [vp, vp, i64, i32, i32, i32, vp, i32, vp, i32, vp, ctypes.c_float, vp, i64,
-                                              vp, vp, sz, vp, sz, i32, vp]),
+                                              vp, vp, sz, vp, sz, i32, i32, vp]),
         "fp4gemv_kv_read": (i32, [vp, vp, i64, vp, i64, i32, i32, vp, vp, i32, vp, i32, i32, vp]),
         "fp4gemv_add_norm": (i32, [vp, i64, i32, vp, i64, i32, vp, vp, i32, vp, i64, i32, i32, i32, ctypes.c_float,
                                    ctypes.c_float, ctypes.c_float, vp, i64, vp, i64, i32, i32, i32, vp]),

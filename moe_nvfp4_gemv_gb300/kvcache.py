@@ -121,6 +121,7 @@ class KvCache8:
                                     self.num_blocks, self.kv_heads, self.block_size, self.head_dim, FORMATS[fmt])
         self._handle = ctypes.addressof(self._struct)
         self._sm_scale = 1.0 / math.sqrt(self.head_dim)
+        self._scratch = {}  # (batch, q_len, heads): bytes of attend_shared's scratch
 
     @classmethod
     def allocate(cls, num_blocks: int, kv_heads: int, head_dim: int, block_size: int = 64, fmt: str = "e4m3",
@@ -197,24 +198,31 @@ class KvCache8:
     def attend_shared(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                       prefix_len: torch.Tensor, sm_scale: float | None = None, out: torch.Tensor | None = None,
                       lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                      scratch: torch.Tensor | None = None, pdl: bool = True) -> torch.Tensor:
+                      scratch: torch.Tensor | None = None, always: bool = False, pdl: bool = True) -> torch.Tensor:
         """``attend`` of sequences whose first ``prefix_len`` tokens (int32 [1],
         device) are the same: every sequence's row of the block table names
         pages with that beginning, usually the same ones, and what fills whole
         pages of it is read and multiplied once for all.  (In multiples of 128
         tokens, and no further than the first query of the shortest sequence;
-        empty sequences do not count.)  ``scratch``: uint8, of
+        empty sequences do not count.)  Batches of few tokens are attended to one
+        by one, which is faster, unless ``always``.  ``scratch``: uint8, of
         ``shared_scratch_bytes``, allocated for the call by default."""
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
         if workspace is None:
-            workspace = attention_workspace(self.device, self.head_dim)
+            stream = _raw_stream(self._index)
+            workspace = _workspaces.get((self._index, stream, self.head_dim))
+            if workspace is None:
+                workspace = attention_workspace(self.device, self.head_dim, stream)
         if scratch is None:
-            nbytes = self.shared_scratch_bytes(*q.shape[:3]) if q.dim() == 4 else 0
+            sizes = tuple(q.shape[:3])
+            nbytes = self._scratch.get(sizes)
+            if nbytes is None:
+                nbytes = self._scratch[sizes] = self.shared_scratch_bytes(*sizes) if len(sizes) == 3 else 0
             scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         status = _attend_shared(self._handle, self._index, self.head_dim, q, block_table, seq_lens,
                                 self._sm_scale if sm_scale is None else sm_scale, 0, out, lse, workspace, pdl,
-                                prefix_len, scratch)
+                                prefix_len, scratch, always)
         if status:
             raise Fp4GemvError(status, "fp4gemv_kv_attention_shared")
         return out

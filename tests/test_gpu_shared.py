@@ -54,7 +54,7 @@ def run(kv, c, fmt, q, table, lens, prefix, sm_scale=None, **kw):
     cache = on_gpu(kv, c, fmt)
     lse = torch.full(q.shape[:3], 7.0, dtype=torch.float32, device=DEV)
     out = cache.attend_shared(q, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
-                              torch.tensor([prefix], dtype=torch.int32, device=DEV), lse=lse, sm_scale=sm_scale, **kw)
+                              torch.tensor([prefix], dtype=torch.int32, device=DEV), lse=lse, sm_scale=sm_scale, always=True, **kw)
     return out, lse
 
 
@@ -173,7 +173,8 @@ def test_shared_small_weights_count(kv, fmt, bits, dim):
     q = torch.zeros(batch, 1, 2, dim, dtype=torch.float16, device=DEV)
     q[..., 0] = 1.0
     out = cache.attend_shared(q, table, torch.full((batch,), n + 1, dtype=torch.int32, device=DEV),
-                              torch.tensor([n], dtype=torch.int32, device=DEV), sm_scale=math.log(2.0)).double()
+                              torch.tensor([n], dtype=torch.int32, device=DEV), sm_scale=math.log(2.0),
+                              always=True).double()
     want = n * 2.0 ** -bits / (1 + n * 2.0 ** -bits)
     assert ((out - want).abs() <= 2.0 ** -10 * want + (n + 1) * 2.0 ** -32).all()
 
@@ -210,6 +211,10 @@ def test_shared_bad_pages(kv, fp4):
     assert ((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -9 * mass + 1e-6).all()
 
 
+def share(cache, *args, **kw):
+    return cache.attend_shared(*args, always=True, **kw)
+
+
 def test_shared_strides_streams_and_graph(kv):
     """q and out inside wider rows; another stream; a captured graph whose prefix, lengths and pages change; two graphs."""
     B, heads, dim, block = 5, 8, 128, 16
@@ -222,8 +227,8 @@ def test_shared_strides_streams_and_graph(kv):
     out = wide[:, :heads * dim].view(B, 1, heads, dim)
     tab, n = table.to(DEV), torch.tensor([600, 513, 700, 0, 555], dtype=torch.int32, device=DEV)
     prefix = torch.tensor([512], dtype=torch.int32, device=DEV)
-    want = cache.attend_shared(q.contiguous(), tab, n, prefix)
-    cache.attend_shared(q, tab, n, prefix, out=out)
+    want = share(cache, q.contiguous(), tab, n, prefix)
+    share(cache, q, tab, n, prefix, out=out)
     assert torch.equal(out, want) and (wide[:, heads * dim:] == 9).all()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -231,16 +236,16 @@ def test_shared_strides_streams_and_graph(kv):
     for _ in range(2):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
-            first = cache.attend_shared(q, tab, n, prefix)
-            outs.append((first, cache.attend_shared(first, tab, n, prefix, pdl=False)))
+            first = share(cache, q, tab, n, prefix)
+            outs.append((first, share(cache, first, tab, n, prefix, pdl=False)))
         graphs.append(graph)
     torch.cuda.current_stream().wait_stream(side)
     for new_prefix, lens in ((512, [600, 513, 700, 0, 555]), (200, [600, 300, 201, 700, 0]), (0, [1, 2, 3, 4, 5]),
                              (512, [700] * 5)):
         n.copy_(torch.tensor(lens, dtype=torch.int32))
         prefix.fill_(new_prefix)
-        want = cache.attend_shared(q, tab, n, prefix)
-        want = want, cache.attend_shared(want, tab, n, prefix)
+        want = share(cache, q, tab, n, prefix)
+        want = want, share(cache, want, tab, n, prefix)
         for graph, got in zip(graphs, outs):
             graph.replay()
             torch.cuda.synchronize()
@@ -254,17 +259,33 @@ def test_shared_two_streams_at_once(kv):
     tab, n = table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
     prefix = torch.tensor([2048], dtype=torch.int32, device=DEV)
     qs = [q, q.flip(0).contiguous()]
-    want = [cache.attend_shared(x, tab, n, prefix) for x in qs]
+    want = [share(cache, x, tab, n, prefix) for x in qs]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
     got = [[], []]
     for _ in range(20):
         for i, s in enumerate(streams):
             with torch.cuda.stream(s):
-                got[i].append(cache.attend_shared(qs[i], tab, n, prefix))
+                got[i].append(share(cache, qs[i], tab, n, prefix))
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, want[i]) for o in got[i])
+
+
+def test_shared_by_size(kv):
+    """Small batches are attended to one by one, with the same results as that call's; large ones together."""
+    c, table, q = case(512, [600, 577], 8, 2, 128, 32, "e4m3", "bf16", 1)
+    cache, tab = on_gpu(kv, c, "e4m3"), table.to(DEV)
+    n, prefix = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([600, 577], [512]))
+    from moe_nvfp4_gemv_gb300 import fp4gemv
+    count = fp4gemv.launch_count()
+    got = cache.attend_shared(q, tab, n, prefix)
+    assert fp4gemv.launch_count() == count + 1 and torch.equal(got, cache.attend(q, tab, n))
+    wide = torch.full((2, 400000), -1, dtype=torch.int32, device=DEV)  # (the sizes that the host knows: the table's)
+    wide[:, :tab.shape[1]] = tab
+    count = fp4gemv.launch_count()
+    got = cache.attend_shared(q, wide, n, prefix)
+    assert fp4gemv.launch_count() == count + 3 and torch.equal(got, cache.attend_shared(q, tab, n, prefix, always=True))
 
 
 def test_shared_refusals(kv, fp4):

@@ -41,13 +41,14 @@ def test_read_cache_validation(fp4, kw, status):
 
 
 def attend(fp4, which, cache=None, q=0, ldq=512, dtype=0, heads=4, q_len=1, max_blocks=4, B=1, sm=0.1, window=0, sinks=4,
-           ldo=512, out=0, pdl=1, ws=0, ws_bytes=1 << 30, prefix=0, scratch=0):
+           ldo=512, out=0, pdl=1, ws=0, ws_bytes=1 << 30, prefix=0, scratch=0, always=0):
     c = ctypes.addressof(cache if cache is not None else struct())
     if which == "sinks":
         return fp4.lib().fp4gemv_kv_attention_sinks(c, vp(q), ldq, dtype, heads, q_len, None, max_blocks, None, B, sm, window,
                                                     sinks, vp(out), ldo, None, vp(ws), ws_bytes, pdl, None)
     return fp4.lib().fp4gemv_kv_attention_shared(c, vp(q), ldq, dtype, heads, q_len, None, max_blocks, None, B, vp(prefix),
-                                                 sm, vp(out), ldo, None, vp(ws), ws_bytes, vp(scratch), 1 << 40, pdl, None)
+                                                 sm, vp(out), ldo, None, vp(ws), ws_bytes, vp(scratch), 1 << 40, always, pdl,
+                                                 None)
 
 
 @pytest.mark.parametrize("which", ["sinks", "shared"])
@@ -62,7 +63,7 @@ def test_attention_host_validation(fp4, which, kw, status):
 
 @pytest.mark.parametrize("which,kw,status", [
     ("sinks", dict(window=-1), 1), ("sinks", dict(sinks=-1), 1), ("sinks", dict(sinks=(1 << 30) + 1), 2),
-    ("shared", dict(prefix=A16 + 2), 3), ("shared", dict(scratch=A16 + 8), 3),
+    ("shared", dict(always=2), 1), ("shared", dict(prefix=A16 + 2), 3), ("shared", dict(scratch=A16 + 8), 3),
     ("shared", dict(B=1024, q_len=16, heads=128, ldq=1 << 20, ldo=1 << 20, max_blocks=1 << 16), 2)])
 def test_attention_own_arguments(fp4, which, kw, status):
     assert attend(fp4, which, **kw) == status
@@ -97,7 +98,7 @@ def test_add_norm_host_validation(fp4, kw, status):
 def test_marshal_counts_arguments(fp4):
     from moe_nvfp4_gemv_gb300 import _marshal
     for fn, count in ((_marshal.kv_read, 10), (_marshal.add_norm, 12), (_marshal.kv_attention_sinks, 13),
-                      (_marshal.kv_attention_shared, 14), (_marshal.bind_more, 4)):
+                      (_marshal.kv_attention_shared, 15), (_marshal.bind_more, 4)):
         for n in (0, count - 1, count + 1):
             with pytest.raises(TypeError):
                 fn(*([None] * n))
