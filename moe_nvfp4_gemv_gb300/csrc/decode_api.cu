@@ -152,7 +152,8 @@ fp4gemv_status fp4gemv_add_norm(const void* x, int64_t ldx, int x_dtype, const v
       (gate && !aligned(gate, size(gate_dtype))))
     return FP4GEMV_ERR_MISALIGNED;
   if (!x || !weight || !out || (y && !residual)) return FP4GEMV_ERR_INVALID_ARG;
-  fp4gemv_status st = fp4::current_device_state(nullptr, nullptr);
+  int sms = 0;
+  fp4gemv_status st = fp4::current_device_state(nullptr, &sms);
   if (st != FP4GEMV_OK) return st;
   fp4::AddNormParams p = {};
   p.x = x;
@@ -182,7 +183,7 @@ fp4gemv_status fp4gemv_add_norm(const void* x, int64_t ldx, int x_dtype, const v
   const bool vec = H % 8 == 0 && rows16(x, ldx) && rows16(out, ldo) && aligned(weight, 16) && aligned(post_weight, 16) &&
                    (!y || (rows16(y, ldy) && rows16(residual, ldr))) && (!channel || rows16(gate, ldg));
   fp4::count_launch();
-  return from_cuda(fp4::launch_add_norm(p, dtype == FP4GEMV_F16, vec, pdl, stream));
+  return from_cuda(fp4::launch_add_norm(p, dtype == FP4GEMV_F16, vec, sms, pdl, stream));
 }
 
 // [arrival counters, three for each CTA | partials, two for each CTA]

@@ -4,9 +4,9 @@
 
 namespace fp4 {
 
-template <bool kF16, bool kVec, int kRow, int kChunks>
+template <bool kF16, bool kVec, bool kX32, int kRow, int kChunks>
 static cudaError_t add_norm_typed(const AddNormParams& p, int pdl, cudaStream_t stream) {
-  constexpr int kThreads = kRow < 256 ? 256 : kRow, kRows = kThreads / kRow;
+  constexpr int kThreads = norm_threads(kRow), kRows = kThreads / kRow;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(p.M) + kRows - 1) / kRows), 1, 1);
   lc.blockDim = dim3(kThreads, 1, 1);
@@ -16,24 +16,43 @@ static cudaError_t add_norm_typed(const AddNormParams& p, int pdl, cudaStream_t 
   attr.val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = &attr;
   lc.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&lc, add_norm_kernel<kF16, kVec, kRow, kChunks>, p);
+  return cudaLaunchKernelEx(&lc, add_norm_kernel<kF16, kVec, kX32, kRow, kChunks>, p);
 }
 
-// The fewest threads that hold a token in one chunk each; above 1024 threads more chunks.
-template <bool kF16, bool kVec>
-static cudaError_t add_norm_width(const AddNormParams& p, int pdl, cudaStream_t stream) {
-  if (p.H <= 256) return add_norm_typed<kF16, kVec, 32, 1>(p, pdl, stream);
-  if (p.H <= 1024) return add_norm_typed<kF16, kVec, 128, 1>(p, pdl, stream);
-  if (p.H <= 2048) return add_norm_typed<kF16, kVec, 256, 1>(p, pdl, stream);
-  if (p.H <= 4096) return add_norm_typed<kF16, kVec, 512, 1>(p, pdl, stream);
-  if (p.H <= 8192) return add_norm_typed<kF16, kVec, 1024, 1>(p, pdl, stream);
-  if (p.H <= 16384) return add_norm_typed<kF16, kVec, 1024, 2>(p, pdl, stream);
-  return add_norm_typed<kF16, kVec, 1024, 4>(p, pdl, stream);
+// Few tokens: the fewest threads that hold one in a chunk each, for the shortest chain.  Many: two chunks each, so that
+// a thread has twice the loads under way and an SM holds more tokens.
+template <bool kF16, bool kVec, bool kX32>
+static cudaError_t add_norm_width(const AddNormParams& p, int sms, int pdl, cudaStream_t stream) {
+  const bool many = p.M > 4 * sms;
+  if (p.H <= 256) return add_norm_typed<kF16, kVec, kX32, 32, 1>(p, pdl, stream);
+  if (many) {
+    if (p.H <= 512) return add_norm_typed<kF16, kVec, kX32, 32, 2>(p, pdl, stream);
+    if (p.H <= 1024) return add_norm_typed<kF16, kVec, kX32, 64, 2>(p, pdl, stream);
+    if (p.H <= 2048) return add_norm_typed<kF16, kVec, kX32, 128, 2>(p, pdl, stream);
+    if (p.H <= 4096) return add_norm_typed<kF16, kVec, kX32, 256, 2>(p, pdl, stream);
+    if (p.H <= 5120) return add_norm_typed<kF16, kVec, kX32, 320, 2>(p, pdl, stream);
+    if (p.H <= 6144) return add_norm_typed<kF16, kVec, kX32, 384, 2>(p, pdl, stream);
+    if (p.H <= 8192) return add_norm_typed<kF16, kVec, kX32, 512, 2>(p, pdl, stream);
+    if (p.H <= 10240) return add_norm_typed<kF16, kVec, kX32, 320, 4>(p, pdl, stream);
+    if (p.H <= 16384) return add_norm_typed<kF16, kVec, kX32, 512, 4>(p, pdl, stream);
+  }
+  if (p.H <= 1024) return add_norm_typed<kF16, kVec, kX32, 128, 1>(p, pdl, stream);
+  if (p.H <= 2048) return add_norm_typed<kF16, kVec, kX32, 256, 1>(p, pdl, stream);
+  if (p.H <= 4096) return add_norm_typed<kF16, kVec, kX32, 512, 1>(p, pdl, stream);
+  if (p.H <= 8192) return add_norm_typed<kF16, kVec, kX32, 1024, 1>(p, pdl, stream);
+  if (p.H <= 16384) return add_norm_typed<kF16, kVec, kX32, 1024, 2>(p, pdl, stream);
+  return add_norm_typed<kF16, kVec, kX32, 1024, 4>(p, pdl, stream);
 }
 
-cudaError_t launch_add_norm(const AddNormParams& p, int f16, int vec, int pdl, cudaStream_t stream) {
-  if (vec) return f16 ? add_norm_width<true, true>(p, pdl, stream) : add_norm_width<false, true>(p, pdl, stream);
-  return f16 ? add_norm_width<true, false>(p, pdl, stream) : add_norm_width<false, false>(p, pdl, stream);
+template <bool kF16>
+static cudaError_t add_norm_half(const AddNormParams& p, int vec, int sms, int pdl, cudaStream_t stream) {
+  if (!vec) return add_norm_width<kF16, false, false>(p, sms, pdl, stream);  // (its loads go by the types at run time)
+  return p.x_type == 2 ? add_norm_width<kF16, true, true>(p, sms, pdl, stream)
+                       : add_norm_width<kF16, true, false>(p, sms, pdl, stream);
+}
+
+cudaError_t launch_add_norm(const AddNormParams& p, int f16, int vec, int sms, int pdl, cudaStream_t stream) {
+  return f16 ? add_norm_half<true>(p, vec, sms, pdl, stream) : add_norm_half<false>(p, vec, sms, pdl, stream);
 }
 
 }  // namespace fp4

@@ -104,17 +104,55 @@ __device__ __forceinline__ void norm_store(void* p, int type, int64_t at, int le
   }
 }
 
-// kRow threads to a token, kChunks times eight values each; CTAs of at least 256 threads.
-template <bool kF16, bool kVec, int kRow, int kChunks>
-__global__ void __launch_bounds__(kRow < 256 ? 256 : kRow) add_norm_kernel(const AddNormParams p) {
-  constexpr int kThreads = kRow < 256 ? 256 : kRow, kRows = kThreads / kRow, kWarps = kRow / 32;
+// Eight values as they lie (kVec): of a half type in `a`, of fp32 in both.
+struct NormRaw {
+  uint4 a, b;
+};
+__device__ __forceinline__ void norm_fetch(const void* p, bool f32, int64_t at, NormRaw& r) {
+  if (f32) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+    r.a = s[0], r.b = s[1];
+  } else {
+    r.a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+  }
+}
+template <bool kF16>
+__device__ __forceinline__ void norm_values(const NormRaw& r, bool f32, float (&v)[8]) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  if (f32) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (kF16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        v[2 * k] = f.x, v[2 * k + 1] = f.y;
+      } else {
+        v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+__device__ __forceinline__ float norm_gate(float g, int sigmoid) { return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-g)) : g; }
+
+// Threads of a CTA: whole tokens, 256 threads or more where that comes out even.
+__host__ __device__ constexpr int norm_threads(int row) { return row < 256 && 256 % row == 0 ? 256 : row; }
+// CTAs per SM that registers are kept for: 1024 threads of two chunks, 640 of four.
+__host__ __device__ constexpr int norm_ctas(int row, int chunks) {
+  return chunks == 1 || row > 512 ? 1 : (chunks == 2 ? 1024 : 640) / norm_threads(row) < 1 ? 1 : (chunks == 2 ? 1024 : 640) / norm_threads(row);
+}
+
+// kRow threads to a token, kChunks times eight values each.  kX32: the stream is fp32.
+template <bool kF16, bool kVec, bool kX32, int kRow, int kChunks>
+__global__ void __launch_bounds__(norm_threads(kRow), norm_ctas(kRow, kChunks)) add_norm_kernel(const AddNormParams p) {
+  constexpr int kThreads = norm_threads(kRow), kRows = kThreads / kRow, kWarps = kRow / 32;
   constexpr int kHalf = kF16 ? 1 : 0;
   __shared__ float sums[2][kThreads / 32];
   const int tid = threadIdx.x % kRow, group = threadIdx.x / kRow;
   if (threadIdx.x == 0) pdl_launch_dependents();
   pdl_wait();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + group;
-  const bool live = row < p.M;
   // the sum over the token's threads, in a fixed order
   auto total = [&](float s, int which) -> float {
 #pragma unroll
@@ -135,24 +173,43 @@ __global__ void __launch_bounds__(kRow < 256 ? 256 : kRow) add_norm_kernel(const
     }
     return s;
   };
-  // chunk i of the thread: its first value, and how many the row has from there
+  // chunk i of the thread: its first value, and whether the row has any from there
   auto first = [&](int i) -> int { return kVec ? (tid + i * kRow) * 8 : i * 8 * kRow + tid; };
+  auto live = [&](int i) -> bool { return row < p.M && first(i) < p.H; };
+  // what the row needs of HBM, under way at once (not kVec: as it comes to be used)
+  NormRaw xr[kChunks], yr[kChunks], gr[kChunks];
+  const bool gated = p.gate && !p.gate_scalar, g32 = p.g_type == 2;
+  if constexpr (kVec) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      if (!live(i)) continue;
+      if (p.y) norm_fetch(p.y, false, row * p.ldy + first(i), yr[i]);
+      norm_fetch(p.x, kX32, row * p.ldx + first(i), xr[i]);
+      if (gated && !g32) norm_fetch(p.gate, false, row * p.ldg + first(i), gr[i]);
+    }
+  }
   float r[kChunks][8];
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i)
+  for (int i = 0; i < kChunks; ++i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) r[i][j] = 0.0f;
+    if (!live(i)) continue;
+    if (p.y) {
+      if constexpr (kVec) norm_values<kF16>(yr[i], false, r[i]);
+      else norm_load<kVec, kRow>(p.y, kHalf, row * p.ldy + first(i), p.H - first(i), r[i]);
+    } else {
+      if constexpr (kVec) norm_values<kF16>(xr[i], kX32, r[i]);
+      else norm_load<kVec, kRow>(p.x, p.x_type, row * p.ldx + first(i), p.H - first(i), r[i]);
+    }
+  }
   if (p.y) {
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      if (live && first(i) < p.H) norm_load<kVec, kRow>(p.y, kHalf, row * p.ldy + first(i), p.H - first(i), r[i]);
     float factor = p.scale;
-    if (p.gate && p.gate_scalar && live) {
+    if (p.gate && p.gate_scalar && row < p.M) {
       float g;
-      if (p.g_type == 2) g = static_cast<const float*>(p.gate)[row * p.ldg];
-      else if (p.g_type == 1) g = __half2float(static_cast<const __half*>(p.gate)[row * p.ldg]);
+      if (g32) g = static_cast<const float*>(p.gate)[row * p.ldg];
+      else if (kF16) g = __half2float(static_cast<const __half*>(p.gate)[row * p.ldg]);
       else g = __bfloat162float(static_cast<const __nv_bfloat16*>(p.gate)[row * p.ldg]);
-      factor *= p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-g)) : g;
+      factor *= norm_gate(g, p.sigmoid);
     }
     if (p.post) {
       float s = 0.0f;
@@ -164,10 +221,11 @@ __global__ void __launch_bounds__(kRow < 256 ? 256 : kRow) add_norm_kernel(const
     }
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      if (!live || first(i) >= p.H) continue;
+      if (!live(i)) continue;
       const int left = p.H - first(i);
       float f[8], x[8];
-      norm_load<kVec, kRow>(p.x, p.x_type, row * p.ldx + first(i), left, x);
+      if constexpr (kVec) norm_values<kF16>(xr[i], kX32, x);
+      else norm_load<kVec, kRow>(p.x, p.x_type, row * p.ldx + first(i), left, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = factor;
       if (p.post) {
@@ -176,20 +234,17 @@ __global__ void __launch_bounds__(kRow < 256 ? 256 : kRow) add_norm_kernel(const
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] *= w[j] + p.offset;
       }
-      if (p.gate && !p.gate_scalar) {
+      if (gated) {
         float g[8];
-        norm_load<kVec, kRow>(p.gate, p.g_type, row * p.ldg + first(i), left, g);
+        if (kVec && !g32) norm_values<kF16>(gr[i], false, g);
+        else norm_load<kVec, kRow>(p.gate, p.g_type, row * p.ldg + first(i), left, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-g[j])) : g[j];
+        for (int j = 0; j < 8; ++j) f[j] *= norm_gate(g[j], p.sigmoid);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[i][j] = kVec || j * kRow < left ? fmaf(r[i][j], f[j], x[j]) : 0.0f;
       norm_store<kVec, kRow>(p.residual, p.x_type, row * p.ldr + first(i), left, r[i]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      if (live && first(i) < p.H) norm_load<kVec, kRow>(p.x, p.x_type, row * p.ldx + first(i), p.H - first(i), r[i]);
   }
   float s = 0.0f;
 #pragma unroll
@@ -199,7 +254,7 @@ __global__ void __launch_bounds__(kRow < 256 ? 256 : kRow) add_norm_kernel(const
   const float f = rsqrtf(total(s, 1) / static_cast<float>(p.H) + p.eps);
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    if (!live || first(i) >= p.H) continue;
+    if (!live(i)) continue;
     const int left = p.H - first(i);
     float w[8];
     norm_load<kVec, kRow>(p.weight, p.w_type, first(i), left, w);
