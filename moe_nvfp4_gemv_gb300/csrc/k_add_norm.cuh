@@ -10,6 +10,13 @@
 // A token's values stay in the registers of one group of threads from the
 // first read to the last write: every input is read once and every output
 // written once, with one sum over the group for each norm.
+//
+// What bounds it: HBM for many tokens, the launch and two dependent trips to L2 for few.  Loads of x, y and gates are all
+// under way before the first sum, two chunks of 8 values to a thread, 1024 threads to an SM.  Of the measured copy
+// bandwidth: 20011 tokens of 4096, bf16, norms on both sides and a gate for each value 132 us, 0.93 (loads as they come to
+// be used, a chunk to a thread: 254); without the gate 0.88, the next norm alone 0.98, an fp32 stream 1.0; 5120 0.77, 6144
+// 0.67, 8192 0.80, 10240 0.79, 16384 0.65 (one CTA to an SM: nothing fills in between its phases).  Rows that are not
+// aligned go value by value: 4099 0.32.  One token of 4096: 3.2 us a call, 37 of 6144 3.6.
 #pragma once
 
 #include <cuda_bf16.h>
