@@ -24,6 +24,8 @@ static cudaError_t add_norm_typed(const AddNormParams& p, int pdl, cudaStream_t 
 template <bool kF16, bool kVec, bool kX32>
 static cudaError_t add_norm_width(const AddNormParams& p, int sms, int pdl, cudaStream_t stream) {
   const bool many = p.M > 4 * sms;
+  if (p.H <= 64) return add_norm_typed<kF16, kVec, kX32, 8, 1>(p, pdl, stream);
+  if (p.H <= 128) return add_norm_typed<kF16, kVec, kX32, 16, 1>(p, pdl, stream);
   if (p.H <= 256) return add_norm_typed<kF16, kVec, kX32, 32, 1>(p, pdl, stream);
   if (many) {
     if (p.H <= 512) return add_norm_typed<kF16, kVec, kX32, 32, 2>(p, pdl, stream);

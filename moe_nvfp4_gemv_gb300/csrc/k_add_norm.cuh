@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(norm_threads(kRow), norm_ctas(kRow, kChunks)) 
   // the sum over the token's threads, in a fixed order
   auto total = [&](float s, int which) -> float {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    for (int o = kRow < 32 ? kRow / 2 : 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     if constexpr (kWarps > 1) {
       if ((threadIdx.x & 31) == 0) sums[which][threadIdx.x >> 5] = s;
       __syncthreads();
