@@ -1,7 +1,8 @@
 """A small mixture-of-experts decoder on this library, step by step.
 
-Every product is an NVFP4 or BF16 product of ``fp4gemv``; the cache is held in
-8 bits (``kvcache.KvCache8``: append, attend), the router's logits go through
+Every product is an NVFP4 or BF16 product of ``fp4gemv``, the residual stream and
+its norms lie in ``fp4gemv.add_norm``; the cache is held in 8 bits
+(``kvcache.KvCache8``: append, attend), the router's logits go through
 ``fp4gemv.moe_route`` to the expert pair, and the answer's log probabilities
 come from ``fp4gemv.token_logprobs``.  Weights are random (seeded), so the text
 means nothing; shapes and order of calls are those of a serving program.
@@ -11,7 +12,11 @@ time (the cache takes several new tokens per sequence); after it every step brin
 per sequence and is one captured CUDA graph: lengths and tokens live on the
 device.
 
-    python examples/moe_decode.py [--batch 4] [--steps 32]
+With ``--window`` layers see a sliding window and the first ``--sinks`` tokens; with
+``--shared`` all sequences begin with the same prompt of that many tokens, whose
+pages they share and attend to together.
+
+    python examples/moe_decode.py [--batch 4] [--steps 32] [--window 0] [--sinks 4] [--shared 0]
 """
 from __future__ import annotations
 
@@ -30,17 +35,13 @@ from moe_nvfp4_gemv_gb300.kvcache import KvCache8  # noqa: E402
 SMALL = dict(layers=2, hidden=1024, heads=16, kv_heads=4, head_dim=64, experts=32, topk=4, inter=512, vocab=4096)
 
 
-def rms_norm(x: torch.Tensor) -> torch.Tensor:
-    y = x.float()
-    return (y * torch.rsqrt(y.square().mean(-1, keepdim=True) + 1e-6)).to(torch.bfloat16)
-
-
 class MoeDecoder:
     """Random-weight decoder: attention over an 8-bit cache, then routed experts with a shared one."""
 
     def __init__(self, batch: int, max_len: int, cfg: dict = SMALL, block_size: int = 16, fmt: str = "e4m3",
-                 seed: int = 0, device: str = "cuda"):
+                 seed: int = 0, device: str = "cuda", window: int = 0, sinks: int = 0):
         self.cfg, self.batch, self.device = cfg, batch, device
+        self.window, self.sinks = window, sinks
         H, E, I = cfg["hidden"], cfg["experts"], cfg["inter"]
         qkv = (cfg["heads"] + 2 * cfg["kv_heads"]) * cfg["head_dim"]
         self._seed = seed
@@ -64,14 +65,19 @@ class MoeDecoder:
                 router=(torch.randn(E, H, generator=g, device=device) / H ** 0.5).to(torch.bfloat16),
                 bias=torch.randn(E, generator=g, device=device) * 0.02,
                 w1=w1, w1_sf=w1_sf, alpha1=g1.expand(E).contiguous(), w2=w2, w2_sf=w2_sf,
-                alpha2=g2.expand(E).contiguous(), shared_up=nvfp4(2 * I, H), shared_down=nvfp4(H, I)))
+                alpha2=g2.expand(E).contiguous(), shared_up=nvfp4(2 * I, H), shared_down=nvfp4(H, I),
+                norm1=torch.ones(H, dtype=torch.bfloat16, device=device),
+                norm2=torch.ones(H, dtype=torch.bfloat16, device=device)))
         self.head = nvfp4(cfg["vocab"], H)
         # one cache per layer; pages are dealt out in advance, one run of them per sequence
         pages = -(-max_len // block_size)
         self.caches = [KvCache8.allocate(batch * pages, cfg["kv_heads"], cfg["head_dim"], block_size, fmt, device)
                        for _ in self.layers]
         self.block_table = torch.arange(batch * pages, dtype=torch.int32, device=device).view(batch, pages)
+        self.own_pages = self.block_table.clone()
         self.seq_lens = torch.zeros(batch, dtype=torch.int32, device=device)
+        self.norm = torch.ones(H, dtype=torch.bfloat16, device=device)
+        self.shared, self.always = None, False  # int32 [1]: tokens that all sequences begin with
 
     def forward(self, tokens: torch.Tensor, trace: list | None = None) -> torch.Tensor:
         """bf16 logits [batch, n, vocab] of n new tokens per sequence (int64 [batch, n], n at most 16 and batch n at
@@ -81,31 +87,55 @@ class MoeDecoder:
         heads, kv, dim, H, I = c["heads"], c["kv_heads"], c["head_dim"], c["hidden"], c["inter"]
         self.seq_lens += n
         x = self.embedding[tokens.reshape(-1)]
+        h, x = fp4gemv.add_norm(x, None, self.layers[0]["norm1"])
         M = B * n
         act = torch.empty(M * c["topk"], I, dtype=torch.bfloat16, device=self.device)
         sact = torch.empty(M, I, dtype=torch.bfloat16, device=self.device)
-        for layer, cache in zip(self.layers, self.caches):
-            qkv = fp4gemv.nvfp4_gemv(rms_norm(x), *layer["qkv"])
+        after = [layer["norm1"] for layer in self.layers[1:]] + [self.norm]  # the norm behind each layer
+        for layer, cache, norm in zip(self.layers, self.caches, after):
+            qkv = fp4gemv.nvfp4_gemv(h, *layer["qkv"])
             k = qkv[:, heads * dim:(heads + kv) * dim].unflatten(1, (kv, dim))  # (views of the projection's rows)
             v = qkv[:, (heads + kv) * dim:].unflatten(1, (kv, dim))
             cache.append(k, v, self.block_table, self.seq_lens)
             q = qkv.view(B, n, -1)[..., :heads * dim].unflatten(2, (heads, dim))
-            att = cache.attend(q, self.block_table, self.seq_lens)
-            x = x + fp4gemv.nvfp4_gemv(att.reshape(M, heads * dim), *layer["out"])
-            h = rms_norm(x)
+            if self.shared is not None:
+                att = cache.attend_shared(q, self.block_table, self.seq_lens, self.shared, always=self.always)
+            else:
+                att = cache.attend(q, self.block_table, self.seq_lens, window=self.window, sinks=self.sinks)
+            block = fp4gemv.nvfp4_gemv(att.reshape(M, heads * dim), *layer["out"])
+            stream = x
+            h, x = fp4gemv.add_norm(stream, block, layer["norm2"])
             logits = fp4gemv.bf16_gemv(h, layer["router"])
             ids, weights = fp4gemv.moe_route(logits, c["topk"], scores="sigmoid", bias=layer["bias"])
             fp4gemv.moe_gate_up(h, ids, layer["w1"], layer["w1_sf"], layer["alpha1"], act, *layer["shared_up"], sact)
             y = torch.empty_like(x)
             fp4gemv.moe_down_combine(act, ids, weights, layer["w2"], layer["w2_sf"], layer["alpha2"], sact,
                                      *layer["shared_down"], y)
-            x = x + y
             if trace is not None:
-                trace.append(dict(q=q, k=k, v=v, att=att, router=logits, ids=ids, weights=weights))
-        return fp4gemv.nvfp4_gemv(rms_norm(x), *self.head).view(B, n, -1)
+                trace.append(dict(q=q, k=k, v=v, att=att, router=logits, ids=ids, weights=weights, stream=stream,
+                                  block=block, h=h, x=x))
+            h, x = fp4gemv.add_norm(x, y, norm)
+        return fp4gemv.nvfp4_gemv(h, *self.head).view(B, n, -1)
+
+    def share(self, tokens: int, always: bool = False) -> None:
+        """All sequences begin with the same ``tokens`` tokens, already in the cache: from now on the first sequence's
+        whole pages of them are everyone's, and steps attend to them together (``always``: however few they are)."""
+        if self.window:
+            raise ValueError("no window together with a shared beginning")
+        full = tokens // self.caches[0].block_size
+        self.block_table[:, :full] = self.block_table[0, :full].clone()
+        self.shared = torch.tensor([tokens], dtype=torch.int32, device=self.device)
+        self.always = always
+
+    def keys_and_values(self, layer: int, tokens: int) -> tuple[torch.Tensor, torch.Tensor]:
+        """bf16 [batch, tokens, kv_heads, head_dim]: what a layer's cache holds of every sequence's last tokens."""
+        k, v = self.caches[layer].read(self.block_table, self.seq_lens, self.batch * tokens)
+        return k.unflatten(0, (self.batch, tokens)), v.unflatten(0, (self.batch, tokens))
 
     def reset(self) -> None:
         self.seq_lens.zero_()
+        self.block_table.copy_(self.own_pages)
+        self.shared = None
 
 
 class Generator:
@@ -162,12 +192,20 @@ def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--batch", type=int, default=4)
     ap.add_argument("--steps", type=int, default=32)
+    ap.add_argument("--window", type=int, default=0)
+    ap.add_argument("--sinks", type=int, default=4)
+    ap.add_argument("--shared", type=int, default=0)
     args = ap.parse_args()
     gen = torch.Generator(device="cuda").manual_seed(1)
-    model = MoeDecoder(args.batch, max_len=12 + args.steps + 1)
+    model = MoeDecoder(args.batch, max_len=12 + args.shared + args.steps + 1, window=args.window, sinks=args.sinks)
     run = Generator(model)
     prompt = torch.randint(0, model.cfg["vocab"], (args.batch, 12), generator=gen, device="cuda")
+    if args.shared:
+        common = torch.randint(0, model.cfg["vocab"], (1, args.shared), generator=gen, device="cuda")
+        prompt = torch.cat([common.expand(args.batch, -1), prompt], 1)
     out = run.start(prompt, gen)
+    if args.shared:
+        model.share(args.shared)
     run.step(gen)  # (captures)
     torch.cuda.synchronize()
     t0 = time.perf_counter()
