@@ -446,6 +446,9 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
   x.block_log2 = p.block_log2;
   x.kv_heads = cache->kv_heads;
   x.group = p.group;
+  x.group_magic = p.group_magic;
+  x.skip_tile = fp4::skipped_stage();
+  x.inv_rows = 1.0f / static_cast<float>(q_len * p.group);
   x.q_len = q_len;
   x.f16 = p.f16;
   x.sm_scale = sm_scale;

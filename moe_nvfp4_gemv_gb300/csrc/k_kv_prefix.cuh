@@ -65,7 +65,10 @@ struct KvPrefixParams {
   KvPrefixLine line;
   int B, max_blocks, num_blocks, block_log2;
   int kv_heads, group, q_len;
+  int group_magic;  // KvAttnParams'
+  int skip_tile;    // test hook: V of this tile of every CTA is not said to be there (-1: of none)
   int f16;
+  float inv_rows;   // 1 / (q_len group)
   float sm_scale;
 };
 
@@ -291,7 +294,10 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int gr = block * 128 + quarter * 32 + t * 8 + (lane >> 2);
-          const int b = gr / rows, in = gr - b * rows, i = in / p.group;
+          int b = static_cast<int>(static_cast<float>(gr) * p.inv_rows);  // gr / rows (below 2^20: at most one off)
+          b -= b * rows > gr;
+          b += b * rows + rows <= gr;
+          const int in = gr - b * rows, i = (in * p.group_magic) >> 16;
           const uint16_t* const src = p.q + (static_cast<int64_t>(b) * p.q_len + i) * p.ldq +
                                       (head * p.group + in - i * p.group) * kDim + half * C::kSplit + part * 8;
 #pragma unroll
@@ -592,7 +598,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(v ? v_full(stage) : k_full(stage));
+      if (lane == 0 && !(v && tile == p.skip_tile)) mbar_arrive(v ? v_full(stage) : k_full(stage));
     };
     const int count = first < jobs ? (jobs - first + C::kMovers - 1) / C::kMovers : 0;  // of the warp
     Job job[2];

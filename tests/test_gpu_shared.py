@@ -288,6 +288,32 @@ def test_shared_by_size(kv):
     assert fp4gemv.launch_count() == count + 3 and torch.equal(got, cache.attend_shared(q, tab, n, prefix, always=True))
 
 
+@pytest.mark.parametrize("dim,prefix,skip,met", [(128, 2048, 0, True), (256, 2048, 0, True), (64, 51200, 1, True),
+                                                 (96, 51200, 2, True), (128, 2048, 5, False)])
+def test_shared_timeout_then_recovery(kv, fp4, dim, prefix, skip, met):
+    """A tile's values that are never said to be there (a host-side hook; nothing is in flight): the call comes back, the
+    error word reads a timeout, every row is NaN (each has a part in every CTA's sums); the next calls are right.  (2048
+    tokens are a tile for each CTA: the hook's sixth is nobody's.)"""
+    lens = [prefix + 5 + 7 * b for b in range(20)]
+    c, table, q = case(prefix, lens, 8, 1, dim, 64, "e4m3", "bf16", 1)
+    cache, tab = on_gpu(kv, c, "e4m3"), table.to(DEV)
+    n, start = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (lens, [prefix]))
+    good = share(cache, q, tab, n, start)
+    assert fp4.get_device_error() == 0
+    try:
+        fp4.set_wait_limit_ns(5_000_000)
+        fp4.debug_skip_stage(skip)
+        lost = share(cache, q, tab, n, start)
+        assert fp4.get_device_error() == (5 if met else 0)
+    finally:
+        fp4.debug_skip_stage(-1)
+        fp4.set_wait_limit_ns(0)
+    assert lost.isnan().all() if met else torch.equal(lost, good)
+    for _ in range(2):
+        assert torch.equal(share(cache, q, tab, n, start), good)
+    assert fp4.get_device_error() == 0
+
+
 def test_shared_refusals(kv, fp4):
     cache = kv.KvCache8.allocate(4, 2, 64, 16)
     table = torch.zeros(2, 2, dtype=torch.int32, device=DEV)
