@@ -114,11 +114,12 @@ template <int kMode>
 using AttnModeParams = std::conditional_t<kMode == kAttnSinks, KvAttnSinksParams,
                                           std::conditional_t<kMode == kAttnRest, KvAttnRestParams, KvAttnParams>>;
 // How many tokens of a beginning of `said` tokens are taken together: a multiple of 128 before every sequence's first query.
-// By a warp; *owner: the first sequence that is not empty.
+// By a warp; *owner: the first sequence that is not empty.  kL2: past the first-level cache.
+template <bool kL2>
 __device__ __forceinline__ int attn_together(int said, const int32_t* lens, int B, int q_len, int64_t cap, int* owner) {
   int low = 0x7FFFFFFF, who = 0x7FFFFFFF;
   for (int b = threadIdx.x & 31; b < B; b += 32) {
-    const int raw = __ldcg(lens + b), n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
+    const int raw = kL2 ? __ldcg(lens + b) : __ldg(lens + b), n = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
     if (n > 0) {
       low = min(low, n - q_len);  // (every row sees them, and some token is left)
       who = min(who, b);
@@ -825,7 +826,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
     if (tid == 0) pdl_launch_dependents();
     if (warp == 0) {  // (the plan is the first warp's, and ends with a barrier)
       int owner;
-      const int taken = attn_together(__ldcg(p.prefix_len), p.lens, p.B, p.q_len,
+      const int taken = attn_together<false>(__ldg(p.prefix_len), p.lens, p.B, p.q_len,
                                       static_cast<int64_t>(p.max_blocks) << p.block_log2, &owner);
       if (lane == 0) attn_taken() = taken;
       __syncwarp();

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
   // for at the end, for those who follow.  Reads go to L2, since no wait has made the first-level cache's lines new.
   if (warp == 0) {
     int owner;
-    const int n = attn_together(__ldcg(p.prefix_len), p.lens, p.B, p.q_len, static_cast<int64_t>(p.max_blocks) << p.block_log2,
+    const int n = attn_together<true>(__ldcg(p.prefix_len), p.lens, p.B, p.q_len, static_cast<int64_t>(p.max_blocks) << p.block_log2,
                                 &owner);
     if (lane == 0) {
       together_s = n;
@@ -713,14 +713,16 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvJoinParam
   const int head_out = head * p.group + in - i * p.group;
   uint16_t* const out = p.out + token * p.ldo + head_out * kDim + d;
   float* const lse = d == 0 && p.lse ? p.lse + token * (p.kv_heads * p.group) + head_out : nullptr;
-  if (__ldg(p.lens + b) <= 0) {
+  // (all under way at once; what an empty sequence's row says is not looked at)
+  const int length = __ldg(p.lens + b), taken = __ldcg(line.tokens);
+  const float2 own = __ldcg(p.ml + at);
+  float4 v = __ldcg(reinterpret_cast<const float4*>(p.sums + at * kDim + d));
+  if (length <= 0) {
     attn_put(make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f, out, lse, p.f16);
     return;
   }
-  const float2 own = __ldcg(p.ml + at);
-  float4 v = __ldcg(reinterpret_cast<const float4*>(p.sums + at * kDim + d));
   float top = own.x, l = own.y;
-  const int tiles = __ldcg(line.tokens) / line.tile;
+  const int tiles = taken / line.tile;
   if (tiles > 0) {
     const int per = prefix_share(tiles * p.kv_heads * line.items, line.ctas), block = all >> 7;
     const int number = line.slots == 1 ? block : block >> 1;
