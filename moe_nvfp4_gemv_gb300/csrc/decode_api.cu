@@ -473,7 +473,7 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
   e = fp4::launch_kv_prefix(x, dim, int8, pdl, stream);
   if (e != cudaSuccess) return from_cuda(e);
   fp4::count_launch();
-  return from_cuda(fp4::launch_kv_join(y, dim, pdl, stream));
+  return from_cuda(fp4::launch_kv_join(y, dim, sms, pdl, stream));
 }
 
 fp4gemv_status fp4gemv_moe_route(const void* logits, int64_t ldl, int dtype, int M, int E, int topk, int scores,

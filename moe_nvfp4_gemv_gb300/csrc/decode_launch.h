@@ -47,7 +47,7 @@ int kv_prefix_slots(int dim);
 int kv_prefix_tile(int dim);
 cudaError_t launch_kv_prefix(const KvPrefixParams& p, int dim, int int8, int pdl, cudaStream_t stream);
 struct KvJoinParams;
-cudaError_t launch_kv_join(const KvJoinParams& p, int dim, int pdl, cudaStream_t stream);
+cudaError_t launch_kv_join(const KvJoinParams& p, int dim, int sms, int pdl, cudaStream_t stream);
 
 // E4M3, head_dim 128, row tiles of 32.
 cudaError_t launch_kv_attention_tc(const KvAttnTcParams& p, int sms, int pdl, cudaStream_t stream);

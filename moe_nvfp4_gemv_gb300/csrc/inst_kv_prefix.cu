@@ -37,11 +37,10 @@ cudaError_t launch_kv_prefix(const KvPrefixParams& p, int dim, int int8, int pdl
   }
 }
 
-template <int kDim>
-static cudaError_t join_typed(const KvJoinParams& p, int pdl, cudaStream_t stream) {
-  const int64_t cells = static_cast<int64_t>(p.B) * p.q_len * p.group * p.kv_heads * (kDim / 4);
+template <int kDim, int kWays>
+static cudaError_t join_typed(const KvJoinParams& p, int64_t cells, int pdl, cudaStream_t stream) {
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(static_cast<unsigned>((cells + kJoinThreads - 1) / kJoinThreads), 1, 1);
+  lc.gridDim = dim3(static_cast<unsigned>((cells * kWays + kJoinThreads - 1) / kJoinThreads), 1, 1);
   lc.blockDim = dim3(kJoinThreads, 1, 1);
   lc.stream = stream;
   cudaLaunchAttribute attr;
@@ -49,14 +48,25 @@ static cudaError_t join_typed(const KvJoinParams& p, int pdl, cudaStream_t strea
   attr.val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = &attr;
   lc.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&lc, kv_join_kernel<kDim>, p);
+  return cudaLaunchKernelEx(&lc, kv_join_kernel<kDim, kWays>, p);
 }
 
-cudaError_t launch_kv_join(const KvJoinParams& p, int dim, int pdl, cudaStream_t stream) {
-  return dim == 64    ? join_typed<64>(p, pdl, stream)
-         : dim == 96  ? join_typed<96>(p, pdl, stream)
-         : dim == 128 ? join_typed<128>(p, pdl, stream)
-                      : join_typed<256>(p, pdl, stream);
+// Up to eight threads to a cell, as long as there are no more than 1024 to an SM.  28 rows on 4 KV heads of 256, 38 pieces
+// of each: the call 55.2 us with one, 49.8 with eight.
+template <int kDim>
+static cudaError_t join_dim(const KvJoinParams& p, int sms, int pdl, cudaStream_t stream) {
+  const int64_t cells = static_cast<int64_t>(p.B) * p.q_len * p.group * p.kv_heads * (kDim / 4), most = 1024ll * sms;
+  if (8 * cells <= most) return join_typed<kDim, 8>(p, cells, pdl, stream);
+  if (4 * cells <= most) return join_typed<kDim, 4>(p, cells, pdl, stream);
+  if (2 * cells <= most) return join_typed<kDim, 2>(p, cells, pdl, stream);
+  return join_typed<kDim, 1>(p, cells, pdl, stream);
+}
+
+cudaError_t launch_kv_join(const KvJoinParams& p, int dim, int sms, int pdl, cudaStream_t stream) {
+  return dim == 64    ? join_dim<64>(p, sms, pdl, stream)
+         : dim == 96  ? join_dim<96>(p, sms, pdl, stream)
+         : dim == 128 ? join_dim<128>(p, sms, pdl, stream)
+                      : join_dim<256>(p, sms, pdl, stream);
 }
 
 }  // namespace fp4

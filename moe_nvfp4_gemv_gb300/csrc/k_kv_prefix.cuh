@@ -695,74 +695,88 @@ struct KvJoinParams {
 };
 constexpr int kJoinThreads = 256;
 
-// Own sums and the pieces of the beginning's to outputs: a thread for four dims of a row, kBatch pieces' loads under way.
-template <int kDim>
+// Own sums and the pieces of the beginning's to outputs: four dims of a row are a cell, of one thread or of kWays that
+// share its pieces out (a warp's lanes by pieces, then by cells), kBatch pieces' loads of each under way.
+template <int kDim, int kWays>
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvJoinParams p) {
   constexpr int kBatch = 8, kCells = kDim / 4;
   if (threadIdx.x == 0) pdl_launch_dependents();
   pdl_wait();
   const KvPrefixLine& line = p.line;
   const int rows = p.q_len * p.group, all_rows = p.B * rows;
-  const int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
-  const int64_t at = x / kCells;
-  const int d = static_cast<int>(x - at * kCells) * 4;
-  if (at >= static_cast<int64_t>(all_rows) * p.kv_heads) return;
+  constexpr int kPerWarp = 32 / kWays;
+  const int lane = threadIdx.x & 31, way = lane / kPerWarp;
+  const int64_t x = (static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5)) * kPerWarp + lane % kPerWarp;
+  const bool live = x < static_cast<int64_t>(all_rows) * p.kv_heads * kCells;
+  const int64_t at = live ? x / kCells : 0;
+  const int d = live ? static_cast<int>(x - at * kCells) * 4 : 0;
   const int head = static_cast<int>(at / all_rows), all = static_cast<int>(at - static_cast<int64_t>(head) * all_rows);
   const int b = all / rows, in = all - b * rows, i = in / p.group;
-  const int64_t token = static_cast<int64_t>(b) * p.q_len + i;
-  const int head_out = head * p.group + in - i * p.group;
-  uint16_t* const out = p.out + token * p.ldo + head_out * kDim + d;
-  float* const lse = d == 0 && p.lse ? p.lse + token * (p.kv_heads * p.group) + head_out : nullptr;
   // (all under way at once; what an empty sequence's row says is not looked at)
   const int length = __ldg(p.lens + b), taken = __ldcg(line.tokens);
   const float2 own = __ldcg(p.ml + at);
-  float4 v = __ldcg(reinterpret_cast<const float4*>(p.sums + at * kDim + d));
-  if (length <= 0) {
-    attn_put(make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f, 0.0f, out, lse, p.f16);
-    return;
-  }
-  float top = own.x, l = own.y;
-  const int tiles = taken / line.tile;
-  if (tiles > 0) {
-    const int per = prefix_share(tiles * p.kv_heads * line.items, line.ctas), block = all >> 7;
-    const int number = line.slots == 1 ? block : block >> 1;
-    const bool both = line.slots == 2 && 2 * number + 1 < line.blocks;  // (else: slots that took the tiles by turns)
-    const int item = head * line.items + number, c0 = item * tiles / per, c1 = ((item + 1) * tiles - 1) / per;
-    const int64_t piece = ((static_cast<int64_t>(c0) + item) * line.slots + (both ? block & 1 : 0)) * 128 + (all & 127);
-    const int step = both ? 2 : 1, cnt = (c1 - c0 + 1) * (line.slots == 1 || both ? 1 : 2);
-    const float2* const ml = line.ml + piece;
-    const float* const sums = line.sums + piece * kDim + d;
+  const float4 sums_own = __ldcg(reinterpret_cast<const float4*>(p.sums + at * kDim + d));
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float top = kAttnFloor, l = 0.0f;
+  if (length > 0) {
+    if (way == 0) v = sums_own, top = own.x, l = own.y;
+    const int tiles = taken / line.tile;
+    if (tiles > 0) {
+      const int per = prefix_share(tiles * p.kv_heads * line.items, line.ctas), block = all >> 7;
+      const int number = line.slots == 1 ? block : block >> 1;
+      const bool both = line.slots == 2 && 2 * number + 1 < line.blocks;  // (else: slots that took the tiles by turns)
+      const int item = head * line.items + number, c0 = item * tiles / per, c1 = ((item + 1) * tiles - 1) / per;
+      const int64_t piece = ((static_cast<int64_t>(c0) + item) * line.slots + (both ? block & 1 : 0)) * 128 + (all & 127);
+      const int step = both ? 2 : 1, cnt = (c1 - c0 + 1) * (line.slots == 1 || both ? 1 : 2);
+      const float2* const ml = line.ml + piece;
+      const float* const sums = line.sums + piece * kDim + d;
 #pragma unroll 1
-    for (int k = 0; k < cnt; k += kBatch) {
-      float2 cm[kBatch];
-      float4 a[kBatch];
+      for (int k = way; k < cnt; k += kBatch * kWays) {
+        float2 cm[kBatch];
+        float4 a[kBatch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        cm[j] = make_float2(kAttnFloor, 0.0f);
-        a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (k + j < cnt) {
-          cm[j] = __ldcg(ml + (k + j) * step * 128);
-          a[j] = __ldcg(reinterpret_cast<const float4*>(sums + static_cast<int64_t>(k + j) * step * (128 * kDim)));
+        for (int j = 0; j < kBatch; ++j) {
+          const int kk = k + j * kWays;
+          cm[j] = make_float2(kAttnFloor, 0.0f);
+          a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (kk < cnt) {
+            cm[j] = __ldcg(ml + static_cast<int64_t>(kk) * step * 128);
+            a[j] = __ldcg(reinterpret_cast<const float4*>(sums + static_cast<int64_t>(kk) * step * (128 * kDim)));
+          }
         }
-      }
-      float mn = top;
+        float mn = top;
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
-      const float fall = attn_ex2(top - mn);
-      v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall;
-      l = attn_lower<kAttnRest>(l, top - mn);
-      top = mn;
+        for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
+        const float fall = attn_ex2(top - mn);
+        v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall;
+        l = attn_lower<kAttnRest>(l, top - mn);
+        top = mn;
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (cm[j].y == 0.0f) a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // (a slot that had no tile wrote no sums)
-        const float f = attn_ex2(cm[j].x - mn);
-        v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
-        v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
-        l += attn_lower<kAttnRest>(cm[j].y, cm[j].x - mn);
+        for (int j = 0; j < kBatch; ++j) {
+          if (cm[j].y == 0.0f) a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // (a slot that had no tile wrote no sums)
+          const float f = attn_ex2(cm[j].x - mn);
+          v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
+          v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
+          l += attn_lower<kAttnRest>(cm[j].y, cm[j].x - mn);
+        }
       }
     }
   }
-  attn_put(v, top, l, out, lse, p.f16);
+#pragma unroll
+  for (int o = kPerWarp; o < 32; o <<= 1) {
+    const float to = __shfl_xor_sync(0xFFFFFFFFu, top, o), lo = __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    const float4 u = make_float4(__shfl_xor_sync(0xFFFFFFFFu, v.x, o), __shfl_xor_sync(0xFFFFFFFFu, v.y, o),
+                                 __shfl_xor_sync(0xFFFFFFFFu, v.z, o), __shfl_xor_sync(0xFFFFFFFFu, v.w, o));
+    const float mn = fmaxf(top, to), f = attn_ex2(top - mn), fo = attn_ex2(to - mn);
+    v.x = v.x * f + u.x * fo, v.y = v.y * f + u.y * fo, v.z = v.z * f + u.z * fo, v.w = v.w * f + u.w * fo;
+    l = attn_lower<kAttnRest>(l, top - mn) + attn_lower<kAttnRest>(lo, to - mn);
+    top = mn;
+  }
+  if (!live || way != 0) return;
+  const int64_t token = static_cast<int64_t>(b) * p.q_len + i;
+  const int head_out = head * p.group + in - i * p.group;
+  attn_put(v, top, l, p.out + token * p.ldo + head_out * kDim + d,
+           d == 0 && p.lse ? p.lse + token * (p.kv_heads * p.group) + head_out : nullptr, p.f16);
 }
 
 }  // namespace fp4
