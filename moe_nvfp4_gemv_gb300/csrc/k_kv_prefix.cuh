@@ -5,28 +5,44 @@
 //
 // The mathematics is k_kv_attention.cuh's: weights 2^(s + log2 vs - m) of codes,
 // f16 for the product with V, m following the maximum lazily, sums fp32; queries
-// are exact f16 operands by a power of two for each row.  What is left per row
-// are m, the sum of weights and the sums of V, which k_kv_attention.cuh joins
-// with those of the sequence's own tokens.
+// are exact f16 operands by a power of two for each row.  m moves by whole
+// numbers here, so weights that are already made move exactly with it.  What is
+// left per row and share are m, the sum of weights and the sums of V.  A last
+// kernel joins them with those of each sequence's own tokens, which
+// k_kv_attention.cuh leaves before this one starts.
 //
 // The beginning is cut at a multiple of 128 tokens that no sequence's first
 // query comes before, so that nothing is masked here: every row sees every
 // token.
 //
-// The layout.  Rows are the M side: blocks of 128 (a row per TMEM lane and per
-// thread, so a row's maximum and sum are registers), tokens the N side of
-// S = Q K^T and the K side of out = P V.  Codes become f16 on their way into
-// shared memory (128-byte swizzle, blocks of 64 dims: K-major for K, the same
-// bytes M-major for V), once for all rows.  P is written over S in tensor memory
-// and is the A operand from there.
+// The layout.  Rows are the M side: blocks of 128 (a row per TMEM lane), tokens
+// the N side of S = Q K^T and the K side of out = P V.  Codes become f16 on
+// their way into shared memory (128-byte swizzle, blocks of 64 dims: K-major for
+// K, the same bytes N-major for V), once for all rows.  P is written over S in
+// tensor memory and is the A operand from there.  Two threads take a row, half a
+// tile's tokens each; they compare their m once a unit.
 //
 // The work.  A CTA per SM.  Items are (KV head, two blocks of rows) and stand on
 // a line, each as long as the beginning has tiles; the line is cut into equal
-// shares.  Two slots, a warpgroup, an S and an accumulator each, take turns on
+// shares.  Two slots, eight warps, an S and an accumulator each, take turns on
 // the tensor core: one makes weights while the other's products run.  An item
 // with two blocks gives each slot a block; with one, the slots take its tiles by
-// turns.  Heads of 256 have room for one accumulator alone: one warpgroup, with
-// the two S in front of it.
+// turns.  Heads of 256 have room for one accumulator alone: one slot, with two S
+// in front of it.  Seven warps move codes, a job of 16 tokens of K or V at a
+// time; one warp issues the products.
+//
+// What bounds it.  64 sequences on 32768 common tokens, 64 heads on 8 of 128, E4M3: the call 98 us, of them 53 for the tiles
+// here, 1.95 us for a tile of 128 tokens and 256 rows (the products alone 1.2 at the measured bf16 rate): shared memory,
+// whose bandwidth the products' operands (Q and K of every step), the movers' loads and their f16 stores share -- a
+// mapping that loads half lines costs 10 percent -- and the chain from scores over weights to the next scores.  The
+// remaining 45: the own tokens' kernel 17 to 24, the start up to the first scores 6.5 (lengths, queries, pages, codes), the
+// sums' way out 4, the join 5, launches.  7 sequences on 65536, heads of 256: 49 us, 1.0 us for 64 tokens, 0.7 of the
+// HBM rate; 24 on 8191, 4 new tokens, INT8 heads of 64: 34, the chain of launches.
+// Steps to it, us: weights in two passes over the scores by one thread a row, the join at the ends of the own tokens' items
+// 177.7; the join's loads out of their loops (registers) 145; scores read once, movers by jobs 121; own tokens first, a kernel for the
+// join 116; two threads a row 97.  Measured and not taken: tiles of 64 tokens with the queries in tensor memory for heads of 128 (112), 11
+// movers (102), one thread for all steps of the products (100), 32 tokens at once per weigher (100), movers without the
+// lanes' exchange of halves (102).
 //
 // Every wait is bounded.  After a failed one (the error word holds
 // FP4_ERR_TIMEOUT) the waits that follow are skipped and the rows' sums are NaN.
@@ -540,8 +556,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
     };
     // the strip of the warp's n-th job, n within this batch or the next
     auto strip_of = [&](int n, int now) -> int {
-      const int a = __shfl_sync(0xFFFFFFFFu, batch, n & 31), c = __shfl_sync(0xFFFFFFFFu, batch_next, n & 31);
-      return (n >> 5) == (now >> 5) ? a : c;
+      return __shfl_sync(0xFFFFFFFFu, (n ^ now) & 32 ? batch_next : batch, n & 31);
     };
     auto source = [&](int n, int strip) -> const uint8_t* {
       const bool v = (first + n * C::kMovers) % C::kJobs >= C::kGroups;
