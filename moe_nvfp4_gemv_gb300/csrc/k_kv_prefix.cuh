@@ -111,16 +111,17 @@ struct PrefixCfg {
   // Movers' jobs: 16 tokens of K or of V, K's of a tile first.
   static constexpr int kJobs = 2 * kGroups;
   static constexpr int kChunks = kDim / 32;             // of 16 codes, per lane and job
-  // Q | K ring | V ring | 2 KB for each weighing warp (of Q, where it is here) | scales [stage][group of 16](K factor, log2 vs, 1 / vs, -) | what a row's
+  // Q | K ring | V ring | 4 KB for each weighing warp (of Q, where it is here) | scales [stage][group of 16](K factor, log2 vs, 1 / vs, -) | what a row's
   // two weighers tell each other [slot][half][row]
   static constexpr int kKOff = kSlots * kQBytes;
   static constexpr int kVOff = kKOff + kStages * kTileBytes;
   static constexpr int kSpareOff = kVOff + kStages * kTileBytes;
-  static constexpr int kScaleOff = kSpareOff + (kQInTmem ? kWeighers / 32 * 2048 : 0);
+  static constexpr int kScaleOff = kSpareOff + (kQInTmem ? kWeighers / 32 * 4096 : 0);
   static constexpr int kRowOff = kScaleOff + kStages * kGroups * 16;
   static constexpr int kSmem = 1024 + kRowOff + kSlots * 256 * 4;
   // TMEM columns: two S, the slots' queries, their sums
   static constexpr uint32_t kCols = 512, kQCol = 2 * kTile, kOCol = 512 - kSlots * kDim;
+  static_assert(kSmem <= 232448, "shared memory");
   static_assert(kQCol + (kQInTmem ? kSlots * kDim / 2 : 0) <= kOCol, "room for all");
 };
 
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
     const uint32_t o_cols = tmem + C::kOCol + slot * kDim + lanes, q_cols = tmem + C::kQCol + slot * (kDim / 2) + lanes;
     float* const row_said = reinterpret_cast<float*>(smem + C::kRowOff) + slot * 256;  // [half][row]
     const uint32_t q_base = sm + slot * C::kQBytes;
-    const uint32_t spare = C::kQInTmem ? sm + C::kSpareOff + warp * 2048 : q_base + (warp & 7) * 2048;  // 32 rows of 64 bytes
+    const uint32_t spare = C::kQInTmem ? sm + C::kSpareOff + warp * 4096 : q_base + (warp & 7) * 4096;  // 32 rows of 128 bytes
     // the two warps of the same rows; whether `v` holds for any of them
     auto both_any = [&](bool v) -> bool { return named_any_of(2 + slot * 4 + quarter, v); };
     int turns[2] = {0, 0};  // units of each S before the segment
@@ -500,21 +501,24 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
         float* const sums = p.line.sums + (piece * 128 + quarter * 32) * kDim;
         if (last >= 0) {
 #pragma unroll 1
-          for (int c = half ? C::kSplit : 0; c < (half ? kDim : C::kSplit); c += 16) {
-            float o[16];
-            tmem_fetch16(o_cols + c, o);
-            tmem_here(o);
+          for (int c = half ? C::kSplit : 0; c < (half ? kDim : C::kSplit); c += 32) {
+            float o[2][16];
+            tmem_fetch16(o_cols + c, o[0]);
+            tmem_fetch16(o_cols + c + 16, o[1]);
+            tmem_here(o[0]);
+            tmem_here(o[1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sts128(spare + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4),
-                     make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
-                                __float_as_uint(o[4 * i + 3])));
+            for (int i = 0; i < 8; ++i) {
+              const float* v = &o[i >> 2][4 * (i & 3)];
+              sts128(spare + lane * 128 + ((i ^ (lane & 7)) << 4),
+                     make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+            }
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = i * 8 + (lane >> 2);
-              const uint4 v = lds128(spare + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-              __stcg(reinterpret_cast<uint4*>(sums + r * kDim + c) + (lane & 3), v);
+            for (int i = 0; i < 8; ++i) {
+              const int r = i * 4 + (lane >> 3);
+              const uint4 v = lds128(spare + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+              __stcg(reinterpret_cast<uint4*>(sums + r * kDim + c) + (lane & 7), v);
             }
             __syncwarp();
           }

@@ -272,6 +272,36 @@ def test_shared_two_streams_at_once(kv):
         assert all(torch.equal(o, want[i]) for o in got[i])
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_shared_right_behind_what_it_reads(kv, dim):
+    """Launches that start early: a beginning written again right before every call, queries that are the last call's
+    outputs, nothing waited for in between; against the same calls one by one."""
+    B, prefix, block = 6, 512, 16
+    lens = [prefix + 3 + 5 * b for b in range(B)]
+    c, table, q0 = case(prefix, lens, 8, 2, dim, block, "e4m3", "bf16", 1)
+    tab, n, start = table.to(DEV), *(torch.tensor(x, dtype=torch.int32, device=DEV) for x in (lens, [prefix]))
+    g = gen(dim)
+    new = [(torch.randn(prefix, 2, dim, generator=g).to(torch.bfloat16).to(DEV),
+            torch.randn(prefix, 2, dim, generator=g).to(torch.bfloat16).to(DEV)) for _ in range(3)]
+    one = torch.tensor([prefix], dtype=torch.int32, device=DEV)
+    results = []
+    for wait in (True, False):
+        cache, q, outs = on_gpu(kv, c, "e4m3"), q0, []
+        torch.cuda.synchronize()
+        for i in range(30):
+            cache.append(*new[i % 3], tab[:1, :prefix // block].contiguous(), one)
+            if wait:
+                torch.cuda.synchronize()
+            q = share(cache, q, tab, n, start)
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(q)
+        torch.cuda.synchronize()
+        results.append(outs)
+    for a, b in zip(*results):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
 def test_shared_by_size(kv):
     """Small batches are attended to one by one, with the same results as that call's; large ones together."""
     c, table, q = case(512, [600, 577], 8, 2, 128, 32, "e4m3", "bf16", 1)
