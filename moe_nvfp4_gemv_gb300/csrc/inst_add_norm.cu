@@ -19,11 +19,13 @@ static cudaError_t add_norm_typed(const AddNormParams& p, int pdl, cudaStream_t 
   return cudaLaunchKernelEx(&lc, add_norm_kernel<kF16, kVec, kX32, kRow, kChunks>, p);
 }
 
-// Few tokens: the fewest threads that hold one in a chunk each, for the shortest chain.  Many: two chunks each, so that
-// a thread has twice the loads under way and an SM holds more tokens.
+// As many tokens as SMs hold at once with a chunk to a thread (1024 threads): that, the shortest chain.  More: two chunks
+// each, so that a thread has twice the loads under way and an SM holds twice the tokens.  One / two chunks, us: 300 tokens
+// of 4096 3.0 / 3.7, 450 5.1 / 3.8; 608 of 2048 3.0 / 3.5; 1 of 4096 2.4 / 2.8.
 template <bool kF16, bool kVec, bool kX32>
 static cudaError_t add_norm_width(const AddNormParams& p, int sms, int pdl, cudaStream_t stream) {
-  const bool many = p.M > 4 * sms;
+  const int threads = p.H <= 1024 ? 128 : p.H <= 2048 ? 256 : p.H <= 4096 ? 512 : 1024;
+  const bool many = static_cast<int64_t>(p.M) * threads > 1024ll * sms;
   if (p.H <= 64) return add_norm_typed<kF16, kVec, kX32, 8, 1>(p, pdl, stream);
   if (p.H <= 128) return add_norm_typed<kF16, kVec, kX32, 16, 1>(p, pdl, stream);
   if (p.H <= 256) return add_norm_typed<kF16, kVec, kX32, 32, 1>(p, pdl, stream);
