@@ -130,8 +130,8 @@ fp4gemv_status fp4gemv_kv_attention(const fp4gemv_kv_cache* cache, const void* q
 /* fp4gemv_kv_attention with first tokens that stay visible: the query at
  * position p sees the tokens t <= p with t > p - window or t < sinks.  Pages
  * of tokens that no query of a sequence sees are not looked at.  window = 0:
- * all of 0 .. p.  sinks >= 0, at most 2^30; the rest as fp4gemv_kv_attention
- * (E4M3, more than 16 rows: exact f16 operands like all others). */
+ * all of 0 .. p.  sinks >= 0, at most 2^30; the rest as
+ * fp4gemv_kv_attention. */
 fp4gemv_status fp4gemv_kv_attention_sinks(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype,
                                           int heads, int q_len, const int32_t* block_table, int max_blocks,
                                           const int32_t* seq_lens, int B, float sm_scale, int window, int sinks,

@@ -378,6 +378,18 @@ fp4gemv_status fp4gemv_kv_attention_sinks(const fp4gemv_kv_cache* cache, const v
   if (sinks == 0 || p.window == 0) return plain_attention(a, p, row_units, sms, stream);
   p.sinks = sinks;
   p.lead = (sinks + 15) / 16;
+  if (row_units == 4 && cache->head_dim == 128 && cache->format == FP4GEMV_KV_E4M3) {
+    CUtensorMap k_map, v_map;
+    const int64_t pages = static_cast<int64_t>(cache->num_blocks) * cache->kv_heads;
+    if (!fp4::encode_pages_128(&k_map, cache->k_codes, cache->block_size, pages) ||
+        !fp4::encode_pages_128(&v_map, cache->v_codes, cache->block_size, pages))
+      return FP4GEMV_ERR_CUDA;
+    p.unit = 8;  // tiles of 128 tokens are of whole pages
+    p.item_cost = fp4::kAttnTcItemCost;
+    p.lead = (p.lead + 7) / 8 * 8;
+    fp4::count_launch();
+    return from_cuda(fp4::launch_kv_attention_tc_sinks(p, k_map, v_map, fp4::skipped_stage(), sms, pdl, stream));
+  }
   fp4::count_launch();
   return from_cuda(fp4::launch_kv_attention_sinks(p, cache->head_dim, cache->format == FP4GEMV_KV_INT8, row_units, sms,
                                                  pdl, stream));

@@ -51,5 +51,7 @@ cudaError_t launch_kv_join(const KvJoinParams& p, int dim, int sms, int pdl, cud
 
 // E4M3, head_dim 128, row tiles of 32.
 cudaError_t launch_kv_attention_tc(const KvAttnTcParams& p, int sms, int pdl, cudaStream_t stream);
+cudaError_t launch_kv_attention_tc_sinks(const KvAttnSinksParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                         int skip_tile, int sms, int pdl, cudaStream_t stream);
 
 }  // namespace fp4

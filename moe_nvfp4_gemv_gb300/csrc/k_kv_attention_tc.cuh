@@ -36,6 +36,11 @@
 // each.  While a group makes weights the other's products run and its own next
 // scores are made.  Shares, segments, partials and their joining are those of
 // k_kv_attention.cuh; shares are cut at tiles, so that tiles hold whole pages.
+// With first tokens that stay visible (kSinks) an item's places are those of its
+// leading tiles and then its window's, and a tile lies on one side of the gap: 32
+// sequences of 32768, window 4096, 4 first tokens, 8 new ones, 32 heads over 8:
+// 72.0 us, the window alone 68.5, mma.sync 97.2; 24 of up to 8191, window 2000, 200
+// first ones, 42.4, 39.1, 58.2.  (One sequence of few tiles may cost one more.)
 //
 // What bounds it.  32 sequences of 16384 tokens, 4 new ones each, 64 heads over
 // 8: 174 us, 0.93 of the measured bandwidth (mma.sync with the codes converted
@@ -56,6 +61,13 @@
 #include "k_kv_attention.cuh"
 
 namespace fp4 {
+
+// ... with first tokens that stay visible (leading strips in whole tiles)
+struct KvAttnTcSinksParams : KvAttnSinksParams {
+  CUtensorMap k_map;  // KvAttnTcParams'
+  CUtensorMap v_map;
+  int skip_tile;
+};
 
 struct AttnTc {
   static constexpr int kDim = 128;
@@ -182,9 +194,11 @@ __device__ __forceinline__ float warp_columns(float (&v)[32], Op op) {
 // they give way to zeros, and the rows that do see their token are noted in nan_dims for the segment's end.  The warp takes
 // four tokens at a time, a lane for each 16 bytes (chunk k of a row lies at k ^ its number mod 8).  A function of its own,
 // since the masks' path is short of instruction cache: 128 sequences of 500 tokens, 4 new ones, 64 heads on 8, 67.4 us,
-// 68.2 where it stands.
+// 68.2 where it stands.  kSinks: tokens before `sinks` of the warp's are outside no window.
+template <bool kSinks>
 __device__ __noinline__ void attn_tc_quiet(uint32_t part, uint32_t v_rows, int since, int window, int q_len, int group,
-                                           int row0, int used, uint32_t (*nan_dims)[AttnTc::kDim / 32], int* nan_any) {
+                                           int row0, int used, uint32_t (*nan_dims)[AttnTc::kDim / 32], int* nan_any,
+                                           int sinks) {
   const int lane = threadIdx.x & 31, k = lane & 7;
   while (part != 0u) {
     uint32_t mine = part;
@@ -207,7 +221,8 @@ __device__ __noinline__ void attn_tc_quiet(uint32_t part, uint32_t v_rows, int s
       dims |= nan_lanes(nan) << (4 * i);
     }
     sts128(at, make_uint4(u[0], u[1], u[2], u[3]));
-    const int first = max(since + token, 0), last = window > 0 ? min(since + token + window, q_len) : q_len;  // its queries
+    const bool stays = window == 0 || (kSinks && token < sinks);
+    const int first = max(since + token, 0), last = stays ? q_len : min(since + token + window, q_len);  // its queries
     for (int r = max(first * group - row0, 0); r < min(last * group - row0, used); ++r) {
       atomicOr(&nan_dims[r][k >> 1], dims << (16 * (k & 1)));
       *nan_any = 1;
@@ -216,7 +231,9 @@ __device__ __noinline__ void attn_tc_quiet(uint32_t part, uint32_t v_rows, int s
   __syncwarp();
 }
 
-__global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(const __grid_constant__ KvAttnTcParams p) {
+template <bool kSinks>
+__global__ void __launch_bounds__(AttnTc::kThreads, 1)
+    kv_attention_tc_kernel(const __grid_constant__ std::conditional_t<kSinks, KvAttnTcSinksParams, KvAttnTcParams> p) {
   using C = AttnTc;
   extern __shared__ __align__(128) uint8_t smem_tc[];
   __shared__ AttnPlace places[3];
@@ -229,6 +246,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
   __shared__ __align__(16) float row_base[C::kGroups][C::kRows];   // kWScale - m; 0 while there is no m to go by
   __shared__ float row_tmp[C::kWeighers / 32][C::kRows];          // maxima, sums of the warps
   __shared__ __align__(16) float row_fall[C::kGroups][C::kRows];
+  __shared__ __align__(16) float row_half[kSinks ? C::kGroups : 1][C::kRows];  // its root, for sums in two steps (attn_lower)
   __shared__ float2 ml[C::kRows];
   __shared__ uint32_t nan_dims[C::kRows][C::kDim / 32];  // of the segment's rows: dims where a token that the row sees is NaN
   __shared__ int nan_any;
@@ -293,6 +311,11 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
   const uint32_t group_o[2] = {tmem + 2 * C::kSCols, tmem + 2 * C::kSCols + C::kOCols};
   AttnPlace cur = places[0];
   int at = begin;
+  // the sequence's strip at place `strip` of an item (a multiple of 8)
+  auto real_strip = [&](const AttnPlace& x) -> int {
+    if constexpr (kSinks) return x.strip >= p.lead ? x.strip + x.first : x.strip;
+    else return x.first + x.strip;
+  };
 
   if (warp >= C::kWeighers / 32 + C::kGroups) {
     // ---- producer of K or of V: lane l looks up page l % 8 of tile l / 8 of every four ----
@@ -315,10 +338,12 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
     auto look_up = [&]() -> Ref {
       Ref r = {0, 0, -1};  // (-1: past the last tile)
       if (at < end) {
-        const int n = tokens[cur.b], page = (((cur.first + cur.strip) << 4) >> p.block_log2) + (lane & 7);
+        const int n = tokens[cur.b], page = ((real_strip(cur) << 4) >> p.block_log2) + (lane & 7);
         const int low = p.window > 0 ? n - p.q_len - p.window + 1 : 0;  // the first token that any query sees
         r.head = cur.head;
-        r.want = (lane & 7) << p.block_log2 < C::kTile && page << p.block_log2 < n && (page + 1) << p.block_log2 > low;
+        r.want = (lane & 7) << p.block_log2 < C::kTile && page << p.block_log2 < n;
+        if constexpr (kSinks) r.want = r.want && ((page + 1) << p.block_log2 > low || page << p.block_log2 < p.sinks);
+        else r.want = r.want && (page + 1) << p.block_log2 > low;
         if (r.want) r.id = __ldg(p.table + static_cast<int64_t>(cur.b) * p.max_blocks + page);
       }
       advance(4);
@@ -460,7 +485,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
     while (at < end) {
       const int seg_end = min(end, at + cur.strips - cur.strip);
       const int tiles = (seg_end - at + 7) >> 3;
-      const int n = tokens[cur.b], row0 = cur.tile * C::kRows, tok0 = (cur.first + cur.strip) << 4;
+      const int n = tokens[cur.b], row0 = cur.tile * C::kRows, tok0 = (kSinks ? cur.strip : cur.first + cur.strip) << 4;
       const int used = min(C::kRows, rows - row0);
       {
         uint32_t raw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -525,7 +550,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
       }
       const int tokens_all = n - p.q_len + 1;                          // every row sees those before this one
       const int tokens_low = p.window > 0 ? max(0, n - p.window) : 0;  // ... from this one on
-      const int tok_end = min(n, tok0 + ((seg_end - at) << 4));
+      const int tok_end = kSinks ? n : min(n, tok0 + ((seg_end - at) << 4));
       const int tok_low = p.window > 0 ? n - p.q_len - p.window + 1 : 0;  // the first token that any query sees
       uint64_t sum[C::kRows / 2];  // of the thread's tokens: weights / vs
 #pragma unroll
@@ -534,7 +559,13 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
       const int j0 = (g - first_tile) & 1;
       for (int j = j0; j < tiles; j += 2, ++count) {
         const int tile = first_tile + j, stage = tile % C::kVStages;
-        const int tile0 = tok0 + j * C::kTile, tok = tile0 + who;
+        int tile0 = tok0 + j * C::kTile, tile_end = tok_end;
+        if constexpr (kSinks) {  // (places, without the gap; a tile lies on one side of it)
+          const int place = tile0;
+          if (place >= p.lead << 4) tile0 += cur.first << 4;
+          tile_end = min(n, tile0 + (tok0 + ((seg_end - at) << 4) - place));
+        }
+        const int tok = tile0 + who;
         wait(scored(g), count & 1);
         wait(v_full(stage), (tile / C::kVStages) & 1);  // the scales and the V row
         tc_fence_after();
@@ -552,8 +583,16 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         const uint32_t scales = sm + C::kScaleOff + stage * 64 + (who >> p.block_log2) * 4;
         const float ks = ldsf(scales), vs = ldsf(scales + 32);
         const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f)), inv_vs = attn_ex2(-lv);
-        const bool live = tok < tok_end && tok >= tok_low;
-        const bool masked = tile0 + C::kTile > min(tokens_all, tok_end) || tile0 < tokens_low;
+        bool live = tok < tile_end && tok >= tok_low;
+        bool masked = tile0 + C::kTile > min(tokens_all, tile_end) || tile0 < tokens_low;
+        bool some = tile0 >= tokens_low;  // every row sees some of the tile
+        bool outside = tok < tokens_low;  // of some row's window
+        if constexpr (kSinks) {
+          live = tok < tile_end && (tok >= tok_low || tok < p.sinks);
+          masked = tile0 + C::kTile > min(tokens_all, tile_end) || (tile0 < tokens_low && tile0 + C::kTile > p.sinks);
+          some = some || tile0 < min(p.sinks, tokens_all);
+          outside = outside && tok >= p.sinks;
+        }
         if (!live) {  // whatever lies there counts nothing
           const uint32_t v_row = sm + C::kVOff + stage * C::kTileBytes + who * 128;
 #pragma unroll
@@ -589,21 +628,26 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
             const int since = tok - (n - p.q_len);
             const int from = max(since, 0) * p.group - row0;
             const int to = !live ? from
-                           : p.window > 0 && since + p.window < p.q_len ? max(since + p.window, 0) * p.group - row0 : C::kRows;
+                           : p.window > 0 && since + p.window < p.q_len && (!kSinks || outside)
+                               ? max(since + p.window, 0) * p.group - row0
+                               : C::kRows;
 #pragma unroll
             for (int r = 0; r < C::kRows; ++r)
               if (r < from || r >= to) v[r] = -__builtin_huge_valf();
-            const uint32_t part = __ballot_sync(0xFFFFFFFFu, live && (tok >= tokens_all || tok < tokens_low));
+            const uint32_t part = __ballot_sync(0xFFFFFFFFu, live && (tok >= tokens_all || outside));
+            int sinks = 0;
+            if constexpr (kSinks) sinks = p.sinks - (tok - lane);
             if (part != 0u)
-              attn_tc_quiet(part, sm + C::kVOff + stage * C::kTileBytes + (who - lane) * 128, tok - lane - (n - p.q_len),
-                            p.window, p.q_len, p.group, row0, used, nan_dims, &nan_any);
+              attn_tc_quiet<kSinks>(part, sm + C::kVOff + stage * C::kTileBytes + (who - lane) * 128,
+                                    tok - lane - (n - p.q_len), p.window, p.q_len, p.group, row0, used, nan_dims, &nan_any,
+                                    sinks);
           }
           float w[32];
 #pragma unroll
           for (int r = 0; r < 32; ++r) w[r] = v[r];
           row_tmp[warp][lane] = warp_columns(w, [](float a, float b) { return fmaxf(a, b); });
           group_sync(g);
-          fresh = fresh && tile0 < tokens_low;
+          fresh = fresh && !some;
           if (who < C::kRows) {
             const float old = row_m[g][who];
             float now = old;
@@ -612,12 +656,18 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
             row_m[g][who] = now;
             row_base[g][who] = fresh ? 0.0f : C::kWScale - now;
             row_fall[g][who] = attn_ex2(old - now);
+            if constexpr (kSinks) row_half[g][who] = attn_ex2(0.5f * (old - now));
           }
           group_sync(g);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             x[i] = pair(v[2 * i] - row_m[g][2 * i] + C::kWScale, v[2 * i + 1] - row_m[g][2 * i + 1] + C::kWScale);
-            sum[i] = mul2(sum[i], *reinterpret_cast<const uint64_t*>(&row_fall[g][2 * i]));
+            if constexpr (kSinks) {
+              const uint64_t half = *reinterpret_cast<const uint64_t*>(&row_half[g][2 * i]);
+              sum[i] = mul2(mul2(sum[i], half), half);
+            } else {
+              sum[i] = mul2(sum[i], *reinterpret_cast<const uint64_t*>(&row_fall[g][2 * i]));
+            }
           }
           if (j > j0) {
             tc_fence_after();
@@ -706,7 +756,8 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         if (tid == 0) nan_any = 0;
       }
       const bool starts = cur.strip == 0, whole = starts && seg_end - at == cur.strips;
-      const AttnItemEnd<C::kDim, C::kWeighers> item_end = {p, cur, row0, used};
+      using EndParams = AttnModeParams<kSinks ? kAttnSinks : kAttnPlain>;
+      const AttnItemEnd<C::kDim, C::kWeighers, EndParams> item_end = {p, cur, row0, used};
       float* const part = item_end.part_of(blockIdx.x, starts ? 1 : 0);
 #pragma unroll
       for (int k = 0; k < C::kRows / (C::kWeighers / 32); ++k) {
@@ -720,7 +771,9 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1) kv_attention_tc_kernel(co
         const float4 u = *reinterpret_cast<const float4*>(a);
         const float4 w = *reinterpret_cast<const float4*>(a + C::kTileBytes / 4);
         const float4 v = make_float4(u.x * f0 + w.x * f1, u.y * f0 + w.y * f1, u.z * f0 + w.z * f1, u.w * f0 + w.w * f1);
-        const float l = failed ? __int_as_float(0x7FC00000) : l0 * f0 + l1 * f1;
+        float l = l0 * f0 + l1 * f1;
+        if constexpr (kSinks) l = attn_lower<kAttnSinks>(l0, m0 - top) + attn_lower<kAttnSinks>(l1, m1 - top);
+        if (failed) l = __int_as_float(0x7FC00000);
         if (whole) {
           item_end.store(r, d, v, top, l);
         } else {

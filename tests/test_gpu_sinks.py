@@ -90,8 +90,9 @@ def test_sinks_of_items_in_pieces(kv, lens, heads, kv_heads, q_len, window, sink
     check(kv, q, c, table, lens, "e4m3", window, sinks)
 
 
-@pytest.mark.parametrize("group,dim,q_len", [(2, 128, 4), (5, 64, 3), (3, 256, 5), (7, 96, 4), (1, 128, 16)])
-@pytest.mark.parametrize("window,sinks", [(1, 3), (20, 18), (130, 5)])
+@pytest.mark.parametrize("group,dim,q_len", [(2, 128, 4), (5, 64, 3), (3, 256, 5), (7, 96, 4), (1, 128, 16), (5, 128, 4),
+                                             (8, 128, 4), (2, 128, 16), (30, 128, 1)])
+@pytest.mark.parametrize("window,sinks", [(1, 3), (20, 18), (130, 5), (150, 140)])
 def test_sinks_nan_values(kv, group, dim, q_len, window, sinks):
     """NaN values among the first tokens, behind them, at the window's begin and at the newest tokens: in the rows that see
     them alone.  Short sequences' first tokens are newer than some queries."""
@@ -109,14 +110,14 @@ def test_sinks_nan_values(kv, group, dim, q_len, window, sinks):
     check(kv, q, c, table, lens, "e4m3", window, sinks, nans=True)
 
 
-@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-def test_sinks_pages_between_are_not_read(kv, fp4, fmt):
+@pytest.mark.parametrize("fmt,dim,heads", [("e4m3", 64, 4), ("int8", 64, 4), ("e4m3", 128, 24)])
+def test_sinks_pages_between_are_not_read(kv, fp4, fmt, dim, heads):
     """Pages of tokens that no query sees may be anyone's: other ids, no ids at all, NaN scales."""
     block, window, sinks, lens = 16, 50, 20, [400, 161, 90]
     g = gen(4)
     table, pages = make_table(lens, block, g)
-    c = scaled(random_cache(pages, 2, block, 64, g, 1.0), fmt)
-    q = torch.randn(3, 2, 4, 64, generator=g).to(torch.bfloat16).to(DEV)
+    c = scaled(random_cache(pages, 2, block, dim, g, 1.0), fmt)
+    q = torch.randn(3, 2, heads, dim, generator=g).to(torch.bfloat16).to(DEV)
     cache, n_len = on_gpu(kv, c, fmt), torch.tensor(lens, dtype=torch.int32, device=DEV)
     want = cache.attend(q, table.to(DEV), n_len, window=window, sinks=sinks)
     for b, n in enumerate(lens):
@@ -125,6 +126,53 @@ def test_sinks_pages_between_are_not_read(kv, fp4, fmt):
             table[b, j] = (-1, 1 << 30)[j % 2]
     got = cache.attend(q, table.to(DEV), n_len, window=window, sinks=sinks)
     assert torch.equal(got, want) and fp4.get_device_error() == 0
+
+
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
+@pytest.mark.parametrize("q_len,group", [(1, 17), (4, 8), (3, 11), (16, 4)])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (30, 128), (128, 129), (200, 4), (513, 300)])
+def test_sinks_many_rows(kv, block, q_len, group, window, sinks):
+    """17 to 64 rows of E4M3 heads of 128: tiles of 128 tokens on both sides of the gap, pages and sets of first tokens that
+    end inside a tile."""
+    lens = [0, 3, 127, 128, 129, 255, 300, 385, 640, 1000, 2111]
+    g = gen(block + window + sinks)
+    table, pages = make_table(lens, block, g)
+    c = scaled(random_cache(pages, 2, block, 128, g, 1.0), "e4m3")
+    for b, n in enumerate(lens):  # (what lies past the ends is NaN)
+        if n % block:
+            for part in ("k_codes", "v_codes"):
+                c[part][int(table[b, n // block]), :, n % block:] = 0x7F
+    q = torch.randn(len(lens), q_len, 2 * group, 128, generator=g).to(torch.bfloat16).to(DEV)
+    check(kv, q, c, table, lens, "e4m3", window, sinks)
+
+
+@pytest.mark.parametrize("lens,heads,kv_heads,q_len,window,sinks", [
+    ([9000], 64, 2, 1, 1024, 4), ([70000], 24, 1, 1, 30000, 700), ([5000, 4000, 3000], 40, 2, 1, 2500, 64),
+    ([3000] * 40, 32, 4, 4, 500, 4)])
+def test_sinks_many_rows_in_pieces(kv, lens, heads, kv_heads, q_len, window, sinks):
+    g = gen(len(lens) + heads)
+    table, pages = make_table(lens, 64, g)
+    c = scaled(random_cache(pages, kv_heads, 64, 128, g, 1.0), "e4m3")
+    q = torch.randn(len(lens), q_len, heads, 128, generator=g).to(torch.float16).to(DEV)
+    check(kv, q, c, table, lens, "e4m3", window, sinks)
+
+
+@pytest.mark.parametrize("fmt,dim,heads", [("e4m3", 128, 24), ("e4m3", 128, 8), ("int8", 64, 24), ("e4m3", 256, 4)])
+@pytest.mark.parametrize("where", [0, 1, 5])
+def test_sinks_zero_pages(kv, fmt, dim, heads, where):
+    """A page of V that is zero, scale 2^-100, beside pages of scale 2^20: its tokens have their part in the sums of weights
+    (the factor between the two kinds' largest exponents is about 2^-120, times what scores differ by)."""
+    block, lens, window, sinks = 64, [1400, 257, 900], 700, 64
+    g = gen(dim + heads + where)
+    table, pages = make_table(lens, block, g)
+    c = scaled(random_cache(pages, 2, block, dim, g, 1.0), fmt)
+    c["v_scale"][:] = 2.0 ** 20
+    for b, n in enumerate(lens):
+        page = int(table[b, min(where * 3, (n - 1) // block)])
+        c["v_codes"][page] = 0
+        c["v_scale"][page] = 2.0 ** -100
+    q = 2 * torch.randn(3, 1, 2 * heads, dim, generator=g).to(torch.bfloat16).to(DEV)
+    check(kv, q, c, table, lens, fmt, window, sinks)
 
 
 def test_sinks_leave_other_calls_alone(kv):
