@@ -153,15 +153,16 @@ size_t fp4gemv_kv_attention_shared_scratch_bytes(int kv_heads, int head_dim, int
  * of 128, less where a sequence's first query stands before that; none is not an
  * error, nor is a negative prefix_len.  Three launches; with always = 0 only
  * where it pays, by the sizes that the host knows: up to
- * FP4GEMV_KV_SHARE_FROM bytes of codes that B sequences as long as the table
- * would have each for itself the call is fp4gemv_kv_attention's.
+ * FP4GEMV_KV_SHARE_FROM bytes of codes that B - 1 sequences as long as the
+ * table have, times the blocks of 16 rows to a KV head (q_len * heads /
+ * kv_heads), the call is fp4gemv_kv_attention's.
  * scratch: 16-byte aligned, fp4gemv_kv_attention_shared_scratch_bytes; the
  * workspace is fp4gemv_kv_attention's.
  * Numerics as fp4gemv_kv_attention's of up to 16 rows: exact f16 operands,
  * probabilities rounded to f16, sums fp32.
  * Shapes as fp4gemv_kv_attention; kv_heads * (B * q_len * heads / kv_heads
  *   rows in blocks of 128) * (max_blocks * block_size / 64) at most 2^30. */
-#define FP4GEMV_KV_SHARE_FROM 100000000ll
+#define FP4GEMV_KV_SHARE_FROM 140000000ll
 fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const void* q, int64_t ldq, int dtype,
                                            int heads, int q_len, const int32_t* block_table, int max_blocks,
                                            const int32_t* seq_lens, int B, const int32_t* prefix_len, float sm_scale,

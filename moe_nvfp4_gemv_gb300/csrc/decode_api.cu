@@ -420,11 +420,15 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
   if (st != FP4GEMV_OK) return st;
   const int dim = cache->head_dim, int8 = cache->format == FP4GEMV_KV_INT8;
   // Where reading a common beginning again and again, out of L2, costs less than two more launches and a beginning cut over
-  // all SMs.  Apart / together, us, heads of 128, E4M3: 4 sequences of 1077 tokens, 8 KV heads (9 MB) 8.9 / 15.1; 16 of 2112
-  // (69 MB) 17 / 26; 8 of 8256 (135 MB) 30 / 29; 16 of 8256 (271 MB) 46 / 31; heads of 256, 32 of 576 (75 MB) 23 / 21.
-  const double apart = static_cast<double>(max_blocks) * cache->block_size * B * cache->kv_heads * dim * 2;
-  if (!always && apart <= FP4GEMV_KV_SHARE_FROM) return plain_attention(a, p, row_units, sms, stream);
+  // all SMs.  What sharing can spare is that of all sequences but one, and reading apart goes over it (or converts it) for
+  // every 16 rows.  Apart / together, us (MB by this measure): 8 rows of 128, E4M3, 16 sequences of 2112 tokens (65) 17 /
+  // 26, 2 of 65375 (134) 48 / 64, 16 of 8256 (254) 46 / 31; 3 rows of 96, INT8, 7 of 37905 (87) 26 / 34; 14 rows of 96,
+  // E4M3, 15 of 6033 (130) 30 / 35; 6 of 64, INT8, 38 of 2071 (157) 39 / 33; more rows: 112 of 128, INT8, 45 of 620 (98) 47 /
+  // 46, 24 of 96, 5 of 11297 (278) 62 / 44, 56 of 256, E4M3, 7 of 14800 (364) 79 / 45.
   const int64_t all_rows = static_cast<int64_t>(B) * q_len * p.group, items = shared_items(all_rows, dim);
+  const double spared = static_cast<double>(max_blocks) * cache->block_size * (B - 1) * cache->kv_heads * dim * 2;
+  if (!always && spared * ((q_len * p.group + 15) / 16) <= FP4GEMV_KV_SHARE_FROM)
+    return plain_attention(a, p, row_units, sms, stream);
   const int64_t piece_ml = shared_ml_bytes(sms + cache->kv_heads * items, dim);
   const int64_t own_ml = static_cast<int64_t>(cache->kv_heads) * ((all_rows + 1) / 2 * 2) * 8;  // (16-byte places)
   char* at = static_cast<char*>(scratch);
