@@ -178,12 +178,16 @@ fp4gemv_status fp4gemv_add_norm(const void* x, int64_t ldx, int x_dtype, const v
   p.scale = scale;
   p.eps = eps;
   p.offset = weight_offset;
-  // whole chunks of 8 values on 16-byte boundaries (an f32 chunk is two of them)
-  auto rows16 = [](const void* q, int64_t ld) { return aligned(q, 16) && ld % 8 == 0; };
-  const bool vec = H % 8 == 0 && rows16(x, ldx) && rows16(out, ldo) && aligned(weight, 16) && aligned(post_weight, 16) &&
-                   (!y || (rows16(y, ldy) && rows16(residual, ldr))) && (!channel || rows16(gate, ldg));
+  // whole chunks of 8 values on 16-byte boundaries (an f32 chunk is two of them); pairs on their own
+  auto parts = [&](int n) {
+    auto at = [&](const void* q, int t) { return aligned(q, std::min<uintptr_t>(n * size(t), 16)); };
+    auto rows = [&](const void* q, int64_t ld, int t) { return at(q, t) && ld % n == 0; };
+    return H % n == 0 && rows(x, ldx, x_dtype) && rows(out, ldo, dtype) && at(weight, weight_dtype) &&
+           at(post_weight, weight_dtype) && (!y || (rows(y, ldy, dtype) && rows(residual, ldr, x_dtype))) &&
+           (!channel || rows(gate, ldg, gate_dtype));
+  };
   fp4::count_launch();
-  return from_cuda(fp4::launch_add_norm(p, dtype == FP4GEMV_F16, vec, sms, pdl, stream));
+  return from_cuda(fp4::launch_add_norm(p, dtype == FP4GEMV_F16, parts(8) ? 8 : parts(2) ? 2 : 1, sms, pdl, stream));
 }
 
 // [arrival counters, three for each CTA | partials, two for each CTA]

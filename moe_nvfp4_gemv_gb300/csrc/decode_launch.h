@@ -26,7 +26,8 @@ cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, int T, int 
 cudaError_t launch_kv_append(const KvAppendParams& p, int int8, int f16, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadParams& p, int int8, int dtype, int sms, int pdl, cudaStream_t stream);
 // vec: rows of 16-byte aligned chunks of 8 values.
-cudaError_t launch_add_norm(const AddNormParams& p, int f16, int vec, int sms, int pdl, cudaStream_t stream);
+// part: values that all rows hold side by side on boundaries of their size, 8 (16 bytes), 2 or 1.
+cudaError_t launch_add_norm(const AddNormParams& p, int f16, int part, int sms, int pdl, cudaStream_t stream);
 // CTAs of the attention kernel at most (the workspace is sized for them).
 int kv_attention_max_ctas(int sms);
 // row_units: row tiles of 8, 16 or 32 rows: 1, 2 or 4 (4 not with head_dim 256).

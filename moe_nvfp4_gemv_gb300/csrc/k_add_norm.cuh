@@ -15,8 +15,11 @@
 // under way before the first sum, two chunks of 8 values to a thread, 1024 threads to an SM.  Of the measured copy
 // bandwidth: 20011 tokens of 4096, bf16, norms on both sides and a gate for each value 132 us, 0.93 (loads as they come to
 // be used, a chunk to a thread: 254); without the gate 0.88, the next norm alone 0.98, an fp32 stream 1.0; 5120 0.77, 6144
-// 0.67, 8192 0.80, 10240 0.79, 16384 0.65 (one CTA to an SM: nothing fills in between its phases).  Rows that are not
-// aligned go value by value: 4099 0.32.  One token of 4096: 3.2 us a call, 37 of 6144 3.6.
+// 0.67, 8192 0.80, 10240 0.79, 16384 0.65 (one CTA to an SM: nothing fills in between its phases).  Rows off these
+// boundaries go by pairs or by values, each a load of its own, neighbours in neighbouring threads, and are bound by the
+// number of these: 4144 of 6892, norms on both sides, 56 us, 0.61 (by values 107), 20011 of 4098 with gates 186, 0.66 (593);
+// 3000 of 10001 110, 0.33.  (Loads of places past the row's end instead of branches around them: 68, 257, 123.)
+// One token of 4096: 3.2 us a call, 37 of 6144 3.6.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -44,91 +47,47 @@ struct AddNormParams {
 
 constexpr int kNormMaxWidth = 32768;
 
-// Eight values of a row, as fp32.  kVec: neighbours, 16-byte aligned; else kStep apart, those before `left` only.
-template <bool kVec, int kStep>
-__device__ __forceinline__ void norm_load(const void* p, int type, int64_t at, int left, float (&v)[8]) {
-  if constexpr (kVec) {
-    if (type == 2) {
-      const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-      const float4 a = s[0], b = s[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// Eight values of a row as they lie, in parts of kPart neighbours that are kStep values apart; those at `left` and behind
+// it are zeros.  Values of a half type by twos in a word each; where a part is one value, a word each.
+template <int kPart, int kStep>
+__device__ __forceinline__ void norm_fetch(const void* p, bool f32, int64_t at, int left, uint32_t (&w)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8 / kPart; ++q) {
+    const bool live = kPart == 8 || q * kStep < left;
+    const int64_t from = at + q * kStep;
+    if (f32) {
+      const float* const s = static_cast<const float*>(p) + from;
+      if constexpr (kPart == 8) {
+        const uint4 a = reinterpret_cast<const uint4*>(s)[0], b = reinterpret_cast<const uint4*>(s)[1];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+      } else if constexpr (kPart == 2) {
+        const uint2 a = live ? *reinterpret_cast<const uint2*>(s) : make_uint2(0, 0);
+        w[2 * q] = a.x, w[2 * q + 1] = a.y;
+      } else {
+        w[q] = live ? *reinterpret_cast<const uint32_t*>(s) : 0u;
+      }
     } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (type == 1) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-          v[2 * k] = f.x, v[2 * k + 1] = f.y;
-        } else {
-          v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = 0.0f;
-      if (j * kStep < left) {
-        const int64_t i = at + j * kStep;
-        if (type == 2) v[j] = static_cast<const float*>(p)[i];
-        else if (type == 1) v[j] = __half2float(static_cast<const __half*>(p)[i]);
-        else v[j] = __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+      const uint16_t* const s = static_cast<const uint16_t*>(p) + from;
+      if constexpr (kPart == 8) {
+        const uint4 a = *reinterpret_cast<const uint4*>(s);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+      } else if constexpr (kPart == 2) {
+        w[q] = live ? *reinterpret_cast<const uint32_t*>(s) : 0u;
+      } else {
+        w[q] = live ? *s : 0u;
       }
     }
   }
 }
-template <bool kVec, int kStep>
-__device__ __forceinline__ void norm_store(void* p, int type, int64_t at, int left, const float (&v)[8]) {
-  if constexpr (kVec) {
-    if (type == 2) {
-      float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-      d[0] = make_float4(v[0], v[1], v[2], v[3]);
-      d[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (type == 1) {
-          const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
-          w[k] = *reinterpret_cast<const uint32_t*>(&h);
-        } else {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-          w[k] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-      }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j * kStep < left) {
-        const int64_t i = at + j * kStep;
-        if (type == 2) static_cast<float*>(p)[i] = v[j];
-        else if (type == 1) static_cast<__half*>(p)[i] = __float2half_rn(v[j]);
-        else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v[j]);
-      }
-  }
-}
-
-// Eight values as they lie (kVec): of a half type in `a`, of fp32 in both.
-struct NormRaw {
-  uint4 a, b;
-};
-__device__ __forceinline__ void norm_fetch(const void* p, bool f32, int64_t at, NormRaw& r) {
-  if (f32) {
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
-    r.a = s[0], r.b = s[1];
-  } else {
-    r.a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-  }
-}
-template <bool kF16>
-__device__ __forceinline__ void norm_values(const NormRaw& r, bool f32, float (&v)[8]) {
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+template <int kPart, bool kF16>
+__device__ __forceinline__ void norm_values(const uint32_t (&w)[8], bool f32, float (&v)[8]) {
   if (f32) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
+  } else if constexpr (kPart == 1) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = kF16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(w[k]))) : __uint_as_float(w[k] << 16);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -141,6 +100,49 @@ __device__ __forceinline__ void norm_values(const NormRaw& r, bool f32, float (&
     }
   }
 }
+template <int kPart, int kStep, bool kF16>
+__device__ __forceinline__ void norm_load(const void* p, bool f32, int64_t at, int left, float (&v)[8]) {
+  uint32_t w[8];
+  norm_fetch<kPart, kStep>(p, f32, at, left, w);
+  norm_values<kPart, kF16>(w, f32, v);
+}
+template <int kPart, int kStep, bool kF16>
+__device__ __forceinline__ void norm_store(void* p, bool f32, int64_t at, int left, const float (&v)[8]) {
+  uint32_t w[4];
+  if (!f32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (kF16) {
+        const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 8 / kPart; ++q) {
+    if (kPart != 8 && q * kStep >= left) continue;
+    const int64_t to = at + q * kStep;
+    if (f32) {
+      float* const d = static_cast<float*>(p) + to;
+      if constexpr (kPart == 8) {
+        reinterpret_cast<float4*>(d)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(d)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else if constexpr (kPart == 2) {
+        *reinterpret_cast<float2*>(d) = make_float2(v[2 * q], v[2 * q + 1]);
+      } else {
+        *d = v[q];
+      }
+    } else {
+      uint16_t* const d = static_cast<uint16_t*>(p) + to;
+      if constexpr (kPart == 8) *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+      else if constexpr (kPart == 2) *reinterpret_cast<uint32_t*>(d) = w[q];
+      else *d = static_cast<uint16_t>(w[q / 2] >> (16 * (q & 1)));
+    }
+  }
+}
 __device__ __forceinline__ float norm_gate(float g, int sigmoid) { return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-g)) : g; }
 
 // Threads of a CTA: whole tokens, 256 threads or more where that comes out even.
@@ -150,11 +152,11 @@ __host__ __device__ constexpr int norm_ctas(int row, int chunks) {
   return chunks == 1 || row > 512 ? 1 : (chunks == 2 ? 1024 : 640) / norm_threads(row) < 1 ? 1 : (chunks == 2 ? 1024 : 640) / norm_threads(row);
 }
 
-// kRow threads to a token, kChunks times eight values each.  kX32: the stream is fp32.
-template <bool kF16, bool kVec, bool kX32, int kRow, int kChunks>
-__global__ void __launch_bounds__(norm_threads(kRow), norm_ctas(kRow, kChunks)) add_norm_kernel(const AddNormParams p) {
-  constexpr int kThreads = norm_threads(kRow), kRows = kThreads / kRow, kWarps = kRow / 32;
-  constexpr int kHalf = kF16 ? 1 : 0;
+// kRow threads to a token, kChunks times eight values each, in parts of kPart neighbours.  kX32: the stream is fp32.
+template <bool kF16, int kPart, bool kX32, int kRow, int kChunks>
+__global__ void __launch_bounds__(norm_threads(kRow), norm_ctas(kRow, kPart == 1 ? 2 * kChunks : kChunks))
+    add_norm_kernel(const AddNormParams p) {
+  constexpr int kThreads = norm_threads(kRow), kRows = kThreads / kRow, kWarps = kRow / 32, kStep = kRow * kPart;
   __shared__ float sums[2][kThreads / 32];
   const int tid = threadIdx.x % kRow, group = threadIdx.x / kRow;
   if (threadIdx.x == 0) pdl_launch_dependents();
@@ -181,19 +183,18 @@ __global__ void __launch_bounds__(norm_threads(kRow), norm_ctas(kRow, kChunks)) 
     return s;
   };
   // chunk i of the thread: its first value, and whether the row has any from there
-  auto first = [&](int i) -> int { return kVec ? (tid + i * kRow) * 8 : i * 8 * kRow + tid; };
+  auto first = [&](int i) -> int { return tid * kPart + i * 8 * kRow; };
   auto live = [&](int i) -> bool { return row < p.M && first(i) < p.H; };
-  // what the row needs of HBM, under way at once (not kVec: as it comes to be used)
-  NormRaw xr[kChunks], yr[kChunks], gr[kChunks];
-  const bool gated = p.gate && !p.gate_scalar, g32 = p.g_type == 2;
-  if constexpr (kVec) {
+  // what the row needs of HBM, under way at once
+  uint32_t xr[kChunks][8], yr[kChunks][8], gr[kChunks][8];
+  const bool gated = p.gate && !p.gate_scalar, g32 = p.g_type == 2, w32 = p.w_type == 2;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      if (!live(i)) continue;
-      if (p.y) norm_fetch(p.y, false, row * p.ldy + first(i), yr[i]);
-      norm_fetch(p.x, kX32, row * p.ldx + first(i), xr[i]);
-      if (gated && !g32) norm_fetch(p.gate, false, row * p.ldg + first(i), gr[i]);
-    }
+  for (int i = 0; i < kChunks; ++i) {
+    if (!live(i)) continue;
+    const int left = p.H - first(i);
+    if (p.y) norm_fetch<kPart, kStep>(p.y, false, row * p.ldy + first(i), left, yr[i]);
+    norm_fetch<kPart, kStep>(p.x, kX32, row * p.ldx + first(i), left, xr[i]);
+    if (gated && !g32) norm_fetch<kPart, kStep>(p.gate, false, row * p.ldg + first(i), left, gr[i]);
   }
   float r[kChunks][8];
 #pragma unroll
@@ -201,13 +202,8 @@ __global__ void __launch_bounds__(norm_threads(kRow), norm_ctas(kRow, kChunks)) 
 #pragma unroll
     for (int j = 0; j < 8; ++j) r[i][j] = 0.0f;
     if (!live(i)) continue;
-    if (p.y) {
-      if constexpr (kVec) norm_values<kF16>(yr[i], false, r[i]);
-      else norm_load<kVec, kRow>(p.y, kHalf, row * p.ldy + first(i), p.H - first(i), r[i]);
-    } else {
-      if constexpr (kVec) norm_values<kF16>(xr[i], kX32, r[i]);
-      else norm_load<kVec, kRow>(p.x, p.x_type, row * p.ldx + first(i), p.H - first(i), r[i]);
-    }
+    if (p.y) norm_values<kPart, kF16>(yr[i], false, r[i]);
+    else norm_values<kPart, kF16>(xr[i], kX32, r[i]);
   }
   if (p.y) {
     float factor = p.scale;
@@ -231,26 +227,25 @@ __global__ void __launch_bounds__(norm_threads(kRow), norm_ctas(kRow, kChunks)) 
       if (!live(i)) continue;
       const int left = p.H - first(i);
       float f[8], x[8];
-      if constexpr (kVec) norm_values<kF16>(xr[i], kX32, x);
-      else norm_load<kVec, kRow>(p.x, p.x_type, row * p.ldx + first(i), left, x);
+      norm_values<kPart, kF16>(xr[i], kX32, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = factor;
       if (p.post) {
         float w[8];
-        norm_load<kVec, kRow>(p.post, p.w_type, first(i), left, w);
+        norm_load<kPart, kStep, kF16>(p.post, w32, first(i), left, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] *= w[j] + p.offset;
       }
       if (gated) {
         float g[8];
-        if (kVec && !g32) norm_values<kF16>(gr[i], false, g);
-        else norm_load<kVec, kRow>(p.gate, p.g_type, row * p.ldg + first(i), left, g);
+        if (g32) norm_load<kPart, kStep, kF16>(p.gate, true, row * p.ldg + first(i), left, g);
+        else norm_values<kPart, kF16>(gr[i], false, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] *= norm_gate(g[j], p.sigmoid);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[i][j] = kVec || j * kRow < left ? fmaf(r[i][j], f[j], x[j]) : 0.0f;
-      norm_store<kVec, kRow>(p.residual, p.x_type, row * p.ldr + first(i), left, r[i]);
+      for (int j = 0; j < 8; ++j) r[i][j] = kPart == 8 || j / kPart * kStep < left ? fmaf(r[i][j], f[j], x[j]) : 0.0f;
+      norm_store<kPart, kStep, kF16>(p.residual, kX32, row * p.ldr + first(i), left, r[i]);
     }
   }
   float s = 0.0f;
@@ -264,10 +259,10 @@ __global__ void __launch_bounds__(norm_threads(kRow), norm_ctas(kRow, kChunks)) 
     if (!live(i)) continue;
     const int left = p.H - first(i);
     float w[8];
-    norm_load<kVec, kRow>(p.weight, p.w_type, first(i), left, w);
+    norm_load<kPart, kStep, kF16>(p.weight, w32, first(i), left, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = r[i][j] * f * (w[j] + p.offset);
-    norm_store<kVec, kRow>(p.out, kHalf, row * p.ldo + first(i), left, w);
+    norm_store<kPart, kStep, kF16>(p.out, false, row * p.ldo + first(i), left, w);
   }
 }
 

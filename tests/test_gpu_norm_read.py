@@ -64,7 +64,9 @@ def check_norm(fp4, x, y, w, post=None, gate=None, sigmoid=False, scale=1.0, eps
 @pytest.mark.parametrize("dtype,res,wt", [(BF16, BF16, BF16), (BF16, F32, F32), (F16, F16, F32), (F16, F32, F16)])
 @pytest.mark.parametrize("m,h,pad", [(1, 4096, 0), (3, 1, 0), (5, 7, 0), (9, 129, 0), (2, 256, 8), (33, 257, 0),
                                      (4, 1000, 24), (3, 2048, 1), (2, 5120, 0), (2, 8192, 8), (3, 8191, 0),
-                                     (2, 16384, 0), (1, 16390, 0), (2, 32768, 0), (1, 32767, 0), (301, 64, 0)])
+                                     (2, 16384, 0), (1, 16390, 0), (2, 32768, 0), (1, 32767, 0), (301, 64, 0),
+                                     (5, 2, 0), (7, 66, 0), (33, 258, 2), (5, 1002, 6), (3, 6146, 1), (1300, 514, 0),
+                                     (1300, 1026, 4), (700, 2050, 0), (300, 5122, 0), (200, 8194, 0), (700, 4099, 0)])
 def test_norm_shapes(fp4, dtype, res, wt, m, h, pad):
     g = torch.Generator(device="cuda").manual_seed(m * 100003 + h)
     x, y = rows(m, h, res, g, pad, 3.0), rows(m, h, dtype, g, pad)
@@ -73,10 +75,27 @@ def test_norm_shapes(fp4, dtype, res, wt, m, h, pad):
     check_norm(fp4, x, y, w, post=post, gate=rows(m, h, dtype, g, pad), sigmoid=True, scale=0.37, offset=1.0)
 
 
+@pytest.mark.parametrize("res", [BF16, F32])
+@pytest.mark.parametrize("which", range(6))
+def test_norm_one_off_its_boundary(fp4, res, which):
+    """All rows on boundaries of pairs but one tensor's (its first value is its buffer's second)."""
+    g = torch.Generator(device="cuda").manual_seed(which)
+    m, h = 5, 642
+    def make(k, dtype, *shape):
+        flat = torch.randn(m * h + 1, generator=g, device="cuda").to(dtype)
+        n = 1
+        for d in shape:
+            n *= d
+        return flat[int(k == which):][:n].view(*shape)
+    x, y, gate = make(0, res, m, h), make(1, BF16, m, h), make(2, BF16, m, h)
+    w, post = make(3, F32, h), make(4, BF16, h) if which == 4 else make(4, F32, h)
+    check_norm(fp4, x, y, w.to(post.dtype) if which == 4 else w, post=post, gate=gate, sigmoid=True)
+
+
 @pytest.mark.parametrize("gate", ["channel", "token", "rows", "expanded"])
 @pytest.mark.parametrize("gate_type", [BF16, F32])
 @pytest.mark.parametrize("sigmoid", [False, True])
-@pytest.mark.parametrize("h", [512, 515])
+@pytest.mark.parametrize("h", [512, 514, 515])
 def test_norm_gates(fp4, gate, gate_type, sigmoid, h):
     m = 13
     g = torch.Generator(device="cuda").manual_seed(h + sigmoid)
