@@ -75,6 +75,7 @@
 namespace fp4 {
 
 struct KvAttnParams {
+  static constexpr bool kByWarps = false;  // whether warps may take items of few strips by themselves (attn_items)
   const uint8_t* k_codes;
   const uint8_t* v_codes;
   const float* k_scale;
@@ -107,11 +108,13 @@ enum AttnMode { kAttnPlain, kAttnSinks, kAttnRest };
 // A sequence's items hold `lead` strips of its beginning, then those of its window, with a gap between them that counts as
 // no strips.
 struct KvAttnSinksParams : KvAttnParams {
+  static constexpr bool kByWarps = true;
   int sinks;  // the first tokens that stay visible
   int lead;   // their strips
 };
 // The beginning's strips count as none; a row's sums are left as they are for k_kv_prefix.cuh's join.
 struct KvAttnRestParams : KvAttnParams {
+  static constexpr bool kByWarps = true;
   const int32_t* prefix_len;
   float* sums;  // [kv_heads][B q_len group rows][dim]
   float2* ml;   // [kv_heads][rows]: m, the sum of weights
@@ -156,6 +159,8 @@ constexpr int kAttnFan = 40;
 constexpr int kAttnFan2 = 20;
 // An item's end, in strips.  256 sequences of 500 tokens, 8 KV heads: 66 us with 8 or 16, 63 with 32.
 constexpr int kAttnItemCost = 32;
+// ... in strips, where a warp takes it by itself.  With 10: 848 items of 3 strips 19.7 us, with 4 8.7.
+constexpr int kAttnWarpCost = 4;
 constexpr int kAttnTcItemCost = 64;  // ... of the kernel on the 5th-generation tensor core (its figures there)
 // The running maximum before any token: finite, so that no difference of two is a NaN, and below every finite score.
 constexpr float kAttnFloor = -0x1.fffffep127f;
@@ -336,6 +341,7 @@ __device__ __forceinline__ void attn_plan(const P& p, int* strips_before, int* l
         plan_words[2] = per;
         plan_words[3] = 0;
         plan_words[4] = 1;
+        plan_words[5] = 0;
       }
     }
   } else if (warp == 0) {
@@ -383,6 +389,14 @@ __device__ __forceinline__ void attn_plan(const P& p, int* strips_before, int* l
         if (longest <= p.uncut) per = max(whole(longest), kAttnRound);
       }
       const bool pieces = per > 0;
+      if (P::kByWarps && lane == 0) {
+        // Items by warps, where that takes fewer rounds: an item's strips one after another, as against eight at a time and
+        // the ends of all of a CTA's.
+        const int slots = ctas * (kThreads / 32);
+        const float turns = static_cast<float>((alive + slots - 1) / slots);
+        plan_words[5] = !pieces && turns * static_cast<float>(longest + kAttnWarpCost) * static_cast<float>(slots) <
+                                       static_cast<float>(total) + static_cast<float>(alive) * p.item_cost;
+      }
       const int lead = pieces ? 0 : p.item_cost;
       if (!pieces) per = max(whole(attn_div_up(total + alive * p.item_cost, ctas, p.inv_ctas)), kAttnRound);
       const float inv_per = __fdividef(1.0f, static_cast<float>(per));
@@ -784,6 +798,324 @@ struct AttnCfg {
   static constexpr int smem(int B) { return kSmem + (B + 1) * 12; }
 };
 
+// The 16 dims a k-step of query `row` of a KV head that thread t of four takes; zeros past the last row.
+template <int kDim>
+__device__ __forceinline__ void attn_q_load(const KvAttnParams& p, const AttnPlace& c, int row, uint4 (&raw)[kDim / 32]) {
+  using L = AttnLayout<kDim>;
+  const bool live = row < p.q_len * p.group;
+  const int i = live ? (row * p.group_magic) >> 16 : 0;
+  const uint16_t* src = p.q + (static_cast<int64_t>(c.b) * p.q_len + i) * p.ldq +
+                        (c.head * p.group + (live ? row - i * p.group : 0)) * kDim;
+#pragma unroll
+  for (int k = 0; k < L::kSteps / 2; ++k) {  // words 2 k and 2 k + 1: eight dims in a row
+    const int d = L::k_dim(2 * k / L::kWords, 2 * k % L::kWords, threadIdx.x & 3);
+    raw[k] = live ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0, 0, 0, 0);
+  }
+}
+// Operands in place; the row's factor of the scores.
+template <int kDim>
+__device__ __forceinline__ float attn_q_scale(const KvAttnParams& p, uint4 (&raw)[kDim / 32]) {
+  const float factor = p.sm_scale * 1.4426950408889634f;
+  if (p.f16) return factor;
+  uint32_t top = 0;  // two magnitudes of bf16: ordered like their bits
+#pragma unroll
+  for (int k = 0; k < kDim / 32; ++k) {
+    const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
+  }
+  top = max(top & 0xFFFFu, top >> 16);
+  top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+  // 2^-e brings the largest to [2^14, 2^15)
+  const int field = static_cast<int>(top >> 7);
+  const int e = field == 0 ? 0 : min(max(field - 127 - 14, -126), 126);
+  const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+  for (int k = 0; k < kDim / 32; ++k) {
+    uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = pack_f16(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
+    raw[k] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return factor * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
+// Items of few strips, where there are many: a warp takes one from its queries to its outputs.  No barriers, nothing to
+// join; the warps' waits fill one another's.  The warp's ring holds strips and, behind them, its queries.  By CTAs an item
+// takes 3 us (16 rows of 256: 7), most of it between barriers.  By CTAs / by warps, us: first tokens and windows of up to 2
+// strips, 784 items of 16 rows of 256 46 / 10.2, 848 of 16 rows of 64 19 / 8.7, 624 of one row of 256 17 / 6.6; 50 sequences
+// of up to 27 tokens of their own, 1600 items of 16 rows of 256, with their beginning 69 / 54.7.
+template <int kDim, bool kInt8, int kN, int kRes, int kMode>
+__device__ __forceinline__ void attn_items(const AttnModeParams<kMode>& p, uint32_t ring, const int* tokens,
+                                           uint32_t (*nan_dims)[kDim / 32], int* nan_any) {
+  using C = AttnCfg<kDim, kN, kRes>;
+  using L = AttnLayout<kDim>;
+  constexpr int kRing = C::kStages - (kN == 1 ? 0 : (kN * L::kSteps * 256 + C::kStageBytes - 1) / C::kStageBytes);
+  static_assert(kRing >= 2, "a strip in use and one on its way");
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
+  const uint32_t q_base = ring + kRing * C::kStageBytes;
+  const int rows = p.q_len * p.group, items = p.kv_heads * p.row_tiles;
+  const int k_place = L::k_place(g, t), v_place = L::v_row_place(g, t);
+  const int copy_first = L::chunk(lane / (kDim / 16), lane % (kDim / 16));
+  const int step = static_cast<int>(gridDim.x) * C::kWarps;
+  if (!kInt8) {
+    for (int i = lane; i < C::kRows * (kDim / 32); i += 32) (&nan_dims[0][0])[i] = 0u;
+    if (lane == 0) *nan_any = 0;
+  }
+  for (int64_t id = blockIdx.x + gridDim.x * warp; id < static_cast<int64_t>(p.B) * items; id += step) {
+    AttnPlace cur;
+    cur.b = static_cast<int>(id) / items;
+    cur.item = static_cast<int>(id) - cur.b * items;
+    cur.head = cur.item / p.row_tiles;
+    cur.tile = cur.item - cur.head * p.row_tiles;
+    const int n = tokens[cur.b];
+    if (n <= 0) continue;
+    cur.first = attn_first_strip(p, n);
+    cur.strip = 0;
+    cur.strips = attn_strips_of(p, n);
+    const int row0 = cur.tile * C::kRows, used = min(C::kRows, rows - row0);
+    auto real = [&](int strip) -> int {
+      if constexpr (kMode == kAttnSinks) return strip >= p.lead ? strip + cur.first : strip;
+      else return strip + cur.first;
+    };
+    int batch = -1, filled = 0, fill_stage = 0;
+    auto issue = [&]() {
+      if ((filled & 31) == 0) {  // the next 32 strips' places: -1 past the last one, -2 on a bad page
+        batch = -1;
+        if (filled + lane < cur.strips) {
+          const int strip = real(filled + lane), per_page = p.block_log2 - 4;
+          const int page = __ldg(p.table + static_cast<int64_t>(cur.b) * p.max_blocks + (strip >> per_page));
+          batch = page >= 0 && page < p.num_blocks
+                      ? ((page * p.kv_heads + cur.head) << per_page) + (strip & ((1 << per_page) - 1))
+                      : -2;
+        }
+      }
+      int strip = __shfl_sync(0xFFFFFFFFu, batch, filled & 31);
+      if (strip != -1) {
+        const uint32_t dst = ring + fill_stage * C::kStageBytes;
+        const uint32_t bytes = strip >= 0 ? 16u : 0u;
+        if (strip < 0) {
+          if (lane == 0) raise_error(p.err, FP4_ERR_BADIDX);
+          strip = 0;
+        }
+        const int64_t at = static_cast<int64_t>(strip) * L::kStripBytes + lane * 16;
+#pragma unroll
+        for (int i = 0; i < kDim / 32; ++i) {
+          cp_async16(dst + L::copy_to(copy_first, i), p.k_codes + at + i * 512, bytes);
+          cp_async16(dst + L::kStripBytes + L::copy_to(copy_first, i), p.v_codes + at + i * 512, bytes);
+        }
+        if (lane < 2) {
+          const float* scale = (lane ? p.v_scale : p.k_scale) + (strip >> (p.block_log2 - 4));
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 2 * L::kStripBytes + 4 * lane),
+                       "l"(scale), "r"(bytes >> 2)
+                       : "memory");
+        }
+      }
+      ++filled;
+      if (++fill_stage == kRing) fill_stage = 0;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    __syncwarp();  // (every lane is past the item before)
+#pragma unroll
+    for (int k = 0; k < kRing - 1; ++k) issue();
+    uint4 qr[L::kSteps / 2];
+    float rs[kN][2], m[kN][2], sum[kN][2], acc[kN][L::kTiles][4];
+#pragma unroll
+    for (int nt = 0; nt < kN; ++nt) {
+      attn_q_load<kDim>(p, cur, row0 + nt * 8 + g, qr);
+      const float f = attn_q_scale<kDim>(p, qr);
+      if (kN > 1) {  // (a lane reads what it wrote)
+#pragma unroll
+        for (int i = 0; i < L::kSteps / 2; ++i) sts128(q_base + ((nt * (L::kSteps / 2) + i) * 32 + lane) * 16, qr[i]);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        rs[nt][h] = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4 * h);
+        m[nt][h] = kAttnFloor;
+        sum[nt][h] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < L::kTiles; ++j) acc[nt][j][h] = acc[nt][j][2 + h] = 0.0f;
+      }
+    }
+    const int tokens_all = n - p.q_len + 1;                          // every row sees those before this one
+    const int tokens_low = p.window > 0 ? max(0, n - p.window) : 0;  // ... from this one on
+    const bool parts = !kInt8 && (p.q_len > 1 || p.window > 0);
+    bool fresh = true;
+    int stage = 0;
+#pragma unroll 1
+    for (int k = 0; k < cur.strips; ++k) {
+      const int here = real(k) << 4, left = n - here;
+      const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + L::kStripBytes;
+      if (++stage == kRing) stage = 0;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+      __syncwarp();  // the strip is there, and every lane is past the stage read last
+      issue();
+      if (parts && (here < tokens_low || here + 16 > tokens_all)) {
+        int sinks = 0;
+        if constexpr (kMode == kAttnSinks) sinks = p.sinks - here;
+        attn_quiet<kDim, kMode == kAttnSinks>(vb, min(16, left), here - (n - p.q_len), p.window, p.q_len, p.group, row0, used,
+                                              nan_dims, nan_any, sinks);
+      }
+      float sc[kN][4];  // tokens g (0, 1) and g + 8 (2, 3) by rows 2t and 2t + 1
+#pragma unroll
+      for (int nt = 0; nt < kN; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+#pragma unroll
+      for (int blk = 0; blk < L::kBlocks; ++blk) {
+        uint32_t w[2][L::kWords];
+        L::k_words(kb, k_place, 0, blk, w[0]);
+        L::k_words(kb, k_place, 1, blk, w[1]);
+#pragma unroll
+        for (int s = 0; s < L::kWords; s += 2) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            a[e][0] = codes2_lo<kInt8>(w[0][s + e]);
+            a[e][1] = codes2_lo<kInt8>(w[1][s + e]);
+            a[e][2] = codes2_hi<kInt8>(w[0][s + e]);
+            a[e][3] = codes2_hi<kInt8>(w[1][s + e]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < kN; ++nt) {
+            const int pair = (blk * L::kWords + s) / 2;
+            uint4 b;
+            if constexpr (kN == 1) b = qr[pair];
+            else b = lds128(q_base + ((nt * (L::kSteps / 2) + pair) * 32 + lane) * 16);
+            mma_f16(sc[nt], a[0], b.x, b.y);
+            mma_f16(sc[nt], a[1], b.z, b.w);
+          }
+        }
+      }
+      float ks, vs;
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(kb + 2 * L::kStripBytes));
+      const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
+      const float inv_vs = attn_ex2(-lv) * kAttnUnlift;
+      bool masked = here + 16 > tokens_all || here < tokens_low;
+      bool some = here >= tokens_low;  // every row sees some of the strip
+      if constexpr (kMode == kAttnSinks) {
+        masked = here + 16 > tokens_all || (here < tokens_low && here + 16 > p.sinks);
+        some = some || here < min(p.sinks, tokens_all);
+      }
+      // exponents; the running maxima move where they must (as in the kernel below)
+      float high = -1.0f;
+#pragma unroll
+      for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float f = rs[nt][h] * ks, base = fresh ? lv : lv - m[nt][h];
+          sc[nt][h] = fmaf(sc[nt][h], f, base);
+          sc[nt][2 + h] = fmaf(sc[nt][2 + h], f, base);
+          high = fmaxf(high, fmaxf(sc[nt][h], sc[nt][2 + h]));
+        }
+      if (masked || fresh || __any_sync(0xFFFFFFFFu, high > kAttnLift + kAttnSlack)) {
+#pragma unroll
+        for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float base = fresh ? 0.0f : m[nt][h];
+            float r0 = sc[nt][h] + base, r1 = sc[nt][2 + h] + base;
+            if (masked) {
+              const int row = min(row0 + nt * 8 + 2 * t + h, rows - 1);
+              const int see_to = n - p.q_len + ((row * p.group_magic) >> 16) + 1;
+              const int see_from = p.window > 0 ? see_to - p.window : 0;
+              bool out0 = here + g < see_from, out1 = here + 8 + g < see_from;
+              if constexpr (kMode == kAttnSinks) {
+                out0 = out0 && here + g >= p.sinks;
+                out1 = out1 && here + 8 + g >= p.sinks;
+              }
+              if (here + g >= see_to || out0) r0 = -__builtin_huge_valf();
+              if (here + 8 + g >= see_to || out1) r1 = -__builtin_huge_valf();
+            }
+            float top = fmaxf(r0, r1);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const float mn = fmaxf(m[nt][h], top - kAttnLift);
+            const float fall = attn_ex2(m[nt][h] - mn);
+            sum[nt][h] = attn_lower<kMode>(sum[nt][h], m[nt][h] - mn);
+            m[nt][h] = mn;
+#pragma unroll
+            for (int j = 0; j < L::kTiles; ++j) {
+              acc[nt][j][h] *= fall;
+              acc[nt][j][2 + h] *= fall;
+            }
+            sc[nt][h] = r0 - mn;
+            sc[nt][2 + h] = r1 - mn;
+          }
+        fresh = fresh && !some;
+      }
+      uint32_t pb[kN][2];
+#pragma unroll
+      for (int nt = 0; nt < kN; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][e] = attn_ex2(sc[nt][e]);
+        sum[nt][0] = fmaf(sc[nt][0] + sc[nt][2], inv_vs, sum[nt][0]);
+        sum[nt][1] = fmaf(sc[nt][1] + sc[nt][3], inv_vs, sum[nt][1]);
+        pb[nt][0] = transpose8x8(pack_f16(sc[nt][0], sc[nt][1]));
+        pb[nt][1] = transpose8x8(pack_f16(sc[nt][2], sc[nt][3]));
+      }
+#pragma unroll
+      for (int blk = 0; blk < L::kBlocks; ++blk) {
+        uint32_t w[4][L::kVWords];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) L::v_words(vb, v_place, c, blk, w[c]);
+        if (left < 16) {  // past the end: whatever lies there counts nothing
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (2 * t + (c & 1) + (c >> 1) * 8 >= left) {
+#pragma unroll
+              for (int i = 0; i < L::kVWords; ++i) w[c][i] = 0u;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < L::kVWords; ++i) {
+          const uint32_t lo[2] = {__byte_perm(w[0][i], w[1][i], 0x5140), __byte_perm(w[0][i], w[1][i], 0x7362)};
+          const uint32_t hi[2] = {__byte_perm(w[2][i], w[3][i], 0x5140), __byte_perm(w[2][i], w[3][i], 0x7362)};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t a[4] = {codes2_lo<kInt8>(lo[j]), codes2_hi<kInt8>(lo[j]), codes2_lo<kInt8>(hi[j]),
+                                   codes2_hi<kInt8>(hi[j])};
+#pragma unroll
+            for (int nt = 0; nt < kN; ++nt) mma_f16(acc[nt][(blk * L::kVWords + i) * 2 + j], a, pb[nt][0], pb[nt][1]);
+          }
+        }
+      }
+    }
+    // ---- outputs, from the registers ----
+    const AttnItemEnd<kDim, C::kThreads, AttnModeParams<kMode>> item_end = {p, cur, row0, used};
+    const bool nans = !kInt8 && *nan_any != 0;  // (every lane's marks are in: attn_quiet ends with a barrier)
+#pragma unroll
+    for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) sum[nt][h] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][h], o);
+        const int r = nt * 8 + 2 * t + h;
+        if (r >= used) continue;
+#pragma unroll
+        for (int k = 0; k < L::kTiles / 2; ++k) {
+          const int d = L::v_dim(k / L::kVWords, k % L::kVWords, g);
+          float v[4] = {acc[nt][2 * k][h] * kAttnUnlift, acc[nt][2 * k][2 + h] * kAttnUnlift,
+                        acc[nt][2 * k + 1][h] * kAttnUnlift, acc[nt][2 * k + 1][2 + h] * kAttnUnlift};
+          if (nans) {
+            const uint32_t which = nan_dims[r][d >> 5] >> (d & 31);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (which >> i & 1u) v[i] = __int_as_float(0x7FC00000);
+          }
+          item_end.store(r, d, make_float4(v[0], v[1], v[2], v[3]), m[nt][h] + kAttnLift, sum[nt][h]);
+        }
+      }
+    if (nans) {
+      __syncwarp();
+      for (int i = lane; i < C::kRows * (kDim / 32); i += 32) (&nan_dims[0][0])[i] = 0u;
+      if (lane == 0) *nan_any = 0;
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 template <int kDim, bool kInt8, int kN, int kRes, int kMode = kAttnPlain>
 __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
     kv_attention_kernel(const AttnModeParams<kMode> p) {
@@ -844,48 +1176,24 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
   const int begin = plan_words[0], end = plan_words[1];
 
   if (kMode != kAttnRest) attn_empty<kDim, C::kThreads>(p, tokens);  // (the join sees to them)
+  // (The rest of sequences, up to 8 rows: the code beside it costs the other path more, heads of 256, 7 sequences on 65536
+  // 49.8 us, with it 56.3, than it spares where items are short: heads of 128, 64 on 16384, up to 20 own tokens, 62.3, 58.5.)
+  if constexpr (kMode == kAttnSinks || (kMode == kAttnRest && kN > 1)) {
+    if (plan_words[5] != 0) {
+      __shared__ uint32_t nan_words[kInt8 ? 1 : C::kWarps][C::kRows][kDim / 32];
+      __shared__ int nan_flags[C::kWarps];
+      attn_items<kDim, kInt8, kN, kRes, kMode>(p, sm + warp * C::kStages * C::kStageBytes, tokens,
+                                               nan_words[kInt8 ? 0 : warp], &nan_flags[warp]);
+      return;
+    }
+  }
   if (begin >= end) return;
 
   // ---- queries: f16 operands; bf16 ones scaled by a power of two for each row ----
   auto q_load = [&](const AttnPlace& c, int tile8, uint4 (&raw)[L::kSteps / 2]) {  // row g of the item's tile of 8
-    const int row = c.tile * C::kRows + tile8 * 8 + g;
-    const bool live = row < rows;
-    const int i = live ? (row * p.group_magic) >> 16 : 0;
-    const uint16_t* src = p.q + (static_cast<int64_t>(c.b) * p.q_len + i) * p.ldq +
-                          (c.head * p.group + (live ? row - i * p.group : 0)) * kDim;
-#pragma unroll
-    for (int k = 0; k < L::kSteps / 2; ++k) {  // words 2 k and 2 k + 1: eight dims in a row
-      const int d = L::k_dim(2 * k / L::kWords, 2 * k % L::kWords, t);
-      raw[k] = live ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0, 0, 0, 0);
-    }
+    attn_q_load<kDim>(p, c, c.tile * C::kRows + tile8 * 8 + g, raw);
   };
-  auto q_scale = [&](uint4 (&raw)[L::kSteps / 2]) -> float {  // operands in place; row g's factor of the scores
-    const float factor = p.sm_scale * 1.4426950408889634f;
-    if (p.f16) return factor;
-    uint32_t top = 0;  // two magnitudes of bf16: ordered like their bits
-#pragma unroll
-    for (int k = 0; k < L::kSteps / 2; ++k) {
-      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
-    }
-    top = max(top & 0xFFFFu, top >> 16);
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    // 2^-e brings the largest to [2^14, 2^15)
-    const int field = static_cast<int>(top >> 7);
-    const int e = field == 0 ? 0 : min(max(field - 127 - 14, -126), 126);
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-    for (int k = 0; k < L::kSteps / 2; ++k) {
-      uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = pack_f16(__uint_as_float(w[j] << 16) * down, __uint_as_float(w[j] & 0xFFFF0000u) * down);
-      raw[k] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    return factor * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-  };
+  auto q_scale = [&](uint4 (&raw)[L::kSteps / 2]) -> float { return attn_q_scale<kDim>(p, raw); };
   uint4 qr[L::kSteps / 2];
   if (C::kQInRegs) q_load(places[0], 0, qr);
 

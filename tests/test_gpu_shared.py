@@ -179,6 +179,17 @@ def test_shared_small_weights_count(kv, fmt, bits, dim):
     assert ((out - want).abs() <= 2.0 ** -10 * want + (n + 1) * 2.0 ** -32).all()
 
 
+@pytest.mark.parametrize("fmt,dim,heads,q_len,block", [
+    ("e4m3", 64, 6, 1, 16), ("int8", 64, 54, 2, 32), ("e4m3", 96, 9, 4, 32), ("int8", 128, 12, 2, 64), ("e4m3", 128, 30, 2, 16),
+    ("int8", 128, 24, 4, 128), ("e4m3", 256, 6, 4, 64), ("int8", 256, 51, 1, 32)])
+@pytest.mark.parametrize("prefix", [130, 500])
+def test_shared_many_short_ends(kv, fmt, dim, heads, q_len, block, prefix):
+    """More sequences' ends than SMs hold CTAs, of few strips each: a warp takes one by itself."""
+    lens = [prefix + q_len + (23 * i) % 70 if i % 9 else 0 for i in range(150)]
+    c, table, q = case(prefix, lens, heads, 3, dim, block, fmt, "bf16", q_len)
+    check(kv, c, fmt, q, table, lens, prefix)
+
+
 def test_shared_nan_codes(kv):
     """A NaN value of the beginning is in every row; one of a sequence's own tokens in that sequence alone; of tokens past
     the ends, and of an idle sequence's pages, in none."""

@@ -175,6 +175,36 @@ def test_sinks_zero_pages(kv, fmt, dim, heads, where):
     check(kv, q, c, table, lens, fmt, window, sinks)
 
 
+@pytest.mark.parametrize("fmt,dim,group,q_len,block", [
+    ("e4m3", 64, 1, 1, 16), ("e4m3", 64, 4, 4, 32), ("int8", 64, 24, 1, 64), ("e4m3", 96, 8, 1, 32), ("int8", 96, 5, 3, 16),
+    ("e4m3", 96, 6, 4, 16), ("e4m3", 128, 8, 1, 64), ("int8", 128, 4, 4, 16), ("int8", 128, 10, 3, 32), ("e4m3", 256, 3, 2, 16),
+    ("int8", 256, 8, 2, 128), ("e4m3", 256, 17, 1, 64)])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (20, 17), (60, 100)])
+def test_sinks_many_short_items(kv, fmt, dim, group, q_len, block, window, sinks):
+    """More items than SMs hold CTAs, of few strips each: a warp takes one by itself."""
+    lens = [(37 * i) % 113 if i % 5 else (11 * i) % 900 for i in range(180)]
+    g = gen(dim + group + window)
+    table, pages = make_table(lens, block, g)
+    c = scaled(random_cache(pages, 2, block, dim, g, 1.0), fmt)
+    q = torch.randn(len(lens), q_len, 2 * group, dim, generator=g).to(torch.bfloat16).to(DEV)
+    check(kv, q, c, table, lens, fmt, window, sinks)
+
+
+@pytest.mark.parametrize("dim,group,q_len", [(64, 3, 4), (96, 4, 2), (128, 2, 5), (256, 3, 4)])
+def test_sinks_many_short_items_nan_values(kv, dim, group, q_len):
+    """NaN values in some items of a warp: in their rows that see them and in no others."""
+    block, window, sinks = 16, 30, 18
+    lens = [3 + (29 * i) % 90 for i in range(200)]
+    g = gen(dim)
+    table, pages = make_table(lens, block, g)
+    c = scaled(random_cache(pages, 2, block, dim, g, 1.0), "e4m3")
+    for b in range(0, 200, 7):
+        for t, head, d in ((0, 0, 5), (lens[b] - 1, 1, dim - 1), (max(lens[b] - window - 1, 0), 0, 33), (min(17, lens[b] - 1), 1, 60)):
+            c["v_codes"][int(table[b, t // block]), head, t % block, d] = 0x7F
+    q = torch.randn(len(lens), q_len, 2 * group, dim, generator=g).to(torch.float16).to(DEV)
+    check(kv, q, c, table, lens, "e4m3", window, sinks, nans=True)
+
+
 def test_sinks_leave_other_calls_alone(kv):
     """No window, a window past every length, no sinks: the results of the calls without."""
     lens = [300, 20, 0]
