@@ -155,7 +155,8 @@ size_t fp4gemv_kv_attention_shared_scratch_bytes(int kv_heads, int head_dim, int
  * where it pays, by the sizes that the host knows: up to
  * FP4GEMV_KV_SHARE_FROM bytes of codes that B - 1 sequences as long as the
  * table have, times the blocks of 16 rows to a KV head (q_len * heads /
- * kv_heads), the call is fp4gemv_kv_attention's.
+ * kv_heads), every sequence is attended to by itself, as fp4gemv_kv_attention
+ * does.
  * scratch: 16-byte aligned, fp4gemv_kv_attention_shared_scratch_bytes; the
  * workspace is fp4gemv_kv_attention's.
  * Numerics as fp4gemv_kv_attention's of up to 16 rows: exact f16 operands,

@@ -332,11 +332,16 @@ static fp4gemv_status attention_params(const AttentionCall& a, fp4::KvAttnParams
   return FP4GEMV_OK;
 }
 
+// Whether the kernel on the 5th-generation tensor core takes the call.
+static bool wide_e4m3(const fp4gemv_kv_cache* cache, int row_units) {
+  return row_units == 4 && cache->head_dim == 128 && cache->format == FP4GEMV_KV_E4M3;
+}
+
 // (the checks are done)
 static fp4gemv_status plain_attention(const AttentionCall& a, const fp4::KvAttnParams& base, int row_units, int sms,
                                       cudaStream_t stream) {
   const fp4gemv_kv_cache* const cache = a.cache;
-  if (row_units == 4 && cache->head_dim == 128 && cache->format == FP4GEMV_KV_E4M3) {
+  if (wide_e4m3(cache, row_units)) {
     fp4::KvAttnTcParams p = {};
     static_cast<fp4::KvAttnParams&>(p) = base;
     const int64_t pages = static_cast<int64_t>(cache->num_blocks) * cache->kv_heads;
@@ -382,7 +387,7 @@ fp4gemv_status fp4gemv_kv_attention_sinks(const fp4gemv_kv_cache* cache, const v
   if (sinks == 0 || p.window == 0) return plain_attention(a, p, row_units, sms, stream);
   p.sinks = sinks;
   p.lead = (sinks + 15) / 16;
-  if (row_units == 4 && cache->head_dim == 128 && cache->format == FP4GEMV_KV_E4M3) {
+  if (wide_e4m3(cache, row_units)) {
     CUtensorMap k_map, v_map;
     const int64_t pages = static_cast<int64_t>(cache->num_blocks) * cache->kv_heads;
     if (!fp4::encode_pages_128(&k_map, cache->k_codes, cache->block_size, pages) ||
@@ -431,8 +436,23 @@ fp4gemv_status fp4gemv_kv_attention_shared(const fp4gemv_kv_cache* cache, const 
   // 46, 24 of 96, 5 of 11297 (278) 62 / 44, 56 of 256, E4M3, 7 of 14800 (364) 79 / 45.
   const int64_t all_rows = static_cast<int64_t>(B) * q_len * p.group, items = shared_items(all_rows, dim);
   const double spared = static_cast<double>(max_blocks) * cache->block_size * (B - 1) * cache->kv_heads * dim * 2;
-  if (!always && spared * ((q_len * p.group + 15) / 16) <= FP4GEMV_KV_SHARE_FROM)
+  if (!always && spared * ((q_len * p.group + 15) / 16) <= FP4GEMV_KV_SHARE_FROM) {
+    // Many items that cannot be long: the kernel whose warps take them by themselves (no window, no first tokens).
+    // us, fp4gemv_kv_attention's kernel / this one: 50 sequences of 58 tokens, 64 rows of 256 on 8 KV heads, INT8, 86 / 25; 64
+    // of 128, 8 rows of 128, E4M3, on 8 14 / 11, 16 rows on 16 32 / 16; 64 of 500, 8 rows, INT8, on 16 39 / 28.
+    const int ctas = sms * (dim == 256 || row_units == 4 ? 1 : 2);
+    const double items = static_cast<double>(B) * p.kv_heads * p.row_tiles;
+    const double strips = (static_cast<double>(max_blocks) * cache->block_size + 15) / 16;
+    if (items > ctas && !wide_e4m3(cache, row_units) &&
+        fp4::attn_by_warps(static_cast<float>(items), static_cast<float>(items * strips), static_cast<float>(strips),
+                           static_cast<float>(8 * ctas))) {
+      fp4::KvAttnSinksParams x = {};
+      static_cast<fp4::KvAttnParams&>(x) = p;
+      fp4::count_launch();
+      return from_cuda(fp4::launch_kv_attention_sinks(x, dim, int8, row_units, sms, pdl, stream));
+    }
     return plain_attention(a, p, row_units, sms, stream);
+  }
   const int64_t piece_ml = shared_ml_bytes(sms + cache->kv_heads * items, dim);
   const int64_t own_ml = static_cast<int64_t>(cache->kv_heads) * ((all_rows + 1) / 2 * 2) * 8;  // (16-byte places)
   char* at = static_cast<char*>(scratch);

@@ -159,8 +159,6 @@ constexpr int kAttnFan = 40;
 constexpr int kAttnFan2 = 20;
 // An item's end, in strips.  256 sequences of 500 tokens, 8 KV heads: 66 us with 8 or 16, 63 with 32.
 constexpr int kAttnItemCost = 32;
-// ... in strips, where a warp takes it by itself.  With 10: 848 items of 3 strips 19.7 us, with 4 8.7.
-constexpr int kAttnWarpCost = 4;
 constexpr int kAttnTcItemCost = 64;  // ... of the kernel on the 5th-generation tensor core (its figures there)
 // The running maximum before any token: finite, so that no difference of two is a NaN, and below every finite score.
 constexpr float kAttnFloor = -0x1.fffffep127f;
@@ -285,6 +283,15 @@ __device__ __forceinline__ int attn_strips_of(const P& p, int n) {
 
 __device__ __forceinline__ int attn_units(const KvAttnParams& p, int strips) { return (strips + p.unit - 1) & -p.unit; }
 
+// Whether `items` of `strips` in all and `longest` at most are done sooner by a warp each than by CTAs one after another:
+// a warp's strips follow on one another and its end is short; a CTA takes eight strips at a time, and an item's end and the
+// chain to the next one's first sums take as long as 112 strips (kAttnItemCost is what the ends cost beside long items).
+// us with 32 / 64 / 112 / 200: 512 items of 10 strips of 128 17.3 / 12.1 / 12.1 / 12.1, 1024 of 41 46.9 / 46.9 / 36.0 / 35.9,
+// 400 of 33, 16 rows of 256, 53 / 53 / 37.3 / 37.3; 512 of 33 27.4 / 27.3 / 27.2 / 28.2.
+inline __host__ __device__ bool attn_by_warps(float items, float strips, float longest, float warps) {
+  return ceilf(items / warps) * (longest + 4.0f) * warps < strips + items * 112.0f;
+}
+
 // The plan, by the first warp (a lane per sequence, in rounds of 32; lens by
 // all threads where there are many).  For every sequence: its tokens, and what
 // the sequences before hold in strips and in length on the line.  The share:
@@ -390,12 +397,9 @@ __device__ __forceinline__ void attn_plan(const P& p, int* strips_before, int* l
       }
       const bool pieces = per > 0;
       if (P::kByWarps && lane == 0) {
-        // Items by warps, where that takes fewer rounds: an item's strips one after another, as against eight at a time and
-        // the ends of all of a CTA's.
-        const int slots = ctas * (kThreads / 32);
-        const float turns = static_cast<float>((alive + slots - 1) / slots);
-        plan_words[5] = !pieces && turns * static_cast<float>(longest + kAttnWarpCost) * static_cast<float>(slots) <
-                                       static_cast<float>(total) + static_cast<float>(alive) * p.item_cost;
+        const float slots = static_cast<float>(ctas * (kThreads / 32));
+        plan_words[5] = !pieces && attn_by_warps(static_cast<float>(alive), static_cast<float>(total),
+                                                 static_cast<float>(longest), slots);
       }
       const int lead = pieces ? 0 : p.item_cost;
       if (!pieces) per = max(whole(attn_div_up(total + alive * p.item_cost, ctas, p.inv_ctas)), kAttnRound);
@@ -844,7 +848,7 @@ __device__ __forceinline__ float attn_q_scale(const KvAttnParams& p, uint4 (&raw
 
 // Items of few strips, where there are many: a warp takes one from its queries to its outputs.  No barriers, nothing to
 // join; the warps' waits fill one another's.  The warp's ring holds strips and, behind them, its queries.  By CTAs an item
-// takes 3 us (16 rows of 256: 7), most of it between barriers.  By CTAs / by warps, us: first tokens and windows of up to 2
+// takes 3 us (16 rows of 256: 7), most of it between barriers.  By CTAs / by warps, us: first tokens and windows of up to 3
 // strips, 784 items of 16 rows of 256 46 / 10.2, 848 of 16 rows of 64 19 / 8.7, 624 of one row of 256 17 / 6.6; 50 sequences
 // of up to 27 tokens of their own, 1600 items of 16 rows of 256, with their beginning 69 / 54.7.
 template <int kDim, bool kInt8, int kN, int kRes, int kMode>

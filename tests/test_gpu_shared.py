@@ -50,17 +50,18 @@ def case(prefix, lens, heads, kv_heads, dim, block, fmt, dtype, q_len, seed=0, s
     return c, table, q
 
 
-def run(kv, c, fmt, q, table, lens, prefix, sm_scale=None, **kw):
+def run(kv, c, fmt, q, table, lens, prefix, sm_scale=None, always=True, **kw):
     cache = on_gpu(kv, c, fmt)
     lse = torch.full(q.shape[:3], 7.0, dtype=torch.float32, device=DEV)
     out = cache.attend_shared(q, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
-                              torch.tensor([prefix], dtype=torch.int32, device=DEV), lse=lse, sm_scale=sm_scale, always=True, **kw)
+                              torch.tensor([prefix], dtype=torch.int32, device=DEV), lse=lse, sm_scale=sm_scale, always=always,
+                              **kw)
     return out, lse
 
 
-def check(kv, c, fmt, q, table, lens, prefix, sm_scale=None, nans=False):
-    out, lse = run(kv, c, fmt, q, table, lens, prefix, sm_scale)
-    again, _ = run(kv, c, fmt, q, table, lens, prefix, sm_scale)
+def check(kv, c, fmt, q, table, lens, prefix, sm_scale=None, nans=False, always=True):
+    out, lse = run(kv, c, fmt, q, table, lens, prefix, sm_scale, always=always)
+    again, _ = run(kv, c, fmt, q, table, lens, prefix, sm_scale, always=always)
     assert torch.equal(out.view(torch.int16), again.view(torch.int16)), "two calls differ"
     scale = sm_scale if sm_scale is not None else 1 / math.sqrt(q.shape[-1])
     want, want_lse, mass, peak = attention64(q, c, table, lens, fmt, scale, 0, 0)
@@ -182,12 +183,23 @@ def test_shared_small_weights_count(kv, fmt, bits, dim):
 @pytest.mark.parametrize("fmt,dim,heads,q_len,block", [
     ("e4m3", 64, 6, 1, 16), ("int8", 64, 54, 2, 32), ("e4m3", 96, 9, 4, 32), ("int8", 128, 12, 2, 64), ("e4m3", 128, 30, 2, 16),
     ("int8", 128, 24, 4, 128), ("e4m3", 256, 6, 4, 64), ("int8", 256, 51, 1, 32)])
-@pytest.mark.parametrize("prefix", [130, 500])
-def test_shared_many_short_ends(kv, fmt, dim, heads, q_len, block, prefix):
-    """More sequences' ends than SMs hold CTAs, of few strips each: a warp takes one by itself."""
+@pytest.mark.parametrize("prefix,always", [(130, True), (500, True), (40, False), (130, False)])
+def test_shared_many_short_ends(kv, fmt, dim, heads, q_len, block, prefix, always):
+    """More sequences' ends, or whole sequences, than SMs hold CTAs, of few strips each: a warp takes one by itself."""
     lens = [prefix + q_len + (23 * i) % 70 if i % 9 else 0 for i in range(150)]
     c, table, q = case(prefix, lens, heads, 3, dim, block, fmt, "bf16", q_len)
-    check(kv, c, fmt, q, table, lens, prefix)
+    check(kv, c, fmt, q, table, lens, prefix, always=always)
+
+
+def test_shared_many_short_sequences_nan_codes(kv):
+    """... their NaN values, each in the rows that see them."""
+    prefix, q_len = 40, 4
+    lens = [prefix + q_len + (23 * i) % 70 for i in range(200)]
+    c, table, q = case(prefix, lens, 6, 3, 64, 16, "e4m3", "bf16", q_len)
+    for b in range(0, 200, 9):
+        for t, d in ((lens[b] - 1, 3), (lens[b] - 3, 40)):
+            c["v_codes"][int(table[b, t // 16]), 1, t % 16, d] = 0x7F
+    check(kv, c, "e4m3", q, table, lens, prefix, nans=True, always=False)
 
 
 def test_shared_nan_codes(kv):

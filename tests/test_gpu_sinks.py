@@ -190,6 +190,17 @@ def test_sinks_many_short_items(kv, fmt, dim, group, q_len, block, window, sinks
     check(kv, q, c, table, lens, fmt, window, sinks)
 
 
+@pytest.mark.parametrize("fmt,dim,group,q_len", [("e4m3", 64, 3, 1), ("int8", 128, 2, 1), ("int8", 96, 3, 4)])
+def test_sinks_many_items_past_a_batch_of_pages(kv, fmt, dim, group, q_len):
+    """Enough items for warps to take those of more than 32 strips by themselves (pages are looked up 32 strips at a time)."""
+    lens = [620 + (41 * i) % 300 if i % 8 else i for i in range(400)]
+    g = gen(dim + group)
+    table, pages = make_table(lens, 32, g)
+    c = scaled(random_cache(pages, 2, 32, dim, g, 1.0), fmt)
+    q = torch.randn(len(lens), q_len, 2 * group, dim, generator=g).to(torch.bfloat16).to(DEV)
+    check(kv, q, c, table, lens, fmt, 560, 20)
+
+
 @pytest.mark.parametrize("dim,group,q_len", [(64, 3, 4), (96, 4, 2), (128, 2, 5), (256, 3, 4)])
 def test_sinks_many_short_items_nan_values(kv, dim, group, q_len):
     """NaN values in some items of a warp: in their rows that see them and in no others."""
