@@ -286,8 +286,8 @@ __device__ __forceinline__ int attn_units(const KvAttnParams& p, int strips) { r
 // Whether `items` of `strips` in all and `longest` at most are done sooner by a warp each than by CTAs one after another:
 // a warp's strips follow on one another and its end is short; a CTA takes eight strips at a time, and an item's end and the
 // chain to the next one's first sums take as long as 112 strips (kAttnItemCost is what the ends cost beside long items).
-// us with 32 / 64 / 112 / 200: 512 items of 10 strips of 128 17.3 / 12.1 / 12.1 / 12.1, 1024 of 41 46.9 / 46.9 / 36.0 / 35.9,
-// 400 of 33, 16 rows of 256, 53 / 53 / 37.3 / 37.3; 512 of 33 27.4 / 27.3 / 27.2 / 28.2.
+// us with 32 / 64 / 112 / 200: 512 items of 10 strips of 128 17.3 / 12.1 / 12.1 / 12.1, 1024 of 41 46.9 / 46.9 / 36.0 /
+// 35.9, 400 of 33, 16 rows of 256, 53 / 53 / 37.3 / 37.3; 512 of 33 27.4 / 27.3 / 27.2 / 28.2.
 inline __host__ __device__ bool attn_by_warps(float items, float strips, float longest, float warps) {
   return ceilf(items / warps) * (longest + 4.0f) * warps < strips + items * 112.0f;
 }
@@ -1180,9 +1180,10 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
   const int begin = plan_words[0], end = plan_words[1];
 
   if (kMode != kAttnRest) attn_empty<kDim, C::kThreads>(p, tokens);  // (the join sees to them)
-  // (The rest of sequences, up to 8 rows: the code beside it costs the other path more, heads of 256, 7 sequences on 65536
-  // 49.8 us, with it 56.3, than it spares where items are short: heads of 128, 64 on 16384, up to 20 own tokens, 62.3, 58.5.)
-  if constexpr (kMode == kAttnSinks || (kMode == kAttnRest && kN > 1)) {
+  // (The rest of sequences, up to 8 rows, or 16 with two CTAs to an SM: the code beside it costs the other path more than
+  // it spares where items are short.  Heads of 256, 7 sequences on 65536, 49.8 us, with it 56.3; 16 rows of 64, 24 on
+  // 8191, 34.4, 35.3; 8 rows of 128, 64 on 16384, up to 20 own tokens, 62.3, 58.5.)
+  if constexpr (kMode == kAttnSinks || (kMode == kAttnRest && kN > 1 && kRes == 1)) {
     if (plan_words[5] != 0) {
       __shared__ uint32_t nan_words[kInt8 ? 1 : C::kWarps][C::kRows][kDim / 32];
       __shared__ int nan_flags[C::kWarps];

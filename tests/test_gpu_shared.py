@@ -191,6 +191,14 @@ def test_shared_many_short_ends(kv, fmt, dim, heads, q_len, block, prefix, alway
     check(kv, c, fmt, q, table, lens, prefix, always=always)
 
 
+@pytest.mark.parametrize("fmt,dim,heads,always", [("e4m3", 256, 16, True), ("int8", 128, 32, True), ("e4m3", 96, 12, True),
+                                                  ("int8", 256, 16, False), ("e4m3", 128, 16, False)])
+def test_shared_largest_batch(kv, fmt, dim, heads, always):
+    lens = [130 + (11 * i) % 90 if i % 7 else 0 for i in range(1024)]
+    c, table, q = case(128, lens, heads, 1, dim, 32, fmt, "bf16", 1)
+    check(kv, c, fmt, q, table, lens, 128, always=always)
+
+
 def test_shared_many_short_sequences_nan_codes(kv):
     """... their NaN values, each in the rows that see them."""
     prefix, q_len = 40, 4

@@ -216,6 +216,38 @@ def test_sinks_many_short_items_nan_values(kv, dim, group, q_len):
     check(kv, q, c, table, lens, "e4m3", window, sinks, nans=True)
 
 
+@pytest.mark.parametrize("fmt,dim,group,q_len", [("e4m3", 128, 9, 2), ("e4m3", 256, 4, 4), ("int8", 128, 16, 2),
+                                                 ("e4m3", 96, 32, 1), ("int8", 64, 2, 1)])
+def test_sinks_largest_batch(kv, fmt, dim, group, q_len):
+    """1024 sequences (the plan's tables fill shared memory to its end), idle ones among them."""
+    lens = [(11 * i) % 150 for i in range(1024)]
+    g = gen(dim)
+    table, pages = make_table(lens, 32, g)
+    c = scaled(random_cache(pages, 1, 32, dim, g, 1.0), fmt)
+    q = torch.randn(1024, q_len, group, dim, generator=g).to(torch.bfloat16).to(DEV)
+    check(kv, q, c, table, lens, fmt, 40, 20)
+
+
+@pytest.mark.parametrize("fmt,dim", [("e4m3", 64), ("int8", 256)])
+def test_sinks_many_short_items_bad_pages(kv, fp4, fmt, dim):
+    """A page id that is none: the error word says so, its sequences read zeros there, the others are untouched."""
+    lens = [20 + (7 * i) % 40 for i in range(200)]
+    g = gen(dim)
+    table, pages = make_table(lens, 16, g)
+    c = scaled(random_cache(pages, 2, 16, dim, g, 1.0), fmt)
+    q = torch.randn(200, 1, 8, dim, generator=g).to(torch.bfloat16).to(DEV)
+    cache, n = on_gpu(kv, c, fmt), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    good = cache.attend(q, table.to(DEV), n, window=30, sinks=4)
+    assert fp4.get_device_error() == 0
+    bad = table.clone()
+    bad[50, 0], bad[120, 1] = pages + 5, -7
+    got = cache.attend(q, bad.to(DEV), n, window=30, sinks=4)
+    assert fp4.get_device_error() == 6
+    assert not got.isnan().any()
+    same = [b for b in range(200) if b not in (50, 120)]
+    assert torch.equal(got[same], good[same])
+
+
 def test_sinks_leave_other_calls_alone(kv):
     """No window, a window past every length, no sinks: the results of the calls without."""
     lens = [300, 20, 0]
