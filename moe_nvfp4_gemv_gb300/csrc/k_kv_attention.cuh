@@ -59,9 +59,8 @@
 //
 // A window with first tokens that stay visible costs what the window alone does (kAttnSinks): 32 sequences of 32768,
 // window 4096, 4 first tokens, 64 heads on 8, E4M3 53.5 us (52.7; 0.75 of the bandwidth on the tokens seen), one of 5000,
-// window 1024, 8.4, 48 ragged ones of up to 3001, window 777, 130 first tokens, 4 new, INT8 heads of 96 29.4.  More than
-// 16 rows of E4M3 heads of 128 stay here as well: 32 rows, window 4096 97 us (the window alone on the 5th-generation
-// tensor core 69).
+// window 1024, 8.4, 48 ragged ones of up to 3001, window 777, 130 first tokens, 4 new, INT8 heads of 96 29.4.  Many short
+// windows go by warps (attn_items); more than 16 rows of E4M3 heads of 128 through k_kv_attention_tc.cuh.
 #pragma once
 
 #include <type_traits>
