@@ -801,11 +801,12 @@ struct AttnCfg {
   static constexpr int smem(int B) { return kSmem + (B + 1) * 12; }
 };
 
-// The 16 dims a k-step of query `row` of a KV head that thread t of four takes; zeros past the last row.
+// What a thread takes of query `row` of a KV head's `rows`; zeros past the last one.
 template <int kDim>
-__device__ __forceinline__ void attn_q_load(const KvAttnParams& p, const AttnPlace& c, int row, uint4 (&raw)[kDim / 32]) {
+__device__ __forceinline__ void attn_q_load(const KvAttnParams& p, const AttnPlace& c, int row, int rows,
+                                            uint4 (&raw)[kDim / 32]) {
   using L = AttnLayout<kDim>;
-  const bool live = row < p.q_len * p.group;
+  const bool live = row < rows;
   const int i = live ? (row * p.group_magic) >> 16 : 0;
   const uint16_t* src = p.q + (static_cast<int64_t>(c.b) * p.q_len + i) * p.ldq +
                         (c.head * p.group + (live ? row - i * p.group : 0)) * kDim;
@@ -928,7 +929,7 @@ __device__ __forceinline__ void attn_items(const AttnModeParams<kMode>& p, uint3
     float rs[kN][2], m[kN][2], sum[kN][2], acc[kN][L::kTiles][4];
 #pragma unroll
     for (int nt = 0; nt < kN; ++nt) {
-      attn_q_load<kDim>(p, cur, row0 + nt * 8 + g, qr);
+      attn_q_load<kDim>(p, cur, row0 + nt * 8 + g, rows, qr);
       const float f = attn_q_scale<kDim>(p, qr);
       if (kN > 1) {  // (a lane reads what it wrote)
 #pragma unroll
@@ -1195,7 +1196,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
 
   // ---- queries: f16 operands; bf16 ones scaled by a power of two for each row ----
   auto q_load = [&](const AttnPlace& c, int tile8, uint4 (&raw)[L::kSteps / 2]) {  // row g of the item's tile of 8
-    attn_q_load<kDim>(p, c, c.tile * C::kRows + tile8 * 8 + g, raw);
+    attn_q_load<kDim>(p, c, c.tile * C::kRows + tile8 * 8 + g, rows, raw);
   };
   auto q_scale = [&](uint4 (&raw)[L::kSteps / 2]) -> float { return attn_q_scale<kDim>(p, raw); };
   uint4 qr[L::kSteps / 2];
