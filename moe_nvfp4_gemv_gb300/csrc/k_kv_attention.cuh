@@ -180,15 +180,18 @@ __device__ __forceinline__ float attn_lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// l 2^d, d <= 0, in two steps: for sums of weights / vs.  Beside a page of V that is zero these reach 2^100 and the
-// factors to other pages' maxima 2^-130, which is no binary32 number; few tokens to a warp make that usual in the modes
-// beyond the plain one.
-template <int kMode>
-__device__ __forceinline__ float attn_lower(float l, float d) {
-  if (kMode == kAttnPlain) return l * attn_ex2(d);
-  const float half = attn_ex2(0.5f * d);
-  return l * half * half;
+// 2^d, d <= 0, as hi lo, for sums of weights / vs: beside a page of V that is zero these reach 2^100 and the factors to
+// other pages' maxima 2^-130, which is no binary32 number.  lo is 1 where 2^d is one.
+struct AttnFall {
+  float hi, lo;
+};
+__device__ __forceinline__ AttnFall attn_fall(float d) {
+  const bool far = d < -126.0f;  // (not for a NaN)
+  return {far ? 0x1p-126f : attn_ex2(d), far ? attn_ex2(d + 126.0f) : 1.0f};
 }
+__device__ __forceinline__ float attn_lower(float l, AttnFall f) { return l * f.lo * f.hi; }
+// Whether l, joined from sums of up to `most` by their hi alone, lacks some that counts (at most `most` 2^-126 each).
+__device__ __forceinline__ bool attn_lacks(float l, float most) { return most * 0x1p-90f > l; }
 // C += A B; A 16 x 16 (rows g and g + 8), B 16 x 8, f16; C fp32.
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -521,6 +524,17 @@ __device__ __forceinline__ void attn_put(float4 v, float top, float l, uint16_t*
   if (lse) *lse = l > 0.0f ? 0.6931471805599453f * (top + log2f(l)) : l == l ? -__builtin_huge_valf() : l;
 }
 
+// The sum of `cnt` partials' sums of weights against the maximum `top`; the first lies `off` further.
+inline __device__ __noinline__ float attn_sums(const float* at, int64_t step, int cnt, int off, float top) {
+  float l = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < cnt; ++k) {
+    const float2 o = __ldcg(reinterpret_cast<const float2*>(at + k * step + (k == 0 ? off : 0)));
+    l += attn_lower(o.y, attn_fall(o.x - top));
+  }
+  return l;
+}
+
 // What follows an item's sums: row r's outputs, or its partials and their
 // joining.  A partial row holds the sums, m and the sum of weights.
 template <int kDim, int kThreads, class P = KvAttnParams>
@@ -587,7 +601,7 @@ struct AttnItemEnd {
         const int way = tid % ways, x = x0 + tid / ways;
         const bool live = x < cells;
         const int r = live ? x / (kDim / 4) : 0, d = live ? (x - r * (kDim / 4)) * 4 : 0;
-        float top = kAttnFloor, l = 0.0f;
+        float top = kAttnFloor, l = 0.0f, most = 0.0f;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int k = way; live && k < cnt; k += kBatch * ways) {
           float2 cm[kBatch];
@@ -608,14 +622,15 @@ struct AttnItemEnd {
           for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
           const float fall = attn_ex2(top - mn);
           v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall;
-          l = kMode != kAttnPlain ? attn_lower<kMode>(l, top - mn) : l * fall;
+          l *= fall;
           top = mn;
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
             const float f = attn_ex2(cm[j].x - mn);
             v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
             v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
-            l = kMode != kAttnPlain ? l + attn_lower<kMode>(cm[j].y, cm[j].x - mn) : fmaf(cm[j].y, f, l);
+            l = fmaf(cm[j].y, f, l);
+            most = fmaxf(most, cm[j].y);
           }
         }
         for (int o = 1; o < ways; o <<= 1) {
@@ -626,9 +641,13 @@ struct AttnItemEnd {
           const float f = attn_ex2(top - mn), fo = attn_ex2(to - mn);
           v.x = v.x * f + u.x * fo, v.y = v.y * f + u.y * fo;
           v.z = v.z * f + u.z * fo, v.w = v.w * f + u.w * fo;
-          l = kMode != kAttnPlain ? attn_lower<kMode>(l, top - mn) + attn_lower<kMode>(lo, to - mn) : l * f + lo * fo;
+          l = l * f + lo * fo;
           top = mn;
+          most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
         }
+        if (live && way == 0 && attn_lacks(l, most))
+          l = attn_sums(part_of(from, 0) + r * kRowFloats + kDim, step * 2 * kAttnMaxRows * kRowFloats, cnt,
+                        from == c0 ? kAttnMaxRows * kRowFloats : 0, top);
         if (live && way == 0) {
           if (final) {
             store(r, d, v, top, l);
@@ -1036,13 +1055,13 @@ __device__ __forceinline__ void attn_items(const AttnModeParams<kMode>& p, uint3
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
             const float mn = fmaxf(m[nt][h], top - kAttnLift);
-            const float fall = attn_ex2(m[nt][h] - mn);
-            sum[nt][h] = attn_lower<kMode>(sum[nt][h], m[nt][h] - mn);
+            const AttnFall fall = attn_fall(m[nt][h] - mn);
+            sum[nt][h] = attn_lower(sum[nt][h], fall);
             m[nt][h] = mn;
 #pragma unroll
             for (int j = 0; j < L::kTiles; ++j) {
-              acc[nt][j][h] *= fall;
-              acc[nt][j][2 + h] *= fall;
+              acc[nt][j][h] *= fall.hi;
+              acc[nt][j][2 + h] *= fall.hi;
             }
             sc[nt][h] = r0 - mn;
             sc[nt][2 + h] = r1 - mn;
@@ -1478,13 +1497,13 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
               const float mn = fmaxf(m[nt][h], top - kAttnLift);
-              const float fall = attn_ex2(m[nt][h] - mn);
-              sum[nt][h] = kMode != kAttnPlain ? attn_lower<kMode>(sum[nt][h], m[nt][h] - mn) : sum[nt][h] * fall;
+              const AttnFall fall = attn_fall(m[nt][h] - mn);
+              sum[nt][h] = attn_lower(sum[nt][h], fall);
               m[nt][h] = mn;
 #pragma unroll
               for (int j = 0; j < L::kTiles; ++j) {
-                acc[nt][j][h] *= fall;
-                acc[nt][j][2 + h] *= fall;
+                acc[nt][j][h] *= fall.hi;
+                acc[nt][j][2 + h] *= fall.hi;
               }
               sc[nt][h] = r0 - mn;
               sc[nt][2 + h] = r1 - mn;
@@ -1582,7 +1601,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
       for (int x = tid; x < 8 * (kDim / 4); x += C::kThreads) {
         const int r8 = x / (kDim / 4), d = (x - r8 * (kDim / 4)) * 4, r = nt * 8 + r8;
         if (r >= used) break;
-        float top = kAttnFloor, l = 0.0f;
+        float top = kAttnFloor, l = 0.0f, most = 0.0f;
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) top = fmaxf(top, ml[w * C::kRows + r].x);
         const int2 place = L::v_place(d);
@@ -1595,7 +1614,16 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
           const float* const cells = reinterpret_cast<const float*>(smem + free_stage[w]);
           const float4 a = *reinterpret_cast<const float4*>(cells + from_cell);
           v.x = fmaf(a.x, fv, v.x), v.y = fmaf(a.y, fv, v.y), v.z = fmaf(a.z, fv, v.z), v.w = fmaf(a.w, fv, v.w);
-          l = kMode != kAttnPlain ? l + attn_lower<kMode>(o.y, o.x - top) : fmaf(o.y, f, l);
+          l = fmaf(o.y, f, l);
+          most = fmaxf(most, o.y);
+        }
+        if (attn_lacks(l, most)) {
+          l = 0.0f;
+#pragma unroll 1
+          for (int w = 0; w < C::kWarps; ++w) {
+            const float2 o = ml[w * C::kRows + r];
+            l += attn_lower(o.y, attn_fall(o.x - top));
+          }
         }
         if (whole) {
           item_end.store(r, d, v, top, l);
