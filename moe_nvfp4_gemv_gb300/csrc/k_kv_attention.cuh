@@ -190,6 +190,9 @@ __device__ __forceinline__ AttnFall attn_fall(float d) {
   return {far ? 0x1p-126f : attn_ex2(d), far ? attn_ex2(d + 126.0f) : 1.0f};
 }
 __device__ __forceinline__ float attn_lower(float l, AttnFall f) { return l * f.lo * f.hi; }
+// Pages of V of smaller scales, by log2: their tokens' weights can leave binary32's range beside others, so that in the
+// sums of weights / vs they stand as 2^(s - m), made from the exponents without log2 vs.
+constexpr float kAttnSmallScale = -60.0f;
 // Whether l, joined from sums of up to `most` by their hi alone, lacks some that counts (at most `most` 2^-126 each).
 __device__ __forceinline__ bool attn_lacks(float l, float most) { return most * 0x1p-90f > l; }
 // C += A B; A 16 x 16 (rows g and g + 8), B 16 x 8, f16; C fp32.
@@ -1014,7 +1017,8 @@ __device__ __forceinline__ void attn_items(const AttnModeParams<kMode>& p, uint3
       float ks, vs;
       asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(kb + 2 * L::kStripBytes));
       const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
-      const float inv_vs = attn_ex2(-lv) * kAttnUnlift;
+      float inv_vs = attn_ex2(-lv) * kAttnUnlift;
+      const bool small = lv < kAttnSmallScale;
       bool masked = here + 16 > tokens_all || here < tokens_low;
       bool some = here >= tokens_low;  // every row sees some of the strip
       if constexpr (kMode == kAttnSinks) {
@@ -1032,7 +1036,7 @@ __device__ __forceinline__ void attn_items(const AttnModeParams<kMode>& p, uint3
           sc[nt][2 + h] = fmaf(sc[nt][2 + h], f, base);
           high = fmaxf(high, fmaxf(sc[nt][h], sc[nt][2 + h]));
         }
-      if (masked || fresh || __any_sync(0xFFFFFFFFu, high > kAttnLift + kAttnSlack)) {
+      if (masked || small || fresh || __any_sync(0xFFFFFFFFu, high > kAttnLift + kAttnSlack)) {
 #pragma unroll
         for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
@@ -1067,6 +1071,14 @@ __device__ __forceinline__ void attn_items(const AttnModeParams<kMode>& p, uint3
             sc[nt][2 + h] = r1 - mn;
           }
         fresh = fresh && !some;
+        if (small) {
+#pragma unroll
+          for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              sum[nt][h] = fmaf(attn_ex2(sc[nt][h] - lv) + attn_ex2(sc[nt][2 + h] - lv), kAttnUnlift, sum[nt][h]);
+          inv_vs = 0.0f;
+        }
       }
       uint32_t pb[kN][2];
 #pragma unroll
@@ -1453,7 +1465,8 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
         float ks, vs;
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(kb + 2 * L::kStripBytes));
         const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
-        const float inv_vs = attn_ex2(-lv) * kAttnUnlift;  // (sums stay those of weights up to 1)
+        float inv_vs = attn_ex2(-lv) * kAttnUnlift;  // (sums stay those of weights up to 1)
+        const bool small = lv < kAttnSmallScale;
         bool masked = here + 16 > tokens_all || here < tokens_low;
         bool some = here >= tokens_low;  // every row sees some of the strip
         if constexpr (kMode == kAttnSinks) {
@@ -1462,7 +1475,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
         }
         // Exponents against the running maxima, in the scores' place; against 0 while the warp has seen no strip that
         // every row sees some of (`fresh`: a row's first maximum is only known then).  Where they are masked, too high
-        // or fresh, the maxima are taken and the exponents made again.
+        // or fresh, or the page's scale is small, the maxima are taken and the exponents made again.
         float high = -1.0f;
 #pragma unroll
         for (int nt = 0; nt < kN; ++nt)
@@ -1474,7 +1487,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
             sc[nt][2 + h] = fmaf(sc[nt][2 + h], f, base);
             high = fmaxf(high, fmaxf(sc[nt][h], sc[nt][2 + h]));
           }
-        if (masked || fresh || __any_sync(0xFFFFFFFFu, high > kAttnLift + kAttnSlack)) {
+        if (masked || small || fresh || __any_sync(0xFFFFFFFFu, high > kAttnLift + kAttnSlack)) {
 #pragma unroll
           for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
@@ -1509,6 +1522,14 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
               sc[nt][2 + h] = r1 - mn;
             }
           fresh = fresh && !some;
+          if (small) {
+#pragma unroll
+            for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                sum[nt][h] = fmaf(attn_ex2(sc[nt][h] - lv) + attn_ex2(sc[nt][2 + h] - lv), kAttnUnlift, sum[nt][h]);
+            inv_vs = 0.0f;
+          }
         }
         uint32_t pb[kN][2];
 #pragma unroll

@@ -582,7 +582,9 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1)
         }
         const uint32_t scales = sm + C::kScaleOff + stage * 64 + (who >> p.block_log2) * 4;
         const float ks = ldsf(scales), vs = ldsf(scales + 32);
-        const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f)), inv_vs = attn_ex2(-lv);
+        const float lv = attn_lg2(fmaxf(vs, 7.888609052210118e-31f));
+        float inv_vs = attn_ex2(-lv);
+        const bool small = lv < kAttnSmallScale;
         bool live = tok < tile_end && tok >= tok_low;
         bool masked = tile0 + C::kTile > min(tokens_all, tile_end) || tile0 < tokens_low;
         bool some = tile0 >= tokens_low;  // every row sees some of the tile
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1)
           }
         }
         if (j > j0) wait(added(g), (count - 1) & 1);  // the sums so far; the weights' tile is free
-        if (named_any(1 + g, 128, masked || fresh || top > C::kSlack + C::kWScale)) {
+        if (named_any(1 + g, 128, masked || fresh || small || top > C::kSlack + C::kWScale)) {
           // ---- masks; the running maxima move ----
           float v[32];
 #pragma unroll
@@ -669,6 +671,15 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1)
             const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(&row_fall_lo[g][2 * i]);
             sum[i] = mul2(mul2(sum[i], lo.x), hi.x);
             sum[i + 1] = mul2(mul2(sum[i + 1], lo.y), hi.y);
+          }
+          if (small) {
+            const uint64_t unscale = pair(C::kWUnscale, C::kWUnscale), back = pair(-lv, -lv);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = unpair(add2(x[i], back));
+              sum[i] = fma2(pair(attn_ex2(e.x), attn_ex2(e.y)), unscale, sum[i]);
+            }
+            inv_vs = 0.0f;
           }
           if (j > j0) {
             tc_fence_after();

@@ -434,8 +434,10 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
               sum = t.x + t.y;
             };
             if (!fresh) weigh();
+            float inv_vs = __uint_as_float(g.z);
+            const bool small = __uint_as_float(g.y) < kAttnSmallScale;  // (all lanes alike)
             // (a sum below f16's largest value has no weight above it)
-            if (fresh || __any_sync(0xFFFFFFFFu, sum > 65000.0f)) {
+            if (fresh || __any_sync(0xFFFFFFFFu, sum > 65000.0f || small)) {
               // (no values are held across the call: the scores are fetched again behind it)
               if (c + 1 < C::kParts) tmem_here(x[(c + 1) & 1]);
               tmem_fetch16(s_cols + 16 * c, v);
@@ -455,9 +457,14 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
               tmem_fetch16(s_cols + 16 * c, v);
               tmem_here(v);
               if (c + 1 < C::kParts) tmem_fetch16(s_cols + 16 * (c + 1), x[(c + 1) & 1]);
+              if (small) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) l += attn_ex2(fmaf(v[i], f, -m));
+                inv_vs = 0.0f;
+              }
               weigh();
             }
-            l = fmaf(sum, __uint_as_float(g.z), l);
+            l = fmaf(sum, inv_vs, l);
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = pack_f16(v[2 * i], v[2 * i + 1]);

@@ -84,11 +84,21 @@ def peaks_among_zeros(n, period, first, bits, batch, fmt, dim, own=16):
 
 @pytest.mark.parametrize("fmt,dim,rows", SHAPES)
 @pytest.mark.parametrize("call", list(CALLS))
-@pytest.mark.parametrize("bits", [5])
+@pytest.mark.parametrize("bits", [5, 14, 20])
 def test_zero_pages_between_peaks(kv, call, fmt, dim, rows, bits):
-    """Of 112 tokens one has score 0 and large values, most have no values and lie 5 powers of two lower: these together
-    have three times its part."""
+    """Of 112 tokens one has score 0 and large values, most have no values and lie 5, 14 or 20 powers of two lower: these
+    together have 3.5, 2^-7.2 and 2^-13 of it."""
     c, table, lens = peaks_among_zeros(152 * 512 if call == "together" else 4096, 7, 2, bits, 2, fmt, dim)
     q = torch.zeros(2, 1, rows, dim, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 1.0
+    check(kv, call, c, q, table, lens, fmt, sm_scale=math.log(2.0))
+
+
+@pytest.mark.parametrize("call", ["sinks", "apart", "together"])
+@pytest.mark.parametrize("fmt,dim,rows", [("e4m3", 256, 16), ("int8", 96, 24), ("int8", 64, 16)])
+def test_zero_pages_of_many_short_items(kv, call, fmt, dim, rows):
+    """A warp to an item: 400 sequences of 272 tokens."""
+    c, table, lens = peaks_among_zeros(256, 7, 2, 14, 400, fmt, dim)
+    q = torch.zeros(400, 1, rows, dim, dtype=torch.bfloat16, device=DEV)
     q[..., 0] = 1.0
     check(kv, call, c, q, table, lens, fmt, sm_scale=math.log(2.0))
