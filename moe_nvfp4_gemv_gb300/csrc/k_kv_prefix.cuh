@@ -182,10 +182,11 @@ inline __device__ __noinline__ void prefix_rescale(uint32_t cols, int columns, f
   }
   tmem_wait_st();
 }
-// `parts` times 16 weights (two to a column) of the lane times f, a power of two.
+// `parts` times 16 weights (two to a column) of the lane times f, a power of two, as two f16 numbers: f itself may be below
+// f16's range where a weight of 2^15 times f is not.
 inline __device__ __noinline__ void prefix_rescale_weights(uint32_t cols, int parts, float f) {
   tmem_wait_st();  // (they may be on their way)
-  const __half2 f2 = __float2half2_rn(f);
+  const __half2 f0 = __float2half2_rn(fmaxf(f, 0x1p-24f)), f1 = __float2half2_rn(fminf(f * 0x1p24f, 1.0f));
 #pragma unroll 1
   for (int c = 0; c < parts; ++c) {
     uint32_t w[8];
@@ -193,7 +194,7 @@ inline __device__ __noinline__ void prefix_rescale_weights(uint32_t cols, int pa
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w[i]), f2);
+      const __half2 x = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&w[i]), f0), f1);
       w[i] = *reinterpret_cast<const uint32_t*>(&x);
     }
     tmem_st8(cols + 8 * c, w);
