@@ -38,3 +38,34 @@ def test_small_weights_before_the_largest(kv, fmt, dim, where, bits):
                               always=True).double()
     want = 128 * 2.0 ** -value / (1 + 128 * 2.0 ** -value)
     assert ((out - want).abs() <= (2.0 ** -10 + 2.0 ** -9) * want + 128 * 2.0 ** -32).all(), float((out / want).min())
+
+
+@pytest.mark.parametrize("dim,fmt", [(64, "e4m3"), (96, "int8"), (128, "e4m3"), (128, "int8"), (256, "e4m3"), (256, "int8")])
+@pytest.mark.parametrize("batch,heads", [(3, 8), (5, 40), (9, 64)])
+def test_maxima_in_later_tiles(kv, dim, fmt, batch, heads):
+    """A CTA holds six tiles and more of one KV head: one block of rows (its slots take the tiles by turns), two blocks (a
+    slot each), five.  Rows meet the token that takes all in the second, third, a middle or the last tile, in one of a
+    beginning's first, middle and last CTAs, some rows several ever larger ones."""
+    tile = 64 if dim == 256 else 128
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    items = -(-batch * heads // (128 if dim == 256 else 256))
+    n, block = ctas * 6 * tile // items, 64
+    n = n // 128 * 128
+    g = gen(dim + batch)
+    full = n // block
+    c = scaled(random_cache(full + batch, 1, block, dim, g, 0.5), fmt)
+    c["k_codes"] = ref.encode(20 * torch.randn(c["k_codes"].shape, generator=g), fmt)  # (room for six times as much)
+    c["k_scale"] = 0.05 * torch.exp2(0.5 * torch.randn(c["k_scale"].shape, generator=g))
+    table = torch.arange(full + 1, dtype=torch.int32).repeat(batch, 1)
+    table[:, -1] += torch.arange(batch, dtype=torch.int32)
+    q = torch.randn(batch, 1, heads, dim, generator=g).to(torch.bfloat16)
+    per = -(-(n // tile) * items // ctas)  # a CTA's tiles
+    flat = q.view(-1, dim)
+    for j, r in enumerate(range(0, len(flat), 3)):
+        for k, size in ((1, 2.0), (2, 3.0), (per // 2, 4.5), (per - 1, 6.0))[j % 4:4 if j % 8 < 4 else j % 4 + 1]:
+            cta = (0, ctas // 2, ctas - 1, 7)[(j // 3) % 4]
+            at = (cta * per + k) % (n // tile) * tile + (11 * r + 5) % tile
+            x = flat[r].float() / flat[r].float().square().mean().sqrt() * size  # its score: about `size` sqrt(dim)
+            s = float(c["k_scale"][at // block, 0])
+            c["k_codes"][at // block, 0, at % block] = ref.encode((x / s).clamp(-448, 448), fmt)
+    check(kv, c, fmt, q.to(DEV), table, [n + 1 + (5 * b) % 60 for b in range(batch)], n)
