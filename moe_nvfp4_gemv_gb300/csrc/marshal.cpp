@@ -160,6 +160,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t ldk = T > 1 ? k.stride(0) : H * D, ldv = T > 1 ? v.stride(0) : H * D;
     const void *pk = address(k), *pv = address(v);
     const int32_t *pt = address_as<int32_t>(table), *pl = address_as<int32_t>(lens);
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(index));
     const cudaStream_t stream = stream_of(index);
     return unlocked([&] {
       return g_append(cache, pk, ldk, pv, ldv, dtype, static_cast<int>(T), cu, pt, max_blocks, pl, B, pdl, stream);
@@ -336,6 +337,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Attention c = attention_of(a);
     if (c.empty) return FP4GEMV_OK;
     if (c.large) return FP4GEMV_ERR_UNSUPPORTED_SHAPE;
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.index));
     const cudaStream_t stream = stream_of(c.index);
     return unlocked([&] {
       return g_attention(c.cache, c.q, c.ldq, c.dtype, c.heads, c.q_len, c.table, c.max_blocks, c.lens, c.B, c.sm_scale,
@@ -434,6 +436,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* px = address(logits);
     int32_t* pi = address_as<int32_t>(ids);
     float* pw = address_as<float>(weights);
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(l.index));
     const cudaStream_t stream = stream_of(l.index);
     return unlocked([&] {
       return g_route(px, l.ld, l.dtype, static_cast<int>(l.rows), static_cast<int>(l.width), topk, scores, bias, n_group,
@@ -469,6 +472,7 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* pr = address_as<int32_t>(rank);
     int32_t* pti = top_n > 0 ? address_as<int32_t>(top_ids) : nullptr;
     float* ptl = top_n > 0 ? address_as<float>(top_logprobs) : nullptr;
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(l.index));
     const cudaStream_t stream = stream_of(l.index);
     return unlocked([&] {
       return g_logprobs(px, l.ld, l.dtype, static_cast<int>(l.rows), static_cast<int>(l.width), pt,

@@ -80,7 +80,7 @@ def attention_workspace(device: torch.device, head_dim: int, stream: int | None 
     on = contextlib.nullcontext()
     if stream != current:  # (cleared on the stream that it is for)
         on = torch.cuda.stream(torch.cuda.ExternalStream(stream, index) if stream else torch.cuda.default_stream(index))
-    with on:
+    with torch.cuda.device(index), on:
         ws = torch.zeros(attention_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
     if capture:
         _captured[key] = (capture, ws)
@@ -228,5 +228,6 @@ class KvCache8:
         return out
 
     def shared_scratch_bytes(self, batch: int, q_len: int, heads: int) -> int:
-        """Bytes of ``attend_shared``'s scratch (0 for sizes that it refuses)."""
-        return int(_lib.fp4gemv_kv_attention_shared_scratch_bytes(self.kv_heads, self.head_dim, heads, q_len, batch))
+        """Bytes of ``attend_shared``'s scratch on the cache's device (0 for sizes that it refuses)."""
+        with torch.cuda.device(self._index):
+            return int(_lib.fp4gemv_kv_attention_shared_scratch_bytes(self.kv_heads, self.head_dim, heads, q_len, batch))
