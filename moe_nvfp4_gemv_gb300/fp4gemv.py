@@ -468,7 +468,9 @@ def add_norm(x: torch.Tensor, y: torch.Tensor | None, weight: torch.Tensor, post
     type or fp32; weights [H] and the gate ([H], [M, H] or [M, 1]) likewise.
     Unit inner strides, any row strides.  ``residual`` may be x and ``out`` may
     be y.  With y = None: (rms_norm(x) * (weight_offset + weight), x), out in
-    x's type, bf16 for fp32, unless ``out`` is given."""
+    x's type, bf16 for fp32, unless ``out`` is given; no ``residual``."""
+    if y is None and residual is not None:
+        raise ValueError("residual needs y")
     if out is None:
         if y is not None:
             out = torch.empty(y.shape, dtype=y.dtype, device=y.device)
