@@ -143,7 +143,16 @@ __device__ __forceinline__ void norm_store(void* p, bool f32, int64_t at, int le
     }
   }
 }
-__device__ __forceinline__ float norm_gate(float g, int sigmoid) { return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-g)) : g; }
+// The logistic function is e / (1 + e) below 0 and 1 / (1 + e) above, e = 2^(-|g| log2(e)): the divisor is within 1 .. 2, and
+// small results keep their digits.  e is a square, so that it may be subnormal.
+__device__ __forceinline__ float norm_gate(float g, int sigmoid) {
+  if (!sigmoid) return g;
+  float root, inv;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(fabsf(g) * -0.7213475204444817f));
+  const float e = root * root;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(1.0f + e));
+  return (g < 0.0f ? e : 1.0f) * inv;
+}
 
 // Threads of a CTA: whole tokens, 256 threads or more where that comes out even.
 __host__ __device__ constexpr int norm_threads(int row) { return row < 256 && 256 % row == 0 ? 256 : row; }
