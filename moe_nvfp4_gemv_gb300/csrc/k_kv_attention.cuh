@@ -180,8 +180,13 @@ __device__ __forceinline__ float attn_lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 2^d, d <= 0, as hi lo, for sums of weights / vs: beside a page of V that is zero these reach 2^100 and the factors to
-// other pages' maxima 2^-130, which is no binary32 number.  lo is 1 where 2^d is one.
+// Sums of weights / vs reach 2^100 beside a page of V that is zero, and the factors 2^d, d <= 0, to other pages' maxima
+// 2^-130, which is no binary32 number; few tokens to a warp make that usual in the modes beyond the plain one.  There the
+// root of 2^d is taken twice; the plain mode, whose loop a root costs more, takes 2^d as hi lo, lo 1 where 2^d is a number.
+__device__ __forceinline__ float attn_halves(float l, float d) {
+  const float half = attn_ex2(0.5f * d);
+  return l * half * half;
+}
 struct AttnFall {
   float hi, lo;
 };
@@ -546,6 +551,7 @@ struct AttnItemEnd {
   static constexpr int kMode = std::is_same_v<P, KvAttnSinksParams>  ? kAttnSinks
                                : std::is_same_v<P, KvAttnRestParams> ? kAttnRest
                                                                      : kAttnPlain;
+  static constexpr bool kHalves = kMode != kAttnPlain;
   const P& p;
   const AttnPlace& cur;
   int row0, used;  // the item's first row, its rows
@@ -625,15 +631,15 @@ struct AttnItemEnd {
           for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
           const float fall = attn_ex2(top - mn);
           v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall;
-          l *= fall;
+          l = kHalves ? attn_halves(l, top - mn) : l * fall;
           top = mn;
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
             const float f = attn_ex2(cm[j].x - mn);
             v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
             v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
-            l = fmaf(cm[j].y, f, l);
-            most = fmaxf(most, cm[j].y);
+            l = kHalves ? l + attn_halves(cm[j].y, cm[j].x - mn) : fmaf(cm[j].y, f, l);
+            if (!kHalves) most = fmaxf(most, cm[j].y);
           }
         }
         for (int o = 1; o < ways; o <<= 1) {
@@ -644,11 +650,11 @@ struct AttnItemEnd {
           const float f = attn_ex2(top - mn), fo = attn_ex2(to - mn);
           v.x = v.x * f + u.x * fo, v.y = v.y * f + u.y * fo;
           v.z = v.z * f + u.z * fo, v.w = v.w * f + u.w * fo;
-          l = l * f + lo * fo;
+          l = kHalves ? attn_halves(l, top - mn) + attn_halves(lo, to - mn) : l * f + lo * fo;
           top = mn;
-          most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+          if (!kHalves) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
         }
-        if (live && way == 0 && attn_lacks(l, most))
+        if (!kHalves && live && way == 0 && attn_lacks(l, most))
           l = attn_sums(part_of(from, 0) + r * kRowFloats + kDim, step * 2 * kAttnMaxRows * kRowFloats, cnt,
                         from == c0 ? kAttnMaxRows * kRowFloats : 0, top);
         if (live && way == 0) {
@@ -1059,13 +1065,13 @@ __device__ __forceinline__ void attn_items(const AttnModeParams<kMode>& p, uint3
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
             const float mn = fmaxf(m[nt][h], top - kAttnLift);
-            const AttnFall fall = attn_fall(m[nt][h] - mn);
-            sum[nt][h] = attn_lower(sum[nt][h], fall);
+            const float fall = attn_ex2(m[nt][h] - mn);
+            sum[nt][h] = attn_halves(sum[nt][h], m[nt][h] - mn);
             m[nt][h] = mn;
 #pragma unroll
             for (int j = 0; j < L::kTiles; ++j) {
-              acc[nt][j][h] *= fall.hi;
-              acc[nt][j][2 + h] *= fall.hi;
+              acc[nt][j][h] *= fall;
+              acc[nt][j][2 + h] *= fall;
             }
             sc[nt][h] = r0 - mn;
             sc[nt][2 + h] = r1 - mn;
@@ -1511,7 +1517,7 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
               for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
               const float mn = fmaxf(m[nt][h], top - kAttnLift);
               const AttnFall fall = attn_fall(m[nt][h] - mn);
-              sum[nt][h] = attn_lower(sum[nt][h], fall);
+              sum[nt][h] = kMode != kAttnPlain ? attn_halves(sum[nt][h], m[nt][h] - mn) : attn_lower(sum[nt][h], fall);
               m[nt][h] = mn;
 #pragma unroll
               for (int j = 0; j < L::kTiles; ++j) {
@@ -1635,10 +1641,10 @@ __global__ void __launch_bounds__(AttnCfg<kDim, kN, kRes>::kThreads, kRes)
           const float* const cells = reinterpret_cast<const float*>(smem + free_stage[w]);
           const float4 a = *reinterpret_cast<const float4*>(cells + from_cell);
           v.x = fmaf(a.x, fv, v.x), v.y = fmaf(a.y, fv, v.y), v.z = fmaf(a.z, fv, v.z), v.w = fmaf(a.w, fv, v.w);
-          l = fmaf(o.y, f, l);
+          l = kMode != kAttnPlain ? l + attn_halves(o.y, o.x - top) : fmaf(o.y, f, l);
           most = fmaxf(most, o.y);
         }
-        if (attn_lacks(l, most)) {
+        if (kMode == kAttnPlain && attn_lacks(l, most)) {
           l = 0.0f;
 #pragma unroll 1
           for (int w = 0; w < C::kWarps; ++w) {

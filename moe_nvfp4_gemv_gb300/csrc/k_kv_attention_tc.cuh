@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1)
   __shared__ __align__(16) float row_base[C::kGroups][C::kRows];   // kWScale - m; 0 while there is no m to go by
   __shared__ float row_tmp[C::kWeighers / 32][C::kRows];          // maxima, sums of the warps
   __shared__ __align__(16) float row_fall[C::kGroups][C::kRows];
-  __shared__ __align__(16) float row_fall_lo[C::kGroups][C::kRows];  // AttnFall's second factor
+  __shared__ __align__(16) float row_fall_lo[C::kGroups][C::kRows];  // AttnFall's second factor; kSinks: the root
   __shared__ float2 ml[C::kRows];
   __shared__ uint32_t nan_dims[C::kRows][C::kDim / 32];  // of the segment's rows: dims where a token that the row sees is NaN
   __shared__ int nan_any;
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1)
             row_base[g][who] = fresh ? 0.0f : C::kWScale - now;
             const AttnFall fall = attn_fall(old - now);
             row_fall[g][who] = fall.hi;
-            row_fall_lo[g][who] = fall.lo;
+            row_fall_lo[g][who] = kSinks ? attn_ex2(0.5f * (old - now)) : fall.lo;
           }
           group_sync(g);
 #pragma unroll
@@ -667,8 +667,8 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1)
             x[i] = pair(v[2 * i] - row_m[g][2 * i] + C::kWScale, v[2 * i + 1] - row_m[g][2 * i + 1] + C::kWScale);
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(&row_fall[g][2 * i]);
             const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(&row_fall_lo[g][2 * i]);
+            const ulonglong2 hi = kSinks ? lo : *reinterpret_cast<const ulonglong2*>(&row_fall[g][2 * i]);
             sum[i] = mul2(mul2(sum[i], lo.x), hi.x);
             sum[i + 1] = mul2(mul2(sum[i + 1], lo.y), hi.y);
           }
@@ -783,8 +783,10 @@ __global__ void __launch_bounds__(AttnTc::kThreads, 1)
         const float4 u = *reinterpret_cast<const float4*>(a);
         const float4 w = *reinterpret_cast<const float4*>(a + C::kTileBytes / 4);
         const float4 v = make_float4(u.x * f0 + w.x * f1, u.y * f0 + w.y * f1, u.z * f0 + w.z * f1, u.w * f0 + w.w * f1);
-        float l = failed ? __int_as_float(0x7FC00000) : l0 * f0 + l1 * f1;
-        if (attn_lacks(l, fmaxf(l0, l1))) l = attn_lower(l0, attn_fall(m0 - top)) + attn_lower(l1, attn_fall(m1 - top));
+        float l = kSinks ? attn_halves(l0, m0 - top) + attn_halves(l1, m1 - top) : l0 * f0 + l1 * f1;
+        if (failed) l = __int_as_float(0x7FC00000);
+        if (!kSinks && attn_lacks(l, fmaxf(l0, l1)))
+          l = attn_lower(l0, attn_fall(m0 - top)) + attn_lower(l1, attn_fall(m1 - top));
         if (whole) {
           item_end.store(r, d, v, top, l);
         } else {

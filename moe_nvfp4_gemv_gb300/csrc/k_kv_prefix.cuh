@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
               const float want = fmaxf(ceilf(fmaf(most, f, __uint_as_float(g.y)) - kAttnLift), kAttnFloor);
               const float now = fresh ? want : fmaxf(m, want);
               if (!fresh) {
-                l = attn_lower(l, attn_fall(m - now));
+                l = attn_halves(l, m - now);
                 prefix_rescale_weights(s_cols, c, attn_ex2(m - now));
               }
               m = now;
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(PrefixCfg<kDim>::kThreads, 1) kv_prefix_kernel
           both_any(false);
           const float now = fmaxf(m, row_said[(half ^ 1) * 128 + row]);
           if (go) {
-            l = attn_lower(l, attn_fall(m - now));
+            l = attn_halves(l, m - now);
             prefix_rescale_weights(s_cols, C::kParts, attn_ex2(m - now));
             if (!first) {
               if (C::kSlots == 1) {  // (one accumulator for both S: the other's sums may be under way)
@@ -744,11 +744,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvJoinParam
   const float2 own = __ldcg(p.ml + at);
   const float4 sums_own = __ldcg(reinterpret_cast<const float4*>(p.sums + at * kDim + d));
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float top = kAttnFloor, l = 0.0f, most = 0.0f;
-  const float2* ml = nullptr;
-  int pieces = 0, step = 1;  // of the beginning; and how many apart
+  float top = kAttnFloor, l = 0.0f;
   if (length > 0) {
-    if (way == 0) v = sums_own, top = own.x, l = own.y, most = own.y;
+    if (way == 0) v = sums_own, top = own.x, l = own.y;
     const int tiles = taken / line.tile;
     if (tiles > 0) {
       const int per = prefix_share(tiles * p.kv_heads * line.items, line.ctas), block = all >> 7;
@@ -756,9 +754,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvJoinParam
       const bool both = line.slots == 2 && 2 * number + 1 < line.blocks;  // (else: slots that took the tiles by turns)
       const int item = head * line.items + number, c0 = item * tiles / per, c1 = ((item + 1) * tiles - 1) / per;
       const int64_t piece = ((static_cast<int64_t>(c0) + item) * line.slots + (both ? block & 1 : 0)) * 128 + (all & 127);
-      step = both ? 2 : 1;
-      pieces = (c1 - c0 + 1) * (line.slots == 1 || both ? 1 : 2);
-      ml = line.ml + piece;
+      const int step = both ? 2 : 1, pieces = (c1 - c0 + 1) * (line.slots == 1 || both ? 1 : 2);
+      const float2* const ml = line.ml + piece;
       const float* const sums = line.sums + piece * kDim + d;
 #pragma unroll 1
       for (int k = way; k < pieces; k += kBatch * kWays) {
@@ -779,7 +776,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvJoinParam
         for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, cm[j].x);
         const float fall = attn_ex2(top - mn);
         v.x *= fall, v.y *= fall, v.z *= fall, v.w *= fall;
-        l *= fall;
+        l = attn_halves(l, top - mn);
         top = mn;
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -787,8 +784,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvJoinParam
           const float f = attn_ex2(cm[j].x - mn);
           v.x = fmaf(a[j].x, f, v.x), v.y = fmaf(a[j].y, f, v.y);
           v.z = fmaf(a[j].z, f, v.z), v.w = fmaf(a[j].w, f, v.w);
-          l = fmaf(cm[j].y, f, l);
-          most = fmaxf(most, cm[j].y);
+          l += attn_halves(cm[j].y, cm[j].x - mn);
         }
       }
     }
@@ -800,19 +796,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const KvJoinParam
                                  __shfl_xor_sync(0xFFFFFFFFu, v.z, o), __shfl_xor_sync(0xFFFFFFFFu, v.w, o));
     const float mn = fmaxf(top, to), f = attn_ex2(top - mn), fo = attn_ex2(to - mn);
     v.x = v.x * f + u.x * fo, v.y = v.y * f + u.y * fo, v.z = v.z * f + u.z * fo, v.w = v.w * f + u.w * fo;
-    l = l * f + lo * fo;
+    l = attn_halves(l, top - mn) + attn_halves(lo, to - mn);
     top = mn;
-    most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
   }
   if (!live || way != 0) return;
-  if (attn_lacks(l, most)) {
-    l = attn_lower(own.y, attn_fall(own.x - top));
-#pragma unroll 1
-    for (int k = 0; k < pieces; ++k) {
-      const float2 o = __ldcg(ml + static_cast<int64_t>(k) * step * 128);
-      l += attn_lower(o.y, attn_fall(o.x - top));
-    }
-  }
   const int64_t token = static_cast<int64_t>(b) * p.q_len + i;
   const int head_out = head * p.group + in - i * p.group;
   attn_put(v, top, l, p.out + token * p.ldo + head_out * kDim + d,
