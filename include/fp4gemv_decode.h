@@ -104,7 +104,9 @@ uint64_t fp4gemv_stream_capture_id(cudaStream_t stream);
  * Numerics: codes and queries are exact f16 operands (queries scaled by a
  * power of two for each row), sums, maxima and statistics fp32,
  * probabilities rounded to f16 for the product with V (below 2^-21 of the
- * largest, at 2^-32 of it), one final rounding.
+ * largest, at 2^-32 of it), one final rounding.  The sum of probabilities
+ * counts every token seen, those on pages whose V scale is 2^-100 (all zeros)
+ * beside scales of 2^20 included.
  * With E4M3, head_dim 128 and more than 16 rows (q_len heads / kv_heads) both
  * become sums of 8-bit parts, which hold f16's probabilities exactly; entries
  * of a query below 2^-14 (f16: 2^-11) of its largest are rounded at 2^-22 of
@@ -159,8 +161,16 @@ size_t fp4gemv_kv_attention_shared_scratch_bytes(int kv_heads, int head_dim, int
  * does.
  * scratch: 16-byte aligned, fp4gemv_kv_attention_shared_scratch_bytes; the
  * workspace is fp4gemv_kv_attention's.
- * Numerics as fp4gemv_kv_attention's of up to 16 rows: exact f16 operands,
- * probabilities rounded to f16, sums fp32.
+ * Numerics of three launches: fp4gemv_kv_attention's of up to 16 rows, whatever
+ * the rows (exact f16 operands, probabilities rounded to f16, sums fp32); where
+ * every sequence is attended to by itself, fp4gemv_kv_attention's for these rows,
+ * which above 16 with E4M3 and head_dim 128 are sums of 8-bit parts.
+ * What the host knows is the table's width: with a table much wider than the
+ * lengths, or a short beginning before long own parts, three launches take
+ * longer than fp4gemv_kv_attention, which is then the call to make.  us, that
+ * one's / these: 16 sequences of 700, 512 common, 8 rows of 128 on 8, a table of
+ * 131072 10 / 21; 32 of 16640, 256 common, E4M3, 8 rows 185 / 191, 32 rows, whose
+ * own parts lack the kernel on the 5th-generation tensor core, 172 / 283.
  * Shapes as fp4gemv_kv_attention; kv_heads * (B * q_len * heads / kv_heads
  *   rows in blocks of 128) * (max_blocks * block_size / 64) at most 2^30. */
 #define FP4GEMV_KV_SHARE_FROM 140000000ll

@@ -25,7 +25,6 @@ cudaError_t launch_moe_route(const RouteParams& p, int dtype, int sms, int pdl, 
 cudaError_t launch_token_logprobs(const LogprobParams& p, int dtype, int T, int sms, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_append(const KvAppendParams& p, int int8, int f16, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_read(const KvReadParams& p, int int8, int dtype, int sms, int pdl, cudaStream_t stream);
-// vec: rows of 16-byte aligned chunks of 8 values.
 // part: values that all rows hold side by side on boundaries of their size, 8 (16 bytes), 2 or 1.
 cudaError_t launch_add_norm(const AddNormParams& p, int f16, int part, int sms, int pdl, cudaStream_t stream);
 // CTAs of the attention kernel at most (the workspace is sized for them).

@@ -7,17 +7,19 @@
 //   h = r / sqrt(mean r^2 + eps) (offset + weight)
 // h comes from r before r is rounded to the stream's type.
 //
-// A token's values stay in the registers of one group of threads from the
-// first read to the last write: every input is read once and every output
-// written once, with one sum over the group for each norm.
+// A token's values stay with one group of threads from the first read to the
+// last write: every input is read once and every output written once, with one
+// sum over the group for each norm.  They are in registers, but for part of a
+// row above 16384 values (1024 threads of 32: 160 to 500 bytes of a thread spill
+// to L1) and 4 to 80 bytes of fp32 streams' and of some narrow forms.
 //
 // What bounds it: HBM for many tokens, the launch and two dependent trips to L2 for few.  Loads of x, y and gates are all
 // under way before the first sum, two chunks of 8 values to a thread, 1024 threads to an SM.  Of the measured copy
 // bandwidth: 20011 tokens of 4096, bf16, norms on both sides and a gate for each value 132 us, 0.93 (loads as they come to
 // be used, a chunk to a thread: 254); without the gate 0.88, the next norm alone 0.98, an fp32 stream 1.0; 5120 0.77, 6144
-// 0.67, 8192 0.80, 10240 0.79, 16384 0.65 (one CTA to an SM: nothing fills in between its phases).  Rows off these
+// 0.67, 8192 0.80, 10240 0.79, 16384 0.64, 32768 0.56 (one CTA to an SM: nothing fills in between its phases).  Rows off these
 // boundaries go by pairs or by values, each a load of its own, neighbours in neighbouring threads, and are bound by the
-// number of these: 4144 of 6892, norms on both sides, 56 us, 0.61 (by values 107), 20011 of 4098 with gates 186, 0.66 (593);
+// number of these: 4144 of 6892, norms on both sides, 56 us, 0.61 (by values 107), 20011 of 4098 with gates 188, 0.65 (593);
 // 3000 of 10001 110, 0.33.  (Loads of places past the row's end instead of branches around them: 68, 257, 123.)
 // One token of 4096: 3.2 us a call, 37 of 6144 3.6.
 #pragma once

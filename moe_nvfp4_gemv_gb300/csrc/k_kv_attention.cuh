@@ -14,6 +14,13 @@
 // from the output that its sum is counted in.  The codes are exact in f16.
 // Queries are made exact f16 operands by a power of two for each row.
 //
+// Sums hold for scales of any sizes side by side: a page of zeros has scale
+// 2^-100 and its tokens' w / vs count like others'.  Sums are brought to another
+// maximum by factors that may be below binary32's range (attn_halves, attn_fall),
+// and on pages of scales below 2^-60 w / vs is made as 2^(s - m) where the maxima
+// move.  That costs 1 percent for 8 and 16 rows, 3 to 5 for 32, whose
+// loop the registers are short of.
+//
 // The work.  KV bytes are read once, 16 tokens (a strip) of K and V of one
 // head at a time, by mma.sync m16n8k16 in the transposed form: the codes are
 // the A operand (S^T = K Q^T with tokens as rows, out^T = V^T w^T with
@@ -52,7 +59,7 @@
 // 188.  Fewer bytes: the launch, the plan, the first strips' latency and the
 // joining, 8 us together: 24 ragged ones of up to 8191 tokens 45.0 us (0.70), one
 // of 131071 (INT8) 51.3 (0.78), one of 777 7.5, one of 16 5.2.  32 rows: issue
-// (INT8 282 us, 0.57; heads of 64 and 96, E4M3, 169 and 228, 0.48 and 0.53; E4M3 of 128 is k_kv_attention_tc.cuh's).  Measured and not
+// (INT8 295 us, 0.54; heads of 64 and 96, E4M3, 174 and 224, 0.46 and 0.54; E4M3 of 128 is k_kv_attention_tc.cuh's).  Measured and not
 // taken: more shares than resident CTAs (24 ragged 46 to 51 .. 73 us: every CTA
 // pays for its plan and first strips), two warps on one ring that part the rows
 // or the dims of 32 rows between them (260 to 344 and 334 us).

@@ -39,18 +39,20 @@
 // With first tokens that stay visible (kSinks) an item's places are those of its
 // leading tiles and then its window's, and a tile lies on one side of the gap: 32
 // sequences of 32768, window 4096, 4 first tokens, 8 new ones, 32 heads over 8:
-// 72.0 us, the window alone 68.5, mma.sync 97.2; 24 of up to 8191, window 2000, 200
-// first ones, 42.4, 39.1, 58.2.  (One sequence of few tiles may cost one more.)
+// 72.0 us, the window alone 71.6, mma.sync 97.2; 24 of up to 8191, window 2000, 200
+// first ones, 41.4, 40.4, 58.2.  (One sequence of few tiles may cost one more.)
 //
 // What bounds it.  32 sequences of 16384 tokens, 4 new ones each, 64 heads over
-// 8: 174 us, 0.93 of the measured bandwidth (mma.sync with the codes converted
+// 8: 177 us, 0.91 of the measured bandwidth (mma.sync with the codes converted
 // in registers: 263, bound by issue: 447 instructions a strip of 16 tokens,
 // where this kernel needs 342).  Steps to it: both rings as one, a V tile held
 // as long as its K and 16 TMA boxes a tile from one warp 228; rings apart, boxes
 // of a page 175.  Short calls pay for the set-up and the first tile's chain
-// (13.4 us for one sequence of 1000 tokens; mma.sync 16), several items in a share
+// (13.9 us for one sequence of 1000 tokens; mma.sync 16), several items in a share
 // for the drains between them (kAttnTcItemCost: 24 ragged sequences of up to
-// 8191 tokens 68 us with 16, 58 with 32, 54 with 64; mma.sync 90).
+// 8191 tokens 68 us with 16, 58 with 32, 54 with 64; mma.sync 90).  Sums beside
+// pages of zeros (k_kv_attention.cuh) lengthen the path on which masks are made and
+// maxima move: those 24 sequences 53.0 to 56.5, the long ones 174.7 to 176.6.
 //
 // Every wait is bounded.  After a failed one (the error word holds
 // FP4_ERR_TIMEOUT) the waits that follow are skipped, so that all roles come to

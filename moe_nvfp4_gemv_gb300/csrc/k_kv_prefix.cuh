@@ -31,13 +31,13 @@
 // in front of it.  Seven warps move codes, a job of 16 tokens of K or V at a
 // time; one warp issues the products.
 //
-// What bounds it.  64 sequences on 32768 common tokens, 64 heads on 8 of 128, E4M3: the call 98 us, of them 53 for the tiles
-// here, 1.95 us for a tile of 128 tokens and 256 rows (the products alone 1.2 at the measured bf16 rate): shared memory,
-// whose bandwidth the products' operands (Q and K of every step), the movers' loads and their f16 stores share -- a
-// mapping that loads half lines costs 10 percent -- and the chain from scores over weights to the next scores.  The
-// remaining 45: the own tokens' kernel 17 to 24, the start up to the first scores 6.5 (lengths, queries, pages, codes), the
-// sums' way out 4, the join 5, launches.  7 sequences on 65536, heads of 256: 49 us, 1.0 us for 64 tokens, 0.7 of the
-// HBM rate; 24 on 8191, 4 new tokens, INT8 heads of 64: 34, the chain of launches.
+// What bounds it.  64 sequences on 32768 common tokens, 64 heads on 8 of 128, E4M3: the call 98 to 101 us, of them 53 for the
+// tiles here, 1.95 us for a tile of 128 tokens and 256 rows (the products alone 1.2 at the measured bf16 rate).  The chain
+// from scores over weights to the next scores holds it: the tensor pipe is active 41 percent, and products and movers move
+// some 70 bytes a cycle through shared memory, whose 128 Q K^T alone would take (a mapping that loads half lines still
+// costs 10 percent).  The remaining 45: the own tokens' kernel 17 to 24, the start up to the first scores 6.5 (lengths,
+// queries, pages, codes), the sums' way out 4, the join 5, launches.  7 sequences on 65536, heads of 256: 49 us, 1.0 us for
+// 64 tokens, 0.7 of the HBM rate; 24 on 8191, 4 new tokens, INT8 heads of 64: 35, the chain of launches.
 // Steps to it, us: weights in two passes over the scores by one thread a row, the join at the ends of the own tokens' items
 // 177.7; the join's loads out of their loops (registers) 145; scores read once, movers by jobs 121; own tokens first, a kernel for the
 // join 116; two threads a row 97.  Measured and not taken: tiles of 64 tokens with the queries in tensor memory for heads of 128 (112), 11

@@ -205,7 +205,10 @@ class KvCache8:
         pages of it is read and multiplied once for all.  (In multiples of 128
         tokens, and no further than the first query of the shortest sequence;
         empty sequences do not count.)  Batches of few tokens are attended to one
-        by one, which is faster, unless ``always``.  ``scratch``: uint8, of
+        by one, which is faster, unless ``always``; how many is judged by the block
+        table's width, so cut a table that is much wider than the lengths (a view of
+        its first columns, made contiguous), and call ``attend`` for a beginning
+        that is short beside the sequences' own tokens.  ``scratch``: uint8, of
         ``shared_scratch_bytes``, allocated for the call by default."""
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
