@@ -106,7 +106,8 @@ uint64_t fp4gemv_stream_capture_id(cudaStream_t stream);
  * probabilities rounded to f16 for the product with V (below 2^-21 of the
  * largest, at 2^-32 of it), one final rounding.  The sum of probabilities
  * counts every token seen, those on pages whose V scale is 2^-100 (all zeros)
- * beside scales of 2^20 included.
+ * beside scales of 2^20 included.  A V scale below 2^-100, which no append
+ * leaves, is taken as 2^-100.
  * With E4M3, head_dim 128 and more than 16 rows (q_len heads / kv_heads) both
  * become sums of 8-bit parts, which hold f16's probabilities exactly; entries
  * of a query below 2^-14 (f16: 2^-11) of its largest are rounded at 2^-22 of
